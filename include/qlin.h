@@ -63,7 +63,8 @@ typedef enum {
   QLIN_ERR_UNSUPPORTED = 2,    /* legal per [OPT] but outside this backend's limits */
   QLIN_ERR_CUDA = 3,           /* a CUDA runtime call or launch failed */
   QLIN_ERR_DEVICE_TIMEOUT = 4, /* a device-side bounded wait expired (status word) */
-  QLIN_ERR_WORKSPACE = 5       /* workspace smaller than the size query returned */
+  QLIN_ERR_WORKSPACE = 5,      /* workspace smaller than the size query returned */
+  QLIN_ERR_BAD_INDEX = 6       /* a device-side index (page, kept row) was out of range (status word) */
 } qlin_status;
 
 typedef enum { QLIN_W4A8 = 0, QLIN_W6A8 = 1 } qlin_format;
@@ -387,6 +388,182 @@ qlin_status qlin_debug_forward_tcgen05(int fmt, int prologue, int M, int64_t N, 
 qlin_status qlin_forward_noalloc(int fmt, int prologue, int M, int64_t N, int64_t K, int64_t G,
                                  const void* packed, const void* x, const void* gate, const void* up,
                                  const float* gamma, float eps, float* y, unsigned flags, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The rest of a decode / verification step: what stands between and behind the
+ * linears ("Doubling the LLM token rate in ComfyUI", section "Adaptive-tree
+ * MTP": one committed token and a tree of drafted ones are verified in one
+ * pass).  q/k/v (qlin_forward_multi) -> qlin_kv_append -> qlin_tree_attention
+ * -> o (qlin_forward) ... -> qlin_sample -> qlin_kv_keep.
+ *
+ * The conventions above hold: device pointers, nothing allocated or
+ * synchronised, errors of arguments returned before anything is enqueued.  The
+ * structs themselves are host memory, read during the call only.
+ * ------------------------------------------------------------------------ */
+typedef enum { QLIN_BF16 = 0, QLIN_F16 = 1, QLIN_F32 = 2 } qlin_dtype;
+
+/*
+ * A paged cache of keys and values.  Token row i of head h on page p starts at
+ * element p * page_stride + h * head_stride + i * token_stride of k and of v
+ * and holds `width` contiguous elements, so [pages, heads, page_size, width]
+ * and [pages, page_size, heads, width] are both caches, and so are slices of
+ * a larger pool.
+ *   dtype      : QLIN_BF16 or QLIN_F16.
+ *   width      : 64, 128 or 256.     heads : 1..1024.
+ *   page_size  : 16, 32, 64, 128 or 256 tokens.    pages : 1..2^31-1.
+ *   k, v       : 16-byte aligned; the strides multiples of 8 elements, each
+ *                in 1..2^36 and token_stride >= width.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t pages, page_stride, head_stride, token_stride;
+  int32_t dtype, heads, width, page_size;
+} qlin_kv_cache;
+
+/*
+ * One step: B sequences, T rows each (row b * T + t of q, k, v and the
+ * output).  Token i of sequence b lies on page page_table[b][i / page_size],
+ * row i % page_size.  Rows are stored behind the sequence's committed tokens:
+ * row t is token len[b] + t.
+ *   page_table : int32 [B, max_pages], rows table_stride entries apart.
+ *                Entries behind the last page in use are not read.
+ *   len        : int32 [B], committed tokens (0: none yet).  len[b] < 0: no
+ *                sequence in this place; nothing of it is read or written.
+ *   count      : int32 [B] or NULL (T rows in every sequence): rows in use;
+ *                the rows behind them are not read, and what they would have
+ *                written is left as it was.
+ *   depth      : int32, row t's distance from the committed tokens, so its
+ *                rotation position is len[b] + depth[t]; NULL: t.
+ *   mask       : int32 bits, bit j of row t: row t sees row j of its own
+ *                sequence (its own bit too); NULL: the rows up to its own.
+ *                T <= 32.  Bits of rows not in use are ignored.
+ *   tree_stride: entries between the sequences' rows of depth and mask; 0 for
+ *                one tree shared by all sequences.
+ * A page index outside [0, pages), or a token behind the table's last page, is
+ * never followed: what it would have read or written is left out, the
+ * sequence's results are unspecified, and QLIN_ERR_BAD_INDEX goes to the
+ * workspace's status word (where the call has a workspace).
+ */
+typedef struct {
+  const int32_t* page_table;
+  const int32_t* len;
+  const int32_t* count;
+  const int32_t* depth;
+  const int32_t* mask;
+  int64_t table_stride, tree_stride;
+  int32_t B, T, max_pages;
+} qlin_kv_step;
+
+/* Rotation frequencies for qlin_kv_append: turns[i] = radians[i] / (2 pi)
+ * modulo 1, as a 64-bit fraction of a turn, so that the angle of any position
+ * is an exact integer product.  Host memory on both sides; copy the result to
+ * the device once.  radians[i] finite, n in 0..128. */
+qlin_status qlin_rope_turns(const double* radians, int n, uint64_t* turns);
+
+/*
+ * The projected rows of a step into the cache: q' = R(q * q_gamma / rms(q))
+ * head by head, k' likewise, and k' and v stored behind the sequences'
+ * committed tokens.  rms(x)^2 = mean(x^2) + eps over one head; R rotates the
+ * first 2 * n_turns elements of a head by the row's position.
+ *   Hq            : query heads (0 with q = NULL).
+ *   src           : type of q, k, v: QLIN_F32 (what qlin_forward writes) or
+ *                   QLIN_BF16.
+ *   q, k, v       : [B * T, heads * width], rows *_stride elements apart,
+ *                   16-byte aligned rows.  q may be NULL (nothing is written
+ *                   to q_out); k and v may both be NULL (nothing is stored).
+ *   q_out         : [B * T, Hq * width] in the cache's type, rows
+ *                   q_out_stride elements apart, 16-byte aligned rows.
+ *   q_gamma, k_gamma : fp32 [width], 16-byte aligned, or NULL: no norm.
+ *   turns, n_turns   : device, from qlin_rope_turns, 8-byte aligned;
+ *                   n_turns in 0..width / 2 (0: no rotation).
+ *   pairs         : 0: element i turns with i + n_turns; 1: 2i with 2i + 1.
+ *   ws            : a workspace (256 bytes) for the status word, or NULL.
+ *   flags         : 0 or QLIN_FLAG_PDL (gamma and turns are read early).
+ * T is not limited: a prompt's rows are appended the same way.  Computed in
+ * fp32 (the angle exactly, see above) and rounded once.
+ */
+qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, int src, const void* q,
+                           int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const float* q_gamma, const float* k_gamma, float eps, const uint64_t* turns, int n_turns,
+                           int pairs, void* q_out, int64_t q_out_stride, void* ws, size_t ws_bytes, unsigned flags,
+                           void* stream);
+
+/*
+ * Attention of a step's rows over the cache: every row sees all committed
+ * tokens of its sequence, and of the step's own rows (already appended) those
+ * that its mask names.  out = sum_j softmax_j(scale * q . k_j) v_j; a row that
+ * sees nothing gives zeros.  Query head h reads cache head h / (Hq / heads).
+ * Masked rows of the step contribute nothing whatever they hold (NaN too).
+ *   T         : 1..32 rows per sequence, T * Hq / heads <= 128.
+ *   Hq        : a multiple of the cache's heads.
+ *   q         : [B * T, Hq * width], the cache's type, rows q_stride elements
+ *               apart, 16-byte aligned rows (q_out of qlin_kv_append).
+ *   out       : bf16 [B * T, Hq * width], rows out_stride elements apart,
+ *               16-byte aligned rows (the o projection's activation).
+ *   scale     : finite.
+ *   ws        : 256-byte aligned, at least
+ *               qlin_tree_attention_workspace_bytes; its first word is the
+ *               status word.  Calls that overlap on the GPU need workspaces
+ *               of their own.
+ *   flags     : 0 or QLIN_FLAG_PDL.
+ * Scores, softmax statistics and sums are fp32; the weights are rounded to the
+ * cache's type for the product with v.  The result does not depend on the
+ * other sequences' values, only (in the order of its sums) on all lengths.
+ */
+#define QLIN_MAX_TREE 32
+qlin_status qlin_tree_attention_workspace_bytes(const qlin_kv_cache* cache, int B, int T, int Hq, size_t* bytes);
+qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, const void* q,
+                                int64_t q_stride, float scale, void* out, int64_t out_stride, void* ws,
+                                size_t ws_bytes, unsigned flags, void* stream);
+
+/*
+ * Keeps an accepted path of a verified tree: row keep[b][i] of sequence b
+ * moves to token len[b] + i, for i < n_keep[b], and len_out[b] = len[b] +
+ * n_keep[b].  The kept rows are given in increasing order (a row's parent
+ * stands before it); a list that is not, or that names a row outside
+ * 0..count[b] - 1, moves nothing, len_out[b] = len[b], and the status word gets
+ * QLIN_ERR_BAD_INDEX.
+ *   keep    : int32 [B, T], rows keep_stride entries apart.
+ *   n_keep  : int32 [B], 0..count[b].
+ *   len_out : int32 [B], or NULL; may be step->len itself.  Not written where
+ *             len[b] < 0.
+ *   ws      : a workspace (256 bytes) for the status word, or NULL.
+ * T <= 32.  depth and mask are not read.
+ */
+qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, const int32_t* keep,
+                         int64_t keep_stride, const int32_t* n_keep, int32_t* len_out, void* ws, size_t ws_bytes,
+                         unsigned flags, void* stream);
+
+/*
+ * One token per row of logits, from a given uniform number.  The row's tokens
+ * stand in order of their logits, equal ones by index.  Kept are the first
+ * top_k; of those the shortest beginning whose mass is at least top_p of
+ * theirs; of those the ones with w >= min_p, where w = exp((x - max) /
+ * temperature).  The token is the first kept one, in order of the vocabulary,
+ * at which the running sum of the kept w exceeds u times their sum.
+ *   logits      : [M, V] of type dtype (QLIN_F32 or QLIN_BF16), rows ld
+ *                 elements apart, aligned to the element.  -inf: a forbidden
+ *                 token, never chosen; +inf: only those tokens are left, alike.
+ *   M >= 0, V   : 1..524288.
+ *   u           : fp32 [M], in [0, 1); values outside are clamped.
+ *   temperature : fp32 [M] or NULL (1).  Not above 0 (or NaN): the row's
+ *                 largest logit, the lowest index of equal ones, prob = 1.
+ *   top_k       : int32 [M] or NULL; below 1 or above V - 1: all tokens.
+ *   top_p       : fp32 [M] or NULL; 1 and above, or NaN: all; 0 and below:
+ *                 the first token alone.
+ *   min_p       : fp32 [M] or NULL; 0 and below, or NaN: all; above 1: as 1.
+ *   token       : int32 [M].  -1 for a row of -inf alone or with a NaN.
+ *   prob        : fp32 [M] or NULL: the token's share of the kept mass (0 with
+ *                 token -1).
+ * The weights are 42-bit fractions (relative error below 2^-31 for w above
+ * 2^-10; a token with w below 2^-43 has none and is never chosen) and every sum of them is an exact integer, so the token does not
+ * depend on an order of summation.
+ */
+#define QLIN_SAMPLE_MAX_V 524288
+qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logits, int64_t ld, const float* u,
+                        const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                        int32_t* token, float* prob, unsigned flags, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,641 @@
+"""The step operators on the GPU against plain 64-bit forms (tests/step_ref.py):
+append with head norms and rotation, tree attention, keep, sampling, and a run
+of them together with the linears."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import step_ref as R
+from gpu_util import DEV, built
+from w6a8_quantized_linear_gb300 import inputs, qlin
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    built()
+    torch.cuda.set_device(DEV)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+class Case:
+    """A cache whose every place that no token lies on holds NaN, a page table in
+    random order, and a step over it."""
+
+    def __init__(self, lens, T, heads, width, page, dtype=BF, layout="hnd", seed=0, parents=None, count=None, tree="shared",
+                 fill=True):
+        g = torch.Generator().manual_seed(seed)
+        self.lens, self.T, self.heads, self.width, self.page, self.dtype, self.count = lens, T, heads, width, page, dtype, count
+        B = len(lens)
+        self.B = B
+        per = [max(1, -(-(max(n, 0) + T) // page)) for n in lens]
+        pages = sum(per) + 2
+        order = torch.randperm(pages, generator=g).tolist()
+        most = max(per) + 1
+        table = torch.full((B, most), -7, dtype=torch.int32)  # entries behind the last page are never read
+        for b in range(B):
+            table[b, : per[b]] = torch.tensor([order.pop() for _ in range(per[b])], dtype=torch.int32)
+        self.table = table
+        shape = (pages, heads, page, width) if layout != "nhd" else (pages, page, heads, width)
+        if layout == "pool":  # k and v of several layers in one pool: slices with wide strides
+            pool = torch.full((pages, 2, 3, heads, page, width), math.nan, dtype=dtype, device=DEV)
+            self.k, self.v = pool[:, 0, 1], pool[:, 1, 1]
+        else:
+            self.k, self.v = (torch.full(shape, math.nan, dtype=dtype, device=DEV) for _ in range(2))
+            if layout == "nhd":
+                self.k, self.v = self.k.transpose(1, 2), self.v.transpose(1, 2)
+        self.host = []  # each sequence's [tokens, heads, width] k and v
+        for b, n in enumerate(lens):
+            m = max(n, 0) + (self.used(b) if fill else 0)
+            k, v = (torch.randn(m, heads, width, generator=g).to(dtype) for _ in range(2))
+            self.host.append([k, v])
+            if m:
+                self.put(b, 0, k, v)
+        parents = parents if parents is not None else [t - 1 for t in range(T)]
+        depth, mask = [], []
+        for t in range(T):
+            depth.append(0 if parents[t] < 0 else depth[parents[t]] + 1)
+            mask.append((0 if parents[t] < 0 else mask[parents[t]]) | 1 << t)
+        self.depth, self.mask = depth, mask
+        if tree == "none":
+            td = tm = None
+        else:
+            td, tm = i32(depth), torch.tensor(mask, dtype=torch.int64).to(torch.int32).to(DEV)
+            if tree == "each":
+                td, tm = td.repeat(B, 1).contiguous(), tm.repeat(B, 1).contiguous()
+        self.cache = qlin.KVCache(self.k, self.v)
+        self.step = qlin.KVStep(table.to(DEV), i32(lens), T, count=None if count is None else i32(count), depth=td, mask=tm)
+
+    def used(self, b):
+        return R.rows_in_use(self.lens, self.count, self.T, b)
+
+    def places(self, b, first, n):
+        at = torch.arange(first, first + n)
+        return self.table[b].long()[at // self.page].to(DEV), (at % self.page).to(DEV)
+
+    def put(self, b, first, k, v):
+        p, r = self.places(b, first, k.shape[0])
+        self.k[p, :, r], self.v[p, :, r] = k.to(DEV), v.to(DEV)
+
+    def get(self, b, first, n):
+        p, r = self.places(b, first, n)
+        return self.k[p, :, r].cpu(), self.v[p, :, r].cpu()
+
+    def seen(self, b, t):
+        n = max(self.lens[b], 0)
+        m = torch.ones(n + self.used(b), dtype=torch.bool)
+        for j in range(self.used(b)):
+            m[n + j] = self.mask[t] >> j & 1
+        return m
+
+
+# ---- append ------------------------------------------------------------------------------------------------------
+
+APPEND = [
+    # lens, T, Hq, heads, width, page, dtype, src, rot, pairs, layout
+    ([0], 1, 4, 4, 64, 16, BF, torch.float32, 64, False, "hnd"),
+    ([15], 1, 24, 4, 256, 64, BF, torch.float32, 64, False, "hnd"),
+    ([100, 3, 16], 8, 12, 2, 128, 16, FP, torch.float32, 128, True, "nhd"),
+    ([1000003], 3, 5, 1, 128, 256, BF, torch.bfloat16, 32, False, "hnd"),
+    ([7, 250], 33, 6, 3, 64, 32, FP, torch.bfloat16, 10, True, "pool"),
+    ([31], 67, 8, 8, 256, 128, BF, torch.float32, 256, False, "nhd"),
+    ([5], 2, 1, 1, 64, 16, BF, torch.float32, 0, False, "hnd"),
+]
+
+
+@pytest.mark.parametrize("case", APPEND, ids=[f"{i}" for i in range(len(APPEND))])
+def test_append_against_64_bits(case):
+    lens, T, Hq, heads, D, page, dtype, src, rot, pairs, layout = case
+    far = max(lens) > 100000  # a far position: the page table's first entries stay unused
+    c = Case([n % 1000 for n in lens] if far else lens, T, heads, D, page, dtype, layout, seed=3, fill=False, tree="none")
+    parents = torch.randint(0, 5, (T,), generator=torch.Generator().manual_seed(1)).tolist()
+    depth = [d + (lens[0] - c.lens[0] if far else 0) for d in parents]  # any distances do
+    c.step = qlin.KVStep(c.step.page_table, c.step.len, T, depth=i32(depth))
+    g = torch.Generator().manual_seed(11)
+    n = len(lens) * T
+    q = (torch.randn(n, Hq * D, generator=g) * 3).to(src)
+    k = (torch.randn(n, heads * D, generator=g) * 0.2).to(src)
+    v = torch.randn(n, heads * D, generator=g).to(src)
+    qg, kg = 0.5 + torch.rand(D, generator=g), 0.5 + torch.rand(D, generator=g)
+    theta = 5e5
+    radians = [theta ** (-2.0 * i / rot) for i in range(rot // 2)] if rot else []
+    before = [x.clone() for x in (c.k, c.v)]
+    turns = qlin.rope_turns(theta, rot, device=DEV) if rot else None
+    out = qlin.kv_append(c.cache, c.step, q=q.to(DEV), k=k.to(DEV), v=v.to(DEV), q_gamma=qg.to(DEV), k_gamma=kg.to(DEV),
+                         eps=1e-5, turns=turns, pairs=pairs)
+    assert out.dtype == dtype
+    touched = torch.zeros(c.k.shape[0], c.k.shape[2], dtype=torch.bool, device=DEV)
+    for b in range(c.B):
+        gk, gv = c.get(b, c.lens[b], T)
+        p, r = c.places(b, c.lens[b], T)
+        touched[p, r] = True
+        for t in range(T):
+            row = b * T + t
+            pos = c.lens[b] + depth[t]
+            ref = R.append_row(q[row].view(Hq, D), qg, 1e-5, pos, radians, pairs)
+            err = (out[row].cpu().double().view(Hq, D) - ref).abs()
+            assert (err <= R.append_bound(ref, dtype)).all(), (b, t, "q", float((err - R.append_bound(ref, dtype)).max()))
+            ref = R.append_row(k[row].view(heads, D), kg, 1e-5, pos, radians, pairs)
+            err = (gk[t].double() - ref).abs()
+            assert (err <= R.append_bound(ref, dtype)).all(), (b, t, "k", float((err - R.append_bound(ref, dtype)).max()))
+            assert torch.equal(gv[t], v[row].view(heads, D).to(dtype))
+    # nothing else of the cache has changed (compared as bits: it holds NaN)
+    for was, now in zip(before, (c.k, c.v)):
+        a, b_ = was.transpose(1, 2).contiguous().view(torch.int16), now.transpose(1, 2).contiguous().view(torch.int16)
+        assert torch.equal(a[~touched], b_[~touched])
+
+
+def test_append_parts_counts_and_absent_sequences():
+    c = Case([4, -1, 9, 20], 3, 2, 64, 16, count=[2, 3, 0, 3], fill=False, tree="none")
+    g = torch.Generator().manual_seed(5)
+    q, k, v = (torch.randn(12, h * 64, generator=g).to(DEV) for h in (4, 2, 2))
+    q_out = torch.full((12, 256), 7.0, dtype=BF, device=DEV)
+    before = c.k.clone()
+    turns = qlin.rope_turns(1e4, 64, device=DEV)
+    qlin.kv_append(c.cache, c.step, q=q, k=k, v=v, turns=turns, q_out=q_out)
+    used = [0, 1, 9, 10, 11]
+    rest = [r for r in range(12) if r not in used]
+    assert (q_out[rest] == 7).all()
+    radians = [1e4 ** (-2.0 * i / 64) for i in range(32)]
+    for row in used:
+        b, t = divmod(row, 3)
+        ref = R.append_row(q[row].cpu().view(4, 64), None, 0, c.lens[b] + t, radians, False)
+        assert ((q_out[row].cpu().double().view(4, 64) - ref).abs() <= R.append_bound(ref, BF)).all()
+    written = (~c.k.isnan() & before.isnan()).any(-1).any(1).sum()  # token places
+    assert written == 5
+    # q alone leaves the cache, k and v alone need no q
+    k0 = c.k.clone()
+    only = qlin.kv_append(c.cache, c.step, q=q, turns=turns, q_out=torch.full_like(q_out, 7.0))
+    assert torch.equal(only, q_out) and torch.equal(c.k.view(torch.int16), k0.view(torch.int16))
+    c.k.fill_(math.nan)
+    c.v.fill_(math.nan)
+    assert qlin.kv_append(c.cache, c.step, k=k, v=v, turns=turns) is None
+    gk, gv = c.get(3, 20, 3)
+    assert not gk.isnan().any() and torch.equal(gv, v[9:].cpu().view(3, 2, 64).to(BF))
+
+
+def test_append_takes_strided_rows_of_one_projection():
+    # q, k and v as columns of one [rows, (Hq + 2 heads) * width] buffer
+    c = Case([30], 5, 2, 128, 16, fill=False)
+    x = torch.randn(5, (4 + 4) * 128, device=DEV)
+    q, k, v = x[:, :512], x[:, 512:768], x[:, 768:]
+    a = qlin.kv_append(c.cache, c.step, q=q, k=k, v=v)
+    got = c.get(0, 30, 5)
+    assert torch.equal(a, q.to(BF)) and torch.equal(got[0].flatten(1), k.cpu().to(BF)) and torch.equal(got[1].flatten(1), v.cpu().to(BF))
+
+
+def test_append_reports_pages_out_of_range():
+    ws = qlin.new_workspace(256, DEV)
+    for bad in (-1, 10 ** 6, 2 ** 31 - 1):
+        c = Case([20], 2, 1, 64, 16, fill=False)
+        c.step.page_table[0, 1] = bad
+        before = c.k.clone()
+        k = torch.randn(2, 64, device=DEV)
+        qlin.workspace_init(ws)
+        out = qlin.kv_append(c.cache, c.step, q=k, k=k, v=k, ws=ws)
+        assert qlin.read_device_status(ws) == qlin.ERR_BAD_INDEX
+        assert torch.equal(c.k.view(torch.int16), before.view(torch.int16)) and torch.equal(out, k.to(BF))
+    c = Case([16 * 3 - 1], 1, 1, 64, 16, fill=False)  # a token behind the table
+    c.step.len.fill_(16 * 50)
+    qlin.workspace_init(ws)
+    qlin.kv_append(c.cache, c.step, k=torch.randn(1, 64, device=DEV), v=torch.randn(1, 64, device=DEV), ws=ws)
+    assert qlin.read_device_status(ws) == qlin.ERR_BAD_INDEX
+
+
+# ---- attention -----------------------------------------------------------------------------------------------------
+
+TREE8 = [-1, 0, 1, 0, 3, 3, 0, 6]
+
+
+def check_attention(c, Hq, q_seed=0, scale=None, q=None, **kw):
+    D = c.width
+    g = torch.Generator().manual_seed(q_seed)
+    if q is None:
+        q = torch.randn(c.B * c.T, Hq * D, generator=g).to(c.dtype)
+    out = torch.full((c.B * c.T, Hq * D), 3.0, dtype=BF, device=DEV)
+    ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, c.B, c.T, Hq), DEV)
+    got = qlin.tree_attention(c.cache, c.step, q.to(DEV), scale=scale, out=out, ws=ws, **kw)
+    assert qlin.read_device_status(ws) == qlin.OK
+    scale = D ** -0.5 if scale is None else scale
+    group = Hq // c.heads
+    got = got.cpu().double().view(c.B, c.T, Hq, D)
+    for b in range(c.B):
+        n = c.used(b)
+        assert (got[b, n:] == 3).all(), "rows not in use were written"
+        if n == 0:
+            continue
+        seen = torch.stack([c.seen(b, t) for t in range(n)])
+        for h in range(c.heads):
+            qq = q.view(c.B, c.T, Hq, D)[b, :n, h * group:(h + 1) * group].reshape(n * group, D)
+            k, v = c.host[b][0][:, h], c.host[b][1][:, h]
+            o, a, size, mass = R.attention_rows(qq, k, v, seen.repeat_interleave(group, 0), scale)
+            have = got[b, :n, h * group:(h + 1) * group].reshape(n * group, D)
+            far = (have - o).abs() - R.attention_bound(o, a, size, mass, D, c.dtype)
+            assert not have.isnan().any() and (far <= 0).all(), (b, h, float(far.max()), float((have - o).abs().max()))
+    return out
+
+
+ATTENTION = [
+    # lens, T, Hq, heads, width, page, dtype, layout, parents, count
+    ([0], 1, 1, 1, 64, 16, BF, "hnd", None, None),
+    ([1], 1, 4, 4, 128, 16, BF, "hnd", None, None),
+    ([0, 5], 8, 6, 1, 256, 32, BF, "hnd", TREE8, None),
+    ([15, 16, 17, 31, 32, 33], 1, 6, 2, 64, 16, FP, "nhd", None, None),
+    ([63, 64, 65, 127, 128, 129], 2, 6, 2, 128, 64, BF, "hnd", None, None),
+    ([255, 1, 256, 0, 257, 511], 3, 8, 1, 128, 32, FP, "pool", None, None),
+    ([700, -1, 3, 0], 8, 8, 4, 64, 16, BF, "hnd", TREE8, [8, 8, 3, 0]),
+    ([1333], 8, 48, 8, 128, 16, BF, "nhd", TREE8, None),
+    ([1777], 1, 24, 4, 256, 64, BF, "hnd", None, None),
+    ([2049], 8, 24, 4, 256, 256, FP, "hnd", TREE8, None),
+    ([900], 32, 4, 1, 128, 128, BF, "hnd", [-1] + [t // 2 for t in range(31)], None),
+    ([333, 90], 16, 16, 2, 64, 32, FP, "hnd", None, [16, 11]),
+    ([5, 40], 1, 128, 1, 128, 16, BF, "hnd", None, None),
+    ([3000, 10, 2999, 517, 1, 64, 128, 4000], 3, 16, 8, 64, 16, BF, "hnd", None, None),
+    ([20011], 8, 8, 1, 128, 64, BF, "hnd", TREE8, None),
+    ([9001], 1, 5, 5, 256, 16, FP, "nhd", None, None),
+]
+
+
+@pytest.mark.parametrize("case", ATTENTION, ids=[f"{i}" for i in range(len(ATTENTION))])
+def test_attention_against_64_bits(case):
+    lens, T, Hq, heads, D, page, dtype, layout, parents, count = case
+    c = Case(lens, T, heads, D, page, dtype, layout, seed=7, parents=parents, count=count, tree="shared" if parents else "none")
+    check_attention(c, Hq)
+
+
+def test_attention_trees_of_each_sequence_and_other_scales():
+    c = Case([70, 200, 9], 8, 2, 128, 16, parents=TREE8, tree="each", seed=2)
+    check_attention(c, 6, scale=0.5)
+    check_attention(c, 6, scale=0.0)
+    check_attention(c, 6, scale=-0.3)
+    # scores far beyond the range of exp: one token takes all, or the weights underflow
+    check_attention(c, 6, scale=40.0)
+
+
+def test_attention_empty_rows_are_zero():
+    c = Case([0, 12], 4, 2, 64, 16, parents=[-1, 0, 1, 2], seed=4)
+    c.mask = [0, 2, 0, 8]
+    c.step = qlin.KVStep(c.step.page_table, c.step.len, 4, mask=i32(c.mask))
+    out = check_attention(c, 4)
+    assert (out[0] == 0).all() and (out[2] == 0).all() and (out[1] != 0).any() and (out[4] != 0).any()
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_masked_rows_contribute_nothing(what, D):
+    """A drafted row that holds NaN or infinities reaches only the rows that see it."""
+    c = Case([130], 8, 2, D, 16, parents=TREE8, seed=8)
+    for x in c.host[0]:
+        x[130 + 4] = what  # row 4: seen by itself alone
+        x[130 + 6, :, 3] = what  # row 6: seen by rows 6 and 7
+    c.put(0, 0, *c.host[0])
+    q = torch.randn(8, 4 * D, generator=torch.Generator().manual_seed(1)).to(BF)
+    ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, 1, 8, 4), DEV)
+    out = qlin.tree_attention(c.cache, c.step, q.to(DEV), ws=ws).cpu()
+    clean = Case([130], 8, 2, D, 16, parents=TREE8, seed=8)
+    want = qlin.tree_attention(clean.cache, clean.step, q.to(DEV), ws=ws).cpu()
+    for t in (0, 1, 2, 3, 5):
+        assert torch.equal(out[t], want[t]), t
+    assert not out[4].isfinite().all()
+
+
+def test_attention_adversarial_maxima():
+    """Scores that rise along the cache, and jump, and a first token that dwarfs the rest."""
+    c = Case([5000], 8, 1, 128, 32, parents=TREE8, seed=9)
+    k, v = c.host[0]
+    ramp = torch.linspace(-3, 6, k.shape[0])
+    ramp[1700:1750] += 9
+    k[:, 0] = (ramp[:, None] * torch.ones(128)).to(BF)
+    c.put(0, 0, k, v)
+    q = torch.ones(8, 8 * 128).to(BF)
+    check_attention(c, 8, q=q)
+    check_attention(c, 8, q=-q)
+    k[0, 0] = 30
+    c.put(0, 0, k, v)
+    check_attention(c, 8, q=q)
+
+
+def test_attention_rows_do_not_depend_on_the_batch_values():
+    c = Case([400, 77], 4, 2, 128, 16, seed=12)
+    ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, 2, 4, 6), DEV)
+    q = torch.randn(8, 6 * 128, generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
+    a = qlin.tree_attention(c.cache, c.step, q, ws=ws)
+    q2 = q.clone()
+    q2[4:] = 5
+    b = qlin.tree_attention(c.cache, c.step, q2, ws=ws)
+    assert torch.equal(a[:4], b[:4])
+    for _ in range(3):  # the same call, the same bits
+        assert torch.equal(a, qlin.tree_attention(c.cache, c.step, q, ws=ws))
+
+
+def test_attention_bad_pages_are_reported_and_not_followed():
+    for bad in (-1, 10 ** 6, 2 ** 31 - 1, -2 ** 31):
+        c = Case([200, 40], 2, 2, 64, 16, seed=3)
+        c.step.page_table[0, 5] = bad
+        ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, 2, 2, 4), DEV)
+        q = torch.randn(4, 256, generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
+        out = qlin.tree_attention(c.cache, c.step, q, ws=ws)
+        assert qlin.read_device_status(ws) == qlin.ERR_BAD_INDEX
+        good = Case([200, 40], 2, 2, 64, 16, seed=3)
+        assert torch.equal(out[2:], qlin.tree_attention(good.cache, good.step, q)[2:])  # the other sequence's rows
+    c = Case([40], 2, 2, 64, 16, seed=3)
+    c.step.len.fill_(2 ** 31 - 5)  # a length far behind the table
+    ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, 1, 2, 4), DEV)
+    qlin.tree_attention(c.cache, c.step, torch.zeros(2, 256, dtype=BF, device=DEV), ws=ws)
+    assert qlin.read_device_status(ws) == qlin.ERR_BAD_INDEX
+
+
+def test_attention_replayed_with_other_lengths():
+    """One captured call serves every length that its table holds."""
+    c = Case([900], 4, 2, 128, 16, seed=21)
+    ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, 1, 4, 8), DEV)
+    q = torch.randn(4, 1024, generator=torch.Generator().manual_seed(2)).to(BF).to(DEV)
+    out = torch.empty(4, 1024, dtype=BF, device=DEV)
+    qlin.tree_attention(c.cache, c.step, q, out=out, ws=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qlin.tree_attention(c.cache, c.step, q, out=out, ws=ws)
+    for n in (900, 0, 1, 128, 129, 500, 900):
+        c.step.len.fill_(n)
+        g.replay()
+        eager = qlin.tree_attention(c.cache, c.step, q)
+        assert torch.equal(out, eager), n
+
+
+def test_attention_on_another_stream_and_with_strided_rows():
+    c = Case([300], 4, 2, 64, 32, seed=5)
+    buf = torch.randn(4, 3 * 256, generator=torch.Generator().manual_seed(3)).to(BF).to(DEV)
+    want = qlin.tree_attention(c.cache, c.step, buf[:, 256:512].contiguous())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    wide = torch.zeros(4, 768, dtype=BF, device=DEV)
+    torch.cuda.synchronize()
+    got = qlin.tree_attention(c.cache, c.step, buf[:, 256:512], out=wide[:, 256:512], stream=s)
+    alloc = qlin.tree_attention(c.cache, c.step, buf[:, 256:512], stream=s)
+    s.synchronize()
+    assert torch.equal(got, want) and torch.equal(alloc, want)
+    assert (wide[:, :256] == 0).all() and (wide[:, 512:] == 0).all()
+
+
+# ---- keep ------------------------------------------------------------------------------------------------------------
+
+KEEP = [([10], 8, 2, 128, 16, BF, "hnd", [[0, 3, 5, 7]]), ([0, 31, 500, -1, 7], 32, 5, 64, 32, FP, "nhd",
+        [[1, 2, 30, 31], list(range(32)), [], [0, 1], [31]]), ([1, 14], 5, 8, 256, 16, BF, "pool", [[0, 4], [2, 3, 4]])]
+
+
+@pytest.mark.parametrize("case", KEEP, ids=["0", "1", "2"])
+def test_keep_moves_the_accepted_rows(case):
+    lens, T, heads, D, page, dtype, layout, kept = case
+    c = Case(lens, T, heads, D, page, dtype, layout, seed=6)
+    keep = torch.full((len(lens), T), 99, dtype=torch.int32)
+    for b, rows in enumerate(kept):
+        keep[b, : len(rows)] = torch.tensor(rows, dtype=torch.int32)
+    ws = qlin.new_workspace(256, DEV)
+    out = torch.full((len(lens),), -5, dtype=torch.int32, device=DEV)
+    qlin.kv_keep(c.cache, c.step, keep.to(DEV), i32([len(r) for r in kept]), len_out=out, ws=ws)
+    assert qlin.read_device_status(ws) == qlin.OK
+    for b, rows in enumerate(kept):
+        if lens[b] < 0:
+            assert out[b] == -5
+            continue
+        assert out[b] == lens[b] + len(rows)
+        for i, x in enumerate(c.get(b, 0, lens[b] + T)):
+            want = c.host[b][i].clone()
+            want[lens[b]: lens[b] + len(rows)] = c.host[b][i][[lens[b] + r for r in rows]]
+            assert torch.equal(x, want)
+
+
+def test_keep_in_place_lengths_and_bad_lists():
+    ws = qlin.new_workspace(256, DEV)
+    lists = [[0, 2], [2, 1], [0, 0], [1, 4], [-1, 2], [0, 1], [3, 3]]
+    counts = [2, 2, 2, 2, 2, 5, -1]
+    c = Case([20] * len(lists), 4, 2, 64, 16, seed=6)
+    keep = torch.zeros(len(lists), 4, dtype=torch.int32)
+    keep[:, :2] = torch.tensor(lists, dtype=torch.int32)
+    qlin.kv_keep(c.cache, c.step, keep.to(DEV), i32(counts), len_out=c.step.len, ws=ws)
+    assert qlin.read_device_status(ws) == qlin.ERR_BAD_INDEX
+    assert c.step.len.tolist() == [22] + [20] * (len(lists) - 1)
+    for b in range(1, len(lists)):
+        for x, y in zip(c.get(b, 0, 24), c.host[b]):
+            assert torch.equal(x, y)
+    qlin.kv_keep(c.cache, c.step, keep.to(DEV), i32([1] + [0] * (len(lists) - 1)), len_out=c.step.len)
+    assert c.step.len.tolist() == [23] + [20] * (len(lists) - 1)
+
+
+# ---- sample ----------------------------------------------------------------------------------------------------------
+
+def logits_of(M, V, seed, dtype=torch.float32, banned=0.0, spread=2.5):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, V, generator=g) * spread
+    x.scatter_(1, torch.randint(0, V, (M, 8), generator=g), 6 + 5 * torch.rand(M, 8, generator=g))
+    if banned:
+        x.masked_fill_(torch.rand(M, V, generator=g) < banned, -math.inf)
+    return x.to(dtype), torch.rand(M, generator=g)
+
+
+def check_sample(x, u, **kw):
+    M = x.shape[0]
+    dev = {n: None if t is None else t.to(DEV) for n, t in kw.items()}
+    prob = torch.full((M,), -1.0, device=DEV)
+    token = qlin.sample(x.to(DEV), u.to(DEV), prob=prob, **dev)
+    rows = x.double().numpy()
+    for m in range(M):
+        pick = {n: float(t[m]) if n != "top_k" else int(t[m]) for n, t in kw.items() if t is not None}
+        want, p = R.sample_row(rows[m], float(u[m]), **pick)
+        assert int(token[m]) == want, (m, pick, float(u[m]), int(token[m]), want)
+        # weights within 2^-31 of theirs or half of 2^-42, sums of them, rounded to fp32
+        assert abs(float(prob[m]) - p) <= 2.0 ** -24 * p + 2.0 ** -29 * p + 2.0 ** -42 * len(rows[m]), (m, float(prob[m]), p)
+    return token
+
+
+SIZES = [1, 2, 31, 33, 1000, 4096, 4097, 32000, 50001, 131071, 262144, 300007, 524288]
+
+
+@pytest.mark.parametrize("V", SIZES)
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_sample_against_64_bits(V, dtype):
+    M = 4
+    x, u = logits_of(M, V, V, dtype)
+    f = torch.tensor
+    check_sample(x, u)
+    check_sample(x, u, temperature=f([0.7, 1.3, 0.0, 5.0]))
+    check_sample(x, u, top_k=f([1, 50, 0, V + 3], dtype=torch.int32))
+    check_sample(x, u, top_p=f([0.9, 0.5, 1.0, 0.999]), temperature=f([1.0, 2.0, 0.9, 30.0]))
+    check_sample(x, u, min_p=f([0.05, 0.3, 0.0, 1.0]))
+    check_sample(x, u, temperature=f([0.8, 1.0, 1.2, 3.0]), top_k=f([40, 400, 7, 3], dtype=torch.int32),
+                 top_p=f([0.95, 0.8, 0.3, 0.99]), min_p=f([0.02, 0.01, 0.1, 0.0]))
+
+
+def test_sample_many_rows_and_banned_tokens():
+    x, u = logits_of(70, 5003, 1, banned=0.4)
+    g = torch.Generator().manual_seed(9)
+    check_sample(x, u, temperature=torch.rand(70, generator=g) * 2, top_k=torch.randint(-3, 6000, (70,), generator=g, dtype=torch.int32),
+                 top_p=torch.rand(70, generator=g) * 1.2, min_p=torch.rand(70, generator=g) * 0.2 - 0.05)
+
+
+@pytest.mark.parametrize("V", [5, 1000, 40000])
+def test_sample_ties_go_to_the_lowest_index(V):
+    """Few distinct values: every border runs through equal logits."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.randint(0, 3, (8, V), generator=g).float() * 0.5
+    x[7] = 1.25  # all equal
+    u = torch.rand(8, generator=g)
+    k = torch.tensor([1, 2, V // 2 + 1, V - 1, 3, V // 3 + 1, 2, V // 2], dtype=torch.int32)
+    check_sample(x, u, top_k=k)
+    check_sample(x, u, top_p=torch.tensor([0.1, 0.37, 0.5, 0.9, 0.99, 0.71, 0.013, 0.33]))
+    check_sample(x, u, top_k=k, top_p=torch.tensor([0.1, 0.37, 0.5, 0.9, 0.99, 0.71, 0.013, 0.33]))
+    check_sample(x, u, min_p=torch.tensor([1.0, 0.99, 0.5, 0.36, 0.2, 0.7, 2.0, 1.0]))
+    check_sample(x, u, temperature=torch.zeros(8))
+
+
+def test_sample_edges():
+    inf, nan = math.inf, math.nan
+    rows = [[-inf] * 5, [0, 1, nan, 2, 3], [inf, 0, inf, 1, -inf], [-inf, -inf, 4, -inf, -inf], [3e38, -3e38, 0, 3e38, 1e38],
+            [-0.0, 0.0, -0.0, 0.0, -1.0], [1e-40, 2e-40, 0, -1e-40, 1e-45], [-1e30, -1e30, -2e30, -3e30, -inf],
+            [88.0, -88.0, 87.5, 0.0, 1.0], [inf, nan, 0, 0, 0]]
+    x = torch.tensor(rows)
+    M = len(rows)
+    one = lambda v: torch.full((M,), float(v))  # noqa: E731
+    for u in (0.0, 0.3, 0.5, 0.75, 1 - 2.0 ** -24, 1.0, -2.0, 7.0):
+        for kw in ({}, dict(top_k=torch.full((M,), 2, dtype=torch.int32)), dict(top_p=one(0.6)), dict(top_p=one(0.0)), dict(top_p=one(-1)),
+                   dict(top_p=one(nan)), dict(min_p=one(0.9)), dict(min_p=one(nan)), dict(temperature=one(0)), dict(temperature=one(-1)),
+                   dict(temperature=one(nan)), dict(temperature=one(1e-30)), dict(temperature=one(1e30)),
+                   dict(top_k=torch.full((M,), 3, dtype=torch.int32), top_p=one(0.9), min_p=one(0.1))):
+            check_sample(x, one(u), **kw)
+    t = qlin.sample(x.to(DEV), one(0.5).to(DEV), temperature=one(inf).to(DEV))  # every token that is not forbidden, alike
+    assert t.tolist()[:4] == [-1, -1, 2, 2] and int(t[8]) == 2
+
+
+def test_sample_strided_rows_and_replay():
+    x, u = logits_of(3, 9001, 4)
+    wide = torch.full((3, 20000), math.nan)
+    wide[:, 7:9008] = x
+    wide = wide.to(DEV)
+    top_p = torch.tensor([0.9, 0.8, 0.7]).to(DEV)
+    want = check_sample(x, u, top_p=top_p.cpu())
+    assert torch.equal(want, qlin.sample(wide[:, 7:9008], u.to(DEV), top_p=top_p))
+    du, token = u.to(DEV), torch.empty(3, dtype=torch.int32, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qlin.sample(wide[:, 7:9008], du, top_p=top_p, token=token)
+    for i in range(5):
+        fresh = torch.rand(3, generator=torch.Generator().manual_seed(i))
+        du.copy_(fresh)
+        g.replay()
+        assert torch.equal(token, check_sample(x, fresh, top_p=top_p.cpu()))
+
+
+def test_sample_frequencies_follow_the_weights():
+    """A grid of uniform numbers: each token's share of them is its probability."""
+    n = 4096
+    x = torch.tensor([[0.0, 1.0, -1.0, 2.0, -math.inf, 0.5]]).repeat(n, 1)
+    u = (torch.arange(n) + 0.5) / n
+    got = torch.bincount(qlin.sample(x.to(DEV), u.to(DEV)).cpu().long(), minlength=6).double() / n
+    assert (got - torch.softmax(x[0].double(), 0)).abs().max() <= 1.0 / n + 1e-9  # a share's ends fall between grid points
+
+
+# ---- together --------------------------------------------------------------------------------------------------------
+
+def test_a_verification_step_with_the_linears():
+    """qkv linear -> append -> tree attention -> o linear -> logits linear -> sample
+    -> keep, eager and as one replayed graph, against 64-bit forms of each part on
+    the bits the part before it gave; and the kept cache equals one into which
+    only the accepted rows were appended."""
+    K, D, Hq, heads, V, T, page = 512, 128, 8, 2, 1040, 8, 16
+    n0 = 45
+    kept_rows = [0, 3, 5]
+    ws = qlin.new_workspace(256, DEV)
+
+    def weight(N, Kw, seed):
+        cs = inputs.make_case("w4a8", "none", 1, N, Kw, 128, seed=seed)
+        w = cs.wbuf.to(DEV)
+        qlin.repack(w, "w4a8", N, Kw, 128)
+        return w
+
+    Ns = [Hq * D, heads * D, heads * D]
+    wqkv = [weight(N, K, 10 + i) for i, N in enumerate(Ns)]
+    wo, wv = weight(K, Hq * D, 20), weight(V, K, 21)
+    gamma = torch.rand(K, device=DEV) + 0.5
+    qg, kg = (torch.rand(D, device=DEV) + 0.5 for _ in range(2))
+    turns = qlin.rope_turns(1e6, D, device=DEV)
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(T, K, generator=g).to(BF).to(DEV)
+    u = torch.rand(T, generator=g).to(DEV)
+    top_p = torch.full((T,), 0.9, device=DEV)
+    c = Case([n0], T, heads, D, page, seed=30, parents=TREE8, fill=False)
+    start = [t.clone() for t in (c.k, c.v)]
+    aws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, 1, T, Hq), DEV)
+    keep = torch.zeros(1, T, dtype=torch.int32)
+    keep[0, :3] = torch.tensor(kept_rows, dtype=torch.int32)
+    keep, n_keep = keep.to(DEV), i32([3])
+    y = [torch.empty(T, N, device=DEV) for N in Ns]
+    q, att = torch.empty(T, Hq * D, dtype=BF, device=DEV), torch.empty(T, Hq * D, dtype=BF, device=DEV)
+    h, logits = torch.empty(T, K, device=DEV), torch.empty(T, V, device=DEV)
+    token = torch.empty(T, dtype=torch.int32, device=DEV)
+
+    def run(flags):
+        qlin.forward_multi("w4a8", "rmsnorm", wqkv, Ns, K, 128, x=x, gamma=gamma, y=y, ws=ws, flags=flags)
+        qlin.kv_append(c.cache, c.step, q=y[0], k=y[1], v=y[2], q_gamma=qg, k_gamma=kg, turns=turns, q_out=q, ws=ws, flags=flags)
+        qlin.tree_attention(c.cache, c.step, q, out=att, ws=aws, flags=flags)
+        qlin.forward("w4a8", "none", wo, K, Hq * D, 128, x=att, y=h, ws=ws, flags=flags)
+        h16 = (h * 0.01).to(BF)
+        qlin.forward("w4a8", "rmsnorm", wv, V, K, 128, x=h16, gamma=gamma, y=logits, ws=ws)
+        qlin.sample(logits, u, top_p=top_p, token=token, flags=flags)
+        qlin.kv_keep(c.cache, c.step, keep, n_keep, len_out=c.step.len, ws=ws, flags=flags)
+
+    run(0)
+    results = [t.clone() for t in (*y, q, att, h, logits, token)]
+    assert qlin.read_device_status(ws) == qlin.OK and qlin.read_device_status(aws) == qlin.OK
+    assert int(c.step.len[0]) == n0 + 3
+    # the parts against 64 bits
+    radians = [1e6 ** (-2.0 * i / D) for i in range(D // 2)]
+    ks = []
+    for t in range(T):
+        pos = n0 + c.depth[t]
+        ref = R.append_row(y[0][t].cpu().view(Hq, D), qg.cpu(), 1e-6, pos, radians, False)
+        assert ((q[t].cpu().double().view(Hq, D) - ref).abs() <= R.append_bound(ref, BF)).all()
+        ks.append(R.append_row(y[1][t].cpu().view(heads, D), kg.cpu(), 1e-6, pos, radians, False))
+    got_k, got_v = c.get(0, n0, 3)
+    for i, r in enumerate(kept_rows):
+        assert ((got_k[i].double() - ks[r]).abs() <= R.append_bound(ks[r], BF)).all()
+        assert torch.equal(got_v[i], y[2][r].cpu().view(heads, D).to(BF))
+    for m in range(T):
+        want, _ = R.sample_row(logits[m].double().cpu().numpy(), float(u[m]), top_p=float(top_p[m]))
+        assert int(token[m]) == want
+    # the accepted rows alone, appended as a chain of three, give the same cache and attention bits
+    after = [t.clone() for t in (c.k, c.v)]
+    chain = Case([n0], 3, heads, D, page, seed=30, fill=False, tree="none")
+    chain.table[0] = c.table[0][: chain.table.shape[1]]
+    chain.k, chain.v = start[0].clone(), start[1].clone()
+    chain.cache = qlin.KVCache(chain.k, chain.v)
+    chain.step = qlin.KVStep(c.step.page_table, i32([n0]), 3)
+    sel = torch.tensor(kept_rows, device=DEV)
+    q3 = qlin.kv_append(chain.cache, chain.step, q=y[0][sel].contiguous(), k=y[1][sel].contiguous(), v=y[2][sel].contiguous(),
+                        q_gamma=qg, k_gamma=kg, turns=turns)
+    # row 3 stands at depth 1, row 5 at depth 2: the same positions as the chain's
+    assert [c.depth[r] for r in kept_rows] == [0, 1, 2] and torch.equal(q3, q[sel])
+    for a, b in zip(c.get(0, 0, n0 + 3), chain.get(0, 0, n0 + 3)):
+        assert torch.equal(a, b)
+    # one graph of the whole step, with and without programmatic dependent launch
+    for flags in (0, qlin.FLAG_PDL):
+        c.step.len.fill_(n0)
+        c.k.copy_(start[0]), c.v.copy_(start[1])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(flags)
+        for t in (*y, q, att, h, logits):
+            t.zero_()
+        graph.replay()
+        for a, b in zip(results, (*y, q, att, h, logits, token)):
+            assert torch.equal(a, b)
+        assert int(c.step.len[0]) == n0 + 3
+        for a, b in zip(after, (c.k, c.v)):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))

@@ -1,0 +1,178 @@
+"""The step operators (append, tree attention, keep, sample) on the host: what
+they refuse before anything reaches the GPU, empty calls, and the rotation
+frequencies."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import __graft_entry__
+from w6a8_quantized_linear_gb300 import qlin
+
+
+@pytest.fixture(scope="module")
+def L():
+    __graft_entry__.build()
+    return qlin.lib()
+
+
+def cache(**kw):
+    """A cache struct whose addresses are never followed."""
+    a = dict(k=4096, v=8192, pages=10, page_stride=4 * 16 * 128, head_stride=16 * 128, token_stride=128, dtype=0, heads=4,
+             width=128, page_size=16)
+    a.update(kw)
+    return qlin._CacheStruct(**a)
+
+
+def step(**kw):
+    a = dict(page_table=4096, len=4096, count=None, depth=None, mask=None, table_stride=5, tree_stride=0, B=2, T=3, max_pages=5)
+    a.update(kw)
+    return qlin._StepStruct(**a)
+
+
+BAD_CACHE = [
+    (dict(k=None), qlin.ERR_INVALID_ARG), (dict(v=4104), qlin.ERR_INVALID_ARG), (dict(dtype=2), qlin.ERR_INVALID_ARG),
+    (dict(dtype=-1), qlin.ERR_INVALID_ARG), (dict(heads=0), qlin.ERR_INVALID_ARG), (dict(pages=0), qlin.ERR_INVALID_ARG),
+    (dict(pages=1 << 31), qlin.ERR_INVALID_ARG), (dict(width=96), qlin.ERR_UNSUPPORTED), (dict(width=512), qlin.ERR_UNSUPPORTED),
+    (dict(page_size=8), qlin.ERR_UNSUPPORTED), (dict(page_size=48), qlin.ERR_UNSUPPORTED), (dict(page_size=512), qlin.ERR_UNSUPPORTED),
+    (dict(page_size=0), qlin.ERR_UNSUPPORTED), (dict(token_stride=120), qlin.ERR_INVALID_ARG),
+    (dict(token_stride=132), qlin.ERR_INVALID_ARG), (dict(head_stride=0), qlin.ERR_INVALID_ARG),
+    (dict(page_stride=-8), qlin.ERR_INVALID_ARG), (dict(page_stride=(1 << 36) + 8), qlin.ERR_INVALID_ARG),
+]
+BAD_STEP = [
+    (dict(B=-1), qlin.ERR_INVALID_ARG), (dict(T=-1), qlin.ERR_INVALID_ARG), (dict(page_table=None), qlin.ERR_INVALID_ARG),
+    (dict(len=None), qlin.ERR_INVALID_ARG), (dict(len=4098), qlin.ERR_INVALID_ARG), (dict(max_pages=0), qlin.ERR_INVALID_ARG),
+    (dict(table_stride=4), qlin.ERR_INVALID_ARG), (dict(count=2), qlin.ERR_INVALID_ARG), (dict(mask=2), qlin.ERR_INVALID_ARG),
+    (dict(depth=2), qlin.ERR_INVALID_ARG), (dict(tree_stride=2), qlin.ERR_INVALID_ARG), (dict(tree_stride=-3), qlin.ERR_INVALID_ARG),
+]
+
+
+def append(L, c=None, s=None, **kw):
+    a = dict(Hq=8, src=2, q=4096, qs=1024, k=4096, ks=512, v=4096, vs=512, qg=None, kg=None, eps=1e-6, turns=None, nt=0, pairs=0,
+             qo=4096, qos=1024, ws=None, wsb=0, flags=0)
+    a.update(kw)
+    c, s = c or cache(), s or step()
+    return L.qlin_kv_append(ctypes.addressof(c), ctypes.addressof(s), a["Hq"], a["src"], a["q"], a["qs"], a["k"], a["ks"], a["v"],
+                            a["vs"], a["qg"], a["kg"], a["eps"], a["turns"], a["nt"], a["pairs"], a["qo"], a["qos"], a["ws"],
+                            a["wsb"], a["flags"], None)
+
+
+def attention(L, c=None, s=None, **kw):
+    a = dict(Hq=8, q=4096, qs=1024, scale=0.1, out=4096, os=1024, ws=4096, wsb=1 << 30, flags=0)
+    a.update(kw)
+    c, s = c or cache(), s or step()
+    return L.qlin_tree_attention(ctypes.addressof(c), ctypes.addressof(s), a["Hq"], a["q"], a["qs"], a["scale"], a["out"], a["os"],
+                                 a["ws"], a["wsb"], a["flags"], None)
+
+
+def keep(L, c=None, s=None, **kw):
+    a = dict(keep=4096, ks=3, n=4096, lo=4096, ws=None, wsb=0, flags=0)
+    a.update(kw)
+    c, s = c or cache(), s or step()
+    return L.qlin_kv_keep(ctypes.addressof(c), ctypes.addressof(s), a["keep"], a["ks"], a["n"], a["lo"], a["ws"], a["wsb"],
+                          a["flags"], None)
+
+
+@pytest.mark.parametrize("call", [append, attention, keep])
+def test_bad_caches_and_steps_are_refused(L, call):
+    for kw, want in BAD_CACHE:
+        assert call(L, c=cache(**kw)) == want, kw
+    for kw, want in BAD_STEP:
+        assert call(L, s=step(**kw)) == want, kw
+    # no sequences or no rows: nothing is read, nothing enqueued
+    assert call(L, s=step(B=0, page_table=None, len=None)) == qlin.OK
+    assert call(L, s=step(T=0, page_table=None, len=None)) == qlin.OK
+    assert call(L, flags=2) == qlin.ERR_INVALID_ARG
+
+
+def test_append_refusals(L):
+    bad = qlin.ERR_INVALID_ARG
+    for kw in (dict(src=1), dict(src=3), dict(Hq=-1), dict(Hq=0), dict(q=4100), dict(qs=1023), dict(qs=1026), dict(qs=1016),
+               dict(k=None), dict(v=None), dict(k=4104), dict(ks=508), dict(vs=514), dict(qo=None), dict(qo=4104), dict(qos=1020),
+               dict(qg=8), dict(kg=4), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(nt=-1), dict(nt=65),
+               dict(nt=64), dict(nt=64, turns=4), dict(pairs=2), dict(ws=128, wsb=256)):
+        assert append(L, **kw) == bad, kw
+    assert append(L, ws=256, wsb=255) == qlin.ERR_WORKSPACE
+    assert append(L, Hq=16385, qs=16385 * 128, qos=16385 * 128) == qlin.ERR_UNSUPPORTED
+    assert append(L, q=None, k=None, v=None) == qlin.OK  # nothing to do
+    # rows beyond 2^31 - 1 do not fit a launch
+    assert append(L, s=step(B=1 << 16, T=1 << 15)) == qlin.ERR_UNSUPPORTED
+
+
+def test_attention_refusals(L):
+    bad = qlin.ERR_INVALID_ARG
+    for kw in (dict(Hq=0), dict(Hq=-4), dict(Hq=6), dict(q=None), dict(q=4104), dict(qs=1016), dict(qs=1028), dict(out=None),
+               dict(out=4104), dict(os=1012), dict(scale=math.nan), dict(scale=math.inf), dict(ws=None), dict(ws=128)):
+        assert attention(L, **kw) == bad, kw
+    assert attention(L, s=step(T=33)) == qlin.ERR_UNSUPPORTED
+    assert attention(L, s=step(T=32), Hq=20) == qlin.ERR_UNSUPPORTED  # 160 query rows per cache head
+    assert attention(L, wsb=0) == qlin.ERR_WORKSPACE
+    n = ctypes.c_size_t()
+    c = cache()
+    assert L.qlin_tree_attention_workspace_bytes(ctypes.addressof(c), 2, 3, 8, ctypes.byref(n)) == qlin.OK
+    assert n.value >= 256
+    assert attention(L, wsb=n.value - 1) == qlin.ERR_WORKSPACE
+    assert L.qlin_tree_attention_workspace_bytes(ctypes.addressof(c), 2, 3, 8, None) == bad
+    assert L.qlin_tree_attention_workspace_bytes(ctypes.addressof(c), -1, 3, 8, ctypes.byref(n)) == bad
+    assert L.qlin_tree_attention_workspace_bytes(None, 2, 3, 8, ctypes.byref(n)) == bad
+
+
+def test_keep_refusals(L):
+    for kw in (dict(keep=None), dict(keep=2), dict(n=None), dict(n=6), dict(lo=2), dict(ks=2), dict(ws=128, wsb=256)):
+        assert keep(L, **kw) == qlin.ERR_INVALID_ARG, kw
+    assert keep(L, s=step(T=33), ks=33) == qlin.ERR_UNSUPPORTED
+    assert keep(L, ws=256, wsb=255) == qlin.ERR_WORKSPACE
+
+
+def test_sample_refusals(L):
+    def call(M=2, V=100, dtype=2, logits=4096, ld=100, u=4096, t=None, k=None, p=None, mp=None, token=4096, prob=None, flags=0):
+        return L.qlin_sample(M, V, dtype, logits, ld, u, t, k, p, mp, token, prob, flags, None)
+
+    bad = qlin.ERR_INVALID_ARG
+    for kw in (dict(M=-1), dict(V=0), dict(dtype=1), dict(dtype=3), dict(logits=None), dict(logits=4098), dict(ld=99), dict(u=None),
+               dict(u=2), dict(token=None), dict(token=2), dict(t=2), dict(k=2), dict(p=2), dict(mp=2), dict(prob=2), dict(flags=2)):
+        assert call(**kw) == bad, kw
+    assert call(V=524289, ld=524289) == qlin.ERR_UNSUPPORTED
+    assert call(M=1 << 25) == qlin.ERR_UNSUPPORTED
+    assert call(M=0, logits=None, u=None, token=None) == qlin.OK
+
+
+def test_rope_turns_are_exact_fractions(L):
+    # whole, half and quarter turns per position; negative ones from the other side
+    t = qlin.rope_turns(radians=[0.0, math.pi, math.pi / 2, -math.pi / 2, 2 * math.pi, 5 * math.pi], device="cpu")
+    want = [0, 1 << 63, 1 << 62, 3 << 62, 0, 1 << 63]
+    assert [int(x) & (2 ** 64 - 1) for x in t] == want
+    t = qlin.rope_turns(1e6, 64, device="cpu")
+    assert t.shape == (32,)
+    for i, x in enumerate(t):
+        assert int(x) / 2 ** 64 == pytest.approx(1e6 ** (-2 * i / 64) / (2 * math.pi), rel=2 ** -51)
+    assert qlin.rope_turns(1e4, 0, device="cpu").shape == (0,)
+    for kw in (dict(radians=[math.nan]), dict(radians=[math.inf]), dict(radians=[0.0] * 129)):
+        with pytest.raises(qlin.QlinError):
+            qlin.rope_turns(device="cpu", **kw)
+    with pytest.raises(ValueError):
+        qlin.rope_turns(1e4, 63)
+
+
+def test_the_binding_refuses_what_it_can_see():
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError):
+        qlin.KVCache(z(2, 4, 16, 64), z(2, 4, 16, 128))
+    with pytest.raises(ValueError):
+        qlin.KVCache(z(2, 4, 16, 64, dt=torch.float32), z(2, 4, 16, 64, dt=torch.float32))
+    with pytest.raises(ValueError):
+        qlin.KVCache(z(2, 4, 16, 64), z(2, 16, 4, 64).transpose(1, 2))
+    with pytest.raises(ValueError):
+        qlin.KVCache(z(2, 4, 64, 16).transpose(2, 3), z(2, 4, 64, 16).transpose(2, 3))
+    c = qlin.KVCache(z(2, 4, 16, 64), z(2, 4, 16, 64))
+    for kw in (dict(page_table=i32(3, 5)), dict(len=i32(2).long()), dict(count=i32(3)), dict(mask=i32(4)), dict(depth=i32(2, 4)),
+               dict(mask=i32(3), depth=i32(2, 3)), dict(page_table=i32(5, 2).t())):
+        with pytest.raises(ValueError):
+            qlin.KVStep(**{**dict(page_table=i32(2, 5), len=i32(2), T=3), **kw})
+    s = qlin.KVStep(i32(2, 5), i32(2), 3)
+    for call in (lambda: qlin.tree_attention(c, s, z(6, 512)), lambda: qlin.kv_append(c, s, q=z(6, 512)),
+                 lambda: qlin.kv_keep(c, s, i32(2, 3), i32(2)), lambda: qlin.sample(z(2, 9), z(2, dt=torch.float32))):
+        with pytest.raises(ValueError, match="not on a GPU"):  # there is no CPU path
+            call()

@@ -1,8 +1,8 @@
 """Build libqlin.so (sm_103a) in-tree with nvcc.
 
-Eight translation units compiled in parallel (the host API with the repack
-kernels, and seven sets of forward-kernel variants), one
--gencode, shared CUDA runtime (so the library and PyTorch share one runtime
+Translation units compiled in parallel (the host API with the repack
+kernels, the sets of forward-kernel variants, and the append, attention and
+sampling kernels), one -gencode, shared CUDA runtime (so the library and PyTorch share one runtime
 and one notion of the current device).  The output goes to
 ``w6a8_quantized_linear_gb300/_build/libqlin.so`` (git-ignored).
 """
@@ -21,9 +21,10 @@ LIB = os.path.join(BUILD, "libqlin.so")
 UNITS = ["qlin_api.cu", "qlin_kernels_w4.cu", "qlin_kernels_w6.cu", "qlin_kernels_codebook.cu",
          "qlin_kernels_moe_w4.cu", "qlin_kernels_moe_w6.cu", "qlin_kernels_export_w4.cu", "qlin_kernels_export_w6.cu",
          "qlin_kernels_tc.cu", "qlin_kernels_tc_export.cu", "qlin_kernels_w4_one_row.cu", "qlin_kernels_w6_one_row.cu",
-         "qlin_kernels_moe_one_row.cu", "qlin_kernels_codebook_one_row.cu"]
+         "qlin_kernels_moe_one_row.cu", "qlin_kernels_codebook_one_row.cu",
+         "qlin_append.cu", "qlin_attention.cu", "qlin_sample.cu"]
 SOURCES = [os.path.join(CSRC, f) for f in UNITS + ["qlin_forward.cuh", "qlin_forward_tc.cuh", "qlin_repack.cuh", "qlin_layout.h",
-                                                   "qlin_ptx.cuh", "qlin_instances.h"]] + [
+                                                   "qlin_ptx.cuh", "qlin_instances.h", "qlin_step.h"]] + [
     os.path.join(INCLUDE, "qlin.h")]
 
 

@@ -525,7 +525,7 @@ qlin_status noalloc_scratch(void** out) {
 extern "C" {
 
 const char* qlin_version(void) {
-  return "qlin 0.3 (sm_103a: fused prologue + TMA-streamed fp16 mma.sync GEMV, cluster split-K)";
+  return "qlin 0.4 (sm_103a: fused prologue + TMA-streamed fp16 mma.sync GEMV, cluster split-K; paged tree attention, sampling)";
 }
 
 const char* qlin_status_string(qlin_status s) {
@@ -536,6 +536,7 @@ const char* qlin_status_string(qlin_status s) {
     case QLIN_ERR_CUDA: return "CUDA error";
     case QLIN_ERR_DEVICE_TIMEOUT: return "device-side wait timed out";
     case QLIN_ERR_WORKSPACE: return "workspace too small";
+    case QLIN_ERR_BAD_INDEX: return "device-side index out of range";
   }
   return "unknown status";
 }

@@ -20,7 +20,9 @@ FORMATS = {"w4a8": 0, "w6a8": 1}
 PROLOGUES = {"none": 0, "rmsnorm": 1, "swiglu": 2}
 FLAG_PDL = 1
 
-OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE_TIMEOUT, ERR_WORKSPACE = range(6)
+OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE_TIMEOUT, ERR_WORKSPACE, ERR_BAD_INDEX = range(7)
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # qlin_dtype
 
 _lock = threading.Lock()
 _lib = None
@@ -75,6 +77,14 @@ def lib() -> ctypes.CDLL:
                 "qlin_debug_repack_tcgen05": (st, [i32, i64, i64, i64, vp, vp, sz, vp]),
                 "qlin_debug_forward_tcgen05": (st, [i32, i32, i32, i64, i64, i64, vp, vp, vp, vp, vp, ctypes.c_float,
                                                     vp, vp, vp, vp, vp, sz, ctypes.c_uint, vp]),
+                "qlin_rope_turns": (st, [vp, i32, vp]),
+                "qlin_kv_append": (st, [vp, vp, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, vp, i32,
+                                        i32, vp, i64, vp, sz, ctypes.c_uint, vp]),
+                "qlin_tree_attention_workspace_bytes": (st, [vp, i32, i32, i32, ctypes.POINTER(sz)]),
+                "qlin_tree_attention": (st, [vp, vp, i32, vp, i64, ctypes.c_float, vp, i64, vp, sz, ctypes.c_uint,
+                                             vp]),
+                "qlin_kv_keep": (st, [vp, vp, vp, i64, vp, vp, vp, sz, ctypes.c_uint, vp]),
+                "qlin_sample": (st, [i32, i64, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint, vp]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -358,3 +368,246 @@ def debug_plan(fmt, M: int, N: int, K: int, G: int) -> dict:
     c, st = ctypes.c_int(), ctypes.c_int()
     _check(lib().qlin_debug_plan(_fmt(fmt), M, N, K, G, ctypes.byref(c), ctypes.byref(st)), "debug_plan")
     return {"cluster": c.value, "stages": st.value}
+
+
+# ---- the rest of a decode / verification step ---------------------------------
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
+class _StepStruct(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("count", ctypes.c_void_p),
+                ("depth", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("tree_stride", ctypes.c_int64), ("B", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
+class KVCache:
+    """A paged cache: ``k`` and ``v`` are [pages, heads, page_size, width] tensors
+    (bf16 or fp16) of equal strides, the last dimension contiguous; a permuted
+    view of a [pages, page_size, heads, width] pool is one too."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must be [pages, heads, page_size, width] tensors of one shape, type and device")
+        if k.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("the cache holds bfloat16 or float16")
+        if k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must have the same strides and contiguous rows")
+        self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
+        self.pages, self.heads, self.page_size, self.width = k.shape
+        # a dimension of one has no stride that matters
+        step = [st if n > 1 else 8 for st, n in zip(k.stride()[:2], k.shape[:2])]
+        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), self.pages, step[0], step[1], k.stride(2),
+                                    DTYPES[k.dtype], self.heads, self.width, self.page_size)
+        self._ref = ctypes.addressof(self._struct)
+
+
+class KVStep:
+    """One step of B sequences, T rows each (``qlin_kv_step``): ``page_table``
+    int32 [B, max_pages], ``len`` int32 [B], optional ``count`` int32 [B], and
+    ``depth`` / ``mask`` int32 [T] (one tree for all sequences) or [B, T].  The
+    tensors are kept, and read by the calls that use the step."""
+
+    def __init__(self, page_table: torch.Tensor, len: torch.Tensor, T: int, count=None, depth=None, mask=None):
+        B = len.shape[0]
+        for name, t in (("page_table", page_table), ("len", len), ("count", count), ("depth", depth), ("mask", mask)):
+            if t is not None and (t.dtype != torch.int32 or t.device != len.device):
+                raise ValueError(f"{name} must be an int32 tensor on the device of len")
+        if len.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != B:
+            raise ValueError("page_table must be [B, max_pages] and len [B]")
+        if B and page_table.stride(1) != 1 and page_table.shape[1] > 1:
+            raise ValueError("the rows of page_table must be contiguous")
+        if not len.is_contiguous() or (count is not None and (count.shape != (B,) or not count.is_contiguous())):
+            raise ValueError("len and count must be contiguous [B] tensors")
+        tree = [t for t in (depth, mask) if t is not None]
+        for t in tree:
+            if t.shape not in ((T,), (B, T)) or not t.is_contiguous() or t.dim() != tree[0].dim():
+                raise ValueError("depth and mask must be contiguous [T] or [B, T] tensors of one shape")
+        self.page_table, self.len, self.count, self.depth, self.mask = page_table, len, count, depth, mask
+        self.B, self.T, self.device = B, T, len.device
+        n = page_table.shape[1]
+        self._struct = _StepStruct(_ptr(page_table), _ptr(len), _ptr(count), _ptr(depth), _ptr(mask),
+                                   page_table.stride(0) if B > 1 else n, T if tree and tree[0].dim() == 2 else 0, B, T, n)
+        self._ref = ctypes.addressof(self._struct)
+
+
+def _fn(name: str):
+    return getattr(_lib or lib(), name)
+
+
+def _same_device(device, *tensors) -> None:
+    """All tensors on ``device``, and that device current (the library launches on the current one)."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"a tensor is on {t.device}, the call's other tensors on {device}")
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}, not on a GPU")
+    if device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on {device}, but cuda:{torch._C._cuda_getDevice()} is the current device")
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for an output of a call on ``stream``, owned by that stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t, n: int, what: str, dtype=None) -> int:
+    """Row stride of a [n, heads * width] (or [n, heads, width]) tensor."""
+    if t.shape[0] != n or (dtype is not None and t.dtype != dtype) or t.stride(-1) != 1 or (
+            t.dim() == 3 and t.stride(1) != t.shape[2]) or t.dim() not in (2, 3):
+        raise ValueError(f"{what} must be a [{n}, heads * width] tensor with contiguous rows"
+                         + (f" of {dtype}" if dtype is not None else ""))
+    return t.stride(0) if n > 1 else t.numel()
+
+
+def _heads(t, width: int, what: str) -> int:
+    n = t.shape[1] if t.dim() == 2 else t.shape[1] * t.shape[2]
+    if n % width:
+        raise ValueError(f"{what} must hold whole heads of width {width}")
+    return n // width
+
+
+def _floats(t, n: int, what: str):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor of {n} values")
+    return t.data_ptr()
+
+
+def _ints(t, n: int, what: str):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of {n} values")
+    return t.data_ptr()
+
+
+def rope_turns(theta: float = 1e4, rot: int = 0, radians=None, device="cuda") -> torch.Tensor:
+    """Rotation frequencies for ``kv_append`` (int64 [rot / 2], 64-bit fractions of
+    a turn per position): theta ** (-2i / rot), or the given ``radians`` per
+    position."""
+    if radians is None:
+        if rot < 0 or rot % 2 or not theta > 0:
+            raise ValueError("rot must be even and not negative, theta above 0")
+        radians = [theta ** (-2.0 * i / rot) for i in range(rot // 2)]
+    n = len(radians)
+    out = torch.empty(n, dtype=torch.int64)
+    src = torch.tensor(list(radians), dtype=torch.float64)
+    _check(_fn("qlin_rope_turns")(src.data_ptr(), n, out.data_ptr()), "rope_turns")
+    return out.to(device)
+
+
+def kv_append(cache: KVCache, step: KVStep, q=None, k=None, v=None, q_gamma=None, k_gamma=None, eps: float = 1e-6,
+              turns=None, pairs: bool = False, q_out=None, ws=None, flags: int = 0, stream=None):
+    """Head norms and rotation of a step's projected q and k ([B * T, heads * width],
+    fp32 or bf16); k and v are stored behind the sequences' committed tokens.
+    Returns the normed and rotated q in the cache's type (or None without q)."""
+    n, D, dev = step.B * step.T, cache.width, cache.device
+    _same_device(dev, step.len, q, k, v, q_gamma, k_gamma, turns, q_out, ws)
+    if (k is None) != (v is None):
+        raise ValueError("k and v are given together")
+    src = q if q is not None else k
+    if src is None:
+        raise ValueError("nothing to append: neither q nor k and v are given")
+    Hq = qs = ks = vs = os_ = 0
+    if q is not None:
+        Hq, qs = _heads(q, D, "q"), _rows(q, n, "q", src.dtype)
+        if q_out is None:
+            q_out = _empty((n, Hq * D), cache.dtype, dev, stream)
+        os_ = _rows(q_out, n, "q_out", cache.dtype)
+        if _heads(q_out, D, "q_out") != Hq:
+            raise ValueError("q_out must have the shape of q")
+    if k is not None:
+        ks, vs = _rows(k, n, "k", src.dtype), _rows(v, n, "v", src.dtype)
+        if _heads(k, D, "k") != cache.heads or _heads(v, D, "v") != cache.heads:
+            raise ValueError("k and v must have the cache's heads")
+    if turns is not None and (turns.dtype != torch.int64 or not turns.is_contiguous()):
+        raise ValueError("turns must come from rope_turns")
+    nt = 0 if turns is None else turns.numel()
+    _check(_fn("qlin_kv_append")(
+        cache._ref, step._ref, Hq, DTYPES.get(src.dtype, -1), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+        _floats(q_gamma, D, "q_gamma"), _floats(k_gamma, D, "k_gamma"), eps, _ptr(turns) if nt else None, nt,
+        1 if pairs else 0, _ptr(q_out) if q is not None else None, os_, _ptr(ws), 0 if ws is None else ws.numel(), flags,
+        _raw_stream(stream, dev)), "kv_append")
+    return q_out
+
+
+def tree_attention_workspace_bytes(cache: KVCache, B: int, T: int, Hq: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_fn("qlin_tree_attention_workspace_bytes")(cache._ref, B, T, Hq, ctypes.byref(n)),
+           "tree_attention_workspace_bytes")
+    return n.value
+
+
+def tree_attention(cache: KVCache, step: KVStep, q: torch.Tensor, scale: float | None = None, out=None, ws=None,
+                   flags: int = 0, stream=None) -> torch.Tensor:
+    """Attention of a step's rows (q of ``kv_append``, [B * T, Hq * width]) over the
+    cache: every row sees the committed tokens of its sequence and the step's
+    rows that its mask names.  Returns bf16 [B * T, Hq * width].  ``scale``:
+    width ** -0.5 unless given."""
+    n, D, dev = step.B * step.T, cache.width, cache.device
+    _same_device(dev, step.len, q, out, ws)
+    Hq, qs = _heads(q, D, "q"), _rows(q, n, "q", cache.dtype)
+    if out is None:
+        out = _empty((n, Hq * D), torch.bfloat16, dev, stream)
+    os_ = _rows(out, n, "out", torch.bfloat16)
+    if _heads(out, D, "out") != Hq:
+        raise ValueError("out must have the shape of q")
+    if ws is None:
+        ws = _empty(tree_attention_workspace_bytes(cache, step.B, step.T, Hq), torch.uint8, dev, stream)
+        workspace_init(ws, _raw_stream(stream, dev))
+    _check(_fn("qlin_tree_attention")(cache._ref, step._ref, Hq, q.data_ptr(), qs, D ** -0.5 if scale is None else scale,
+                                      out.data_ptr(), os_, ws.data_ptr(), ws.numel(), flags, _raw_stream(stream, dev)),
+           "tree_attention")
+    return out
+
+
+def kv_keep(cache: KVCache, step: KVStep, keep: torch.Tensor, n_keep: torch.Tensor, len_out=None, ws=None,
+            flags: int = 0, stream=None) -> None:
+    """Move the accepted rows ``keep[b, :n_keep[b]]`` (int32 [B, T], increasing) of each
+    sequence up behind its committed tokens; ``len_out`` (int32 [B], may be the
+    step's ``len``) gets the new lengths."""
+    _same_device(cache.device, step.len, keep, n_keep, len_out, ws)
+    if keep.shape != (step.B, step.T) or keep.dtype != torch.int32 or (step.T > 1 and keep.stride(1) != 1):
+        raise ValueError("keep must be an int32 [B, T] tensor with contiguous rows")
+    _check(_fn("qlin_kv_keep")(cache._ref, step._ref, keep.data_ptr(), keep.stride(0) if step.B > 1 else step.T,
+                               _ints(n_keep, step.B, "n_keep"), _ints(len_out, step.B, "len_out"), _ptr(ws),
+                               0 if ws is None else ws.numel(), flags, _raw_stream(stream, cache.device)), "kv_keep")
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None, token=None,
+           prob=None, flags: int = 0, stream=None) -> torch.Tensor:
+    """One token per row of ``logits`` ([M, V], fp32 or bf16) from the uniform numbers
+    ``u`` (fp32 [M]); temperature, top_p, min_p fp32 [M], top_k int32 [M], each
+    optional.  Returns int32 [M]; ``prob`` (fp32 [M], optional) gets each
+    token's probability among the kept ones."""
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [M, V] with contiguous rows")
+    M, V = logits.shape
+    dev = logits.device
+    _same_device(dev, u, temperature, top_k, top_p, min_p, token, prob)
+    if token is None:
+        token = _empty((M,), torch.int32, dev, stream)
+    _check(_fn("qlin_sample")(M, V, DTYPES.get(logits.dtype, -1), logits.data_ptr(), logits.stride(0) if M > 1 else V,
+                              _floats(u, M, "u"), _floats(temperature, M, "temperature"), _ints(top_k, M, "top_k"),
+                              _floats(top_p, M, "top_p"), _floats(min_p, M, "min_p"), _ints(token, M, "token"),
+                              _floats(prob, M, "prob"), flags, _raw_stream(stream, dev)), "sample")
+    return token
