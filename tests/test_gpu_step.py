@@ -222,6 +222,7 @@ def check_attention(c, Hq, q_seed=0, scale=None, q=None, **kw):
         q = torch.randn(c.B * c.T, Hq * D, generator=g).to(c.dtype)
     out = torch.full((c.B * c.T, Hq * D), 3.0, dtype=BF, device=DEV)
     ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, c.B, c.T, Hq), DEV)
+    ws[256:] = 0xFF  # what an earlier call left must not matter: NaN everywhere
     got = qlin.tree_attention(c.cache, c.step, q.to(DEV), scale=scale, out=out, ws=ws, **kw)
     assert qlin.read_device_status(ws) == qlin.OK
     scale = D ** -0.5 if scale is None else scale

@@ -1,5 +1,18 @@
 // qlin_tree_attention: a step's rows over the paged cache.
+//
+// Two launches.  The first streams the committed tokens: their (sequence,
+// cache head) items' tiles are laid end to end and cut into equal runs, one
+// per CTA, whatever the lengths are, and each CTA leaves unnormalised partial
+// results of the items it touched.  Every row sees all of these tokens, so no
+// mask enters.  The second joins an item's partial results with the step's own
+// rows (at most 32 keys, under the tree's mask, on the CUDA cores, each row
+// reading only the keys that it sees) and normalises; it computes the scores
+// of those while the first still runs.
+#include <cuda.h>
+
 #include <cmath>
+#include <mutex>
+#include <type_traits>
 
 #include "qlin_ptx.cuh"
 #include "qlin_step.h"
@@ -7,105 +20,694 @@
 namespace qlin {
 namespace {
 
-constexpr int ATT_WARPS = 4;
+constexpr int ATT_THREADS = 224;   // four softmax warps, then the producer, MMA and cleaner warps
+constexpr int PRODUCER = 4, ISSUER = 5, CLEANER = 6;
+constexpr int ATT_ROWS = 128;      // query rows of an item at most: the lanes of tensor memory
+constexpr int ATT_MAX_CTAS = 160;  // the workspace holds the partial results of this many (one per SM)
+constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_COLS = 64;
+constexpr float RESCALE_AT = 8.f;  // log2 units that a row's maximum may rise before its sums are rescaled
+
+// Tokens of a tile: 32 KB of keys and of values (16 KB at width 64).
+__host__ __device__ constexpr int tile_tokens(int width) { return width == 256 ? 64 : 128; }
+__host__ __device__ constexpr int tile_bytes(int width) { return tile_tokens(width) * width * 2; }
+__host__ __device__ constexpr int q_bytes(int width) { return ATT_ROWS * width * 2; }
+// Ring buffers beside the query rows: 200 KB together, so that blocks of the
+// second launch find room on the SM (threads and registers likewise) and form
+// their scores while the first still runs.
+__host__ __device__ constexpr int ring_buffers(int width) { return (200 * 1024 - q_bytes(width)) / tile_bytes(width); }
+constexpr int MAX_RING = 11;
 
 struct AttentionParams {
+  CUtensorMap map_k, map_v;
   qlin_kv_cache cache;
   qlin_kv_step step;
   const void* q;
-  void* out;
+  __nv_bfloat16* out;
   int64_t q_stride, out_stride;
   uint32_t* status;
+  float* partial;    // [slot][width + 2][padded rows]: sums, then maxima (log2 units) and weights' sums
   float scale_log2;  // scale * log2(e): weights are powers of two
-  int Hq;
+  int Hq, group, R, Rp;  // query rows of an item: T * group, padded to 8
+  int ctas;
+  int box;           // tokens per TMA copy: a page or a tile, whichever is smaller
 };
 
-// One block per row and query head, each warp every fourth token, with the
-// running maximum and sum; the warps' partial results joined at the end.
+__device__ __forceinline__ int64_t committed(const AttentionParams& p, int b) {  // tokens that are there
+  const int64_t len = p.step.len[b];
+  if (len <= 0 || step_rows(p.step, b) == 0) return 0;
+  const int64_t most = (int64_t)p.step.max_pages * p.cache.page_size;
+  return len < most ? len : most;
+}
+template <int D>
+__device__ __forceinline__ int64_t tiles_of(const AttentionParams& p, int b) {
+  return (committed(p, b) + tile_tokens(D) - 1) / tile_tokens(D);
+}
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+// Tiles of the sequences before b (per cache head), and of all; a whole warp.
+template <int D>
+__device__ __forceinline__ void tiles_before(const AttentionParams& p, int b, int64_t* before, int64_t* all) {
+  const int lane = threadIdx.x & 31;
+  int64_t x = 0, y = 0;
+  for (int i = lane; i < p.step.B; i += 32) {
+    const int64_t n = tiles_of<D>(p, i);
+    y += n;
+    if (i < b) x += n;
+  }
+  *before = warp_sum64(x);
+  *all = warp_sum64(y);
+}
+
+// A CTA's run of tiles, item by item.
+struct Walk {
+  int64_t left;    // tiles of the run still ahead, this item's included
+  int64_t tile;    // first tile of this item's part
+  int64_t n;       // tiles of this part
+  int64_t tokens;  // committed tokens of the sequence
+  int b, h;
+};
+template <int D>
+__device__ __forceinline__ void enter(const AttentionParams& p, Walk& w) {  // the part of the item that w names
+  w.tokens = committed(p, w.b);
+  const int64_t n = (w.tokens + tile_tokens(D) - 1) / tile_tokens(D) - w.tile;
+  w.n = n < w.left ? n : w.left;
+}
+template <int D>
+__device__ __forceinline__ bool next_item(const AttentionParams& p, Walk& w) {
+  w.left -= w.n;
+  if (w.left <= 0) return false;
+  w.tile = 0;
+  if (++w.h == p.cache.heads) {
+    w.h = 0;
+    do w.b++;
+    while (w.b < p.step.B && committed(p, w.b) == 0);
+    if (w.b >= p.step.B) return false;  // not reached: the run's tiles are counted from the same lengths
+  }
+  enter<D>(p, w);
+  return true;
+}
+// Runs that N tiles are cut into: none is empty, so that the CTAs between an
+// item's first and last have all left a partial result of it.
+__device__ __forceinline__ int runs_of(const AttentionParams& p, int64_t N) { return N < p.ctas ? (int)N : p.ctas; }
+// Where CTA c's run begins; a whole warp.
+template <int D>
+__device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
+  int64_t none, all;
+  tiles_before<D>(p, 0, &none, &all);
+  const int64_t N = all * p.cache.heads;
+  const int runs = runs_of(p, N);
+  Walk w = {0, 0, 0, 0, 0, 0};
+  if (c >= runs) return w;
+  const int64_t x0 = N * c / runs;
+  w.left = N * (c + 1) / runs - x0;
+  const int lane = threadIdx.x & 31;
+  int64_t run = 0;
+  for (int i0 = 0; i0 < p.step.B; i0 += 32) {
+    const int64_t n = i0 + lane < p.step.B ? tiles_of<D>(p, i0 + lane) * p.cache.heads : 0;
+    int64_t inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t a = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += a;
+    }
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, x0 < run + inc);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      const int64_t start = __shfl_sync(0xFFFFFFFFu, run + inc - n, l);
+      const int64_t per = __shfl_sync(0xFFFFFFFFu, n, l) / p.cache.heads;
+      w.b = i0 + l;
+      w.h = (int)((x0 - start) / per);
+      w.tile = (x0 - start) % per;
+      enter<D>(p, w);
+      return w;
+    }
+    run += __shfl_sync(0xFFFFFFFFu, inc, 31);
+  }
+  w.left = 0;
+  return w;
+}
+// The CTA whose run holds tile x of N: floor(c N / runs) <= x < floor((c + 1) N / runs)
+__device__ __forceinline__ int cta_of(int64_t x, int64_t N, int runs) { return (int)(((x + 1) * runs - 1) / N); }
+
+// ---- PTX -------------------------------------------------------------------------
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int token, int head, int page,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// Matrix descriptor of a 128-byte-swizzled operand: rows of 64 16-bit values
+// (128 bytes, on a 1024-byte boundary every eighth), `lbo` bytes between its
+// 64-wide panels where the panels run along M or N, 1024 between groups of
+// eight rows.
+__device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+struct AttentionShared {
+  uint64_t full[MAX_RING], empty[MAX_RING];
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2];
+  uint64_t q_full, o_full, v_dirty, v_clean, drained;
+  uint32_t tmem;
+  int dead;  // a wait has expired: every role leaves its loop
+  Walk walk;
+};
+
+// A bounded wait of one role; on expiry the workspace's status word is set and
+// all roles leave.
+__device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, AttentionShared* s, uint32_t* status) {
+  if (*(volatile int*)&s->dead) return false;
+  if (mbar_wait(bar, parity)) return true;
+  s->dead = 1;
+  report(status, QLIN_ERR_DEVICE_TIMEOUT);
+  return false;
+}
+
+// The committed tokens.  S = Q K^T (128 query lanes x a tile's tokens) and
+// O += P V on tcgen05 with fp32 accumulators in tensor memory: lane = query
+// row, so that a softmax thread owns a row and needs no exchange.  P goes from
+// registers into tensor memory in the cache's type and is the A operand of the
+// second product; keys and values are read by the tensor cores straight from
+// the ring that TMA fills (128-byte swizzle; V as the transposed operand).
+// Bound by the stream of keys and values: a 64 KB pair of tiles takes an SM
+// about 2800 cycles at the measured bandwidth, its products about 1000, its
+// softmax about 1500 (two score buffers overlap them).  A row's maximum may
+// grow by 2^8 before its sums are rescaled in tensor memory: weights are
+// relative to a maximum of the past, at most 2^8, which fp16 holds.
 template <typename T, int D>
-__global__ void __launch_bounds__(ATT_WARPS * 32) qlin_attention_kernel(const __grid_constant__ AttentionParams p) {
-  __shared__ float part[ATT_WARPS][D + 2];
-  constexpr int E = D / 32;
-  const int row = blockIdx.x, head = blockIdx.y;
-  const int b = row / p.step.T, t = row - b * p.step.T;
+__global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __grid_constant__ AttentionParams p) {
+  extern __shared__ uint8_t raw[];
+  __shared__ AttentionShared sh;
+  constexpr int TK = tile_tokens(D), TB = tile_bytes(D), NB = ring_buffers(D), PANELS = D / 64;
+  constexpr uint32_t O_COL = 0, S_COL = D, P_COL = D + 2 * TK;  // columns of tensor memory
+  static_assert(P_COL + TK <= 512 && NB >= 4 && NB <= MAX_RING, "tensor memory and ring");
+  AttentionShared* s = &sh;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t q_smem = base, ring = base + q_bytes(D);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int active = (p.R + 31) / 32;  // softmax warps with rows
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NB; i++) mbar_init(&s->full[i], 1), mbar_init(&s->empty[i], 1);
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&s->s_full[i], 1);
+      mbar_init(&s->s_free[i], active);
+      mbar_init(&s->p_full[i], active);
+      mbar_init(&s->p_free[i], 1);
+    }
+    mbar_init(&s->q_full, 4);
+    mbar_init(&s->o_full, 1);
+    mbar_init(&s->v_dirty, 1);
+    mbar_init(&s->v_clean, 1);
+    mbar_init(&s->drained, 1);
+    s->dead = 0;
+    mbar_fence_init();
+  }
+  if (warp == ISSUER) tmem_alloc(&s->tmem, 512);
   pdl_wait();
   pdl_launch_dependents();
-  const int len = p.step.len[b];
-  const int rows = step_rows(p.step, b);
-  if (len < 0 || t >= rows) return;
-  const uint32_t mask = step_mask(p.step, b, t);
-  const int hk = head / (p.Hq / p.cache.heads);
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  const T* qp = static_cast<const T*>(p.q) + row * p.q_stride + (int64_t)head * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const float2 f = unpack2(*reinterpret_cast<const uint32_t*>(qp + e), T());
-    q[e] = f.x * p.scale_log2, q[e + 1] = f.y * p.scale_log2;
-    o[e] = o[e + 1] = 0.f;
+  if (warp == PRODUCER) {
+    const Walk w = first_item<D>(p, blockIdx.x);
+    if (lane == 0) s->walk = w;
   }
-  for (int64_t j = warp; j < (int64_t)len + rows; j += ATT_WARPS) {
-    if (j >= len && !(mask >> (j - len) & 1)) continue;
-    const int64_t at = token_offset(p.cache, p.step, b, j);
-    if (at < 0) {
-      if (lane == 0) report(p.status, QLIN_ERR_BAD_INDEX);
-      continue;
-    }
-    const T* kp = static_cast<const T*>(p.cache.k) + at + hk * p.cache.head_stride + lane * E;
-    const T* vp = static_cast<const T*>(p.cache.v) + at + hk * p.cache.head_stride + lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 f = unpack2(*reinterpret_cast<const uint32_t*>(kp + e), T());
-      s = fmaf(q[e], f.x, fmaf(q[e + 1], f.y, s));
-    }
-#pragma unroll
-    for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, i);
-    const float mn = fmaxf(m, s);
-    const float keep = m == mn ? 1.f : exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = l * keep + w;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 f = unpack2(*reinterpret_cast<const uint32_t*>(vp + e), T());
-      o[e] = fmaf(w, f.x, o[e] * keep), o[e + 1] = fmaf(w, f.y, o[e + 1] * keep);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < E; e++) part[warp][lane * E + e] = o[e];
-  if (lane == 0) part[warp][D] = m, part[warp][D + 1] = l;
+  tc_fence_before();
   __syncthreads();
-  float mx = -INFINITY, sum = 0.f;
-  for (int w = 0; w < ATT_WARPS; w++) mx = fmaxf(mx, part[w][D]);
-  float f[ATT_WARPS];
-  for (int w = 0; w < ATT_WARPS; w++) {
-    f[w] = part[w][D] == -INFINITY ? 0.f : exp2f(part[w][D] - mx);
-    sum += f[w] * part[w][D + 1];
+  tc_fence_after();
+  const uint32_t tmem = s->tmem;
+  Walk w = s->walk;
+
+  if (w.left > 0) {
+    if (warp == PRODUCER) {
+      // ---- producer: a lane per TMA copy (a page's or a tile's rows of one 64-wide panel)
+      constexpr uint32_t row_bytes = 128;
+      const int boxes = TK / p.box, copies = boxes * PANELS;  // <= 16
+      const int box = lane % boxes, panel = lane / boxes;
+      uint32_t i = 0;  // ring position
+      bool ok = true;
+      do {
+        for (int64_t t = 0; t < w.n && ok; t++) {
+          const int64_t token = (w.tile + t) * TK + box * p.box;
+          int page = -1;
+          if (lane < copies && token < w.tokens) {
+            page = p.step.page_table[w.b * p.step.table_stride + token / p.cache.page_size];
+            if (page < 0 || page >= p.cache.pages) {
+              page = -1;
+              report(p.status, QLIN_ERR_BAD_INDEX);
+            }
+          }
+          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0)) * p.box * row_bytes;
+          for (int kv = 0; kv < 2; kv++, i++) {
+            const uint32_t slot = i % NB, use = i / NB;
+            if (use) ok = role_wait(&s->empty[slot], (use - 1) & 1, s, p.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&s->full[slot], bytes);
+            __syncwarp();
+            if (page >= 0)
+              tma_load_4d(ring + slot * TB + (panel * TK + box * p.box) * 128, kv ? &p.map_v : &p.map_k, panel * 64,
+                          (int)(token % p.cache.page_size), w.h, page, &s->full[slot]);
+          }
+        }
+      } while (ok && next_item<D>(p, w));
+      // nothing leaves while its copies are in flight
+      if (!ok)
+        for (uint32_t j = i > NB ? i - NB : 0; j < i; j++) (void)mbar_wait(&s->full[j % NB], (j / NB) & 1);
+    } else if (warp == ISSUER) {
+      // ---- MMA: one thread issues
+      if (lane == 0) {
+        constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u;
+        constexpr uint32_t id_s = mma_idesc_f16(128, TK) | type;
+        constexpr uint32_t id_o = mma_idesc_f16(128, D) | type | (1u << 16);  // B along N
+        uint32_t n = 0, seg = 0, dirty = 0;
+        bool ok = true;
+        do {
+          ok = role_wait(&s->q_full, seg & 1, s, p.status);
+          tc_fence_after();
+          for (int64_t t = 0; t <= w.n && ok; t++) {
+            if (t < w.n) {  // S(t)
+              const uint32_t m = n + (uint32_t)t, slot = (2 * m) % NB, use = (2 * m) / NB;
+              ok = role_wait(&s->full[slot], use & 1, s, p.status);
+              if (ok && m >= 2) ok = role_wait(&s->s_free[m & 1], ((m >> 1) - 1) & 1, s, p.status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t kb = ring + slot * TB;
+#pragma unroll
+              for (int e = 0; e < D / 16; e++)
+                mma_smem_a(tmem + S_COL + (m & 1) * TK,
+                           swizzled_desc(q_smem + (e / 4) * (ATT_ROWS * 128) + (e % 4) * 32, 16),
+                           swizzled_desc(kb + (e / 4) * (TK * 128) + (e % 4) * 32, 16), id_s, e > 0);
+              mma_commit(&s->empty[slot]);
+              mma_commit(&s->s_full[m & 1]);
+            }
+            if (t > 0) {  // O += P(t - 1) V(t - 1)
+              const uint32_t m = n + (uint32_t)t - 1, slot = (2 * m + 1) % NB, use = (2 * m + 1) / NB;
+              ok = role_wait(&s->full[slot], use & 1, s, p.status);
+              const bool ragged = (w.tile + t) * TK > w.tokens;  // the sequence's last tile, not full
+              if (ok && ragged) mbar_arrive(&s->v_dirty);
+              if (ok) ok = role_wait(&s->p_full[m & 1], (m >> 1) & 1, s, p.status);
+              if (ok && ragged) ok = role_wait(&s->v_clean, dirty++ & 1, s, p.status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t vb = ring + slot * TB;
+#pragma unroll
+              for (int e = 0; e < TK / 16; e++)
+                mma_tmem_a(tmem + O_COL, tmem + P_COL + (m & 1) * (TK / 2) + e * 8, swizzled_desc(vb + e * 2048, TK * 128),
+                           id_o, t > 1 || e > 0);
+              mma_commit(&s->empty[slot]);
+              mma_commit(&s->p_free[m & 1]);
+              if (t == w.n) mma_commit(&s->o_full);
+            }
+          }
+          n += (uint32_t)w.n;
+          seg++;
+        } while (ok && next_item<D>(p, w));
+        if (!ok) {  // the products in flight end before tensor memory is freed
+          mma_commit(&s->drained);
+          (void)mbar_wait(&s->drained, 0);
+        }
+      }
+    } else if (warp == CLEANER) {
+      // ---- cleaner: the rows behind the last token hold whatever the page or
+      // the ring held; their weight is 0, but 0 * NaN is not.  Asked for each
+      // ragged tile once its copies have landed.
+      uint32_t n = 0, dirty = 0;
+      bool ok = true;
+      do {
+        n += (uint32_t)w.n;
+        const int64_t end = (w.tile + w.n) * TK;
+        if (end > w.tokens) {
+          ok = __all_sync(0xFFFFFFFFu, role_wait(&s->v_dirty, dirty++ & 1, s, p.status));
+          if (!ok) break;
+          const uint32_t v = ring + ((2 * n - 1) % NB) * TB;
+          const int valid = (int)(w.tokens - (end - TK)), units = (TK - valid) * 8;
+          for (int c = lane; c < PANELS * units; c += 32)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + ((c / units) * TK + valid) * 128 +
+                                                                          (c % units) * 16),
+                         "r"(0)
+                         : "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s->v_clean);
+        }
+      } while (next_item<D>(p, w));
+    } else {
+      // ---- softmax: a thread per query row
+      const int sw = warp, row = sw * 32 + lane;
+      const bool live = row < p.R;
+      const uint32_t lanes = (uint32_t)(sw * 32) << 16;
+      uint32_t n = 0, seg = 0;
+      bool ok = true;
+      do {
+        {  // the item's query rows, in the swizzled layout
+          const int rows = step_rows(p.step, w.b) * p.group;
+          const T* q = static_cast<const T*>(p.q) + (int64_t)w.b * p.step.T * p.q_stride + (int64_t)w.h * p.group * D;
+          for (int c = threadIdx.x; c < rows * (D / 8); c += 128) {
+            const int r = c / (D / 8), e = c % (D / 8);
+            const uint4 x = *reinterpret_cast<const uint4*>(q + (r / p.group) * p.q_stride + (r % p.group) * D + e * 8);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_smem + (e / 8) * (ATT_ROWS * 128) + r * 128 +
+                                                                          (((e & 7) ^ (r & 7)) << 4)),
+                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                         : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s->q_full);
+        }
+        float m_used = -INFINITY, l = 0.f;
+        if (sw < active) {
+          for (int64_t t = 0; t < w.n; t++) {
+            const uint32_t m = n + (uint32_t)t;
+            ok = __all_sync(0xFFFFFFFFu, role_wait(&s->s_full[m & 1], (m >> 1) & 1, s, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            float x[TK];
+#pragma unroll
+            for (int c = 0; c < TK; c += 32)
+              tmem_ld32(tmem + lanes + S_COL + (m & 1) * TK + c, reinterpret_cast<uint32_t*>(x) + c);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s->s_free[m & 1]);
+            const int64_t ahead = w.tokens - (w.tile + t) * TK;
+            if (ahead < TK) {
+              const int valid = (int)ahead;
+#pragma unroll
+              for (int c = 0; c < TK; c++) x[c] = c < valid ? x[c] * p.scale_log2 : -INFINITY;
+            } else {
+#pragma unroll
+              for (int c = 0; c < TK; c++) x[c] *= p.scale_log2;
+            }
+            float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int c = 4; c < TK; c++) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            float keep = 1.f;
+            bool rescale = false;
+            if (t == 0) {
+              m_used = mt;
+            } else if (mt > m_used + RESCALE_AT) {
+              keep = exp2_approx(m_used - mt);
+              m_used = mt;
+              l *= keep;
+              rescale = live;
+            }
+            // the sums in tensor memory, where a row's maximum rose: once the
+            // product before this one has been added
+            if (__any_sync(0xFFFFFFFFu, rescale)) {
+              ok = __all_sync(0xFFFFFFFFu, role_wait(&s->p_free[(m - 1) & 1], ((m - 1) >> 1) & 1, s, p.status));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tmem + lanes + O_COL + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                tmem_st32(tmem + lanes + O_COL + c, o);
+              }
+              tmem_wait_st();
+            }
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t w2[TK / 2];
+#pragma unroll
+            for (int c = 0; c < TK; c += 2) {
+              const float a = exp2_approx(x[c] - m_used), b2 = exp2_approx(x[c + 1] - m_used);
+              sum[(c >> 1) & 3] += a + b2;
+              w2[c / 2] = pack2(a, b2, T());
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (m >= 2) {
+              ok = __all_sync(0xFFFFFFFFu, role_wait(&s->p_free[m & 1], ((m >> 1) - 1) & 1, s, p.status));
+              if (!ok) break;
+              tc_fence_after();
+            }
+#pragma unroll
+            for (int c = 0; c < TK / 2; c += 32) tmem_st32(tmem + lanes + P_COL + (m & 1) * (TK / 2) + c, w2 + c);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s->p_full[m & 1]);
+          }
+        }
+        if (!ok) break;
+        ok = __all_sync(0xFFFFFFFFu, role_wait(&s->o_full, seg & 1, s, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        if (sw < active) {  // [column][row]: a warp's store is one run
+          float* part = p.partial + (int64_t)(blockIdx.x + w.b * p.cache.heads + w.h) * (D + 2) * p.Rp + row;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lanes + O_COL + c, o);
+            tmem_wait_ld();
+            if (live) {
+#pragma unroll
+              for (int e = 0; e < 32; e++) part[(c + e) * p.Rp] = __uint_as_float(o[e]);
+            }
+          }
+          if (live) {
+            part[D * p.Rp] = m_used;
+            part[(D + 1) * p.Rp] = l;
+          }
+          tc_fence_before();
+        }
+        n += (uint32_t)w.n;
+        seg++;
+      } while (next_item<D>(p, w));
+    }
   }
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.out_stride + (int64_t)head * D;
-  for (int e = threadIdx.x; e < D; e += ATT_WARPS * 32) {
-    float x = 0.f;
-    for (int w = 0; w < ATT_WARPS; w++)
-      if (f[w] != 0.f) x += f[w] * part[w][e];
-    out[e] = __float2bfloat16(sum == 0.f ? 0.f : x / sum);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == ISSUER) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
-const void* attention_fn(int dtype, int width) {
+// Joins an item's partial results with the step's own rows, eight query rows
+// and 64 columns per block: o = (sum_s 2^(m_s - M) O_s + sum_j 2^(x_j - M) v_j)
+// / (the same sum of weights).  The scores x_j of the keys that a row sees are
+// formed before the first launch is waited for.  A few hundred KB from L2.
+template <typename T, int D>
+__global__ void __launch_bounds__(JOIN_THREADS) qlin_attention_join_kernel(const __grid_constant__ AttentionParams p) {
+  __shared__ float weight[ATT_MAX_CTAS][8];  // of each partial result, per row
+  __shared__ float own[8][QLIN_MAX_TREE];    // of each of the step's rows
+  __shared__ int64_t place[QLIN_MAX_TREE];
+  __shared__ float o[8][JOIN_COLS + 1];
+  __shared__ int64_t range[2];
+  constexpr int E = D / 32;
+  const int item = blockIdx.x, b = item / p.cache.heads, h = item % p.cache.heads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r0 = blockIdx.y * 8, row = r0 + warp, t = row / p.group;
+  const int len = p.step.len[b], rows = step_rows(p.step, b);
+  const bool live = len >= 0 && row < p.R && t < rows;
+  if (len >= 0 && warp == 0) {
+    int64_t before, all;
+    tiles_before<D>(p, b, &before, &all);
+    if (lane == 0) range[0] = before, range[1] = all;
+    if (lane < rows) {
+      place[lane] = token_offset(p.cache, p.step, b, (int64_t)len + lane);
+      if (place[lane] < 0 || (int64_t)len > (int64_t)p.step.max_pages * p.cache.page_size)
+        report(p.status, QLIN_ERR_BAD_INDEX);
+    }
+  }
+  __syncthreads();
+  float mine = -INFINITY;  // lane j: the score of row j of the step
+  if (live) {
+    const uint32_t mask = step_mask(p.step, b, t);
+    const int64_t head = (int64_t)h * p.group + row % p.group;
+    const T* q = static_cast<const T*>(p.q) + ((int64_t)b * p.step.T + t) * p.q_stride + head * D + lane * E;
+    float2 f[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) f[e / 2] = unpack2(*reinterpret_cast<const uint32_t*>(q + e), T());
+    for (int j = 0; j < rows; j++) {
+      if (!(mask >> j & 1) || place[j] < 0) continue;
+      const T* k = static_cast<const T*>(p.cache.k) + place[j] + h * p.cache.head_stride + lane * E;
+      float x = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 g = unpack2(*reinterpret_cast<const uint32_t*>(k + e), T());
+        x = fmaf(f[e / 2].x, g.x, fmaf(f[e / 2].y, g.y, x));
+      }
+#pragma unroll
+      for (int i = 16; i; i >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, i);
+      if (lane == j) mine = x * p.scale_log2;
+    }
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (len < 0 || rows == 0) return;
+  // this item's tiles among all, and the CTAs whose runs hold them
+  const int64_t per = tiles_of<D>(p, b), N = range[1] * p.cache.heads;
+  const int64_t start = range[0] * p.cache.heads + h * per;
+  const int runs = runs_of(p, N);
+  const int first = per ? cta_of(start, N, runs) : 0;
+  const int parts = per ? cta_of(start + per - 1, N, runs) - first + 1 : 0;
+  const int64_t step = (int64_t)(D + 2) * p.Rp;
+  const float* part = p.partial + (int64_t)(first + item) * step + r0;
+  if (live) {
+    float m = mine;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, part[i * step + (int64_t)D * p.Rp + warp]);
+#pragma unroll
+    for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, i));
+    const bool seen = lane < rows && (step_mask(p.step, b, t) >> lane & 1) && place[lane] >= 0;
+    const float w = seen ? exp2f(mine - m) : 0.f;
+    float l = w;
+    for (int i = lane; i < parts; i += 32) {
+      const float* ml = part + i * step + (int64_t)D * p.Rp + warp;
+      const float f = exp2f(ml[0] - m);
+      weight[i][warp] = f;
+      l = fmaf(f, ml[p.Rp], l);
+    }
+#pragma unroll
+    for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, i);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    own[warp][lane] = w * inv;
+    for (int i = lane; i < parts; i += 32) weight[i][warp] *= inv;
+  }
+  __syncthreads();
+  const int r = threadIdx.x & 7, t2 = (r0 + r) / p.group;
+  if (r0 + r < p.R && t2 < rows) {
+    const uint32_t mask = step_mask(p.step, b, t2);
+    for (int c = threadIdx.x >> 3; c < JOIN_COLS; c += JOIN_THREADS / 8) {
+      const int col = blockIdx.z * JOIN_COLS + c;
+      float acc = 0.f;
+      const float* x = part + (int64_t)col * p.Rp + r;
+#pragma unroll 8
+      for (int i = 0; i < parts; i++) acc = fmaf(weight[i][r], x[i * step], acc);
+      const T* v = static_cast<const T*>(p.cache.v) + h * p.cache.head_stride + col;
+      for (int j = 0; j < rows; j++)
+        if ((mask >> j & 1) && place[j] >= 0) acc = fmaf(own[r][j], to_float(v[place[j]]), acc);
+      o[r][c] = acc;
+    }
+  }
+  __syncthreads();
+  if (live) {  // a row's 64 columns: one run
+    __nv_bfloat16* out = p.out + ((int64_t)b * p.step.T + t) * p.out_stride +
+                         ((int64_t)h * p.group + row % p.group) * D + blockIdx.z * JOIN_COLS;
+    *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack2(o[warp][2 * lane], o[warp][2 * lane + 1], __nv_bfloat16());
+  }
+}
+
+struct Kernels {
+  const void *main, *join;
+};
+template <typename T, int D>
+Kernels kernels_of() {
+  return {reinterpret_cast<const void*>(qlin_attention_kernel<T, D>),
+          reinterpret_cast<const void*>(qlin_attention_join_kernel<T, D>)};
+}
+Kernels attention_kernels(int dtype, int width) {
   if (dtype == QLIN_BF16)
-    return width == 64    ? reinterpret_cast<const void*>(qlin_attention_kernel<__nv_bfloat16, 64>)
-           : width == 128 ? reinterpret_cast<const void*>(qlin_attention_kernel<__nv_bfloat16, 128>)
-                          : reinterpret_cast<const void*>(qlin_attention_kernel<__nv_bfloat16, 256>);
-  return width == 64    ? reinterpret_cast<const void*>(qlin_attention_kernel<__half, 64>)
-         : width == 128 ? reinterpret_cast<const void*>(qlin_attention_kernel<__half, 128>)
-                        : reinterpret_cast<const void*>(qlin_attention_kernel<__half, 256>);
+    return width == 64    ? kernels_of<__nv_bfloat16, 64>()
+           : width == 128 ? kernels_of<__nv_bfloat16, 128>()
+                          : kernels_of<__nv_bfloat16, 256>();
+  return width == 64 ? kernels_of<__half, 64>() : width == 128 ? kernels_of<__half, 128>() : kernels_of<__half, 256>();
+}
+constexpr size_t attention_smem(int width) {  // query rows, ring, and the way to a 1024-byte boundary
+  return (size_t)q_bytes(width) + (size_t)ring_buffers(width) * tile_bytes(width) + 1024;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+struct AttentionDevice {
+  std::once_flag once;
+  qlin_status ready = QLIN_ERR_CUDA;
+  int ctas = 0;
+};
+AttentionDevice g_attention[64];
+EncodeTiled g_encode = nullptr;
+std::once_flag g_encode_once;
+
+// SM count, kernel attributes and the driver's encoder, once per device.
+qlin_status attention_setup(int* ctas) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return status_of(e);
+  if (dev < 0 || dev >= 64) return QLIN_ERR_CUDA;
+  AttentionDevice& d = g_attention[dev];
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) ==
+            cudaSuccess &&
+        found == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<EncodeTiled>(fn);
+  });
+  std::call_once(d.once, [&d, dev] {
+    int sms = 0;
+    cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    for (int dtype : {QLIN_BF16, QLIN_F16})
+      for (int width : {64, 128, 256})
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(attention_kernels(dtype, width).main, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)attention_smem(width));
+    d.ctas = sms < ATT_MAX_CTAS ? sms : ATT_MAX_CTAS;
+    d.ready = e == cudaSuccess && g_encode && sms > 0 ? QLIN_OK : QLIN_ERR_CUDA;
+    if (e != cudaSuccess) (void)cudaGetLastError();
+  });
+  *ctas = d.ctas;
+  return d.ready;
+}
+
+// [pages, heads, page_size, width] as boxes of 64 elements x `box` tokens,
+// 128-byte swizzled
+bool encode(CUtensorMap* map, const qlin_kv_cache* c, void* base, int box) {
+  const cuuint64_t dims[4] = {(cuuint64_t)c->width, (cuuint64_t)c->page_size, (cuuint64_t)c->heads,
+                              (cuuint64_t)c->pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)c->token_stride * 2, (cuuint64_t)c->head_stride * 2,
+                                 (cuuint64_t)c->page_stride * 2};
+  const cuuint32_t shape[4] = {64, (cuuint32_t)box, 1, 1}, one[4] = {1, 1, 1, 1};
+  return g_encode(map, c->dtype == QLIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  base, dims, strides, shape, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 qlin_status check_heads(const qlin_kv_cache* c, int64_t B, int64_t T, int Hq) {
   if (B < 0 || T < 0 || Hq < 1 || Hq % c->heads) return QLIN_ERR_INVALID_ARG;
-  if (T > QLIN_MAX_TREE || T * (Hq / c->heads) > 128) return QLIN_ERR_UNSUPPORTED;
+  if (T > QLIN_MAX_TREE || T * (Hq / c->heads) > ATT_ROWS) return QLIN_ERR_UNSUPPORTED;
+  if (B * c->heads > (1 << 24)) return QLIN_ERR_UNSUPPORTED;
   return QLIN_OK;
 }
+int padded_rows(int64_t T, int group) { return (int)((T * group + 7) / 8 * 8); }
 
 }  // namespace
 }  // namespace qlin
@@ -120,7 +722,9 @@ qlin_status qlin_tree_attention_workspace_bytes(const qlin_kv_cache* cache, int 
   st = check_heads(cache, B, T, Hq);
   if (st != QLIN_OK) return st;
   if (!bytes) return QLIN_ERR_INVALID_ARG;
-  *bytes = (size_t)STEP_WS_HEADER;
+  // a part of an item ends where the item or a CTA's run ends
+  const size_t slots = ATT_MAX_CTAS + (size_t)B * cache->heads;
+  *bytes = (size_t)STEP_WS_HEADER + slots * (cache->width + 2) * padded_rows(T, Hq / cache->heads) * sizeof(float);
   return QLIN_OK;
 }
 
@@ -141,12 +745,33 @@ qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* 
   if (!rows_ok(q, q_stride, Hq * D, 2) || !rows_ok(out, out_stride, Hq * D, 2)) return QLIN_ERR_INVALID_ARG;
   if (!ws || !is_aligned(ws, 256)) return QLIN_ERR_INVALID_ARG;
   if (ws_bytes < need) return QLIN_ERR_WORKSPACE;
-  AttentionParams p = {*cache, *step,      q, out, q_stride, out_stride, static_cast<uint32_t*>(ws),
-                       scale * 1.4426950408889634f, Hq};
+  int ctas = 0;
+  st = attention_setup(&ctas);
+  if (st != QLIN_OK) return st;
+  AttentionParams p;
+  const int tile = tile_tokens(cache->width);
+  p.box = cache->page_size < tile ? cache->page_size : tile;
+  if (!encode(&p.map_k, cache, cache->k, p.box) || !encode(&p.map_v, cache, cache->v, p.box)) return QLIN_ERR_CUDA;
+  p.cache = *cache;
+  p.step = *step;
+  p.q = q;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.q_stride = q_stride, p.out_stride = out_stride;
+  p.status = static_cast<uint32_t*>(ws);
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + STEP_WS_HEADER);
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.Hq = Hq;
+  p.group = Hq / cache->heads;
+  p.R = step->T * p.group;
+  p.Rp = padded_rows(step->T, p.group);
+  p.ctas = ctas;
   void* args[] = {&p};
-  return launch_step(attention_fn(cache->dtype, cache->width), dim3((unsigned)(step->B * step->T), (unsigned)Hq, 1),
-                     dim3(ATT_WARPS * 32, 1, 1), 0, static_cast<cudaStream_t>(stream), args,
-                     (flags & QLIN_FLAG_PDL) != 0);
+  const Kernels fn = attention_kernels(cache->dtype, cache->width);
+  st = launch_step(fn.main, dim3((unsigned)ctas, 1, 1), dim3(ATT_THREADS, 1, 1), attention_smem(cache->width),
+                   static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0);
+  if (st != QLIN_OK) return st;
+  return launch_step(fn.join, dim3((unsigned)(step->B * cache->heads), (unsigned)(p.Rp / 8), (unsigned)(D / JOIN_COLS)),
+                     dim3(JOIN_THREADS, 1, 1), 0, static_cast<cudaStream_t>(stream), args, true);
 }
 
 }  // extern "C"
