@@ -24,8 +24,9 @@ constexpr int ATT_THREADS = 224;   // four softmax warps, then the producer, MMA
 constexpr int PRODUCER = 4, ISSUER = 5, CLEANER = 6;
 constexpr int ATT_ROWS = 128;      // query rows of an item at most: the lanes of tensor memory
 constexpr int ATT_MAX_CTAS = 160;  // the workspace holds the partial results of this many (one per SM)
-constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_THREADS = 512;
 constexpr int JOIN_COLS = 64;
+constexpr int JOIN_GROUPS = JOIN_THREADS / (2 * JOIN_COLS);  // threads that share a column's partial results
 constexpr float RESCALE_AT = 8.f;  // log2 units that a row's maximum may rise before its sums are rescaled
 
 // Tokens of a tile: 32 KB of keys and of values (16 KB at width 64).
@@ -60,8 +61,10 @@ __device__ __forceinline__ int64_t committed(const AttentionParams& p, int b) { 
   return len < most ? len : most;
 }
 template <int D>
+__device__ __forceinline__ int64_t tokens_to_tiles(int64_t n) { return (n + tile_tokens(D) - 1) / tile_tokens(D); }
+template <int D>
 __device__ __forceinline__ int64_t tiles_of(const AttentionParams& p, int b) {
-  return (committed(p, b) + tile_tokens(D) - 1) / tile_tokens(D);
+  return tokens_to_tiles<D>(committed(p, b));
 }
 __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
 #pragma unroll
@@ -92,8 +95,7 @@ struct Walk {
 };
 template <int D>
 __device__ __forceinline__ void enter(const AttentionParams& p, Walk& w) {  // the part of the item that w names
-  w.tokens = committed(p, w.b);
-  const int64_t n = (w.tokens + tile_tokens(D) - 1) / tile_tokens(D) - w.tile;
+  const int64_t n = tokens_to_tiles<D>(w.tokens) - w.tile;
   w.n = n < w.left ? n : w.left;
 }
 template <int D>
@@ -103,9 +105,10 @@ __device__ __forceinline__ bool next_item(const AttentionParams& p, Walk& w) {
   w.tile = 0;
   if (++w.h == p.cache.heads) {
     w.h = 0;
-    do w.b++;
-    while (w.b < p.step.B && committed(p, w.b) == 0);
-    if (w.b >= p.step.B) return false;  // not reached: the run's tiles are counted from the same lengths
+    do {
+      if (++w.b >= p.step.B) return false;  // not reached: the run's tiles are counted from the same lengths
+      w.tokens = committed(p, w.b);
+    } while (w.tokens == 0);
   }
   enter<D>(p, w);
   return true;
@@ -113,21 +116,23 @@ __device__ __forceinline__ bool next_item(const AttentionParams& p, Walk& w) {
 // Runs that N tiles are cut into: none is empty, so that the CTAs between an
 // item's first and last have all left a partial result of it.
 __device__ __forceinline__ int runs_of(const AttentionParams& p, int64_t N) { return N < p.ctas ? (int)N : p.ctas; }
-// Where CTA c's run begins; a whole warp.
+// Where CTA c's run begins; a whole warp.  Up to 32 sequences' lengths are
+// read once, in one trip.
 template <int D>
 __device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
-  int64_t none, all;
-  tiles_before<D>(p, 0, &none, &all);
-  const int64_t N = all * p.cache.heads;
+  const int lane = threadIdx.x & 31;
+  int64_t tokens = lane < p.step.B ? committed(p, lane) : 0, all = tokens_to_tiles<D>(tokens);
+  for (int i = lane + 32; i < p.step.B; i += 32) all += tiles_of<D>(p, i);
+  const int64_t N = warp_sum64(all) * p.cache.heads;
   const int runs = runs_of(p, N);
   Walk w = {0, 0, 0, 0, 0, 0};
   if (c >= runs) return w;
   const int64_t x0 = N * c / runs;
   w.left = N * (c + 1) / runs - x0;
-  const int lane = threadIdx.x & 31;
   int64_t run = 0;
   for (int i0 = 0; i0 < p.step.B; i0 += 32) {
-    const int64_t n = i0 + lane < p.step.B ? tiles_of<D>(p, i0 + lane) * p.cache.heads : 0;
+    if (i0) tokens = i0 + lane < p.step.B ? committed(p, i0 + lane) : 0;
+    const int64_t n = tokens_to_tiles<D>(tokens) * p.cache.heads;
     int64_t inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -139,10 +144,11 @@ __device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
       const int l = __ffs(hit) - 1;
       const int64_t start = __shfl_sync(0xFFFFFFFFu, run + inc - n, l);
       const int64_t per = __shfl_sync(0xFFFFFFFFu, n, l) / p.cache.heads;
+      w.tokens = __shfl_sync(0xFFFFFFFFu, tokens, l);
       w.b = i0 + l;
       w.h = (int)((x0 - start) / per);
       w.tile = (x0 - start) % per;
-      enter<D>(p, w);
+      w.n = per - w.tile < w.left ? per - w.tile : w.left;
       return w;
     }
     run += __shfl_sync(0xFFFFFFFFu, inc, 31);
@@ -184,6 +190,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 // Matrix descriptor of a 128-byte-swizzled operand: rows of 64 16-bit values
 // (128 bytes, on a 1024-byte boundary every eighth), `lbo` bytes between its
 // 64-wide panels where the panels run along M or N, 1024 between groups of
@@ -198,6 +209,19 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// A barrier of the four softmax warps that tells all of them whether all are
+// still at work (every wait before it is bounded, so all four reach it).
+__device__ __forceinline__ bool softmax_bar(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+
 struct AttentionShared {
   uint64_t full[MAX_RING], empty[MAX_RING];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2];
@@ -205,13 +229,14 @@ struct AttentionShared {
   uint32_t tmem;
   int dead;  // a wait has expired: every role leaves its loop
   Walk walk;
+  float m[ATT_ROWS], l[ATT_ROWS];  // each lane's maximum and sum of weights at an item's end
 };
 
 // A bounded wait of one role; on expiry the workspace's status word is set and
 // all roles leave.
 __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, AttentionShared* s, uint32_t* status) {
-  if (*(volatile int*)&s->dead) return false;
-  if (mbar_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
+  if (!*(volatile int*)&s->dead && mbar_wait(bar, parity)) return true;
   s->dead = 1;
   report(status, QLIN_ERR_DEVICE_TIMEOUT);
   return false;
@@ -223,12 +248,19 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, Attent
 // registers into tensor memory in the cache's type and is the A operand of the
 // second product; keys and values are read by the tensor cores straight from
 // the ring that TMA fills (128-byte swizzle; V as the transposed operand).
-// Bound by the stream of keys and values: a 64 KB pair of tiles takes an SM
-// about 2800 cycles at the measured bandwidth, its products about 1000, its
-// softmax about 1500 (two score buffers overlap them).  A row's maximum may
-// grow by 2^8 before its sums are rescaled in tensor memory: weights are
-// relative to a maximum of the past, at most 2^8, which fp16 holds.
-template <typename T, int D>
+//
+// A warp reaches 32 lanes, so with few rows most softmax warps would idle while
+// one takes longer over a tile (128 tokens: 1.9 us measured) than the tile's
+// 64 KB take from memory (1.5 us).  SPLIT = 2 or 4 therefore lays the query
+// rows down that many times (up to 64 or 32 rows), and each copy's warps take
+// their own part of a tile's tokens: P is zero elsewhere, once and for all, and
+// each copy's lanes of O hold its tokens' sums, which are added at the item's
+// end.
+//
+// A row's maximum may grow by 2^8 before its sums are rescaled in tensor
+// memory: weights are relative to a maximum of the past, at most 2^8, which
+// fp16 holds.
+template <typename T, int D, int SPLIT>
 __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __grid_constant__ AttentionParams p) {
   extern __shared__ uint8_t raw[];
   __shared__ AttentionShared sh;
@@ -239,7 +271,8 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t q_smem = base, ring = base + q_bytes(D);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int active = (p.R + 31) / 32;  // softmax warps with rows
+  constexpr int LANES = ATT_ROWS / SPLIT, CW = TK / SPLIT;  // rows of a copy, tokens of a tile that it takes
+  const int active = SPLIT > 1 ? 4 : (p.R + 31) / 32;      // softmax warps with rows
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NB; i++) mbar_init(&s->full[i], 1), mbar_init(&s->empty[i], 1);
@@ -279,16 +312,17 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
       uint32_t i = 0;  // ring position
       bool ok = true;
       do {
-        for (int64_t t = 0; t < w.n && ok; t++) {
-          const int64_t token = (w.tile + t) * TK + box * p.box;
-          int page = -1;
-          if (lane < copies && token < w.tokens) {
-            page = p.step.page_table[w.b * p.step.table_stride + token / p.cache.page_size];
-            if (page < 0 || page >= p.cache.pages) {
-              page = -1;
-              report(p.status, QLIN_ERR_BAD_INDEX);
-            }
+        // page indexes are read a tile ahead
+        const int32_t* table = p.step.page_table + w.b * p.step.table_stride;
+        int64_t token = w.tile * TK + box * p.box;
+        int next = lane < copies && token < w.tokens ? table[token / p.cache.page_size] : -1;
+        for (int64_t t = 0; t < w.n && ok; t++, token += TK) {
+          int page = next;
+          if (lane < copies && token < w.tokens && (page < 0 || page >= p.cache.pages)) {
+            page = -1;
+            report(p.status, QLIN_ERR_BAD_INDEX);
           }
+          next = t + 1 < w.n && lane < copies && token + TK < w.tokens ? table[(token + TK) / p.cache.page_size] : -1;
           const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0)) * p.box * row_bytes;
           for (int kv = 0; kv < 2; kv++, i++) {
             const uint32_t slot = i % NB, use = i / NB;
@@ -386,54 +420,81 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
       } while (next_item<D>(p, w));
     } else {
       // ---- softmax: a thread per query row
-      const int sw = warp, row = sw * 32 + lane;
+      const int at = threadIdx.x, row = at % LANES, copy = at / LANES;  // `at`: the lane of tensor memory
       const bool live = row < p.R;
-      const uint32_t lanes = (uint32_t)(sw * 32) << 16;
+      const uint32_t lanes = (uint32_t)(warp * 32) << 16;
       uint32_t n = 0, seg = 0;
       bool ok = true;
+      if (SPLIT > 1) {  // the other copies' tokens
+        uint32_t zero[32];
+#pragma unroll
+        for (int e = 0; e < 32; e++) zero[e] = 0;
+#pragma unroll
+        for (int c = 0; c < TK; c += 32) tmem_st32(tmem + lanes + P_COL + c, zero);
+        tmem_wait_st();
+      }
       do {
-        {  // the item's query rows, in the swizzled layout
-          const int rows = step_rows(p.step, w.b) * p.group;
+        {  // the item's query rows, in the swizzled layout, once per copy
+          const int units = step_rows(p.step, w.b) * p.group * (D / 8);
           const T* q = static_cast<const T*>(p.q) + (int64_t)w.b * p.step.T * p.q_stride + (int64_t)w.h * p.group * D;
-          for (int c = threadIdx.x; c < rows * (D / 8); c += 128) {
-            const int r = c / (D / 8), e = c % (D / 8);
-            const uint4 x = *reinterpret_cast<const uint4*>(q + (r / p.group) * p.q_stride + (r % p.group) * D + e * 8);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_smem + (e / 8) * (ATT_ROWS * 128) + r * 128 +
-                                                                          (((e & 7) ^ (r & 7)) << 4)),
-                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                         : "memory");
+          for (int c0 = at; c0 < units; c0 += 8 * ATT_ROWS) {  // eight loads in flight
+            uint4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+              const int c = c0 + u * ATT_ROWS, r = c / (D / 8), t = r / p.group;
+              if (c < units)
+                x[u] = *reinterpret_cast<const uint4*>(q + t * p.q_stride + (r - t * p.group) * D + c % (D / 8) * 8);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+              const int c = c0 + u * ATT_ROWS, r = c / (D / 8), e = c % (D / 8);
+              if (c < units) {
+#pragma unroll
+                for (int k = 0; k < SPLIT; k++)
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                   q_smem + (e / 8) * (ATT_ROWS * 128) + (k * LANES + r) * 128 + (((e & 7) ^ (r & 7)) << 4)),
+                               "r"(x[u].x), "r"(x[u].y), "r"(x[u].z), "r"(x[u].w)
+                               : "memory");
+              }
+            }
           }
           fence_proxy_async_smem();
+          tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s->q_full);
         }
         float m_used = -INFINITY, l = 0.f;
-        if (sw < active) {
+        if (warp < active) {
           for (int64_t t = 0; t < w.n; t++) {
             const uint32_t m = n + (uint32_t)t;
             ok = __all_sync(0xFFFFFFFFu, role_wait(&s->s_full[m & 1], (m >> 1) & 1, s, p.status));
             if (!ok) break;
             tc_fence_after();
-            float x[TK];
+            float x[CW];
 #pragma unroll
-            for (int c = 0; c < TK; c += 32)
-              tmem_ld32(tmem + lanes + S_COL + (m & 1) * TK + c, reinterpret_cast<uint32_t*>(x) + c);
+            for (int c = 0; c < CW; c += (CW < 32 ? 16 : 32)) {
+              if constexpr (CW < 32)
+                tmem_ld16(tmem + lanes + S_COL + (m & 1) * TK + copy * CW + c,
+                          *reinterpret_cast<uint32_t(*)[16]>(reinterpret_cast<uint32_t*>(x) + c));
+              else
+                tmem_ld32(tmem + lanes + S_COL + (m & 1) * TK + copy * CW + c, reinterpret_cast<uint32_t*>(x) + c);
+            }
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s->s_free[m & 1]);
             const int64_t ahead = w.tokens - (w.tile + t) * TK;
             if (ahead < TK) {
-              const int valid = (int)ahead;
+              const int valid = (int)ahead - copy * CW;
 #pragma unroll
-              for (int c = 0; c < TK; c++) x[c] = c < valid ? x[c] * p.scale_log2 : -INFINITY;
+              for (int c = 0; c < CW; c++) x[c] = c < valid ? x[c] * p.scale_log2 : -INFINITY;
             } else {
 #pragma unroll
-              for (int c = 0; c < TK; c++) x[c] *= p.scale_log2;
+              for (int c = 0; c < CW; c++) x[c] *= p.scale_log2;
             }
             float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int c = 4; c < TK; c++) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+            for (int c = 4; c < CW; c++) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
             const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             float keep = 1.f;
             bool rescale = false;
@@ -462,11 +523,12 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
               }
               tmem_wait_st();
             }
+            const float m_ref = m_used == -INFINITY ? 0.f : m_used;  // none of a copy's tokens is there
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t w2[TK / 2];
+            uint32_t w2[CW / 2];
 #pragma unroll
-            for (int c = 0; c < TK; c += 2) {
-              const float a = exp2_approx(x[c] - m_used), b2 = exp2_approx(x[c + 1] - m_used);
+            for (int c = 0; c < CW; c += 2) {
+              const float a = exp2_approx(x[c] - m_ref), b2 = exp2_approx(x[c + 1] - m_ref);
               sum[(c >> 1) & 3] += a + b2;
               w2[c / 2] = pack2(a, b2, T());
             }
@@ -476,35 +538,82 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
               if (!ok) break;
               tc_fence_after();
             }
+            const uint32_t pt = tmem + lanes + P_COL + (m & 1) * (TK / 2) + copy * (CW / 2);
+            if constexpr (CW / 2 >= 32) {
 #pragma unroll
-            for (int c = 0; c < TK / 2; c += 32) tmem_st32(tmem + lanes + P_COL + (m & 1) * (TK / 2) + c, w2 + c);
+              for (int c = 0; c < CW / 2; c += 32) tmem_st32(pt + c, w2 + c);
+            } else if constexpr (CW / 2 == 16) {
+              tmem_st16(pt, w2);
+            } else {
+              tmem_st8(pt, w2);
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s->p_full[m & 1]);
           }
         }
-        if (!ok) break;
-        ok = __all_sync(0xFFFFFFFFu, role_wait(&s->o_full, seg & 1, s, p.status));
-        if (!ok) break;
+        if (ok) ok = __all_sync(0xFFFFFFFFu, role_wait(&s->o_full, seg & 1, s, p.status));
+        s->m[at] = m_used;
+        s->l[at] = l;
+        if (!softmax_bar(ok)) break;
         tc_fence_after();
-        if (sw < active) {  // [column][row]: a warp's store is one run
-          float* part = p.partial + (int64_t)(blockIdx.x + w.b * p.cache.heads + w.h) * (D + 2) * p.Rp + row;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lanes + O_COL + c, o);
-            tmem_wait_ld();
-            if (live) {
+        // the copies' sums on a common maximum, added through the query rows'
+        // memory (their product is done), 32 or 64 columns at a time, and
+        // written [column][row]: a warp's store is one run
+        float top = -INFINITY, total = 0.f;
 #pragma unroll
-              for (int e = 0; e < 32; e++) part[(c + e) * p.Rp] = __uint_as_float(o[e]);
+        for (int k = 0; k < SPLIT; k++) top = fmaxf(top, s->m[k * LANES + row]);
+#pragma unroll
+        for (int k = 0; k < SPLIT; k++) {
+          const float mk = s->m[k * LANES + row];
+          if (mk != -INFINITY) total += s->l[k * LANES + row] * exp2_approx(mk - top);
+        }
+        const float f = m_used == -INFINITY ? 0.f : exp2_approx(m_used - top);
+        float* part = p.partial + (int64_t)(blockIdx.x + w.b * p.cache.heads + w.h) * (D + 2) * p.Rp + row;
+        constexpr int CH = D >= 128 ? 64 : 32, MINE = CH / SPLIT;
+        const uint32_t buf = q_smem + at * 4;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += CH) {
+          if (warp < active) {
+            uint32_t o[CH];
+#pragma unroll
+            for (int c = 0; c < CH; c += 32) tmem_ld32(tmem + lanes + O_COL + c0 + c, o + c);
+            tmem_wait_ld();
+            if constexpr (SPLIT == 1) {
+              if (live) {
+#pragma unroll
+                for (int c = 0; c < CH; c++) part[(c0 + c) * p.Rp] = __uint_as_float(o[c]);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < CH; c++)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + c * (ATT_ROWS * 4)), "f"(__uint_as_float(o[c]) * f)
+                             : "memory");
             }
           }
-          if (live) {
-            part[D * p.Rp] = m_used;
-            part[(D + 1) * p.Rp] = l;
+          if constexpr (SPLIT > 1) {
+            (void)softmax_bar(true);
+            if (live) {
+#pragma unroll
+              for (int c = 0; c < MINE; c++) {
+                const uint32_t a = q_smem + ((copy * MINE + c) * ATT_ROWS + row) * 4;
+                float v = 0.f;
+#pragma unroll
+                for (int k = 0; k < SPLIT; k++) {
+                  float y;
+                  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(a + k * LANES * 4) : "memory");
+                  v += y;
+                }
+                part[(c0 + copy * MINE + c) * p.Rp] = v;
+              }
+            }
+            (void)softmax_bar(true);
           }
-          tc_fence_before();
+        }
+        if (live && copy == 0) {
+          part[D * p.Rp] = top;
+          part[(D + 1) * p.Rp] = total;
         }
         n += (uint32_t)w.n;
         seg++;
@@ -526,21 +635,23 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
 // formed before the first launch is waited for.  A few hundred KB from L2.
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) qlin_attention_join_kernel(const __grid_constant__ AttentionParams p) {
-  __shared__ float weight[ATT_MAX_CTAS][8];  // of each partial result, per row
-  __shared__ float own[8][QLIN_MAX_TREE];    // of each of the step's rows
+  __shared__ __align__(16) float weight[ATT_MAX_CTAS][8];  // of each partial result, per row
+  __shared__ float own[QLIN_MAX_TREE][8];                  // of each of the step's rows
   __shared__ int64_t place[QLIN_MAX_TREE];
-  __shared__ float o[8][JOIN_COLS + 1];
+  __shared__ __align__(16) float sums[JOIN_GROUPS][JOIN_COLS][8];
   __shared__ int64_t range[2];
   constexpr int E = D / 32;
   const int item = blockIdx.x, b = item / p.cache.heads, h = item % p.cache.heads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r0 = blockIdx.y * 8, row = r0 + warp, t = row / p.group;
   const int len = p.step.len[b], rows = step_rows(p.step, b);
-  const bool live = len >= 0 && row < p.R && t < rows;
-  if (len >= 0 && warp == 0) {
+  const bool live = len >= 0 && warp < 8 && row < p.R && t < rows;  // a warp per row for its weights
+  if (warp == 8) {
     int64_t before, all;
     tiles_before<D>(p, b, &before, &all);
     if (lane == 0) range[0] = before, range[1] = all;
+  }
+  if (len >= 0 && warp == 0) {
     if (lane < rows) {
       place[lane] = token_offset(p.cache, p.step, b, (int64_t)len + lane);
       if (place[lane] < 0 || (int64_t)len > (int64_t)p.step.max_pages * p.cache.page_size)
@@ -556,6 +667,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) qlin_attention_join_kernel(const
     float2 f[E / 2];
 #pragma unroll
     for (int e = 0; e < E; e += 2) f[e / 2] = unpack2(*reinterpret_cast<const uint32_t*>(q + e), T());
+#pragma unroll 4
     for (int j = 0; j < rows; j++) {
       if (!(mask >> j & 1) || place[j] < 0) continue;
       const T* k = static_cast<const T*>(p.cache.k) + place[j] + h * p.cache.head_stride + lane * E;
@@ -582,55 +694,88 @@ __global__ void __launch_bounds__(JOIN_THREADS) qlin_attention_join_kernel(const
   const int64_t step = (int64_t)(D + 2) * p.Rp;
   const float* part = p.partial + (int64_t)(first + item) * step + r0;
   if (live) {
-    float m = mine;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, part[i * step + (int64_t)D * p.Rp + warp]);
+    constexpr int PER = (ATT_MAX_CTAS + 31) / 32;
+    float pm[PER], pl[PER], m = mine;
+#pragma unroll
+    for (int k = 0; k < PER; k++) {
+      const float* ml = part + (lane + 32 * k) * step + (int64_t)D * p.Rp + warp;
+      const bool there = lane + 32 * k < parts;
+      pm[k] = there ? ml[0] : -INFINITY;
+      pl[k] = there ? ml[p.Rp] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < PER; k++) m = fmaxf(m, pm[k]);
 #pragma unroll
     for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, i));
     const bool seen = lane < rows && (step_mask(p.step, b, t) >> lane & 1) && place[lane] >= 0;
     const float w = seen ? exp2f(mine - m) : 0.f;
     float l = w;
-    for (int i = lane; i < parts; i += 32) {
-      const float* ml = part + i * step + (int64_t)D * p.Rp + warp;
-      const float f = exp2f(ml[0] - m);
-      weight[i][warp] = f;
-      l = fmaf(f, ml[p.Rp], l);
+#pragma unroll
+    for (int k = 0; k < PER; k++) {
+      pm[k] = lane + 32 * k < parts ? exp2f(pm[k] - m) : 0.f;
+      l = fmaf(pm[k], pl[k], l);
     }
 #pragma unroll
     for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, i);
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    own[warp][lane] = w * inv;
-    for (int i = lane; i < parts; i += 32) weight[i][warp] *= inv;
+    own[lane][warp] = w * inv;
+#pragma unroll
+    for (int k = 0; k < PER; k++)
+      if (lane + 32 * k < parts) weight[lane + 32 * k][warp] = pm[k] * inv;
   }
   __syncthreads();
-  const int r = threadIdx.x & 7, t2 = (r0 + r) / p.group;
-  if (r0 + r < p.R && t2 < rows) {
-    const uint32_t mask = step_mask(p.step, b, t2);
-    for (int c = threadIdx.x >> 3; c < JOIN_COLS; c += JOIN_THREADS / 8) {
-      const int col = blockIdx.z * JOIN_COLS + c;
-      float acc = 0.f;
-      const float* x = part + (int64_t)col * p.Rp + r;
+  {  // four rows and a column per thread, every fourth partial result
+    const int half = threadIdx.x & 1, c = (threadIdx.x >> 1) % JOIN_COLS, group = threadIdx.x / (2 * JOIN_COLS);
+    const int col = blockIdx.z * JOIN_COLS + c;
+    const float4* x = reinterpret_cast<const float4*>(part + (int64_t)col * p.Rp + half * 4);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-      for (int i = 0; i < parts; i++) acc = fmaf(weight[i][r], x[i * step], acc);
-      const T* v = static_cast<const T*>(p.cache.v) + h * p.cache.head_stride + col;
-      for (int j = 0; j < rows; j++)
-        if ((mask >> j & 1) && place[j] >= 0) acc = fmaf(own[r][j], to_float(v[place[j]]), acc);
-      o[r][c] = acc;
+    for (int i = group; i < parts; i += JOIN_GROUPS) {
+      const float4 v = x[i * (step / 4)], f = *reinterpret_cast<const float4*>(&weight[i][half * 4]);
+      acc.x = fmaf(f.x, v.x, acc.x), acc.y = fmaf(f.y, v.y, acc.y);
+      acc.z = fmaf(f.z, v.z, acc.z), acc.w = fmaf(f.w, v.w, acc.w);
     }
+    const T* v = static_cast<const T*>(p.cache.v) + h * p.cache.head_stride + col;
+    uint32_t mask[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const int r = r0 + half * 4 + k, tr = r / p.group;
+      mask[k] = r < p.R && tr < rows ? step_mask(p.step, b, tr) : 0;
+    }
+    for (int j = group; j < rows; j += JOIN_GROUPS) {
+      if (!((mask[0] | mask[1] | mask[2] | mask[3]) >> j & 1) || place[j] < 0) continue;
+      const float y = to_float(v[place[j]]);
+      const float* f = &own[j][half * 4];
+      if (mask[0] >> j & 1) acc.x = fmaf(f[0], y, acc.x);
+      if (mask[1] >> j & 1) acc.y = fmaf(f[1], y, acc.y);
+      if (mask[2] >> j & 1) acc.z = fmaf(f[2], y, acc.z);
+      if (mask[3] >> j & 1) acc.w = fmaf(f[3], y, acc.w);
+    }
+    *reinterpret_cast<float4*>(&sums[group][c][half * 4]) = acc;
   }
   __syncthreads();
   if (live) {  // a row's 64 columns: one run
+    float o[2];
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      o[k] = 0.f;
+#pragma unroll
+      for (int g = 0; g < JOIN_GROUPS; g++) o[k] += sums[g][2 * lane + k][warp];
+    }
     __nv_bfloat16* out = p.out + ((int64_t)b * p.step.T + t) * p.out_stride +
                          ((int64_t)h * p.group + row % p.group) * D + blockIdx.z * JOIN_COLS;
-    *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack2(o[warp][2 * lane], o[warp][2 * lane + 1], __nv_bfloat16());
+    *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack2(o[0], o[1], __nv_bfloat16());
   }
 }
 
 struct Kernels {
-  const void *main, *join;
+  const void *main[3], *join;  // main: 1, 2 and 4 copies of the query rows
 };
 template <typename T, int D>
 Kernels kernels_of() {
-  return {reinterpret_cast<const void*>(qlin_attention_kernel<T, D>),
+  return {{reinterpret_cast<const void*>(qlin_attention_kernel<T, D, 1>),
+           reinterpret_cast<const void*>(qlin_attention_kernel<T, D, 2>),
+           reinterpret_cast<const void*>(qlin_attention_kernel<T, D, 4>)},
           reinterpret_cast<const void*>(qlin_attention_join_kernel<T, D>)};
 }
 Kernels attention_kernels(int dtype, int width) {
@@ -677,9 +822,9 @@ qlin_status attention_setup(int* ctas) {
     cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     for (int dtype : {QLIN_BF16, QLIN_F16})
       for (int width : {64, 128, 256})
-        if (e == cudaSuccess)
-          e = cudaFuncSetAttribute(attention_kernels(dtype, width).main, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   (int)attention_smem(width));
+        for (const void* fn : attention_kernels(dtype, width).main)
+          if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attention_smem(width));
     d.ctas = sms < ATT_MAX_CTAS ? sms : ATT_MAX_CTAS;
     d.ready = e == cudaSuccess && g_encode && sms > 0 ? QLIN_OK : QLIN_ERR_CUDA;
     if (e != cudaSuccess) (void)cudaGetLastError();
@@ -767,7 +912,8 @@ qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* 
   p.ctas = ctas;
   void* args[] = {&p};
   const Kernels fn = attention_kernels(cache->dtype, cache->width);
-  st = launch_step(fn.main, dim3((unsigned)ctas, 1, 1), dim3(ATT_THREADS, 1, 1), attention_smem(cache->width),
+  const int copies = p.R > ATT_ROWS / 2 ? 0 : p.R > ATT_ROWS / 4 ? 1 : 2;
+  st = launch_step(fn.main[copies], dim3((unsigned)ctas, 1, 1), dim3(ATT_THREADS, 1, 1), attention_smem(cache->width),
                    static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0);
   if (st != QLIN_OK) return st;
   return launch_step(fn.join, dim3((unsigned)(step->B * cache->heads), (unsigned)(p.Rp / 8), (unsigned)(D / JOIN_COLS)),
