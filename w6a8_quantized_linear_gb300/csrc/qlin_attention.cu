@@ -25,7 +25,7 @@ constexpr int PRODUCER = 4, ISSUER = 5, CLEANER = 6;
 constexpr int ATT_ROWS = 128;      // query rows of an item at most: the lanes of tensor memory
 constexpr int ATT_MAX_CTAS = 160;  // the workspace holds the partial results of this many (one per SM)
 constexpr int JOIN_THREADS = 512;
-constexpr int JOIN_COLS = 64;
+constexpr int JOIN_COLS = 32;
 constexpr int JOIN_GROUPS = JOIN_THREADS / (2 * JOIN_COLS);  // threads that share a column's partial results
 constexpr float RESCALE_AT = 8.f;  // log2 units that a row's maximum may rise before its sums are rescaled
 
@@ -52,6 +52,7 @@ struct AttentionParams {
   int Hq, group, R, Rp;  // query rows of an item: T * group, padded to 8
   int ctas;
   int box;           // tokens per TMA copy: a page or a tile, whichever is smaller
+  int page_shift;    // log2 of the page size
 };
 
 __device__ __forceinline__ int64_t committed(const AttentionParams& p, int b) {  // tokens that are there
@@ -116,6 +117,11 @@ __device__ __forceinline__ bool next_item(const AttentionParams& p, Walk& w) {
 // Runs that N tiles are cut into: none is empty, so that the CTAs between an
 // item's first and last have all left a partial result of it.
 __device__ __forceinline__ int runs_of(const AttentionParams& p, int64_t N) { return N < p.ctas ? (int)N : p.ctas; }
+// First tile of run c, floor(N c / runs), in 32 bits where they suffice.
+__device__ __forceinline__ int64_t run_start(int64_t N, int c, int runs) {
+  const int64_t x = N * c;
+  return x >> 32 ? x / runs : (int64_t)((uint32_t)x / (uint32_t)runs);
+}
 // Where CTA c's run begins; a whole warp.  Up to 32 sequences' lengths are
 // read once, in one trip.
 template <int D>
@@ -127,8 +133,8 @@ __device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
   const int runs = runs_of(p, N);
   Walk w = {0, 0, 0, 0, 0, 0};
   if (c >= runs) return w;
-  const int64_t x0 = N * c / runs;
-  w.left = N * (c + 1) / runs - x0;
+  const int64_t x0 = run_start(N, c, runs);
+  w.left = run_start(N, c + 1, runs) - x0;
   int64_t run = 0;
   for (int i0 = 0; i0 < p.step.B; i0 += 32) {
     if (i0) tokens = i0 + lane < p.step.B ? committed(p, i0 + lane) : 0;
@@ -143,11 +149,11 @@ __device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
     if (hit) {
       const int l = __ffs(hit) - 1;
       const int64_t start = __shfl_sync(0xFFFFFFFFu, run + inc - n, l);
-      const int64_t per = __shfl_sync(0xFFFFFFFFu, n, l) / p.cache.heads;
       w.tokens = __shfl_sync(0xFFFFFFFFu, tokens, l);
+      const int64_t per = tokens_to_tiles<D>(w.tokens);
       w.b = i0 + l;
-      w.h = (int)((x0 - start) / per);
-      w.tile = (x0 - start) % per;
+      w.h = (int)run_start(x0 - start, 1, (int)per);  // tiles of one head: below 2^31
+      w.tile = x0 - start - w.h * per;
       w.n = per - w.tile < w.left ? per - w.tile : w.left;
       return w;
     }
@@ -157,7 +163,10 @@ __device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
   return w;
 }
 // The CTA whose run holds tile x of N: floor(c N / runs) <= x < floor((c + 1) N / runs)
-__device__ __forceinline__ int cta_of(int64_t x, int64_t N, int runs) { return (int)(((x + 1) * runs - 1) / N); }
+__device__ __forceinline__ int cta_of(int64_t x, int64_t N, int runs) {
+  const int64_t y = (x + 1) * runs - 1;
+  return y >> 32 ? (int)(y / N) : (int)((uint32_t)y / (uint32_t)N);  // y >= N - 1: N fits where y does, but for y = N - 1
+}
 
 // ---- PTX -------------------------------------------------------------------------
 
@@ -261,7 +270,7 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, Attent
 // memory: weights are relative to a maximum of the past, at most 2^8, which
 // fp16 holds.
 template <typename T, int D, int SPLIT>
-__global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __grid_constant__ AttentionParams p) {
+__global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention_kernel(const __grid_constant__ AttentionParams p) {
   extern __shared__ uint8_t raw[];
   __shared__ AttentionShared sh;
   constexpr int TK = tile_tokens(D), TB = tile_bytes(D), NB = ring_buffers(D), PANELS = D / 64;
@@ -315,14 +324,14 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
         // page indexes are read a tile ahead
         const int32_t* table = p.step.page_table + w.b * p.step.table_stride;
         int64_t token = w.tile * TK + box * p.box;
-        int next = lane < copies && token < w.tokens ? table[token / p.cache.page_size] : -1;
+        int next = lane < copies && token < w.tokens ? table[token >> p.page_shift] : -1;
         for (int64_t t = 0; t < w.n && ok; t++, token += TK) {
           int page = next;
           if (lane < copies && token < w.tokens && (page < 0 || page >= p.cache.pages)) {
             page = -1;
             report(p.status, QLIN_ERR_BAD_INDEX);
           }
-          next = t + 1 < w.n && lane < copies && token + TK < w.tokens ? table[(token + TK) / p.cache.page_size] : -1;
+          next = t + 1 < w.n && lane < copies && token + TK < w.tokens ? table[(token + TK) >> p.page_shift] : -1;
           const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0)) * p.box * row_bytes;
           for (int kv = 0; kv < 2; kv++, i++) {
             const uint32_t slot = i % NB, use = i / NB;
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
             __syncwarp();
             if (page >= 0)
               tma_load_4d(ring + slot * TB + (panel * TK + box * p.box) * 128, kv ? &p.map_v : &p.map_k, panel * 64,
-                          (int)(token % p.cache.page_size), w.h, page, &s->full[slot]);
+                          (int)(token & (p.cache.page_size - 1)), w.h, page, &s->full[slot]);
           }
         }
       } while (ok && next_item<D>(p, w));
@@ -437,16 +446,17 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
         {  // the item's query rows, in the swizzled layout, once per copy
           const int units = step_rows(p.step, w.b) * p.group * (D / 8);
           const T* q = static_cast<const T*>(p.q) + (int64_t)w.b * p.step.T * p.q_stride + (int64_t)w.h * p.group * D;
-          for (int c0 = at; c0 < units; c0 += 8 * ATT_ROWS) {  // eight loads in flight
-            uint4 x[8];
+          constexpr int BATCH = 8;  // loads in flight
+          for (int c0 = at; c0 < units; c0 += BATCH * ATT_ROWS) {
+            uint4 x[BATCH];
 #pragma unroll
-            for (int u = 0; u < 8; u++) {
+            for (int u = 0; u < BATCH; u++) {
               const int c = c0 + u * ATT_ROWS, r = c / (D / 8), t = r / p.group;
               if (c < units)
                 x[u] = *reinterpret_cast<const uint4*>(q + t * p.q_stride + (r - t * p.group) * D + c % (D / 8) * 8);
             }
 #pragma unroll
-            for (int u = 0; u < 8; u++) {
+            for (int u = 0; u < BATCH; u++) {
               const int c = c0 + u * ATT_ROWS, r = c / (D / 8), e = c % (D / 8);
               if (c < units) {
 #pragma unroll
@@ -470,31 +480,34 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
             ok = __all_sync(0xFFFFFFFFu, role_wait(&s->s_full[m & 1], (m >> 1) & 1, s, p.status));
             if (!ok) break;
             tc_fence_after();
-            float x[CW];
-#pragma unroll
-            for (int c = 0; c < CW; c += (CW < 32 ? 16 : 32)) {
-              if constexpr (CW < 32)
-                tmem_ld16(tmem + lanes + S_COL + (m & 1) * TK + copy * CW + c,
-                          *reinterpret_cast<uint32_t(*)[16]>(reinterpret_cast<uint32_t*>(x) + c));
+            // 32 scores at a time: the maximum first, then (read again, but for
+            // the last 32) the weights
+            constexpr int CX = CW < 32 ? CW : 32;
+            const int64_t ahead = w.tokens - (w.tile + t) * TK - copy * CW;  // of this copy's tokens, those that are there
+            const int valid = ahead < CW ? (int)ahead : CW;
+            const uint32_t st = tmem + lanes + S_COL + (m & 1) * TK + copy * CW;
+            float x[CX];
+            auto scores = [&](int c0) {
+              if constexpr (CX < 32)
+                tmem_ld16(st + c0, *reinterpret_cast<uint32_t(*)[16]>(x));
               else
-                tmem_ld32(tmem + lanes + S_COL + (m & 1) * TK + copy * CW + c, reinterpret_cast<uint32_t*>(x) + c);
+                tmem_ld32(st + c0, reinterpret_cast<uint32_t*>(x));
+              tmem_wait_ld();
+              if (valid < CW) {
+#pragma unroll
+                for (int c = 0; c < CX; c++) x[c] = c0 + c < valid ? x[c] * p.scale_log2 : -INFINITY;
+              } else {
+#pragma unroll
+                for (int c = 0; c < CX; c++) x[c] *= p.scale_log2;
+              }
+            };
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c0 = 0; c0 < CW; c0 += CX) {
+              scores(c0);
+#pragma unroll
+              for (int c = 0; c < CX; c++) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
             }
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s->s_free[m & 1]);
-            const int64_t ahead = w.tokens - (w.tile + t) * TK;
-            if (ahead < TK) {
-              const int valid = (int)ahead - copy * CW;
-#pragma unroll
-              for (int c = 0; c < CW; c++) x[c] = c < valid ? x[c] * p.scale_log2 : -INFINITY;
-            } else {
-#pragma unroll
-              for (int c = 0; c < CW; c++) x[c] *= p.scale_log2;
-            }
-            float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int c = 4; c < CW; c++) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
             const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             float keep = 1.f;
             bool rescale = false;
@@ -524,29 +537,32 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
               tmem_wait_st();
             }
             const float m_ref = m_used == -INFINITY ? 0.f : m_used;  // none of a copy's tokens is there
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t w2[CW / 2];
-#pragma unroll
-            for (int c = 0; c < CW; c += 2) {
-              const float a = exp2_approx(x[c] - m_ref), b2 = exp2_approx(x[c + 1] - m_ref);
-              sum[(c >> 1) & 3] += a + b2;
-              w2[c / 2] = pack2(a, b2, T());
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             if (m >= 2) {
               ok = __all_sync(0xFFFFFFFFu, role_wait(&s->p_free[m & 1], ((m >> 1) - 1) & 1, s, p.status));
               if (!ok) break;
               tc_fence_after();
             }
             const uint32_t pt = tmem + lanes + P_COL + (m & 1) * (TK / 2) + copy * (CW / 2);
-            if constexpr (CW / 2 >= 32) {
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int c = 0; c < CW / 2; c += 32) tmem_st32(pt + c, w2 + c);
-            } else if constexpr (CW / 2 == 16) {
-              tmem_st16(pt, w2);
-            } else {
-              tmem_st8(pt, w2);
+            for (int c0 = CW - CX; c0 >= 0; c0 -= CX) {
+              if (c0 != CW - CX) scores(c0);
+              uint32_t w2[CX / 2];
+#pragma unroll
+              for (int c = 0; c < CX; c += 2) {
+                const float a = exp2_approx(x[c] - m_ref), b2 = exp2_approx(x[c + 1] - m_ref);
+                sum[(c >> 1) & 3] += a + b2;
+                w2[c / 2] = pack2(a, b2, T());
+              }
+              if constexpr (CX == 32)
+                tmem_st16(pt + c0 / 2, w2);
+              else
+                tmem_st8(pt + c0 / 2, w2);
             }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s->s_free[m & 1]);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -559,7 +575,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
         if (!softmax_bar(ok)) break;
         tc_fence_after();
         // the copies' sums on a common maximum, added through the query rows'
-        // memory (their product is done), 32 or 64 columns at a time, and
+        // memory (their product is done), 32 columns at a time, and
         // written [column][row]: a warp's store is one run
         float top = -INFINITY, total = 0.f;
 #pragma unroll
@@ -571,24 +587,26 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
         }
         const float f = m_used == -INFINITY ? 0.f : exp2_approx(m_used - top);
         float* part = p.partial + (int64_t)(blockIdx.x + w.b * p.cache.heads + w.h) * (D + 2) * p.Rp + row;
-        constexpr int CH = D >= 128 ? 64 : 32, MINE = CH / SPLIT;
-        const uint32_t buf = q_smem + at * 4;
+        // 32 columns of a lane are 128 bytes, their 16-byte units swizzled by the lane
+        constexpr int CH = 32, MINE = CH / SPLIT, BUFFERS = q_bytes(D) >= 2 * ATT_ROWS * CH * 4 ? 2 : 1;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += CH) {
+          const uint32_t buf = q_smem + (c0 / CH % BUFFERS) * (ATT_ROWS * CH * 4);
           if (warp < active) {
             uint32_t o[CH];
-#pragma unroll
-            for (int c = 0; c < CH; c += 32) tmem_ld32(tmem + lanes + O_COL + c0 + c, o + c);
+            tmem_ld32(tmem + lanes + O_COL + c0, o);
             tmem_wait_ld();
             if constexpr (SPLIT == 1) {
               if (live) {
 #pragma unroll
                 for (int c = 0; c < CH; c++) part[(c0 + c) * p.Rp] = __uint_as_float(o[c]);
               }
-            } else {
+            } else if (live) {
 #pragma unroll
-              for (int c = 0; c < CH; c++)
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + c * (ATT_ROWS * 4)), "f"(__uint_as_float(o[c]) * f)
+              for (int c = 0; c < CH; c += 4)
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(buf + at * 128 + (((c / 4) ^ (at & 7)) << 4)),
+                             "f"(__uint_as_float(o[c]) * f), "f"(__uint_as_float(o[c + 1]) * f),
+                             "f"(__uint_as_float(o[c + 2]) * f), "f"(__uint_as_float(o[c + 3]) * f)
                              : "memory");
             }
           }
@@ -596,19 +614,25 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
             (void)softmax_bar(true);
             if (live) {
 #pragma unroll
-              for (int c = 0; c < MINE; c++) {
-                const uint32_t a = q_smem + ((copy * MINE + c) * ATT_ROWS + row) * 4;
-                float v = 0.f;
+              for (int c = 0; c < MINE; c += 4) {
+                float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < SPLIT; k++) {
-                  float y;
-                  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(a + k * LANES * 4) : "memory");
-                  v += y;
+                  float y[4];
+                  const int from = k * LANES + row;
+                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                               : "=f"(y[0]), "=f"(y[1]), "=f"(y[2]), "=f"(y[3])
+                               : "r"(buf + from * 128 + ((((copy * MINE + c) / 4) ^ (from & 7)) << 4))
+                               : "memory");
+#pragma unroll
+                  for (int e = 0; e < 4; e++) v[e] += y[e];
                 }
-                part[(c0 + copy * MINE + c) * p.Rp] = v;
+#pragma unroll
+                for (int e = 0; e < 4; e++) part[(c0 + copy * MINE + c + e) * p.Rp] = v[e];
               }
             }
-            (void)softmax_bar(true);
+            // with two buffers the next chunk's barrier stands between these reads and the writes after it
+            if (BUFFERS == 1 || c0 + CH == D) (void)softmax_bar(true);
           }
         }
         if (live && copy == 0) {
@@ -630,11 +654,11 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) qlin_attention_kernel(const __
 }
 
 // Joins an item's partial results with the step's own rows, eight query rows
-// and 64 columns per block: o = (sum_s 2^(m_s - M) O_s + sum_j 2^(x_j - M) v_j)
+// and 32 columns per block: o = (sum_s 2^(m_s - M) O_s + sum_j 2^(x_j - M) v_j)
 // / (the same sum of weights).  The scores x_j of the keys that a row sees are
 // formed before the first launch is waited for.  A few hundred KB from L2.
 template <typename T, int D>
-__global__ void __launch_bounds__(JOIN_THREADS) qlin_attention_join_kernel(const __grid_constant__ AttentionParams p) {
+__global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(const __grid_constant__ AttentionParams p) {
   __shared__ __align__(16) float weight[ATT_MAX_CTAS][8];  // of each partial result, per row
   __shared__ float own[QLIN_MAX_TREE][8];                  // of each of the step's rows
   __shared__ int64_t place[QLIN_MAX_TREE];
@@ -682,15 +706,35 @@ __global__ void __launch_bounds__(JOIN_THREADS) qlin_attention_join_kernel(const
       if (lane == j) mine = x * p.scale_log2;
     }
   }
-  pdl_wait();
-  pdl_launch_dependents();
-  if (len < 0 || rows == 0) return;
   // this item's tiles among all, and the CTAs whose runs hold them
   const int64_t per = tiles_of<D>(p, b), N = range[1] * p.cache.heads;
   const int64_t start = range[0] * p.cache.heads + h * per;
   const int runs = runs_of(p, N);
   const int first = per ? cta_of(start, N, runs) : 0;
   const int parts = per ? cta_of(start + per - 1, N, runs) - first + 1 : 0;
+  // four rows and a column per thread, every JOIN_GROUPS-th partial result and row of the step
+  const int half = threadIdx.x & 1, c = (threadIdx.x >> 1) % JOIN_COLS, group = threadIdx.x / (2 * JOIN_COLS);
+  const int col = blockIdx.z * JOIN_COLS + c;
+  uint32_t mask[4];
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const int r = r0 + half * 4 + k, tr = r / p.group;
+    mask[k] = len >= 0 && r < p.R && tr < rows ? step_mask(p.step, b, tr) : 0;
+  }
+  const uint32_t any = mask[0] | mask[1] | mask[2] | mask[3];
+  constexpr int OWN = QLIN_MAX_TREE / JOIN_GROUPS;
+  float y[OWN];
+#pragma unroll
+  for (int i = 0; i < OWN; i++) {
+    const int j = group + i * JOIN_GROUPS;
+    y[i] = 0.f;
+    if (j < rows && (any >> j & 1) && place[j] >= 0)
+      y[i] = to_float(static_cast<const T*>(p.cache.v)[place[j] + h * p.cache.head_stride + col]);
+  }
+  const uint32_t seen_mask = live ? step_mask(p.step, b, t) : 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (len < 0 || rows == 0) return;
   const int64_t step = (int64_t)(D + 2) * p.Rp;
   const float* part = p.partial + (int64_t)(first + item) * step + r0;
   if (live) {
@@ -707,7 +751,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) qlin_attention_join_kernel(const
     for (int k = 0; k < PER; k++) m = fmaxf(m, pm[k]);
 #pragma unroll
     for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, i));
-    const bool seen = lane < rows && (step_mask(p.step, b, t) >> lane & 1) && place[lane] >= 0;
+    const bool seen = lane < rows && (seen_mask >> lane & 1) && place[lane] >= 0;
     const float w = seen ? exp2f(mine - m) : 0.f;
     float l = w;
 #pragma unroll
@@ -724,47 +768,46 @@ __global__ void __launch_bounds__(JOIN_THREADS) qlin_attention_join_kernel(const
       if (lane + 32 * k < parts) weight[lane + 32 * k][warp] = pm[k] * inv;
   }
   __syncthreads();
-  {  // four rows and a column per thread, every fourth partial result
-    const int half = threadIdx.x & 1, c = (threadIdx.x >> 1) % JOIN_COLS, group = threadIdx.x / (2 * JOIN_COLS);
-    const int col = blockIdx.z * JOIN_COLS + c;
+  {
     const float4* x = reinterpret_cast<const float4*>(part + (int64_t)col * p.Rp + half * 4);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = group; i < parts; i += JOIN_GROUPS) {
-      const float4 v = x[i * (step / 4)], f = *reinterpret_cast<const float4*>(&weight[i][half * 4]);
-      acc.x = fmaf(f.x, v.x, acc.x), acc.y = fmaf(f.y, v.y, acc.y);
-      acc.z = fmaf(f.z, v.z, acc.z), acc.w = fmaf(f.w, v.w, acc.w);
-    }
-    const T* v = static_cast<const T*>(p.cache.v) + h * p.cache.head_stride + col;
-    uint32_t mask[4];
+    for (int i0 = group; i0 < parts; i0 += 4 * JOIN_GROUPS) {
+      float4 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const int r = r0 + half * 4 + k, tr = r / p.group;
-      mask[k] = r < p.R && tr < rows ? step_mask(p.step, b, tr) : 0;
+      for (int k = 0; k < 4; k++) {
+        const int i = i0 + k * JOIN_GROUPS;
+        if (i < parts) v[k] = x[i * (step / 4)];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const int i = i0 + k * JOIN_GROUPS;
+        if (i < parts) {
+          const float4 f = *reinterpret_cast<const float4*>(&weight[i][half * 4]);
+          acc.x = fmaf(f.x, v[k].x, acc.x), acc.y = fmaf(f.y, v[k].y, acc.y);
+          acc.z = fmaf(f.z, v[k].z, acc.z), acc.w = fmaf(f.w, v[k].w, acc.w);
+        }
+      }
     }
-    for (int j = group; j < rows; j += JOIN_GROUPS) {
-      if (!((mask[0] | mask[1] | mask[2] | mask[3]) >> j & 1) || place[j] < 0) continue;
-      const float y = to_float(v[place[j]]);
-      const float* f = &own[j][half * 4];
-      if (mask[0] >> j & 1) acc.x = fmaf(f[0], y, acc.x);
-      if (mask[1] >> j & 1) acc.y = fmaf(f[1], y, acc.y);
-      if (mask[2] >> j & 1) acc.z = fmaf(f[2], y, acc.z);
-      if (mask[3] >> j & 1) acc.w = fmaf(f[3], y, acc.w);
+#pragma unroll
+    for (int i = 0; i < OWN; i++) {  // only what a row sees: what it does not may be NaN
+      const int j = group + i * JOIN_GROUPS;
+      if (j < rows && (any >> j & 1) && place[j] >= 0) {
+        const float* f = &own[j][half * 4];
+        if (mask[0] >> j & 1) acc.x = fmaf(f[0], y[i], acc.x);
+        if (mask[1] >> j & 1) acc.y = fmaf(f[1], y[i], acc.y);
+        if (mask[2] >> j & 1) acc.z = fmaf(f[2], y[i], acc.z);
+        if (mask[3] >> j & 1) acc.w = fmaf(f[3], y[i], acc.w);
+      }
     }
     *reinterpret_cast<float4*>(&sums[group][c][half * 4]) = acc;
   }
   __syncthreads();
-  if (live) {  // a row's 64 columns: one run
-    float o[2];
+  if (live) {  // a row's columns: one run
+    float o = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-      o[k] = 0.f;
-#pragma unroll
-      for (int g = 0; g < JOIN_GROUPS; g++) o[k] += sums[g][2 * lane + k][warp];
-    }
-    __nv_bfloat16* out = p.out + ((int64_t)b * p.step.T + t) * p.out_stride +
-                         ((int64_t)h * p.group + row % p.group) * D + blockIdx.z * JOIN_COLS;
-    *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack2(o[0], o[1], __nv_bfloat16());
+    for (int g = 0; g < JOIN_GROUPS; g++) o += sums[g][lane][warp];
+    p.out[((int64_t)b * p.step.T + t) * p.out_stride + ((int64_t)h * p.group + row % p.group) * D +
+          blockIdx.z * JOIN_COLS + lane] = __float2bfloat16(o);
   }
 }
 
@@ -897,6 +940,8 @@ qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* 
   const int tile = tile_tokens(cache->width);
   p.box = cache->page_size < tile ? cache->page_size : tile;
   if (!encode(&p.map_k, cache, cache->k, p.box) || !encode(&p.map_v, cache, cache->v, p.box)) return QLIN_ERR_CUDA;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < cache->page_size) p.page_shift++;
   p.cache = *cache;
   p.step = *step;
   p.q = q;

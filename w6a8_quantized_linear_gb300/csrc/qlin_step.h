@@ -100,11 +100,12 @@ __device__ __forceinline__ uint32_t step_mask(const qlin_kv_step& s, int b, int 
 // Element offset of a token's row in k and v, without its head; -1 where the
 // page is out of range.
 __device__ __forceinline__ int64_t token_offset(const qlin_kv_cache& c, const qlin_kv_step& s, int b, int64_t token) {
-  const int64_t slot = token / c.page_size;
+  const int shift = 31 - __clz(c.page_size);  // a power of two
+  const int64_t slot = token >> shift;
   if (slot >= s.max_pages) return -1;
   const int page = s.page_table[b * s.table_stride + slot];
   if (page < 0 || page >= c.pages) return -1;
-  return page * c.page_stride + (token % c.page_size) * c.token_stride;
+  return page * c.page_stride + (token & (c.page_size - 1)) * c.token_stride;
 }
 __device__ __forceinline__ void report(uint32_t* status, uint32_t what) {
   if (status) atomicCAS(status, 0u, what);  // the first finding stays
