@@ -13,6 +13,7 @@
 #include <cmath>
 #include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "qlin_ptx.cuh"
 #include "qlin_step.h"
@@ -25,8 +26,6 @@ constexpr int PRODUCER = 4, ISSUER = 5, CLEANER = 6;
 constexpr int ATT_ROWS = 128;      // query rows of an item at most: the lanes of tensor memory
 constexpr int ATT_MAX_CTAS = 160;  // the workspace holds the partial results of this many (one per SM)
 constexpr int JOIN_THREADS = 512;
-constexpr int JOIN_COLS = 32;
-constexpr int JOIN_GROUPS = JOIN_THREADS / (2 * JOIN_COLS);  // threads that share a column's partial results
 constexpr float RESCALE_AT = 8.f;  // log2 units that a row's maximum may rise before its sums are rescaled
 
 // Tokens of a tile: 32 KB of keys and of values (16 KB at width 64).
@@ -40,7 +39,7 @@ __host__ __device__ constexpr int ring_buffers(int width) { return (200 * 1024 -
 constexpr int MAX_RING = 11;
 
 struct AttentionParams {
-  CUtensorMap map_k, map_v;
+  CUtensorMap map_k, map_v, map_q;
   qlin_kv_cache cache;
   qlin_kv_step step;
   const void* q;
@@ -178,6 +177,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -230,6 +236,8 @@ __device__ __forceinline__ bool softmax_bar(bool ok) {
       : "memory");
   return all != 0;
 }
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
 struct AttentionShared {
   uint64_t full[MAX_RING], empty[MAX_RING];
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
       mbar_init(&s->p_full[i], active);
       mbar_init(&s->p_free[i], 1);
     }
-    mbar_init(&s->q_full, 4);
+    mbar_init(&s->q_full, 1);
     mbar_init(&s->o_full, 1);
     mbar_init(&s->v_dirty, 1);
     mbar_init(&s->v_clean, 1);
@@ -443,35 +451,14 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
         tmem_wait_st();
       }
       do {
-        {  // the item's query rows, in the swizzled layout, once per copy
-          const int units = step_rows(p.step, w.b) * p.group * (D / 8);
-          const T* q = static_cast<const T*>(p.q) + (int64_t)w.b * p.step.T * p.q_stride + (int64_t)w.h * p.group * D;
-          constexpr int BATCH = 8;  // loads in flight
-          for (int c0 = at; c0 < units; c0 += BATCH * ATT_ROWS) {
-            uint4 x[BATCH];
+        if (at == 0) {  // the item's query rows, T x group of them, once per copy
+          mbar_arrive_expect_tx(&s->q_full, (uint32_t)(SPLIT * PANELS * p.R * 128));
 #pragma unroll
-            for (int u = 0; u < BATCH; u++) {
-              const int c = c0 + u * ATT_ROWS, r = c / (D / 8), t = r / p.group;
-              if (c < units)
-                x[u] = *reinterpret_cast<const uint4*>(q + t * p.q_stride + (r - t * p.group) * D + c % (D / 8) * 8);
-            }
+          for (int k = 0; k < SPLIT; k++)
 #pragma unroll
-            for (int u = 0; u < BATCH; u++) {
-              const int c = c0 + u * ATT_ROWS, r = c / (D / 8), e = c % (D / 8);
-              if (c < units) {
-#pragma unroll
-                for (int k = 0; k < SPLIT; k++)
-                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                   q_smem + (e / 8) * (ATT_ROWS * 128) + (k * LANES + r) * 128 + (((e & 7) ^ (r & 7)) << 4)),
-                               "r"(x[u].x), "r"(x[u].y), "r"(x[u].z), "r"(x[u].w)
-                               : "memory");
-              }
-            }
-          }
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s->q_full);
+            for (int e = 0; e < PANELS; e++)
+              tma_load_3d(q_smem + e * (ATT_ROWS * 128) + k * LANES * 128, &p.map_q, e * 64, w.h * p.group, w.b * p.step.T,
+                          &s->q_full);
         }
         float m_used = -INFINITY, l = 0.f;
         if (warp < active) {
@@ -589,29 +576,30 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
         float* part = p.partial + (int64_t)(blockIdx.x + w.b * p.cache.heads + w.h) * (D + 2) * p.Rp + row;
         // 32 columns of a lane are 128 bytes, their 16-byte units swizzled by the lane
         constexpr int CH = 32, MINE = CH / SPLIT, BUFFERS = q_bytes(D) >= 2 * ATT_ROWS * CH * 4 ? 2 : 1;
+        uint32_t x[CH];
+        if (warp < active) tmem_ld32(tmem + lanes + O_COL, x);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += CH) {
-          const uint32_t buf = q_smem + (c0 / CH % BUFFERS) * (ATT_ROWS * CH * 4);
+          const uint32_t buf = q_smem + c0 / CH % BUFFERS * (ATT_ROWS * CH * 4);
           if (warp < active) {
-            uint32_t o[CH];
-            tmem_ld32(tmem + lanes + O_COL + c0, o);
             tmem_wait_ld();
             if constexpr (SPLIT == 1) {
               if (live) {
 #pragma unroll
-                for (int c = 0; c < CH; c++) part[(c0 + c) * p.Rp] = __uint_as_float(o[c]);
+                for (int c = 0; c < CH; c++) part[(c0 + c) * p.Rp] = __uint_as_float(x[c]);
               }
             } else if (live) {
 #pragma unroll
               for (int c = 0; c < CH; c += 4)
                 asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(buf + at * 128 + (((c / 4) ^ (at & 7)) << 4)),
-                             "f"(__uint_as_float(o[c]) * f), "f"(__uint_as_float(o[c + 1]) * f),
-                             "f"(__uint_as_float(o[c + 2]) * f), "f"(__uint_as_float(o[c + 3]) * f)
+                             "f"(__uint_as_float(x[c]) * f), "f"(__uint_as_float(x[c + 1]) * f),
+                             "f"(__uint_as_float(x[c + 2]) * f), "f"(__uint_as_float(x[c + 3]) * f)
                              : "memory");
             }
+            if (c0 + CH < D) tmem_ld32(tmem + lanes + O_COL + c0 + CH, x);  // on its way during the exchange
           }
           if constexpr (SPLIT > 1) {
-            (void)softmax_bar(true);
+            softmax_sync();
             if (live) {
 #pragma unroll
               for (int c = 0; c < MINE; c += 4) {
@@ -632,9 +620,14 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
               }
             }
             // with two buffers the next chunk's barrier stands between these reads and the writes after it
-            if (BUFFERS == 1 || c0 + CH == D) (void)softmax_bar(true);
+            if (BUFFERS == 1 && c0 + CH < D) softmax_sync();
           }
         }
+        // the next item's query rows may land once all four warps are done
+        // with this memory and with O
+        fence_proxy_async_smem();
+        tc_fence_before();
+        softmax_sync();
         if (live && copy == 0) {
           part[D * p.Rp] = top;
           part[(D + 1) * p.Rp] = total;
@@ -654,11 +647,12 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
 }
 
 // Joins an item's partial results with the step's own rows, eight query rows
-// and 32 columns per block: o = (sum_s 2^(m_s - M) O_s + sum_j 2^(x_j - M) v_j)
+// and 32 to 128 columns per block: o = (sum_s 2^(m_s - M) O_s + sum_j 2^(x_j - M) v_j)
 // / (the same sum of weights).  The scores x_j of the keys that a row sees are
 // formed before the first launch is waited for.  A few hundred KB from L2.
-template <typename T, int D>
+template <typename T, int D, int JOIN_COLS>
 __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(const __grid_constant__ AttentionParams p) {
+  constexpr int JOIN_GROUPS = JOIN_THREADS / (2 * JOIN_COLS);  // threads that share a column's partial results
   __shared__ __align__(16) float weight[ATT_MAX_CTAS][8];  // of each partial result, per row
   __shared__ float own[QLIN_MAX_TREE][8];                  // of each of the step's rows
   __shared__ int64_t place[QLIN_MAX_TREE];
@@ -722,15 +716,14 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(co
     mask[k] = len >= 0 && r < p.R && tr < rows ? step_mask(p.step, b, tr) : 0;
   }
   const uint32_t any = mask[0] | mask[1] | mask[2] | mask[3];
-  constexpr int OWN = QLIN_MAX_TREE / JOIN_GROUPS;
-  float y[OWN];
+  auto own_value = [&](int j) -> float {
+    if (j >= rows || !(any >> j & 1) || place[j] < 0) return 0.f;
+    return to_float(static_cast<const T*>(p.cache.v)[place[j] + h * p.cache.head_stride + col]);
+  };
+  constexpr int EARLY = 2;  // of a thread's rows of the step, those whose value is read before the wait
+  float y[EARLY];
 #pragma unroll
-  for (int i = 0; i < OWN; i++) {
-    const int j = group + i * JOIN_GROUPS;
-    y[i] = 0.f;
-    if (j < rows && (any >> j & 1) && place[j] >= 0)
-      y[i] = to_float(static_cast<const T*>(p.cache.v)[place[j] + h * p.cache.head_stride + col]);
-  }
+  for (int i = 0; i < EARLY; i++) y[i] = own_value(group + i * JOIN_GROUPS);
   const uint32_t seen_mask = live ? step_mask(p.step, b, t) : 0;
   pdl_wait();
   pdl_launch_dependents();
@@ -788,38 +781,46 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(co
         }
       }
     }
+    auto add_own = [&](int j, float value) {  // only what a row sees: what it does not may be NaN
+      const float* f = &own[j][half * 4];
+      if (mask[0] >> j & 1) acc.x = fmaf(f[0], value, acc.x);
+      if (mask[1] >> j & 1) acc.y = fmaf(f[1], value, acc.y);
+      if (mask[2] >> j & 1) acc.z = fmaf(f[2], value, acc.z);
+      if (mask[3] >> j & 1) acc.w = fmaf(f[3], value, acc.w);
+    };
 #pragma unroll
-    for (int i = 0; i < OWN; i++) {  // only what a row sees: what it does not may be NaN
-      const int j = group + i * JOIN_GROUPS;
-      if (j < rows && (any >> j & 1) && place[j] >= 0) {
-        const float* f = &own[j][half * 4];
-        if (mask[0] >> j & 1) acc.x = fmaf(f[0], y[i], acc.x);
-        if (mask[1] >> j & 1) acc.y = fmaf(f[1], y[i], acc.y);
-        if (mask[2] >> j & 1) acc.z = fmaf(f[2], y[i], acc.z);
-        if (mask[3] >> j & 1) acc.w = fmaf(f[3], y[i], acc.w);
-      }
-    }
+    for (int i = 0; i < EARLY; i++)
+      if (group + i * JOIN_GROUPS < rows && place[group + i * JOIN_GROUPS] >= 0) add_own(group + i * JOIN_GROUPS, y[i]);
+#pragma unroll 4
+    for (int j = group + EARLY * JOIN_GROUPS; j < rows; j += JOIN_GROUPS)
+      if (place[j] >= 0) add_own(j, own_value(j));
     *reinterpret_cast<float4*>(&sums[group][c][half * 4]) = acc;
   }
   __syncthreads();
   if (live) {  // a row's columns: one run
-    float o = 0.f;
+    __nv_bfloat16* out = p.out + ((int64_t)b * p.step.T + t) * p.out_stride +
+                         ((int64_t)h * p.group + row % p.group) * D + blockIdx.z * JOIN_COLS;
 #pragma unroll
-    for (int g = 0; g < JOIN_GROUPS; g++) o += sums[g][lane][warp];
-    p.out[((int64_t)b * p.step.T + t) * p.out_stride + ((int64_t)h * p.group + row % p.group) * D +
-          blockIdx.z * JOIN_COLS + lane] = __float2bfloat16(o);
+    for (int e = lane; e < JOIN_COLS; e += 32) {
+      float o = 0.f;
+#pragma unroll
+      for (int g = 0; g < JOIN_GROUPS; g++) o += sums[g][e][warp];
+      out[e] = __float2bfloat16(o);
+    }
   }
 }
 
 struct Kernels {
-  const void *main[3], *join;  // main: 1, 2 and 4 copies of the query rows
+  const void *main[3], *join[3];  // main: 1, 2 and 4 copies of the query rows; join: 32, 64 and (from width 128) 128 columns
 };
 template <typename T, int D>
 Kernels kernels_of() {
   return {{reinterpret_cast<const void*>(qlin_attention_kernel<T, D, 1>),
            reinterpret_cast<const void*>(qlin_attention_kernel<T, D, 2>),
            reinterpret_cast<const void*>(qlin_attention_kernel<T, D, 4>)},
-          reinterpret_cast<const void*>(qlin_attention_join_kernel<T, D>)};
+          {reinterpret_cast<const void*>(qlin_attention_join_kernel<T, D, 32>),
+           reinterpret_cast<const void*>(qlin_attention_join_kernel<T, D, 64>),
+           reinterpret_cast<const void*>(qlin_attention_join_kernel<T, D, (D < 128 ? 64 : 128)>)}};
 }
 Kernels attention_kernels(int dtype, int width) {
   if (dtype == QLIN_BF16)
@@ -866,8 +867,10 @@ qlin_status attention_setup(int* ctas) {
     for (int dtype : {QLIN_BF16, QLIN_F16})
       for (int width : {64, 128, 256})
         for (const void* fn : attention_kernels(dtype, width).main)
-          if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attention_smem(width));
+          for (auto set : {std::make_pair(cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attention_smem(width)),
+                           // all of it as shared memory, so that the second launch's blocks fit beside
+                           std::make_pair(cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared)})
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, set.first, set.second);
     d.ctas = sms < ATT_MAX_CTAS ? sms : ATT_MAX_CTAS;
     d.ready = e == cudaSuccess && g_encode && sms > 0 ? QLIN_OK : QLIN_ERR_CUDA;
     if (e != cudaSuccess) (void)cudaGetLastError();
@@ -887,6 +890,18 @@ bool encode(CUtensorMap* map, const qlin_kv_cache* c, void* base, int box) {
   return g_encode(map, c->dtype == QLIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                   base, dims, strides, shape, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The query rows [B * T, Hq, width] as boxes of 64 elements x group x T: an
+// item's rows in order, row t * group + i
+bool encode_q(CUtensorMap* map, const qlin_kv_cache* c, const qlin_kv_step* s, const void* q, int64_t stride, int Hq) {
+  const cuuint64_t dims[3] = {(cuuint64_t)c->width, (cuuint64_t)Hq, (cuuint64_t)((int64_t)s->B * s->T)};
+  const cuuint64_t strides[2] = {(cuuint64_t)c->width * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t shape[3] = {64, (cuuint32_t)(Hq / c->heads), (cuuint32_t)s->T}, one[3] = {1, 1, 1};
+  return g_encode(map, c->dtype == QLIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                  const_cast<void*>(q), dims, strides, shape, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 qlin_status check_heads(const qlin_kv_cache* c, int64_t B, int64_t T, int Hq) {
@@ -939,7 +954,9 @@ qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* 
   AttentionParams p;
   const int tile = tile_tokens(cache->width);
   p.box = cache->page_size < tile ? cache->page_size : tile;
-  if (!encode(&p.map_k, cache, cache->k, p.box) || !encode(&p.map_v, cache, cache->v, p.box)) return QLIN_ERR_CUDA;
+  if (!encode(&p.map_k, cache, cache->k, p.box) || !encode(&p.map_v, cache, cache->v, p.box) ||
+      !encode_q(&p.map_q, cache, step, q, q_stride, Hq))
+    return QLIN_ERR_CUDA;
   p.page_shift = 0;
   while ((1 << p.page_shift) < cache->page_size) p.page_shift++;
   p.cache = *cache;
@@ -961,7 +978,11 @@ qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* 
   st = launch_step(fn.main[copies], dim3((unsigned)ctas, 1, 1), dim3(ATT_THREADS, 1, 1), attention_smem(cache->width),
                    static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0);
   if (st != QLIN_OK) return st;
-  return launch_step(fn.join, dim3((unsigned)(step->B * cache->heads), (unsigned)(p.Rp / 8), (unsigned)(D / JOIN_COLS)),
+  // blocks of many columns repeat less work; of few, spread a few items over the SMs
+  const int64_t blocks = (int64_t)step->B * cache->heads * (p.Rp / 8);
+  int wide = D < 128 ? 1 : 2;
+  while (wide > 0 && blocks * (D / (32 << wide)) < ctas) wide--;
+  return launch_step(fn.join[wide], dim3((unsigned)(step->B * cache->heads), (unsigned)(p.Rp / 8), (unsigned)(D / (32 << wide))),
                      dim3(JOIN_THREADS, 1, 1), 0, static_cast<cudaStream_t>(stream), args, true);
 }
 
