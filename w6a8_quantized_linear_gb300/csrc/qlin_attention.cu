@@ -573,9 +573,10 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
           if (mk != -INFINITY) total += s->l[k * LANES + row] * exp2_approx(mk - top);
         }
         const float f = m_used == -INFINITY ? 0.f : exp2_approx(m_used - top);
-        float* part = p.partial + (int64_t)(blockIdx.x + w.b * p.cache.heads + w.h) * (D + 2) * p.Rp + row;
+        float* item = p.partial + (int64_t)(blockIdx.x + w.b * p.cache.heads + w.h) * (D + 2) * p.Rp;
+        float* part = item + row;
         // 32 columns of a lane are 128 bytes, their 16-byte units swizzled by the lane
-        constexpr int CH = 32, MINE = CH / SPLIT, BUFFERS = q_bytes(D) >= 2 * ATT_ROWS * CH * 4 ? 2 : 1;
+        constexpr int CH = 32, BUFFERS = q_bytes(D) >= 2 * ATT_ROWS * CH * 4 ? 2 : 1;
         uint32_t x[CH];
         if (warp < active) tmem_ld32(tmem + lanes + O_COL, x);
 #pragma unroll 1
@@ -600,24 +601,22 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
           }
           if constexpr (SPLIT > 1) {
             softmax_sync();
-            if (live) {
+            // two columns of every eighth row per thread
+            const int r8 = at & 7, c = at >> 3 << 1;
+            for (int r = r8; r < p.R; r += 8) {
+              float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int c = 0; c < MINE; c += 4) {
-                float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < SPLIT; k++) {
-                  float y[4];
-                  const int from = k * LANES + row;
-                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                               : "=f"(y[0]), "=f"(y[1]), "=f"(y[2]), "=f"(y[3])
-                               : "r"(buf + from * 128 + ((((copy * MINE + c) / 4) ^ (from & 7)) << 4))
-                               : "memory");
-#pragma unroll
-                  for (int e = 0; e < 4; e++) v[e] += y[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 4; e++) part[(c0 + copy * MINE + c + e) * p.Rp] = v[e];
+              for (int k = 0; k < SPLIT; k++) {
+                float2 y;
+                const int from = k * LANES + r;  // from & 7 = r8
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                             : "=f"(y.x), "=f"(y.y)
+                             : "r"(buf + from * 128 + (((c >> 2) ^ r8) << 4) + ((c & 2) << 2))
+                             : "memory");
+                v.x += y.x, v.y += y.y;
               }
+              item[(c0 + c) * p.Rp + r] = v.x;
+              item[(c0 + c + 1) * p.Rp + r] = v.y;
             }
             // with two buffers the next chunk's barrier stands between these reads and the writes after it
             if (BUFFERS == 1 && c0 + CH < D) softmax_sync();
@@ -978,10 +977,11 @@ qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* 
   st = launch_step(fn.main[copies], dim3((unsigned)ctas, 1, 1), dim3(ATT_THREADS, 1, 1), attention_smem(cache->width),
                    static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0);
   if (st != QLIN_OK) return st;
-  // blocks of many columns repeat less work; of few, spread a few items over the SMs
+  // the narrowest blocks that all find room while the first launch runs, one
+  // per SM: more of them would start behind it
   const int64_t blocks = (int64_t)step->B * cache->heads * (p.Rp / 8);
-  int wide = D < 128 ? 1 : 2;
-  while (wide > 0 && blocks * (D / (32 << wide)) < ctas) wide--;
+  int wide = 0;
+  while (wide < (D < 128 ? 1 : 2) && blocks * (D / (32 << wide)) > ctas) wide++;
   return launch_step(fn.join[wide], dim3((unsigned)(step->B * cache->heads), (unsigned)(p.Rp / 8), (unsigned)(D / (32 << wide))),
                      dim3(JOIN_THREADS, 1, 1), 0, static_cast<cudaStream_t>(stream), args, true);
 }

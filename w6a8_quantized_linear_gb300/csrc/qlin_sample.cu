@@ -17,10 +17,12 @@
 namespace qlin {
 namespace {
 
-constexpr int SAMPLE_THREADS = 1024;
+constexpr int SAMPLE_THREADS = 512;
 constexpr int SAMPLE_WARPS = SAMPLE_THREADS / 32;
-constexpr int BINS = 1024;               // one per thread in the scans
+constexpr int BINS = SAMPLE_THREADS;     // one per thread in the scans
 constexpr int MAX_C = 16;                // CTAs of a row's cluster, at most
+constexpr int FEW = 128;                 // a bin of at most this many tokens is settled by comparing all pairs
+constexpr int LIST = 1024;               // so many survivors of top-k are carried on by one CTA
 constexpr int ONE_BITS = 42;             // weights are multiples of 2^-42; 2^19 of them sum below 2^62
 constexpr uint32_t ALL = 0xFFFFFFFFu;
 
@@ -51,18 +53,25 @@ struct Round {  // what the CTAs of a row tell each other outside the histograms
   uint32_t nan, first;
   unsigned long long sum;
 };
+struct __align__(16) Candidate {
+  uint32_t key, index;  // in the row
+  unsigned long long weight;
+};
 
 struct SampleShared {
   uint32_t lo[BINS], hi[BINS], count[BINS], kmin[BINS], kmax[BINS];  // this CTA's histogram
   Bin bins[BINS];
+  Candidate few[FEW];
+  float list_x[LIST];          // survivors of top-k, in order of their index
+  uint32_t list_index[LIST];
   Round peer[3][MAX_C];
   unsigned long long warp_sum[SAMPLE_WARPS];
-  uint32_t warp_a[SAMPLE_WARPS];
+  uint32_t warp_a[SAMPLE_WARPS], warp_b[SAMPLE_WARPS];
   float warp_f[SAMPLE_WARPS], warp_g[SAMPLE_WARPS];
   uint32_t table[32];  // 2^(i/32) in [2^31, 2^32)
   int pick;
+  uint32_t pick_key, pick_index, filled;
   unsigned long long before;
-  uint32_t tie;
 };
 
 __device__ __forceinline__ uint32_t key_of(float x) {  // larger logit, larger key (no -0 among the logits)
@@ -97,19 +106,31 @@ __device__ __forceinline__ unsigned long long weight_of(float x, float mx, float
 }
 
 // Which part of the order survives: keys above `key`, and equal ones up to
-// `index` of this CTA's slice.
+// `index` in the row (a bound that only this CTA's tokens have to agree with).
 struct Kept {
   uint32_t key;
-  int index;
-  __device__ __forceinline__ bool has(uint32_t k, int i) const { return k > key || (k == key && i <= index); }
+  int64_t index;
+  __device__ __forceinline__ bool has(uint32_t k, int64_t i) const { return k > key || (k == key && i <= index); }
 };
 
+// The tokens that a CTA works on: a slice of the row in shared memory, or (one
+// CTA) the survivors of top-k.
+template <typename T>
 struct Row {
-  const float* x;  // this CTA's slice
-  int n, w0, w1;   // its tokens, this warp's part of them
+  const T* x;
+  int n, w0, w1;     // tokens, this warp's contiguous part of them
+  int64_t first;     // index of the slice's first token
   float mx, ch, cl, to_bin;
   uint32_t rank, C;
   SampleShared* s;
+  __device__ __forceinline__ float at(int i) const { return to_float(x[i]) + 0.f; }  // -0 becomes 0
+  __device__ __forceinline__ unsigned long long weight(float v) const { return weight_of(v, mx, ch, cl, s->table); }
+  __device__ __forceinline__ void part(int tokens) {
+    const int per = (tokens + 32 * SAMPLE_WARPS - 1) / (32 * SAMPLE_WARPS) * 32, warp = threadIdx.x >> 5;
+    n = tokens;
+    w0 = min(n, warp * per);
+    w1 = min(n, w0 + per);
+  }
 };
 
 template <typename T>
@@ -119,7 +140,8 @@ __device__ __forceinline__ T warp_sum(T v) {
   return v;
 }
 
-__device__ __forceinline__ void row_sync(const Row& r) {
+template <typename T>
+__device__ __forceinline__ void row_sync(const Row<T>& r) {
   if (r.C == 1) {
     __syncthreads();
   } else {
@@ -128,13 +150,9 @@ __device__ __forceinline__ void row_sync(const Row& r) {
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void to_peer(const void* local, uint32_t rank, T v);
-template <>
 __device__ __forceinline__ void to_peer(const void* local, uint32_t rank, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_addr(local, rank)), "r"(v) : "memory");
 }
-template <>
 __device__ __forceinline__ void to_peer(const void* local, uint32_t rank, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dsmem_addr(local, rank)), "l"(v) : "memory");
 }
@@ -144,10 +162,12 @@ __device__ __forceinline__ uint32_t from_peer(const uint32_t* local, uint32_t ra
   return v;
 }
 
-__device__ __forceinline__ int bin0(const Row& r, float x) {  // of the row's range of logits
+template <typename T>
+__device__ __forceinline__ int bin0(const Row<T>& r, float x) {  // of the row's range of logits
   return min(BINS - 1, (int)((r.mx - x) * r.to_bin));
 }
-__device__ __forceinline__ int bin1(const Row& r, float x, int b0) {  // of the range of one such bin
+template <typename T>
+__device__ __forceinline__ int bin1(const Row<T>& r, float x, int b0) {  // of the range of one such bin
   return max(0, min(BINS - 1, (int)(((r.mx - x) * r.to_bin - (float)b0) * (float)BINS)));
 }
 
@@ -165,24 +185,20 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
   __syncthreads();  // the previous scan's sums have been read
   if (lane == 31) s->warp_sum[warp] = inc;
   __syncthreads();
-  unsigned long long w = s->warp_sum[lane], winc = w;  // 32 warps, one per lane
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long a = __shfl_up_sync(ALL, winc, o);
-    if (lane >= o) winc += a;
-  }
-  *total = __shfl_sync(ALL, winc, 31);
-  return __shfl_sync(ALL, winc - w, warp) + inc - v;
+  const unsigned long long w = lane < SAMPLE_WARPS ? s->warp_sum[lane] : 0;
+  *total = warp_sum(w);
+  return warp_sum(lane < warp ? w : 0ull) + inc - v;
 }
 
-// The slice's index of the quota-th token (from 1) with this key among those up
-// to `bound`; -1 for none.  All threads of the CTA.
-__device__ __forceinline__ int index_of(const Row& r, uint32_t key, int bound, uint32_t quota) {
+// The row index of the quota-th token (from 1) with this key among the
+// survivors of this CTA; -1 for none.  All threads of the CTA.
+template <typename T>
+__device__ __forceinline__ int64_t index_of(const Row<T>& r, uint32_t key, int64_t bound, uint32_t quota) {
   if (quota == 0) return -1;
   SampleShared* s = r.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t n = 0;
-  for (int i = r.w0 + lane; i < r.w1; i += 32) n += key_of(r.x[i]) == key && i <= bound;
+  for (int i = r.w0 + lane; i < r.w1; i += 32) n += key_of(r.at(i)) == key && r.first + i <= bound;
   n = warp_sum(n);
   if (lane == 0) s->warp_a[warp] = n;
   __syncthreads();
@@ -192,50 +208,50 @@ __device__ __forceinline__ int index_of(const Row& r, uint32_t key, int bound, u
     uint32_t left = quota - before;
     for (int i0 = r.w0; i0 < r.w1; i0 += 32) {
       const int i = i0 + lane;
-      const uint32_t hit = __ballot_sync(ALL, i < r.w1 && key_of(r.x[i]) == key && i <= bound);
+      const uint32_t hit = __ballot_sync(ALL, i < r.w1 && key_of(r.at(i)) == key && r.first + i <= bound);
       if ((uint32_t)__popc(hit) >= left) {
-        if (lane == 0) s->tie = i0 + __fns(hit, 0, left);
+        if (lane == 0) s->pick_index = (uint32_t)(r.first + i0 + __fns(hit, 0, left));
         break;
       }
       left -= __popc(hit);
     }
   }
   __syncthreads();
-  return (int)s->tie;
+  return s->pick_index;
 }
 
-// The shortest beginning of the survivors' order whose count (by_mass false)
+// The shortest beginning of the survivors' order whose count (BY_MASS false)
 // reaches `want`, or whose mass reaches the share top_p of theirs; `kept` is
-// narrowed to it.  All CTAs of the row take part and agree on everything but
-// kept.index, which is of each CTA's own slice.
-__device__ __forceinline__ void narrow(const Row& r, Kept& kept, bool by_mass, unsigned long long want, float top_p) {
+// narrowed to it.  All CTAs of the row take part.  Usually three exchanges
+// between them: the histograms, their sums, the few tokens of the bin in which
+// the border lies.
+template <bool BY_MASS, typename T>
+__device__ __noinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long long want, float top_p) {
   SampleShared* s = r.s;
   const int lane = threadIdx.x & 31;
   int b0 = 0, level = 0, sh = 0;
   uint32_t kmax = 0, kmin = 0;
+  // the bin of a surviving token at this level, -1 outside the range that is split
+  auto bin_of = [&](float x, uint32_t key) -> int {
+    if (level == 0) return bin0(r, x);
+    if (level == 1) return bin0(r, x) != b0 ? -1 : bin1(r, x, b0);
+    return key < kmin || key > kmax ? -1 : (int)((kmax - key) >> sh);
+  };
   while (true) {
-    for (int i = threadIdx.x; i < BINS; i += SAMPLE_THREADS) {
-      s->lo[i] = s->hi[i] = s->count[i] = s->kmax[i] = 0;
-      s->kmin[i] = ALL;
-    }
+    const int mine = threadIdx.x;
+    s->lo[mine] = s->hi[mine] = s->count[mine] = s->kmax[mine] = 0;
+    s->kmin[mine] = ALL;
+    if (threadIdx.x == 0) s->filled = 0;
     __syncthreads();
     for (int i = r.w0 + lane; i < r.w1; i += 32) {
-      const float x = r.x[i];
+      const float x = r.at(i);
       const uint32_t key = key_of(x);
-      if (x == -INFINITY || !kept.has(key, i)) continue;
-      int b;
-      if (level == 0) {
-        b = bin0(r, x);
-      } else if (level == 1) {
-        if (bin0(r, x) != b0) continue;
-        b = bin1(r, x, b0);
-      } else {
-        if (key < kmin || key > kmax) continue;
-        b = (int)((kmax - key) >> sh);
-      }
+      if (x == -INFINITY || !kept.has(key, r.first + i)) continue;
+      const int b = bin_of(x, key);
+      if (b < 0) continue;
       atomicAdd(&s->count[b], 1u);
-      if (by_mass) {
-        const unsigned long long w = weight_of(x, r.mx, r.ch, r.cl, s->table);
+      if (BY_MASS) {
+        const unsigned long long w = r.weight(x);
         const uint32_t wl = (uint32_t)w;
         const uint32_t wh = (uint32_t)(w >> 32) + ((uint32_t)(atomicAdd(&s->lo[b], wl) + wl) < wl ? 1u : 0u);  // the carry
         if (wh) atomicAdd(&s->hi[b], wh);
@@ -246,60 +262,108 @@ __device__ __forceinline__ void narrow(const Row& r, Kept& kept, bool by_mass, u
       }
     }
     row_sync(r);  // every CTA's histogram is complete
-    // each CTA joins its share of the bins and gives them to all
-    const int share = BINS / r.C;
-    for (int i = threadIdx.x; i < share; i += SAMPLE_THREADS) {
-      const int b = r.rank * share + i;
+    // each CTA joins its share of the bins, C lanes to a bin (one per CTA),
+    // and lane c gives the sum to CTA c
+    if (r.C == 1) {
+      s->bins[mine] = {((unsigned long long)s->hi[mine] << 32) + s->lo[mine], s->count[mine], s->kmin[mine], s->kmax[mine], 0};
+    } else {
+      const uint32_t c = threadIdx.x % r.C;
+      const int b = r.rank * (BINS / r.C) + threadIdx.x / r.C;
+      uint32_t count = from_peer(&s->count[b], c), lo = ALL, hi = 0;
       unsigned long long mass = 0;
-      uint32_t count = 0, lo = ALL, hi = 0;
-      for (uint32_t c = 0; c < r.C; c++) {
-        mass += from_peer(&s->lo[b], c) + ((unsigned long long)from_peer(&s->hi[b], c) << 32);
-        count += from_peer(&s->count[b], c);
-        lo = min(lo, from_peer(&s->kmin[b], c));
-        hi = max(hi, from_peer(&s->kmax[b], c));
+      if (BY_MASS) mass = from_peer(&s->lo[b], c) + ((unsigned long long)from_peer(&s->hi[b], c) << 32);
+      if (level) lo = from_peer(&s->kmin[b], c), hi = from_peer(&s->kmax[b], c);
+      for (uint32_t o = 1; o < r.C; o <<= 1) {
+        count += __shfl_xor_sync(ALL, count, o);
+        if (BY_MASS) mass += __shfl_xor_sync(ALL, mass, o);
+        if (level) {
+          lo = min(lo, __shfl_xor_sync(ALL, lo, o));
+          hi = max(hi, __shfl_xor_sync(ALL, hi, o));
+        }
       }
-      for (uint32_t c = 0; c < r.C; c++) {
-        to_peer(&s->bins[b].mass, c, mass);
-        to_peer(&s->bins[b].count, c, count);
+      to_peer(&s->bins[b].count, c, count);
+      if (BY_MASS) to_peer(&s->bins[b].mass, c, mass);
+      if (level) {
         to_peer(&s->bins[b].kmin, c, lo);
         to_peer(&s->bins[b].kmax, c, hi);
       }
     }
     row_sync(r);
-    const Bin mine = s->bins[threadIdx.x];
     unsigned long long total;
-    const unsigned long long v = by_mass ? mine.mass : mine.count;
+    const unsigned long long v = BY_MASS ? s->bins[mine].mass : s->bins[mine].count;
     const unsigned long long before = block_scan(v, &total, s);
-    if (level == 0 && by_mass) {
+    if (level == 0 && BY_MASS) {
       const double t = ceil((double)top_p * (double)total);
       want = t < 1. ? 1 : (unsigned long long)t;
       if (want > total) want = total;
     }
     if (total < want || total == 0) return;  // all survivors (the same in every CTA)
     if (before < want && want <= before + v) {
-      s->pick = threadIdx.x;
+      s->pick = mine;
       s->before = before;
     }
     __syncthreads();
     const int b = s->pick;
     want -= s->before;
     const Bin hit = s->bins[b];
+    if (hit.count <= FEW) {
+      // its tokens into every CTA's list, this CTA's behind those of the CTAs before it
+      uint32_t ahead = 0;
+      if (r.C > 1) {
+        const uint32_t n = lane < (int)r.C ? from_peer(&s->count[b], lane) : 0;
+        ahead = warp_sum(lane < (int)r.rank ? n : 0u);
+      }
+      if (s->count[b])
+        for (int i = r.w0 + lane; i < r.w1; i += 32) {
+          const float x = r.at(i);
+          const uint32_t key = key_of(x);
+          if (x == -INFINITY || !kept.has(key, r.first + i) || bin_of(x, key) != b) continue;
+          const unsigned long long w = BY_MASS ? r.weight(x) : 1;
+          const Candidate* at = &s->few[ahead + atomicAdd(&s->filled, 1u)];
+          for (uint32_t c = 0; c < r.C; c++)
+            asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dsmem_addr(at, c)), "r"(key),
+                         "r"((uint32_t)(r.first + i)), "r"((uint32_t)w), "r"((uint32_t)(w >> 32))
+                         : "memory");
+        }
+      row_sync(r);
+      // each token's sum of those before it; one of them is the last that is kept
+      if (threadIdx.x < hit.count) {
+        const Candidate me = s->few[threadIdx.x];
+        unsigned long long sum = 0;
+        for (uint32_t k = 0; k < hit.count; k++) {
+          const Candidate o = s->few[k];
+          if (o.key > me.key || (o.key == me.key && o.index < me.index)) sum += o.weight;
+        }
+        if (sum < want && want <= sum + me.weight) {
+          s->pick_key = me.key;
+          s->pick_index = me.index;
+        }
+      }
+      __syncthreads();
+      kept.key = s->pick_key;
+      kept.index = s->pick_index;
+      __syncthreads();
+      return;
+    }
     if (level == 0) {
       b0 = b;
     } else {
       kmin = hit.kmin;
       kmax = hit.kmax;
       if (kmin == kmax) {  // one key: its first `want` by index
-        if (by_mass) {
+        if (BY_MASS) {
           const unsigned long long w = hit.mass / hit.count;  // they weigh the same
           want = w ? (want + w - 1) / w : hit.count;
         }
-        const int bound = kmax == kept.key ? kept.index : 0x7FFFFFFF;
+        const int64_t bound = kmax == kept.key ? kept.index : 0x7FFFFFFF;
         kept.key = kmax;
         kept.index = bound;
         if (want < hit.count) {  // the same in every CTA
-          unsigned long long ahead = 0;
-          for (uint32_t c = 0; c < r.rank; c++) ahead += from_peer(&s->count[b], c);
+          uint32_t ahead = 0;
+          if (r.C > 1) {
+            const uint32_t n = lane < (int)r.C ? from_peer(&s->count[b], lane) : 0;
+            ahead = warp_sum(lane < (int)r.rank ? n : 0u);
+          }
           const uint32_t own = s->count[b];
           const uint32_t quota = want <= ahead ? 0 : want - ahead >= own ? own : (uint32_t)(want - ahead);
           if (quota < own) kept.index = index_of(r, kmax, bound, quota);
@@ -315,99 +379,149 @@ __device__ __forceinline__ void narrow(const Row& r, Kept& kept, bool by_mass, u
   }
 }
 
-__device__ __forceinline__ float load_logit(const float* p) { return __ldcs(p) + 0.f; }  // -0 becomes 0
-__device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p) + 0.f; }
-
+// The first kept token, in order of the index, at which the running sum of
+// the kept weights exceeds u times their sum.  `index`: the tokens' places in
+// the row where they are not first + i.
 template <typename T>
-__global__ void __launch_bounds__(SAMPLE_THREADS) qlin_sample_kernel(const __grid_constant__ SampleParams p, int C) {
+__device__ __forceinline__ void choose(const Row<T>& r, const Kept& kept, float min_p, float u, const uint32_t* index,
+                                       int32_t* token, float* prob) {
+  SampleShared* s = r.s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned long long least = 1;
+  if (min_p > 0.f) least = max(1ull, (unsigned long long)ceil((double)fminf(min_p, 1.f) * (double)(1ull << ONE_BITS)));
+  auto weight = [&](int i) -> unsigned long long {
+    const float v = r.at(i);
+    if (!kept.has(key_of(v), r.first + i)) return 0;
+    const unsigned long long w = r.weight(v);
+    return w < least ? 0 : w;
+  };
+  // the kept mass of each warp's tokens, of the CTAs, of the row
+  unsigned long long mine = 0;
+  for (int i = r.w0 + lane; i < r.w1; i += 32) mine += weight(i);
+  mine = warp_sum(mine);
+  __syncthreads();  // warp_sum has been read
+  if (lane == 0) s->warp_sum[warp] = mine;
+  __syncthreads();
+  const unsigned long long theirs = lane < SAMPLE_WARPS ? s->warp_sum[lane] : 0;
+  unsigned long long before = warp_sum(lane < warp ? theirs : 0ull);
+  unsigned long long total = warp_sum(theirs);
+  if (r.C > 1) {
+    if (threadIdx.x < r.C) to_peer(&s->peer[2][r.rank].sum, threadIdx.x, total);
+    row_sync(r);
+    const unsigned long long v = lane < (int)r.C ? s->peer[2][lane].sum : 0;
+    before += warp_sum(lane < (int)r.rank ? v : 0ull);
+    total = warp_sum(v);
+  }
+  unsigned long long target = u > 0.f ? (unsigned long long)((double)fminf(u, 1.f) * (double)total) + 1 : 1;
+  if (target > total) target = total;
+  if (!(before < target && target <= before + mine)) return;
+  for (int i0 = r.w0; i0 < r.w1; i0 += 32) {
+    const int i = i0 + lane;
+    const unsigned long long w = i < r.w1 ? weight(i) : 0;
+    unsigned long long inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long a = __shfl_up_sync(ALL, inc, o);
+      if (lane >= o) inc += a;
+    }
+    if (before + inc >= target && before + inc - w < target) {
+      *token = index ? (int32_t)index[i] : (int32_t)(r.first + i);
+      if (prob) *prob = (float)((double)w / (double)total);
+    }
+    before += __shfl_sync(ALL, inc, 31);
+    if (before >= target) return;
+  }
+}
+
+// One row per cluster of C CTAs, its logits read once, into shared memory.
+// Bound by latency: reading (one trip), then the exchanges between the CTAs
+// (two per level of a search) and passes over 16 to 32 tokens per thread.
+template <typename T>
+__global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __grid_constant__ SampleParams p, int C) {
   extern __shared__ __align__(16) uint8_t raw[];
   SampleShared* s = reinterpret_cast<SampleShared*>(raw);
-  float* x = reinterpret_cast<float*>(raw + sizeof(SampleShared));
+  T* x = reinterpret_cast<T*>(raw + sizeof(SampleShared));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Row r;
+  Row<T> r;
   r.x = x;
   r.s = s;
   r.C = C;
   r.rank = C == 1 ? 0 : cluster_ctarank();
+  r.first = (int64_t)r.rank * p.slice;
   const int row = blockIdx.x / C;
-  const int64_t first = (int64_t)r.rank * p.slice;
-  r.n = (int)max((int64_t)0, min((int64_t)p.slice, p.V - first));
-  const int part = (r.n + 32 * SAMPLE_WARPS - 1) / (32 * SAMPLE_WARPS) * 32;  // contiguous tokens of one warp
-  r.w0 = min(r.n, warp * part);
-  r.w1 = min(r.n, r.w0 + part);
+  r.part((int)max((int64_t)0, min((int64_t)p.slice, p.V - r.first)));
   if (C > 1) cluster_arrive_relaxed();
   if (threadIdx.x < 32) s->table[threadIdx.x] = TABLE[threadIdx.x];
   pdl_wait();
   pdl_launch_dependents();
-  const T* src = static_cast<const T*>(p.logits) + row * p.ld + first;
+  const float temperature = p.temperature ? p.temperature[row] : 1.f;
+  const int top_k = p.top_k ? p.top_k[row] : 0;
+  const float top_p = p.top_p ? p.top_p[row] : 1.f;
+  const float min_p = p.min_p ? p.min_p[row] : 0.f;
+  const float u = p.u[row];
+  const T* src = static_cast<const T*>(p.logits) + row * p.ld + r.first;
   float mx = -INFINITY, mn = INFINITY;
-  uint32_t nan = 0;
-  for (int i = r.w0 + lane; i < r.w1; i += 32) {
-    const float v = load_logit(src + i);
-    x[i] = v;
-    nan |= v != v;
-    mx = fmaxf(mx, v);
-    if (v > -INFINITY) mn = fminf(mn, v);
-  }
+  uint32_t nan = 0, top = 0;  // top: the lowest index of the largest
+  constexpr int BATCH = 16;   // loads in flight per thread
+  for (int i0 = r.w0 + lane; i0 < r.w1; i0 += 32 * BATCH) {
+    T v[BATCH];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    mx = fmaxf(mx, __shfl_xor_sync(ALL, mx, o));
-    mn = fminf(mn, __shfl_xor_sync(ALL, mn, o));
-    nan |= __shfl_xor_sync(ALL, nan, o);
+    for (int k = 0; k < BATCH; k++)
+      if (i0 + 32 * k < r.w1) v[k] = src[i0 + 32 * k];
+#pragma unroll
+    for (int k = 0; k < BATCH; k++) {
+      const int i = i0 + 32 * k;
+      if (i >= r.w1) break;
+      x[i] = v[k];
+      const float f = to_float(v[k]) + 0.f;
+      nan |= f != f;
+      if (f > mx) mx = f, top = (uint32_t)(r.first + i);
+      if (f > -INFINITY) mn = fminf(mn, f);
+    }
   }
-  if (lane == 0) s->warp_f[warp] = mx, s->warp_g[warp] = mn, s->warp_a[warp] = nan;
+  // of the warp, the CTA, the row
+  auto join = [&](float omx, float omn, uint32_t onan, uint32_t otop) {
+    if (omx > mx || (omx == mx && otop < top)) mx = omx, top = otop;
+    mn = fminf(mn, omn);
+    nan |= onan;
+  };
+  auto join_lanes = [&]() {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      join(__shfl_xor_sync(ALL, mx, o), __shfl_xor_sync(ALL, mn, o), __shfl_xor_sync(ALL, nan, o),
+           __shfl_xor_sync(ALL, top, o));
+  };
+  join_lanes();
+  if (lane == 0) s->warp_f[warp] = mx, s->warp_g[warp] = mn, s->warp_a[warp] = nan, s->warp_b[warp] = top;
   __syncthreads();
-  mx = s->warp_f[lane], mn = s->warp_g[lane], nan = s->warp_a[lane];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    mx = fmaxf(mx, __shfl_xor_sync(ALL, mx, o));
-    mn = fminf(mn, __shfl_xor_sync(ALL, mn, o));
-    nan |= __shfl_xor_sync(ALL, nan, o);
-  }
+  if (lane < SAMPLE_WARPS) mx = s->warp_f[lane], mn = s->warp_g[lane], nan = s->warp_a[lane], top = s->warp_b[lane];
+  join_lanes();
   if (C > 1) {
     cluster_wait();  // every CTA of the row has started
     if (threadIdx.x < C) {
-      to_peer(&s->peer[0][r.rank].mx, threadIdx.x, __float_as_uint(mx));
-      to_peer(&s->peer[0][r.rank].mn, threadIdx.x, __float_as_uint(mn));
-      to_peer(&s->peer[0][r.rank].nan, threadIdx.x, nan);
+      const Round* at = &s->peer[0][r.rank];
+      to_peer(&at->mx, threadIdx.x, __float_as_uint(mx));
+      to_peer(&at->mn, threadIdx.x, __float_as_uint(mn));
+      to_peer(&at->nan, threadIdx.x, nan);
+      to_peer(&at->first, threadIdx.x, top);
     }
     row_sync(r);
-    for (int c = 0; c < C; c++) {
-      mx = fmaxf(mx, s->peer[0][c].mx);
-      mn = fminf(mn, s->peer[0][c].mn);
-      nan |= s->peer[0][c].nan;
+    if (lane < C) {
+      const Round o = s->peer[0][lane];
+      mx = o.mx, mn = o.mn, nan = o.nan, top = o.first;
     }
+    join_lanes();
   }
-  if (nan || mx == -INFINITY) {  // no token
+  if (nan || mx == -INFINITY || !(temperature > 0.f)) {  // no token, or the largest
+    const bool none = nan || mx == -INFINITY;
     if (r.rank == 0 && threadIdx.x == 0) {
-      p.token[row] = -1;
-      if (p.prob) p.prob[row] = 0.f;
-    }
-    return;
-  }
-  const float temperature = p.temperature ? p.temperature[row] : 1.f;
-  if (!(temperature > 0.f)) {
-    uint32_t at = ALL;
-    for (int i = r.w0 + lane; i < r.w1; i += 32)
-      if (x[i] == mx) at = min(at, (uint32_t)(first + i));
-    at = __reduce_min_sync(ALL, at);
-    __syncthreads();  // warp_a has been read
-    if (lane == 0) s->warp_a[warp] = at;
-    __syncthreads();
-    at = __reduce_min_sync(ALL, s->warp_a[lane]);
-    if (C > 1) {
-      if (threadIdx.x < C) to_peer(&s->peer[1][r.rank].first, threadIdx.x, at);
-      row_sync(r);
-      for (int c = 0; c < C; c++) at = min(at, s->peer[1][c].first);
-    }
-    if (r.rank == 0 && threadIdx.x == 0) {
-      p.token[row] = (int32_t)at;
-      if (p.prob) p.prob[row] = 1.f;
+      p.token[row] = none ? -1 : (int32_t)top;
+      if (p.prob) p.prob[row] = none ? 0.f : 1.f;
     }
     return;
   }
   if (mx == INFINITY) {  // the infinite ones are left, alike
-    for (int i = r.w0 + lane; i < r.w1; i += 32) x[i] = x[i] == INFINITY ? 0.f : -INFINITY;
+    for (int i = r.w0 + lane; i < r.w1; i += 32) x[i] = to_float(x[i]) == INFINITY ? T(0.f) : T(-INFINITY);
     __syncwarp();
     mx = mn = 0.f;
   }
@@ -418,69 +532,71 @@ __global__ void __launch_bounds__(SAMPLE_THREADS) qlin_sample_kernel(const __gri
   r.to_bin = mx - mn > 0.f ? (float)(BINS - 1) / (mx - mn) : 0.f;
 
   Kept kept = {0u, 0x7FFFFFFF};
-  const int top_k = p.top_k ? p.top_k[row] : 0;
-  if (top_k > 0 && top_k < p.V) narrow(r, kept, false, (unsigned long long)top_k, 0.f);
-  const float top_p = p.top_p ? p.top_p[row] : 1.f;
-  if (top_p < 1.f) narrow(r, kept, true, 0, fmaxf(top_p, 0.f));
-  const float min_p = p.min_p ? p.min_p[row] : 0.f;
-  unsigned long long least = 1;
-  if (min_p > 0.f) least = max(1ull, (unsigned long long)ceil((double)fminf(min_p, 1.f) * (double)(1ull << ONE_BITS)));
-
-  // the kept mass of each warp's tokens, of the CTAs, of the row
-  unsigned long long mine = 0;
-  for (int i = r.w0 + lane; i < r.w1; i += 32) {
-    const float v = x[i];
-    if (!kept.has(key_of(v), i)) continue;
-    const unsigned long long w = weight_of(v, r.mx, r.ch, r.cl, s->table);
-    if (w >= least) mine += w;
-  }
-  mine = warp_sum(mine);
-  __syncthreads();  // warp_sum has been read
-  if (lane == 0) s->warp_sum[warp] = mine;
-  __syncthreads();
-  const unsigned long long theirs = s->warp_sum[lane];
-  const unsigned long long cta = warp_sum(theirs);
-  unsigned long long before = warp_sum(lane < warp ? theirs : 0ull);
-  unsigned long long total = cta;
-  if (C > 1) {
-    if (threadIdx.x < C) to_peer(&s->peer[2][r.rank].sum, threadIdx.x, cta);
-    row_sync(r);
-    total = 0;
-    for (int c2 = 0; c2 < C; c2++) {
-      const unsigned long long v = s->peer[2][c2].sum;
-      if (c2 < (int)r.rank) before += v;
-      total += v;
+  if (top_k > 0 && top_k < p.V) {
+    narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
+    if (C > 1 && top_k <= LIST) {
+      // the survivors, in order of their index, into the first CTA's list
+      uint32_t n = 0;
+      for (int i = r.w0 + lane; i < r.w1; i += 32) {
+        const float v = r.at(i);
+        n += v > -INFINITY && kept.has(key_of(v), r.first + i);
+      }
+      n = warp_sum(n);
+      if (lane == 0) s->warp_a[warp] = n;
+      __syncthreads();
+      const uint32_t theirs = lane < SAMPLE_WARPS ? s->warp_a[lane] : 0;
+      uint32_t at = warp_sum(lane < warp ? theirs : 0u);
+      const uint32_t cta = warp_sum(theirs);
+      if (threadIdx.x < C) to_peer(&s->peer[1][r.rank].first, threadIdx.x, cta);
+      row_sync(r);
+      const uint32_t others = lane < C ? s->peer[1][lane].first : 0;
+      at += warp_sum(lane < (int)r.rank ? others : 0u);
+      const uint32_t all = warp_sum(others);
+      if (n)
+        for (int i0 = r.w0; i0 < r.w1; i0 += 32) {
+          const int i = i0 + lane;
+          const float v = i < r.w1 ? r.at(i) : -INFINITY;
+          const bool in = v > -INFINITY && kept.has(key_of(v), r.first + i);
+          const uint32_t set = __ballot_sync(ALL, in);
+          if (in) {
+            const uint32_t to = at + __popc(set & ((1u << lane) - 1));
+            to_peer(&s->list_x[to], 0, __float_as_uint(v));
+            to_peer(&s->list_index[to], 0, (uint32_t)(r.first + i));
+          }
+          at += __popc(set);
+        }
+      row_sync(r);
+      if (r.rank) return;
+      Row<float> one;
+      one.x = s->list_x;
+      one.s = s;
+      one.C = 1;
+      one.rank = 0;
+      one.first = 0;
+      one.part((int)all);
+      one.mx = r.mx, one.ch = r.ch, one.cl = r.cl, one.to_bin = r.to_bin;
+      kept = {0u, 0x7FFFFFFF};
+      if (top_p < 1.f) narrow<true>(one, kept, 0, fmaxf(top_p, 0.f));
+      choose(one, kept, min_p, u, s->list_index, p.token + row, p.prob ? p.prob + row : nullptr);
+      return;
     }
   }
-  const float u = p.u[row];
-  unsigned long long target = u > 0.f ? (unsigned long long)((double)fminf(u, 1.f) * (double)total) + 1 : 1;
-  if (target > total) target = total;
-  if (!(before < target && target <= before + mine)) return;
-  for (int i0 = r.w0; i0 < r.w1; i0 += 32) {
-    const int i = i0 + lane;
-    unsigned long long w = 0;
-    if (i < r.w1 && kept.has(key_of(x[i]), i)) {
-      w = weight_of(x[i], r.mx, r.ch, r.cl, s->table);
-      if (w < least) w = 0;
-    }
-    unsigned long long inc = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long a = __shfl_up_sync(ALL, inc, o);
-      if (lane >= o) inc += a;
-    }
-    if (before + inc >= target && before + inc - w < target) {
-      p.token[row] = (int32_t)(first + i);
-      if (p.prob) p.prob[row] = (float)((double)w / (double)total);
-    }
-    before += __shfl_sync(ALL, inc, 31);
-    if (before >= target) return;
-  }
+  if (top_p < 1.f) narrow<true>(r, kept, 0, fmaxf(top_p, 0.f));
+  choose(r, kept, min_p, u, nullptr, p.token + row, p.prob ? p.prob + row : nullptr);
 }
 
 const void* sample_fn(int dtype) {
   return dtype == QLIN_F32 ? reinterpret_cast<const void*>(qlin_sample_kernel<float>)
                            : reinterpret_cast<const void*>(qlin_sample_kernel<__nv_bfloat16>);
+}
+
+// CTAs per row: a power of two, 16 tokens per thread where the GPU has room
+// for that many clusters at once, 32 and more where it has not.
+int sample_ctas(int64_t M, int64_t V) {
+  int C = 1;
+  while (C < 8 && V > (int64_t)C * 16 * SAMPLE_THREADS) C *= 2;
+  if (C == 8 && V > 8 * 16 * SAMPLE_THREADS && (M <= 8 || V > 8 * 32768)) C = 16;
+  return C;
 }
 
 std::once_flag g_sample_once[64];
@@ -521,13 +637,12 @@ extern "C" qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logi
     if (!is_aligned(a, 4)) return QLIN_ERR_INVALID_ARG;
   qlin_status st = sample_setup();
   if (st != QLIN_OK) return st;
-  int C = 1;
-  while (C < 8 && V > (int64_t)C * 4096) C *= 2;
-  if (V > 8 * 32768) C = 16;
+  const int C = sample_ctas(M, V);
   SampleParams p = {logits, ld, u, temperature, top_p, min_p, top_k, token, prob, (int)V,
                     (int)(((V + C - 1) / C + 31) / 32 * 32)};
-  void* args[] = {&p, &C};
+  int c = C;
+  void* args[] = {&p, &c};
   return launch_step(sample_fn(dtype), dim3((unsigned)(M * C), 1, 1), dim3(SAMPLE_THREADS, 1, 1),
-                     sizeof(SampleShared) + (size_t)p.slice * 4, static_cast<cudaStream_t>(stream), args,
+                     sizeof(SampleShared) + (size_t)p.slice * (dtype == QLIN_F32 ? 4 : 2), static_cast<cudaStream_t>(stream), args,
                      (flags & QLIN_FLAG_PDL) != 0, C);
 }
