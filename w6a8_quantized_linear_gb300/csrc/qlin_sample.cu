@@ -21,8 +21,10 @@ constexpr int SAMPLE_THREADS = 512;
 constexpr int SAMPLE_WARPS = SAMPLE_THREADS / 32;
 constexpr int BINS = SAMPLE_THREADS;     // one per thread in the scans
 constexpr int MAX_C = 16;                // CTAs of a row's cluster, at most
+constexpr int CHUNK = 128;               // consecutive tokens that a warp takes at once, four per lane
 constexpr int FEW = 128;                 // a bin of at most this many tokens is settled by comparing all pairs
 constexpr int LIST = 1024;               // so many survivors of top-k are carried on by one CTA
+constexpr int LIST_ROOM = (LIST + CHUNK * SAMPLE_WARPS - 1) / (CHUNK * SAMPLE_WARPS) * CHUNK * SAMPLE_WARPS;
 constexpr int ONE_BITS = 42;             // weights are multiples of 2^-42; 2^19 of them sum below 2^62
 constexpr uint32_t ALL = 0xFFFFFFFFu;
 
@@ -41,7 +43,7 @@ struct SampleParams {
   const int32_t* top_k;
   int32_t* token;
   float* prob;
-  int V, slice;  // tokens of the row, of one CTA (a multiple of 32)
+  int V, slice;  // tokens of the row, of one CTA (a multiple of CHUNK)
 };
 
 struct Bin {  // of the whole row, in every CTA
@@ -62,7 +64,7 @@ struct SampleShared {
   uint32_t lo[BINS], hi[BINS], count[BINS], kmin[BINS], kmax[BINS];  // this CTA's histogram
   Bin bins[BINS];
   Candidate few[FEW];
-  float list_x[LIST];          // survivors of top-k, in order of their index
+  __align__(16) float list_x[LIST_ROOM];  // survivors of top-k, in order of their index
   uint32_t list_index[LIST];
   Round peer[3][MAX_C];
   unsigned long long warp_sum[SAMPLE_WARPS];
@@ -77,6 +79,10 @@ struct SampleShared {
 __device__ __forceinline__ uint32_t key_of(float x) {  // larger logit, larger key (no -0 among the logits)
   const uint32_t b = __float_as_uint(x);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float logit_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
 // exp((x - max) / T) as a multiple of 2^-42.  With c = log2(e) / T as a pair
@@ -105,32 +111,74 @@ __device__ __forceinline__ unsigned long long weight_of(float x, float mx, float
   return shift > ONE_BITS + 1 ? 0 : ((((unsigned long long)m << (ONE_BITS - 31 + 1)) >> shift) + 1) >> 1;
 }
 
-// Which part of the order survives: keys above `key`, and equal ones up to
+// ceil or floor of n * f for n below 2^62 and f in [0, 1], exactly: f is a
+// 24-bit integer over a power of two.  (fp64 is slow here.)
+template <bool CEIL>
+__device__ __forceinline__ unsigned long long share_of(unsigned long long n, float f) {
+  const uint32_t bits = __float_as_uint(f), e = bits >> 23;
+  const unsigned long long m = e ? (bits & 0x7FFFFFu) | 0x800000u : bits & 0x7FFFFFu;
+  const int shift = 150 - (int)(e ? e : 1);  // f = m 2^-shift, 23 <= shift <= 149
+  unsigned long long lo = n * m, hi = __umul64hi(n, m);
+  if (CEIL) {  // 2^shift - 1 more; n m + 2^shift stays below 2^127 unless the result is 0 or 1
+    if (shift >= 126) return lo | hi ? 1 : 0;
+    const unsigned long long al = shift < 64 ? (1ull << shift) - 1 : ~0ull, ah = shift < 64 ? 0 : (1ull << (shift - 64)) - 1;
+    const unsigned long long s = lo + al;
+    hi += ah + (s < lo);
+    lo = s;
+  }
+  if (shift >= 128) return 0;
+  return shift >= 64 ? hi >> (shift - 64) : (lo >> shift) | (hi << (64 - shift));
+}
+
+// a / b to 2^-31 and rounded, for 0 < a <= b: 32-bit division of the numbers'
+// leading bits (fp64 division would cost a microsecond here)
+__device__ __forceinline__ float ratio(unsigned long long a, unsigned long long b) {
+  const int za = __clzll(a), zb = __clzll(b);
+  const unsigned long long q = (a << za) / ((b << zb) >> 32);  // in [2^31, 2^33]
+  return ldexpf((float)q, zb - za - 32);
+}
+
+// Which part of the order survives: logits above x, and equal ones up to
 // `index` in the row (a bound that only this CTA's tokens have to agree with).
+// Forbidden tokens (-inf) never do.
 struct Kept {
-  uint32_t key;
-  int64_t index;
-  __device__ __forceinline__ bool has(uint32_t k, int64_t i) const { return k > key || (k == key && i <= index); }
+  float x;
+  int index;
+  __device__ __forceinline__ bool has(float v, int i) const { return v > x || (v == x && i <= index); }
 };
+__device__ __forceinline__ Kept everything() { return {-INFINITY, -1}; }
 
 // The tokens that a CTA works on: a slice of the row in shared memory, or (one
-// CTA) the survivors of top-k.
+// CTA) the survivors of top-k; filled up with -inf to whole chunks per warp.
 template <typename T>
 struct Row {
   const T* x;
-  int n, w0, w1;     // tokens, this warp's contiguous part of them
-  int64_t first;     // index of the slice's first token
+  int w0, w1;        // this warp's contiguous part
+  int first;         // index of the slice's first token
   float mx, ch, cl, to_bin;
   uint32_t rank, C;
   SampleShared* s;
-  __device__ __forceinline__ float at(int i) const { return to_float(x[i]) + 0.f; }  // -0 becomes 0
   __device__ __forceinline__ unsigned long long weight(float v) const { return weight_of(v, mx, ch, cl, s->table); }
-  __device__ __forceinline__ void part(int tokens) {
-    const int per = (tokens + 32 * SAMPLE_WARPS - 1) / (32 * SAMPLE_WARPS) * 32, warp = threadIdx.x >> 5;
-    n = tokens;
-    w0 = min(n, warp * per);
-    w1 = min(n, w0 + per);
+  __device__ __forceinline__ void part(int tokens) {  // whole chunks, alike for all warps
+    const int per = (tokens + CHUNK * SAMPLE_WARPS - 1) / (CHUNK * SAMPLE_WARPS) * CHUNK;
+    w0 = (threadIdx.x >> 5) * per;
+    w1 = w0 + per;
   }
+  // tokens 4 lane .. 4 lane + 3 of the chunk at i
+  __device__ __forceinline__ void four(int i, float (&v)[4]) const {
+    const T* at = x + i + (threadIdx.x & 31) * 4;
+    if constexpr (sizeof(T) == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(at);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+      const uint2 f = *reinterpret_cast<const uint2*>(at);
+      const float2 a = unpack2(f.x, T()), b = unpack2(f.y, T());
+      v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+    }
+  }
+  // Place among the row's BINS equal parts of its logits' range, largest
+  // first, whole bins as integers: it falls with x, the same in every use.
+  __device__ __forceinline__ float place(float v) const { return fminf((mx - v) * to_bin, (float)(BINS - 1)); }
 };
 
 template <typename T>
@@ -162,15 +210,6 @@ __device__ __forceinline__ uint32_t from_peer(const uint32_t* local, uint32_t ra
   return v;
 }
 
-template <typename T>
-__device__ __forceinline__ int bin0(const Row<T>& r, float x) {  // of the row's range of logits
-  return min(BINS - 1, (int)((r.mx - x) * r.to_bin));
-}
-template <typename T>
-__device__ __forceinline__ int bin1(const Row<T>& r, float x, int b0) {  // of the range of one such bin
-  return max(0, min(BINS - 1, (int)(((r.mx - x) * r.to_bin - (float)b0) * (float)BINS)));
-}
-
 // The sum over this CTA's threads of v before this thread (exclusive), and
 // the total.
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* total,
@@ -190,34 +229,44 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
   return warp_sum(lane < warp ? w : 0ull) + inc - v;
 }
 
-// The row index of the quota-th token (from 1) with this key among the
+// The row index of the quota-th token (from 1) with this logit among the
 // survivors of this CTA; -1 for none.  All threads of the CTA.
 template <typename T>
-__device__ __forceinline__ int64_t index_of(const Row<T>& r, uint32_t key, int64_t bound, uint32_t quota) {
+__device__ __forceinline__ int index_of(const Row<T>& r, const Kept& kept, float x, uint32_t quota) {
   if (quota == 0) return -1;
   SampleShared* s = r.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto hits = [&](int i0) -> uint32_t {  // a bit for each of a lane's four tokens
+    float v[4];
+    r.four(i0, v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 4; e++) m |= (v[e] == x && kept.has(v[e], r.first + i0 + lane * 4 + e) ? 1u : 0u) << e;
+    return m;
+  };
   uint32_t n = 0;
-  for (int i = r.w0 + lane; i < r.w1; i += 32) n += key_of(r.at(i)) == key && r.first + i <= bound;
+  for (int i = r.w0; i < r.w1; i += CHUNK) n += __popc(hits(i));
   n = warp_sum(n);
   if (lane == 0) s->warp_a[warp] = n;
   __syncthreads();
   uint32_t before = 0;
   for (int w = 0; w < warp; w++) before += s->warp_a[w];
   if (before < quota && quota <= before + n) {
-    uint32_t left = quota - before;
-    for (int i0 = r.w0; i0 < r.w1; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t hit = __ballot_sync(ALL, i < r.w1 && key_of(r.at(i)) == key && r.first + i <= bound);
-      if ((uint32_t)__popc(hit) >= left) {
-        if (lane == 0) s->pick_index = (uint32_t)(r.first + i0 + __fns(hit, 0, left));
-        break;
+    for (int i = r.w0; i < r.w1 && before < quota; i += CHUNK) {
+      const uint32_t m = hits(i), c = __popc(m);
+      uint32_t inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t a = __shfl_up_sync(ALL, inc, o);
+        if (lane >= o) inc += a;
       }
-      left -= __popc(hit);
+      if (before + inc >= quota && before + inc - c < quota)
+        s->pick_index = (uint32_t)(r.first + i + lane * 4 + __fns(m, 0, quota - (before + inc - c)));
+      before += __shfl_sync(ALL, inc, 31);
     }
   }
   __syncthreads();
-  return s->pick_index;
+  return (int)s->pick_index;
 }
 
 // The shortest beginning of the survivors' order whose count (BY_MASS false)
@@ -226,16 +275,27 @@ __device__ __forceinline__ int64_t index_of(const Row<T>& r, uint32_t key, int64
 // between them: the histograms, their sums, the few tokens of the bin in which
 // the border lies.
 template <bool BY_MASS, typename T>
-__device__ __noinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long long want, float top_p) {
+__device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long long want, float top_p) {
   SampleShared* s = r.s;
   const int lane = threadIdx.x & 31;
-  int b0 = 0, level = 0, sh = 0;
+  int level = 0, sh = 0;
+  float b0 = 0.f;
   uint32_t kmax = 0, kmin = 0;
-  // the bin of a surviving token at this level, -1 outside the range that is split
-  auto bin_of = [&](float x, uint32_t key) -> int {
-    if (level == 0) return bin0(r, x);
-    if (level == 1) return bin0(r, x) != b0 ? -1 : bin1(r, x, b0);
-    return key < kmin || key > kmax ? -1 : (int)((kmax - key) >> sh);
+  // a surviving token's place among the bins of this level; whether it is
+  // in the range that the level splits
+  auto place = [&](float x) -> float {
+    if (level == 0) return r.place(x);
+    if (level == 1) return fminf((r.place(x) - b0) * (float)BINS, (float)(BINS - 1));
+    return (float)((kmax - key_of(x)) >> sh);
+  };
+  auto inside = [&](float x) -> bool {
+    if (level == 0) return true;
+    if (level == 1) {
+      const float t = r.place(x);
+      return t >= b0 && t < b0 + 1.f;
+    }
+    const uint32_t key = key_of(x);
+    return key >= kmin && key <= kmax;
   };
   while (true) {
     const int mine = threadIdx.x;
@@ -243,22 +303,26 @@ __device__ __noinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long l
     s->kmin[mine] = ALL;
     if (threadIdx.x == 0) s->filled = 0;
     __syncthreads();
-    for (int i = r.w0 + lane; i < r.w1; i += 32) {
-      const float x = r.at(i);
-      const uint32_t key = key_of(x);
-      if (x == -INFINITY || !kept.has(key, r.first + i)) continue;
-      const int b = bin_of(x, key);
-      if (b < 0) continue;
-      atomicAdd(&s->count[b], 1u);
-      if (BY_MASS) {
-        const unsigned long long w = r.weight(x);
-        const uint32_t wl = (uint32_t)w;
-        const uint32_t wh = (uint32_t)(w >> 32) + ((uint32_t)(atomicAdd(&s->lo[b], wl) + wl) < wl ? 1u : 0u);  // the carry
-        if (wh) atomicAdd(&s->hi[b], wh);
-      }
-      if (level) {
-        atomicMin(&s->kmin[b], key);
-        atomicMax(&s->kmax[b], key);
+    for (int i = r.w0; i < r.w1; i += CHUNK) {
+      float x[4];
+      r.four(i, x);
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        if (!kept.has(x[e], r.first + i + lane * 4 + e) || !inside(x[e])) continue;
+        const int b = (int)place(x[e]);
+        atomicAdd(&s->count[b], 1u);
+        if (BY_MASS) {
+          const unsigned long long w = r.weight(x[e]);
+          const uint32_t wl = (uint32_t)w;
+          const uint32_t wh =
+              (uint32_t)(w >> 32) + ((uint32_t)(atomicAdd(&s->lo[b], wl) + wl) < wl ? 1u : 0u);  // the carry
+          if (wh) atomicAdd(&s->hi[b], wh);
+        }
+        if (level) {
+          const uint32_t key = key_of(x[e]);
+          atomicMin(&s->kmin[b], key);
+          atomicMax(&s->kmax[b], key);
+        }
       }
     }
     row_sync(r);  // every CTA's histogram is complete
@@ -293,8 +357,7 @@ __device__ __noinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long l
     const unsigned long long v = BY_MASS ? s->bins[mine].mass : s->bins[mine].count;
     const unsigned long long before = block_scan(v, &total, s);
     if (level == 0 && BY_MASS) {
-      const double t = ceil((double)top_p * (double)total);
-      want = t < 1. ? 1 : (unsigned long long)t;
+      want = max(1ull, share_of<true>(total, top_p));
       if (want > total) want = total;
     }
     if (total < want || total == 0) return;  // all survivors (the same in every CTA)
@@ -314,16 +377,20 @@ __device__ __noinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long l
         ahead = warp_sum(lane < (int)r.rank ? n : 0u);
       }
       if (s->count[b])
-        for (int i = r.w0 + lane; i < r.w1; i += 32) {
-          const float x = r.at(i);
-          const uint32_t key = key_of(x);
-          if (x == -INFINITY || !kept.has(key, r.first + i) || bin_of(x, key) != b) continue;
-          const unsigned long long w = BY_MASS ? r.weight(x) : 1;
-          const Candidate* at = &s->few[ahead + atomicAdd(&s->filled, 1u)];
-          for (uint32_t c = 0; c < r.C; c++)
-            asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dsmem_addr(at, c)), "r"(key),
-                         "r"((uint32_t)(r.first + i)), "r"((uint32_t)w), "r"((uint32_t)(w >> 32))
-                         : "memory");
+        for (int i = r.w0; i < r.w1; i += CHUNK) {
+          float x[4];
+          r.four(i, x);
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const int index = r.first + i + lane * 4 + e;
+            if (!kept.has(x[e], index) || !inside(x[e]) || (int)place(x[e]) != b) continue;
+            const unsigned long long w = BY_MASS ? r.weight(x[e]) : 1;
+            const Candidate* at = &s->few[ahead + atomicAdd(&s->filled, 1u)];
+            for (uint32_t c = 0; c < r.C; c++)
+              asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dsmem_addr(at, c)),
+                           "r"(key_of(x[e])), "r"((uint32_t)index), "r"((uint32_t)w), "r"((uint32_t)(w >> 32))
+                           : "memory");
+          }
         }
       row_sync(r);
       // each token's sum of those before it; one of them is the last that is kept
@@ -340,13 +407,13 @@ __device__ __noinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long l
         }
       }
       __syncthreads();
-      kept.key = s->pick_key;
-      kept.index = s->pick_index;
+      kept.x = logit_of(s->pick_key);
+      kept.index = (int)s->pick_index;
       __syncthreads();
       return;
     }
     if (level == 0) {
-      b0 = b;
+      b0 = (float)b;
     } else {
       kmin = hit.kmin;
       kmax = hit.kmax;
@@ -355,9 +422,8 @@ __device__ __noinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long l
           const unsigned long long w = hit.mass / hit.count;  // they weigh the same
           want = w ? (want + w - 1) / w : hit.count;
         }
-        const int64_t bound = kmax == kept.key ? kept.index : 0x7FFFFFFF;
-        kept.key = kmax;
-        kept.index = bound;
+        const float x = logit_of(kmax);
+        int bound = x == kept.x ? kept.index : 0x7FFFFFFF;
         if (want < hit.count) {  // the same in every CTA
           uint32_t ahead = 0;
           if (r.C > 1) {
@@ -366,9 +432,10 @@ __device__ __noinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long l
           }
           const uint32_t own = s->count[b];
           const uint32_t quota = want <= ahead ? 0 : want - ahead >= own ? own : (uint32_t)(want - ahead);
-          if (quota < own) kept.index = index_of(r, kmax, bound, quota);
+          if (quota < own) bound = index_of(r, kept, x, quota);
           row_sync(r);  // the counts have been read
         }
+        kept = {x, bound};
         return;
       }
       sh = 0;
@@ -388,16 +455,23 @@ __device__ __forceinline__ void choose(const Row<T>& r, const Kept& kept, float 
   SampleShared* s = r.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long least = 1;
-  if (min_p > 0.f) least = max(1ull, (unsigned long long)ceil((double)fminf(min_p, 1.f) * (double)(1ull << ONE_BITS)));
-  auto weight = [&](int i) -> unsigned long long {
-    const float v = r.at(i);
-    if (!kept.has(key_of(v), r.first + i)) return 0;
-    const unsigned long long w = r.weight(v);
-    return w < least ? 0 : w;
+  if (min_p > 0.f) least = max(1ull, share_of<true>(1ull << ONE_BITS, fminf(min_p, 1.f)));
+  auto weights = [&](int i0, unsigned long long (&w)[4]) -> unsigned long long {
+    float v[4];
+    r.four(i0, v);
+    unsigned long long sum = 0;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      w[e] = 0;
+      if (kept.has(v[e], r.first + i0 + lane * 4 + e)) w[e] = r.weight(v[e]);
+      if (w[e] < least) w[e] = 0;
+      sum += w[e];
+    }
+    return sum;
   };
   // the kept mass of each warp's tokens, of the CTAs, of the row
-  unsigned long long mine = 0;
-  for (int i = r.w0 + lane; i < r.w1; i += 32) mine += weight(i);
+  unsigned long long mine = 0, w[4];
+  for (int i = r.w0; i < r.w1; i += CHUNK) mine += weights(i, w);
   mine = warp_sum(mine);
   __syncthreads();  // warp_sum has been read
   if (lane == 0) s->warp_sum[warp] = mine;
@@ -412,24 +486,30 @@ __device__ __forceinline__ void choose(const Row<T>& r, const Kept& kept, float 
     before += warp_sum(lane < (int)r.rank ? v : 0ull);
     total = warp_sum(v);
   }
-  unsigned long long target = u > 0.f ? (unsigned long long)((double)fminf(u, 1.f) * (double)total) + 1 : 1;
+  unsigned long long target = u > 0.f ? share_of<false>(total, fminf(u, 1.f)) + 1 : 1;
   if (target > total) target = total;
   if (!(before < target && target <= before + mine)) return;
-  for (int i0 = r.w0; i0 < r.w1; i0 += 32) {
-    const int i = i0 + lane;
-    const unsigned long long w = i < r.w1 ? weight(i) : 0;
-    unsigned long long inc = w;
+  for (int i0 = r.w0; i0 < r.w1 && before < target; i0 += CHUNK) {
+    const unsigned long long sum = weights(i0, w);
+    unsigned long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned long long a = __shfl_up_sync(ALL, inc, o);
       if (lane >= o) inc += a;
     }
-    if (before + inc >= target && before + inc - w < target) {
-      *token = index ? (int32_t)index[i] : (int32_t)(r.first + i);
-      if (prob) *prob = (float)((double)w / (double)total);
+    if (before + inc >= target && before + inc - sum < target) {  // one lane
+      unsigned long long run = before + inc - sum;
+      int e = 0;
+#pragma unroll
+      for (int k = 0; k < 3; k++) {
+        if (e == k && run + w[k] < target) run += w[k], e++;
+      }
+      const unsigned long long hit = e == 0 ? w[0] : e == 1 ? w[1] : e == 2 ? w[2] : w[3];
+      const int i = i0 + lane * 4 + e;
+      *token = index ? (int32_t)index[i] : r.first + i;
+      if (prob) *prob = ratio(hit, total);
     }
     before += __shfl_sync(ALL, inc, 31);
-    if (before >= target) return;
   }
 }
 
@@ -447,9 +527,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   r.s = s;
   r.C = C;
   r.rank = C == 1 ? 0 : cluster_ctarank();
-  r.first = (int64_t)r.rank * p.slice;
+  r.first = (int)(r.rank * p.slice);
   const int row = blockIdx.x / C;
-  r.part((int)max((int64_t)0, min((int64_t)p.slice, p.V - r.first)));
+  const int tokens = max(0, min(p.slice, p.V - r.first));
+  r.part(p.slice);
   if (C > 1) cluster_arrive_relaxed();
   if (threadIdx.x < 32) s->table[threadIdx.x] = TABLE[threadIdx.x];
   pdl_wait();
@@ -466,19 +547,19 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   for (int i0 = r.w0 + lane; i0 < r.w1; i0 += 32 * BATCH) {
     T v[BATCH];
 #pragma unroll
-    for (int k = 0; k < BATCH; k++)
-      if (i0 + 32 * k < r.w1) v[k] = src[i0 + 32 * k];
+    for (int k = 0; k < BATCH; k++) v[k] = i0 + 32 * k < tokens ? src[i0 + 32 * k] : T(-INFINITY);
 #pragma unroll
     for (int k = 0; k < BATCH; k++) {
       const int i = i0 + 32 * k;
       if (i >= r.w1) break;
-      x[i] = v[k];
-      const float f = to_float(v[k]) + 0.f;
+      const float f = to_float(v[k]) + 0.f;  // -0 becomes 0
+      x[i] = T(f);
       nan |= f != f;
       if (f > mx) mx = f, top = (uint32_t)(r.first + i);
       if (f > -INFINITY) mn = fminf(mn, f);
     }
   }
+  __syncwarp();
   // of the warp, the CTA, the row
   auto join = [&](float omx, float omn, uint32_t onan, uint32_t otop) {
     if (omx > mx || (omx == mx && otop < top)) mx = omx, top = otop;
@@ -521,26 +602,34 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
     return;
   }
   if (mx == INFINITY) {  // the infinite ones are left, alike
+    __syncwarp();
     for (int i = r.w0 + lane; i < r.w1; i += 32) x[i] = to_float(x[i]) == INFINITY ? T(0.f) : T(-INFINITY);
     __syncwarp();
     mx = mn = 0.f;
   }
   r.mx = mx;
-  const double c = 1.4426950408889634 / (double)temperature;
-  r.ch = (float)c;
-  r.cl = (float)(c - (double)r.ch);
-  r.to_bin = mx - mn > 0.f ? (float)(BINS - 1) / (mx - mn) : 0.f;
+  // log2(e) / T as a pair of floats: the quotient of the leading part, and that
+  // of what is left
+  constexpr float E_HI = 1.44269502f, E_LO = (float)(1.44269504088896341 - (double)E_HI);
+  r.ch = E_HI / temperature;
+  r.cl = (fmaf(-r.ch, temperature, E_HI) + E_LO) / temperature;
+  r.to_bin = mx - mn > 0.f ? fminf((float)(BINS - 1) / (mx - mn), 3e38f) : 0.f;
 
-  Kept kept = {0u, 0x7FFFFFFF};
+  Kept kept = everything();
   if (top_k > 0 && top_k < p.V) {
     narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
     if (C > 1 && top_k <= LIST) {
       // the survivors, in order of their index, into the first CTA's list
       uint32_t n = 0;
-      for (int i = r.w0 + lane; i < r.w1; i += 32) {
-        const float v = r.at(i);
-        n += v > -INFINITY && kept.has(key_of(v), r.first + i);
-      }
+      auto survivors = [&](int i0, float (&v)[4]) -> uint32_t {  // a bit for each of a lane's four tokens
+        r.four(i0, v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 4; e++) m |= (kept.has(v[e], r.first + i0 + lane * 4 + e) ? 1u : 0u) << e;
+        return m;
+      };
+      float v[4];
+      for (int i = r.w0; i < r.w1; i += CHUNK) n += __popc(survivors(i, v));
       n = warp_sum(n);
       if (lane == 0) s->warp_a[warp] = n;
       __syncthreads();
@@ -553,20 +642,29 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
       at += warp_sum(lane < (int)r.rank ? others : 0u);
       const uint32_t all = warp_sum(others);
       if (n)
-        for (int i0 = r.w0; i0 < r.w1; i0 += 32) {
-          const int i = i0 + lane;
-          const float v = i < r.w1 ? r.at(i) : -INFINITY;
-          const bool in = v > -INFINITY && kept.has(key_of(v), r.first + i);
-          const uint32_t set = __ballot_sync(ALL, in);
-          if (in) {
-            const uint32_t to = at + __popc(set & ((1u << lane) - 1));
-            to_peer(&s->list_x[to], 0, __float_as_uint(v));
-            to_peer(&s->list_index[to], 0, (uint32_t)(r.first + i));
+        for (int i = r.w0; i < r.w1; i += CHUNK) {
+          const uint32_t m = survivors(i, v);
+          if (!__any_sync(ALL, m)) continue;
+          uint32_t inc = __popc(m);
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t a = __shfl_up_sync(ALL, inc, o);
+            if (lane >= o) inc += a;
           }
-          at += __popc(set);
+          uint32_t to = at + inc - __popc(m);
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            if (m >> e & 1) {
+              to_peer(&s->list_x[to], 0, __float_as_uint(v[e]));
+              to_peer(&s->list_index[to], 0, (uint32_t)(r.first + i + lane * 4 + e));
+              to++;
+            }
+          at += __shfl_sync(ALL, inc, 31);
         }
       row_sync(r);
       if (r.rank) return;
+      for (uint32_t i = all + threadIdx.x; i < LIST_ROOM; i += SAMPLE_THREADS) s->list_x[i] = -INFINITY;
+      __syncthreads();
       Row<float> one;
       one.x = s->list_x;
       one.s = s;
@@ -575,7 +673,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
       one.first = 0;
       one.part((int)all);
       one.mx = r.mx, one.ch = r.ch, one.cl = r.cl, one.to_bin = r.to_bin;
-      kept = {0u, 0x7FFFFFFF};
+      kept = everything();
       if (top_p < 1.f) narrow<true>(one, kept, 0, fmaxf(top_p, 0.f));
       choose(one, kept, min_p, u, s->list_index, p.token + row, p.prob ? p.prob + row : nullptr);
       return;
@@ -639,7 +737,7 @@ extern "C" qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logi
   if (st != QLIN_OK) return st;
   const int C = sample_ctas(M, V);
   SampleParams p = {logits, ld, u, temperature, top_p, min_p, top_k, token, prob, (int)V,
-                    (int)(((V + C - 1) / C + 31) / 32 * 32)};
+                    (int)(((V + C - 1) / C + CHUNK * SAMPLE_WARPS - 1) / (CHUNK * SAMPLE_WARPS) * (CHUNK * SAMPLE_WARPS))};
   int c = C;
   void* args[] = {&p, &c};
   return launch_step(sample_fn(dtype), dim3((unsigned)(M * C), 1, 1), dim3(SAMPLE_THREADS, 1, 1),
