@@ -22,9 +22,8 @@ constexpr int SAMPLE_WARPS = SAMPLE_THREADS / 32;
 constexpr int BINS = SAMPLE_THREADS;     // one per thread in the scans
 constexpr int MAX_C = 16;                // CTAs of a row's cluster, at most
 constexpr int CHUNK = 128;               // consecutive tokens that a warp takes at once, four per lane
-constexpr int FEW = 128;                 // a bin of at most this many tokens is settled by comparing all pairs
-constexpr int LIST = 1024;               // so many survivors of top-k are carried on by one CTA
-constexpr int LIST_ROOM = (LIST + CHUNK * SAMPLE_WARPS - 1) / (CHUNK * SAMPLE_WARPS) * CHUNK * SAMPLE_WARPS;
+constexpr int FEW = 128;                 // a bin of at most this many tokens is settled by comparing all pairs, four threads each
+constexpr int LIST = 2048;               // so many survivors of top-k are carried on by one CTA
 constexpr int ONE_BITS = 42;             // weights are multiples of 2^-42; 2^19 of them sum below 2^62
 constexpr uint32_t ALL = 0xFFFFFFFFu;
 
@@ -64,8 +63,6 @@ struct SampleShared {
   uint32_t lo[BINS], hi[BINS], count[BINS], kmin[BINS], kmax[BINS];  // this CTA's histogram
   Bin bins[BINS];
   Candidate few[FEW];
-  __align__(16) float list_x[LIST_ROOM];  // survivors of top-k, in order of their index
-  uint32_t list_index[LIST];
   Round peer[3][MAX_C];
   unsigned long long warp_sum[SAMPLE_WARPS];
   uint32_t warp_a[SAMPLE_WARPS], warp_b[SAMPLE_WARPS];
@@ -158,6 +155,7 @@ struct Row {
   float mx, ch, cl, to_bin;
   uint32_t rank, C;
   SampleShared* s;
+  uint32_t* all;     // [C][BINS]: the CTAs' counts
   __device__ __forceinline__ unsigned long long weight(float v) const { return weight_of(v, mx, ch, cl, s->table); }
   __device__ __forceinline__ void part(int tokens) {  // whole chunks, alike for all warps
     const int per = (tokens + CHUNK * SAMPLE_WARPS - 1) / (CHUNK * SAMPLE_WARPS) * CHUNK;
@@ -271,11 +269,13 @@ __device__ __forceinline__ int index_of(const Row<T>& r, const Kept& kept, float
 
 // The shortest beginning of the survivors' order whose count (BY_MASS false)
 // reaches `want`, or whose mass reaches the share top_p of theirs; `kept` is
-// narrowed to it.  All CTAs of the row take part.  Usually three exchanges
-// between them: the histograms, their sums, the few tokens of the bin in which
-// the border lies.
+// narrowed to it.  All CTAs of the row take part.  The first counts are pushed
+// to every CTA (one exchange); masses, and what later levels need, are joined
+// by shares of the bins (two).  The few tokens of the bin in which the border
+// lies take one more.  Returns how many tokens of the CTAs before this one
+// survive where a count was settled at once, -1 elsewhere.
 template <bool BY_MASS, typename T>
-__device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long long want, float top_p) {
+__device__ __forceinline__ int narrow(const Row<T>& r, Kept& kept, unsigned long long want, float top_p) {
   SampleShared* s = r.s;
   const int lane = threadIdx.x & 31;
   int level = 0, sh = 0;
@@ -325,10 +325,30 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
         }
       }
     }
+    const bool push = !BY_MASS && level == 0 && r.C > 1;
+    if (push) {
+      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < r.C * (BINS / 4); i += SAMPLE_THREADS) {
+        const uint32_t c = i / (BINS / 4), q = i % (BINS / 4) * 4;
+        const uint4 x = *reinterpret_cast<const uint4*>(&s->count[q]);
+        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dsmem_addr(r.all + r.rank * BINS + q, c)),
+                     "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                     : "memory");
+      }
+    }
     row_sync(r);  // every CTA's histogram is complete
+    uint32_t ahead_of = 0;  // tokens of this thread's bin in the CTAs before this one
     // each CTA joins its share of the bins, C lanes to a bin (one per CTA),
     // and lane c gives the sum to CTA c
-    if (r.C == 1) {
+    if (push) {
+      uint32_t n = 0;
+      for (uint32_t c = 0; c < r.C; c++) {
+        const uint32_t m = r.all[c * BINS + mine];
+        n += m;
+        if (c < r.rank) ahead_of += m;
+      }
+      s->bins[mine].count = n;
+    } else if (r.C == 1) {
       s->bins[mine] = {((unsigned long long)s->hi[mine] << 32) + s->lo[mine], s->count[mine], s->kmin[mine], s->kmax[mine], 0};
     } else {
       const uint32_t c = threadIdx.x % r.C;
@@ -352,7 +372,10 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
         to_peer(&s->bins[b].kmax, c, hi);
       }
     }
-    row_sync(r);
+    if (push)
+      __syncthreads();
+    else
+      row_sync(r);
     unsigned long long total;
     const unsigned long long v = BY_MASS ? s->bins[mine].mass : s->bins[mine].count;
     const unsigned long long before = block_scan(v, &total, s);
@@ -360,7 +383,7 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
       want = max(1ull, share_of<true>(total, top_p));
       if (want > total) want = total;
     }
-    if (total < want || total == 0) return;  // all survivors (the same in every CTA)
+    if (total < want || total == 0) return -1;  // all survivors (the same in every CTA)
     if (before < want && want <= before + v) {
       s->pick = mine;
       s->before = before;
@@ -372,7 +395,9 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
     if (hit.count <= FEW) {
       // its tokens into every CTA's list, this CTA's behind those of the CTAs before it
       uint32_t ahead = 0;
-      if (r.C > 1) {
+      if (push) {
+        ahead = warp_sum(lane < (int)r.rank ? r.all[lane * BINS + b] : 0u);
+      } else if (r.C > 1) {
         const uint32_t n = lane < (int)r.C ? from_peer(&s->count[b], lane) : 0;
         ahead = warp_sum(lane < (int)r.rank ? n : 0u);
       }
@@ -394,23 +419,33 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
         }
       row_sync(r);
       // each token's sum of those before it; one of them is the last that is kept
-      if (threadIdx.x < hit.count) {
-        const Candidate me = s->few[threadIdx.x];
-        unsigned long long sum = 0;
-        for (uint32_t k = 0; k < hit.count; k++) {
+      const uint32_t cand = threadIdx.x / 4;
+      const bool one = cand < hit.count;
+      const Candidate me = s->few[one ? cand : 0];
+      unsigned long long sum = 0;
+      if (one)
+        for (uint32_t k = threadIdx.x % 4; k < hit.count; k += 4) {
           const Candidate o = s->few[k];
           if (o.key > me.key || (o.key == me.key && o.index < me.index)) sum += o.weight;
         }
-        if (sum < want && want <= sum + me.weight) {
-          s->pick_key = me.key;
-          s->pick_index = me.index;
-        }
+      sum += __shfl_xor_sync(ALL, sum, 1);
+      sum += __shfl_xor_sync(ALL, sum, 2);
+      if (one && sum < want && want <= sum + me.weight) {
+        s->pick_key = me.key;
+        s->pick_index = me.index;
       }
-      __syncthreads();
+      int lower = -1;
+      if (push) {
+        unsigned long long n;
+        (void)block_scan(mine < b ? ahead_of : 0, &n, s);
+        lower = (int)n + __syncthreads_count(one && threadIdx.x % 4 == 0 && sum < want && (int)me.index < r.first);
+      } else {
+        __syncthreads();
+      }
       kept.x = logit_of(s->pick_key);
       kept.index = (int)s->pick_index;
       __syncthreads();
-      return;
+      return lower;
     }
     if (level == 0) {
       b0 = (float)b;
@@ -436,7 +471,7 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
           row_sync(r);  // the counts have been read
         }
         kept = {x, bound};
-        return;
+        return -1;
       }
       sh = 0;
       while (((kmax - kmin) >> sh) >= (uint32_t)BINS) sh++;
@@ -444,6 +479,11 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
     level++;
     __syncthreads();  // pick and bins have been read
   }
+}
+
+// Bytes of shared memory for all CTAs' counts, or the list of survivors after them.
+__host__ __device__ constexpr size_t shared_counts(int C) {
+  return C == 1 ? 0 : C * BINS * 4 > LIST * 8 ? (size_t)C * BINS * 4 : (size_t)LIST * 8;
 }
 
 // The first kept token, in order of the index, at which the running sum of
@@ -520,11 +560,17 @@ template <typename T>
 __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __grid_constant__ SampleParams p, int C) {
   extern __shared__ __align__(16) uint8_t raw[];
   SampleShared* s = reinterpret_cast<SampleShared*>(raw);
-  T* x = reinterpret_cast<T*>(raw + sizeof(SampleShared));
+  uint32_t* all = reinterpret_cast<uint32_t*>(raw + sizeof(SampleShared));
+  // the list of survivors takes the place of the counts: those have been read
+  // when the exchange before it ends
+  float* list_x = reinterpret_cast<float*>(all);
+  uint32_t* list_index = all + LIST;
+  T* x = reinterpret_cast<T*>(raw + sizeof(SampleShared) + shared_counts(C));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Row<T> r;
   r.x = x;
   r.s = s;
+  r.all = all;
   r.C = C;
   r.rank = C == 1 ? 0 : cluster_ctarank();
   r.first = (int)(r.rank * p.slice);
@@ -617,7 +663,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
 
   Kept kept = everything();
   if (top_k > 0 && top_k < p.V) {
-    narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
+    const int lower = narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
     if (C > 1 && top_k <= LIST) {
       // the survivors, in order of their index, into the first CTA's list
       uint32_t n = 0;
@@ -636,11 +682,18 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
       const uint32_t theirs = lane < SAMPLE_WARPS ? s->warp_a[lane] : 0;
       uint32_t at = warp_sum(lane < warp ? theirs : 0u);
       const uint32_t cta = warp_sum(theirs);
-      if (threadIdx.x < C) to_peer(&s->peer[1][r.rank].first, threadIdx.x, cta);
-      row_sync(r);
-      const uint32_t others = lane < C ? s->peer[1][lane].first : 0;
-      at += warp_sum(lane < (int)r.rank ? others : 0u);
-      const uint32_t all = warp_sum(others);
+      uint32_t all_n = (uint32_t)top_k;
+      if (lower >= 0) {  // exactly top_k survive
+        at += lower;
+      } else {
+        if (threadIdx.x < C) to_peer(&s->peer[1][r.rank].first, threadIdx.x, cta);
+        row_sync(r);
+        const uint32_t others = lane < C ? s->peer[1][lane].first : 0;
+        at += warp_sum(lane < (int)r.rank ? others : 0u);
+        all_n = warp_sum(others);
+      }
+      // up to 512: one per lane, in the first of its four places
+      const int spread = all_n <= SAMPLE_THREADS ? 4 : 1;
       if (n)
         for (int i = r.w0; i < r.w1; i += CHUNK) {
           const uint32_t m = survivors(i, v);
@@ -655,27 +708,29 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
 #pragma unroll
           for (int e = 0; e < 4; e++)
             if (m >> e & 1) {
-              to_peer(&s->list_x[to], 0, __float_as_uint(v[e]));
-              to_peer(&s->list_index[to], 0, (uint32_t)(r.first + i + lane * 4 + e));
+              to_peer(&list_x[to * spread], 0, __float_as_uint(v[e]));
+              to_peer(&list_index[to * spread], 0, (uint32_t)(r.first + i + lane * 4 + e));
               to++;
             }
           at += __shfl_sync(ALL, inc, 31);
         }
       row_sync(r);
       if (r.rank) return;
-      for (uint32_t i = all + threadIdx.x; i < LIST_ROOM; i += SAMPLE_THREADS) s->list_x[i] = -INFINITY;
+      for (uint32_t i = threadIdx.x; i < LIST; i += SAMPLE_THREADS)
+        if (i % spread || i / spread >= all_n) list_x[i] = -INFINITY;
       __syncthreads();
       Row<float> one;
-      one.x = s->list_x;
+      one.x = list_x;
       one.s = s;
       one.C = 1;
       one.rank = 0;
       one.first = 0;
-      one.part((int)all);
+      one.part(LIST);
+      one.all = nullptr;
       one.mx = r.mx, one.ch = r.ch, one.cl = r.cl, one.to_bin = r.to_bin;
       kept = everything();
       if (top_p < 1.f) narrow<true>(one, kept, 0, fmaxf(top_p, 0.f));
-      choose(one, kept, min_p, u, s->list_index, p.token + row, p.prob ? p.prob + row : nullptr);
+      choose(one, kept, min_p, u, list_index, p.token + row, p.prob ? p.prob + row : nullptr);
       return;
     }
   }
@@ -688,12 +743,12 @@ const void* sample_fn(int dtype) {
                            : reinterpret_cast<const void*>(qlin_sample_kernel<__nv_bfloat16>);
 }
 
-// CTAs per row: a power of two, 16 tokens per thread where the GPU has room
-// for that many clusters at once, 32 and more where it has not.
-int sample_ctas(int64_t M, int64_t V) {
+// CTAs per row, a power of two: as many as one wave of clusters holds while
+// each has four tokens per thread (a pass costs less than an exchange saves),
+// and at least so many that two CTAs' slices (64 KB) share an SM.
+int sample_ctas(int64_t M, int64_t V, int64_t size) {
   int C = 1;
-  while (C < 8 && V > (int64_t)C * 16 * SAMPLE_THREADS) C *= 2;
-  if (C == 8 && V > 8 * 16 * SAMPLE_THREADS && (M <= 8 || V > 8 * 32768)) C = 16;
+  while (C < MAX_C && ((C * (int64_t)SAMPLE_THREADS * 4 < V && 2 * C * M <= 128) || C * (int64_t)65536 < V * size)) C *= 2;
   return C;
 }
 
@@ -735,12 +790,12 @@ extern "C" qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logi
     if (!is_aligned(a, 4)) return QLIN_ERR_INVALID_ARG;
   qlin_status st = sample_setup();
   if (st != QLIN_OK) return st;
-  const int C = sample_ctas(M, V);
+  const int C = sample_ctas(M, V, dtype == QLIN_F32 ? 4 : 2);
   SampleParams p = {logits, ld, u, temperature, top_p, min_p, top_k, token, prob, (int)V,
                     (int)(((V + C - 1) / C + CHUNK * SAMPLE_WARPS - 1) / (CHUNK * SAMPLE_WARPS) * (CHUNK * SAMPLE_WARPS))};
   int c = C;
   void* args[] = {&p, &c};
   return launch_step(sample_fn(dtype), dim3((unsigned)(M * C), 1, 1), dim3(SAMPLE_THREADS, 1, 1),
-                     sizeof(SampleShared) + (size_t)p.slice * (dtype == QLIN_F32 ? 4 : 2), static_cast<cudaStream_t>(stream), args,
+                     sizeof(SampleShared) + shared_counts(C) + (size_t)p.slice * (dtype == QLIN_F32 ? 4 : 2), static_cast<cudaStream_t>(stream), args,
                      (flags & QLIN_FLAG_PDL) != 0, C);
 }
