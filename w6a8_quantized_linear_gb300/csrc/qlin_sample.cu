@@ -23,7 +23,7 @@ constexpr int BINS = SAMPLE_THREADS;     // one per thread in the scans
 constexpr int MAX_C = 16;                // CTAs of a row's cluster, at most
 constexpr int CHUNK = 128;               // consecutive tokens that a warp takes at once, four per lane
 constexpr int FEW = 128;                 // a bin of at most this many tokens is settled by comparing all pairs, four threads each
-constexpr int LIST = 2048;               // so many survivors of top-k are carried on by one CTA
+constexpr int LIST = 4096;               // so many tokens, what top-k may leave, are carried on by one CTA
 constexpr int ONE_BITS = 42;             // weights are multiples of 2^-42; 2^19 of them sum below 2^62
 constexpr uint32_t ALL = 0xFFFFFFFFu;
 
@@ -45,13 +45,9 @@ struct SampleParams {
   int V, slice;  // tokens of the row, of one CTA (a multiple of CHUNK)
 };
 
-struct Bin {  // of the whole row, in every CTA
-  unsigned long long mass;
-  uint32_t count, kmin, kmax, pad;
-};
 struct Round {  // what the CTAs of a row tell each other outside the histograms
-  float mx, mn;
-  uint32_t nan, first;
+  float mx, mn, low;
+  uint32_t nan, first, count;
   unsigned long long sum;
 };
 struct __align__(16) Candidate {
@@ -60,17 +56,19 @@ struct __align__(16) Candidate {
 };
 
 struct SampleShared {
-  uint32_t lo[BINS], hi[BINS], count[BINS], kmin[BINS], kmax[BINS];  // this CTA's histogram
-  Bin bins[BINS];
+  __align__(16) uint32_t hist[3][BINS];  // this CTA's histogram: counts, masses' low and high words
+  unsigned long long mass[BINS];         // the row's
+  uint32_t count[BINS];
   Candidate few[FEW];
-  Round peer[3][MAX_C];
+  Round peer[3][MAX_C];  // [0]: also the first of two counts of survivors
+  uint2 range[MAX_C];
   unsigned long long warp_sum[SAMPLE_WARPS];
   uint32_t warp_a[SAMPLE_WARPS], warp_b[SAMPLE_WARPS];
-  float warp_f[SAMPLE_WARPS], warp_g[SAMPLE_WARPS];
+  float warp_f[SAMPLE_WARPS], warp_g[SAMPLE_WARPS], warp_h[SAMPLE_WARPS];
   uint32_t table[32];  // 2^(i/32) in [2^31, 2^32)
   int pick;
-  uint32_t pick_key, pick_index, filled;
-  unsigned long long before;
+  uint32_t pick_key, pick_index, pick_count, filled;
+  unsigned long long before, pick_mass;
 };
 
 __device__ __forceinline__ uint32_t key_of(float x) {  // larger logit, larger key (no -0 among the logits)
@@ -174,6 +172,10 @@ struct Row {
       v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
     }
   }
+  // Whether any of the warp's tokens in a chunk may survive.
+  __device__ __forceinline__ bool any(const float (&v)[4], float least) const {
+    return __any_sync(0xFFFFFFFFu, fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) >= least);
+  }
   // Place among the row's BINS equal parts of its logits' range, largest
   // first, whole bins as integers: it falls with x, the same in every use.
   __device__ __forceinline__ float place(float v) const { return fminf((mx - v) * to_bin, (float)(BINS - 1)); }
@@ -238,6 +240,7 @@ __device__ __forceinline__ int index_of(const Row<T>& r, const Kept& kept, float
     float v[4];
     r.four(i0, v);
     uint32_t m = 0;
+    if (!r.any(v, x)) return m;
 #pragma unroll
     for (int e = 0; e < 4; e++) m |= (v[e] == x && kept.has(v[e], r.first + i0 + lane * 4 + e) ? 1u : 0u) << e;
     return m;
@@ -269,146 +272,122 @@ __device__ __forceinline__ int index_of(const Row<T>& r, const Kept& kept, float
 
 // The shortest beginning of the survivors' order whose count (BY_MASS false)
 // reaches `want`, or whose mass reaches the share top_p of theirs; `kept` is
-// narrowed to it.  All CTAs of the row take part.  The first counts are pushed
-// to every CTA (one exchange); masses, and what later levels need, are joined
-// by shares of the bins (two).  The few tokens of the bin in which the border
-// lies take one more.  Returns how many tokens of the CTAs before this one
-// survive where a count was settled at once, -1 elsewhere.
+// narrowed to it.  All CTAs of the row take part.  Each level costs one
+// exchange for counts (histograms pushed to every CTA) and two for masses
+// (joined by shares of the bins: three times the bytes make the push slower
+// than a second exchange, 5.7 against 3.9 us with 16 CTAs); the few tokens of
+// the bin in which the border lies take one more.
 template <bool BY_MASS, typename T>
-__device__ __forceinline__ int narrow(const Row<T>& r, Kept& kept, unsigned long long want, float top_p) {
+__device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long long want, float top_p) {
   SampleShared* s = r.s;
-  const int lane = threadIdx.x & 31;
-  int level = 0, sh = 0;
-  float b0 = 0.f;
+  const int lane = threadIdx.x & 31, mine = threadIdx.x;
+  int sh = 0;
   uint32_t kmax = 0, kmin = 0;
-  // a surviving token's place among the bins of this level; whether it is
-  // in the range that the level splits
-  auto place = [&](float x) -> float {
-    if (level == 0) return r.place(x);
-    if (level == 1) return fminf((r.place(x) - b0) * (float)BINS, (float)(BINS - 1));
-    return (float)((kmax - key_of(x)) >> sh);
-  };
-  auto inside = [&](float x) -> bool {
-    if (level == 0) return true;
-    if (level == 1) {
-      const float t = r.place(x);
-      return t >= b0 && t < b0 + 1.f;
-    }
-    const uint32_t key = key_of(x);
-    return key >= kmin && key <= kmax;
-  };
-  while (true) {
-    const int mine = threadIdx.x;
-    s->lo[mine] = s->hi[mine] = s->count[mine] = s->kmax[mine] = 0;
-    s->kmin[mine] = ALL;
+  const bool push = r.C > 1 && !BY_MASS;
+  for (int level = 0;; level++) {
+    // a surviving token's bin: of the row's range of logits, then of a range of keys
+    auto bin = [&](float x) -> float { return level == 0 ? r.place(x) : (float)((kmax - key_of(x)) >> sh); };
+    const float least = level == 0 ? kept.x : logit_of(kmin);
+    auto inside = [&](float x, int i) -> bool {
+      return x >= least && kept.has(x, i) && (level == 0 || key_of(x) <= kmax);
+    };
+    s->hist[0][mine] = s->hist[1][mine] = s->hist[2][mine] = 0;
     if (threadIdx.x == 0) s->filled = 0;
     __syncthreads();
     for (int i = r.w0; i < r.w1; i += CHUNK) {
       float x[4];
       r.four(i, x);
+      if (!r.any(x, least)) continue;
+      uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        if (!kept.has(x[e], r.first + i + lane * 4 + e) || !inside(x[e])) continue;
-        const int b = (int)place(x[e]);
-        atomicAdd(&s->count[b], 1u);
+      for (int e = 0; e < 4; e++) m |= (inside(x[e], r.first + i + lane * 4 + e) ? 1u : 0u) << e;
+      for (; m; m &= m - 1) {  // lanes take their tokens together, whichever of their four they are
+        const float v = m & 1 ? x[0] : m & 2 ? x[1] : m & 4 ? x[2] : x[3];
+        const int b = (int)bin(v);
+        atomicAdd(&s->hist[0][b], 1u);
         if (BY_MASS) {
-          const unsigned long long w = r.weight(x[e]);
+          const unsigned long long w = r.weight(v);
           const uint32_t wl = (uint32_t)w;
           const uint32_t wh =
-              (uint32_t)(w >> 32) + ((uint32_t)(atomicAdd(&s->lo[b], wl) + wl) < wl ? 1u : 0u);  // the carry
-          if (wh) atomicAdd(&s->hi[b], wh);
-        }
-        if (level) {
-          const uint32_t key = key_of(x[e]);
-          atomicMin(&s->kmin[b], key);
-          atomicMax(&s->kmax[b], key);
+              (uint32_t)(w >> 32) + ((uint32_t)(atomicAdd(&s->hist[1][b], wl) + wl) < wl ? 1u : 0u);  // the carry
+          if (wh) atomicAdd(&s->hist[2][b], wh);
         }
       }
     }
-    const bool push = !BY_MASS && level == 0 && r.C > 1;
     if (push) {
       __syncthreads();
       for (uint32_t i = threadIdx.x; i < r.C * (BINS / 4); i += SAMPLE_THREADS) {
         const uint32_t c = i / (BINS / 4), q = i % (BINS / 4) * 4;
-        const uint4 x = *reinterpret_cast<const uint4*>(&s->count[q]);
+        const uint4 x = *reinterpret_cast<const uint4*>(&s->hist[0][q]);
         asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dsmem_addr(r.all + r.rank * BINS + q, c)),
                      "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
                      : "memory");
       }
     }
     row_sync(r);  // every CTA's histogram is complete
-    uint32_t ahead_of = 0;  // tokens of this thread's bin in the CTAs before this one
-    // each CTA joins its share of the bins, C lanes to a bin (one per CTA),
-    // and lane c gives the sum to CTA c
+    uint32_t count = 0;
+    unsigned long long mass = 0;
     if (push) {
-      uint32_t n = 0;
       for (uint32_t c = 0; c < r.C; c++) {
-        const uint32_t m = r.all[c * BINS + mine];
-        n += m;
-        if (c < r.rank) ahead_of += m;
+        count += r.all[c * BINS + mine];
       }
-      s->bins[mine].count = n;
     } else if (r.C == 1) {
-      s->bins[mine] = {((unsigned long long)s->hi[mine] << 32) + s->lo[mine], s->count[mine], s->kmin[mine], s->kmax[mine], 0};
+      count = s->hist[0][mine];
+      mass = s->hist[1][mine] + ((unsigned long long)s->hist[2][mine] << 32);
     } else {
+      // each CTA joins its share of the bins, C lanes to a bin (one per CTA),
+      // and lane c gives the sum to CTA c
       const uint32_t c = threadIdx.x % r.C;
       const int b = r.rank * (BINS / r.C) + threadIdx.x / r.C;
-      uint32_t count = from_peer(&s->count[b], c), lo = ALL, hi = 0;
-      unsigned long long mass = 0;
-      if (BY_MASS) mass = from_peer(&s->lo[b], c) + ((unsigned long long)from_peer(&s->hi[b], c) << 32);
-      if (level) lo = from_peer(&s->kmin[b], c), hi = from_peer(&s->kmax[b], c);
+      count = from_peer(&s->hist[0][b], c);
+      mass = from_peer(&s->hist[1][b], c) + ((unsigned long long)from_peer(&s->hist[2][b], c) << 32);
       for (uint32_t o = 1; o < r.C; o <<= 1) {
         count += __shfl_xor_sync(ALL, count, o);
-        if (BY_MASS) mass += __shfl_xor_sync(ALL, mass, o);
-        if (level) {
-          lo = min(lo, __shfl_xor_sync(ALL, lo, o));
-          hi = max(hi, __shfl_xor_sync(ALL, hi, o));
-        }
+        mass += __shfl_xor_sync(ALL, mass, o);
       }
-      to_peer(&s->bins[b].count, c, count);
-      if (BY_MASS) to_peer(&s->bins[b].mass, c, mass);
-      if (level) {
-        to_peer(&s->bins[b].kmin, c, lo);
-        to_peer(&s->bins[b].kmax, c, hi);
-      }
-    }
-    if (push)
-      __syncthreads();
-    else
+      to_peer(&s->count[b], c, count);
+      to_peer(&s->mass[b], c, mass);
       row_sync(r);
-    unsigned long long total;
-    const unsigned long long v = BY_MASS ? s->bins[mine].mass : s->bins[mine].count;
-    const unsigned long long before = block_scan(v, &total, s);
-    if (level == 0 && BY_MASS) {
-      want = max(1ull, share_of<true>(total, top_p));
-      if (want > total) want = total;
+      count = s->count[mine];
+      mass = s->mass[mine];
     }
-    if (total < want || total == 0) return -1;  // all survivors (the same in every CTA)
+    unsigned long long total;
+    const unsigned long long v = BY_MASS ? mass : count;
+    const unsigned long long before = block_scan(v, &total, s);
+    if (level == 0 && BY_MASS) want = max(1ull, share_of<true>(total, top_p));
+    if (total < want || total == 0) {  // all survivors (the same in every CTA)
+      row_sync(r);                     // the counts have been read
+      return;
+    }
     if (before < want && want <= before + v) {
       s->pick = mine;
+      s->pick_count = count;
+      s->pick_mass = mass;
       s->before = before;
     }
     __syncthreads();
     const int b = s->pick;
+    const uint32_t n = s->pick_count;
     want -= s->before;
-    const Bin hit = s->bins[b];
-    if (hit.count <= FEW) {
-      // its tokens into every CTA's list, this CTA's behind those of the CTAs before it
-      uint32_t ahead = 0;
-      if (push) {
-        ahead = warp_sum(lane < (int)r.rank ? r.all[lane * BINS + b] : 0u);
-      } else if (r.C > 1) {
-        const uint32_t n = lane < (int)r.C ? from_peer(&s->count[b], lane) : 0;
-        ahead = warp_sum(lane < (int)r.rank ? n : 0u);
-      }
-      if (s->count[b])
+    // the bin's tokens in the CTAs before this one, and in this one
+    uint32_t ahead = 0;
+    if (r.C > 1) {
+      const uint32_t m = lane >= (int)r.C ? 0 : push ? r.all[lane * BINS + b] : from_peer(&s->hist[0][b], lane);
+      ahead = warp_sum(lane < (int)r.rank ? m : 0u);
+    }
+    const uint32_t own = s->hist[0][b];
+    if (n <= FEW) {
+      // into every CTA's list, this CTA's behind those of the CTAs before it
+      if (own)
         for (int i = r.w0; i < r.w1; i += CHUNK) {
           float x[4];
           r.four(i, x);
+          const float most = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+          if (!__any_sync(ALL, most >= least && (level > 0 || r.place(most) < (float)(b + 1)))) continue;
 #pragma unroll
           for (int e = 0; e < 4; e++) {
             const int index = r.first + i + lane * 4 + e;
-            if (!kept.has(x[e], index) || !inside(x[e]) || (int)place(x[e]) != b) continue;
+            if (!inside(x[e], index) || (int)bin(x[e]) != b) continue;
             const unsigned long long w = BY_MASS ? r.weight(x[e]) : 1;
             const Candidate* at = &s->few[ahead + atomicAdd(&s->filled, 1u)];
             for (uint32_t c = 0; c < r.C; c++)
@@ -420,11 +399,11 @@ __device__ __forceinline__ int narrow(const Row<T>& r, Kept& kept, unsigned long
       row_sync(r);
       // each token's sum of those before it; one of them is the last that is kept
       const uint32_t cand = threadIdx.x / 4;
-      const bool one = cand < hit.count;
+      const bool one = cand < n;
       const Candidate me = s->few[one ? cand : 0];
       unsigned long long sum = 0;
       if (one)
-        for (uint32_t k = threadIdx.x % 4; k < hit.count; k += 4) {
+        for (uint32_t k = threadIdx.x % 4; k < n; k += 4) {
           const Candidate o = s->few[k];
           if (o.key > me.key || (o.key == me.key && o.index < me.index)) sum += o.weight;
         }
@@ -434,54 +413,61 @@ __device__ __forceinline__ int narrow(const Row<T>& r, Kept& kept, unsigned long
         s->pick_key = me.key;
         s->pick_index = me.index;
       }
-      int lower = -1;
-      if (push) {
-        unsigned long long n;
-        (void)block_scan(mine < b ? ahead_of : 0, &n, s);
-        lower = (int)n + __syncthreads_count(one && threadIdx.x % 4 == 0 && sum < want && (int)me.index < r.first);
-      } else {
-        __syncthreads();
-      }
+      __syncthreads();
       kept.x = logit_of(s->pick_key);
       kept.index = (int)s->pick_index;
       __syncthreads();
-      return lower;
+      return;
     }
-    if (level == 0) {
-      b0 = (float)b;
-    } else {
-      kmin = hit.kmin;
-      kmax = hit.kmax;
-      if (kmin == kmax) {  // one key: its first `want` by index
-        if (BY_MASS) {
-          const unsigned long long w = hit.mass / hit.count;  // they weigh the same
-          want = w ? (want + w - 1) / w : hit.count;
+    // the range of the bin's keys, of this CTA and of the row
+    uint32_t lo = ALL, hi = 0;
+    for (int i = r.w0; i < r.w1; i += CHUNK) {
+      float x[4];
+      r.four(i, x);
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (inside(x[e], r.first + i + lane * 4 + e) && (int)bin(x[e]) == b) {
+          lo = min(lo, key_of(x[e]));
+          hi = max(hi, key_of(x[e]));
         }
-        const float x = logit_of(kmax);
-        int bound = x == kept.x ? kept.index : 0x7FFFFFFF;
-        if (want < hit.count) {  // the same in every CTA
-          uint32_t ahead = 0;
-          if (r.C > 1) {
-            const uint32_t n = lane < (int)r.C ? from_peer(&s->count[b], lane) : 0;
-            ahead = warp_sum(lane < (int)r.rank ? n : 0u);
-          }
-          const uint32_t own = s->count[b];
-          const uint32_t quota = want <= ahead ? 0 : want - ahead >= own ? own : (uint32_t)(want - ahead);
-          if (quota < own) bound = index_of(r, kept, x, quota);
-          row_sync(r);  // the counts have been read
-        }
-        kept = {x, bound};
-        return -1;
+    }
+    lo = __reduce_min_sync(ALL, lo), hi = __reduce_max_sync(ALL, hi);
+    if (lane == 0) s->warp_a[threadIdx.x >> 5] = lo, s->warp_b[threadIdx.x >> 5] = hi;
+    __syncthreads();
+    lo = __reduce_min_sync(ALL, lane < SAMPLE_WARPS ? s->warp_a[lane] : ALL);
+    hi = __reduce_max_sync(ALL, lane < SAMPLE_WARPS ? s->warp_b[lane] : 0);
+    if (r.C > 1) {
+      if (threadIdx.x < r.C) {
+        to_peer(&s->range[r.rank].x, threadIdx.x, lo);
+        to_peer(&s->range[r.rank].y, threadIdx.x, hi);
       }
-      sh = 0;
-      while (((kmax - kmin) >> sh) >= (uint32_t)BINS) sh++;
+      row_sync(r);
+      lo = __reduce_min_sync(ALL, lane < (int)r.C ? s->range[lane].x : ALL);
+      hi = __reduce_max_sync(ALL, lane < (int)r.C ? s->range[lane].y : 0);
     }
-    level++;
-    __syncthreads();  // pick and bins have been read
+    kmin = lo, kmax = hi;
+    if (kmin == kmax) {  // one key: its first `want` by index
+      if (BY_MASS) {
+        const unsigned long long w = s->pick_mass / n;  // they weigh the same
+        want = w ? (want + w - 1) / w : n;
+      }
+      const float x = logit_of(kmax);
+      int bound = x == kept.x ? kept.index : 0x7FFFFFFF;
+      if (want < n) {  // the same in every CTA
+        const uint32_t quota = want <= ahead ? 0 : want - ahead >= own ? own : (uint32_t)(want - ahead);
+        if (quota < own) bound = index_of(r, kept, x, quota);
+      }
+      kept = {x, bound};
+      __syncthreads();  // pick_index and pick_mass have been read
+      return;
+    }
+    sh = 0;
+    while (((kmax - kmin) >> sh) >= (uint32_t)BINS) sh++;
+    __syncthreads();  // pick has been read
   }
 }
 
-// Bytes of shared memory for all CTAs' counts, or the list of survivors after them.
+// Bytes of shared memory for all CTAs' histograms, or the list of survivors after them.
 __host__ __device__ constexpr size_t shared_counts(int C) {
   return C == 1 ? 0 : C * BINS * 4 > LIST * 8 ? (size_t)C * BINS * 4 : (size_t)LIST * 8;
 }
@@ -500,9 +486,10 @@ __device__ __forceinline__ void choose(const Row<T>& r, const Kept& kept, float 
     float v[4];
     r.four(i0, v);
     unsigned long long sum = 0;
+    w[0] = w[1] = w[2] = w[3] = 0;
+    if (!r.any(v, kept.x)) return sum;
 #pragma unroll
     for (int e = 0; e < 4; e++) {
-      w[e] = 0;
       if (kept.has(v[e], r.first + i0 + lane * 4 + e)) w[e] = r.weight(v[e]);
       if (w[e] < least) w[e] = 0;
       sum += w[e];
@@ -607,6 +594,21 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   }
   __syncwarp();
   // of the warp, the CTA, the row
+  // A logit that top_k tokens reach at least: of the row's warps with a full
+  // part, each with its 32 lanes' largest tokens, the least j-th largest,
+  // j * warps >= top_k.  (The other warps take none lower.)
+  const uint32_t full = (uint32_t)p.V / (uint32_t)(r.w1 - r.w0);
+  const uint32_t per_warp = top_k > 0 && full ? (top_k + full - 1) / full : 33;
+  float low = -INFINITY;
+  if (C > 1 && per_warp <= 32) low = INFINITY;
+  if (low > 0.f && r.w1 <= tokens) {
+    uint32_t key = key_of(mx), best = 0;
+    for (uint32_t j = 0; j < per_warp; j++) {
+      best = __reduce_max_sync(ALL, key);
+      if (lane == __ffs(__ballot_sync(ALL, key == best)) - 1) key = 0;
+    }
+    low = best ? logit_of(best) : -INFINITY;
+  }
   auto join = [&](float omx, float omn, uint32_t onan, uint32_t otop) {
     if (omx > mx || (omx == mx && otop < top)) mx = omx, top = otop;
     mn = fminf(mn, omn);
@@ -619,10 +621,19 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
            __shfl_xor_sync(ALL, top, o));
   };
   join_lanes();
-  if (lane == 0) s->warp_f[warp] = mx, s->warp_g[warp] = mn, s->warp_a[warp] = nan, s->warp_b[warp] = top;
+  if (lane == 0) {
+    s->warp_f[warp] = mx, s->warp_g[warp] = mn, s->warp_a[warp] = nan, s->warp_b[warp] = top;
+    s->warp_h[warp] = low;
+  }
   __syncthreads();
-  if (lane < SAMPLE_WARPS) mx = s->warp_f[lane], mn = s->warp_g[lane], nan = s->warp_a[lane], top = s->warp_b[lane];
+  const int from = lane % SAMPLE_WARPS;
+  mx = s->warp_f[from], mn = s->warp_g[from], nan = s->warp_a[from], top = s->warp_b[from], low = s->warp_h[from];
   join_lanes();
+  auto least_of_lanes = [&]() {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) low = fminf(low, __shfl_xor_sync(ALL, low, o));
+  };
+  least_of_lanes();
   if (C > 1) {
     cluster_wait();  // every CTA of the row has started
     if (threadIdx.x < C) {
@@ -631,13 +642,15 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
       to_peer(&at->mn, threadIdx.x, __float_as_uint(mn));
       to_peer(&at->nan, threadIdx.x, nan);
       to_peer(&at->first, threadIdx.x, top);
+      to_peer(&at->low, threadIdx.x, __float_as_uint(low));
     }
     row_sync(r);
     if (lane < C) {
       const Round o = s->peer[0][lane];
-      mx = o.mx, mn = o.mn, nan = o.nan, top = o.first;
+      mx = o.mx, mn = o.mn, nan = o.nan, top = o.first, low = o.low;
     }
     join_lanes();
+    least_of_lanes();
   }
   if (nan || mx == -INFINITY || !(temperature > 0.f)) {  // no token, or the largest
     const bool none = nan || mx == -INFINITY;
@@ -652,6 +665,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
     for (int i = r.w0 + lane; i < r.w1; i += 32) x[i] = to_float(x[i]) == INFINITY ? T(0.f) : T(-INFINITY);
     __syncwarp();
     mx = mn = 0.f;
+    low = -INFINITY;
   }
   r.mx = mx;
   // log2(e) / T as a pair of floats: the quotient of the leading part, and that
@@ -661,39 +675,50 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   r.cl = (fmaf(-r.ch, temperature, E_HI) + E_LO) / temperature;
   r.to_bin = mx - mn > 0.f ? fminf((float)(BINS - 1) / (mx - mn), 3e38f) : 0.f;
 
-  Kept kept = everything();
+  Kept kept = low > -INFINITY ? Kept{low, 0x7FFFFFFF} : everything();
   if (top_k > 0 && top_k < p.V) {
-    const int lower = narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
-    if (C > 1 && top_k <= LIST) {
-      // the survivors, in order of their index, into the first CTA's list
-      uint32_t n = 0;
+    // Where few tokens are left, the first CTA of the row goes on alone: with
+    // those that reach `low`, if they are few, else with those that top-k
+    // leaves.  Each pass over the slices costs less than an exchange.
+    bool settled = C == 1;  // kept is what top-k leaves
+    if (settled) narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
+    for (int round = low > -INFINITY ? 0 : 1; C > 1 && round < 2; round++) {
+      if (round == 1) {
+        if (top_k > LIST) {
+          narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
+          break;
+        }
+        narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
+        settled = true;
+      }
       auto survivors = [&](int i0, float (&v)[4]) -> uint32_t {  // a bit for each of a lane's four tokens
         r.four(i0, v);
         uint32_t m = 0;
+        if (!r.any(v, kept.x)) return m;
 #pragma unroll
         for (int e = 0; e < 4; e++) m |= (kept.has(v[e], r.first + i0 + lane * 4 + e) ? 1u : 0u) << e;
         return m;
       };
       float v[4];
+      uint32_t n = 0;
       for (int i = r.w0; i < r.w1; i += CHUNK) n += __popc(survivors(i, v));
       n = warp_sum(n);
+      __syncthreads();  // warp_a has been read
       if (lane == 0) s->warp_a[warp] = n;
       __syncthreads();
       const uint32_t theirs = lane < SAMPLE_WARPS ? s->warp_a[lane] : 0;
       uint32_t at = warp_sum(lane < warp ? theirs : 0u);
       const uint32_t cta = warp_sum(theirs);
-      uint32_t all_n = (uint32_t)top_k;
-      if (lower >= 0) {  // exactly top_k survive
-        at += lower;
-      } else {
-        if (threadIdx.x < C) to_peer(&s->peer[1][r.rank].first, threadIdx.x, cta);
-        row_sync(r);
-        const uint32_t others = lane < C ? s->peer[1][lane].first : 0;
-        at += warp_sum(lane < (int)r.rank ? others : 0u);
-        all_n = warp_sum(others);
-      }
-      // up to 512: one per lane, in the first of its four places
-      const int spread = all_n <= SAMPLE_THREADS ? 4 : 1;
+      if (threadIdx.x < C) to_peer(&s->peer[round][r.rank].count, threadIdx.x, cta);
+      row_sync(r);
+      const uint32_t others = lane < C ? s->peer[round][lane].count : 0;
+      at += warp_sum(lane < (int)r.rank ? others : 0u);
+      const uint32_t left = warp_sum(others);
+      if (left > LIST) continue;
+      // in order of their index; fewer than half a lane's four places each
+      // leave gaps, so that all warps have their share
+      int spread = 1;
+      while (spread < 4 && left * spread * 2 <= CHUNK * SAMPLE_WARPS) spread *= 2;
       if (n)
         for (int i = r.w0; i < r.w1; i += CHUNK) {
           const uint32_t m = survivors(i, v);
@@ -716,19 +741,21 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
         }
       row_sync(r);
       if (r.rank) return;
-      for (uint32_t i = threadIdx.x; i < LIST; i += SAMPLE_THREADS)
-        if (i % spread || i / spread >= all_n) list_x[i] = -INFINITY;
-      __syncthreads();
       Row<float> one;
       one.x = list_x;
       one.s = s;
+      one.all = nullptr;
       one.C = 1;
       one.rank = 0;
       one.first = 0;
-      one.part(LIST);
-      one.all = nullptr;
+      one.part((int)left * spread);
       one.mx = r.mx, one.ch = r.ch, one.cl = r.cl, one.to_bin = r.to_bin;
+      const int room = (one.w1 - one.w0) * SAMPLE_WARPS;
+      for (int i = threadIdx.x; i < room; i += SAMPLE_THREADS)
+        if (i % spread || i >= (int)left * spread) list_x[i] = -INFINITY;
+      __syncthreads();
       kept = everything();
+      if (!settled) narrow<false>(one, kept, (unsigned long long)top_k, 0.f);
       if (top_p < 1.f) narrow<true>(one, kept, 0, fmaxf(top_p, 0.f));
       choose(one, kept, min_p, u, list_index, p.token + row, p.prob ? p.prob + row : nullptr);
       return;
@@ -737,6 +764,9 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   if (top_p < 1.f) narrow<true>(r, kept, 0, fmaxf(top_p, 0.f));
   choose(r, kept, min_p, u, nullptr, p.token + row, p.prob ? p.prob + row : nullptr);
 }
+
+constexpr size_t SAMPLE_SMEM = 220 * 1024;
+static_assert(sizeof(SampleShared) + shared_counts(MAX_C) + QLIN_SAMPLE_MAX_V / MAX_C * 4 <= SAMPLE_SMEM, "largest slice");
 
 const void* sample_fn(int dtype) {
   return dtype == QLIN_F32 ? reinterpret_cast<const void*>(qlin_sample_kernel<float>)
@@ -763,7 +793,7 @@ qlin_status sample_setup() {
   if (dev < 0 || dev >= 64) return QLIN_ERR_CUDA;
   std::call_once(g_sample_once[dev], [dev] {
     for (int dtype : {QLIN_F32, QLIN_BF16}) {
-      cudaError_t e = cudaFuncSetAttribute(sample_fn(dtype), cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+      cudaError_t e = cudaFuncSetAttribute(sample_fn(dtype), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SAMPLE_SMEM);
       if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_fn(dtype), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       g_sample_ready[dev] = status_of(e);
       if (e != cudaSuccess) return;
