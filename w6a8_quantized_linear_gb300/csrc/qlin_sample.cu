@@ -23,7 +23,7 @@ constexpr int BINS = SAMPLE_THREADS;     // one per thread in the scans
 constexpr int MAX_C = 16;                // CTAs of a row's cluster, at most
 constexpr int CHUNK = 128;               // consecutive tokens that a warp takes at once, four per lane
 constexpr int FEW = 128;                 // a bin of at most this many tokens is settled by comparing all pairs, four threads each
-constexpr int LIST = 4096;               // so many tokens, what top-k may leave, are carried on by one CTA
+constexpr int LIST = 2048;               // so many tokens, what top-k may leave, are carried on by one CTA
 constexpr int ONE_BITS = 42;             // weights are multiples of 2^-42; 2^19 of them sum below 2^62
 constexpr uint32_t ALL = 0xFFFFFFFFu;
 
@@ -46,8 +46,7 @@ struct SampleParams {
 };
 
 struct Round {  // what the CTAs of a row tell each other outside the histograms
-  float mx, mn, low;
-  uint32_t nan, first, count;
+  uint32_t kmx, kmn, klow, nan, top, pad;
   unsigned long long sum;
 };
 struct __align__(16) Candidate {
@@ -60,11 +59,10 @@ struct SampleShared {
   unsigned long long mass[BINS];         // the row's
   uint32_t count[BINS];
   Candidate few[FEW];
-  Round peer[3][MAX_C];  // [0]: also the first of two counts of survivors
+  Round peer[2][MAX_C];
   uint2 range[MAX_C];
   unsigned long long warp_sum[SAMPLE_WARPS];
-  uint32_t warp_a[SAMPLE_WARPS], warp_b[SAMPLE_WARPS];
-  float warp_f[SAMPLE_WARPS], warp_g[SAMPLE_WARPS], warp_h[SAMPLE_WARPS];
+  uint32_t warp_a[SAMPLE_WARPS], warp_b[SAMPLE_WARPS], warp_c[SAMPLE_WARPS], warp_d[SAMPLE_WARPS], warp_e[SAMPLE_WARPS];
   uint32_t table[32];  // 2^(i/32) in [2^31, 2^32)
   int pick;
   uint32_t pick_key, pick_index, pick_count, filled;
@@ -145,9 +143,10 @@ __device__ __forceinline__ Kept everything() { return {-INFINITY, -1}; }
 
 // The tokens that a CTA works on: a slice of the row in shared memory, or (one
 // CTA) the survivors of top-k; filled up with -inf to whole chunks per warp.
-template <typename T>
+template <typename T, int CHUNKS>
 struct Row {
   const T* x;
+  float top[CHUNKS];  // the largest of this lane's four tokens in each of its warp's chunks
   int w0, w1;        // this warp's contiguous part
   int first;         // index of the slice's first token
   float mx, ch, cl, to_bin;
@@ -172,9 +171,24 @@ struct Row {
       v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
     }
   }
-  // Whether any of the warp's tokens in a chunk may survive.
-  __device__ __forceinline__ bool any(const float (&v)[4], float least) const {
-    return __any_sync(0xFFFFFFFFu, fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) >= least);
+  __device__ __forceinline__ void tops() {
+#pragma unroll
+    for (int c = 0; c < CHUNKS; c++) {
+      top[c] = -INFINITY;
+      if (w0 + c * CHUNK < w1) {
+        float v[4];
+        four(w0 + c * CHUNK, v);
+        top[c] = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+      }
+    }
+  }
+  // The warp's chunks in which some token reaches `least`, as bits: most
+  // passes look for a few tokens and read only these.
+  __device__ __forceinline__ uint32_t chunks(float least) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; c++) m |= (__any_sync(0xFFFFFFFFu, top[c] >= least) ? 1u : 0u) << c;
+    return m & ((2u << ((w1 - w0) / CHUNK - 1)) - 1);
   }
   // Place among the row's BINS equal parts of its logits' range, largest
   // first, whole bins as integers: it falls with x, the same in every use.
@@ -188,8 +202,8 @@ __device__ __forceinline__ T warp_sum(T v) {
   return v;
 }
 
-template <typename T>
-__device__ __forceinline__ void row_sync(const Row<T>& r) {
+template <typename R>
+__device__ __forceinline__ void row_sync(const R& r) {
   if (r.C == 1) {
     __syncthreads();
   } else {
@@ -231,8 +245,8 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
 
 // The row index of the quota-th token (from 1) with this logit among the
 // survivors of this CTA; -1 for none.  All threads of the CTA.
-template <typename T>
-__device__ __forceinline__ int index_of(const Row<T>& r, const Kept& kept, float x, uint32_t quota) {
+template <typename R>
+__device__ __forceinline__ int index_of(const R& r, const Kept& kept, float x, uint32_t quota) {
   if (quota == 0) return -1;
   SampleShared* s = r.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -240,20 +254,21 @@ __device__ __forceinline__ int index_of(const Row<T>& r, const Kept& kept, float
     float v[4];
     r.four(i0, v);
     uint32_t m = 0;
-    if (!r.any(v, x)) return m;
 #pragma unroll
     for (int e = 0; e < 4; e++) m |= (v[e] == x && kept.has(v[e], r.first + i0 + lane * 4 + e) ? 1u : 0u) << e;
     return m;
   };
   uint32_t n = 0;
-  for (int i = r.w0; i < r.w1; i += CHUNK) n += __popc(hits(i));
+  const uint32_t chunks = r.chunks(x);
+  for (uint32_t m = chunks; m; m &= m - 1) n += __popc(hits(r.w0 + (__ffs(m) - 1) * CHUNK));
   n = warp_sum(n);
   if (lane == 0) s->warp_a[warp] = n;
   __syncthreads();
   uint32_t before = 0;
   for (int w = 0; w < warp; w++) before += s->warp_a[w];
   if (before < quota && quota <= before + n) {
-    for (int i = r.w0; i < r.w1 && before < quota; i += CHUNK) {
+    for (uint32_t k = chunks; k && before < quota; k &= k - 1) {
+      const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
       const uint32_t m = hits(i), c = __popc(m);
       uint32_t inc = c;
 #pragma unroll
@@ -270,6 +285,19 @@ __device__ __forceinline__ int index_of(const Row<T>& r, const Kept& kept, float
   return (int)s->pick_index;
 }
 
+// This CTA's counts to all CTAs of the row.
+template <typename R>
+__device__ __forceinline__ void push_counts(const R& r) {
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < r.C * (BINS / 4); i += SAMPLE_THREADS) {
+    const uint32_t c = i / (BINS / 4), q = i % (BINS / 4) * 4;
+    const uint4 x = *reinterpret_cast<const uint4*>(&r.s->hist[0][q]);
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dsmem_addr(r.all + r.rank * BINS + q, c)),
+                 "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                 : "memory");
+  }
+}
+
 // The shortest beginning of the survivors' order whose count (BY_MASS false)
 // reaches `want`, or whose mass reaches the share top_p of theirs; `kept` is
 // narrowed to it.  All CTAs of the row take part.  Each level costs one
@@ -277,8 +305,8 @@ __device__ __forceinline__ int index_of(const Row<T>& r, const Kept& kept, float
 // (joined by shares of the bins: three times the bytes make the push slower
 // than a second exchange, 5.7 against 3.9 us with 16 CTAs); the few tokens of
 // the bin in which the border lies take one more.
-template <bool BY_MASS, typename T>
-__device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned long long want, float top_p) {
+template <bool BY_MASS, typename R>
+__device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long long want, float top_p) {
   SampleShared* s = r.s;
   const int lane = threadIdx.x & 31, mine = threadIdx.x;
   int sh = 0;
@@ -294,10 +322,11 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
     s->hist[0][mine] = s->hist[1][mine] = s->hist[2][mine] = 0;
     if (threadIdx.x == 0) s->filled = 0;
     __syncthreads();
-    for (int i = r.w0; i < r.w1; i += CHUNK) {
+    const uint32_t chunks = r.chunks(least);
+    for (uint32_t k = chunks; k; k &= k - 1) {
+      const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
       float x[4];
       r.four(i, x);
-      if (!r.any(x, least)) continue;
       uint32_t m = 0;
 #pragma unroll
       for (int e = 0; e < 4; e++) m |= (inside(x[e], r.first + i + lane * 4 + e) ? 1u : 0u) << e;
@@ -314,16 +343,7 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
         }
       }
     }
-    if (push) {
-      __syncthreads();
-      for (uint32_t i = threadIdx.x; i < r.C * (BINS / 4); i += SAMPLE_THREADS) {
-        const uint32_t c = i / (BINS / 4), q = i % (BINS / 4) * 4;
-        const uint4 x = *reinterpret_cast<const uint4*>(&s->hist[0][q]);
-        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dsmem_addr(r.all + r.rank * BINS + q, c)),
-                     "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                     : "memory");
-      }
-    }
+    if (push) push_counts(r);
     row_sync(r);  // every CTA's histogram is complete
     uint32_t count = 0;
     unsigned long long mass = 0;
@@ -379,7 +399,8 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
     if (n <= FEW) {
       // into every CTA's list, this CTA's behind those of the CTAs before it
       if (own)
-        for (int i = r.w0; i < r.w1; i += CHUNK) {
+        for (uint32_t k = chunks; k; k &= k - 1) {
+          const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
           float x[4];
           r.four(i, x);
           const float most = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
@@ -421,7 +442,8 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
     }
     // the range of the bin's keys, of this CTA and of the row
     uint32_t lo = ALL, hi = 0;
-    for (int i = r.w0; i < r.w1; i += CHUNK) {
+    for (uint32_t k = chunks; k; k &= k - 1) {
+      const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
       float x[4];
       r.four(i, x);
 #pragma unroll
@@ -467,16 +489,14 @@ __device__ __forceinline__ void narrow(const Row<T>& r, Kept& kept, unsigned lon
   }
 }
 
-// Bytes of shared memory for all CTAs' histograms, or the list of survivors after them.
-__host__ __device__ constexpr size_t shared_counts(int C) {
-  return C == 1 ? 0 : C * BINS * 4 > LIST * 8 ? (size_t)C * BINS * 4 : (size_t)LIST * 8;
-}
+// Bytes of shared memory for all CTAs' counts and the list of survivors.
+__host__ __device__ constexpr size_t shared_counts(int C) { return C == 1 ? 0 : (size_t)C * BINS * 4 + LIST * 8; }
 
 // The first kept token, in order of the index, at which the running sum of
 // the kept weights exceeds u times their sum.  `index`: the tokens' places in
 // the row where they are not first + i.
-template <typename T>
-__device__ __forceinline__ void choose(const Row<T>& r, const Kept& kept, float min_p, float u, const uint32_t* index,
+template <typename R>
+__device__ __forceinline__ void choose(const R& r, const Kept& kept, float min_p, float u, const uint32_t* index,
                                        int32_t* token, float* prob) {
   SampleShared* s = r.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -487,7 +507,6 @@ __device__ __forceinline__ void choose(const Row<T>& r, const Kept& kept, float 
     r.four(i0, v);
     unsigned long long sum = 0;
     w[0] = w[1] = w[2] = w[3] = 0;
-    if (!r.any(v, kept.x)) return sum;
 #pragma unroll
     for (int e = 0; e < 4; e++) {
       if (kept.has(v[e], r.first + i0 + lane * 4 + e)) w[e] = r.weight(v[e]);
@@ -498,7 +517,8 @@ __device__ __forceinline__ void choose(const Row<T>& r, const Kept& kept, float 
   };
   // the kept mass of each warp's tokens, of the CTAs, of the row
   unsigned long long mine = 0, w[4];
-  for (int i = r.w0; i < r.w1; i += CHUNK) mine += weights(i, w);
+  const uint32_t chunks = r.chunks(kept.x);
+  for (uint32_t k = chunks; k; k &= k - 1) mine += weights(r.w0 + (__ffs(k) - 1) * CHUNK, w);
   mine = warp_sum(mine);
   __syncthreads();  // warp_sum has been read
   if (lane == 0) s->warp_sum[warp] = mine;
@@ -507,16 +527,17 @@ __device__ __forceinline__ void choose(const Row<T>& r, const Kept& kept, float 
   unsigned long long before = warp_sum(lane < warp ? theirs : 0ull);
   unsigned long long total = warp_sum(theirs);
   if (r.C > 1) {
-    if (threadIdx.x < r.C) to_peer(&s->peer[2][r.rank].sum, threadIdx.x, total);
+    if (threadIdx.x < r.C) to_peer(&s->peer[1][r.rank].sum, threadIdx.x, total);
     row_sync(r);
-    const unsigned long long v = lane < (int)r.C ? s->peer[2][lane].sum : 0;
+    const unsigned long long v = lane < (int)r.C ? s->peer[1][lane].sum : 0;
     before += warp_sum(lane < (int)r.rank ? v : 0ull);
     total = warp_sum(v);
   }
   unsigned long long target = u > 0.f ? share_of<false>(total, fminf(u, 1.f)) + 1 : 1;
   if (target > total) target = total;
   if (!(before < target && target <= before + mine)) return;
-  for (int i0 = r.w0; i0 < r.w1 && before < target; i0 += CHUNK) {
+  for (uint32_t k = chunks; k && before < target; k &= k - 1) {
+    const int i0 = r.w0 + (__ffs(k) - 1) * CHUNK;
     const unsigned long long sum = weights(i0, w);
     unsigned long long inc = sum;
 #pragma unroll
@@ -548,13 +569,11 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   extern __shared__ __align__(16) uint8_t raw[];
   SampleShared* s = reinterpret_cast<SampleShared*>(raw);
   uint32_t* all = reinterpret_cast<uint32_t*>(raw + sizeof(SampleShared));
-  // the list of survivors takes the place of the counts: those have been read
-  // when the exchange before it ends
-  float* list_x = reinterpret_cast<float*>(all);
-  uint32_t* list_index = all + LIST;
+  float* list_x = reinterpret_cast<float*>(all + C * BINS);
+  uint32_t* list_index = reinterpret_cast<uint32_t*>(list_x + LIST);
   T* x = reinterpret_cast<T*>(raw + sizeof(SampleShared) + shared_counts(C));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Row<T> r;
+  Row<T, 16> r;  // 32768 tokens of a slice at most
   r.x = x;
   r.s = s;
   r.all = all;
@@ -593,65 +612,59 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
     }
   }
   __syncwarp();
-  // of the warp, the CTA, the row
+  r.tops();
+  // of the warp, the CTA, the row, as keys; the index of the largest
+  uint32_t kmx = key_of(mx), kmn = key_of(mn);
+  auto join = [&](bool in) {
+    const uint32_t best = __reduce_max_sync(ALL, in ? kmx : 0);
+    top = __reduce_min_sync(ALL, in && kmx == best ? top : ALL);
+    kmx = best;
+    kmn = __reduce_min_sync(ALL, in ? kmn : ALL);
+    nan = __any_sync(ALL, in && nan);
+  };
   // A logit that top_k tokens reach at least: of the row's warps with a full
   // part, each with its 32 lanes' largest tokens, the least j-th largest,
   // j * warps >= top_k.  (The other warps take none lower.)
   const uint32_t full = (uint32_t)p.V / (uint32_t)(r.w1 - r.w0);
   const uint32_t per_warp = top_k > 0 && full ? (top_k + full - 1) / full : 33;
-  float low = -INFINITY;
-  if (C > 1 && per_warp <= 32) low = INFINITY;
-  if (low > 0.f && r.w1 <= tokens) {
-    uint32_t key = key_of(mx), best = 0;
+  uint32_t klow = C > 1 && per_warp <= 32 ? ALL : 0;
+  if (klow && r.w1 <= tokens) {
+    uint32_t key = kmx;
     for (uint32_t j = 0; j < per_warp; j++) {
-      best = __reduce_max_sync(ALL, key);
-      if (lane == __ffs(__ballot_sync(ALL, key == best)) - 1) key = 0;
+      klow = __reduce_max_sync(ALL, key);
+      if (lane == __ffs(__ballot_sync(ALL, key == klow)) - 1) key = 0;
     }
-    low = best ? logit_of(best) : -INFINITY;
   }
-  auto join = [&](float omx, float omn, uint32_t onan, uint32_t otop) {
-    if (omx > mx || (omx == mx && otop < top)) mx = omx, top = otop;
-    mn = fminf(mn, omn);
-    nan |= onan;
-  };
-  auto join_lanes = [&]() {
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-      join(__shfl_xor_sync(ALL, mx, o), __shfl_xor_sync(ALL, mn, o), __shfl_xor_sync(ALL, nan, o),
-           __shfl_xor_sync(ALL, top, o));
-  };
-  join_lanes();
+  join(true);
   if (lane == 0) {
-    s->warp_f[warp] = mx, s->warp_g[warp] = mn, s->warp_a[warp] = nan, s->warp_b[warp] = top;
-    s->warp_h[warp] = low;
+    s->warp_a[warp] = nan, s->warp_b[warp] = top, s->warp_c[warp] = kmx, s->warp_d[warp] = kmn;
+    s->warp_e[warp] = klow;
   }
   __syncthreads();
   const int from = lane % SAMPLE_WARPS;
-  mx = s->warp_f[from], mn = s->warp_g[from], nan = s->warp_a[from], top = s->warp_b[from], low = s->warp_h[from];
-  join_lanes();
-  auto least_of_lanes = [&]() {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) low = fminf(low, __shfl_xor_sync(ALL, low, o));
-  };
-  least_of_lanes();
+  nan = s->warp_a[from], top = s->warp_b[from], kmx = s->warp_c[from], kmn = s->warp_d[from];
+  klow = __reduce_min_sync(ALL, s->warp_e[from]);
+  join(true);
   if (C > 1) {
     cluster_wait();  // every CTA of the row has started
     if (threadIdx.x < C) {
       const Round* at = &s->peer[0][r.rank];
-      to_peer(&at->mx, threadIdx.x, __float_as_uint(mx));
-      to_peer(&at->mn, threadIdx.x, __float_as_uint(mn));
+      to_peer(&at->kmx, threadIdx.x, kmx);
+      to_peer(&at->kmn, threadIdx.x, kmn);
+      to_peer(&at->klow, threadIdx.x, klow);
       to_peer(&at->nan, threadIdx.x, nan);
-      to_peer(&at->first, threadIdx.x, top);
-      to_peer(&at->low, threadIdx.x, __float_as_uint(low));
+      to_peer(&at->top, threadIdx.x, top);
     }
     row_sync(r);
     if (lane < C) {
       const Round o = s->peer[0][lane];
-      mx = o.mx, mn = o.mn, nan = o.nan, top = o.first, low = o.low;
+      kmx = o.kmx, kmn = o.kmn, nan = o.nan, top = o.top, klow = o.klow;
     }
-    join_lanes();
-    least_of_lanes();
+    join(lane < C);
+    klow = __reduce_min_sync(ALL, klow);
   }
+  mx = logit_of(kmx), mn = logit_of(kmn);
+  float low = klow == 0 || klow == ALL ? -INFINITY : logit_of(klow);
   if (nan || mx == -INFINITY || !(temperature > 0.f)) {  // no token, or the largest
     const bool none = nan || mx == -INFINITY;
     if (r.rank == 0 && threadIdx.x == 0) {
@@ -664,6 +677,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
     __syncwarp();
     for (int i = r.w0 + lane; i < r.w1; i += 32) x[i] = to_float(x[i]) == INFINITY ? T(0.f) : T(-INFINITY);
     __syncwarp();
+    r.tops();
     mx = mn = 0.f;
     low = -INFINITY;
   }
@@ -677,52 +691,74 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
 
   Kept kept = low > -INFINITY ? Kept{low, 0x7FFFFFFF} : everything();
   if (top_k > 0 && top_k < p.V) {
-    // Where few tokens are left, the first CTA of the row goes on alone: with
-    // those that reach `low`, if they are few, else with those that top-k
-    // leaves.  Each pass over the slices costs less than an exchange.
-    bool settled = C == 1;  // kept is what top-k leaves
-    if (settled) narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
-    for (int round = low > -INFINITY ? 0 : 1; C > 1 && round < 2; round++) {
-      if (round == 1) {
-        if (top_k > LIST) {
-          narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
-          break;
-        }
-        narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
-        settled = true;
-      }
-      auto survivors = [&](int i0, float (&v)[4]) -> uint32_t {  // a bit for each of a lane's four tokens
-        r.four(i0, v);
-        uint32_t m = 0;
-        if (!r.any(v, kept.x)) return m;
-#pragma unroll
-        for (int e = 0; e < 4; e++) m |= (kept.has(v[e], r.first + i0 + lane * 4 + e) ? 1u : 0u) << e;
-        return m;
-      };
-      float v[4];
-      uint32_t n = 0;
-      for (int i = r.w0; i < r.w1; i += CHUNK) n += __popc(survivors(i, v));
-      n = warp_sum(n);
-      __syncthreads();  // warp_a has been read
-      if (lane == 0) s->warp_a[warp] = n;
+    if (C > 1 && top_k <= LIST / 2) {
+      // The bins down to the one in which top-k ends hold little more than
+      // top_k tokens: if few, the first CTA of the row goes on alone with
+      // them.  (An exchange between the CTAs costs more than a pass over a
+      // list.)  The bins divide what lies above `low`.
+      if (low > -INFINITY) r.to_bin = mx - low > 0.f ? fminf((float)(BINS - 1) / (mx - low), 3e38f) : 0.f;
+      const int mine = threadIdx.x;
+      s->hist[0][mine] = 0;
       __syncthreads();
-      const uint32_t theirs = lane < SAMPLE_WARPS ? s->warp_a[lane] : 0;
-      uint32_t at = warp_sum(lane < warp ? theirs : 0u);
-      const uint32_t cta = warp_sum(theirs);
-      if (threadIdx.x < C) to_peer(&s->peer[round][r.rank].count, threadIdx.x, cta);
+      const uint32_t chunks = r.chunks(kept.x);
+      for (uint32_t k = chunks; k; k &= k - 1) {
+        const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
+        float v[4];
+        r.four(i, v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 4; e++) m |= (kept.has(v[e], r.first + i + lane * 4 + e) ? 1u : 0u) << e;
+        for (; m; m &= m - 1) atomicAdd(&s->hist[0][(int)r.place(m & 1 ? v[0] : m & 2 ? v[1] : m & 4 ? v[2] : v[3])], 1u);
+      }
+      push_counts(r);
       row_sync(r);
-      const uint32_t others = lane < C ? s->peer[round][lane].count : 0;
-      at += warp_sum(lane < (int)r.rank ? others : 0u);
-      const uint32_t left = warp_sum(others);
-      if (left > LIST) continue;
-      // in order of their index; fewer than half a lane's four places each
-      // leave gaps, so that all warps have their share
-      int spread = 1;
-      while (spread < 4 && left * spread * 2 <= CHUNK * SAMPLE_WARPS) spread *= 2;
-      if (n)
-        for (int i = r.w0; i < r.w1; i += CHUNK) {
+      uint32_t count = 0, ahead = 0;  // tokens of this thread's bin, and of those in the CTAs before this one
+      for (uint32_t c = 0; c < r.C; c++) {
+        const uint32_t m = all[c * BINS + mine];
+        count += m;
+        if (c < r.rank) ahead += m;
+      }
+      unsigned long long total, sum;
+      const unsigned long long before = block_scan(count, &total, s);
+      if (threadIdx.x == 0) s->pick = BINS - 1, s->pick_count = (uint32_t)total;  // fewer than top_k in all
+      __syncthreads();
+      if (before < (uint32_t)top_k && (uint32_t)top_k <= before + count) {
+        s->pick = mine;
+        s->pick_count = (uint32_t)before + count;
+      }
+      __syncthreads();
+      const int last = s->pick;
+      const uint32_t left = s->pick_count;
+      (void)block_scan(mine <= last ? ahead : 0, &sum, s);
+      if (left <= LIST) {
+        // in order of their index; fewer than half a lane's four places each
+        // leave gaps, so that all warps have their share
+        int spread = 1;
+        while (spread < 4 && left * spread * 2 <= CHUNK * SAMPLE_WARPS) spread *= 2;
+        auto survivors = [&](int i, float (&v)[4]) -> uint32_t {  // a bit for each of a lane's four tokens
+          r.four(i, v);
+          uint32_t m = 0;
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            m |= (kept.has(v[e], r.first + i + lane * 4 + e) && r.place(v[e]) < (float)(last + 1) ? 1u : 0u) << e;
+          return m;
+        };
+        float v[4];
+        uint32_t n = 0, ours = 0;  // tokens of this warp; the chunks that hold them
+        // (mx - v) to_bin < last + 1 leaves v above this, whatever rounds
+        const float edge = mx - ((float)last + 1.5f) / r.to_bin - fabsf(mx) * 0x1p-22f;
+        for (uint32_t k = r.chunks(fmaxf(edge, kept.x)); k; k &= k - 1) {
+          const uint32_t m = survivors(r.w0 + (__ffs(k) - 1) * CHUNK, v);
+          n += __popc(m);
+          if (__any_sync(ALL, m)) ours |= k & (0u - k);
+        }
+        n = warp_sum(n);
+        if (lane == 0) s->warp_a[warp] = n;
+        __syncthreads();
+        uint32_t at = (uint32_t)sum + warp_sum(lane < warp ? s->warp_a[lane] : 0u);
+        for (uint32_t k = ours; k; k &= k - 1) {
+          const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
           const uint32_t m = survivors(i, v);
-          if (!__any_sync(ALL, m)) continue;
           uint32_t inc = __popc(m);
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -739,27 +775,31 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
             }
           at += __shfl_sync(ALL, inc, 31);
         }
-      row_sync(r);
-      if (r.rank) return;
-      Row<float> one;
-      one.x = list_x;
-      one.s = s;
-      one.all = nullptr;
-      one.C = 1;
-      one.rank = 0;
-      one.first = 0;
-      one.part((int)left * spread);
-      one.mx = r.mx, one.ch = r.ch, one.cl = r.cl, one.to_bin = r.to_bin;
-      const int room = (one.w1 - one.w0) * SAMPLE_WARPS;
-      for (int i = threadIdx.x; i < room; i += SAMPLE_THREADS)
-        if (i % spread || i >= (int)left * spread) list_x[i] = -INFINITY;
-      __syncthreads();
-      kept = everything();
-      if (!settled) narrow<false>(one, kept, (unsigned long long)top_k, 0.f);
-      if (top_p < 1.f) narrow<true>(one, kept, 0, fmaxf(top_p, 0.f));
-      choose(one, kept, min_p, u, list_index, p.token + row, p.prob ? p.prob + row : nullptr);
-      return;
+        row_sync(r);
+        if (r.rank) return;
+        Row<float, LIST / (CHUNK * SAMPLE_WARPS)> one;
+        one.x = list_x;
+        one.s = s;
+        one.all = nullptr;
+        one.C = 1;
+        one.rank = 0;
+        one.first = 0;
+        one.part((int)left * spread);
+        one.mx = r.mx, one.ch = r.ch, one.cl = r.cl, one.to_bin = r.to_bin;
+        const int room = (one.w1 - one.w0) * SAMPLE_WARPS;
+        for (int i = threadIdx.x; i < room; i += SAMPLE_THREADS)
+          if (i % spread || i >= (int)left * spread) list_x[i] = -INFINITY;
+        __syncthreads();
+        one.tops();
+        kept = everything();
+        if (left > (uint32_t)top_k) narrow<false>(one, kept, (unsigned long long)top_k, 0.f);
+        if (top_p < 1.f) narrow<true>(one, kept, 0, fmaxf(top_p, 0.f));
+        choose(one, kept, min_p, u, list_index, p.token + row, p.prob ? p.prob + row : nullptr);
+        return;
+      }
+      row_sync(r);  // the counts have been read
     }
+    narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
   }
   if (top_p < 1.f) narrow<true>(r, kept, 0, fmaxf(top_p, 0.f));
   choose(r, kept, min_p, u, nullptr, p.token + row, p.prob ? p.prob + row : nullptr);
