@@ -21,7 +21,7 @@ struct AppendParams {
   uint32_t* status;
   float eps;
   int Hq, n_turns, pairs;
-  int first, heads;      // the head rows of a token that this launch works on: first .. first + heads - 1 of q, k, v
+  int heads;  // head rows of a token: of q, k and v
   int heads_per_block;
 };
 
@@ -75,21 +75,38 @@ __device__ __forceinline__ void store_row(const HeadRow<D>& r, DST* p, int lane)
   }
 }
 
-// One block per token row and run of heads, one warp per head at a time.
+// One block per token row and run of heads, one warp per head, two or four
+// heads of a warp in flight.
 //   x' = x gamma / sqrt(mean(x^2) + eps);  (a, b) -> (a cos - b sin, b cos + a sin)
 // The angle is pos * turns[i] mod 1, exact in 64-bit integers whatever the
 // position, so only its last conversion to fp32 rounds.  Bound by the bytes of
-// the rows (6 to 4 per element) for a prompt, by the launch for a step.
+// the rows (6 or 4 per element) for a prompt, by the launch for a step.
 template <typename SRC, typename DST, int D>
 __global__ void __launch_bounds__(APPEND_WARPS * 32) qlin_append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ float2 cs[D / 2];                     // cos, sin of this row's angles
   __shared__ float rows[APPEND_WARPS][D];
+  constexpr int AHEAD = D == 256 ? 2 : 4;
   const int row = blockIdx.x, b = row / p.step.T, t = row - b * p.step.T;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_launch_dependents();
   const int len = p.step.len[b];
   if (len < 0 || t >= step_rows(p.step, b)) return;
+  const int h0 = blockIdx.y * p.heads_per_block + warp;
+  const int h1 = min((int)(blockIdx.y + 1) * p.heads_per_block, p.heads);
+  // the heads of a token: of q, then of k, then of v
+  auto load = [&](HeadRow<D>& x, int head) {
+    const int hk = head - p.Hq;
+    const SRC* src = hk < 0 ? static_cast<const SRC*>(p.q) + row * p.q_stride + (int64_t)head * D
+                     : hk < p.cache.heads
+                         ? static_cast<const SRC*>(p.k) + row * p.k_stride + (int64_t)hk * D
+                         : static_cast<const SRC*>(p.v) + row * p.v_stride + (int64_t)(hk - p.cache.heads) * D;
+    load_row<D>(x, src, lane);
+  };
+  HeadRow<D> x[AHEAD];
+#pragma unroll
+  for (int u = 0; u < AHEAD; u++)
+    if (h0 + u * APPEND_WARPS < h1) load(x[u], h0 + u * APPEND_WARPS);
   const int depth = p.step.depth ? p.step.depth[b * p.step.tree_stride + t] : t;
   const int64_t pos = (int64_t)len + depth;
   for (int i = threadIdx.x; i < p.n_turns; i += APPEND_WARPS * 32) {
@@ -101,20 +118,14 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) qlin_append_kernel(const __
   const int64_t at = p.k ? token_offset(p.cache, p.step, b, (int64_t)len + t) : 0;
   if (at < 0 && threadIdx.x == 0) report(p.status, QLIN_ERR_BAD_INDEX);
   __syncthreads();
-  const int h0 = blockIdx.y * p.heads_per_block;
-  const int h1 = min(h0 + p.heads_per_block, p.heads);
-  for (int h = h0 + warp; h < h1; h += APPEND_WARPS) {
-    const int head = p.first + h;  // q heads, then k heads, then v heads
-    const bool is_q = head < p.Hq, is_v = head >= p.Hq + p.cache.heads;
-    const int hk = is_v ? head - p.Hq - p.cache.heads : head - p.Hq;
-    const SRC* src = is_q   ? static_cast<const SRC*>(p.q) + row * p.q_stride + (int64_t)head * D
-                     : is_v ? static_cast<const SRC*>(p.v) + row * p.v_stride + (int64_t)hk * D
-                            : static_cast<const SRC*>(p.k) + row * p.k_stride + (int64_t)hk * D;
-    HeadRow<D> x;
-    load_row<D>(x, src, lane);
+  auto finish = [&](HeadRow<D>& x, int head) {
+    const int hk = head - p.Hq;
+    const bool is_q = hk < 0, is_v = hk >= p.cache.heads;
     if (!is_v) {
       const float* gamma = is_q ? p.q_gamma : p.k_gamma;
       if (gamma) {
+        HeadRow<D> g;
+        load_row<D>(g, gamma, lane);
         float ss = 0.f;
 #pragma unroll
         for (int c = 0; c < x.NC; c++)
@@ -123,8 +134,6 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) qlin_append_kernel(const __
 #pragma unroll
         for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
         const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-        HeadRow<D> g;
-        load_row<D>(g, gamma, lane);
 #pragma unroll
         for (int c = 0; c < x.NC; c++)
 #pragma unroll
@@ -132,22 +141,34 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) qlin_append_kernel(const __
       }
       if (p.n_turns) {
         float* mine = rows[warp];
+        if (!p.pairs) {  // the other of a pair may be another lane's
+#pragma unroll
+          for (int c = 0; c < x.NC; c++)
+#pragma unroll
+            for (int e = 0; e < x.E; e++) mine[(c * 32 + lane) * x.E + e] = x.x[c][e];
+          __syncwarp();
+        }
 #pragma unroll
         for (int c = 0; c < x.NC; c++)
 #pragma unroll
-          for (int e = 0; e < x.E; e++) mine[(c * 32 + lane) * x.E + e] = x.x[c][e];
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < x.NC; c++)
-#pragma unroll
-          for (int e = 0; e < x.E; e++) {
+          for (int e = 0; e < x.E; e += 2) {
             const int i = (c * 32 + lane) * x.E + e;
-            if (i < 2 * p.n_turns) {
-              const int turn = p.pairs ? i >> 1 : i < p.n_turns ? i : i - p.n_turns;
-              const bool second = p.pairs ? i & 1 : i >= p.n_turns;
-              const float other = mine[p.pairs ? i ^ 1 : second ? i - p.n_turns : i + p.n_turns];
-              const float2 w = cs[turn];
-              x.x[c][e] = x.x[c][e] * w.x + (second ? other : -other) * w.y;
+            if (i >= 2 * p.n_turns) continue;
+            if (p.pairs) {
+              const float2 w = cs[i >> 1];
+              const float a = x.x[c][e], b2 = x.x[c][e + 1];
+              x.x[c][e] = a * w.x - b2 * w.y;
+              x.x[c][e + 1] = b2 * w.x + a * w.y;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 2; k++) {
+                const bool second = i + k >= p.n_turns;
+                if (i + k < 2 * p.n_turns) {
+                  const float other = mine[second ? i + k - p.n_turns : i + k + p.n_turns];
+                  const float2 w = cs[second ? i + k - p.n_turns : i + k];
+                  x.x[c][e + k] = x.x[c][e + k] * w.x + (second ? other : -other) * w.y;
+                }
+              }
             }
           }
         __syncwarp();
@@ -157,7 +178,18 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) qlin_append_kernel(const __
       store_row<D>(x, static_cast<DST*>(p.q_out) + row * p.q_out_stride + (int64_t)head * D, lane);
     } else if (at >= 0) {
       DST* dst = static_cast<DST*>(is_v ? p.cache.v : p.cache.k);
-      store_row<D>(x, dst + at + hk * p.cache.head_stride, lane);
+      store_row<D>(x, dst + at + (is_v ? hk - p.cache.heads : hk) * p.cache.head_stride, lane);
+    }
+  };
+  for (int h = h0; h < h1; h += AHEAD * APPEND_WARPS) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; u++) {
+      const int head = h + u * APPEND_WARPS;
+      if (head < h1) {
+        HeadRow<D> now = x[u];
+        if (head + AHEAD * APPEND_WARPS < h1) load(x[u], head + AHEAD * APPEND_WARPS);
+        finish(now, head);
+      }
     }
   }
 }
@@ -305,7 +337,6 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step,
   p.Hq = q ? Hq : 0;
   p.n_turns = n_turns;
   p.pairs = pairs;
-  p.first = 0;
   p.heads = p.Hq + (k ? 2 * cache->heads : 0);
   const int64_t rows = (int64_t)step->B * step->T;
   // a few blocks per SM where the step has that many heads, a whole row per block beyond

@@ -401,6 +401,7 @@ class KVCache:
             raise ValueError("k and v must have the same strides and contiguous rows")
         self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
         self.pages, self.heads, self.page_size, self.width = k.shape
+        self._index = k.get_device()  # -1: not on a GPU
         # a dimension of one has no stride that matters
         step = [st if n > 1 else 8 for st, n in zip(k.stride()[:2], k.shape[:2])]
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), self.pages, step[0], step[1], k.stride(2),
@@ -437,24 +438,31 @@ class KVStep:
         self._ref = ctypes.addressof(self._struct)
 
 
+_fns: dict = {}
+
+
 def _fn(name: str):
-    return getattr(_lib or lib(), name)
+    fn = _fns.get(name)
+    if fn is None or _lib is None:
+        fn = _fns[name] = getattr(lib(), name)
+    return fn
 
 
-def _same_device(device, *tensors) -> None:
-    """All tensors on ``device``, and that device current (the library launches on the current one)."""
+def _same_device(index: int, *tensors) -> None:
+    """All tensors on GPU ``index``, and that device current (the library launches on the current one)."""
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"a tensor is on {t.device}, the call's other tensors on {device}")
-    if device.type != "cuda":
-        raise ValueError(f"the tensors are on {device}, not on a GPU")
-    if device.index != torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors are on {device}, but cuda:{torch._C._cuda_getDevice()} is the current device")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"a tensor is on {t.device}, another of the call's tensors on "
+                             + (f"cuda:{index}" if index >= 0 else "the CPU, not on a GPU"))
+    if index < 0:
+        raise ValueError("the tensors are on the CPU, not on a GPU")
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{index}, but cuda:{torch._C._cuda_getDevice()} is the current device")
 
 
-def _raw_stream(stream, device) -> int:
+def _raw_stream(stream, index: int) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -468,26 +476,31 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(t, n: int, what: str, dtype=None) -> int:
-    """Row stride of a [n, heads * width] (or [n, heads, width]) tensor."""
-    if t.shape[0] != n or (dtype is not None and t.dtype != dtype) or t.stride(-1) != 1 or (
-            t.dim() == 3 and t.stride(1) != t.shape[2]) or t.dim() not in (2, 3):
-        raise ValueError(f"{what} must be a [{n}, heads * width] tensor with contiguous rows"
-                         + (f" of {dtype}" if dtype is not None else ""))
-    return t.stride(0) if n > 1 else t.numel()
+def _rows(t, n: int, width: int, dtype, what: str) -> int:
+    """Row stride of a [n, width] (or [n, heads, D]) tensor of ``dtype``."""
+    if t.dtype is dtype:
+        if t.is_contiguous():
+            if t.shape == (n, width) or (t.dim() == 3 and t.shape[0] == n and t.numel() == n * width):
+                return width
+        elif t.dim() == 2 and t.shape == (n, width) and t.stride(1) == 1:
+            return t.stride(0) if n > 1 else width
+        elif t.dim() == 3 and t.shape[0] == n and t.shape[1] * t.shape[2] == width and t.stride(2) == 1 and (
+                t.stride(1) == t.shape[2]):
+            return t.stride(0) if n > 1 else width
+    raise ValueError(f"{what} must be a [{n}, {width}] tensor of {dtype} with contiguous rows")
 
 
 def _heads(t, width: int, what: str) -> int:
-    n = t.shape[1] if t.dim() == 2 else t.shape[1] * t.shape[2]
-    if n % width:
-        raise ValueError(f"{what} must hold whole heads of width {width}")
+    n = t.shape[1] if t.dim() == 2 else t.shape[1] * t.shape[2] if t.dim() == 3 else 0
+    if n < 1 or n % width:
+        raise ValueError(f"{what} must be [rows, heads * {width}], whole heads in each row")
     return n // width
 
 
 def _floats(t, n: int, what: str):
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous float32 tensor of {n} values")
     return t.data_ptr()
 
@@ -495,7 +508,7 @@ def _floats(t, n: int, what: str):
 def _ints(t, n: int, what: str):
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of {n} values")
     return t.data_ptr()
 
@@ -520,33 +533,33 @@ def kv_append(cache: KVCache, step: KVStep, q=None, k=None, v=None, q_gamma=None
     """Head norms and rotation of a step's projected q and k ([B * T, heads * width],
     fp32 or bf16); k and v are stored behind the sequences' committed tokens.
     Returns the normed and rotated q in the cache's type (or None without q)."""
-    n, D, dev = step.B * step.T, cache.width, cache.device
+    n, D, dev = step.B * step.T, cache.width, cache._index
     _same_device(dev, step.len, q, k, v, q_gamma, k_gamma, turns, q_out, ws)
     if (k is None) != (v is None):
         raise ValueError("k and v are given together")
     src = q if q is not None else k
     if src is None:
         raise ValueError("nothing to append: neither q nor k and v are given")
+    dtype = src.dtype
     Hq = qs = ks = vs = os_ = 0
     if q is not None:
-        Hq, qs = _heads(q, D, "q"), _rows(q, n, "q", src.dtype)
+        Hq = _heads(q, D, "q")
+        qs = _rows(q, n, Hq * D, dtype, "q")
         if q_out is None:
-            q_out = _empty((n, Hq * D), cache.dtype, dev, stream)
-        os_ = _rows(q_out, n, "q_out", cache.dtype)
-        if _heads(q_out, D, "q_out") != Hq:
-            raise ValueError("q_out must have the shape of q")
+            q_out = _empty((n, Hq * D), cache.dtype, cache.device, stream)
+        os_ = _rows(q_out, n, Hq * D, cache.dtype, "q_out")
     if k is not None:
-        ks, vs = _rows(k, n, "k", src.dtype), _rows(v, n, "v", src.dtype)
-        if _heads(k, D, "k") != cache.heads or _heads(v, D, "v") != cache.heads:
-            raise ValueError("k and v must have the cache's heads")
-    if turns is not None and (turns.dtype != torch.int64 or not turns.is_contiguous()):
-        raise ValueError("turns must come from rope_turns")
-    nt = 0 if turns is None else turns.numel()
+        ks, vs = _rows(k, n, cache.heads * D, dtype, "k"), _rows(v, n, cache.heads * D, dtype, "v")
+    nt = 0
+    if turns is not None:
+        nt = turns.numel()
+        if turns.dtype is not torch.int64 or not turns.is_contiguous():
+            raise ValueError("turns must come from rope_turns")
     _check(_fn("qlin_kv_append")(
-        cache._ref, step._ref, Hq, DTYPES.get(src.dtype, -1), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
-        _floats(q_gamma, D, "q_gamma"), _floats(k_gamma, D, "k_gamma"), eps, _ptr(turns) if nt else None, nt,
-        1 if pairs else 0, _ptr(q_out) if q is not None else None, os_, _ptr(ws), 0 if ws is None else ws.numel(), flags,
-        _raw_stream(stream, dev)), "kv_append")
+        cache._ref, step._ref, Hq, DTYPES.get(dtype, -1), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+        _floats(q_gamma, D, "q_gamma"), _floats(k_gamma, D, "k_gamma"), eps, turns.data_ptr() if nt else None, nt,
+        1 if pairs else 0, q_out.data_ptr() if q is not None else None, os_, _ptr(ws), 0 if ws is None else ws.numel(),
+        flags, _raw_stream(stream, dev)), "kv_append")
     return q_out
 
 
@@ -563,20 +576,19 @@ def tree_attention(cache: KVCache, step: KVStep, q: torch.Tensor, scale: float |
     cache: every row sees the committed tokens of its sequence and the step's
     rows that its mask names.  Returns bf16 [B * T, Hq * width].  ``scale``:
     width ** -0.5 unless given."""
-    n, D, dev = step.B * step.T, cache.width, cache.device
+    n, D, dev = step.B * step.T, cache.width, cache._index
     _same_device(dev, step.len, q, out, ws)
-    Hq, qs = _heads(q, D, "q"), _rows(q, n, "q", cache.dtype)
+    Hq = _heads(q, D, "q")
+    qs = _rows(q, n, Hq * D, cache.dtype, "q")
     if out is None:
-        out = _empty((n, Hq * D), torch.bfloat16, dev, stream)
-    os_ = _rows(out, n, "out", torch.bfloat16)
-    if _heads(out, D, "out") != Hq:
-        raise ValueError("out must have the shape of q")
+        out = _empty((n, Hq * D), torch.bfloat16, cache.device, stream)
+    os_ = _rows(out, n, Hq * D, torch.bfloat16, "out")
+    raw = _raw_stream(stream, dev)
     if ws is None:
-        ws = _empty(tree_attention_workspace_bytes(cache, step.B, step.T, Hq), torch.uint8, dev, stream)
-        workspace_init(ws, _raw_stream(stream, dev))
+        ws = _empty(tree_attention_workspace_bytes(cache, step.B, step.T, Hq), torch.uint8, cache.device, stream)
+        workspace_init(ws, raw)
     _check(_fn("qlin_tree_attention")(cache._ref, step._ref, Hq, q.data_ptr(), qs, D ** -0.5 if scale is None else scale,
-                                      out.data_ptr(), os_, ws.data_ptr(), ws.numel(), flags, _raw_stream(stream, dev)),
-           "tree_attention")
+                                      out.data_ptr(), os_, ws.data_ptr(), ws.numel(), flags, raw), "tree_attention")
     return out
 
 
@@ -585,12 +597,13 @@ def kv_keep(cache: KVCache, step: KVStep, keep: torch.Tensor, n_keep: torch.Tens
     """Move the accepted rows ``keep[b, :n_keep[b]]`` (int32 [B, T], increasing) of each
     sequence up behind its committed tokens; ``len_out`` (int32 [B], may be the
     step's ``len``) gets the new lengths."""
-    _same_device(cache.device, step.len, keep, n_keep, len_out, ws)
-    if keep.shape != (step.B, step.T) or keep.dtype != torch.int32 or (step.T > 1 and keep.stride(1) != 1):
+    _same_device(cache._index, step.len, keep, n_keep, len_out, ws)
+    B, T = step.B, step.T
+    if keep.shape != (B, T) or keep.dtype is not torch.int32 or (T > 1 and keep.stride(1) != 1):
         raise ValueError("keep must be an int32 [B, T] tensor with contiguous rows")
-    _check(_fn("qlin_kv_keep")(cache._ref, step._ref, keep.data_ptr(), keep.stride(0) if step.B > 1 else step.T,
-                               _ints(n_keep, step.B, "n_keep"), _ints(len_out, step.B, "len_out"), _ptr(ws),
-                               0 if ws is None else ws.numel(), flags, _raw_stream(stream, cache.device)), "kv_keep")
+    _check(_fn("qlin_kv_keep")(cache._ref, step._ref, keep.data_ptr(), keep.stride(0) if B > 1 else T,
+                               _ints(n_keep, B, "n_keep"), _ints(len_out, B, "len_out"), _ptr(ws),
+                               0 if ws is None else ws.numel(), flags, _raw_stream(stream, cache._index)), "kv_keep")
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None, token=None,
@@ -602,10 +615,10 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
         raise ValueError("logits must be [M, V] with contiguous rows")
     M, V = logits.shape
-    dev = logits.device
+    dev = logits.get_device()
     _same_device(dev, u, temperature, top_k, top_p, min_p, token, prob)
     if token is None:
-        token = _empty((M,), torch.int32, dev, stream)
+        token = _empty((M,), torch.int32, logits.device, stream)
     _check(_fn("qlin_sample")(M, V, DTYPES.get(logits.dtype, -1), logits.data_ptr(), logits.stride(0) if M > 1 else V,
                               _floats(u, M, "u"), _floats(temperature, M, "temperature"), _ints(top_k, M, "top_k"),
                               _floats(top_p, M, "top_p"), _floats(min_p, M, "min_p"), _ints(token, M, "token"),
