@@ -429,10 +429,11 @@ typedef struct {
  *   page_table : int32 [B, max_pages], rows table_stride entries apart.
  *                Entries behind the last page in use are not read.
  *   len        : int32 [B], committed tokens (0: none yet).  len[b] < 0: no
- *                sequence in this place; nothing of it is read or written.
+ *                sequence in this place; its rows have no effect and nothing of
+ *                it is written.
  *   count      : int32 [B] or NULL (T rows in every sequence): rows in use;
- *                the rows behind them are not read, and what they would have
- *                written is left as it was.
+ *                the rows behind them have no effect, whatever they hold, and
+ *                what they would have written is left as it was.
  *   depth      : int32, row t's distance from the committed tokens, so its
  *                rotation position is len[b] + depth[t]; NULL: t.
  *   mask       : int32 bits, bit j of row t: row t sees row j of its own

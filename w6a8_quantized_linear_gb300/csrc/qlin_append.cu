@@ -8,7 +8,7 @@
 namespace qlin {
 namespace {
 
-constexpr int APPEND_WARPS = 8;
+constexpr int APPEND_THREADS = 128;
 
 struct AppendParams {
   qlin_kv_cache cache;
@@ -25,171 +25,152 @@ struct AppendParams {
   int heads_per_block;
 };
 
-// A head row of D elements on a warp: NC chunks of E consecutive elements a
-// lane (chunk c covers elements c * 32 * E ..), so that each load and store of
-// a warp is one contiguous run.
-template <int D>
-struct HeadRow {
-  static constexpr int E = D >= 128 ? 4 : 2;
-  static constexpr int NC = D / (32 * E);
-  float x[NC][E];
-};
-
-template <int D>
-__device__ __forceinline__ void load_row(HeadRow<D>& r, const float* p, int lane) {
-#pragma unroll
-  for (int c = 0; c < HeadRow<D>::NC; c++) {
-    const float* s = p + (c * 32 + lane) * HeadRow<D>::E;
-    if constexpr (HeadRow<D>::E == 4) {
-      const float4 f = *reinterpret_cast<const float4*>(s);
-      r.x[c][0] = f.x, r.x[c][1] = f.y, r.x[c][2] = f.z, r.x[c][3] = f.w;
-    } else {
-      const float2 f = *reinterpret_cast<const float2*>(s);
-      r.x[c][0] = f.x, r.x[c][1] = f.y;
-    }
-  }
+__device__ __forceinline__ void load8(float (&x)[8], const float* p) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
-template <int D>
-__device__ __forceinline__ void load_row(HeadRow<D>& r, const __nv_bfloat16* p, int lane) {
+__device__ __forceinline__ void load8(float (&x)[8], const __nv_bfloat16* p) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const float2 f[4] = {unpack2(a.x, __nv_bfloat16()), unpack2(a.y, __nv_bfloat16()), unpack2(a.z, __nv_bfloat16()),
+                       unpack2(a.w, __nv_bfloat16())};
 #pragma unroll
-  for (int c = 0; c < HeadRow<D>::NC; c++) {
-    const __nv_bfloat16* s = p + (c * 32 + lane) * HeadRow<D>::E;
-#pragma unroll
-    for (int e = 0; e < HeadRow<D>::E; e += 2) {
-      const float2 f = unpack2(*reinterpret_cast<const uint32_t*>(s + e), __nv_bfloat16());
-      r.x[c][e] = f.x, r.x[c][e + 1] = f.y;
-    }
-  }
+  for (int e = 0; e < 4; e++) x[2 * e] = f[e].x, x[2 * e + 1] = f[e].y;
 }
-template <int D, typename DST>
-__device__ __forceinline__ void store_row(const HeadRow<D>& r, DST* p, int lane) {
-#pragma unroll
-  for (int c = 0; c < HeadRow<D>::NC; c++) {
-    DST* s = p + (c * 32 + lane) * HeadRow<D>::E;
-    if constexpr (HeadRow<D>::E == 4) {
-      *reinterpret_cast<uint2*>(s) =
-          make_uint2(pack2(r.x[c][0], r.x[c][1], DST()), pack2(r.x[c][2], r.x[c][3], DST()));
-    } else {
-      *reinterpret_cast<uint32_t*>(s) = pack2(r.x[c][0], r.x[c][1], DST());
-    }
-  }
+template <typename DST>
+__device__ __forceinline__ void store8(const float (&x)[8], DST* p) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1], DST()), pack2(x[2], x[3], DST()),
+                                            pack2(x[4], x[5], DST()), pack2(x[6], x[7], DST()));
 }
 
-// One block per token row and run of heads, one warp per head, two or four
-// heads of a warp in flight.
+// One block per token row and run of heads; D / 8 lanes per head, eight
+// consecutive elements each, so that a warp's instructions work on up to four
+// heads, and two passes' loads in flight.
 //   x' = x gamma / sqrt(mean(x^2) + eps);  (a, b) -> (a cos - b sin, b cos + a sin)
 // The angle is pos * turns[i] mod 1, exact in 64-bit integers whatever the
 // position, so only its last conversion to fp32 rounds.  Bound by the bytes of
-// the rows (6 or 4 per element) for a prompt, by the launch for a step.
+// the rows (6 or 4 per element) for a prompt, by the launch for a step.  (A
+// warp per head, four elements a lane, issued three times the instructions and
+// was bound by them: 48 us against 29 us of bytes for 4001 rows of 64 heads.)
 template <typename SRC, typename DST, int D>
-__global__ void __launch_bounds__(APPEND_WARPS * 32) qlin_append_kernel(const __grid_constant__ AppendParams p) {
-  __shared__ float2 cs[D / 2];                     // cos, sin of this row's angles
-  __shared__ float rows[APPEND_WARPS][D];
-  constexpr int AHEAD = D == 256 ? 2 : 4;
+__global__ void __launch_bounds__(APPEND_THREADS) qlin_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int LANES = D / 8, PASS = APPEND_THREADS / LANES;  // lanes of a head, heads of a pass
+  constexpr int AHEAD = 2;
+  __shared__ float2 cs[D / 2];                  // cos, sin of this row's angles
+  __shared__ __align__(16) float gamma[2][D];   // of q, of k
+  __shared__ float rows[PASS][D];
   const int row = blockIdx.x, b = row / p.step.T, t = row - b * p.step.T;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int at8 = threadIdx.x % LANES * 8, slot = threadIdx.x / LANES;  // this thread's elements, its head of a pass
   pdl_wait();
   pdl_launch_dependents();
-  const int len = p.step.len[b];
-  if (len < 0 || t >= step_rows(p.step, b)) return;
-  const int h0 = blockIdx.y * p.heads_per_block + warp;
+  // everything that is read goes out before anything is waited for
   const int h1 = min((int)(blockIdx.y + 1) * p.heads_per_block, p.heads);
+  int h = blockIdx.y * p.heads_per_block + slot;
   // the heads of a token: of q, then of k, then of v
-  auto load = [&](HeadRow<D>& x, int head) {
-    const int hk = head - p.Hq;
-    const SRC* src = hk < 0 ? static_cast<const SRC*>(p.q) + row * p.q_stride + (int64_t)head * D
-                     : hk < p.cache.heads
-                         ? static_cast<const SRC*>(p.k) + row * p.k_stride + (int64_t)hk * D
-                         : static_cast<const SRC*>(p.v) + row * p.v_stride + (int64_t)(hk - p.cache.heads) * D;
-    load_row<D>(x, src, lane);
-  };
-  HeadRow<D> x[AHEAD];
+  const int v0 = p.Hq + p.cache.heads;
+  const SRC* qs = static_cast<const SRC*>(p.q) + row * p.q_stride + at8;
+  const SRC* ks = static_cast<const SRC*>(p.k) + (row * p.k_stride - (int64_t)p.Hq * D) + at8;
+  const SRC* vs = static_cast<const SRC*>(p.v) + (row * p.v_stride - (int64_t)v0 * D) + at8;
+  auto load = [&](float (&x)[8], int head) { load8(x, (head < p.Hq ? qs : head < v0 ? ks : vs) + head * D); };
+  float x[AHEAD][8];
 #pragma unroll
   for (int u = 0; u < AHEAD; u++)
-    if (h0 + u * APPEND_WARPS < h1) load(x[u], h0 + u * APPEND_WARPS);
+    if (h + u * PASS < h1) load(x[u], h + u * PASS);
+  const uint64_t turn = threadIdx.x < p.n_turns ? p.turns[threadIdx.x] : 0;
+  for (int i = threadIdx.x; i < D; i += APPEND_THREADS) {
+    gamma[0][i] = p.q_gamma ? p.q_gamma[i] : 1.f;
+    gamma[1][i] = p.k_gamma ? p.k_gamma[i] : 1.f;
+  }
+  const int len = p.step.len[b], used = step_rows(p.step, b);
   const int depth = p.step.depth ? p.step.depth[b * p.step.tree_stride + t] : t;
-  const int64_t pos = (int64_t)len + depth;
-  for (int i = threadIdx.x; i < p.n_turns; i += APPEND_WARPS * 32) {
-    const int64_t turn = (int64_t)((uint64_t)pos * p.turns[i]);  // in [-1/2, 1/2) turns of 2^64
+  if (len < 0 || t >= used) return;
+  const int n = p.n_turns;
+  static_assert(APPEND_THREADS >= D / 2, "a thread per angle");
+  if (threadIdx.x < n) {
+    const int64_t angle = (int64_t)((uint64_t)((int64_t)len + depth) * turn);  // in [-1/2, 1/2) turns of 2^64
     float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-    cs[i] = make_float2(c, s);
+    sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &s, &c);
+    cs[threadIdx.x] = make_float2(c, s);
   }
   const int64_t at = p.k ? token_offset(p.cache, p.step, b, (int64_t)len + t) : 0;
   if (at < 0 && threadIdx.x == 0) report(p.status, QLIN_ERR_BAD_INDEX);
   __syncthreads();
-  auto finish = [&](HeadRow<D>& x, int head) {
-    const int hk = head - p.Hq;
-    const bool is_q = hk < 0, is_v = hk >= p.cache.heads;
-    if (!is_v) {
-      const float* gamma = is_q ? p.q_gamma : p.k_gamma;
-      if (gamma) {
-        HeadRow<D> g;
-        load_row<D>(g, gamma, lane);
-        float ss = 0.f;
+  // This thread's cosines, and sines with the sign of its side, the same for
+  // all heads.  Where half a turned range is a power of two of whole lanes,
+  // the other of a pair lies in lane ^ flip; else it goes through shared
+  // memory (pairs: it is the thread's own).
+  const int flip = n % 8 == 0 && (n & (n - 1)) == 0 ? n / 8 : 0;
+  float tc[8], ts[8];
 #pragma unroll
-        for (int c = 0; c < x.NC; c++)
+  for (int e = 0; e < 8; e++) {
+    const int i = at8 + e;
+    const bool second = p.pairs ? i & 1 : i >= n;
+    const float2 w = i < 2 * n ? cs[p.pairs ? i >> 1 : second ? i - n : i] : make_float2(1.f, 0.f);
+    tc[e] = w.x;
+    ts[e] = second ? w.y : -w.y;
+  }
+  DST* const qd = static_cast<DST*>(p.q_out) + row * p.q_out_stride + at8;
+  auto finish = [&](float (&x)[8], int head) {
+    const bool is_q = head < p.Hq, is_v = head >= v0, here = head < h1;
+    if (__any_sync(0xFFFFFFFFu, here && !is_v)) {  // all lanes: the warp's heads may differ in kind
+      const float* g = gamma[is_q ? 0 : 1] + at8;
+      float ss = 0.f;
 #pragma unroll
-          for (int e = 0; e < x.E; e++) ss = fmaf(x.x[c][e], x.x[c][e], ss);
+      for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-#pragma unroll
-        for (int c = 0; c < x.NC; c++)
-#pragma unroll
-          for (int e = 0; e < x.E; e++) x.x[c][e] *= r * g.x[c][e];
+      for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+      const float a = ss * (1.0f / D) + p.eps;
+      float r = rsqrtf(a);  // and a Newton step, to one ulp (a = 0 or infinite: as it is)
+      const float d = fmaf(-a * r, r, 1.f);
+      if (fabsf(d) < 1.f) r = fmaf(0.5f * r, d, r);
+      if ((is_q ? p.q_gamma : p.k_gamma) && !is_v) {
+        const float4 g0 = reinterpret_cast<const float4*>(g)[0], g1 = reinterpret_cast<const float4*>(g)[1];
+        x[0] *= r * g0.x, x[1] *= r * g0.y, x[2] *= r * g0.z, x[3] *= r * g0.w;
+        x[4] *= r * g1.x, x[5] *= r * g1.y, x[6] *= r * g1.z, x[7] *= r * g1.w;
       }
-      if (p.n_turns) {
-        float* mine = rows[warp];
-        if (!p.pairs) {  // the other of a pair may be another lane's
+      if (n) {
+        float other[8];
+        if (p.pairs) {
 #pragma unroll
-          for (int c = 0; c < x.NC; c++)
+          for (int e = 0; e < 8; e++) other[e] = x[e ^ 1];
+        } else if (flip) {
 #pragma unroll
-            for (int e = 0; e < x.E; e++) mine[(c * 32 + lane) * x.E + e] = x.x[c][e];
+          for (int e = 0; e < 8; e++) other[e] = __shfl_xor_sync(0xFFFFFFFFu, x[e], flip);
+        } else {
+          float* mine = rows[slot];
+#pragma unroll
+          for (int e = 0; e < 8; e++) mine[at8 + e] = x[e];
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const int i = at8 + e;
+            other[e] = i < 2 * n ? mine[i >= n ? i - n : i + n] : 0.f;
+          }
           __syncwarp();
         }
 #pragma unroll
-        for (int c = 0; c < x.NC; c++)
-#pragma unroll
-          for (int e = 0; e < x.E; e += 2) {
-            const int i = (c * 32 + lane) * x.E + e;
-            if (i >= 2 * p.n_turns) continue;
-            if (p.pairs) {
-              const float2 w = cs[i >> 1];
-              const float a = x.x[c][e], b2 = x.x[c][e + 1];
-              x.x[c][e] = a * w.x - b2 * w.y;
-              x.x[c][e + 1] = b2 * w.x + a * w.y;
-            } else {
-#pragma unroll
-              for (int k = 0; k < 2; k++) {
-                const bool second = i + k >= p.n_turns;
-                if (i + k < 2 * p.n_turns) {
-                  const float other = mine[second ? i + k - p.n_turns : i + k + p.n_turns];
-                  const float2 w = cs[second ? i + k - p.n_turns : i + k];
-                  x.x[c][e + k] = x.x[c][e + k] * w.x + (second ? other : -other) * w.y;
-                }
-              }
-            }
-          }
-        __syncwarp();
+        for (int e = 0; e < 8; e++)
+          if (at8 + e < 2 * n && !is_v) x[e] = x[e] * tc[e] + other[e] * ts[e];
       }
     }
+    if (!here) return;
     if (is_q) {
-      store_row<D>(x, static_cast<DST*>(p.q_out) + row * p.q_out_stride + (int64_t)head * D, lane);
+      store8(x, qd + head * D);
     } else if (at >= 0) {
       DST* dst = static_cast<DST*>(is_v ? p.cache.v : p.cache.k);
-      store_row<D>(x, dst + at + (is_v ? hk - p.cache.heads : hk) * p.cache.head_stride, lane);
+      store8(x, dst + at + (head - (is_v ? v0 : p.Hq)) * p.cache.head_stride + at8);
     }
   };
-  for (int h = h0; h < h1; h += AHEAD * APPEND_WARPS) {
+  const int warp_first = h - slot + (int)(threadIdx.x & ~31u) / LANES;  // the same in all lanes of a warp
+  for (int off = 0; warp_first + off < h1; off += AHEAD * PASS) {
 #pragma unroll
     for (int u = 0; u < AHEAD; u++) {
-      const int head = h + u * APPEND_WARPS;
-      if (head < h1) {
-        HeadRow<D> now = x[u];
-        if (head + AHEAD * APPEND_WARPS < h1) load(x[u], head + AHEAD * APPEND_WARPS);
-        finish(now, head);
-      }
+      const int head = h + off + u * PASS;
+      if (warp_first + off + u * PASS >= h1) break;
+      float now[8];
+#pragma unroll
+      for (int e = 0; e < 8; e++) now[e] = x[u][e];
+      if (head + AHEAD * PASS < h1) load(x[u], head + AHEAD * PASS);
+      finish(now, head);
     }
   }
 }
@@ -342,11 +323,12 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step,
   // a few blocks per SM where the step has that many heads, a whole row per block beyond
   const int64_t want = (1216 + rows - 1) / rows;
   int64_t per = (p.heads + want - 1) / want;
-  per = (per + APPEND_WARPS - 1) / APPEND_WARPS * APPEND_WARPS;
+  const int64_t pass = APPEND_THREADS / (D / 8);
+  per = (per + pass - 1) / pass * pass;
   p.heads_per_block = (int)per;
   void* args[] = {&p};
   return launch_step(append_fn(src, cache->dtype, cache->width),
-                     dim3((unsigned)rows, (unsigned)((p.heads + per - 1) / per), 1), dim3(APPEND_WARPS * 32, 1, 1), 0,
+                     dim3((unsigned)rows, (unsigned)((p.heads + per - 1) / per), 1), dim3(APPEND_THREADS, 1, 1), 0,
                      static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0);
 }
 
