@@ -25,53 +25,74 @@ struct AppendParams {
   int heads_per_block;
 };
 
-__device__ __forceinline__ void load8(float (&x)[8], const float* p) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(float (&x)[8], const __nv_bfloat16* p) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const float2 f[4] = {unpack2(a.x, __nv_bfloat16()), unpack2(a.y, __nv_bfloat16()), unpack2(a.z, __nv_bfloat16()),
-                       unpack2(a.w, __nv_bfloat16())};
+// A thread's two runs of four elements of a head, as they were loaded.
+template <typename SRC>
+struct Raw;
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, int half) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + half);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int half) {
+    a = *reinterpret_cast<const uint2*>(p);
+    b = *reinterpret_cast<const uint2*>(p + half);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-  for (int e = 0; e < 4; e++) x[2 * e] = f[e].x, x[2 * e + 1] = f[e].y;
-}
+    for (int e = 0; e < 4; e++) {
+      const float2 f = unpack2(w[e], __nv_bfloat16());
+      x[2 * e] = f.x, x[2 * e + 1] = f.y;
+    }
+  }
+};
 template <typename DST>
-__device__ __forceinline__ void store8(const float (&x)[8], DST* p) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1], DST()), pack2(x[2], x[3], DST()),
-                                            pack2(x[4], x[5], DST()), pack2(x[6], x[7], DST()));
+__device__ __forceinline__ void store4(const float* x, DST* p) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0], x[1], DST()), pack2(x[2], x[3], DST()));
 }
 
-// One block per token row and run of heads; D / 8 lanes per head, eight
-// consecutive elements each, so that a warp's instructions work on up to four
-// heads, and two passes' loads in flight.
+// One block per token row and run of heads; D / 8 lanes per head, so that a
+// warp's instructions work on up to four heads, and two or four passes' loads
+// in flight.  Lane l of a head holds elements 4 l .. 4 l + 3 of each half, so that
+// where a whole head turns, both of a pair are the lane's own.
 //   x' = x gamma / sqrt(mean(x^2) + eps);  (a, b) -> (a cos - b sin, b cos + a sin)
 // The angle is pos * turns[i] mod 1, exact in 64-bit integers whatever the
 // position, so only its last conversion to fp32 rounds.  Bound by the bytes of
-// the rows (6 or 4 per element) for a prompt, by the launch for a step.  (A
-// warp per head, four elements a lane, issued three times the instructions and
-// was bound by them: 48 us against 29 us of bytes for 4001 rows of 64 heads.)
+// the rows (6 or 4 per element) for a prompt, by the launch for a step.
+// Measured, 4001 rows of 64 heads of 128: fp32 34.2 us (197 MB, 5.7 TB/s, 0.85
+// of the measured copy), bf16 29.6 us (131 MB; 40 us with half the loads in
+// flight).  A warp per head with four elements a lane issued three times the
+// instructions and was bound by them (48 us).
 template <typename SRC, typename DST, int D>
-__global__ void __launch_bounds__(APPEND_THREADS) qlin_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(APPEND_THREADS, 7) qlin_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LANES = D / 8, PASS = APPEND_THREADS / LANES;  // lanes of a head, heads of a pass
-  constexpr int AHEAD = 2;
+  constexpr int AHEAD = sizeof(SRC) == 4 ? 2 : 4, H = D / 2;  // passes in flight: 64 bytes a thread
   __shared__ float2 cs[D / 2];                  // cos, sin of this row's angles
   __shared__ __align__(16) float gamma[2][D];   // of q, of k
   __shared__ float rows[PASS][D];
   const int row = blockIdx.x, b = row / p.step.T, t = row - b * p.step.T;
-  const int at8 = threadIdx.x % LANES * 8, slot = threadIdx.x / LANES;  // this thread's elements, its head of a pass
+  const int at4 = threadIdx.x % LANES * 4, slot = threadIdx.x / LANES;  // this thread's elements, its head of a pass
   pdl_wait();
   pdl_launch_dependents();
   // everything that is read goes out before anything is waited for
   const int h1 = min((int)(blockIdx.y + 1) * p.heads_per_block, p.heads);
-  int h = blockIdx.y * p.heads_per_block + slot;
+  const int h = blockIdx.y * p.heads_per_block + slot;
   // the heads of a token: of q, then of k, then of v
   const int v0 = p.Hq + p.cache.heads;
-  const SRC* qs = static_cast<const SRC*>(p.q) + row * p.q_stride + at8;
-  const SRC* ks = static_cast<const SRC*>(p.k) + (row * p.k_stride - (int64_t)p.Hq * D) + at8;
-  const SRC* vs = static_cast<const SRC*>(p.v) + (row * p.v_stride - (int64_t)v0 * D) + at8;
-  auto load = [&](float (&x)[8], int head) { load8(x, (head < p.Hq ? qs : head < v0 ? ks : vs) + head * D); };
-  float x[AHEAD][8];
+  const SRC* qs = static_cast<const SRC*>(p.q) + row * p.q_stride + at4;
+  const SRC* ks = static_cast<const SRC*>(p.k) + (row * p.k_stride - (int64_t)p.Hq * D) + at4;
+  const SRC* vs = static_cast<const SRC*>(p.v) + (row * p.v_stride - (int64_t)v0 * D) + at4;
+  auto load = [&](Raw<SRC>& x, int head) { x.load((head < p.Hq ? qs : head < v0 ? ks : vs) + head * D, H); };
+  Raw<SRC> x[AHEAD];
 #pragma unroll
   for (int u = 0; u < AHEAD; u++)
     if (h + u * PASS < h1) load(x[u], h + u * PASS);
@@ -94,70 +115,91 @@ __global__ void __launch_bounds__(APPEND_THREADS) qlin_append_kernel(const __gri
   const int64_t at = p.k ? token_offset(p.cache, p.step, b, (int64_t)len + t) : 0;
   if (at < 0 && threadIdx.x == 0) report(p.status, QLIN_ERR_BAD_INDEX);
   __syncthreads();
-  // This thread's cosines, and sines with the sign of its side, the same for
-  // all heads.  Where half a turned range is a power of two of whole lanes,
-  // the other of a pair lies in lane ^ flip; else it goes through shared
-  // memory (pairs: it is the thread's own).
-  const int flip = n % 8 == 0 && (n & (n - 1)) == 0 ? n / 8 : 0;
-  float tc[8], ts[8];
+  // How a head turns: not at all; pairs, or whole halves, within the lane;
+  // a power of two of whole lanes, with lane ^ flip; any other, through shared
+  // memory.  The lane's cosines and sines are the same for all heads.
+  const int flip = !p.pairs && n && n < H && n % 4 == 0 && (n & (n - 1)) == 0 && 2 * n <= H ? n / 4 : 0;
+  const bool own = !p.pairs && n == H;
+  float tc[4], ts[4];  // pairs: of elements 0 and 2 of each half; else of the first half's (flip: signed by its side)
 #pragma unroll
-  for (int e = 0; e < 8; e++) {
-    const int i = at8 + e;
-    const bool second = p.pairs ? i & 1 : i >= n;
-    const float2 w = i < 2 * n ? cs[p.pairs ? i >> 1 : second ? i - n : i] : make_float2(1.f, 0.f);
+  for (int e = 0; e < 4; e++) {
+    int i = at4 + e;
+    if (p.pairs) i = (e < 2 ? at4 + 2 * e : H + at4 + 2 * (e - 2)) / 2;
+    const bool second = flip && i >= n;
+    if (second) i -= n;
+    const float2 w = i < n ? cs[i] : make_float2(1.f, 0.f);
     tc[e] = w.x;
-    ts[e] = second ? w.y : -w.y;
+    ts[e] = flip && !second ? -w.y : w.y;
   }
-  DST* const qd = static_cast<DST*>(p.q_out) + row * p.q_out_stride + at8;
+  DST* const qd = static_cast<DST*>(p.q_out) + row * p.q_out_stride + at4;
   auto finish = [&](float (&x)[8], int head) {
     const bool is_q = head < p.Hq, is_v = head >= v0, here = head < h1;
     if (__any_sync(0xFFFFFFFFu, here && !is_v)) {  // all lanes: the warp's heads may differ in kind
-      const float* g = gamma[is_q ? 0 : 1] + at8;
-      float ss = 0.f;
+      if (p.q_gamma || p.k_gamma) {
+        float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
+        for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-      for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-      const float a = ss * (1.0f / D) + p.eps;
-      float r = rsqrtf(a);  // and a Newton step, to one ulp (a = 0 or infinite: as it is)
-      const float d = fmaf(-a * r, r, 1.f);
-      if (fabsf(d) < 1.f) r = fmaf(0.5f * r, d, r);
-      if ((is_q ? p.q_gamma : p.k_gamma) && !is_v) {
-        const float4 g0 = reinterpret_cast<const float4*>(g)[0], g1 = reinterpret_cast<const float4*>(g)[1];
-        x[0] *= r * g0.x, x[1] *= r * g0.y, x[2] *= r * g0.z, x[3] *= r * g0.w;
-        x[4] *= r * g1.x, x[5] *= r * g1.y, x[6] *= r * g1.z, x[7] *= r * g1.w;
-      }
-      if (n) {
-        float other[8];
-        if (p.pairs) {
-#pragma unroll
-          for (int e = 0; e < 8; e++) other[e] = x[e ^ 1];
-        } else if (flip) {
-#pragma unroll
-          for (int e = 0; e < 8; e++) other[e] = __shfl_xor_sync(0xFFFFFFFFu, x[e], flip);
-        } else {
-          float* mine = rows[slot];
-#pragma unroll
-          for (int e = 0; e < 8; e++) mine[at8 + e] = x[e];
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 8; e++) {
-            const int i = at8 + e;
-            other[e] = i < 2 * n ? mine[i >= n ? i - n : i + n] : 0.f;
-          }
-          __syncwarp();
+        for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        const float a = ss * (1.0f / D) + p.eps;
+        float r = rsqrtf(a);  // and a Newton step, to one ulp (a = 0 or infinite: as it is)
+        const float d = fmaf(-a * r, r, 1.f);
+        if (fabsf(d) < 1.f) r = fmaf(0.5f * r, d, r);
+        if ((is_q ? p.q_gamma : p.k_gamma) && !is_v) {
+          const float* g = gamma[is_q ? 0 : 1] + at4;
+          const float4 g0 = *reinterpret_cast<const float4*>(g), g1 = *reinterpret_cast<const float4*>(g + H);
+          x[0] *= r * g0.x, x[1] *= r * g0.y, x[2] *= r * g0.z, x[3] *= r * g0.w;
+          x[4] *= r * g1.x, x[5] *= r * g1.y, x[6] *= r * g1.z, x[7] *= r * g1.w;
         }
+      }
+      if (p.pairs) {
 #pragma unroll
-        for (int e = 0; e < 8; e++)
-          if (at8 + e < 2 * n && !is_v) x[e] = x[e] * tc[e] + other[e] * ts[e];
+        for (int e = 0; e < 4; e++) {
+          const int i = e < 2 ? 2 * e : 4 + 2 * (e - 2);
+          const float u = x[i], w = x[i + 1];
+          if ((e < 2 ? at4 + 2 * e : H + at4 + 2 * (e - 2)) < 2 * n && !is_v) {
+            x[i] = u * tc[e] - w * ts[e];
+            x[i + 1] = w * tc[e] + u * ts[e];
+          }
+        }
+      } else if (own) {
+        if (!is_v)
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const float u = x[e], w = x[4 + e];
+            x[e] = u * tc[e] - w * ts[e];
+            x[4 + e] = w * tc[e] + u * ts[e];
+          }
+      } else if (flip) {
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const float other = __shfl_xor_sync(0xFFFFFFFFu, x[e], flip);
+          if (at4 < 2 * n && !is_v) x[e] = x[e] * tc[e] + other * ts[e];
+        }
+      } else if (n) {
+        float* mine = rows[slot];
+#pragma unroll
+        for (int e = 0; e < 8; e++) mine[at4 + e % 4 + e / 4 * H] = x[e];
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const int i = at4 + e % 4 + e / 4 * H;
+          if (i < 2 * n && !is_v) {
+            const float2 w = cs[i >= n ? i - n : i];
+            x[e] = i >= n ? x[e] * w.x + mine[i - n] * w.y : x[e] * w.x - mine[i + n] * w.y;
+          }
+        }
+        __syncwarp();
       }
     }
     if (!here) return;
     if (is_q) {
-      store8(x, qd + head * D);
+      store4(x, qd + head * D);
+      store4(x + 4, qd + head * D + H);
     } else if (at >= 0) {
-      DST* dst = static_cast<DST*>(is_v ? p.cache.v : p.cache.k);
-      store8(x, dst + at + (head - (is_v ? v0 : p.Hq)) * p.cache.head_stride + at8);
+      DST* dst = static_cast<DST*>(is_v ? p.cache.v : p.cache.k) + at + (head - (is_v ? v0 : p.Hq)) * p.cache.head_stride + at4;
+      store4(x, dst);
+      store4(x + 4, dst + H);
     }
   };
   const int warp_first = h - slot + (int)(threadIdx.x & ~31u) / LANES;  // the same in all lanes of a warp
@@ -167,8 +209,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) qlin_append_kernel(const __gri
       const int head = h + off + u * PASS;
       if (warp_first + off + u * PASS >= h1) break;
       float now[8];
-#pragma unroll
-      for (int e = 0; e < 8; e++) now[e] = x[u][e];
+      x[u].get(now);
       if (head + AHEAD * PASS < h1) load(x[u], head + AHEAD * PASS);
       finish(now, head);
     }
