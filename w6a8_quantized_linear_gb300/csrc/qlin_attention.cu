@@ -572,7 +572,11 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
           const float mk = s->m[k * LANES + row];
           if (mk != -INFINITY) total += s->l[k * LANES + row] * exp2_approx(mk - top);
         }
-        const float f = m_used == -INFINITY ? 0.f : exp2_approx(m_used - top);
+        if constexpr (SPLIT > 1) {  // this lane's factor, for the threads that add the copies
+          softmax_sync();           // the maxima have been read
+          s->m[at] = m_used == -INFINITY ? 0.f : exp2_approx(m_used - top);
+          softmax_sync();
+        }
         float* item = p.partial + (int64_t)(blockIdx.x + w.b * p.cache.heads + w.h) * (D + 2) * p.Rp;
         float* part = item + row;
         // 32 columns of a lane are 128 bytes, their 16-byte units swizzled by the lane
@@ -593,8 +597,8 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
 #pragma unroll
               for (int c = 0; c < CH; c += 4)
                 asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(buf + at * 128 + (((c / 4) ^ (at & 7)) << 4)),
-                             "f"(__uint_as_float(x[c]) * f), "f"(__uint_as_float(x[c + 1]) * f),
-                             "f"(__uint_as_float(x[c + 2]) * f), "f"(__uint_as_float(x[c + 3]) * f)
+                             "f"(__uint_as_float(x[c])), "f"(__uint_as_float(x[c + 1])),
+                             "f"(__uint_as_float(x[c + 2])), "f"(__uint_as_float(x[c + 3]))
                              : "memory");
             }
             if (c0 + CH < D) tmem_ld32(tmem + lanes + O_COL + c0 + CH, x);  // on its way during the exchange
@@ -613,7 +617,8 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
                              : "=f"(y.x), "=f"(y.y)
                              : "r"(buf + from * 128 + (((c >> 2) ^ r8) << 4) + ((c & 2) << 2))
                              : "memory");
-                v.x += y.x, v.y += y.y;
+                const float f = s->m[from];
+                v.x = fmaf(f, y.x, v.x), v.y = fmaf(f, y.y, v.y);
               }
               item[(c0 + c) * p.Rp + r] = v.x;
               item[(c0 + c + 1) * p.Rp + r] = v.y;
@@ -763,15 +768,15 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(co
   {
     const float4* x = reinterpret_cast<const float4*>(part + (int64_t)col * p.Rp + half * 4);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = group; i0 < parts; i0 += 4 * JOIN_GROUPS) {
-      float4 v[4];
+    for (int i0 = group; i0 < parts; i0 += 6 * JOIN_GROUPS) {
+      float4 v[6];
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
+      for (int k = 0; k < 6; k++) {
         const int i = i0 + k * JOIN_GROUPS;
         if (i < parts) v[k] = x[i * (step / 4)];
       }
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
+      for (int k = 0; k < 6; k++) {
         const int i = i0 + k * JOIN_GROUPS;
         if (i < parts) {
           const float4 f = *reinterpret_cast<const float4*>(&weight[i][half * 4]);
