@@ -495,7 +495,9 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step,
  * tokens of its sequence, and of the step's own rows (already appended) those
  * that its mask names.  out = sum_j softmax_j(scale * q . k_j) v_j; a row that
  * sees nothing gives zeros.  Query head h reads cache head h / (Hq / heads).
- * Masked rows of the step contribute nothing whatever they hold (NaN too).
+ * Masked rows of the step contribute nothing whatever they hold (NaN too); a
+ * committed token that is not finite makes the columns of the results that it
+ * reaches not finite either.
  *   T         : 1..32 rows per sequence, T * Hq / heads <= 128.
  *   Hq        : a multiple of the cache's heads.
  *   q         : [B * T, Hq * width], the cache's type, rows q_stride elements

@@ -2,6 +2,9 @@
 append with head norms and rotation, tree attention, keep, sampling, and a run
 of them together with the linears."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -108,6 +111,12 @@ APPEND = [
     ([7, 250], 33, 6, 3, 64, 32, FP, torch.bfloat16, 10, True, "pool"),
     ([31], 67, 8, 8, 256, 128, BF, torch.float32, 256, False, "nhd"),
     ([5], 2, 1, 1, 64, 16, BF, torch.float32, 0, False, "hnd"),
+    # a head whose pairs lie in other lanes, in the lane itself, or anywhere; heads of one warp of different kinds
+    ([50], 3, 3, 1, 256, 16, BF, torch.bfloat16, 128, False, "hnd"),
+    ([50], 3, 7, 3, 128, 16, FP, torch.float32, 8, False, "nhd"),
+    ([50, 1], 2, 9, 3, 128, 32, BF, torch.float32, 96, False, "hnd"),
+    ([50], 3, 5, 1, 64, 16, BF, torch.bfloat16, 64, True, "hnd"),
+    ([9, 0, 40, 17, 3], 1, 40, 5, 256, 64, FP, torch.float32, 256, True, "pool"),
 ]
 
 
@@ -262,6 +271,13 @@ ATTENTION = [
     ([3000, 10, 2999, 517, 1, 64, 128, 4000], 3, 16, 8, 64, 16, BF, "hnd", None, None),
     ([20011], 8, 8, 1, 128, 64, BF, "hnd", TREE8, None),
     ([9001], 1, 5, 5, 256, 16, FP, "nhd", None, None),
+    # more sequences than a warp has lanes, some absent, some empty
+    ([(37 * b) % 300 - (b % 7 == 3) * 1000 for b in range(45)], 2, 4, 2, 64, 16, BF, "hnd", None,
+     [(b % 5 != 2) + (b % 3 != 1) for b in range(45)]),
+    # 65 to 128 query rows of one cache head, every width
+    ([700, 64], 9, 8, 1, 256, 16, FP, "hnd", None, None),
+    ([1300], 32, 6, 2, 64, 64, BF, "nhd", [-1] + [max(0, t - 3) for t in range(31)], None),
+    ([515], 11, 7, 1, 128, 32, BF, "hnd", None, None),
 ]
 
 
@@ -386,6 +402,82 @@ def test_attention_on_another_stream_and_with_strided_rows():
     assert (wide[:, :256] == 0).all() and (wide[:, 512:] == 0).all()
 
 
+def test_attention_workspace_shared_by_two_graphs_and_two_streams_apart():
+    """Two captured calls of different shapes on one workspace, replayed in turn;
+    and two calls at once, each with its own."""
+    a, b = Case([700], 4, 2, 128, 16, seed=1), Case([90, 1500, 33], 2, 1, 256, 64, seed=2)
+    qa = torch.randn(4, 8 * 128, generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
+    qb = torch.randn(6, 5 * 256, generator=torch.Generator().manual_seed(2)).to(BF).to(DEV)
+    want = [qlin.tree_attention(c.cache, c.step, q).clone() for c, q in ((a, qa), (b, qb))]
+    need = max(qlin.tree_attention_workspace_bytes(a.cache, 1, 4, 8), qlin.tree_attention_workspace_bytes(b.cache, 3, 2, 5))
+    ws = qlin.new_workspace(need, DEV)
+    outs, graphs = [torch.empty_like(w) for w in want], []
+    for (c, q), o in zip(((a, qa), (b, qb)), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            qlin.tree_attention(c.cache, c.step, q, out=o, ws=ws, flags=qlin.FLAG_PDL)
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for g in (graphs[0], graphs[1], graphs[1], graphs[0]):
+            g.replay()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    wss = [qlin.new_workspace(need, DEV) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (c, q), o, s, w in zip(((a, qa), (b, qb)), outs, streams, wss):
+            qlin.tree_attention(c.cache, c.step, q, out=o, ws=w, stream=s, flags=qlin.FLAG_PDL)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+def test_attention_layer_after_layer_on_one_workspace():
+    """Calls in a row under programmatic dependent launch, each reading the last one's output."""
+    c = Case([600], 8, 4, 128, 16, seed=15, parents=TREE8)
+    ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, 1, 8, 8), DEV)
+    q0 = torch.randn(8, 1024, generator=torch.Generator().manual_seed(4)).to(BF).to(DEV)
+
+    def run(flags):
+        x = q0
+        for _ in range(12):
+            x = qlin.tree_attention(c.cache, c.step, x, ws=ws, flags=flags)
+        return x
+
+    want = run(0)
+    for _ in range(3):
+        assert torch.equal(run(qlin.FLAG_PDL), want)
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    code = """
+import torch
+from w6a8_quantized_linear_gb300 import qlin
+dev = torch.device("cuda:0")
+k = torch.randn(8, 2, 16, 64, device=dev).bfloat16()
+cache = qlin.KVCache(k, k.clone())
+step = qlin.KVStep(torch.arange(8, dtype=torch.int32, device=dev)[None], torch.tensor([70], dtype=torch.int32, device=dev), 2)
+q = torch.randn(2, 256, device=dev)
+kv = torch.randn(2, 128, device=dev)
+logits, u = torch.randn(3, 40000, device=dev), torch.rand(3, device=dev)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    h = qlin.kv_append(cache, step, q=q, k=kv, v=kv)
+    out = qlin.tree_attention(cache, step, h)
+    token = qlin.sample(logits, u)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, qlin.tree_attention(cache, step, qlin.kv_append(cache, step, q=q, k=kv, v=kv)))
+assert torch.equal(token, qlin.sample(logits, u))
+print("captured first")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=280)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
 # ---- keep ------------------------------------------------------------------------------------------------------------
 
 KEEP = [([10], 8, 2, 128, 16, BF, "hnd", [[0, 3, 5, 7]]), ([0, 31, 500, -1, 7], 32, 5, 64, 32, FP, "nhd",
@@ -473,6 +565,23 @@ def test_sample_against_64_bits(V, dtype):
     check_sample(x, u, min_p=f([0.05, 0.3, 0.0, 1.0]))
     check_sample(x, u, temperature=f([0.8, 1.0, 1.2, 3.0]), top_k=f([40, 400, 7, 3], dtype=torch.int32),
                  top_p=f([0.95, 0.8, 0.3, 0.99]), min_p=f([0.02, 0.01, 0.1, 0.0]))
+
+
+@pytest.mark.parametrize("V", [30000, 140001])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_sample_many_kept_tokens(V, dtype):
+    """Counts on both sides of what one CTA carries on alone, and masses that reach far down."""
+    x, u = logits_of(6, V, V + 1, dtype, banned=0.2, spread=0.3)
+    f = torch.tensor
+    k = f([1023, 1024, 1025, 2049, V // 3, V // 2], dtype=torch.int32)
+    check_sample(x, u, top_k=k)
+    check_sample(x, u, top_k=k, top_p=f([0.99, 0.999, 0.5, 0.9, 0.97, 0.2]), temperature=f([9.0, 1.0, 20.0, 3.0, 50.0, 7.0]))
+    check_sample(x, u, top_p=f([0.9999, 0.999999, 0.99, 1 - 2.0 ** -24, 0.7, 0.01]), temperature=f([9.0, 1.0, 20.0, 3.0, 50.0, 7.0]))
+
+
+def test_sample_a_large_batch_of_small_rows():
+    x, u = logits_of(3001, 257, 77)
+    check_sample(x, u, top_p=torch.full((3001,), 0.8))
 
 
 def test_sample_many_rows_and_banned_tokens():

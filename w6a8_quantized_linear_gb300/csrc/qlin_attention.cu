@@ -164,7 +164,7 @@ __device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
 // The CTA whose run holds tile x of N: floor(c N / runs) <= x < floor((c + 1) N / runs)
 __device__ __forceinline__ int cta_of(int64_t x, int64_t N, int runs) {
   const int64_t y = (x + 1) * runs - 1;
-  return y >> 32 ? (int)(y / N) : (int)((uint32_t)y / (uint32_t)N);  // y >= N - 1: N fits where y does, but for y = N - 1
+  return (y | N) >> 32 ? (int)(y / N) : (int)((uint32_t)y / (uint32_t)N);
 }
 
 // ---- PTX -------------------------------------------------------------------------

@@ -816,30 +816,57 @@ const void* sample_fn(int dtype) {
 // CTAs per row, a power of two: as many as one wave of clusters holds while
 // each has four tokens per thread (a pass costs less than an exchange saves),
 // and at least so many that two CTAs' slices (64 KB) share an SM.
-int sample_ctas(int64_t M, int64_t V, int64_t size) {
+int sample_ctas(int64_t M, int64_t V, int64_t size, int most) {
   int C = 1;
-  while (C < MAX_C && ((C * (int64_t)SAMPLE_THREADS * 4 < V && 2 * C * M <= 128) || C * (int64_t)65536 < V * size)) C *= 2;
+  while (C < most && ((C * (int64_t)SAMPLE_THREADS * 4 < V && 2 * C * M <= 128) || C * (int64_t)65536 < V * size)) C *= 2;
   return C;
 }
 
-std::once_flag g_sample_once[64];
-qlin_status g_sample_ready[64];
+struct SampleDevice {
+  std::once_flag once;
+  qlin_status ready = QLIN_ERR_CUDA;
+  int most = 8;  // CTAs of a cluster
+};
+SampleDevice g_sample[64];
 
-// the kernels' attributes, once per device
-qlin_status sample_setup() {
+// The kernels' attributes, and whether the device holds clusters of 16 with the
+// largest slice, once per device.
+qlin_status sample_setup(int* most) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return status_of(e);
   if (dev < 0 || dev >= 64) return QLIN_ERR_CUDA;
-  std::call_once(g_sample_once[dev], [dev] {
+  SampleDevice& d = g_sample[dev];
+  std::call_once(d.once, [&d] {
+    cudaError_t e = cudaSuccess;
+    int clusters = 1;
     for (int dtype : {QLIN_F32, QLIN_BF16}) {
-      cudaError_t e = cudaFuncSetAttribute(sample_fn(dtype), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SAMPLE_SMEM);
-      if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_fn(dtype), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      g_sample_ready[dev] = status_of(e);
-      if (e != cudaSuccess) return;
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(sample_fn(dtype), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SAMPLE_SMEM);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(sample_fn(dtype), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(MAX_C, 1, 1);
+      cfg.blockDim = dim3(SAMPLE_THREADS, 1, 1);
+      cfg.dynamicSmemBytes = SAMPLE_SMEM;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = MAX_C;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (e == cudaSuccess && cudaOccupancyMaxActiveClusters(&n, sample_fn(dtype), &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+      }
+      if (n < clusters) clusters = n;
     }
+    if (clusters > 0) d.most = MAX_C;
+    d.ready = status_of(e);
   });
-  return g_sample_ready[dev];
+  *most = d.most;
+  return d.ready;
 }
 
 }  // namespace
@@ -858,9 +885,11 @@ extern "C" qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logi
   for (const void* a : {(const void*)u, (const void*)temperature, (const void*)top_k, (const void*)top_p,
                         (const void*)min_p, (const void*)token, (const void*)prob})
     if (!is_aligned(a, 4)) return QLIN_ERR_INVALID_ARG;
-  qlin_status st = sample_setup();
+  int most = 0;
+  qlin_status st = sample_setup(&most);
   if (st != QLIN_OK) return st;
-  const int C = sample_ctas(M, V, dtype == QLIN_F32 ? 4 : 2);
+  if (V > (int64_t)most * (QLIN_SAMPLE_MAX_V / MAX_C)) return QLIN_ERR_UNSUPPORTED;  // a slice of 32768 per CTA
+  const int C = sample_ctas(M, V, dtype == QLIN_F32 ? 4 : 2, most);
   SampleParams p = {logits, ld, u, temperature, top_p, min_p, top_k, token, prob, (int)V,
                     (int)(((V + C - 1) / C + CHUNK * SAMPLE_WARPS - 1) / (CHUNK * SAMPLE_WARPS) * (CHUNK * SAMPLE_WARPS))};
   int c = C;
