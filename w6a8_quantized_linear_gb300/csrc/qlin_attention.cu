@@ -71,13 +71,23 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-// Tiles of the sequences before b (per cache head), and of all; a whole warp.
+// Work is measured in tiles, and GAP more between two items: what a CTA
+// loses when its run goes on with another item (the sums' way out of tensor
+// memory, other query rows, the pipeline filled again).
+//   item i of n tiles: [start, start + n), then GAP of the gap behind it
 template <int D>
-__device__ __forceinline__ void tiles_before(const AttentionParams& p, int b, int64_t* before, int64_t* all) {
+__host__ __device__ constexpr int gap() { return GAPS; }
+template <int D>
+__device__ __forceinline__ int64_t work_of(const AttentionParams& p, int64_t tiles) {  // a sequence's
+  return tiles ? (tiles + GAP) * p.cache.heads : 0;
+}
+// Work of the sequences before b, and of all; a whole warp.
+template <int D>
+__device__ __forceinline__ void work_before(const AttentionParams& p, int b, int64_t* before, int64_t* all) {
   const int lane = threadIdx.x & 31;
   int64_t x = 0, y = 0;
   for (int i = lane; i < p.step.B; i += 32) {
-    const int64_t n = tiles_of<D>(p, i);
+    const int64_t n = work_of<D>(p, tiles_of<D>(p, i));
     y += n;
     if (i < b) x += n;
   }
@@ -85,9 +95,9 @@ __device__ __forceinline__ void tiles_before(const AttentionParams& p, int b, in
   *all = warp_sum64(y);
 }
 
-// A CTA's run of tiles, item by item.
+// A CTA's run, item by item.
 struct Walk {
-  int64_t left;    // tiles of the run still ahead, this item's included
+  int64_t left;    // work of the run still ahead, this item's included
   int64_t tile;    // first tile of this item's part
   int64_t n;       // tiles of this part
   int64_t tokens;  // committed tokens of the sequence
@@ -100,23 +110,23 @@ __device__ __forceinline__ void enter(const AttentionParams& p, Walk& w) {  // t
 }
 template <int D>
 __device__ __forceinline__ bool next_item(const AttentionParams& p, Walk& w) {
-  w.left -= w.n;
+  w.left -= w.n + GAP;
   if (w.left <= 0) return false;
   w.tile = 0;
   if (++w.h == p.cache.heads) {
     w.h = 0;
     do {
-      if (++w.b >= p.step.B) return false;  // not reached: the run's tiles are counted from the same lengths
+      if (++w.b >= p.step.B) return false;  // the run ends in the gap behind the last item
       w.tokens = committed(p, w.b);
     } while (w.tokens == 0);
   }
   enter<D>(p, w);
   return true;
 }
-// Runs that N tiles are cut into: none is empty, so that the CTAs between an
-// item's first and last have all left a partial result of it.
+// Runs that work N is cut into: each at least one long, so that the CTAs
+// between an item's first and last have all left a partial result of it.
 __device__ __forceinline__ int runs_of(const AttentionParams& p, int64_t N) { return N < p.ctas ? (int)N : p.ctas; }
-// First tile of run c, floor(N c / runs), in 32 bits where they suffice.
+// Where run c begins, floor(N c / runs), in 32 bits where they suffice.
 __device__ __forceinline__ int64_t run_start(int64_t N, int c, int runs) {
   const int64_t x = N * c;
   return x >> 32 ? x / runs : (int64_t)((uint32_t)x / (uint32_t)runs);
@@ -126,9 +136,9 @@ __device__ __forceinline__ int64_t run_start(int64_t N, int c, int runs) {
 template <int D>
 __device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
   const int lane = threadIdx.x & 31;
-  int64_t tokens = lane < p.step.B ? committed(p, lane) : 0, all = tokens_to_tiles<D>(tokens);
-  for (int i = lane + 32; i < p.step.B; i += 32) all += tiles_of<D>(p, i);
-  const int64_t N = warp_sum64(all) * p.cache.heads;
+  int64_t tokens = lane < p.step.B ? committed(p, lane) : 0, all = work_of<D>(p, tokens_to_tiles<D>(tokens));
+  for (int i = lane + 32; i < p.step.B; i += 32) all += work_of<D>(p, tiles_of<D>(p, i));
+  const int64_t N = warp_sum64(all);
   const int runs = runs_of(p, N);
   Walk w = {0, 0, 0, 0, 0, 0};
   if (c >= runs) return w;
@@ -137,7 +147,7 @@ __device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
   int64_t run = 0;
   for (int i0 = 0; i0 < p.step.B; i0 += 32) {
     if (i0) tokens = i0 + lane < p.step.B ? committed(p, i0 + lane) : 0;
-    const int64_t n = tokens_to_tiles<D>(tokens) * p.cache.heads;
+    const int64_t n = work_of<D>(p, tokens_to_tiles<D>(tokens));
     int64_t inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -149,11 +159,17 @@ __device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
       const int l = __ffs(hit) - 1;
       const int64_t start = __shfl_sync(0xFFFFFFFFu, run + inc - n, l);
       w.tokens = __shfl_sync(0xFFFFFFFFu, tokens, l);
-      const int64_t per = tokens_to_tiles<D>(w.tokens);
+      const int64_t tiles = tokens_to_tiles<D>(w.tokens), per = tiles + GAP;
       w.b = i0 + l;
       w.h = (int)run_start(x0 - start, 1, (int)per);  // tiles of one head: below 2^31
       w.tile = x0 - start - w.h * per;
-      w.n = per - w.tile < w.left ? per - w.tile : w.left;
+      if (w.tile < tiles) {
+        enter<D>(p, w);
+      } else {  // in a gap: on with the item behind it
+        w.left += w.tile - tiles;
+        w.n = 0;
+        if (!next_item<D>(p, w)) w.left = 0;
+      }
       return w;
     }
     run += __shfl_sync(0xFFFFFFFFu, inc, 31);
@@ -161,7 +177,7 @@ __device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
   w.left = 0;
   return w;
 }
-// The CTA whose run holds tile x of N: floor(c N / runs) <= x < floor((c + 1) N / runs)
+// The CTA whose run holds place x of N: floor(c N / runs) <= x < floor((c + 1) N / runs)
 __device__ __forceinline__ int cta_of(int64_t x, int64_t N, int runs) {
   const int64_t y = (x + 1) * runs - 1;
   return (y | N) >> 32 ? (int)(y / N) : (int)((uint32_t)y / (uint32_t)N);
@@ -670,7 +686,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(co
   const bool live = len >= 0 && warp < 8 && row < p.R && t < rows;  // a warp per row for its weights
   if (warp == 8) {
     int64_t before, all;
-    tiles_before<D>(p, b, &before, &all);
+    work_before<D>(p, b, &before, &all);
     if (lane == 0) range[0] = before, range[1] = all;
   }
   if (len >= 0 && warp == 0) {
@@ -705,8 +721,8 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(co
     }
   }
   // this item's tiles among all, and the CTAs whose runs hold them
-  const int64_t per = tiles_of<D>(p, b), N = range[1] * p.cache.heads;
-  const int64_t start = range[0] * p.cache.heads + h * per;
+  const int64_t per = tiles_of<D>(p, b), N = range[1];
+  const int64_t start = range[0] + h * (per + GAP);
   const int runs = runs_of(p, N);
   const int first = per ? cta_of(start, N, runs) : 0;
   const int parts = per ? cta_of(start + per - 1, N, runs) - first + 1 : 0;
