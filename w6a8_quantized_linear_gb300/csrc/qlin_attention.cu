@@ -71,12 +71,13 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-// Work is measured in tiles, and GAP more between two items: what a CTA
-// loses when its run goes on with another item (the sums' way out of tensor
-// memory, other query rows, the pipeline filled again).
-//   item i of n tiles: [start, start + n), then GAP of the gap behind it
-template <int D>
-__host__ __device__ constexpr int gap() { return GAPS; }
+// Work is measured in tiles, and GAP more between two items: what a CTA loses
+// when its run goes on with another item (the sums' way out of tensor memory,
+// other query rows, the pipeline filled again: 5 to 7 us against 1.5 us for a
+// tile; with 1, 2, 3, 4 and 6, five items of 275 tiles took 31.1, 29.9, 28.9,
+// 29.5 and 29.2 us, 152 of 4 to 14 tiles 33.5, 32.0, 30.8, 31.5 and 32.2).  An
+// item's n tiles are [start, start + n), and the gap follows.
+constexpr int GAP = 3;
 template <int D>
 __device__ __forceinline__ int64_t work_of(const AttentionParams& p, int64_t tiles) {  // a sequence's
   return tiles ? (tiles + GAP) * p.cache.heads : 0;
