@@ -227,6 +227,12 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+// One lane of the warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
 // Matrix descriptor of a 128-byte-swizzled operand: rows of 64 16-bit values
 // (128 bytes, on a 1024-byte boundary every eighth), `lbo` bytes between its
 // 64-wide panels where the panels run along M or N, 1024 between groups of
@@ -375,24 +381,30 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
       if (!ok)
         for (uint32_t j = i > NB ? i - NB : 0; j < i; j++) (void)mbar_wait(&s->full[j % NB], (j / NB) & 1);
     } else if (warp == ISSUER) {
-      // ---- MMA: one thread issues
-      if (lane == 0) {
-        constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u;
-        constexpr uint32_t id_s = mma_idesc_f16(128, TK) | type;
-        constexpr uint32_t id_o = mma_idesc_f16(128, D) | type | (1u << 16);  // B along N
-        uint32_t n = 0, seg = 0, dirty = 0;
-        bool ok = true;
-        do {
-          ok = role_wait(&s->q_full, seg & 1, s, p.status);
-          tc_fence_after();
-          for (int64_t t = 0; t <= w.n && ok; t++) {
-            if (t < w.n) {  // S(t)
-              const uint32_t m = n + (uint32_t)t, slot = (2 * m) % NB, use = (2 * m) / NB;
-              ok = role_wait(&s->full[slot], use & 1, s, p.status);
-              if (ok && m >= 2) ok = role_wait(&s->s_free[m & 1], ((m >> 1) - 1) & 1, s, p.status);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t kb = ring + slot * TB;
+      // ---- MMA: the whole warp keeps the books, so that descriptors stay in
+      // uniform registers, and one elected thread issues (built by that thread
+      // alone they cost it 70 cycles an MMA, and it bound the kernel)
+      constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u;
+      constexpr uint32_t id_s = mma_idesc_f16(128, TK) | type;
+      constexpr uint32_t id_o = mma_idesc_f16(128, D) | type | (1u << 16);  // B along N
+      uint32_t n = 0, seg = 0, dirty = 0;
+      uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // ring places of the next keys and values, and their parities
+      bool ok = true;
+      do {
+        ok = __all_sync(0xFFFFFFFFu, role_wait(&s->q_full, seg & 1, s, p.status));
+        const int tiles = __shfl_sync(0xFFFFFFFFu, (int)w.n, 0);
+        const int full_tiles = __shfl_sync(0xFFFFFFFFu, (int)min(w.n, w.tokens / TK - w.tile), 0);
+        tc_fence_after();
+        for (int t = 0; t <= tiles && ok; t++) {
+          if (t < tiles) {  // S(t)
+            const uint32_t m = __shfl_sync(0xFFFFFFFFu, n + t, 0);
+            ok = role_wait(&s->full[ks], kp, s, p.status);
+            if (ok && m >= 2) ok = role_wait(&s->s_free[m & 1], ((m >> 1) - 1) & 1, s, p.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t slot = __shfl_sync(0xFFFFFFFFu, ks, 0), kb = ring + slot * TB;
+            if (elect_one()) {
 #pragma unroll
               for (int e = 0; e < D / 16; e++)
                 mma_smem_a(tmem + S_COL + (m & 1) * TK,
@@ -401,32 +413,41 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
               mma_commit(&s->empty[slot]);
               mma_commit(&s->s_full[m & 1]);
             }
-            if (t > 0) {  // O += P(t - 1) V(t - 1)
-              const uint32_t m = n + (uint32_t)t - 1, slot = (2 * m + 1) % NB, use = (2 * m + 1) / NB;
-              ok = role_wait(&s->full[slot], use & 1, s, p.status);
-              const bool ragged = (w.tile + t) * TK > w.tokens;  // the sequence's last tile, not full
-              if (ok && ragged) mbar_arrive(&s->v_dirty);
-              if (ok) ok = role_wait(&s->p_full[m & 1], (m >> 1) & 1, s, p.status);
-              if (ok && ragged) ok = role_wait(&s->v_clean, dirty++ & 1, s, p.status);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t vb = ring + slot * TB;
+            __syncwarp();
+            ks += 2;
+            if (ks >= NB) ks -= NB, kp ^= 1;
+          }
+          if (t > 0) {  // O += P(t - 1) V(t - 1)
+            const uint32_t m = __shfl_sync(0xFFFFFFFFu, n + t - 1, 0);
+            ok = role_wait(&s->full[vs], vp, s, p.status);
+            const bool ragged = t > full_tiles;  // the sequence's last tile, not full
+            if (ok && ragged && lane == 0) mbar_arrive(&s->v_dirty);
+            if (ok) ok = role_wait(&s->p_full[m & 1], (m >> 1) & 1, s, p.status);
+            if (ok && ragged) ok = role_wait(&s->v_clean, dirty++ & 1, s, p.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t slot = __shfl_sync(0xFFFFFFFFu, vs, 0), vb = ring + slot * TB;
+            if (elect_one()) {
 #pragma unroll
               for (int e = 0; e < TK / 16; e++)
                 mma_tmem_a(tmem + O_COL, tmem + P_COL + (m & 1) * (TK / 2) + e * 8, swizzled_desc(vb + e * 2048, TK * 128),
                            id_o, t > 1 || e > 0);
               mma_commit(&s->empty[slot]);
               mma_commit(&s->p_free[m & 1]);
-              if (t == w.n) mma_commit(&s->o_full);
+              if (t == tiles) mma_commit(&s->o_full);
             }
+            __syncwarp();
+            vs += 2;
+            if (vs >= NB) vs -= NB, vp ^= 1;
           }
-          n += (uint32_t)w.n;
-          seg++;
-        } while (ok && next_item<D>(p, w));
-        if (!ok) {  // the products in flight end before tensor memory is freed
-          mma_commit(&s->drained);
-          (void)mbar_wait(&s->drained, 0);
         }
+        n += tiles;
+        seg++;
+      } while (ok && next_item<D>(p, w));
+      if (!ok && elect_one()) {  // the products in flight end before tensor memory is freed
+        mma_commit(&s->drained);
+        (void)mbar_wait(&s->drained, 0);
       }
     } else if (warp == CLEANER) {
       // ---- cleaner: the rows behind the last token hold whatever the page or
