@@ -243,7 +243,7 @@ __device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr, uint32_t lbo) {
 }
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // below 2^-126: 0
   return y;
 }
 
@@ -518,20 +518,19 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
               else
                 tmem_ld32(st + c0, reinterpret_cast<uint32_t*>(x));
               tmem_wait_ld();
-              if (valid < CW) {
-#pragma unroll
-                for (int c = 0; c < CX; c++) x[c] = c0 + c < valid ? x[c] * p.scale_log2 : -INFINITY;
-              } else {
-#pragma unroll
-                for (int c = 0; c < CX; c++) x[c] *= p.scale_log2;
-              }
             };
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int c0 = 0; c0 < CW; c0 += CX) {
               scores(c0);
+              if (valid < CW) {
 #pragma unroll
-              for (int c = 0; c < CX; c++) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+                for (int c = 0; c < CX; c++)
+                  if (c0 + c < valid) mx[c & 3] = fmaxf(mx[c & 3], x[c] * p.scale_log2);
+              } else {
+#pragma unroll
+                for (int c = 0; c < CX; c++) mx[c & 3] = fmaxf(mx[c & 3], x[c] * p.scale_log2);
+              }
             }
             const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             float keep = 1.f;
@@ -569,15 +568,21 @@ __global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention
             }
             const uint32_t pt = tmem + lanes + P_COL + (m & 1) * (TK / 2) + copy * (CW / 2);
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
             for (int c0 = CW - CX; c0 >= 0; c0 -= CX) {
               if (c0 != CW - CX) scores(c0);
               uint32_t w2[CX / 2];
 #pragma unroll
+              for (int c = 0; c < CX; c++) x[c] = exp2_approx(fmaf(x[c], p.scale_log2, -m_ref));
+              if (valid < CW) {
+#pragma unroll
+                for (int c = 0; c < CX; c++)
+                  if (c0 + c >= valid) x[c] = 0.f;
+              }
+#pragma unroll
               for (int c = 0; c < CX; c += 2) {
-                const float a = exp2_approx(x[c] - m_ref), b2 = exp2_approx(x[c + 1] - m_ref);
-                sum[(c >> 1) & 3] += a + b2;
-                w2[c / 2] = pack2(a, b2, T());
+                sum[(c >> 1) & 3] += x[c] + x[c + 1];
+                w2[c / 2] = pack2(x[c], x[c + 1], T());
               }
               if constexpr (CX == 32)
                 tmem_st16(pt + c0 / 2, w2);
