@@ -289,9 +289,17 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, Attent
 // second product; keys and values are read by the tensor cores straight from
 // the ring that TMA fills (128-byte swizzle; V as the transposed operand).
 //
+// Bound by the stream of keys and values: a tile's 64 KB take an SM 1.5 us at
+// the measured copy bandwidth, its products 0.5 to 0.7 us, its softmax 0.6 us
+// where the warps share it.  Measured (both launches): 48 query rows over
+// 131k tokens of 4 heads of 256, 97.7 us for 537 MB (5.5 TB/s, 0.81 of the
+// copy; the stream itself runs at 0.97, the rest is start, joining and the
+// SMs' different ends); 24 rows over 8 sequences, 111 us for 661 MB (0.88);
+// width 64 streams 0.66 of the copy, bound by the softmax's latency per tile.
+//
 // A warp reaches 32 lanes, so with few rows most softmax warps would idle while
-// one takes longer over a tile (128 tokens: 1.9 us measured) than the tile's
-// 64 KB take from memory (1.5 us).  SPLIT = 2 or 4 therefore lays the query
+// one takes longer over a tile (128 tokens: 1.9 us when this was measured) than
+// the tile's bytes take.  SPLIT = 2 or 4 therefore lays the query
 // rows down that many times (up to 64 or 32 rows), and each copy's warps take
 // their own part of a tile's tokens: P is zero elsewhere, once and for all, and
 // each copy's lanes of O hold its tokens' sums, which are added at the item's
@@ -300,8 +308,9 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, Attent
 // A row's maximum may grow by 2^8 before its sums are rescaled in tensor
 // memory: weights are relative to a maximum of the past, at most 2^8, which
 // fp16 holds.
+// (At most 128 registers, so that blocks of the second launch find room beside.)
 template <typename T, int D, int SPLIT>
-__global__ void __launch_bounds__(ATT_THREADS, SPLIT > 1 ? 2 : 1) qlin_attention_kernel(const __grid_constant__ AttentionParams p) {
+__global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __grid_constant__ AttentionParams p) {
   extern __shared__ uint8_t raw[];
   __shared__ AttentionShared sh;
   constexpr int TK = tile_tokens(D), TB = tile_bytes(D), NB = ring_buffers(D), PANELS = D / 64;
