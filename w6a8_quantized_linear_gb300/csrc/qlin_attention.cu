@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
         if (!softmax_bar(ok)) break;
         tc_fence_after();
         // the copies' sums on a common maximum, added through the query rows'
-        // memory (their product is done), 32 columns at a time, and
+        // memory (their product is done), 32 or 64 columns at a time, and
         // written [column][row]: a warp's store is one run
         float top = -INFINITY, total = 0.f;
 #pragma unroll
@@ -631,14 +631,22 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
         }
         float* item = p.partial + (int64_t)(blockIdx.x + w.b * p.cache.heads + w.h) * (D + 2) * p.Rp;
         float* part = item + row;
-        // 32 columns of a lane are 128 bytes, their 16-byte units swizzled by the lane
-        constexpr int CH = 32, BUFFERS = q_bytes(D) >= 2 * ATT_ROWS * CH * 4 ? 2 : 1;
+        // a lane's columns lie together, their 16-byte units swizzled by the lane
+        // (64 at a time where registers allow)
+        constexpr int CH = (D == 256 && SPLIT > 1) || (D == 128 && SPLIT == 4) ? 64 : 32, UNITS = CH / 16;  // a thread's own of them
+        constexpr int BUFFERS = q_bytes(D) >= 2 * ATT_ROWS * CH * 4 ? 2 : 1;
         uint32_t x[CH];
-        if (warp < active) tmem_ld32(tmem + lanes + O_COL, x);
+        auto fetch = [&](int c0) {
+#pragma unroll
+          for (int c = 0; c < CH; c += 32) tmem_ld32(tmem + lanes + O_COL + c0 + c, x + c);
+        };
+        constexpr bool EARLY = CH == 32 && SPLIT > 1;  // the next columns on their way during the exchange
+        if (EARLY && warp < active) fetch(0);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += CH) {
           const uint32_t buf = q_smem + c0 / CH % BUFFERS * (ATT_ROWS * CH * 4);
           if (warp < active) {
+            if (!EARLY) fetch(c0);
             tmem_wait_ld();
             if constexpr (SPLIT == 1) {
               if (live) {
@@ -648,32 +656,38 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
             } else if (live) {
 #pragma unroll
               for (int c = 0; c < CH; c += 4)
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(buf + at * 128 + (((c / 4) ^ (at & 7)) << 4)),
-                             "f"(__uint_as_float(x[c])), "f"(__uint_as_float(x[c + 1])),
-                             "f"(__uint_as_float(x[c + 2])), "f"(__uint_as_float(x[c + 3]))
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + at * (CH * 4) + (((c / 4) ^ (at & 7)) << 4)),
+                             "r"(x[c]), "r"(x[c + 1]), "r"(x[c + 2]), "r"(x[c + 3])
                              : "memory");
             }
-            if (c0 + CH < D) tmem_ld32(tmem + lanes + O_COL + c0 + CH, x);  // on its way during the exchange
+            if (EARLY && c0 + CH < D) fetch(c0 + CH);
           }
           if constexpr (SPLIT > 1) {
             softmax_sync();
-            // two columns of every eighth row per thread
-            const int r8 = at & 7, c = at >> 3 << 1;
+            // CH / 16 columns of every eighth row per thread
+            const int r8 = at & 7, c = (at >> 3) * UNITS;
             for (int r = r8; r < p.R; r += 8) {
-              float2 v = make_float2(0.f, 0.f);
+              float v[UNITS];
+#pragma unroll
+              for (int e = 0; e < UNITS; e++) v[e] = 0.f;
 #pragma unroll
               for (int k = 0; k < SPLIT; k++) {
-                float2 y;
                 const int from = k * LANES + r;  // from & 7 = r8
-                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                             : "=f"(y.x), "=f"(y.y)
-                             : "r"(buf + from * 128 + (((c >> 2) ^ r8) << 4) + ((c & 2) << 2))
-                             : "memory");
                 const float f = s->m[from];
-                v.x = fmaf(f, y.x, v.x), v.y = fmaf(f, y.y, v.y);
+                const uint32_t a = buf + from * (CH * 4) + (((c >> 2) ^ r8) << 4) + ((c & 2) << 2);
+                float y[4];
+                if constexpr (UNITS == 4)
+                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                               : "=f"(y[0]), "=f"(y[1]), "=f"(y[2]), "=f"(y[3])
+                               : "r"(a)
+                               : "memory");
+                else
+                  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(y[0]), "=f"(y[1]) : "r"(a) : "memory");
+#pragma unroll
+                for (int e = 0; e < UNITS; e++) v[e] = fmaf(f, y[e], v[e]);
               }
-              item[(c0 + c) * p.Rp + r] = v.x;
-              item[(c0 + c + 1) * p.Rp + r] = v.y;
+#pragma unroll
+              for (int e = 0; e < UNITS; e++) item[(c0 + c + e) * p.Rp + r] = v[e];
             }
             // with two buffers the next chunk's barrier stands between these reads and the writes after it
             if (BUFFERS == 1 && c0 + CH < D) softmax_sync();
