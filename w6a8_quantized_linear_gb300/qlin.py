@@ -439,6 +439,8 @@ class KVStep:
 
 
 _fns: dict = {}
+_F32, _I32 = torch.float32, torch.int32
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _fn(name: str):
@@ -456,13 +458,13 @@ def _same_device(index: int, *tensors) -> None:
                              + (f"cuda:{index}" if index >= 0 else "the CPU, not on a GPU"))
     if index < 0:
         raise ValueError("the tensors are on the CPU, not on a GPU")
-    if index != torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors are on cuda:{index}, but cuda:{torch._C._cuda_getDevice()} is the current device")
+    if index != _current_device():
+        raise ValueError(f"the tensors are on cuda:{index}, but cuda:{_current_device()} is the current device")
 
 
 def _raw_stream(stream, index: int) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
+        return _current_stream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -480,7 +482,9 @@ def _rows(t, n: int, width: int, dtype, what: str) -> int:
     """Row stride of a [n, width] (or [n, heads, D]) tensor of ``dtype``."""
     if t.dtype is dtype:
         if t.is_contiguous():
-            if t.shape == (n, width) or (t.dim() == 3 and t.shape[0] == n and t.numel() == n * width):
+            if t.shape == (n, width):
+                return width
+            if t.dim() == 3 and t.shape[0] == n and t.numel() == n * width:
                 return width
         elif t.dim() == 2 and t.shape == (n, width) and t.stride(1) == 1:
             return t.stride(0) if n > 1 else width
@@ -500,7 +504,7 @@ def _heads(t, width: int, what: str) -> int:
 def _floats(t, n: int, what: str):
     if t is None:
         return None
-    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _F32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous float32 tensor of {n} values")
     return t.data_ptr()
 
@@ -508,7 +512,7 @@ def _floats(t, n: int, what: str):
 def _ints(t, n: int, what: str):
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _I32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of {n} values")
     return t.data_ptr()
 
@@ -555,11 +559,14 @@ def kv_append(cache: KVCache, step: KVStep, q=None, k=None, v=None, q_gamma=None
         nt = turns.numel()
         if turns.dtype is not torch.int64 or not turns.is_contiguous():
             raise ValueError("turns must come from rope_turns")
-    _check(_fn("qlin_kv_append")(
-        cache._ref, step._ref, Hq, DTYPES.get(dtype, -1), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+    status = _fn("qlin_kv_append")(
+        cache._ref, step._ref, Hq, DTYPES.get(dtype, -1), None if q is None else q.data_ptr(), qs,
+        None if k is None else k.data_ptr(), ks, None if v is None else v.data_ptr(), vs,
         _floats(q_gamma, D, "q_gamma"), _floats(k_gamma, D, "k_gamma"), eps, turns.data_ptr() if nt else None, nt,
-        1 if pairs else 0, q_out.data_ptr() if q is not None else None, os_, _ptr(ws), 0 if ws is None else ws.numel(),
-        flags, _raw_stream(stream, dev)), "kv_append")
+        1 if pairs else 0, None if q is None else q_out.data_ptr(), os_, None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.numel(), flags, _current_stream(dev) if stream is None else _raw_stream(stream, dev))
+    if status:
+        _check(status, "kv_append")
     return q_out
 
 
