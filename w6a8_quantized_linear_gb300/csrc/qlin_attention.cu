@@ -611,7 +611,10 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
         if (ok) ok = __all_sync(0xFFFFFFFFu, role_wait(&s->o_full, seg & 1, s, p.status));
         s->m[at] = m_used;
         s->l[at] = l;
-        if (!softmax_bar(ok)) break;
+        if (!softmax_bar(ok)) {
+          if (at == 0) (void)mbar_wait(&s->q_full, seg & 1);  // nothing leaves while its copies are in flight
+          break;
+        }
         tc_fence_after();
         // the copies' sums on a common maximum, added through the query rows'
         // memory (their product is done), 32 or 64 columns at a time, and
