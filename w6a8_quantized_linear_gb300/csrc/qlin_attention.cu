@@ -292,7 +292,7 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, Attent
 // Bound by the stream of keys and values: a tile's 64 KB take an SM 1.5 us at
 // the measured copy bandwidth, its products 0.5 to 0.7 us, its softmax 0.6 us
 // where the warps share it.  Measured (both launches): 48 query rows over
-// 131k tokens of 4 heads of 256, 96.1 us for 537 MB (5.6 TB/s, 0.82 of the
+// 131k tokens of 4 heads of 256, 95.7 us for 537 MB (5.6 TB/s, 0.82 of the
 // copy; the stream itself runs at 0.97, the rest is start, joining and the
 // SMs' different ends); 18 rows over 8 sequences of 8 heads of 128, 111 us for 661 MB (0.88);
 // width 64 streams 0.66 of the copy, bound by the softmax's latency per tile.
@@ -803,6 +803,13 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(co
   if (len < 0 || rows == 0) return;
   const int64_t step = (int64_t)(D + 2) * p.Rp;
   const float* part = p.partial + (int64_t)(first + item) * step + r0;
+  // the first partial results are on their way while the weights are formed
+  constexpr int AHEAD = 6;
+  const float4* x = reinterpret_cast<const float4*>(part + (int64_t)col * p.Rp + half * 4);
+  float4 early[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; k++)
+    if (group + k * JOIN_GROUPS < parts) early[k] = x[(group + k * JOIN_GROUPS) * (step / 4)];
   if (live) {
     constexpr int PER = (ATT_MAX_CTAS + 31) / 32;
     float pm[PER], pl[PER], m = mine;
@@ -835,24 +842,23 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(co
   }
   __syncthreads();
   {
-    const float4* x = reinterpret_cast<const float4*>(part + (int64_t)col * p.Rp + half * 4);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = group; i0 < parts; i0 += 6 * JOIN_GROUPS) {
-      float4 v[6];
+    auto add = [&](int i, const float4& v) {
+      const float4 f = *reinterpret_cast<const float4*>(&weight[i][half * 4]);
+      acc.x = fmaf(f.x, v.x, acc.x), acc.y = fmaf(f.y, v.y, acc.y);
+      acc.z = fmaf(f.z, v.z, acc.z), acc.w = fmaf(f.w, v.w, acc.w);
+    };
 #pragma unroll
-      for (int k = 0; k < 6; k++) {
-        const int i = i0 + k * JOIN_GROUPS;
-        if (i < parts) v[k] = x[i * (step / 4)];
-      }
+    for (int k = 0; k < AHEAD; k++)
+      if (group + k * JOIN_GROUPS < parts) add(group + k * JOIN_GROUPS, early[k]);
+    for (int i0 = group + AHEAD * JOIN_GROUPS; i0 < parts; i0 += AHEAD * JOIN_GROUPS) {
+      float4 v[AHEAD];
 #pragma unroll
-      for (int k = 0; k < 6; k++) {
-        const int i = i0 + k * JOIN_GROUPS;
-        if (i < parts) {
-          const float4 f = *reinterpret_cast<const float4*>(&weight[i][half * 4]);
-          acc.x = fmaf(f.x, v[k].x, acc.x), acc.y = fmaf(f.y, v[k].y, acc.y);
-          acc.z = fmaf(f.z, v[k].z, acc.z), acc.w = fmaf(f.w, v[k].w, acc.w);
-        }
-      }
+      for (int k = 0; k < AHEAD; k++)
+        if (i0 + k * JOIN_GROUPS < parts) v[k] = x[(i0 + k * JOIN_GROUPS) * (step / 4)];
+#pragma unroll
+      for (int k = 0; k < AHEAD; k++)
+        if (i0 + k * JOIN_GROUPS < parts) add(i0 + k * JOIN_GROUPS, v[k]);
     }
     auto add_own = [&](int j, float value) {  // only what a row sees: what it does not may be NaN
       const float* f = &own[j][half * 4];
