@@ -523,6 +523,33 @@ def test_keep_in_place_lengths_and_bad_lists():
     assert c.step.len.tolist() == [23] + [20] * (len(lists) - 1)
 
 
+def test_offsets_past_32_bits_and_a_table_inside_a_wider_one():
+    """The same step on the last pages of a cache of 2.3e9 elements and on a small
+    one, through a table that is a slice of a wider one: the same bits."""
+    heads, page, D, T, n = 4, 64, 128, 4, 300
+    many = 70001  # pages of 32768 elements
+    g = torch.Generator().manual_seed(3)
+    k0, v0 = (torch.randn(6, heads, page, D, generator=g).to(BF).to(DEV) for _ in range(2))
+    q, k, v = (torch.randn(T, h * D, generator=g).to(DEV) for h in (8, heads, heads))
+    turns = qlin.rope_turns(1e6, D, device=DEV)
+    results = []
+    for pages, order in ((6, [2, 0, 5, 1, 4, 3]), (many, [many - 1, many - 5, 66000, many - 2, 65537, 69000])):
+        ck, cv = (torch.empty(pages, heads, page, D, dtype=BF, device=DEV) for _ in range(2))
+        ck[torch.tensor(order, device=DEV)], cv[torch.tensor(order, device=DEV)] = k0, v0
+        wide = torch.full((1, 9), -3, dtype=torch.int32, device=DEV)
+        wide[0, 2:8] = i32(order)
+        step = qlin.KVStep(wide[:, 2:8], i32([n]), T, depth=i32([0, 1, 1, 2]), mask=i32([1, 3, 5, 13]))
+        cache = qlin.KVCache(ck, cv)
+        h = qlin.kv_append(cache, step, q=q, k=k, v=v, turns=turns)
+        out = qlin.tree_attention(cache, step, h)
+        qlin.kv_keep(cache, step, i32([[0, 2, 3, 0]]), i32([3]), len_out=step.len)
+        at = torch.tensor(order, device=DEV)
+        results.append((h, out, ck[at], cv[at], step.len.clone()))
+        del ck, cv, cache, step
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
 # ---- sample ----------------------------------------------------------------------------------------------------------
 
 def logits_of(M, V, seed, dtype=torch.float32, banned=0.0, spread=2.5):
