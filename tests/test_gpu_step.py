@@ -633,6 +633,29 @@ def test_sample_ties_go_to_the_lowest_index(V):
     check_sample(x, u, temperature=torch.zeros(8))
 
 
+@pytest.mark.parametrize("V", [4097, 40000, 131071])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_sample_uneven_rows(V, dtype):
+    """The likely tokens all in one place, or few allowed ones: what the row's parts hand on is far from even."""
+    x, u = logits_of(8, V, V + 3)
+    x[0] = x[0].sort(descending=True).values
+    x[1] = x[1].sort().values
+    x[2, torch.arange(V) % (V // 5) != 7] = -math.inf  # five or six are allowed
+    x[3, V // 2: V // 2 + 300] += 20
+    x[4, : V // 2] = -math.inf
+    x[5] = -9.0
+    x[5, V - 3:] = 4.0
+    x[6, V // 3: V // 3 + 70] = math.inf
+    x[7, 128:] -= 40
+    x = x.to(dtype)
+    f = torch.tensor
+    for k in ([1, 1, 3, 1, 1, 2, 1, 1], [100, 90, 400, 250, 33, 5, 69, 127], [900, 1024, 2, 301, 1000, 700, 71, 128]):
+        k = f(k, dtype=torch.int32)
+        check_sample(x, u, top_k=k)
+        check_sample(x, u, top_k=k, top_p=f([0.9, 0.99, 0.8, 0.999, 0.5, 0.95, 0.7, 0.97]), temperature=f([1.0, 0.7, 9.0, 2.0, 1.0, 3.0, 1.0, 20.0]),
+                     min_p=f([0.0, 0.1, 0.0, 0.02, 0.3, 0.0, 0.0, 0.0]))
+
+
 def test_sample_edges():
     inf, nan = math.inf, math.nan
     rows = [[-inf] * 5, [0, 1, nan, 2, 3], [inf, 0, inf, 1, -inf], [-inf, -inf, 4, -inf, -inf], [3e38, -3e38, 0, 3e38, 1e38],

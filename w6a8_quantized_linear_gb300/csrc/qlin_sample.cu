@@ -10,6 +10,7 @@
 // (42-bit fractions), so all sums are exact and independent of their order.
 // (Bitonic sorts of the survivors and of a bin, in place of those steps,
 // measured 1.4 us slower on one and eight rows.)
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 
@@ -26,6 +27,7 @@ constexpr int MAX_C = 16;                // CTAs of a row's cluster, at most
 constexpr int CHUNK = 128;               // consecutive tokens that a warp takes at once, four per lane
 constexpr int FEW = 128;                 // a bin of at most this many tokens is settled by comparing all pairs, four threads each
 constexpr int LIST = 2048;               // so many tokens, what top-k may leave, are carried on by one CTA
+constexpr int OWN = 64;                  // of them from one warp at most
 constexpr int ONE_BITS = 42;             // weights are multiples of 2^-42; 2^19 of them sum below 2^62
 constexpr uint32_t ALL = 0xFFFFFFFFu;
 
@@ -48,7 +50,7 @@ struct SampleParams {
 };
 
 struct Round {  // what the CTAs of a row tell each other outside the histograms
-  uint32_t kmx, kmn, klow, nan, top, pad;
+  uint32_t kmx, kmn, nan, top, left, pad;
   unsigned long long sum;
 };
 struct __align__(16) Candidate {
@@ -61,10 +63,11 @@ struct SampleShared {
   unsigned long long mass[BINS];         // the row's
   uint32_t count[BINS];
   Candidate few[FEW];
+  uint32_t reach[MAX_C * SAMPLE_WARPS];  // by warps of the row: the key that so many of its tokens reach
   Round peer[2][MAX_C];
   uint2 range[MAX_C];
   unsigned long long warp_sum[SAMPLE_WARPS];
-  uint32_t warp_a[SAMPLE_WARPS], warp_b[SAMPLE_WARPS], warp_c[SAMPLE_WARPS], warp_d[SAMPLE_WARPS], warp_e[SAMPLE_WARPS];
+  uint32_t warp_a[SAMPLE_WARPS], warp_b[SAMPLE_WARPS], warp_c[SAMPLE_WARPS], warp_d[SAMPLE_WARPS];
   uint32_t table[32];  // 2^(i/32) in [2^31, 2^32)
   int pick;
   uint32_t pick_key, pick_index, pick_count, filled;
@@ -567,8 +570,8 @@ __device__ __forceinline__ void choose(const R& r, const Kept& kept, float min_p
 // Bound by latency, not by the bytes (0.6 us for 8 rows of 131071): reading
 // (2 us), the exchanges between the CTAs (1 to 2 us each with 16 CTAs), and
 // passes over 4 to 64 tokens per thread; for many rows by the instructions of
-// those passes.  Measured: 8 rows of 131071, all filters, 20.3 us; 1 row of
-// 32000, top-p, 17.9 us; 64 rows of 262144 in bf16, top-k and top-p, 54.7 us;
+// those passes.  Measured: 8 rows of 131071, all filters, 17.1 us; 1 row of
+// 32000, top-p, 17.9 us; 64 rows of 262144 in bf16, top-k and top-p, 43.8 us;
 // top-p alone has to weigh every token: 1 row of 131071, 32 us.  CTAs of a
 // row: with 4, 8 and 16, 8 rows of 131071 take 25.6, 20.2 and 20.4 us, 1 row
 // of 32000 25.3, 19.4 and 18.6 us, 64 rows of 262144 55.6, 54.9 and 82.9 us.
@@ -630,28 +633,29 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
     kmn = __reduce_min_sync(ALL, in ? kmn : ALL);
     nan = __any_sync(ALL, in && nan);
   };
-  // A logit that top_k tokens reach at least: of the row's warps with a full
-  // part, each with its 32 lanes' largest tokens, the least j-th largest,
-  // j * warps >= top_k.  (The other warps take none lower.)
+  // A logit that top_k tokens reach at least: each of the row's warps with a
+  // full part gives the j-th of its 32 lanes' largest tokens, and the
+  // ceil(top_k / j)-th of these is reached by j tokens in as many warps.  With j
+  // about top_k over the warps, some 1.8 top_k tokens of normally distributed
+  // logits reach it (the least of all warps' would be reached by 3 to 40 top_k).
   const uint32_t full = (uint32_t)p.V / (uint32_t)(r.w1 - r.w0);
-  const uint32_t per_warp = top_k > 0 && full ? (top_k + full - 1) / full : 33;
-  uint32_t klow = C > 1 && per_warp <= 32 ? ALL : 0;
-  if (klow && r.w1 <= tokens) {
+  const uint32_t per_warp = C > 1 && top_k > 0 && top_k < p.V && full ? top_k / full + 1 : 33;
+  uint32_t reach = 0;
+  if (per_warp <= 32 && r.w1 <= tokens) {
     uint32_t key = kmx;
     for (uint32_t j = 0; j < per_warp; j++) {
-      klow = __reduce_max_sync(ALL, key);
-      if (lane == __ffs(__ballot_sync(ALL, key == klow)) - 1) key = 0;
+      reach = __reduce_max_sync(ALL, key);
+      if (lane == __ffs(__ballot_sync(ALL, key == reach)) - 1) key = 0;
     }
   }
   join(true);
   if (lane == 0) {
     s->warp_a[warp] = nan, s->warp_b[warp] = top, s->warp_c[warp] = kmx, s->warp_d[warp] = kmn;
-    s->warp_e[warp] = klow;
+    if (C > 1) s->reach[r.rank * SAMPLE_WARPS + warp] = reach;
   }
   __syncthreads();
   const int from = lane % SAMPLE_WARPS;
   nan = s->warp_a[from], top = s->warp_b[from], kmx = s->warp_c[from], kmn = s->warp_d[from];
-  klow = __reduce_min_sync(ALL, s->warp_e[from]);
   join(true);
   if (C > 1) {
     cluster_wait();  // every CTA of the row has started
@@ -659,20 +663,22 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
       const Round* at = &s->peer[0][r.rank];
       to_peer(&at->kmx, threadIdx.x, kmx);
       to_peer(&at->kmn, threadIdx.x, kmn);
-      to_peer(&at->klow, threadIdx.x, klow);
       to_peer(&at->nan, threadIdx.x, nan);
       to_peer(&at->top, threadIdx.x, top);
+    }
+    if (per_warp <= 32 && threadIdx.x < C * SAMPLE_WARPS) {
+      const uint32_t c = threadIdx.x / SAMPLE_WARPS;
+      const uint32_t* at = &s->reach[r.rank * SAMPLE_WARPS + threadIdx.x % SAMPLE_WARPS];
+      if (c != r.rank) to_peer(at, c, *at);
     }
     row_sync(r);
     if (lane < C) {
       const Round o = s->peer[0][lane];
-      kmx = o.kmx, kmn = o.kmn, nan = o.nan, top = o.top, klow = o.klow;
+      kmx = o.kmx, kmn = o.kmn, nan = o.nan, top = o.top;
     }
     join(lane < C);
-    klow = __reduce_min_sync(ALL, klow);
   }
   mx = logit_of(kmx), mn = logit_of(kmn);
-  float low = klow == 0 || klow == ALL ? -INFINITY : logit_of(klow);
   if (nan || mx == -INFINITY || !(temperature > 0.f)) {  // no token, or the largest
     const bool none = nan || mx == -INFINITY;
     if (r.rank == 0 && threadIdx.x == 0) {
@@ -680,6 +686,26 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
       if (p.prob) p.prob[row] = none ? 0.f : 1.f;
     }
     return;
+  }
+  float low = -INFINITY;
+  if (per_warp <= 32) {  // by bisection of the keys' leading halves (what is cut off lowers it), alike in all warps
+    const uint32_t need = (top_k + per_warp - 1) / per_warp;
+    uint32_t keys[MAX_C * SAMPLE_WARPS / 32], lo = ALL, hi = 0;
+#pragma unroll
+    for (int k = 0; k < MAX_C * SAMPLE_WARPS / 32; k++) {
+      keys[k] = lane + 32 * k < C * SAMPLE_WARPS ? s->reach[lane + 32 * k] >> 16 : 0;
+      lo = min(lo, keys[k] ? keys[k] : ALL), hi = max(hi, keys[k]);
+    }
+    lo = __reduce_min_sync(ALL, lo), hi = __reduce_max_sync(ALL, hi);
+    while (lo < hi) {
+      const uint32_t mid = hi - (hi - lo) / 2;
+      uint32_t n = 0;
+#pragma unroll
+      for (int k = 0; k < MAX_C * SAMPLE_WARPS / 32; k++) n += keys[k] >= mid ? 1 : 0;
+      if (__reduce_add_sync(ALL, n) >= need) lo = mid;
+      else hi = mid - 1;
+    }
+    if (lo > key_of(-INFINITY) >> 16) low = logit_of(lo << 16);
   }
   if (mx == INFINITY) {  // the infinite ones are left, alike
     __syncwarp();
@@ -695,93 +721,57 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   constexpr float E_HI = 1.44269502f, E_LO = (float)(1.44269504088896341 - (double)E_HI);
   r.ch = E_HI / temperature;
   r.cl = (fmaf(-r.ch, temperature, E_HI) + E_LO) / temperature;
+  if (low > -INFINITY) mn = low;  // the bins divide what lies above
   r.to_bin = mx - mn > 0.f ? fminf((float)(BINS - 1) / (mx - mn), 3e38f) : 0.f;
 
   Kept kept = low > -INFINITY ? Kept{low, 0x7FFFFFFF} : everything();
   if (top_k > 0 && top_k < p.V) {
     if (C > 1 && top_k <= LIST / 2) {
-      // The bins down to the one in which top-k ends hold little more than
-      // top_k tokens: if few, the first CTA of the row goes on alone with
-      // them.  (An exchange between the CTAs costs more than a pass over a
-      // list.)  The bins divide what lies above `low`.
-      if (low > -INFINITY) r.to_bin = mx - low > 0.f ? fminf((float)(BINS - 1) / (mx - low), 3e38f) : 0.f;
-      const int mine = threadIdx.x;
-      s->hist[0][mine] = 0;
-      __syncthreads();
-      const uint32_t chunks = r.chunks(kept.x);
-      for (uint32_t k = chunks; k; k &= k - 1) {
+      // The tokens that reach `low` (without one, those that are not
+      // forbidden): if few, the first CTA of the row goes on alone with them.
+      // (An exchange between the CTAs costs more than a pass over a list.)
+      // Each warp lays down its own, then the CTAs' numbers give their places.
+      uint2* own = reinterpret_cast<uint2*>(s->hist) + warp * OWN;
+      static_assert(offsetof(SampleShared, count) >= SAMPLE_WARPS * OWN * sizeof(uint2), "hist and mass hold the lists");
+      const float least = fmaxf(low, -FLT_MAX);
+      uint32_t n = 0;
+      for (uint32_t k = r.chunks(least); k; k &= k - 1) {
         const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
         float v[4];
         r.four(i, v);
-        uint32_t m = 0;
+        uint32_t at = n;
+        const uint32_t ahead = (1u << lane) - 1;
 #pragma unroll
-        for (int e = 0; e < 4; e++) m |= (kept.has(v[e], r.first + i + lane * 4 + e) ? 1u : 0u) << e;
-        for (; m; m &= m - 1) atomicAdd(&s->hist[0][(int)r.place(m & 1 ? v[0] : m & 2 ? v[1] : m & 4 ? v[2] : v[3])], 1u);
+        for (int e = 0; e < 4; e++) {
+          const uint32_t them = __ballot_sync(ALL, v[e] >= least);
+          at += __popc(them & ahead);
+          n += __popc(them);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          if (v[e] >= least) {
+            if (at < OWN) own[at] = make_uint2(__float_as_uint(v[e]), (uint32_t)(r.first + i + lane * 4 + e));
+            at++;
+          }
       }
-      push_counts(r);
+      if (lane == 0) s->warp_a[warp] = n <= OWN ? n : LIST + 1;
+      __syncthreads();
+      const uint32_t theirs = lane < SAMPLE_WARPS ? s->warp_a[lane] : 0;
+      uint32_t at = warp_sum(lane < warp ? theirs : 0u);
+      const uint32_t ours = warp_sum(theirs);
+      if (threadIdx.x < C) to_peer(&s->peer[0][r.rank].left, threadIdx.x, ours);
       row_sync(r);
-      uint32_t count = 0, ahead = 0;  // tokens of this thread's bin, and of those in the CTAs before this one
-      for (uint32_t c = 0; c < r.C; c++) {
-        const uint32_t m = all[c * BINS + mine];
-        count += m;
-        if (c < r.rank) ahead += m;
-      }
-      unsigned long long total, sum;
-      const unsigned long long before = block_scan(count, &total, s);
-      if (threadIdx.x == 0) s->pick = BINS - 1, s->pick_count = (uint32_t)total;  // fewer than top_k in all
-      __syncthreads();
-      if (before < (uint32_t)top_k && (uint32_t)top_k <= before + count) {
-        s->pick = mine;
-        s->pick_count = (uint32_t)before + count;
-      }
-      __syncthreads();
-      const int last = s->pick;
-      const uint32_t left = s->pick_count;
-      (void)block_scan(mine <= last ? ahead : 0, &sum, s);
+      const uint32_t m = lane < C ? s->peer[0][lane].left : 0;
+      const uint32_t left = warp_sum(m);
+      at += warp_sum(lane < (int)r.rank ? m : 0u);
       if (left <= LIST) {
         // in order of their index; fewer than half a lane's four places each
         // leave gaps, so that all warps have their share
         int spread = 1;
         while (spread < 4 && left * spread * 2 <= CHUNK * SAMPLE_WARPS) spread *= 2;
-        auto survivors = [&](int i, float (&v)[4]) -> uint32_t {  // a bit for each of a lane's four tokens
-          r.four(i, v);
-          uint32_t m = 0;
-#pragma unroll
-          for (int e = 0; e < 4; e++)
-            m |= (kept.has(v[e], r.first + i + lane * 4 + e) && r.place(v[e]) < (float)(last + 1) ? 1u : 0u) << e;
-          return m;
-        };
-        float v[4];
-        uint32_t n = 0, ours = 0;  // tokens of this warp; the chunks that hold them
-        // (mx - v) to_bin < last + 1 leaves v above this, whatever rounds
-        const float edge = mx - ((float)last + 1.5f) / r.to_bin - fabsf(mx) * 0x1p-22f;
-        for (uint32_t k = r.chunks(fmaxf(edge, kept.x)); k; k &= k - 1) {
-          const uint32_t m = survivors(r.w0 + (__ffs(k) - 1) * CHUNK, v);
-          n += __popc(m);
-          if (__any_sync(ALL, m)) ours |= k & (0u - k);
-        }
-        n = warp_sum(n);
-        if (lane == 0) s->warp_a[warp] = n;
-        __syncthreads();
-        uint32_t at = (uint32_t)sum + warp_sum(lane < warp ? s->warp_a[lane] : 0u);
-        for (uint32_t k = ours; k; k &= k - 1) {
-          const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
-          const uint32_t m = survivors(i, v);
-          uint32_t inc = __popc(m);
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t a = __shfl_up_sync(ALL, inc, o);
-            if (lane >= o) inc += a;
-          }
-          uint32_t to = at + inc - __popc(m);
-#pragma unroll
-          for (int e = 0; e < 4; e++)
-            if (m >> e & 1) {
-              to_peer(&list_x[to * spread], 0, __float_as_uint(v[e]));
-              to_peer(&list_index[to * spread], 0, (uint32_t)(r.first + i + lane * 4 + e));
-              to++;
-            }
-          at += __shfl_sync(ALL, inc, 31);
+        for (uint32_t t = lane; t < n; t += 32) {
+          to_peer(&list_x[(at + t) * spread], 0, own[t].x);
+          to_peer(&list_index[(at + t) * spread], 0, own[t].y);
         }
         row_sync(r);
         if (r.rank) return;
@@ -805,7 +795,6 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
         choose(one, kept, min_p, u, list_index, p.token + row, p.prob ? p.prob + row : nullptr);
         return;
       }
-      row_sync(r);  // the counts have been read
     }
     narrow<false>(r, kept, (unsigned long long)top_k, 0.f);
   }
