@@ -200,11 +200,15 @@ struct Row {
   __device__ __forceinline__ float place(float v) const { return fminf((mx - v) * to_bin, (float)(BINS - 1)); }
 };
 
-template <typename T>
-__device__ __forceinline__ T warp_sum(T v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(ALL, v, o);
-  return v;
+__device__ __forceinline__ uint32_t warp_sum(uint32_t v) { return __reduce_add_sync(ALL, v); }
+
+// of numbers below 2^62, in three parts of 27 bits: three reductions at a time
+// instead of ten shuffles, five in a row
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+  constexpr uint32_t PART = (1u << 27) - 1;
+  const uint32_t a = __reduce_add_sync(ALL, (uint32_t)v & PART), b = __reduce_add_sync(ALL, (uint32_t)(v >> 27) & PART),
+                 c = __reduce_add_sync(ALL, (uint32_t)(v >> 54));
+  return a + ((unsigned long long)b << 27) + ((unsigned long long)c << 54);
 }
 
 template <typename R>
@@ -570,8 +574,8 @@ __device__ __forceinline__ void choose(const R& r, const Kept& kept, float min_p
 // Bound by latency, not by the bytes (0.6 us for 8 rows of 131071): reading
 // (2 us), the exchanges between the CTAs (1 to 2 us each with 16 CTAs), and
 // passes over 4 to 64 tokens per thread; for many rows by the instructions of
-// those passes.  Measured: 8 rows of 131071, all filters, 17.1 us; 1 row of
-// 32000, top-p, 17.9 us; 64 rows of 262144 in bf16, top-k and top-p, 43.8 us;
+// those passes.  Measured: 8 rows of 131071, all filters, 16.5 us; 1 row of
+// 32000, top-p, 17.5 us; 64 rows of 262144 in bf16, top-k and top-p, 43.1 us;
 // top-p alone has to weigh every token: 1 row of 131071, 32 us.  CTAs of a
 // row: with 4, 8 and 16, 8 rows of 131071 take 25.6, 20.2 and 20.4 us, 1 row
 // of 32000 25.3, 19.4 and 18.6 us, 64 rows of 262144 55.6, 54.9 and 82.9 us.
