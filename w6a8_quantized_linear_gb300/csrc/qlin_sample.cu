@@ -23,6 +23,7 @@ namespace {
 constexpr int SAMPLE_THREADS = 512;
 constexpr int SAMPLE_WARPS = SAMPLE_THREADS / 32;
 constexpr int BINS = SAMPLE_THREADS;     // one per thread in the scans
+constexpr int GROUPS = BINS / 32;
 constexpr int MAX_C = 16;                // CTAs of a row's cluster, at most
 constexpr int CHUNK = 128;               // consecutive tokens that a warp takes at once, four per lane
 constexpr int FEW = 128;                 // a bin of at most this many tokens is settled by comparing all pairs, four threads each
@@ -60,12 +61,11 @@ struct __align__(16) Candidate {
 
 struct SampleShared {
   __align__(16) uint32_t hist[3][BINS];  // this CTA's histogram: counts, masses' low and high words
-  unsigned long long mass[BINS];         // the row's
-  uint32_t count[BINS];
+  unsigned long long mass[MAX_C][32];    // a group of bins, by CTAs
+  uint32_t count[MAX_C][32];
   Candidate few[FEW];
   uint32_t reach[MAX_C * SAMPLE_WARPS];  // by warps of the row: the key that so many of its tokens reach
   Round peer[2][MAX_C];
-  uint2 range[MAX_C];
   unsigned long long warp_sum[SAMPLE_WARPS];
   uint32_t warp_a[SAMPLE_WARPS], warp_b[SAMPLE_WARPS], warp_c[SAMPLE_WARPS], warp_d[SAMPLE_WARPS];
   uint32_t table[32];  // 2^(i/32) in [2^31, 2^32)
@@ -150,14 +150,16 @@ __device__ __forceinline__ Kept everything() { return {-INFINITY, -1}; }
 // CTA) the survivors of top-k; filled up with -inf to whole chunks per warp.
 template <typename T, int CHUNKS>
 struct Row {
+  static constexpr int KEY_BITS = 8 * sizeof(T);  // leading bits that tell keys apart
   const T* x;
   float top[CHUNKS];  // the largest of this lane's four tokens in each of its warp's chunks
   int w0, w1;        // this warp's contiguous part
   int first;         // index of the slice's first token
-  float mx, ch, cl, to_bin;
+  float mx, mn, ch, cl, to_bin;
   uint32_t rank, C;
   SampleShared* s;
   uint32_t* all;     // [C][BINS]: the CTAs' counts
+  unsigned long long* group;  // [C][GROUPS]: the CTAs' masses of 32 bins at a time
   __device__ __forceinline__ unsigned long long weight(float v) const { return weight_of(v, mx, ch, cl, s->table); }
   __device__ __forceinline__ void part(int tokens) {  // whole chunks, alike for all warps
     const int per = (tokens + CHUNK * SAMPLE_WARPS - 1) / (CHUNK * SAMPLE_WARPS) * CHUNK;
@@ -211,6 +213,17 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
   return a + ((unsigned long long)b << 27) + ((unsigned long long)c << 54);
 }
 
+// of v in this lane and those before it
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T a = __shfl_up_sync(ALL, v, o);
+    if ((threadIdx.x & 31) >= o) v += a;
+  }
+  return v;
+}
+
 template <typename R>
 __device__ __forceinline__ void row_sync(const R& r) {
   if (r.C == 1) {
@@ -238,12 +251,7 @@ __device__ __forceinline__ uint32_t from_peer(const uint32_t* local, uint32_t ra
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* total,
                                                          SampleShared* s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long inc = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long a = __shfl_up_sync(ALL, inc, o);
-    if (lane >= o) inc += a;
-  }
+  const unsigned long long inc = warp_scan(v);
   __syncthreads();  // the previous scan's sums have been read
   if (lane == 31) s->warp_sum[warp] = inc;
   __syncthreads();
@@ -279,12 +287,7 @@ __device__ __forceinline__ int index_of(const R& r, const Kept& kept, float x, u
     for (uint32_t k = chunks; k && before < quota; k &= k - 1) {
       const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
       const uint32_t m = hits(i), c = __popc(m);
-      uint32_t inc = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t a = __shfl_up_sync(ALL, inc, o);
-        if (lane >= o) inc += a;
-      }
+      const uint32_t inc = warp_scan(c);
       if (before + inc >= quota && before + inc - c < quota)
         s->pick_index = (uint32_t)(r.first + i + lane * 4 + __fns(m, 0, quota - (before + inc - c)));
       before += __shfl_sync(ALL, inc, 31);
@@ -307,17 +310,39 @@ __device__ __forceinline__ void push_counts(const R& r) {
   }
 }
 
+// The lowest and the highest key whose logits fall into bin b of the row's
+// range: 16 lanes try as many keys at once for either.  All warps alike, no
+// exchange.  (The tokens' own lowest and highest took a pass and an exchange.)
+template <typename R>
+__device__ __forceinline__ void keys_of_bin(const R& r, const Kept& kept, int b, uint32_t* kmin, uint32_t* kmax) {
+  const int lane = threadIdx.x & 31;
+  const bool up = lane < 16;  // the highest: upwards from the survivors' lowest
+  const uint32_t lowest = key_of(fmaxf(kept.x, r.mn)), highest = key_of(r.mx), i = lane % 16 + 1;
+  uint32_t at = 0, len = highest - lowest;  // `at` steps are not too far; what is sought is at most len further
+  while (__any_sync(ALL, len)) {
+    const uint32_t step = len / 16 + 1, y = at + min(i * step, len);
+    const int bin = (int)r.place(logit_of(up ? lowest + y : highest - y));
+    const uint32_t hits = __ballot_sync(ALL, up ? bin >= b : bin <= b);  // a half's come first
+    const uint32_t n = __popc(up ? hits & 0xFFFFu : hits >> 16), to = min(n * step, len);
+    len = n == 16 ? 0 : min((n + 1) * step, len + 1) - 1 - to;  // a try at `len` may have failed: it is made again
+    at += to;
+  }
+  *kmax = lowest + __shfl_sync(ALL, at, 0);
+  *kmin = highest - __shfl_sync(ALL, at, 16);
+}
+
 // The shortest beginning of the survivors' order whose count (BY_MASS false)
 // reaches `want`, or whose mass reaches the share top_p of theirs; `kept` is
 // narrowed to it.  All CTAs of the row take part.  Each level costs one
-// exchange for counts (histograms pushed to every CTA) and two for masses
-// (joined by shares of the bins: three times the bytes make the push slower
-// than a second exchange, 5.7 against 3.9 us with 16 CTAs); the few tokens of
-// the bin in which the border lies take one more.
+// exchange: histograms of counts are pushed to every CTA; of masses, three
+// times the bytes, only the sums of 32 bins, and each CTA then reads the 32
+// bins in which the border lies from the others (all bins joined by shares
+// took a second exchange: 17.5 against 16.1 us for 1 row of 32000).  The few
+// tokens of the border's bin take one more.
 template <bool BY_MASS, typename R>
 __device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long long want, float top_p) {
   SampleShared* s = r.s;
-  const int lane = threadIdx.x & 31, mine = threadIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = threadIdx.x;
   int sh = 0;
   uint32_t kmax = 0, kmin = 0;
   const bool push = r.C > 1 && !BY_MASS;
@@ -352,58 +377,75 @@ __device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long lon
         }
       }
     }
-    if (push) push_counts(r);
-    row_sync(r);  // every CTA's histogram is complete
-    uint32_t count = 0;
-    unsigned long long mass = 0;
     if (push) {
-      for (uint32_t c = 0; c < r.C; c++) {
-        count += r.all[c * BINS + mine];
+      push_counts(r);
+    } else if (r.C > 1) {
+      __syncthreads();
+      const unsigned long long sum = warp_sum(s->hist[1][mine] + ((unsigned long long)s->hist[2][mine] << 32));
+      if (lane < (int)r.C) to_peer(&r.group[r.rank * GROUPS + warp], lane, sum);
+    }
+    row_sync(r);  // every CTA's histogram is complete
+    int b;
+    uint32_t n, ahead = 0;  // tokens of the border's bin, and of those in the CTAs before this one
+    unsigned long long total, picked;
+    if (BY_MASS && r.C > 1) {  // all warps alike
+      unsigned long long sum = 0, inc;
+      for (uint32_t c = 0; c < r.C; c++) sum += lane < GROUPS ? r.group[c * GROUPS + lane] : 0;
+      inc = warp_scan(sum);
+      total = __shfl_sync(ALL, inc, 31);
+      if (level == 0) want = max(1ull, share_of<true>(total, top_p));
+      if (total < want || total == 0) {  // all survivors (the same in every CTA)
+        row_sync(r);                     // the sums have been read
+        return;
       }
-    } else if (r.C == 1) {
-      count = s->hist[0][mine];
-      mass = s->hist[1][mine] + ((unsigned long long)s->hist[2][mine] << 32);
+      const int g = __ffs(__ballot_sync(ALL, inc >= want)) - 1;
+      want -= __shfl_sync(ALL, inc - sum, g);
+      if (warp < (int)r.C) {
+        const int at = g * 32 + lane;
+        s->count[warp][lane] = from_peer(&s->hist[0][at], warp);
+        s->mass[warp][lane] = from_peer(&s->hist[1][at], warp) + ((unsigned long long)from_peer(&s->hist[2][at], warp) << 32);
+      }
+      __syncthreads();
+      uint32_t count = 0;
+      sum = 0;
+      for (uint32_t c = 0; c < r.C; c++) count += s->count[c][lane], sum += s->mass[c][lane];
+      inc = warp_scan(sum);
+      const int l = __ffs(__ballot_sync(ALL, inc >= want)) - 1;
+      want -= __shfl_sync(ALL, inc - sum, l);
+      n = __shfl_sync(ALL, count, l);
+      picked = __shfl_sync(ALL, sum, l);
+      b = g * 32 + l;
+      ahead = warp_sum(lane < (int)r.rank ? s->count[lane % MAX_C][l] : 0u);
     } else {
-      // each CTA joins its share of the bins, C lanes to a bin (one per CTA),
-      // and lane c gives the sum to CTA c
-      const uint32_t c = threadIdx.x % r.C;
-      const int b = r.rank * (BINS / r.C) + threadIdx.x / r.C;
-      count = from_peer(&s->hist[0][b], c);
-      mass = from_peer(&s->hist[1][b], c) + ((unsigned long long)from_peer(&s->hist[2][b], c) << 32);
-      for (uint32_t o = 1; o < r.C; o <<= 1) {
-        count += __shfl_xor_sync(ALL, count, o);
-        mass += __shfl_xor_sync(ALL, mass, o);
+      uint32_t count = 0;
+      unsigned long long mass = 0;
+      if (push) {
+        for (uint32_t c = 0; c < r.C; c++) count += r.all[c * BINS + mine];
+      } else {
+        count = s->hist[0][mine];
+        mass = s->hist[1][mine] + ((unsigned long long)s->hist[2][mine] << 32);
       }
-      to_peer(&s->count[b], c, count);
-      to_peer(&s->mass[b], c, mass);
-      row_sync(r);
-      count = s->count[mine];
-      mass = s->mass[mine];
+      const unsigned long long v = BY_MASS ? mass : count;
+      const unsigned long long before = block_scan(v, &total, s);
+      if (level == 0 && BY_MASS) want = max(1ull, share_of<true>(total, top_p));
+      if (total < want || total == 0) {  // all survivors (the same in every CTA)
+        row_sync(r);                     // the counts have been read
+        return;
+      }
+      if (before < want && want <= before + v) {
+        s->pick = mine;
+        s->pick_count = count;
+        s->pick_mass = mass;
+        s->before = before;
+      }
+      __syncthreads();
+      b = s->pick;
+      n = s->pick_count;
+      picked = s->pick_mass;
+      want -= s->before;
+      if (push) ahead = warp_sum(lane < (int)r.rank ? r.all[lane * BINS + b] : 0u);
     }
-    unsigned long long total;
-    const unsigned long long v = BY_MASS ? mass : count;
-    const unsigned long long before = block_scan(v, &total, s);
-    if (level == 0 && BY_MASS) want = max(1ull, share_of<true>(total, top_p));
-    if (total < want || total == 0) {  // all survivors (the same in every CTA)
-      row_sync(r);                     // the counts have been read
-      return;
-    }
-    if (before < want && want <= before + v) {
-      s->pick = mine;
-      s->pick_count = count;
-      s->pick_mass = mass;
-      s->before = before;
-    }
-    __syncthreads();
-    const int b = s->pick;
-    const uint32_t n = s->pick_count;
-    want -= s->before;
-    // the bin's tokens in the CTAs before this one, and in this one
-    uint32_t ahead = 0;
-    if (r.C > 1) {
-      const uint32_t m = lane >= (int)r.C ? 0 : push ? r.all[lane * BINS + b] : from_peer(&s->hist[0][b], lane);
-      ahead = warp_sum(lane < (int)r.rank ? m : 0u);
-    }
+    if (r.C > 1) cluster_arrive();  // the others' numbers have been read
     const uint32_t own = s->hist[0][b];
     if (n <= FEW) {
       // into every CTA's list, this CTA's behind those of the CTAs before it
@@ -426,6 +468,7 @@ __device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long lon
                            : "memory");
           }
         }
+      if (r.C > 1) cluster_wait();
       row_sync(r);
       // each token's sum of those before it; one of them is the last that is kept
       const uint32_t cand = threadIdx.x / 4;
@@ -449,37 +492,41 @@ __device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long lon
       __syncthreads();
       return;
     }
-    // the range of the bin's keys, of this CTA and of the row
-    uint32_t lo = ALL, hi = 0;
-    for (uint32_t k = chunks; k; k &= k - 1) {
-      const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
-      float x[4];
-      r.four(i, x);
+    // the range of the bin's keys
+    if (r.C == 1) {
+      uint32_t lo = ALL, hi = 0;
+      for (uint32_t k = chunks; k; k &= k - 1) {
+        const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
+        float x[4];
+        r.four(i, x);
 #pragma unroll
-      for (int e = 0; e < 4; e++)
-        if (inside(x[e], r.first + i + lane * 4 + e) && (int)bin(x[e]) == b) {
-          lo = min(lo, key_of(x[e]));
-          hi = max(hi, key_of(x[e]));
-        }
-    }
-    lo = __reduce_min_sync(ALL, lo), hi = __reduce_max_sync(ALL, hi);
-    if (lane == 0) s->warp_a[threadIdx.x >> 5] = lo, s->warp_b[threadIdx.x >> 5] = hi;
-    __syncthreads();
-    lo = __reduce_min_sync(ALL, lane < SAMPLE_WARPS ? s->warp_a[lane] : ALL);
-    hi = __reduce_max_sync(ALL, lane < SAMPLE_WARPS ? s->warp_b[lane] : 0);
-    if (r.C > 1) {
-      if (threadIdx.x < r.C) {
-        to_peer(&s->range[r.rank].x, threadIdx.x, lo);
-        to_peer(&s->range[r.rank].y, threadIdx.x, hi);
+        for (int e = 0; e < 4; e++)
+          if (inside(x[e], r.first + i + lane * 4 + e) && (int)bin(x[e]) == b) {
+            lo = min(lo, key_of(x[e]));
+            hi = max(hi, key_of(x[e]));
+          }
       }
-      row_sync(r);
-      lo = __reduce_min_sync(ALL, lane < (int)r.C ? s->range[lane].x : ALL);
-      hi = __reduce_max_sync(ALL, lane < (int)r.C ? s->range[lane].y : 0);
+      lo = __reduce_min_sync(ALL, lo), hi = __reduce_max_sync(ALL, hi);
+      if (lane == 0) s->warp_a[warp] = lo, s->warp_b[warp] = hi;
+      __syncthreads();
+      kmin = __reduce_min_sync(ALL, lane < SAMPLE_WARPS ? s->warp_a[lane] : ALL);
+      kmax = __reduce_max_sync(ALL, lane < SAMPLE_WARPS ? s->warp_b[lane] : 0);
+    } else {
+      if (level == 0) {
+        keys_of_bin(r, kept, b, &kmin, &kmax);
+      } else {
+        kmax -= (uint32_t)b << sh;
+        if (kmax - kmin >> sh) kmin = kmax - ((1u << sh) - 1);
+      }
+      if (R::KEY_BITS == 16) {  // to the keys of 16-bit logits, which end in zeros, the negative ones' in ones
+        kmax = kmax >> 31 ? kmax & ~0xFFFFu : kmax - ((kmax + 1) & 0xFFFFu);
+        kmin = kmin >> 31 ? (kmin + 0xFFFFu) & ~0xFFFFu : kmin | 0xFFFFu;
+        if (kmin == 0x7FFFFFFFu) kmin++;  // -0, which does not occur
+      }
     }
-    kmin = lo, kmax = hi;
     if (kmin == kmax) {  // one key: its first `want` by index
       if (BY_MASS) {
-        const unsigned long long w = s->pick_mass / n;  // they weigh the same
+        const unsigned long long w = picked / n;  // they weigh the same
         want = w ? (want + w - 1) / w : n;
       }
       const float x = logit_of(kmax);
@@ -489,11 +536,13 @@ __device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long lon
         if (quota < own) bound = index_of(r, kept, x, quota);
       }
       kept = {x, bound};
-      __syncthreads();  // pick_index and pick_mass have been read
+      if (r.C > 1) cluster_wait();
+      __syncthreads();  // pick_index has been read
       return;
     }
-    sh = 0;
+    sh = r.C > 1 ? 32 - R::KEY_BITS : 0;
     while (((kmax - kmin) >> sh) >= (uint32_t)BINS) sh++;
+    if (r.C > 1) cluster_wait();
     __syncthreads();  // pick has been read
   }
 }
@@ -548,12 +597,7 @@ __device__ __forceinline__ void choose(const R& r, const Kept& kept, float min_p
   for (uint32_t k = chunks; k && before < target; k &= k - 1) {
     const int i0 = r.w0 + (__ffs(k) - 1) * CHUNK;
     const unsigned long long sum = weights(i0, w);
-    unsigned long long inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long a = __shfl_up_sync(ALL, inc, o);
-      if (lane >= o) inc += a;
-    }
+    const unsigned long long inc = warp_scan(sum);
     if (before + inc >= target && before + inc - sum < target) {  // one lane
       unsigned long long run = before + inc - sum;
       int e = 0;
@@ -575,8 +619,8 @@ __device__ __forceinline__ void choose(const R& r, const Kept& kept, float min_p
 // (2 us), the exchanges between the CTAs (1 to 2 us each with 16 CTAs), and
 // passes over 4 to 64 tokens per thread; for many rows by the instructions of
 // those passes.  Measured: 8 rows of 131071, all filters, 16.5 us; 1 row of
-// 32000, top-p, 17.5 us; 64 rows of 262144 in bf16, top-k and top-p, 43.1 us;
-// top-p alone has to weigh every token: 1 row of 131071, 32 us.  CTAs of a
+// 32000, top-p, 16.1 us; 64 rows of 262144 in bf16, top-k and top-p, 42.5 us;
+// top-p alone has to weigh every token: 1 row of 131071, 29 us.  CTAs of a
 // row: with 4, 8 and 16, 8 rows of 131071 take 25.6, 20.2 and 20.4 us, 1 row
 // of 32000 25.3, 19.4 and 18.6 us, 64 rows of 262144 55.6, 54.9 and 82.9 us.
 template <typename T>
@@ -592,6 +636,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   r.x = x;
   r.s = s;
   r.all = all;
+  r.group = reinterpret_cast<unsigned long long*>(list_x);  // a list of survivors has no use for it
   r.C = C;
   r.rank = C == 1 ? 0 : cluster_ctarank();
   r.first = (int)(r.rank * p.slice);
@@ -719,13 +764,13 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
     mx = mn = 0.f;
     low = -INFINITY;
   }
-  r.mx = mx;
+  if (low > -INFINITY) mn = low;  // the bins divide what lies above
+  r.mx = mx, r.mn = mn;
   // log2(e) / T as a pair of floats: the quotient of the leading part, and that
   // of what is left
   constexpr float E_HI = 1.44269502f, E_LO = (float)(1.44269504088896341 - (double)E_HI);
   r.ch = E_HI / temperature;
   r.cl = (fmaf(-r.ch, temperature, E_HI) + E_LO) / temperature;
-  if (low > -INFINITY) mn = low;  // the bins divide what lies above
   r.to_bin = mx - mn > 0.f ? fminf((float)(BINS - 1) / (mx - mn), 3e38f) : 0.f;
 
   Kept kept = low > -INFINITY ? Kept{low, 0x7FFFFFFF} : everything();
