@@ -656,6 +656,35 @@ def test_sample_uneven_rows(V, dtype):
                      min_p=f([0.0, 0.1, 0.0, 0.02, 0.3, 0.0, 0.0, 0.0]))
 
 
+@pytest.mark.parametrize("M, V, dtype", [(44, 100003, torch.float32), (20, 140001, torch.float32), (20, 300007, BF)])
+def test_sample_many_long_rows(M, V, dtype):
+    """More than the SMs hold at a time, rows at every alignment, each kind of row among them."""
+    x, u = logits_of(M, V, V + 5, dtype)
+    inf = math.inf
+    x[0, V // 2] = math.nan
+    x[1] = -inf
+    x[2, ::30011] = inf
+    x[3] = x[3].sort(descending=True).values
+    x[4] = x[4].sort().values
+    x[5, torch.arange(V) % (V // 5) != 7] = -inf
+    x[6] = 0.75
+    x[7] = (x[7] * 0.5).round()
+    x[8, ::2] = -0.0
+    x[9] *= 1e-30
+    x[10, V - 1] = 60.0
+    g = torch.Generator().manual_seed(V)
+    t = 0.5 + torch.rand(M, generator=g)
+    t[11] = 0
+    k = torch.randint(1, 1500, (M,), generator=g, dtype=torch.int32)
+    k[12], k[13], k[14] = 0, V // 3, 1
+    p = 0.3 + 0.7 * torch.rand(M, generator=g)
+    q = 0.2 * torch.rand(M, generator=g)
+    check_sample(x, u, temperature=t)
+    check_sample(x, u, top_k=k)
+    check_sample(x, u, temperature=t, top_p=p)
+    check_sample(x, u, temperature=t, top_k=k, top_p=p, min_p=q)
+
+
 def test_sample_edges():
     inf, nan = math.inf, math.nan
     rows = [[-inf] * 5, [0, 1, nan, 2, 3], [inf, 0, inf, 1, -inf], [-inf, -inf, 4, -inf, -inf], [3e38, -3e38, 0, 3e38, 1e38],

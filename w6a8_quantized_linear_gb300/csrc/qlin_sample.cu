@@ -13,6 +13,7 @@
 #include <cfloat>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "qlin_ptx.cuh"
 #include "qlin_step.h"
@@ -146,15 +147,21 @@ struct Kept {
 };
 __device__ __forceinline__ Kept everything() { return {-INFINITY, -1}; }
 
-// The tokens that a CTA works on: a slice of the row in shared memory, or (one
-// CTA) the survivors of top-k; filled up with -inf to whole chunks per warp.
-template <typename T, int CHUNKS>
+// The tokens that a CTA works on, filled up with -inf to whole chunks per warp:
+// a slice of the row in shared memory (STAGED), or where it is, or (one CTA)
+// the survivors of top-k.
+template <typename T, int CHUNKS, bool STAGED = true>
 struct Row {
+  using Four = std::conditional_t<sizeof(T) == 4, float4, uint2>;
   static constexpr int KEY_BITS = 8 * sizeof(T);  // leading bits that tell keys apart
   const T* x;
-  float top[CHUNKS];  // the largest of this lane's four tokens in each of its warp's chunks
+  // The largest of this lane's four tokens in each of its warp's chunks; not
+  // STAGED two in a word, rounded up to bf16.
+  std::conditional_t<STAGED, float, uint32_t> top[STAGED ? CHUNKS : CHUNKS / 2];
   int w0, w1;        // this warp's contiguous part
   int first;         // index of the slice's first token
+  int tokens;        // not STAGED: those of the row in the slice
+  bool wide, inf;    // not STAGED: four tokens at a time; the infinite ones are left, alike
   float mx, mn, ch, cl, to_bin;
   uint32_t rank, C;
   SampleShared* s;
@@ -166,26 +173,87 @@ struct Row {
     w0 = (threadIdx.x >> 5) * per;
     w1 = w0 + per;
   }
-  // tokens 4 lane .. 4 lane + 3 of the chunk at i
-  __device__ __forceinline__ void four(int i, float (&v)[4]) const {
-    const T* at = x + i + (threadIdx.x & 31) * 4;
+  // tokens 4 lane .. 4 lane + 3 of the chunk at i, as they are in memory
+  __device__ __forceinline__ Four load(int i) const {
+    i += (threadIdx.x & 31) * 4;
+    const T* at = x + i;
+    if (STAGED || (wide && i + 4 <= tokens)) return *reinterpret_cast<const Four*>(at);
+    T v[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[e] = i + e < tokens ? at[e] : T(-INFINITY);
     if constexpr (sizeof(T) == 4) {
-      const float4 f = *reinterpret_cast<const float4*>(at);
+      return {v[0], v[1], v[2], v[3]};
+    } else {
+      auto two = [](T a, T b) { return (uint32_t)__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16; };
+      return {two(v[0], v[1]), two(v[2], v[3])};
+    }
+  }
+  __device__ __forceinline__ void values(const Four& f, float (&v)[4]) const {
+    if constexpr (sizeof(T) == 4) {
       v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
     } else {
-      const uint2 f = *reinterpret_cast<const uint2*>(at);
       const float2 a = unpack2(f.x, T()), b = unpack2(f.y, T());
       v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
     }
+    if constexpr (!STAGED) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        v[e] += 0.f;  // -0 becomes 0
+        if (inf) v[e] = v[e] == INFINITY ? 0.f : -INFINITY;
+      }
+    }
+  }
+  __device__ __forceinline__ void four(int i, float (&v)[4]) const { values(load(i), v); }
+  // f(i, v) for the chunks named by `m`, in order; not STAGED with AHEAD more
+  // on their way.
+  template <typename F>
+  __device__ __forceinline__ void each(uint32_t m, const F& f) const {
+    if constexpr (STAGED) {
+      for (; m; m &= m - 1) {
+        float v[4];
+        const int i = w0 + (__ffs(m) - 1) * CHUNK;
+        four(i, v);
+        f(i, v);
+      }
+    } else {
+      float v[4];
+      constexpr int AHEAD = sizeof(T) == 4 ? 2 : 3;
+      Four next[AHEAD];
+      uint32_t far = m;
+#pragma unroll
+      for (int a = 0; a < AHEAD; a++, far &= far - 1)
+        if (far) next[a] = load(w0 + (__ffs(far) - 1) * CHUNK);
+      for (; m; m &= m - 1, far &= far - 1) {
+        const Four now = next[0];
+#pragma unroll
+        for (int a = 0; a + 1 < AHEAD; a++) next[a] = next[a + 1];
+        if (far) next[AHEAD - 1] = load(w0 + (__ffs(far) - 1) * CHUNK);
+        values(now, v);
+        f(w0 + (__ffs(m) - 1) * CHUNK, v);
+      }
+    }
+  }
+  __device__ __forceinline__ void set_top(int c, const float (&v)[4]) {
+    const float t = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+    if constexpr (STAGED) {
+      top[c] = t;
+    } else {
+      const uint32_t up = __bfloat16_as_ushort(__float2bfloat16_ru(t));
+      top[c / 2] = c & 1 ? (top[c / 2] & 0xFFFFu) | up << 16 : up | 0xFF800000u;
+    }
+  }
+  __device__ __forceinline__ void no_top(int c) {
+    if constexpr (STAGED) top[c] = -INFINITY;
+    else if (c % 2 == 0) top[c / 2] = 0xFF80FF80u;
   }
   __device__ __forceinline__ void tops() {
 #pragma unroll
     for (int c = 0; c < CHUNKS; c++) {
-      top[c] = -INFINITY;
+      no_top(c);
       if (w0 + c * CHUNK < w1) {
         float v[4];
         four(w0 + c * CHUNK, v);
-        top[c] = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+        set_top(c, v);
       }
     }
   }
@@ -194,7 +262,12 @@ struct Row {
   __device__ __forceinline__ uint32_t chunks(float least) const {
     uint32_t m = 0;
 #pragma unroll
-    for (int c = 0; c < CHUNKS; c++) m |= (__any_sync(0xFFFFFFFFu, top[c] >= least) ? 1u : 0u) << c;
+    for (int c = 0; c < CHUNKS; c++) {
+      float t;
+      if constexpr (STAGED) t = top[c];
+      else t = __uint_as_float(c & 1 ? top[c / 2] & 0xFFFF0000u : top[c / 2] << 16);
+      m |= (__any_sync(0xFFFFFFFFu, t >= least) ? 1u : 0u) << c;
+    }
     return m & ((2u << ((w1 - w0) / CHUNK - 1)) - 1);
   }
   // Place among the row's BINS equal parts of its logits' range, largest
@@ -267,9 +340,7 @@ __device__ __forceinline__ int index_of(const R& r, const Kept& kept, float x, u
   if (quota == 0) return -1;
   SampleShared* s = r.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto hits = [&](int i0) -> uint32_t {  // a bit for each of a lane's four tokens
-    float v[4];
-    r.four(i0, v);
+  auto hits = [&](int i0, const float (&v)[4]) -> uint32_t {  // a bit for each of a lane's four tokens
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 4; e++) m |= (v[e] == x && kept.has(v[e], r.first + i0 + lane * 4 + e) ? 1u : 0u) << e;
@@ -277,7 +348,7 @@ __device__ __forceinline__ int index_of(const R& r, const Kept& kept, float x, u
   };
   uint32_t n = 0;
   const uint32_t chunks = r.chunks(x);
-  for (uint32_t m = chunks; m; m &= m - 1) n += __popc(hits(r.w0 + (__ffs(m) - 1) * CHUNK));
+  r.each(chunks, [&](int i, const float (&v)[4]) { n += __popc(hits(i, v)); });
   n = warp_sum(n);
   if (lane == 0) s->warp_a[warp] = n;
   __syncthreads();
@@ -286,7 +357,9 @@ __device__ __forceinline__ int index_of(const R& r, const Kept& kept, float x, u
   if (before < quota && quota <= before + n) {
     for (uint32_t k = chunks; k && before < quota; k &= k - 1) {
       const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
-      const uint32_t m = hits(i), c = __popc(m);
+      float v[4];
+      r.four(i, v);
+      const uint32_t m = hits(i, v), c = __popc(m);
       const uint32_t inc = warp_scan(c);
       if (before + inc >= quota && before + inc - c < quota)
         s->pick_index = (uint32_t)(r.first + i + lane * 4 + __fns(m, 0, quota - (before + inc - c)));
@@ -357,10 +430,7 @@ __device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long lon
     if (threadIdx.x == 0) s->filled = 0;
     __syncthreads();
     const uint32_t chunks = r.chunks(least);
-    for (uint32_t k = chunks; k; k &= k - 1) {
-      const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
-      float x[4];
-      r.four(i, x);
+    r.each(chunks, [&](int i, const float (&x)[4]) {
       uint32_t m = 0;
 #pragma unroll
       for (int e = 0; e < 4; e++) m |= (inside(x[e], r.first + i + lane * 4 + e) ? 1u : 0u) << e;
@@ -376,7 +446,7 @@ __device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long lon
           if (wh) atomicAdd(&s->hist[2][b], wh);
         }
       }
-    }
+    });
     if (push) {
       push_counts(r);
     } else if (r.C > 1) {
@@ -450,12 +520,9 @@ __device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long lon
     if (n <= FEW) {
       // into every CTA's list, this CTA's behind those of the CTAs before it
       if (own)
-        for (uint32_t k = chunks; k; k &= k - 1) {
-          const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
-          float x[4];
-          r.four(i, x);
+        r.each(chunks, [&](int i, const float (&x)[4]) {
           const float most = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-          if (!__any_sync(ALL, most >= least && (level > 0 || r.place(most) < (float)(b + 1)))) continue;
+          if (!__any_sync(ALL, most >= least && (level > 0 || r.place(most) < (float)(b + 1)))) return;
 #pragma unroll
           for (int e = 0; e < 4; e++) {
             const int index = r.first + i + lane * 4 + e;
@@ -467,7 +534,7 @@ __device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long lon
                            "r"(key_of(x[e])), "r"((uint32_t)index), "r"((uint32_t)w), "r"((uint32_t)(w >> 32))
                            : "memory");
           }
-        }
+        });
       if (r.C > 1) cluster_wait();
       row_sync(r);
       // each token's sum of those before it; one of them is the last that is kept
@@ -560,9 +627,7 @@ __device__ __forceinline__ void choose(const R& r, const Kept& kept, float min_p
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long least = 1;
   if (min_p > 0.f) least = max(1ull, share_of<true>(1ull << ONE_BITS, fminf(min_p, 1.f)));
-  auto weights = [&](int i0, unsigned long long (&w)[4]) -> unsigned long long {
-    float v[4];
-    r.four(i0, v);
+  auto weights = [&](int i0, const float (&v)[4], unsigned long long (&w)[4]) -> unsigned long long {
     unsigned long long sum = 0;
     w[0] = w[1] = w[2] = w[3] = 0;
 #pragma unroll
@@ -576,7 +641,7 @@ __device__ __forceinline__ void choose(const R& r, const Kept& kept, float min_p
   // the kept mass of each warp's tokens, of the CTAs, of the row
   unsigned long long mine = 0, w[4];
   const uint32_t chunks = r.chunks(kept.x);
-  for (uint32_t k = chunks; k; k &= k - 1) mine += weights(r.w0 + (__ffs(k) - 1) * CHUNK, w);
+  r.each(chunks, [&](int i, const float (&v)[4]) { mine += weights(i, v, w); });
   mine = warp_sum(mine);
   __syncthreads();  // warp_sum has been read
   if (lane == 0) s->warp_sum[warp] = mine;
@@ -596,7 +661,9 @@ __device__ __forceinline__ void choose(const R& r, const Kept& kept, float min_p
   if (!(before < target && target <= before + mine)) return;
   for (uint32_t k = chunks; k && before < target; k &= k - 1) {
     const int i0 = r.w0 + (__ffs(k) - 1) * CHUNK;
-    const unsigned long long sum = weights(i0, w);
+    float v[4];
+    r.four(i0, v);
+    const unsigned long long sum = weights(i0, v, w);
     const unsigned long long inc = warp_scan(sum);
     if (before + inc >= target && before + inc - sum < target) {  // one lane
       unsigned long long run = before + inc - sum;
@@ -614,16 +681,16 @@ __device__ __forceinline__ void choose(const R& r, const Kept& kept, float min_p
   }
 }
 
-// One row per cluster of C CTAs, its logits read once, into shared memory.
+// One row per cluster of C CTAs.  STAGED: its logits are read once, into shared
+// memory; else the chunks that a pass needs are read again where they are,
+// mostly from L2, so that slices of 65536 tokens leave room for two CTAs per SM.
 // Bound by latency, not by the bytes (0.6 us for 8 rows of 131071): reading
 // (2 us), the exchanges between the CTAs (1 to 2 us each with 16 CTAs), and
 // passes over 4 to 64 tokens per thread; for many rows by the instructions of
-// those passes.  Measured: 8 rows of 131071, all filters, 16.5 us; 1 row of
-// 32000, top-p, 16.1 us; 64 rows of 262144 in bf16, top-k and top-p, 42.5 us;
-// top-p alone has to weigh every token: 1 row of 131071, 29 us.  CTAs of a
-// row: with 4, 8 and 16, 8 rows of 131071 take 25.6, 20.2 and 20.4 us, 1 row
-// of 32000 25.3, 19.4 and 18.6 us, 64 rows of 262144 55.6, 54.9 and 82.9 us.
-template <typename T>
+// those passes.  Measured: 8 rows of 131071, all filters, 15.9 us; 1 row of
+// 32000, top-p, 16.0 us; 64 rows of 262144 in bf16, top-k and top-p, 37.8 us;
+// top-p alone has to weigh every token: 1 row of 131071, 29 us.
+template <typename T, bool STAGED>
 __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __grid_constant__ SampleParams p, int C) {
   extern __shared__ __align__(16) uint8_t raw[];
   SampleShared* s = reinterpret_cast<SampleShared*>(raw);
@@ -632,8 +699,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   uint32_t* list_index = reinterpret_cast<uint32_t*>(list_x + LIST);
   T* x = reinterpret_cast<T*>(raw + sizeof(SampleShared) + shared_counts(C));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Row<T, 16> r;  // 32768 tokens of a slice at most
-  r.x = x;
+  Row<T, STAGED ? 16 : 32, STAGED> r;  // a slice of 32768 or 65536 tokens at most
   r.s = s;
   r.all = all;
   r.group = reinterpret_cast<unsigned long long*>(list_x);  // a list of survivors has no use for it
@@ -655,24 +721,55 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   const T* src = static_cast<const T*>(p.logits) + row * p.ld + r.first;
   float mx = -INFINITY, mn = INFINITY;
   uint32_t nan = 0, top = 0;  // top: the lowest index of the largest
-  constexpr int BATCH = 16;   // loads in flight per thread
-  for (int i0 = r.w0 + lane; i0 < r.w1; i0 += 32 * BATCH) {
-    T v[BATCH];
+  auto look = [&](float f, int i) {
+    nan |= f != f;
+    if (f > mx) mx = f, top = (uint32_t)(r.first + i);
+    if (f > -INFINITY) mn = fminf(mn, f);
+  };
+  if constexpr (STAGED) {
+    r.x = x;
+    constexpr int BATCH = 16;  // loads in flight per thread
+    for (int i0 = r.w0 + lane; i0 < r.w1; i0 += 32 * BATCH) {
+      T v[BATCH];
 #pragma unroll
-    for (int k = 0; k < BATCH; k++) v[k] = i0 + 32 * k < tokens ? src[i0 + 32 * k] : T(-INFINITY);
+      for (int k = 0; k < BATCH; k++) v[k] = i0 + 32 * k < tokens ? src[i0 + 32 * k] : T(-INFINITY);
 #pragma unroll
-    for (int k = 0; k < BATCH; k++) {
-      const int i = i0 + 32 * k;
-      if (i >= r.w1) break;
-      const float f = to_float(v[k]) + 0.f;  // -0 becomes 0
-      x[i] = T(f);
-      nan |= f != f;
-      if (f > mx) mx = f, top = (uint32_t)(r.first + i);
-      if (f > -INFINITY) mn = fminf(mn, f);
+      for (int k = 0; k < BATCH; k++) {
+        const int i = i0 + 32 * k;
+        if (i >= r.w1) break;
+        const float f = to_float(v[k]) + 0.f;  // -0 becomes 0
+        x[i] = T(f);
+        look(f, i);
+      }
+    }
+    __syncwarp();
+    r.tops();
+  } else {
+    r.x = src;
+    r.tokens = tokens;
+    r.wide = (reinterpret_cast<uintptr_t>(src) & (4 * sizeof(T) - 1)) == 0;
+    r.inf = false;
+    constexpr int BATCH = sizeof(T) == 4 ? 4 : 8;
+#pragma unroll
+    for (int c0 = 0; c0 < 32; c0 += BATCH) {
+      typename decltype(r)::Four f[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; k++)
+        if (r.w0 + (c0 + k) * CHUNK < r.w1) f[k] = r.load(r.w0 + (c0 + k) * CHUNK);
+#pragma unroll
+      for (int k = 0; k < BATCH; k++) {
+        const int i = r.w0 + (c0 + k) * CHUNK;
+        r.no_top(c0 + k);
+        if (i < r.w1) {
+          float v[4];
+          r.values(f[k], v);
+#pragma unroll
+          for (int e = 0; e < 4; e++) look(v[e], i + lane * 4 + e);
+          r.set_top(c0 + k, v);
+        }
+      }
     }
   }
-  __syncwarp();
-  r.tops();
   // of the warp, the CTA, the row, as keys; the index of the largest
   uint32_t kmx = key_of(mx), kmn = key_of(mn);
   auto join = [&](bool in) {
@@ -757,9 +854,13 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
     if (lo > key_of(-INFINITY) >> 16) low = logit_of(lo << 16);
   }
   if (mx == INFINITY) {  // the infinite ones are left, alike
-    __syncwarp();
-    for (int i = r.w0 + lane; i < r.w1; i += 32) x[i] = to_float(x[i]) == INFINITY ? T(0.f) : T(-INFINITY);
-    __syncwarp();
+    if constexpr (STAGED) {
+      __syncwarp();
+      for (int i = r.w0 + lane; i < r.w1; i += 32) x[i] = to_float(x[i]) == INFINITY ? T(0.f) : T(-INFINITY);
+      __syncwarp();
+    } else {
+      r.inf = true;
+    }
     r.tops();
     mx = mn = 0.f;
     low = -INFINITY;
@@ -784,10 +885,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
       static_assert(offsetof(SampleShared, count) >= SAMPLE_WARPS * OWN * sizeof(uint2), "hist and mass hold the lists");
       const float least = fmaxf(low, -FLT_MAX);
       uint32_t n = 0;
-      for (uint32_t k = r.chunks(least); k; k &= k - 1) {
-        const int i = r.w0 + (__ffs(k) - 1) * CHUNK;
-        float v[4];
-        r.four(i, v);
+      r.each(r.chunks(least), [&](int i, const float (&v)[4]) {
         uint32_t at = n;
         const uint32_t ahead = (1u << lane) - 1;
 #pragma unroll
@@ -802,7 +900,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
             if (at < OWN) own[at] = make_uint2(__float_as_uint(v[e]), (uint32_t)(r.first + i + lane * 4 + e));
             at++;
           }
-      }
+      });
       if (lane == 0) s->warp_a[warp] = n <= OWN ? n : LIST + 1;
       __syncthreads();
       const uint32_t theirs = lane < SAMPLE_WARPS ? s->warp_a[lane] : 0;
@@ -854,18 +952,49 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
 constexpr size_t SAMPLE_SMEM = 220 * 1024;
 static_assert(sizeof(SampleShared) + shared_counts(MAX_C) + QLIN_SAMPLE_MAX_V / MAX_C * 4 <= SAMPLE_SMEM, "largest slice");
 
-const void* sample_fn(int dtype) {
-  return dtype == QLIN_F32 ? reinterpret_cast<const void*>(qlin_sample_kernel<float>)
-                           : reinterpret_cast<const void*>(qlin_sample_kernel<__nv_bfloat16>);
+const void* sample_fn(int dtype, bool staged) {
+  if (dtype == QLIN_F32)
+    return staged ? reinterpret_cast<const void*>(qlin_sample_kernel<float, true>)
+                  : reinterpret_cast<const void*>(qlin_sample_kernel<float, false>);
+  return staged ? reinterpret_cast<const void*>(qlin_sample_kernel<__nv_bfloat16, true>)
+                : reinterpret_cast<const void*>(qlin_sample_kernel<__nv_bfloat16, false>);
 }
 
-// CTAs per row, a power of two: as many as one wave of clusters holds while
-// each has four tokens per thread (a pass costs less than an exchange saves),
-// and at least so many that two CTAs' slices (64 KB) share an SM.
-int sample_ctas(int64_t M, int64_t V, int64_t size, int most) {
-  int C = 1;
-  while (C < most && ((C * (int64_t)SAMPLE_THREADS * 4 < V && 2 * C * M <= 128) || C * (int64_t)65536 < V * size)) C *= 2;
-  return C;
+struct SamplePlan {
+  int C;  // CTAs per row, a power of two
+  bool staged;
+};
+
+// Slices of 64 KB in shared memory leave room for two CTAs per SM.  Few rows
+// take more CTAs each: a pass costs less, an exchange more.  Under top-k the
+// passes are over few tokens: up to 128 CTAs (8 rows of 131071: 4, 8 and 16
+// CTAs per row 18.3, 16.0 and 17.4 us; 64 rows of 32000 with 2 and 4: 17.1 and
+// 18.6), clusters of 16 for four rows at most (4 rows of 262144 with 8 and 16:
+// 17.3 and 15.8; 1 row of 32000: 12.7 and 13.2).  Else all tokens are weighed:
+// up to 256 CTAs (32 rows of 32000 with 4 and 8: 31.8 and 28.0; 64 rows with 4
+// and 8: 41.2 and 48.2), and clusters of 16 while their slices are large
+// beside the rows' number (16 rows of 131071 with 8 and 16: 54.5 and 49.9; of
+// 32000: 23.7 and 27.9).  From 16384 tokens on two CTAs pay for any number of
+// rows (256 rows of 32000 in bf16 with 1 and 2: 71 and 41 us).
+// Rows that fill more than one wave in this way are read where they are, by
+// fewer CTAs, if under top-k (64 rows of 262144 in bf16 with 8 staged and 4
+// such CTAs: 43.5 and 38.0 us; in fp32, with 16 and 4: 85.7 and 39.5; but rows
+// below 256 KB, 128 of 131071 in bf16: 45.6 and 48.5) or if it would take
+// clusters of 16, of which few fit at a time (32 rows of 262144 in fp32 under
+// top-p with 16 staged and 8 such CTAs: 202 and 148; but with 8 staged, 64
+// rows of 262144 in bf16: 216 and 250).
+SamplePlan sample_plan(int64_t M, int64_t V, int64_t size, bool by_count, int most) {
+  constexpr int64_t WAVE = 2 * 152;
+  int C = V > 16384 ? 2 : 1;
+  while (C < most && C * (int64_t)65536 < V * size) C *= 2;
+  if (by_count ? C >= 8 && M * C > (C == 16 ? 128 : WAVE) : C == 16 && M * C > WAVE) {
+    for (C = 2; C * (int64_t)65536 < V;) C *= 2;
+    while (C < 8 && 2 * C * M <= WAVE) C *= 2;
+    return {C, false};
+  }
+  while (C < 8 && C * (int64_t)(SAMPLE_THREADS * 4) < V && 2 * C * M <= (by_count ? 128 : 256)) C *= 2;
+  if (C == 8 && most == 16 && (by_count ? M <= 4 && V >= 65536 : M <= 16 && V > 16384 && V >= 2048 * M)) C = 16;
+  return {C, true};
 }
 
 struct SampleDevice {
@@ -887,10 +1016,12 @@ qlin_status sample_setup(int* most) {
     cudaError_t e = cudaSuccess;
     int clusters = 1;
     for (int dtype : {QLIN_F32, QLIN_BF16}) {
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(sample_fn(dtype), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SAMPLE_SMEM);
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(sample_fn(dtype), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      for (bool staged : {true, false}) {
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(sample_fn(dtype, staged), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SAMPLE_SMEM);
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(sample_fn(dtype, staged), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      }
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(MAX_C, 1, 1);
       cfg.blockDim = dim3(SAMPLE_THREADS, 1, 1);
@@ -902,7 +1033,7 @@ qlin_status sample_setup(int* most) {
       cfg.attrs = &attr;
       cfg.numAttrs = 1;
       int n = 0;
-      if (e == cudaSuccess && cudaOccupancyMaxActiveClusters(&n, sample_fn(dtype), &cfg) != cudaSuccess) {
+      if (e == cudaSuccess && cudaOccupancyMaxActiveClusters(&n, sample_fn(dtype, true), &cfg) != cudaSuccess) {
         (void)cudaGetLastError();
         n = 0;
       }
@@ -935,12 +1066,14 @@ extern "C" qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logi
   qlin_status st = sample_setup(&most);
   if (st != QLIN_OK) return st;
   if (V > (int64_t)most * (QLIN_SAMPLE_MAX_V / MAX_C)) return QLIN_ERR_UNSUPPORTED;  // a slice of 32768 per CTA
-  const int C = sample_ctas(M, V, dtype == QLIN_F32 ? 4 : 2, most);
+  const SamplePlan plan = sample_plan(M, V, dtype == QLIN_F32 ? 4 : 2, top_k != nullptr, most);
+  const int C = plan.C;
   SampleParams p = {logits, ld, u, temperature, top_p, min_p, top_k, token, prob, (int)V,
                     (int)(((V + C - 1) / C + CHUNK * SAMPLE_WARPS - 1) / (CHUNK * SAMPLE_WARPS) * (CHUNK * SAMPLE_WARPS))};
   int c = C;
   void* args[] = {&p, &c};
-  return launch_step(sample_fn(dtype), dim3((unsigned)(M * C), 1, 1), dim3(SAMPLE_THREADS, 1, 1),
-                     sizeof(SampleShared) + shared_counts(C) + (size_t)p.slice * (dtype == QLIN_F32 ? 4 : 2), static_cast<cudaStream_t>(stream), args,
+  const size_t slice = plan.staged ? (size_t)p.slice * (dtype == QLIN_F32 ? 4 : 2) : 0;
+  return launch_step(sample_fn(dtype, plan.staged), dim3((unsigned)(M * C), 1, 1), dim3(SAMPLE_THREADS, 1, 1),
+                     sizeof(SampleShared) + shared_counts(C) + slice, static_cast<cudaStream_t>(stream), args,
                      (flags & QLIN_FLAG_PDL) != 0, C);
 }
