@@ -137,6 +137,14 @@ __device__ __forceinline__ float ratio(unsigned long long a, unsigned long long 
   return ldexpf((float)q, zb - za - 32);
 }
 
+// the largest; NaN if one is
+__device__ __forceinline__ float max_of(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+__device__ __forceinline__ float max_of(const float (&v)[4]) { return max_of(max_of(v[0], v[1]), max_of(v[2], v[3])); }
+
 // Which part of the order survives: logits above x, and equal ones up to
 // `index` in the row (a bound that only this CTA's tokens have to agree with).
 // Forbidden tokens (-inf) never do.
@@ -160,9 +168,9 @@ struct Row {
   std::conditional_t<STAGED, float, uint32_t> top[STAGED ? CHUNKS : CHUNKS / 2];
   int w0, w1;        // this warp's contiguous part
   int first;         // index of the slice's first token
-  int tokens;        // not STAGED: those of the row in the slice
-  bool wide, inf;    // not STAGED: four tokens at a time; the infinite ones are left, alike
-  float mx, mn, ch, cl, to_bin;
+  int tokens;        // those of the row in the slice
+  bool wide, inf;    // in memory four tokens at a time; not STAGED: the infinite ones are left, alike
+  float mx, mn, ch, cl, to_bin;  // mn: nothing that is left is below it
   uint32_t rank, C;
   SampleShared* s;
   uint32_t* all;     // [C][BINS]: the CTAs' counts
@@ -173,11 +181,11 @@ struct Row {
     w0 = (threadIdx.x >> 5) * per;
     w1 = w0 + per;
   }
-  // tokens 4 lane .. 4 lane + 3 of the chunk at i, as they are in memory
-  __device__ __forceinline__ Four load(int i) const {
+  // tokens 4 lane .. 4 lane + 3 of the chunk at i of the slice in memory
+  __device__ __forceinline__ Four fetch(const T* from, int i) const {
     i += (threadIdx.x & 31) * 4;
-    const T* at = x + i;
-    if (STAGED || (wide && i + 4 <= tokens)) return *reinterpret_cast<const Four*>(at);
+    const T* at = from + i;
+    if (wide && i + 4 <= tokens) return *reinterpret_cast<const Four*>(at);
     T v[4];
 #pragma unroll
     for (int e = 0; e < 4; e++) v[e] = i + e < tokens ? at[e] : T(-INFINITY);
@@ -188,6 +196,10 @@ struct Row {
       return {two(v[0], v[1]), two(v[2], v[3])};
     }
   }
+  __device__ __forceinline__ Four load(int i) const {
+    if constexpr (STAGED) return *reinterpret_cast<const Four*>(x + i + (threadIdx.x & 31) * 4);
+    else return fetch(x, i);
+  }
   __device__ __forceinline__ void values(const Four& f, float (&v)[4]) const {
     if constexpr (sizeof(T) == 4) {
       v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
@@ -195,12 +207,11 @@ struct Row {
       const float2 a = unpack2(f.x, T()), b = unpack2(f.y, T());
       v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
     }
-    if constexpr (!STAGED) {
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        v[e] += 0.f;  // -0 becomes 0
+    for (int e = 0; e < 4; e++) {
+      v[e] += 0.f;  // -0 becomes 0
+      if constexpr (!STAGED)
         if (inf) v[e] = v[e] == INFINITY ? 0.f : -INFINITY;
-      }
     }
   }
   __device__ __forceinline__ void four(int i, float (&v)[4]) const { values(load(i), v); }
@@ -233,8 +244,7 @@ struct Row {
       }
     }
   }
-  __device__ __forceinline__ void set_top(int c, const float (&v)[4]) {
-    const float t = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+  __device__ __forceinline__ void set_top(int c, float t) {
     if constexpr (STAGED) {
       top[c] = t;
     } else {
@@ -253,7 +263,7 @@ struct Row {
       if (w0 + c * CHUNK < w1) {
         float v[4];
         four(w0 + c * CHUNK, v);
-        set_top(c, v);
+        set_top(c, max_of(v));
       }
     }
   }
@@ -687,8 +697,8 @@ __device__ __forceinline__ void choose(const R& r, const Kept& kept, float min_p
 // Bound by latency, not by the bytes (0.6 us for 8 rows of 131071): reading
 // (2 us), the exchanges between the CTAs (1 to 2 us each with 16 CTAs), and
 // passes over 4 to 64 tokens per thread; for many rows by the instructions of
-// those passes.  Measured: 8 rows of 131071, all filters, 15.9 us; 1 row of
-// 32000, top-p, 16.0 us; 64 rows of 262144 in bf16, top-k and top-p, 37.8 us;
+// those passes.  Measured: 8 rows of 131071, all filters, 15.2 us; 1 row of
+// 32000, top-p, 14.9 us; 64 rows of 262144 in bf16, top-k and top-p, 36.3 us;
 // top-p alone has to weigh every token: 1 row of 131071, 29 us.
 template <typename T, bool STAGED>
 __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __grid_constant__ SampleParams p, int C) {
@@ -719,14 +729,43 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   const float min_p = p.min_p ? p.min_p[row] : 0.f;
   const float u = p.u[row];
   const T* src = static_cast<const T*>(p.logits) + row * p.ld + r.first;
-  float mx = -INFINITY, mn = INFINITY;
-  uint32_t nan = 0, top = 0;  // top: the lowest index of the largest
-  auto look = [&](float f, int i) {
-    nan |= f != f;
-    if (f > mx) mx = f, top = (uint32_t)(r.first + i);
-    if (f > -INFINITY) mn = fminf(mn, f);
+  r.tokens = tokens;
+  r.wide = (reinterpret_cast<uintptr_t>(src) & (4 * sizeof(T) - 1)) == 0;
+  r.inf = false;
+  // Of four tokens at a time only the largest counts for now: an instruction or
+  // two per token (looking at each for the least and the first of the largest
+  // made it 15).
+  float mx = -INFINITY, mn = INFINITY;  // the largest, NaN if one is; the least of the largest of four
+  auto look = [&](int c, const float (&v)[4]) {
+    const float t = max_of(v);
+    r.set_top(c, t);
+    mx = max_of(mx, t);
+    if (t > -INFINITY) mn = fminf(mn, t);
   };
-  if constexpr (STAGED) {
+  constexpr int CHUNKS = STAGED ? 16 : 32;
+  if (!STAGED || (r.wide && sizeof(T) == 2)) {  // (fp32 is staged faster by single words: 8 rows of 524288 28.5 against 22.4 us)
+    r.x = STAGED ? x : src;
+    constexpr int BATCH = sizeof(T) == 4 ? 2 : STAGED ? 16 : 4;  // more spill registers
+#pragma unroll
+    for (int c0 = 0; c0 < CHUNKS; c0 += BATCH) {
+      typename decltype(r)::Four f[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; k++)
+        if (r.w0 + (c0 + k) * CHUNK < r.w1) f[k] = r.fetch(src, r.w0 + (c0 + k) * CHUNK);
+#pragma unroll
+      for (int k = 0; k < BATCH; k++) {
+        const int i = r.w0 + (c0 + k) * CHUNK;
+        r.no_top(c0 + k);
+        if (i < r.w1) {
+          if constexpr (STAGED) *reinterpret_cast<typename decltype(r)::Four*>(x + i + lane * 4) = f[k];
+          float v[4];
+          r.values(f[k], v);
+          look(c0 + k, v);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
     r.x = x;
     constexpr int BATCH = 16;  // loads in flight per thread
     for (int i0 = r.w0 + lane; i0 < r.w1; i0 += 32 * BATCH) {
@@ -734,40 +773,29 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
 #pragma unroll
       for (int k = 0; k < BATCH; k++) v[k] = i0 + 32 * k < tokens ? src[i0 + 32 * k] : T(-INFINITY);
 #pragma unroll
-      for (int k = 0; k < BATCH; k++) {
-        const int i = i0 + 32 * k;
-        if (i >= r.w1) break;
-        const float f = to_float(v[k]) + 0.f;  // -0 becomes 0
-        x[i] = T(f);
-        look(f, i);
-      }
+      for (int k = 0; k < BATCH; k++)
+        if (i0 + 32 * k < r.w1) x[i0 + 32 * k] = v[k];
     }
     __syncwarp();
-    r.tops();
-  } else {
-    r.x = src;
-    r.tokens = tokens;
-    r.wide = (reinterpret_cast<uintptr_t>(src) & (4 * sizeof(T) - 1)) == 0;
-    r.inf = false;
-    constexpr int BATCH = sizeof(T) == 4 ? 4 : 8;
 #pragma unroll
-    for (int c0 = 0; c0 < 32; c0 += BATCH) {
-      typename decltype(r)::Four f[BATCH];
-#pragma unroll
-      for (int k = 0; k < BATCH; k++)
-        if (r.w0 + (c0 + k) * CHUNK < r.w1) f[k] = r.load(r.w0 + (c0 + k) * CHUNK);
-#pragma unroll
-      for (int k = 0; k < BATCH; k++) {
-        const int i = r.w0 + (c0 + k) * CHUNK;
-        r.no_top(c0 + k);
-        if (i < r.w1) {
-          float v[4];
-          r.values(f[k], v);
-#pragma unroll
-          for (int e = 0; e < 4; e++) look(v[e], i + lane * 4 + e);
-          r.set_top(c0 + k, v);
-        }
+    for (int c = 0; c < CHUNKS; c++) {
+      r.no_top(c);
+      if (r.w0 + c * CHUNK < r.w1) {
+        float v[4];
+        r.four(r.w0 + c * CHUNK, v);
+        look(c, v);
       }
+    }
+  }
+  uint32_t nan = mx != mx, top = ALL;  // top: the lowest index of the largest, if that is the answer
+  if (!(temperature > 0.f)) {
+#pragma unroll 1
+    for (int i = r.w0; i < r.w1; i += CHUNK) {
+      float v[4];
+      r.four(i, v);
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (v[e] == mx) top = min(top, (uint32_t)(r.first + i + lane * 4 + e));
     }
   }
   // of the warp, the CTA, the row, as keys; the index of the largest
@@ -862,11 +890,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
       r.inf = true;
     }
     r.tops();
-    mx = mn = 0.f;
-    low = -INFINITY;
+    mx = mn = low = 0.f;
   }
   if (low > -INFINITY) mn = low;  // the bins divide what lies above
-  r.mx = mx, r.mn = mn;
+  r.mx = mx, r.mn = fmaxf(low, -FLT_MAX);
   // log2(e) / T as a pair of floats: the quotient of the leading part, and that
   // of what is left
   constexpr float E_HI = 1.44269502f, E_LO = (float)(1.44269504088896341 - (double)E_HI);
