@@ -656,6 +656,24 @@ def test_sample_uneven_rows(V, dtype):
                      min_p=f([0.0, 0.1, 0.0, 0.02, 0.3, 0.0, 0.0, 0.0]))
 
 
+@pytest.mark.parametrize("n", [100, 128, 129, 600])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_sample_ties_among_the_likely(n, dtype):
+    """Borders of both filters inside a run of equal likely tokens, short and long."""
+    V = 40000
+    x, u = logits_of(6, V, n, dtype)
+    g = torch.Generator().manual_seed(n)
+    for m in range(6):
+        x[m, torch.randperm(V, generator=g)[:n]] = 9.25
+        x[m, torch.randperm(V, generator=g)[:3]] = 10.5
+    f = torch.tensor
+    k = f([n // 2, n - 1, n + 3, n + 60, 2, 900], dtype=torch.int32)
+    for t in ([1.0] * 6, [0.8, 1.0, 3.0, 1.3, 0.5, 1.0]):
+        check_sample(x, u, temperature=f(t), top_k=k)
+        check_sample(x, u, temperature=f(t), top_k=k, top_p=f([0.5, 0.9, 0.999, 0.4, 0.9, 0.7]), min_p=f([0.0, 0.1, 0.0, 0.4, 0.0, 0.2]))
+        check_sample(x, u, temperature=f(t), top_p=f([0.01, 0.05, 0.1, 0.3, 0.02, 0.5]))
+
+
 @pytest.mark.parametrize("M, V, dtype", [(44, 100003, torch.float32), (20, 140001, torch.float32), (20, 300007, BF)])
 def test_sample_many_long_rows(M, V, dtype):
     """More than the SMs hold at a time, rows at every alignment, each kind of row among them."""

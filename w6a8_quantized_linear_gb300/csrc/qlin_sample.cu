@@ -393,6 +393,14 @@ __device__ __forceinline__ void push_counts(const R& r) {
   }
 }
 
+// A token of weight w in bin b of this CTA's histogram.
+__device__ __forceinline__ void add_mass(SampleShared* s, int b, unsigned long long w) {
+  atomicAdd(&s->hist[0][b], 1u);
+  const uint32_t wl = (uint32_t)w;
+  const uint32_t wh = (uint32_t)(w >> 32) + ((uint32_t)(atomicAdd(&s->hist[1][b], wl) + wl) < wl ? 1u : 0u);  // the carry
+  if (wh) atomicAdd(&s->hist[2][b], wh);
+}
+
 // The lowest and the highest key whose logits fall into bin b of the row's
 // range: 16 lanes try as many keys at once for either.  All warps alike, no
 // exchange.  (The tokens' own lowest and highest took a pass and an exchange.)
@@ -447,14 +455,8 @@ __device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long lon
       for (; m; m &= m - 1) {  // lanes take their tokens together, whichever of their four they are
         const float v = m & 1 ? x[0] : m & 2 ? x[1] : m & 4 ? x[2] : x[3];
         const int b = (int)bin(v);
-        atomicAdd(&s->hist[0][b], 1u);
-        if (BY_MASS) {
-          const unsigned long long w = r.weight(v);
-          const uint32_t wl = (uint32_t)w;
-          const uint32_t wh =
-              (uint32_t)(w >> 32) + ((uint32_t)(atomicAdd(&s->hist[1][b], wl) + wl) < wl ? 1u : 0u);  // the carry
-          if (wh) atomicAdd(&s->hist[2][b], wh);
-        }
+        if (BY_MASS) add_mass(s, b, r.weight(v));
+        else atomicAdd(&s->hist[0][b], 1u);
       }
     });
     if (push) {
@@ -691,14 +693,134 @@ __device__ __forceinline__ void choose(const R& r, const Kept& kept, float min_p
   }
 }
 
+// Both filters and the choice over a list of `left` survivors in order of their
+// index, `spread` places apart, four places per thread, which keeps their
+// weights in registers.  One histogram of counts and masses serves both
+// filters (one for each, and weights formed anew in every pass, took 3.4 us
+// more).  False, with nothing written, where more than FEW tokens share the
+// bin of a border.
+template <typename R>
+__device__ __forceinline__ bool finish(const R& r, const float* list_x, const uint32_t* list_index, uint32_t left, int spread,
+                                       uint32_t top_k, float top_p, float min_p, float u, int32_t* token, float* prob) {
+  static_assert(LIST == SAMPLE_THREADS * 4, "four places per thread");
+  SampleShared* s = r.s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = threadIdx.x;
+  const float4 f = *reinterpret_cast<const float4*>(list_x + mine * 4);
+  float v[4] = {f.x, f.y, f.z, f.w};
+  unsigned long long w[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    if (e % spread || mine * 4 + e >= (int)left * spread) v[e] = -INFINITY;
+    w[e] = r.weight(v[e]);  // of -inf: 0
+  }
+  Kept kept = everything();
+  if (left > top_k || top_p < 1.f) {
+    s->hist[0][mine] = s->hist[1][mine] = s->hist[2][mine] = 0;
+    if (mine == 0) s->filled = 0;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (v[e] > -INFINITY) add_mass(s, (int)r.place(v[e]), w[e]);
+    __syncthreads();
+    const uint32_t count = s->hist[0][mine];
+    const unsigned long long mass = s->hist[1][mine] + ((unsigned long long)s->hist[2][mine] << 32);
+    uint32_t before = warp_scan(count);
+    unsigned long long below = warp_scan(mass);
+    if (lane == 31) s->warp_a[warp] = before, s->warp_sum[warp] = below;
+    __syncthreads();
+    const uint32_t counts = lane < SAMPLE_WARPS ? s->warp_a[lane] : 0;
+    const unsigned long long masses = lane < SAMPLE_WARPS ? s->warp_sum[lane] : 0;
+    before += warp_sum(lane < warp ? counts : 0u) - count;
+    below += warp_sum(lane < warp ? masses : 0ull) - mass;
+    unsigned long long total = warp_sum(masses), sum = 0, ahead = 0;
+    const uint32_t cand = mine / 4;
+    Candidate me = {};
+    bool one = false;
+    uint32_t rank = 0;
+    // the bin's tokens, and for each the number and mass of those before it
+    auto settle = [&](int b, uint32_t n) {
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (v[e] > -INFINITY && (int)r.place(v[e]) == b)
+          s->few[atomicAdd(&s->filled, 1u)] = {key_of(v[e]), (uint32_t)(mine * 4 + e), w[e]};
+      __syncthreads();
+      one = cand < n;
+      me = s->few[one ? cand : 0];
+      sum = 0, rank = 0;
+      if (one)
+        for (uint32_t k = mine % 4; k < n; k += 4) {
+          const Candidate o = s->few[k];
+          if (o.key > me.key || (o.key == me.key && o.index < me.index)) sum += o.weight, rank++;
+        }
+      sum += __shfl_xor_sync(ALL, sum, 1), rank += __shfl_xor_sync(ALL, rank, 1);
+      sum += __shfl_xor_sync(ALL, sum, 2), rank += __shfl_xor_sync(ALL, rank, 2);
+    };
+    if (left > top_k) {
+      if (before < top_k && top_k <= before + count) {
+        s->pick = mine, s->pick_count = count, s->pick_index = before;
+        s->before = below;
+      }
+      __syncthreads();
+      const uint32_t n = s->pick_count, last = top_k - s->pick_index - 1;
+      ahead = s->before;
+      if (n > FEW) return false;
+      settle(s->pick, n);
+      if (one && rank == last) s->pick_key = me.key, s->pick_index = me.index, s->pick_mass = sum + me.weight;
+      __syncthreads();
+      kept = {logit_of(s->pick_key), (int)s->pick_index};
+      total = ahead + s->pick_mass;
+    }
+    if (top_p < 1.f) {
+      unsigned long long want = max(1ull, share_of<true>(total, fmaxf(top_p, 0.f)));
+      __syncthreads();  // what was picked, and the list, have been read
+      if (left > top_k && want > ahead) {
+        want -= ahead;  // in the same bin
+      } else {
+        if (below < want && want <= below + mass) s->pick = mine, s->pick_count = count, s->before = below;
+        if (mine == 0) s->filled = 0;
+        __syncthreads();
+        const uint32_t n = s->pick_count;
+        want -= s->before;
+        if (n > FEW) return false;
+        settle(s->pick, n);
+      }
+      if (one && sum < want && want <= sum + me.weight) s->pick_key = me.key, s->pick_index = me.index;
+      __syncthreads();
+      kept = {logit_of(s->pick_key), (int)s->pick_index};
+    }
+  }
+  unsigned long long least = 1, ours = 0;
+  if (min_p > 0.f) least = max(1ull, share_of<true>(1ull << ONE_BITS, fminf(min_p, 1.f)));
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    if (!kept.has(v[e], mine * 4 + e) || w[e] < least) w[e] = 0;
+    ours += w[e];
+  }
+  const unsigned long long upto = warp_scan(ours);
+  if (lane == 31) s->warp_sum[warp] = upto;  // the scan's have been read, some barriers ago
+  __syncthreads();
+  const unsigned long long theirs = lane < SAMPLE_WARPS ? s->warp_sum[lane] : 0, all = warp_sum(theirs);
+  unsigned long long run = warp_sum(lane < warp ? theirs : 0ull) + upto - ours;
+  const unsigned long long target = min(all, u > 0.f ? share_of<false>(all, fminf(u, 1.f)) + 1 : 1);
+  if (run < target && target <= run + ours) {  // one thread
+    int e = 0;
+#pragma unroll
+    for (int k = 0; k < 3; k++)
+      if (e == k && run + w[k] < target) run += w[k], e++;
+    *token = (int32_t)list_index[mine * 4 + e];
+    if (prob) *prob = ratio(e == 0 ? w[0] : e == 1 ? w[1] : e == 2 ? w[2] : w[3], all);
+  }
+  return true;
+}
+
 // One row per cluster of C CTAs.  STAGED: its logits are read once, into shared
 // memory; else the chunks that a pass needs are read again where they are,
 // mostly from L2, so that slices of 65536 tokens leave room for two CTAs per SM.
 // Bound by latency, not by the bytes (0.6 us for 8 rows of 131071): reading
 // (2 us), the exchanges between the CTAs (1 to 2 us each with 16 CTAs), and
 // passes over 4 to 64 tokens per thread; for many rows by the instructions of
-// those passes.  Measured: 8 rows of 131071, all filters, 15.2 us; 1 row of
-// 32000, top-p, 14.9 us; 64 rows of 262144 in bf16, top-k and top-p, 36.3 us;
+// those passes.  Measured: 8 rows of 131071, all filters, 11.9 us; 1 row of
+// 32000, top-p, 14.9 us; 64 rows of 262144 in bf16, top-k and top-p, 32.8 us;
 // top-p alone has to weigh every token: 1 row of 131071, 29 us.
 template <typename T, bool STAGED>
 __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __grid_constant__ SampleParams p, int C) {
@@ -949,6 +1071,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
         }
         row_sync(r);
         if (r.rank) return;
+        int32_t* const token = p.token + row;
+        float* const prob = p.prob ? p.prob + row : nullptr;
+        if (finish(r, list_x, list_index, left, spread, (uint32_t)top_k, top_p, min_p, u, token, prob)) return;
+        __syncthreads();
         Row<float, LIST / (CHUNK * SAMPLE_WARPS)> one;
         one.x = list_x;
         one.s = s;
@@ -966,7 +1092,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
         kept = everything();
         if (left > (uint32_t)top_k) narrow<false>(one, kept, (unsigned long long)top_k, 0.f);
         if (top_p < 1.f) narrow<true>(one, kept, 0, fmaxf(top_p, 0.f));
-        choose(one, kept, min_p, u, list_index, p.token + row, p.prob ? p.prob + row : nullptr);
+        choose(one, kept, min_p, u, list_index, token, prob);
         return;
       }
     }
