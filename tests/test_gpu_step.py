@@ -674,7 +674,8 @@ def test_sample_ties_among_the_likely(n, dtype):
         check_sample(x, u, temperature=f(t), top_p=f([0.01, 0.05, 0.1, 0.3, 0.02, 0.5]))
 
 
-@pytest.mark.parametrize("M, V, dtype", [(44, 100003, torch.float32), (20, 140001, torch.float32), (20, 300007, BF)])
+@pytest.mark.parametrize("M, V, dtype", [(44, 100003, torch.float32), (20, 140001, torch.float32), (20, 300007, BF), (66, 90001, torch.float32),
+                                         (16, 262143, torch.float32)])
 def test_sample_many_long_rows(M, V, dtype):
     """More than the SMs hold at a time, rows at every alignment, each kind of row among them."""
     x, u = logits_of(M, V, V + 5, dtype)

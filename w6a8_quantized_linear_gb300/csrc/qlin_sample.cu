@@ -820,7 +820,7 @@ __device__ __forceinline__ bool finish(const R& r, const float* list_x, const ui
 // (2 us), the exchanges between the CTAs (1 to 2 us each with 16 CTAs), and
 // passes over 4 to 64 tokens per thread; for many rows by the instructions of
 // those passes.  Measured: 8 rows of 131071, all filters, 11.9 us; 1 row of
-// 32000, top-p, 14.9 us; 64 rows of 262144 in bf16, top-k and top-p, 32.8 us;
+// 32000, top-p, 15.2 us; 64 rows of 262144 in bf16, top-k and top-p, 29.0 us;
 // top-p alone has to weigh every token: 1 row of 131071, 29 us.
 template <typename T, bool STAGED>
 __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __grid_constant__ SampleParams p, int C) {
@@ -1121,28 +1121,30 @@ struct SamplePlan {
 // Slices of 64 KB in shared memory leave room for two CTAs per SM.  Few rows
 // take more CTAs each: a pass costs less, an exchange more.  Under top-k the
 // passes are over few tokens: up to 128 CTAs (8 rows of 131071: 4, 8 and 16
-// CTAs per row 18.3, 16.0 and 17.4 us; 64 rows of 32000 with 2 and 4: 17.1 and
-// 18.6), clusters of 16 for four rows at most (4 rows of 262144 with 8 and 16:
-// 17.3 and 15.8; 1 row of 32000: 12.7 and 13.2).  Else all tokens are weighed:
-// up to 256 CTAs (32 rows of 32000 with 4 and 8: 31.8 and 28.0; 64 rows with 4
-// and 8: 41.2 and 48.2), and clusters of 16 while their slices are large
-// beside the rows' number (16 rows of 131071 with 8 and 16: 54.5 and 49.9; of
-// 32000: 23.7 and 27.9).  From 16384 tokens on two CTAs pay for any number of
-// rows (256 rows of 32000 in bf16 with 1 and 2: 71 and 41 us).
-// Rows that fill more than one wave in this way are read where they are, by
-// fewer CTAs, if under top-k (64 rows of 262144 in bf16 with 8 staged and 4
-// such CTAs: 43.5 and 38.0 us; in fp32, with 16 and 4: 85.7 and 39.5; but rows
-// below 256 KB, 128 of 131071 in bf16: 45.6 and 48.5) or if it would take
-// clusters of 16, of which few fit at a time (32 rows of 262144 in fp32 under
-// top-p with 16 staged and 8 such CTAs: 202 and 148; but with 8 staged, 64
-// rows of 262144 in bf16: 216 and 250).
+// CTAs per row 13.9, 12.0 and 13.9 us; 64 rows of 32000 with 2 and 4: 13.0 and
+// 14.0), clusters of 16 for four rows at most (4 rows of 262144 with 8 and 16:
+// 13.2 and 12.2; 1 row of 32000: 10.1 and 10.8).  Else all tokens are weighed:
+// up to 256 CTAs (32 rows of 32000 with 4 and 8: 30.6 and 26.3; 64 rows with 4
+// and 8: 38.5 and 45.1), and clusters of 16 while their slices are large
+// beside the rows' number (16 rows of 131071 with 8 and 16: 53.0 and 48.2; of
+// 32000: 22.3 and 27.7).  From 16384 tokens on two CTAs pay for any number of
+// rows (256 rows of 32000 in bf16 with 1 and 2: 65 and 30 us).
+// Clusters of 16, of which few fit at a time, are worth avoiding: by slices of
+// 128 KB while one wave of them does (16 rows of 262144 in fp32 under top-k
+// with 16 and 8 CTAs: 25.6 and 19.9), else by reading the rows where they are
+// (64 rows of 262144 in fp32 under top-k with 16 staged and 4 such CTAs: 76.2
+// and 34.9; 32 rows under top-p with 16 and 8: 200 and 145).  With 8 that pays
+// for many fp32 rows under top-k (128 rows of 131071 with 8 and 2: 49.2 and
+// 40.9; 48 rows with 8 and 4: 25.6 and 26.3), not for bf16 (64 rows of 262144
+// with 8 and 4: 29.5 and 33.0) or top-p (203 and 258).
 SamplePlan sample_plan(int64_t M, int64_t V, int64_t size, bool by_count, int most) {
-  constexpr int64_t WAVE = 2 * 152;
+  constexpr int64_t SMS = 152;
   int C = V > 16384 ? 2 : 1;
   while (C < most && C * (int64_t)65536 < V * size) C *= 2;
-  if (by_count ? C >= 8 && M * C > (C == 16 ? 128 : WAVE) : C == 16 && M * C > WAVE) {
+  if (by_count && C == 16 && V <= 8 * 32768 && M > 4 && 8 * M <= SMS) return {8, true};
+  if (by_count ? C == 16 ? M > 8 : C == 8 && size == 4 && M >= 64 : C == 16 && C * M > 2 * SMS) {
     for (C = 2; C * (int64_t)65536 < V;) C *= 2;
-    while (C < 8 && 2 * C * M <= WAVE) C *= 2;
+    while (C < 8 && 2 * C * M <= 2 * SMS) C *= 2;
     return {C, false};
   }
   while (C < 8 && C * (int64_t)(SAMPLE_THREADS * 4) < V && 2 * C * M <= (by_count ? 128 : 256)) C *= 2;
