@@ -674,6 +674,29 @@ def test_sample_ties_among_the_likely(n, dtype):
         check_sample(x, u, temperature=f(t), top_p=f([0.01, 0.05, 0.1, 0.3, 0.02, 0.5]))
 
 
+@pytest.mark.parametrize("V, n", [(300, 129), (2000, 700), (2048, 2048), (8001, 3000)])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_sample_borders_inside_long_runs_of_one_logit(V, n, dtype):
+    """Rows that one CTA takes (8001 tokens too, in so many rows), the border of either filter inside a bin of more than
+    128 equal logits: the bin's range of keys and the places of its equal tokens are found one after the other.  Every
+    row's answer, and the same in each of many launches."""
+    M = 200
+    g = torch.Generator().manual_seed(V + n)
+    x = torch.randn(M, V, generator=g)
+    run = torch.rand(M, V, generator=g).argsort(1)[:, :n]
+    x.scatter_(1, run, 4.25)  # above nearly all others
+    x = x.to(dtype)
+    u = torch.rand(M, generator=g)
+    k = torch.randint(max(1, n // 8), n, (M,), generator=g, dtype=torch.int32)
+    p = 0.02 + 0.5 * torch.rand(M, generator=g)
+    for kw in (dict(top_k=k), dict(top_p=p), dict(top_k=k, top_p=p)):
+        want = check_sample(x, u, **kw)
+        dev = {name: t.to(DEV) for name, t in kw.items()}
+        dx, du = x.to(DEV), u.to(DEV)
+        again = [qlin.sample(dx, du, **dev) for _ in range(20)]
+        assert all(torch.equal(want, t) for t in again)
+
+
 @pytest.mark.parametrize("M, V, dtype", [(44, 100003, torch.float32), (20, 140001, torch.float32), (20, 300007, BF), (66, 90001, torch.float32),
                                          (16, 262143, torch.float32)])
 def test_sample_many_long_rows(M, V, dtype):

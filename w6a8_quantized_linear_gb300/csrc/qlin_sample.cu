@@ -590,6 +590,7 @@ __device__ __forceinline__ void narrow(const R& r, Kept& kept, unsigned long lon
       __syncthreads();
       kmin = __reduce_min_sync(ALL, lane < SAMPLE_WARPS ? s->warp_a[lane] : ALL);
       kmax = __reduce_max_sync(ALL, lane < SAMPLE_WARPS ? s->warp_b[lane] : 0);
+      __syncthreads();  // read by all warps: index_of writes its counts there
     } else {
       if (level == 0) {
         keys_of_bin(r, kept, b, &kmin, &kmax);
