@@ -521,6 +521,22 @@ qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* 
                                 size_t ws_bytes, unsigned flags, void* stream);
 
 /*
+ * Test export for failure detection: qlin_tree_attention without flags, except
+ * that the launch's first CTA never issues its `copy`-th copy of a tile (0: the
+ * keys of its first tile, 1: their values, 2: the next tile's keys ...).  The
+ * bounded waits on it expire after about a second; the kernel writes
+ * QLIN_ERR_DEVICE_TIMEOUT into the status word, waits (bounded) for the copies
+ * and products that it did issue, frees its tensor memory and returns, leaving
+ * the context and the workspace usable.  out is unspecified afterwards.
+ * Nothing faults.  bf16 caches of width 128 and T * Hq / heads <= 32 only
+ * (else QLIN_ERR_UNSUPPORTED).
+ */
+qlin_status qlin_debug_tree_attention_fault(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq,
+                                            const void* q, int64_t q_stride, float scale, void* out,
+                                            int64_t out_stride, void* ws, size_t ws_bytes, int64_t copy,
+                                            void* stream);
+
+/*
  * Keeps an accepted path of a verified tree: row keep[b][i] of sequence b
  * moves to token len[b] + i, for i < n_keep[b], and len_out[b] = len[b] +
  * n_keep[b].  The kept rows are given in increasing order (a row's parent

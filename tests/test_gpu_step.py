@@ -370,6 +370,32 @@ def test_attention_bad_pages_are_reported_and_not_followed():
     assert qlin.read_device_status(ws) == qlin.ERR_BAD_INDEX
 
 
+@pytest.mark.parametrize("copy", [0, 1, 2, 5, 13])
+@pytest.mark.parametrize("n", [100, 150000])
+def test_attention_an_expired_wait_is_reported_not_hung(n, copy):
+    """A tile's keys or values that are never asked for, in a run of one tile and in one longer than the ring (a copy
+    that the run does not have is not missed): the waits expire, the status word says so, and the next calls on the
+    same workspace give what they gave before."""
+    c = Case([n], 4, 1, 128, 64, seed=5)
+    q = torch.randn(4, 8 * 128, generator=torch.Generator().manual_seed(3)).to(BF).to(DEV)
+    out = torch.empty_like(q)
+    ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, 1, 4, 8), DEV)
+    want = qlin.tree_attention(c.cache, c.step, q, ws=ws)
+    assert qlin.read_device_status(ws) == qlin.OK
+    assert qlin.debug_tree_attention_fault(c.cache, c.step, q, out, ws, copy) == qlin.OK
+    status = qlin.read_device_status(ws)
+    if n == 100 and copy > 1:
+        assert status == qlin.OK and torch.equal(out, want)
+        return
+    assert status == qlin.ERR_DEVICE_TIMEOUT
+    for _ in range(2):
+        assert torch.equal(qlin.tree_attention(c.cache, c.step, q, ws=ws), want)
+    assert qlin.read_device_status(ws) == qlin.ERR_DEVICE_TIMEOUT  # until it is cleared
+    qlin.workspace_init(ws)
+    assert torch.equal(qlin.tree_attention(c.cache, c.step, q, ws=ws), want)
+    assert qlin.read_device_status(ws) == qlin.OK
+
+
 def test_attention_replayed_with_other_lengths():
     """One captured call serves every length that its table holds."""
     c = Case([900], 4, 2, 128, 16, seed=21)

@@ -118,6 +118,20 @@ def test_attention_refusals(L):
     assert L.qlin_tree_attention_workspace_bytes(None, 2, 3, 8, ctypes.byref(n)) == bad
 
 
+def test_attention_fault_export_refusals(L):
+    def call(c=None, s=None, Hq=8, copy=0, ws=4096):
+        c, s = c or cache(), s or step()
+        return L.qlin_debug_tree_attention_fault(ctypes.addressof(c), ctypes.addressof(s), Hq, 4096, 1024, 0.1, 4096, 1024, ws,
+                                                 1 << 30, copy, None)
+
+    assert call(copy=-1) == qlin.ERR_INVALID_ARG
+    assert call(ws=None) == qlin.ERR_INVALID_ARG
+    assert call(c=cache(dtype=1)) == qlin.ERR_UNSUPPORTED
+    assert call(c=cache(width=64)) == qlin.ERR_UNSUPPORTED
+    assert call(s=step(T=17)) == qlin.ERR_UNSUPPORTED  # 34 query rows per cache head
+    assert call(s=step(T=0)) == qlin.OK
+
+
 def test_keep_refusals(L):
     for kw in (dict(keep=None), dict(keep=2), dict(n=None), dict(n=6), dict(lo=2), dict(ks=2), dict(ws=128, wsb=256)):
         assert keep(L, **kw) == qlin.ERR_INVALID_ARG, kw

@@ -52,6 +52,7 @@ struct AttentionParams {
   int ctas;
   int box;           // tokens per TMA copy: a page or a tile, whichever is smaller
   int page_shift;    // log2 of the page size
+  int64_t fault_copy;  // test only (FAULT): the copy that the first CTA never issues
 };
 
 __device__ __forceinline__ int64_t committed(const AttentionParams& p, int b) {  // tokens that are there
@@ -309,7 +310,7 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, Attent
 // memory: weights are relative to a maximum of the past, at most 2^8, which
 // fp16 holds.
 // (At most 128 registers, so that blocks of the second launch find room beside.)
-template <typename T, int D, int SPLIT>
+template <typename T, int D, int SPLIT, bool FAULT = false>
 __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __grid_constant__ AttentionParams p) {
   extern __shared__ uint8_t raw[];
   __shared__ AttentionShared sh;
@@ -380,15 +381,17 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&s->full[slot], bytes);
             __syncwarp();
-            if (page >= 0)
+            const bool lost = FAULT && blockIdx.x == 0 && i == p.fault_copy;  // test only: this phase never completes
+            if (page >= 0 && !lost)
               tma_load_4d(ring + slot * TB + (panel * TK + box * p.box) * 128, kv ? &p.map_v : &p.map_k, panel * 64,
                           (int)(token & (p.cache.page_size - 1)), w.h, page, &s->full[slot]);
           }
         }
       } while (ok && next_item<D>(p, w));
-      // nothing leaves while its copies are in flight
-      if (!ok)
-        for (uint32_t j = i > NB ? i - NB : 0; j < i; j++) (void)mbar_wait(&s->full[j % NB], (j / NB) & 1);
+      // nothing leaves while its copies are in flight, whichever role gave up
+      // (this one may have issued its last copy long before); where none did,
+      // they are all waited for elsewhere too
+      for (uint32_t j = i > NB ? i - NB : 0; j < i; j++) (void)mbar_wait(&s->full[j % NB], (j / NB) & 1);
     } else if (warp == ISSUER) {
       // ---- MMA: the whole warp keeps the books, so that descriptors stay in
       // uniform registers, and one elected thread issues (built by that thread
@@ -908,6 +911,10 @@ Kernels attention_kernels(int dtype, int width) {
                           : kernels_of<__nv_bfloat16, 256>();
   return width == 64 ? kernels_of<__half, 64>() : width == 128 ? kernels_of<__half, 128>() : kernels_of<__half, 256>();
 }
+// A test's: bf16 of width 128, up to 32 query rows of a cache head.
+const void* attention_fault_kernel() {
+  return reinterpret_cast<const void*>(qlin_attention_kernel<__nv_bfloat16, 128, 4, true>);
+}
 constexpr size_t attention_smem(int width) {  // query rows, ring, and the way to a 1024-byte boundary
   return (size_t)q_bytes(width) + (size_t)ring_buffers(width) * tile_bytes(width) + 1024;
 }
@@ -943,13 +950,16 @@ qlin_status attention_setup(int* ctas) {
   std::call_once(d.once, [&d, dev] {
     int sms = 0;
     cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    auto prepare = [&e](const void* fn, int width) {
+      for (auto set : {std::make_pair(cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attention_smem(width)),
+                       // all of it as shared memory, so that the second launch's blocks fit beside
+                       std::make_pair(cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared)})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, set.first, set.second);
+    };
     for (int dtype : {QLIN_BF16, QLIN_F16})
       for (int width : {64, 128, 256})
-        for (const void* fn : attention_kernels(dtype, width).main)
-          for (auto set : {std::make_pair(cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attention_smem(width)),
-                           // all of it as shared memory, so that the second launch's blocks fit beside
-                           std::make_pair(cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared)})
-            if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, set.first, set.second);
+        for (const void* fn : attention_kernels(dtype, width).main) prepare(fn, width);
+    prepare(attention_fault_kernel(), 128);
     d.ctas = sms < ATT_MAX_CTAS ? sms : ATT_MAX_CTAS;
     d.ready = e == cudaSuccess && g_encode && sms > 0 ? QLIN_OK : QLIN_ERR_CUDA;
     if (e != cudaSuccess) (void)cudaGetLastError();
@@ -1010,9 +1020,9 @@ qlin_status qlin_tree_attention_workspace_bytes(const qlin_kv_cache* cache, int 
   return QLIN_OK;
 }
 
-qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, const void* q,
-                                int64_t q_stride, float scale, void* out, int64_t out_stride, void* ws,
-                                size_t ws_bytes, unsigned flags, void* stream) {
+static qlin_status attend(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, const void* q, int64_t q_stride,
+                          float scale, void* out, int64_t out_stride, void* ws, size_t ws_bytes, unsigned flags,
+                          void* stream, int64_t fault_copy = -1) {
   qlin_status st = check_cache(cache);
   if (st != QLIN_OK) return st;
   st = check_step(step, QLIN_MAX_TREE);
@@ -1051,10 +1061,11 @@ qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* 
   p.R = step->T * p.group;
   p.Rp = padded_rows(step->T, p.group);
   p.ctas = ctas;
+  p.fault_copy = fault_copy;
   void* args[] = {&p};
   const Kernels fn = attention_kernels(cache->dtype, cache->width);
   const int copies = p.R > ATT_ROWS / 2 ? 0 : p.R > ATT_ROWS / 4 ? 1 : 2;
-  st = launch_step(fn.main[copies], dim3((unsigned)ctas, 1, 1), dim3(ATT_THREADS, 1, 1), attention_smem(cache->width),
+  st = launch_step(fault_copy < 0 ? fn.main[copies] : attention_fault_kernel(), dim3((unsigned)ctas, 1, 1), dim3(ATT_THREADS, 1, 1), attention_smem(cache->width),
                    static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0);
   if (st != QLIN_OK) return st;
   // the narrowest blocks that all find room while the first launch runs, one
@@ -1064,6 +1075,24 @@ qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* 
   while (wide < (D < 128 ? 1 : 2) && blocks * (D / (32 << wide)) > ctas) wide++;
   return launch_step(fn.join[wide], dim3((unsigned)(step->B * cache->heads), (unsigned)(p.Rp / 8), (unsigned)(D / (32 << wide))),
                      dim3(JOIN_THREADS, 1, 1), 0, static_cast<cudaStream_t>(stream), args, true);
+}
+
+qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, const void* q,
+                                int64_t q_stride, float scale, void* out, int64_t out_stride, void* ws,
+                                size_t ws_bytes, unsigned flags, void* stream) {
+  return attend(cache, step, Hq, q, q_stride, scale, out, out_stride, ws, ws_bytes, flags, stream);
+}
+
+qlin_status qlin_debug_tree_attention_fault(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq,
+                                            const void* q, int64_t q_stride, float scale, void* out,
+                                            int64_t out_stride, void* ws, size_t ws_bytes, int64_t copy,
+                                            void* stream) {
+  const qlin_status st = check_cache(cache);
+  if (st != QLIN_OK) return st;
+  if (copy < 0 || !step || step->T < 0 || Hq < 1) return QLIN_ERR_INVALID_ARG;
+  if (cache->dtype != QLIN_BF16 || cache->width != 128 || (int64_t)step->T * (Hq / cache->heads) > ATT_ROWS / 4)
+    return QLIN_ERR_UNSUPPORTED;
+  return attend(cache, step, Hq, q, q_stride, scale, out, out_stride, ws, ws_bytes, 0, stream, copy);
 }
 
 }  // extern "C"

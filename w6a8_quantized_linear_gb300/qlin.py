@@ -83,6 +83,7 @@ def lib() -> ctypes.CDLL:
                 "qlin_tree_attention_workspace_bytes": (st, [vp, i32, i32, i32, ctypes.POINTER(sz)]),
                 "qlin_tree_attention": (st, [vp, vp, i32, vp, i64, ctypes.c_float, vp, i64, vp, sz, ctypes.c_uint,
                                              vp]),
+                "qlin_debug_tree_attention_fault": (st, [vp, vp, i32, vp, i64, ctypes.c_float, vp, i64, vp, sz, i64, vp]),
                 "qlin_kv_keep": (st, [vp, vp, vp, i64, vp, vp, vp, sz, ctypes.c_uint, vp]),
                 "qlin_sample": (st, [i32, i64, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint, vp]),
             }
@@ -597,6 +598,19 @@ def tree_attention(cache: KVCache, step: KVStep, q: torch.Tensor, scale: float |
     _check(_fn("qlin_tree_attention")(cache._ref, step._ref, Hq, q.data_ptr(), qs, D ** -0.5 if scale is None else scale,
                                       out.data_ptr(), os_, ws.data_ptr(), ws.numel(), flags, raw), "tree_attention")
     return out
+
+
+def debug_tree_attention_fault(cache: KVCache, step: KVStep, q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+                               copy: int, stream=None) -> int:
+    """Test export: ``tree_attention`` (scale width ** -0.5) whose first CTA never issues its
+    ``copy``-th copy of a tile; returns the launch status (the device status word is read
+    separately)."""
+    n, D, dev = step.B * step.T, cache.width, cache._index
+    _same_device(dev, step.len, q, out, ws)
+    Hq = _heads(q, D, "q")
+    return _fn("qlin_debug_tree_attention_fault")(
+        cache._ref, step._ref, Hq, q.data_ptr(), _rows(q, n, Hq * D, cache.dtype, "q"), D ** -0.5, out.data_ptr(),
+        _rows(out, n, Hq * D, torch.bfloat16, "out"), ws.data_ptr(), ws.numel(), copy, _raw_stream(stream, dev))
 
 
 def kv_keep(cache: KVCache, step: KVStep, keep: torch.Tensor, n_keep: torch.Tensor, len_out=None, ws=None,
