@@ -340,6 +340,31 @@ def test_attention_adversarial_maxima():
     check_attention(c, 8, q=q)
 
 
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("group", [1, 2, 4])
+def test_attention_small_weights_add_up(group, dtype):
+    """In each sequence four tokens, one in each part of the first tile, dwarf 200000 others of 2^-25.6 of their weight,
+    which together weigh 0.1 % of them: as many sequences (over the same pages) as there are SMs, so that one run of
+    tiles holds the whole of one.  The dwarfing tokens' values are zero, the others' one: o is the others' share."""
+    n, T, D, page, w = 200000, 32, 64, 64, 2.0 ** -25.6
+    B = torch.cuda.get_device_properties(DEV).multi_processor_count
+    pages = n // page + 1
+    k, v = torch.zeros(pages, 1, page, D, dtype=dtype, device=DEV), torch.ones(pages, 1, page, D, dtype=dtype, device=DEV)
+    for token in (0, 32, 64, 96):
+        k[token // page, 0, token % page] = 1
+        v[token // page, 0, token % page] = 0
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).repeat(B, 1)
+    step = qlin.KVStep(table, i32([n] * B), T, mask=i32([0] * T))
+    q = torch.ones(B * T, group * D, dtype=dtype, device=DEV)
+    out = qlin.tree_attention(qlin.KVCache(k, v), step, q, scale=25.6 * math.log(2) / D).double()
+    others = (n - 4) * w
+    want = others / (4 + others)
+    # a weight is rounded by half a step (the smallest fp16 ones, 2^7 of the largest's scale, step by 2^-24: half of that
+    # is 2^-32 of the largest), its exponent by 2 * 2^-24 * 25.6, the result by half a step of bf16
+    each = max(R.HALF[dtype] * w, 2.0 ** -32 if dtype is FP else 0.0) + 2.0 ** -18 * w
+    assert float((out - want).abs().max()) <= 2.0 ** -8 * want + (1 + 2.0 ** -8) * (n - 4) * each / 4
+
+
 def test_attention_rows_do_not_depend_on_the_batch_values():
     c = Case([400, 77], 4, 2, 128, 16, seed=12)
     ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, 2, 4, 6), DEV)

@@ -27,6 +27,12 @@ constexpr int ATT_ROWS = 128;      // query rows of an item at most: the lanes o
 constexpr int ATT_MAX_CTAS = 160;  // the workspace holds the partial results of this many (one per SM)
 constexpr int JOIN_THREADS = 512;
 constexpr float RESCALE_AT = 8.f;  // log2 units that a row's maximum may rise before its sums are rescaled
+// Weights are relative to a reference that lies so many log2 units below the
+// maximum that set it: fp16 holds 2^(7 + RESCALE_AT), and its smallest steps
+// are then 2^-31 of the largest weight instead of 2^-24.  (200000 tokens of
+// 2^-25 each, 0.6 % of the row, were all rounded away from the sums of v.)
+template <typename T>
+constexpr float BELOW = std::is_same<T, __half>::value ? 7.f : 0.f;
 
 // Tokens of a tile: 32 KB of keys and of values (16 KB at width 64).
 __host__ __device__ constexpr int tile_tokens(int width) { return width == 256 ? 64 : 128; }
@@ -46,7 +52,7 @@ struct AttentionParams {
   __nv_bfloat16* out;
   int64_t q_stride, out_stride;
   uint32_t* status;
-  float* partial;    // [slot][width + 2][padded rows]: sums, then maxima (log2 units) and weights' sums
+  float* partial;    // [slot][width + 2][padded rows]: sums, then references (log2 units) and weights' sums
   float scale_log2;  // scale * log2(e): weights are powers of two
   int Hq, group, R, Rp;  // query rows of an item: T * group, padded to 8
   int ctas;
@@ -270,7 +276,7 @@ struct AttentionShared {
   uint32_t tmem;
   int dead;  // a wait has expired: every role leaves its loop
   Walk walk;
-  float m[ATT_ROWS], l[ATT_ROWS];  // each lane's maximum and sum of weights at an item's end
+  float m[ATT_ROWS], l[ATT_ROWS];  // each lane's reference and sum of weights at an item's end
 };
 
 // A bounded wait of one role; on expiry the workspace's status word is set and
@@ -307,8 +313,8 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, Attent
 // end.
 //
 // A row's maximum may grow by 2^8 before its sums are rescaled in tensor
-// memory: weights are relative to a maximum of the past, at most 2^8, which
-// fp16 holds.
+// memory: weights are relative to a maximum of the past (in fp16 to 2^-7 of
+// it), at most 2^8 (2^15), which fp16 holds.
 // (At most 128 registers, so that blocks of the second launch find room beside.)
 template <typename T, int D, int SPLIT, bool FAULT = false>
 __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __grid_constant__ AttentionParams p) {
@@ -510,7 +516,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
               tma_load_3d(q_smem + e * (ATT_ROWS * 128) + k * LANES * 128, &p.map_q, e * 64, w.h * p.group, w.b * p.step.T,
                           &s->q_full);
         }
-        float m_used = -INFINITY, l = 0.f;
+        float m_used = -INFINITY, l = 0.f;  // the reference, the sum of weights relative to it
         if (warp < active) {
           for (int64_t t = 0; t < w.n; t++) {
             const uint32_t m = n + (uint32_t)t;
@@ -547,11 +553,12 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
             const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             float keep = 1.f;
             bool rescale = false;
+            const float ref = mt - BELOW<T>;
             if (t == 0) {
-              m_used = mt;
-            } else if (mt > m_used + RESCALE_AT) {
-              keep = exp2_approx(m_used - mt);
-              m_used = mt;
+              m_used = ref;
+            } else if (ref > m_used + RESCALE_AT) {
+              keep = exp2_approx(m_used - ref);
+              m_used = ref;
               l *= keep;
               rescale = live;
             }
