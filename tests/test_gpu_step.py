@@ -365,6 +365,30 @@ def test_attention_small_weights_add_up(group, dtype):
     assert float((out - want).abs().max()) <= 2.0 ** -8 * want + (1 + 2.0 ** -8) * (n - 4) * each / 4
 
 
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("T, Hq, scale", [(1, 2, 2.0 ** 28), (4, 4, 2.0 ** 24), (16, 6, 2.0 ** 28), (20, 8, -2.0 ** 33), (3, 2, 2.0 ** 40)])
+def test_attention_huge_scores_choose_the_largest(T, Hq, scale, dtype):
+    """Whole-number q and k under a scale of 2^24 and more: every score but the largest (and its equals) has no weight,
+    however far the fp32 scores' own steps are apart."""
+    c = Case([3000, 5, 0, 700], T, 2, 128, 32, dtype, seed=T)
+    g = torch.Generator().manual_seed(T)
+    for b, n in enumerate(c.lens):
+        k = torch.randint(-2, 3, c.host[b][0].shape, generator=g).to(dtype)
+        c.host[b][0] = k
+        c.put(b, 0, k, c.host[b][1])
+    q = torch.randint(-2, 3, (c.B * T, Hq * 128), generator=g).to(dtype)
+    got = qlin.tree_attention(c.cache, c.step, q.to(DEV), scale=scale).cpu().double().view(c.B, T, Hq, 128)
+    group = Hq // 2
+    for b in range(c.B):
+        seen = torch.stack([c.seen(b, t) for t in range(T)]).repeat_interleave(group, 0)
+        for h in range(2):
+            qq = q.view(c.B, T, Hq, 128)[b, :, h * group:(h + 1) * group].reshape(T * group, 128)
+            o, a, _, _ = R.attention_rows(qq, c.host[b][0][:, h], c.host[b][1][:, h], seen, scale)
+            have = got[b, :, h * group:(h + 1) * group].reshape(T * group, 128)
+            # the weights are one or nothing: what is rounded is their shares (2^-24 each) and the result, by half a step
+            assert bool(((have - o).abs() <= 2.0 ** -8 * o.abs() + 2.0 ** -20 * a).all()), (b, h, float((have - o).abs().max()))
+
+
 def test_attention_rows_do_not_depend_on_the_batch_values():
     c = Case([400, 77], 4, 2, 128, 16, seed=12)
     ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(c.cache, 2, 4, 6), DEV)

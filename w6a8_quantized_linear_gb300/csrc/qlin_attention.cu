@@ -33,6 +33,8 @@ constexpr float RESCALE_AT = 8.f;  // log2 units that a row's maximum may rise b
 // 2^-25 each, 0.6 % of the row, were all rounded away from the sums of v.)
 template <typename T>
 constexpr float BELOW = std::is_same<T, __half>::value ? 7.f : 0.f;
+// From here on fp32 scores (log2 units) are a step or more apart.
+constexpr float FAR = 0x1p23f;
 
 // Tokens of a tile: 32 KB of keys and of values (16 KB at width 64).
 __host__ __device__ constexpr int tile_tokens(int width) { return width == 256 ? 64 : 128; }
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
             const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             float keep = 1.f;
             bool rescale = false;
-            const float ref = mt - BELOW<T>;
+            const float ref = fabsf(mt) < FAR ? mt - BELOW<T> : mt;
             if (t == 0) {
               m_used = ref;
             } else if (ref > m_used + RESCALE_AT) {
@@ -580,6 +582,12 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
               tmem_wait_st();
             }
             const float m_ref = m_used == -INFINITY ? 0.f : m_used;  // none of a copy's tokens is there
+            // The reference comes from a rounded product; a fused weight's exponent
+            // keeps what was rounded off there, up to half a step.  Of scores FAR out
+            // that passes the type's range (fp16's from 2^24 on, bf16's from 2^31
+            // on), so there the product is rounded as the maximum's was.
+            const bool far = __any_sync(0xFFFFFFFFu, fabsf(m_ref) >= FAR);
+            const float factor = far ? 1.f : p.scale_log2;
             if (m >= 2) {
               ok = __all_sync(0xFFFFFFFFu, role_wait(&s->p_free[m & 1], ((m >> 1) - 1) & 1, s, p.status));
               if (!ok) break;
@@ -591,8 +599,12 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
             for (int c0 = CW - CX; c0 >= 0; c0 -= CX) {
               if (c0 != CW - CX) scores(c0);
               uint32_t w2[CX / 2];
+              if (far) {
 #pragma unroll
-              for (int c = 0; c < CX; c++) x[c] = exp2_approx(fmaf(x[c], p.scale_log2, -m_ref));
+                for (int c = 0; c < CX; c++) x[c] = __fmul_rn(x[c], p.scale_log2);
+              }
+#pragma unroll
+              for (int c = 0; c < CX; c++) x[c] = exp2_approx(fmaf(x[c], factor, -m_ref));
               if (valid < CW) {
 #pragma unroll
                 for (int c = 0; c < CX; c++)
