@@ -584,6 +584,15 @@ qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logits, int64_t
                         const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                         int32_t* token, float* prob, unsigned flags, void* stream);
 
+/*
+ * Test export: the weights that qlin_sample gives to logits x under their row's
+ * largest (finite, x <= max) and a temperature above 0, as multiples of 2^-42.
+ * Host memory, computed on the host by the kernel's own source; nothing is
+ * enqueued.
+ */
+qlin_status qlin_debug_sample_weight(int n, const float* x, const float* max, const float* temperature,
+                                     uint64_t* weight);
+
 #ifdef __cplusplus
 }
 #endif

@@ -820,6 +820,34 @@ def test_sample_edges():
     assert t.tolist()[:4] == [-1, -1, 2, 2] and int(t[8]) == 2
 
 
+@pytest.mark.parametrize("V", [5, 3001, 40000])
+def test_sample_differences_beyond_fp32(V):
+    """Rows whose logits are finite and their differences are not, at temperatures that leave them weights; infinite ones."""
+    g = torch.Generator().manual_seed(V)
+    M = 6
+    x = (torch.rand(M, V, generator=g) * 2 - 1) * 3e38
+    x[:, :2] = torch.tensor([3e38, -3e38])
+    x[3, 2::3] = -math.inf
+    u = torch.rand(M, generator=g)
+    one = lambda v: torch.full((M,), float(v))  # noqa: E731
+    k = torch.full((M,), V // 2 + 1, dtype=torch.int32)
+    prob = torch.empty(M, device=DEV)
+    for T in (1e38, 6e37):
+        for kw in ({}, dict(top_p=one(0.9)), dict(top_k=k, min_p=one(0.01))):
+            kw["temperature"] = one(T)
+            token = qlin.sample(x.to(DEV), u.to(DEV), prob=prob, **{n: t.to(DEV) for n, t in kw.items()})
+            for m in range(M):
+                want, p = R.sample_row(x[m].double().numpy(), float(u[m]), **{n: t[m].item() for n, t in kw.items()})
+                # 1 / T is a multiple of 2^-149 above 2^-127: off by 2^-24 of itself in either of two terms, and an exponent
+                # of up to 6e38 / T = 10 by ten times that
+                assert int(token[m]) == want and abs(float(prob[m]) - p) <= 2.0 ** -19 * p, (T, m, int(token[m]), want)
+    token = qlin.sample(x.to(DEV), u.to(DEV), temperature=one(math.inf).to(DEV), prob=prob).cpu()
+    for m in range(M):  # all that are not forbidden, alike
+        alive = x[m].isfinite().nonzero().flatten()
+        want = int(alive[min(int(float(u[m]) * len(alive)), len(alive) - 1)])
+        assert int(token[m]) == want and float(prob[m]) == pytest.approx(1 / len(alive), rel=2.0 ** -22), m
+
+
 def test_sample_strided_rows_and_replay():
     x, u = logits_of(3, 9001, 4)
     wide = torch.full((3, 20000), math.nan)

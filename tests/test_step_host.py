@@ -152,6 +152,36 @@ def test_sample_refusals(L):
     assert call(M=0, logits=None, u=None, token=None) == qlin.OK
 
 
+def test_sample_weight_export_refusals(L):
+    one, z = torch.ones(1), torch.zeros(1)
+    for x, m, t in ((2 * one, one, one), (math.nan * one, one, one), (z, math.inf * one, one), (z, one, z), (z, one, -one),
+                    (z, one, math.nan * one)):
+        with pytest.raises(qlin.QlinError):
+            qlin.debug_sample_weight(x, m, t)
+    assert L.qlin_debug_sample_weight(-1, None, None, None, None) == qlin.ERR_INVALID_ARG
+    assert L.qlin_debug_sample_weight(1, None, None, None, None) == qlin.ERR_INVALID_ARG
+    assert L.qlin_debug_sample_weight(0, None, None, None, None) == qlin.OK
+
+
+def test_sample_weights_of_differences_beyond_fp32(L):
+    """Finite logits whose difference is above the largest fp32 have the weight that the temperature gives them; an
+    infinite temperature gives all of them the same, a forbidden token none."""
+    mx = torch.tensor([3e38, 3.4e38, 2e38, 3e38])
+    x = torch.tensor([-3e38, -3.4e38, -1.9e38, -1e38])
+    one = 1 << 42
+    for T in (3.4e38, 1e38, 6e37, 3e37):
+        T32 = float(torch.tensor(T))
+        want = torch.exp((x.double() - mx.double()) / T32)
+        have = qlin.debug_sample_weight(x, mx, torch.tensor(T32)).double() / one
+        # 1 / T below 2^-126 is a multiple of 2^-149: half a unit of its 2^-128 and more, times y, two fp32 terms
+        y = (want.log().abs() / math.log(2)).double()
+        assert bool(((have - want).abs() <= want * (2.0 ** -21 * y * math.log(2) + 2.0 ** -29) + 1 / one).all()), (T, have, want)
+    assert (qlin.debug_sample_weight(x, mx, torch.tensor(math.inf)) == one).all()
+    assert (qlin.debug_sample_weight(torch.tensor(-math.inf), mx, torch.tensor([math.inf, 1.0, 1e38, 1e-40])) == 0).all()
+    for T in (1e30, 1.0, 1e-40):  # too far below at these
+        assert (qlin.debug_sample_weight(x, mx, torch.tensor(T)) == 0).all()
+
+
 def test_rope_turns_are_exact_fractions(L):
     # whole, half and quarter turns per position; negative ones from the other side
     t = qlin.rope_turns(radians=[0.0, math.pi, math.pi / 2, -math.pi / 2, 2 * math.pi, 5 * math.pi], device="cpu")

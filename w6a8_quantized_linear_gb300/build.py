@@ -24,7 +24,8 @@ UNITS = ["qlin_api.cu", "qlin_kernels_w4.cu", "qlin_kernels_w6.cu", "qlin_kernel
          "qlin_kernels_moe_one_row.cu", "qlin_kernels_codebook_one_row.cu",
          "qlin_append.cu", "qlin_attention.cu", "qlin_sample.cu"]
 SOURCES = [os.path.join(CSRC, f) for f in UNITS + ["qlin_forward.cuh", "qlin_forward_tc.cuh", "qlin_repack.cuh", "qlin_layout.h",
-                                                   "qlin_ptx.cuh", "qlin_instances.h", "qlin_step.h"]] + [
+                                                   "qlin_ptx.cuh", "qlin_instances.h", "qlin_step.h",
+                                                   "qlin_sample_weight.h"]] + [
     os.path.join(INCLUDE, "qlin.h")]
 
 

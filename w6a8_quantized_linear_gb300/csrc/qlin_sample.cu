@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "qlin_ptx.cuh"
+#include "qlin_sample_weight.h"
 #include "qlin_step.h"
 
 namespace qlin {
@@ -30,16 +31,9 @@ constexpr int CHUNK = 128;               // consecutive tokens that a warp takes
 constexpr int FEW = 128;                 // a bin of at most this many tokens is settled by comparing all pairs, four threads each
 constexpr int LIST = 2048;               // so many tokens, what top-k may leave, are carried on by one CTA
 constexpr int OWN = 64;                  // of them from one warp at most
-constexpr int ONE_BITS = 42;             // weights are multiples of 2^-42; 2^19 of them sum below 2^62
 constexpr uint32_t ALL = 0xFFFFFFFFu;
 
-// 2^(i/32) in units of 2^-31, to the nearest
-__constant__ uint32_t TABLE[32] = {
-    0x80000000u, 0x82CD8699u, 0x85AAC368u, 0x88980E81u, 0x8B95C1E4u, 0x8EA4398Bu, 0x91C3D374u, 0x94F4EFA9u,
-    0x9837F052u, 0x9B8D39BAu, 0x9EF53261u, 0xA2704303u, 0xA5FED6AAu, 0xA9A15AB5u, 0xAD583EEAu, 0xB123F582u,
-    0xB504F334u, 0xB8FBAF47u, 0xBD08A39Fu, 0xC12C4CCAu, 0xC5672A11u, 0xC9B9BD86u, 0xCE248C15u, 0xD2A81D92u,
-    0xD744FCCBu, 0xDBFBB798u, 0xE0CCDEECu, 0xE5B906E7u, 0xEAC0C6E8u, 0xEFE4B99Cu, 0xF5257D15u, 0xFA83B2DBu,
-};
+__constant__ uint32_t TABLE[32] = QLIN_EXP2_TABLE;
 
 struct SampleParams {
   const void* logits;
@@ -82,32 +76,6 @@ __device__ __forceinline__ uint32_t key_of(float x) {  // larger logit, larger k
 
 __device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
-}
-
-// exp((x - max) / T) as a multiple of 2^-42.  With c = log2(e) / T as a pair
-// of floats, y = (x - max) c is formed to about 2^-40, split into integer part
-// and a 32-bit fraction f; 2^f is a table of 2^(i/32) times the series of
-// e^z, z < ln(2)/32 (table and short series: Tang, "Table-driven
-// implementation of the exponential function", 1989), its first-order term in
-// integers and the rest, below 2^-12, in fp32.
-__device__ __forceinline__ unsigned long long weight_of(float x, float mx, float ch, float cl, const uint32_t* table) {
-  const float d = x - mx;
-  if (!(d < 0.f)) return d == 0.f ? 1ull << ONE_BITS : 0;  // the largest; NaN cannot come here
-  const float t = d - x;
-  const float e = (x - (d - t)) + (-mx - t);  // d + e = x - mx exactly
-  const float yh = d * ch;
-  if (!(yh > -(ONE_BITS + 2.f))) return 0;  // below half a unit (-inf too)
-  const float yl = fmaf(d, ch, -yh) + fmaf(d, cl, e * ch);
-  const long long fix = __float2ll_rn(yh * 4294967296.f) + __float2int_rn(yl * 4294967296.f);
-  if (fix >= 0) return 1ull << ONE_BITS;  // yh = 0 and a correction that rounds to it
-  const uint32_t f = (uint32_t)fix;
-  const int shift = -(int)(fix >> 32);  // >= 1
-  const uint32_t z = __umulhi(f << 5, 0xB17217F8u);  // (f mod 1/32) ln 2, in units of 2^-37
-  const float zf = (float)z * 0x1p-37f;
-  const uint32_t em1 = z + (uint32_t)(zf * zf * fmaf(zf, fmaf(zf, 1.f / 24, 1.f / 6), 0.5f) * 0x1p37f);  // e^z - 1
-  const uint32_t base = table[f >> 27];
-  const uint32_t m = base + (__umulhi(base, em1) >> 5);  // 2^f in units of 2^-31
-  return shift > ONE_BITS + 1 ? 0 : ((((unsigned long long)m << (ONE_BITS - 31 + 1)) >> shift) + 1) >> 1;
 }
 
 // ceil or floor of n * f for n below 2^62 and f in [0, 1], exactly: f is a
@@ -170,12 +138,13 @@ struct Row {
   int first;         // index of the slice's first token
   int tokens;        // those of the row in the slice
   bool wide, inf;    // in memory four tokens at a time; not STAGED: the infinite ones are left, alike
-  float mx, mn, ch, cl, to_bin;  // mn: nothing that is left is below it
+  float mx, mn, to_bin;  // mn: nothing that is left is below it
+  Weighing weighing;
   uint32_t rank, C;
   SampleShared* s;
   uint32_t* all;     // [C][BINS]: the CTAs' counts
   unsigned long long* group;  // [C][GROUPS]: the CTAs' masses of 32 bins at a time
-  __device__ __forceinline__ unsigned long long weight(float v) const { return weight_of(v, mx, ch, cl, s->table); }
+  __device__ __forceinline__ unsigned long long weight(float v) const { return weight_of(v, weighing, s->table); }
   __device__ __forceinline__ void part(int tokens) {  // whole chunks, alike for all warps
     const int per = (tokens + CHUNK * SAMPLE_WARPS - 1) / (CHUNK * SAMPLE_WARPS) * CHUNK;
     w0 = (threadIdx.x >> 5) * per;
@@ -1017,11 +986,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   }
   if (low > -INFINITY) mn = low;  // the bins divide what lies above
   r.mx = mx, r.mn = fmaxf(low, -FLT_MAX);
-  // log2(e) / T as a pair of floats: the quotient of the leading part, and that
-  // of what is left
-  constexpr float E_HI = 1.44269502f, E_LO = (float)(1.44269504088896341 - (double)E_HI);
-  r.ch = E_HI / temperature;
-  r.cl = (fmaf(-r.ch, temperature, E_HI) + E_LO) / temperature;
+  r.weighing = weighing(mx, temperature);
   r.to_bin = mx - mn > 0.f ? fminf((float)(BINS - 1) / (mx - mn), 3e38f) : 0.f;
 
   Kept kept = low > -INFINITY ? Kept{low, 0x7FFFFFFF} : everything();
@@ -1084,7 +1049,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
         one.rank = 0;
         one.first = 0;
         one.part((int)left * spread);
-        one.mx = r.mx, one.ch = r.ch, one.cl = r.cl, one.to_bin = r.to_bin;
+        one.mx = r.mx, one.to_bin = r.to_bin, one.weighing = r.weighing;
         const int room = (one.w1 - one.w0) * SAMPLE_WARPS;
         for (int i = threadIdx.x; i < room; i += SAMPLE_THREADS)
           if (i % spread || i >= (int)left * spread) list_x[i] = -INFINITY;
@@ -1232,4 +1197,14 @@ extern "C" qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logi
   return launch_step(sample_fn(dtype, plan.staged), dim3((unsigned)(M * C), 1, 1), dim3(SAMPLE_THREADS, 1, 1),
                      sizeof(SampleShared) + shared_counts(C) + slice, static_cast<cudaStream_t>(stream), args,
                      (flags & QLIN_FLAG_PDL) != 0, C);
+}
+
+extern "C" qlin_status qlin_debug_sample_weight(int n, const float* x, const float* max, const float* temperature,
+                                                uint64_t* weight) {
+  static const uint32_t table[32] = QLIN_EXP2_TABLE;
+  if (n < 0 || (n && (!x || !max || !temperature || !weight))) return QLIN_ERR_INVALID_ARG;
+  for (int i = 0; i < n; i++)
+    if (!(x[i] <= max[i]) || !std::isfinite(max[i]) || !(temperature[i] > 0.f)) return QLIN_ERR_INVALID_ARG;
+  for (int i = 0; i < n; i++) weight[i] = weight_of(x[i], weighing(max[i], temperature[i]), table);
+  return QLIN_OK;
 }

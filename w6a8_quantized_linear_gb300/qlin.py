@@ -85,6 +85,7 @@ def lib() -> ctypes.CDLL:
                                              vp]),
                 "qlin_debug_tree_attention_fault": (st, [vp, vp, i32, vp, i64, ctypes.c_float, vp, i64, vp, sz, i64, vp]),
                 "qlin_kv_keep": (st, [vp, vp, vp, i64, vp, vp, vp, sz, ctypes.c_uint, vp]),
+                "qlin_debug_sample_weight": (st, [i32, vp, vp, vp, vp]),
                 "qlin_sample": (st, [i32, i64, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint, vp]),
             }
             for name, (res, args) in sig.items():
@@ -645,3 +646,13 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
                               _floats(top_p, M, "top_p"), _floats(min_p, M, "min_p"), _ints(token, M, "token"),
                               _floats(prob, M, "prob"), flags, _raw_stream(stream, dev)), "sample")
     return token
+
+
+def debug_sample_weight(x: torch.Tensor, max: torch.Tensor, temperature: torch.Tensor) -> torch.Tensor:
+    """Test export: the weights that ``sample`` gives to logits ``x`` under their rows' largest ``max`` (fp32, on the
+    CPU), as int64 multiples of 2^-42."""
+    x, max, temperature = (t.to("cpu", torch.float32).contiguous() for t in torch.broadcast_tensors(x, max, temperature))
+    out = torch.empty(x.shape, dtype=torch.int64)
+    _check(_fn("qlin_debug_sample_weight")(x.numel(), x.data_ptr(), max.data_ptr(), temperature.data_ptr(),
+                                           out.data_ptr()), "debug_sample_weight")
+    return out
