@@ -593,6 +593,15 @@ qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logits, int64_t
 qlin_status qlin_debug_sample_weight(int n, const float* x, const float* max, const float* temperature,
                                      uint64_t* weight);
 
+/*
+ * Test export: the plan that qlin_sample uses for M rows of V logits of type
+ * dtype, with top_k given (1) or not (0), on a device whose clusters hold at
+ * most `most` CTAs (8 or 16): *ctas = CTAs per row, *in_place = 1 where they
+ * read the row where it is (up to 65536 tokens each) and 0 where from shared
+ * memory (up to 32768 each).  Host only.
+ */
+qlin_status qlin_debug_sample_plan(int64_t M, int64_t V, int dtype, int top_k, int most, int* ctas, int* in_place);
+
 #ifdef __cplusplus
 }
 #endif

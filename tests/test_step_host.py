@@ -152,6 +152,26 @@ def test_sample_refusals(L):
     assert call(M=0, logits=None, u=None, token=None) == qlin.OK
 
 
+@pytest.mark.parametrize("most", [8, 16])
+def test_sample_plans_hold_every_row(L, most):
+    """Whatever the number and the length of the rows, and whether the device holds clusters of 16 CTAs or of 8: no more
+    CTAs than a cluster holds, and a slice that each has room for."""
+    lengths = sorted({V + d for n in range(20) for V in (1 << n, 3 << n) for d in (-1, 0, 1)} | {32000, 131071, 262144, 300007, 524288})
+    rows = sorted({1, 3, 5, 6, 7, 12, 20, 63, 65, 1000, 1 << 20, 1 << 24} | {1 << n for n in range(11)} | {9, 17, 19, 38, 76, 152})
+    for V in (v for v in lengths if 1 <= v <= 524288):
+        for M in rows:
+            for dtype in (torch.float32, torch.bfloat16):
+                for top_k in (False, True):
+                    C, in_place = qlin.debug_sample_plan(M, V, dtype, top_k, most)
+                    assert C in (1, 2, 4, 8, 16) and C <= most, (M, V, dtype, top_k)
+                    assert C * (65536 if in_place else 32768) >= V, (M, V, dtype, top_k, C, in_place)
+                    assert C > 1 or (not in_place and V <= 16384)
+    for bad in ((0, 100, torch.float32, False, most), (1, 0, torch.float32, False, most), (1, 524289, torch.float32, False, most),
+                (1, 100, torch.float16, False, most), (1, 100, torch.float32, False, 4)):
+        with pytest.raises(qlin.QlinError):
+            qlin.debug_sample_plan(*bad)
+
+
 def test_sample_weight_export_refusals(L):
     one, z = torch.ones(1), torch.zeros(1)
     for x, m, t in ((2 * one, one, one), (math.nan * one, one, one), (z, math.inf * one, one), (z, one, z), (z, one, -one),

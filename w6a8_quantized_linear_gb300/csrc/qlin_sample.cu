@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   uint32_t* list_index = reinterpret_cast<uint32_t*>(list_x + LIST);
   T* x = reinterpret_cast<T*>(raw + sizeof(SampleShared) + shared_counts(C));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Row<T, STAGED ? 16 : 32, STAGED> r;  // a slice of 32768 or 65536 tokens at most
+  Row<T, STAGED ? 16 : 32, STAGED> r;  // a slice of 32768 or 65536 tokens at most (STAGED_SLICE, IN_PLACE_SLICE)
   r.s = s;
   r.all = all;
   r.group = reinterpret_cast<unsigned long long*>(list_x);  // a list of survivors has no use for it
@@ -1068,8 +1068,11 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __
   choose(r, kept, min_p, u, nullptr, p.token + row, p.prob ? p.prob + row : nullptr);
 }
 
+constexpr int STAGED_SLICE = 32768;  // tokens of a slice in shared memory at most
+constexpr int IN_PLACE_SLICE = 65536;
 constexpr size_t SAMPLE_SMEM = 220 * 1024;
-static_assert(sizeof(SampleShared) + shared_counts(MAX_C) + QLIN_SAMPLE_MAX_V / MAX_C * 4 <= SAMPLE_SMEM, "largest slice");
+static_assert(sizeof(SampleShared) + shared_counts(MAX_C) + STAGED_SLICE * 4 <= SAMPLE_SMEM, "largest slice");
+static_assert(MAX_C * STAGED_SLICE >= QLIN_SAMPLE_MAX_V && 8 * IN_PLACE_SLICE >= QLIN_SAMPLE_MAX_V, "the longest row");
 
 const void* sample_fn(int dtype, bool staged) {
   if (dtype == QLIN_F32)
@@ -1107,9 +1110,10 @@ SamplePlan sample_plan(int64_t M, int64_t V, int64_t size, bool by_count, int mo
   constexpr int64_t SMS = 152;
   int C = V > 16384 ? 2 : 1;
   while (C < most && C * (int64_t)65536 < V * size) C *= 2;
+  if (V > C * (int64_t)STAGED_SLICE) return {8, false};  // where clusters of 16 do not fit the device
   if (by_count && C == 16 && V <= 8 * 32768 && M > 4 && 8 * M <= SMS) return {8, true};
   if (by_count ? C == 16 ? M > 8 : C == 8 && size == 4 && M >= 64 : C == 16 && C * M > 2 * SMS) {
-    for (C = 2; C * (int64_t)65536 < V;) C *= 2;
+    for (C = 2; C * (int64_t)IN_PLACE_SLICE < V;) C *= 2;
     while (C < 8 && 2 * C * M <= 2 * SMS) C *= 2;
     return {C, false};
   }
@@ -1186,7 +1190,6 @@ extern "C" qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logi
   int most = 0;
   qlin_status st = sample_setup(&most);
   if (st != QLIN_OK) return st;
-  if (V > (int64_t)most * (QLIN_SAMPLE_MAX_V / MAX_C)) return QLIN_ERR_UNSUPPORTED;  // a slice of 32768 per CTA
   const SamplePlan plan = sample_plan(M, V, dtype == QLIN_F32 ? 4 : 2, top_k != nullptr, most);
   const int C = plan.C;
   SampleParams p = {logits, ld, u, temperature, top_p, min_p, top_k, token, prob, (int)V,
@@ -1206,5 +1209,16 @@ extern "C" qlin_status qlin_debug_sample_weight(int n, const float* x, const flo
   for (int i = 0; i < n; i++)
     if (!(x[i] <= max[i]) || !std::isfinite(max[i]) || !(temperature[i] > 0.f)) return QLIN_ERR_INVALID_ARG;
   for (int i = 0; i < n; i++) weight[i] = weight_of(x[i], weighing(max[i], temperature[i]), table);
+  return QLIN_OK;
+}
+
+extern "C" qlin_status qlin_debug_sample_plan(int64_t M, int64_t V, int dtype, int top_k, int most, int* ctas,
+                                              int* in_place) {
+  if (M < 1 || M > (1 << 24) || V < 1 || V > QLIN_SAMPLE_MAX_V || (dtype != QLIN_F32 && dtype != QLIN_BF16) ||
+      (top_k != 0 && top_k != 1) || (most != 8 && most != MAX_C) || !ctas || !in_place)
+    return QLIN_ERR_INVALID_ARG;
+  const SamplePlan plan = sample_plan(M, V, dtype == QLIN_F32 ? 4 : 2, top_k != 0, most);
+  *ctas = plan.C;
+  *in_place = plan.staged ? 0 : 1;
   return QLIN_OK;
 }

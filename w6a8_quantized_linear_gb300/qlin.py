@@ -85,6 +85,7 @@ def lib() -> ctypes.CDLL:
                                              vp]),
                 "qlin_debug_tree_attention_fault": (st, [vp, vp, i32, vp, i64, ctypes.c_float, vp, i64, vp, sz, i64, vp]),
                 "qlin_kv_keep": (st, [vp, vp, vp, i64, vp, vp, vp, sz, ctypes.c_uint, vp]),
+                "qlin_debug_sample_plan": (st, [i64, i64, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
                 "qlin_debug_sample_weight": (st, [i32, vp, vp, vp, vp]),
                 "qlin_sample": (st, [i32, i64, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint, vp]),
             }
@@ -656,3 +657,12 @@ def debug_sample_weight(x: torch.Tensor, max: torch.Tensor, temperature: torch.T
     _check(_fn("qlin_debug_sample_weight")(x.numel(), x.data_ptr(), max.data_ptr(), temperature.data_ptr(),
                                            out.data_ptr()), "debug_sample_weight")
     return out
+
+
+def debug_sample_plan(M: int, V: int, dtype, top_k: bool, most: int) -> tuple[int, bool]:
+    """Test export: (CTAs per row, whether they read it where it is) of ``sample`` for M rows of V logits on a device
+    whose clusters hold at most ``most`` CTAs (8 or 16)."""
+    ctas, in_place = ctypes.c_int(), ctypes.c_int()
+    _check(_fn("qlin_debug_sample_plan")(M, V, DTYPES.get(dtype, -1), int(top_k), most, ctypes.byref(ctas),
+                                         ctypes.byref(in_place)), "debug_sample_plan")
+    return ctas.value, bool(in_place.value)
