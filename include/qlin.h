@@ -575,9 +575,11 @@ qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, c
  *   token       : int32 [M].  -1 for a row of -inf alone or with a NaN.
  *   prob        : fp32 [M] or NULL: the token's share of the kept mass (0 with
  *                 token -1).
- * The weights are 42-bit fractions (relative error below 2^-31 for w above
- * 2^-10; a token with w below 2^-43 has none and is never chosen) and every sum of them is an exact integer, so the token does not
- * depend on an order of summation.
+ * The weights are 42-bit fractions and every sum of them is an exact integer,
+ * so the token does not depend on an order of summation.  A weight above 2^-10
+ * is within 2.5 * 2^-31 of itself at temperatures up to 2^100, a lower one
+ * within half of 2^-42 besides; a token with w below 2^-43 has none and is
+ * never chosen.
  */
 #define QLIN_SAMPLE_MAX_V 524288
 qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logits, int64_t ld, const float* u,

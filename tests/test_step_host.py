@@ -4,6 +4,7 @@ frequencies."""
 import ctypes
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -181,6 +182,33 @@ def test_sample_weight_export_refusals(L):
     assert L.qlin_debug_sample_weight(-1, None, None, None, None) == qlin.ERR_INVALID_ARG
     assert L.qlin_debug_sample_weight(1, None, None, None, None) == qlin.ERR_INVALID_ARG
     assert L.qlin_debug_sample_weight(0, None, None, None, None) == qlin.OK
+
+
+def test_sample_weights_are_as_close_as_stated(L):
+    """Weights above 2^-10 within 2.5 * 2^-31 of theirs, as the header says.  In units of 2^-31 of a weight 2^y, by the
+    steps of its making: the table's entry 1/2, the product's cut-off part 1, z and the constant in it 1/32, the series'
+    fp32 roundings (four of 2^-24 of z^2 / 2 < 2^-12) 1/8 and its first term left out (z^5 / 120) 1/11, y's two roundings
+    (2^-32 together, times ln 2) 0.35, the last one to a multiple of 2^-42 (2^-43 / 2^-10) 1/4: 2.4.  Below: within half a
+    unit of 2^-42 more."""
+    g = torch.Generator().manual_seed(3)
+    n = 400000
+    T = torch.exp2(torch.rand(n, generator=g) * 40 - 20)
+    mx = torch.randn(n, generator=g) * T * torch.exp2(torch.rand(n, generator=g) * 8 - 4)
+    x = mx - T * torch.rand(n, generator=g) * 7.0
+    x[::2] = mx[::2] - T[::2] * torch.rand(n // 2, generator=g) * 31.0
+    have = qlin.debug_sample_weight(x, mx, T).numpy().astype(np.longdouble) / 2 ** 42
+    a, b, t = (v.numpy().astype(np.longdouble) for v in (x, mx, T))
+    want = np.exp((a - b) / t)
+    off = np.abs(have - want)
+    big = want >= 2.0 ** -10
+    assert big.sum() > n // 3 and float((off[big] / want[big]).max()) <= 2.5 * 2.0 ** -31
+    assert float((off - 2.5 * 2.0 ** -31 * want).max()) <= 2.0 ** -43
+    # every entry of the table, every sign of what follows it
+    y = -(np.arange(64)[:, None] + np.array([0.0, 1e-4, 0.25, 0.5, 0.75, 0.9999])) / 32
+    x = torch.tensor(y * math.log(2), dtype=torch.float32)
+    have = qlin.debug_sample_weight(x, torch.zeros(()), torch.ones(())).numpy().astype(np.longdouble) / 2 ** 42
+    want = np.exp(x.numpy().astype(np.longdouble))
+    assert float((np.abs(have - want) / want).max()) <= 2.5 * 2.0 ** -31
 
 
 def test_sample_weights_of_differences_beyond_fp32(L):
