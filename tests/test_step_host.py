@@ -3,6 +3,9 @@ they refuse before anything reaches the GPU, empty calls, and the rotation
 frequencies."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -268,3 +271,23 @@ def test_the_binding_refuses_what_it_can_see():
                  lambda: qlin.kv_keep(c, s, i32(2, 3), i32(2)), lambda: qlin.sample(z(2, 9), z(2, dt=torch.float32))):
         with pytest.raises(ValueError, match="not on a GPU"):  # there is no CPU path
             call()
+
+
+def test_the_package_imports_on_a_torch_without_cuda():
+    """Such a torch has no raw device and stream getters; calls on tensors are refused as on any machine without a GPU."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from w6a8_quantized_linear_gb300 import qlin
+try:
+    qlin.sample(torch.zeros(2, 9), torch.zeros(2))
+except ValueError as e:
+    assert "not on a GPU" in str(e)
+else:
+    raise SystemExit("not refused")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr

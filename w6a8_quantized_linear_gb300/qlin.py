@@ -443,7 +443,10 @@ class KVStep:
 
 _fns: dict = {}
 _F32, _I32 = torch.float32, torch.int32
-_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# Bound once, as each costs a call some host time; the public forms where a torch has no such names (built without CUDA).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _fn(name: str):
