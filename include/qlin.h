@@ -474,7 +474,10 @@ qlin_status qlin_rope_turns(const double* radians, int n, uint64_t* turns);
  *                   16-byte aligned rows.  q may be NULL (nothing is written
  *                   to q_out); k and v may both be NULL (nothing is stored).
  *   q_out         : [B * T, Hq * width] in the cache's type, rows
- *                   q_out_stride elements apart, 16-byte aligned rows.
+ *                   q_out_stride elements apart, 16-byte aligned rows.  Its
+ *                   rows share no memory with those of q, k and v
+ *                   (QLIN_ERR_INVALID_ARG), but a bf16 q of the same rows may
+ *                   be q_out itself.
  *   q_gamma, k_gamma : fp32 [width], 16-byte aligned, or NULL: no norm.
  *   turns, n_turns   : device, from qlin_rope_turns, 8-byte aligned;
  *                   n_turns in 0..width / 2 (0: no rotation).
@@ -503,7 +506,8 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step,
  *   q         : [B * T, Hq * width], the cache's type, rows q_stride elements
  *               apart, 16-byte aligned rows (q_out of qlin_kv_append).
  *   out       : bf16 [B * T, Hq * width], rows out_stride elements apart,
- *               16-byte aligned rows (the o projection's activation).
+ *               16-byte aligned rows (the o projection's activation) that
+ *               share no memory with those of q (QLIN_ERR_INVALID_ARG).
  *   scale     : finite.
  *   ws        : 256-byte aligned, at least
  *               qlin_tree_attention_workspace_bytes; its first word is the

@@ -201,6 +201,25 @@ def test_append_takes_strided_rows_of_one_projection():
     assert torch.equal(a, q.to(BF)) and torch.equal(got[0].flatten(1), k.cpu().to(BF)) and torch.equal(got[1].flatten(1), v.cpu().to(BF))
 
 
+@pytest.mark.parametrize("rot, pairs", [(128, False), (64, False), (96, False), (128, True)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_append_in_place_of_a_bf16_projection(dtype, rot, pairs):
+    """q_out is q itself, woven with k and v into one projection: what a call with memory of its own gives."""
+    D, Hq, heads, T = 128, 40, 4, 70
+    c = Case([50, 3], T, heads, D, 16, dtype, fill=False, tree="none")
+    x = torch.randn(2 * T, (Hq + 2 * heads) * D, generator=torch.Generator().manual_seed(rot)).to(BF).to(DEV)
+    q, k, v = x[:, : Hq * D], x[:, Hq * D: (Hq + heads) * D], x[:, (Hq + heads) * D:]
+    kw = dict(k=k, v=v, q_gamma=torch.rand(D, device=DEV), k_gamma=torch.rand(D, device=DEV),
+              turns=qlin.rope_turns(1e5, rot, device=DEV), pairs=pairs)
+    want, rest = qlin.kv_append(c.cache, c.step, q=q, **kw), x[:, Hq * D:].clone()
+    stored = [t.clone() for t in (c.k, c.v)]
+    own = q if dtype is BF else x.view(FP)[:, : Hq * D]
+    assert qlin.kv_append(c.cache, c.step, q=q, q_out=own, **kw) is own
+    assert torch.equal(own, want) and torch.equal(x[:, Hq * D:], rest)
+    for a, b in zip(stored, (c.k, c.v)):
+        assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
+
+
 def test_append_reports_pages_out_of_range():
     ws = qlin.new_workspace(256, DEV)
     for bad in (-1, 10 ** 6, 2 ** 31 - 1):

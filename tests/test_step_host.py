@@ -136,6 +136,38 @@ def test_attention_fault_export_refusals(L):
     assert call(s=step(T=0)) == qlin.OK
 
 
+def test_outputs_that_share_memory_with_inputs_are_refused(L):
+    """Two rows of 1024 and 512 elements here (B = 2, T = 1): inside one another, end to end, and woven into one pool."""
+    s = step(T=1)
+
+    def att(q, qs, out, os):
+        return attention(L, s=s, q=q, qs=qs, out=out, os=os)
+
+    bad = qlin.ERR_INVALID_ARG
+    M = 1 << 20
+    for q, qs, out, os in ((M, 1024, M, 1024), (M, 1024, M + 16, 1024), (M, 1024, M + 4096 - 16, 1024), (M + 4096 - 16, 1024, M, 1024),
+                           (M, 2048, M + 2048 - 16, 2048), (M, 2048, M + 4096 + 2048 - 16, 2048), (M, 2048, M, 4096),
+                           (M, 4096, M + 4096, 1024)):
+        assert att(q, qs, out, os) == bad, (q - M, qs, out - M, os)
+    # apart: this far the arguments are right, and the call goes on to ask for a device
+    for q, qs, out, os in ((M, 1024, M + 4096, 1024), (M + 4096, 1024, M, 1024), (M, 2048, M + 2048, 2048), (M + 2048, 2048, M, 2048),
+                           (M, 1 << 40, M + 2048, 1 << 40), (M, 2048, M + 8192, 4096)):
+        assert att(q, qs, out, os) != bad, (q - M, qs, out - M, os)
+
+    def app(**kw):
+        return append(L, s=s, **{**dict(src=0, q=M, qs=1024, k=2 * M, ks=512, v=3 * M, vs=512, qo=4 * M, qos=1024), **kw})
+
+    assert app() != bad and app(src=2, qs=1024) != bad
+    assert app(qo=M) != bad  # bf16 rows in their own places
+    for kw in (dict(qo=M + 16), dict(qo=M, src=2), dict(qo=M, qos=1032), dict(qo=2 * M), dict(qo=2 * M + 2048 - 16), dict(qo=3 * M - 2048),
+               dict(qo=3 * M + 1024 * 2 - 16)):
+        assert app(**kw) == bad, kw
+    # q, k and v woven into one projection of 2048 elements a row, q in its own place, or written between
+    row = dict(qs=2048, k=M + 2048, ks=2048, v=M + 3072, vs=2048)
+    assert app(**row, qo=M, qos=2048) != bad
+    assert app(**row, qo=M + 2048, qos=2048) == bad and app(**row, qo=M + 16, qos=2048) == bad
+
+
 def test_keep_refusals(L):
     for kw in (dict(keep=None), dict(keep=2), dict(n=None), dict(n=6), dict(lo=2), dict(ks=2), dict(ws=128, wsb=256)):
         assert keep(L, **kw) == qlin.ERR_INVALID_ARG, kw

@@ -346,6 +346,14 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step,
   if (k && (!rows_ok(k, k_stride, cache->heads * D, size) || !rows_ok(v, v_stride, cache->heads * D, size)))
     return QLIN_ERR_INVALID_ARG;
   if (!q && !k) return QLIN_OK;
+  if (q) {  // a row of q_out is written while other heads of q, k and v are still to be read
+    const int64_t n = (int64_t)step->B * step->T, kv = cache->heads * D;
+    const bool in_place = q_out == q && size == 2 && q_out_stride == q_stride;  // a thread writes what it alone read
+    if ((!in_place && rows_overlap(q_out, q_out_stride * 2, Hq * D * 2, q, q_stride * size, Hq * D * size, n)) ||
+        rows_overlap(q_out, q_out_stride * 2, Hq * D * 2, k, k_stride * size, kv * size, n) ||
+        rows_overlap(q_out, q_out_stride * 2, Hq * D * 2, v, v_stride * size, kv * size, n))
+      return QLIN_ERR_INVALID_ARG;
+  }
   AppendParams p = {};
   p.cache = *cache;
   p.step = *step;

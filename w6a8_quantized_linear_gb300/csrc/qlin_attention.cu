@@ -1056,6 +1056,9 @@ static qlin_status attend(const qlin_kv_cache* cache, const qlin_kv_step* step, 
   if (!rows_ok(q, q_stride, Hq * D, 2) || !rows_ok(out, out_stride, Hq * D, 2)) return QLIN_ERR_INVALID_ARG;
   if (!ws || !is_aligned(ws, 256)) return QLIN_ERR_INVALID_ARG;
   if (ws_bytes < need) return QLIN_ERR_WORKSPACE;
+  // the second launch writes some columns of a row while others read its q
+  if (rows_overlap(out, out_stride * 2, Hq * D * 2, q, q_stride * 2, Hq * D * 2, (int64_t)step->B * step->T))
+    return QLIN_ERR_INVALID_ARG;
   int ctas = 0;
   st = attention_setup(&ctas);
   if (st != QLIN_OK) return st;

@@ -54,6 +54,22 @@ inline bool rows_ok(const void* p, int64_t stride, int64_t width, int64_t size) 
   return p && is_aligned(p, 16) && stride >= width && (stride * size) % 16 == 0;
 }
 
+// Whether n rows of wa bytes, sa bytes apart from a on, share a byte with n rows
+// of wb bytes, sb apart from b on (rows of unequal strides: the ranges they lie
+// in).  wa <= sa, wb <= sb.
+inline bool rows_overlap(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb, int64_t wb, int64_t n) {
+  using wide = __int128;
+  if (!a || !b || n < 1) return false;
+  const wide ahead = (wide)reinterpret_cast<uintptr_t>(b) - (wide)reinterpret_cast<uintptr_t>(a);
+  if (ahead >= (wide)(n - 1) * sa + wa || -ahead >= (wide)(n - 1) * sb + wb) return false;
+  if (n == 1 || sa != sb) return true;
+  // the first k > -n for which row i + k of b does not end before row i of a begins
+  const wide gap = -ahead - wb;
+  wide k = gap / sa - (gap % sa < 0) + 1;
+  if (k < 1 - n) k = 1 - n;
+  return k < n && ahead + k * sa < wa;
+}
+
 inline qlin_status check_status_ws(const void* ws, size_t ws_bytes) {  // an optional workspace
   if (!ws) return QLIN_OK;
   if (!is_aligned(ws, 256)) return QLIN_ERR_INVALID_ARG;
