@@ -307,6 +307,72 @@ def test_attention_against_64_bits(case):
     check_attention(c, Hq)
 
 
+EVERY = [
+    # lens, T, Hq, heads, width, page, dtype, parents
+    ([20011], 8, 8, 1, 128, 64, BF, TREE8),
+    ([130999], 8, 24, 4, 256, 64, BF, TREE8),
+    ([30011, 9001, 517, 0, 22222, 1, 127, 128, 15000], 3, 48, 8, 128, 32, FP, None),
+    ([9001], 1, 5, 5, 256, 16, FP, None),
+    ([50001, 300], 32, 8, 2, 64, 128, BF, [-1] + [t // 2 for t in range(31)]),
+    ([40003], 1, 2, 2, 64, 256, FP, None),
+    ([70007, 3], 10, 10, 2, 128, 16, BF, None),
+]
+
+
+@pytest.mark.parametrize("case", EVERY, ids=[f"{i}" for i in range(len(EVERY))])
+def test_attention_counts_every_token_once(case):
+    """All keys are alike, so each of the n tokens that a row sees has the weight 1 / n, and all values are zero but for
+    one token a column: that column gives 4096 / n if the row sees the token, or zero.  One call after another until every
+    token of every sequence and cache head has had its column: one that is lost, doubled, or read from another place
+    is off by all of its column, however long the context is."""
+    lens, T, Hq, heads, D, page, dtype, parents = case
+    B, group, parents = len(lens), Hq // heads, parents or [t - 1 for t in range(T)]
+    g = torch.Generator().manual_seed(T)
+    per = [-(-(n + T) // page) for n in lens]
+    order = torch.randperm(sum(per) + 2, generator=g).to(torch.int32)
+    table = torch.full((B, max(per)), -7, dtype=torch.int32)
+    for b in range(B):
+        table[b, : per[b]] = order[sum(per[:b]): sum(per[: b + 1])]
+    table = table.to(DEV)
+    k, v = (torch.full((sum(per) + 2, heads, page, D), math.nan, dtype=dtype, device=DEV) for _ in range(2))
+    tail = []  # the places behind the last token
+    for b, n in enumerate(lens):
+        k[table[b, : per[b]].long()] = 0.5
+        tail.append((table[b, per[b] - 1].long(), n + T - (per[b] - 1) * page))
+        k[tail[b][0], :, tail[b][1]:] = math.nan
+    mask = [0] * T
+    for t in range(T):
+        mask[t] = (mask[parents[t]] if parents[t] >= 0 else 0) | 1 << t
+    cache = qlin.KVCache(k, v)
+    step = qlin.KVStep(table, i32(lens), T, mask=torch.tensor(mask).to(torch.int32).to(DEV))
+    q = torch.randn(B * T, Hq * D, generator=g).to(dtype).to(DEV)
+    ws = qlin.new_workspace(qlin.tree_attention_workspace_bytes(cache, B, T, Hq), DEV)
+    n = torch.tensor(lens, device=DEV)[:, None, None]
+    rows = torch.tensor(mask, device=DEV)
+    count = torch.tensor([bin(m).count("1") for m in mask], device=DEV)
+    share = (4096.0 / (n + count[None, :, None])).double()[..., None]  # [B, T, 1, 1]
+    col, head = torch.arange(D, device=DEV), torch.arange(heads, device=DEV)[:, None]
+    wrong = torch.zeros((), dtype=torch.int64, device=DEV)
+    for first in range(0, max(lens) + T, heads * D):
+        token = (first + head * D + col).expand(B, heads, D)
+        there = token < n + T
+        v.zero_()
+        for page_of, at in tail:
+            v[page_of, :, at:] = math.nan
+        b, h, c = there.nonzero(as_tuple=True)
+        at = token[b, h, c]
+        v[table[b, at // page].long(), h, at % page, c] = 4096
+        out = qlin.tree_attention(cache, step, q, ws=ws).view(B, T, heads, group, D).double()
+        ahead = (token - n)[:, None]                                                # [B, 1, heads, D]
+        bit = rows[None, :, None, None] >> ahead.clamp(0, 31) & 1 == 1
+        seen = there[:, None] & ((ahead < 0) | bit)
+        want = torch.where(seen, share, 0.0)[:, :, :, None]
+        # half a step for the weight's rounding and for the result's, the fp32 sums and exponents
+        wrong += (~((out - want).abs() <= (2 * 2.0 ** -8 + 2.0 ** -14) * want)).sum()
+    assert int(wrong) == 0
+    assert qlin.read_device_status(ws) == qlin.OK
+
+
 def test_attention_trees_of_each_sequence_and_other_scales():
     c = Case([70, 200, 9], 8, 2, 128, 16, parents=TREE8, tree="each", seed=2)
     check_attention(c, 6, scale=0.5)
