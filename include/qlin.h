@@ -398,7 +398,8 @@ qlin_status qlin_forward_noalloc(int fmt, int prologue, int M, int64_t N, int64_
  *
  * The conventions above hold: device pointers, nothing allocated or
  * synchronised, errors of arguments returned before anything is enqueued.  The
- * structs themselves are host memory, read during the call only.
+ * structs themselves are host memory, read during the call only.  A step of no
+ * sequences or no rows enqueues nothing and writes nothing.
  * ------------------------------------------------------------------------ */
 typedef enum { QLIN_BF16 = 0, QLIN_F16 = 1, QLIN_F32 = 2 } qlin_dtype;
 
@@ -482,8 +483,10 @@ qlin_status qlin_rope_turns(const double* radians, int n, uint64_t* turns);
  *   turns, n_turns   : device, from qlin_rope_turns, 8-byte aligned;
  *                   n_turns in 0..width / 2 (0: no rotation).
  *   pairs         : 0: element i turns with i + n_turns; 1: 2i with 2i + 1.
- *   ws            : a workspace (256 bytes) for the status word, or NULL.
- *   flags         : 0 or QLIN_FLAG_PDL (gamma and turns are read early).
+ *   ws            : a workspace (256 bytes) for the status word, or NULL (a bad
+ *                   index is then not followed either, but not reported).
+ *   flags         : 0 or QLIN_FLAG_PDL (nothing is read before earlier kernels
+ *                   complete).
  * T is not limited: a prompt's rows are appended the same way.  Computed in
  * fp32 (the angle exactly, see above) and rounded once.
  */
@@ -551,7 +554,8 @@ qlin_status qlin_debug_tree_attention_fault(const qlin_kv_cache* cache, const ql
  *   n_keep  : int32 [B], 0..count[b].
  *   len_out : int32 [B], or NULL; may be step->len itself.  Not written where
  *             len[b] < 0.
- *   ws      : a workspace (256 bytes) for the status word, or NULL.
+ *   ws      : a workspace (256 bytes) for the status word, or NULL (a bad list
+ *             or index then moves nothing either, but is not reported).
  * T <= 32.  depth and mask are not read.
  */
 qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, const int32_t* keep,

@@ -56,7 +56,7 @@ struct AttentionParams {
   uint32_t* status;
   float* partial;    // [slot][width + 2][padded rows]: sums, then references (log2 units) and weights' sums
   float scale_log2;  // scale * log2(e): weights are powers of two
-  int Hq, group, R, Rp;  // query rows of an item: T * group, padded to 8
+  int group, R, Rp;  // query heads of a cache head; query rows of an item: T * group, padded to 8
   int ctas;
   int box;           // tokens per TMA copy: a page or a tile, whichever is smaller
   int page_shift;    // log2 of the page size
@@ -294,8 +294,11 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, Attent
 // The committed tokens.  S = Q K^T (128 query lanes x a tile's tokens) and
 // O += P V on tcgen05 with fp32 accumulators in tensor memory: lane = query
 // row, so that a softmax thread owns a row and needs no exchange.  P goes from
-// registers into tensor memory in the cache's type and is the A operand of the
-// second product; keys and values are read by the tensor cores straight from
+// registers into tensor memory in the cache's type (half a step each, 2^-8 of a
+// weight in bf16: both operands of a product have one type, and weights in two
+// parts would need tensor memory that scores and sums take, and half as many
+// products again; their sum l adds them unrounded in fp32) and is the A operand
+// of the second product; keys and values are read by the tensor cores straight from
 // the ring that TMA fills (128-byte swizzle; V as the transposed operand).
 //
 // Bound by the stream of keys and values: a tile's 64 KB take an SM 1.5 us at
@@ -1078,7 +1081,6 @@ static qlin_status attend(const qlin_kv_cache* cache, const qlin_kv_step* step, 
   p.status = static_cast<uint32_t*>(ws);
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + STEP_WS_HEADER);
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  p.Hq = Hq;
   p.group = Hq / cache->heads;
   p.R = step->T * p.group;
   p.Rp = padded_rows(step->T, p.group);

@@ -97,8 +97,8 @@ __device__ __forceinline__ unsigned long long share_of(unsigned long long n, flo
   return shift >= 64 ? hi >> (shift - 64) : (lo >> shift) | (hi << (64 - shift));
 }
 
-// a / b to 2^-31 and rounded, for 0 < a <= b: 32-bit division of the numbers'
-// leading bits (fp64 division would cost a microsecond here)
+// a / b to 2^-31 and rounded, for 0 < a <= b: an integer division of the
+// numbers' leading 64 and 32 bits (fp64 division would cost a microsecond here)
 __device__ __forceinline__ float ratio(unsigned long long a, unsigned long long b) {
   const int za = __clzll(a), zb = __clzll(b);
   const unsigned long long q = (a << za) / ((b << zb) >> 32);  // in [2^31, 2^33]

@@ -542,7 +542,9 @@ def kv_append(cache: KVCache, step: KVStep, q=None, k=None, v=None, q_gamma=None
               turns=None, pairs: bool = False, q_out=None, ws=None, flags: int = 0, stream=None):
     """Head norms and rotation of a step's projected q and k ([B * T, heads * width],
     fp32 or bf16); k and v are stored behind the sequences' committed tokens.
-    Returns the normed and rotated q in the cache's type (or None without q)."""
+    Returns the normed and rotated q in the cache's type (or None without q).
+    ``ws`` (256 bytes): its status word gets ``ERR_BAD_INDEX`` for a page out of
+    range; without one nothing is reported."""
     n, D, dev = step.B * step.T, cache.width, cache._index
     _same_device(dev, step.len, q, k, v, q_gamma, k_gamma, turns, q_out, ws)
     if (k is None) != (v is None):
@@ -588,7 +590,9 @@ def tree_attention(cache: KVCache, step: KVStep, q: torch.Tensor, scale: float |
     """Attention of a step's rows (q of ``kv_append``, [B * T, Hq * width]) over the
     cache: every row sees the committed tokens of its sequence and the step's
     rows that its mask names.  Returns bf16 [B * T, Hq * width].  ``scale``:
-    width ** -0.5 unless given."""
+    width ** -0.5 unless given.  Without ``ws`` the call takes memory of its own,
+    and what its status word gets (``ERR_BAD_INDEX``, ``ERR_DEVICE_TIMEOUT``) is
+    lost with it: a caller that reads ``read_device_status`` gives one."""
     n, D, dev = step.B * step.T, cache.width, cache._index
     _same_device(dev, step.len, q, out, ws)
     Hq = _heads(q, D, "q")
@@ -622,7 +626,8 @@ def kv_keep(cache: KVCache, step: KVStep, keep: torch.Tensor, n_keep: torch.Tens
             flags: int = 0, stream=None) -> None:
     """Move the accepted rows ``keep[b, :n_keep[b]]`` (int32 [B, T], increasing) of each
     sequence up behind its committed tokens; ``len_out`` (int32 [B], may be the
-    step's ``len``) gets the new lengths."""
+    step's ``len``) gets the new lengths.  ``ws`` (256 bytes): its status word gets
+    ``ERR_BAD_INDEX`` for a bad list or page; without one nothing is reported."""
     _same_device(cache._index, step.len, keep, n_keep, len_out, ws)
     B, T = step.B, step.T
     if keep.shape != (B, T) or keep.dtype is not torch.int32 or (T > 1 and keep.stride(1) != 1):
