@@ -304,10 +304,10 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, Attent
 // Bound by the stream of keys and values: a tile's 64 KB take an SM 1.5 us at
 // the measured copy bandwidth, its products 0.5 to 0.7 us, its softmax 0.6 us
 // where the warps share it.  Measured (both launches): 48 query rows over
-// 131k tokens of 4 heads of 256, 95.7 us for 537 MB (5.6 TB/s, 0.82 of the
+// 131k tokens of 4 heads of 256, 95.8 us for 537 MB (5.6 TB/s, 0.82 of the
 // copy; the stream itself runs at 0.97, the rest is start, joining and the
 // SMs' different ends); 18 rows over 8 sequences of 8 heads of 128, 111 us for 661 MB (0.88);
-// width 64 streams 0.66 of the copy, bound by the softmax's latency per tile.
+// width 64 streams 0.62 to 0.66 of the copy, bound by the softmax's latency per tile.
 //
 // A warp reaches 32 lanes, so with few rows most softmax warps would idle while
 // one takes longer over a tile (128 tokens: 1.9 us when this was measured) than

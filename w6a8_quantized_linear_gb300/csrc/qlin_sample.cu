@@ -789,9 +789,9 @@ __device__ __forceinline__ bool finish(const R& r, const float* list_x, const ui
 // Bound by latency, not by the bytes (0.6 us for 8 rows of 131071): reading
 // (2 us), the exchanges between the CTAs (1 to 2 us each with 16 CTAs), and
 // passes over 4 to 64 tokens per thread; for many rows by the instructions of
-// those passes.  Measured: 8 rows of 131071, all filters, 11.9 us; 1 row of
-// 32000, top-p, 15.2 us; 64 rows of 262144 in bf16, top-k and top-p, 29.0 us;
-// top-p alone has to weigh every token: 1 row of 131071, 29 us.
+// those passes.  Measured: 8 rows of 131071, all filters, 12.0 us; 1 row of
+// 32000, top-p, 15.4 us; 64 rows of 262144 in bf16, top-k and top-p, 29.2 us;
+// top-p alone has to weigh every token: 1 row of 131071, 32 us.
 template <typename T, bool STAGED>
 __global__ void __launch_bounds__(SAMPLE_THREADS, 2) qlin_sample_kernel(const __grid_constant__ SampleParams p, int C) {
   extern __shared__ __align__(16) uint8_t raw[];
