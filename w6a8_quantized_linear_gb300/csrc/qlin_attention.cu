@@ -30,7 +30,7 @@ constexpr float RESCALE_AT = 8.f;  // log2 units that a row's maximum may rise b
 // Weights are relative to a reference that lies so many log2 units below the
 // maximum that set it: fp16 holds 2^(7 + RESCALE_AT), and its smallest steps
 // are then 2^-31 of the largest weight instead of 2^-24.  (200000 tokens of
-// 2^-25 each, 0.6 % of the row, were all rounded away from the sums of v.)
+// 2^-25.6 each were all rounded away from the sums of v, and counted in l.)
 template <typename T>
 constexpr float BELOW = std::is_same<T, __half>::value ? 7.f : 0.f;
 // From here on fp32 scores (log2 units) are a step or more apart.
@@ -298,16 +298,17 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, Attent
 // weight in bf16: both operands of a product have one type, and weights in two
 // parts would need tensor memory that scores and sums take, and half as many
 // products again; their sum l adds them unrounded in fp32) and is the A operand
-// of the second product; keys and values are read by the tensor cores straight from
-// the ring that TMA fills (128-byte swizzle; V as the transposed operand).
+// of the second product; keys and values are read by the tensor cores straight
+// from the ring that TMA fills (128-byte swizzle; V as the transposed operand).
 //
 // Bound by the stream of keys and values: a tile's 64 KB take an SM 1.5 us at
 // the measured copy bandwidth, its products 0.5 to 0.7 us, its softmax 0.6 us
 // where the warps share it.  Measured (both launches): 48 query rows over
 // 131k tokens of 4 heads of 256, 95.8 us for 537 MB (5.6 TB/s, 0.82 of the
 // copy; the stream itself runs at 0.97, the rest is start, joining and the
-// SMs' different ends); 18 rows over 8 sequences of 8 heads of 128, 111 us for 661 MB (0.88);
-// width 64 streams 0.62 to 0.66 of the copy, bound by the softmax's latency per tile.
+// SMs' different ends); 18 rows over 8 sequences of 8 heads of 128, 111 us for
+// 661 MB (0.88); width 64 streams 0.62 to 0.66 of the copy, bound by the
+// softmax's latency per tile.
 //
 // A warp reaches 32 lanes, so with few rows most softmax warps would idle while
 // one takes longer over a tile (128 tokens: 1.9 us when this was measured) than
@@ -1089,7 +1090,8 @@ static qlin_status attend(const qlin_kv_cache* cache, const qlin_kv_step* step, 
   void* args[] = {&p};
   const Kernels fn = attention_kernels(cache->dtype, cache->width);
   const int copies = p.R > ATT_ROWS / 2 ? 0 : p.R > ATT_ROWS / 4 ? 1 : 2;
-  st = launch_step(fault_copy < 0 ? fn.main[copies] : attention_fault_kernel(), dim3((unsigned)ctas, 1, 1), dim3(ATT_THREADS, 1, 1), attention_smem(cache->width),
+  const void* const main = fault_copy < 0 ? fn.main[copies] : attention_fault_kernel();
+  st = launch_step(main, dim3((unsigned)ctas, 1, 1), dim3(ATT_THREADS, 1, 1), attention_smem(cache->width),
                    static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0);
   if (st != QLIN_OK) return st;
   // the narrowest blocks that all find room while the first launch runs, one
