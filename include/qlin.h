@@ -497,6 +497,29 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step,
                            void* stream);
 
 /*
+ * qlin_kv_append with the rows' positions given, on up to four axes: pair i of
+ * a head turns by position[row][axis[i]] * turns[i].  For the rows of an image
+ * or a video (time, height and width each turn pairs of their own), and for
+ * rows whose place in the cache is not their position (after qlin_kv_evict).
+ * Rows are stored behind the committed tokens as by qlin_kv_append; depth is
+ * not read.
+ *   position : int32, row b * T + t of it position_stride entries behind the
+ *              one before, `axes` entries each; any values (negative too).
+ *              Shares no memory with q_out.  Rows not in use are read, but
+ *              have no effect.
+ *   axes     : 1..QLIN_MAX_AXES.
+ *   axis     : host memory, read during the call: n_turns values below axes.
+ *              NULL: axis 0 everywhere (axes = 1 only).
+ */
+#define QLIN_MAX_AXES 4
+qlin_status qlin_kv_append_at(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, int src, const void* q,
+                              int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              const float* q_gamma, const float* k_gamma, float eps, const uint64_t* turns,
+                              int n_turns, int pairs, const int32_t* position, int64_t position_stride, int axes,
+                              const uint8_t* axis, void* q_out, int64_t q_out_stride, void* ws, size_t ws_bytes,
+                              unsigned flags, void* stream);
+
+/*
  * Attention of a step's rows over the cache: every row sees all committed
  * tokens of its sequence, and of the step's own rows (already appended) those
  * that its mask names.  out = sum_j softmax_j(scale * q . k_j) v_j; a row that
@@ -593,6 +616,56 @@ qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, c
 qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logits, int64_t ld, const float* u,
                         const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                         int32_t* token, float* prob, unsigned flags, void* stream);
+
+/*
+ * Logits before qlin_sample: penalties for repeated tokens, biases, a grammar's
+ * mask.  Row b * T + t belongs to sequence b.  A token v stands n times in the
+ * row's generated text: in the history from prompt_len on, and on the row's
+ * path of drafted tokens.  Then, in fp32, rounded once at the end,
+ *   x' = x / r if x > 0, else x * r   where v stands in the history or the path
+ *   x' = x' - frequency * n - presence            where n > 0
+ *   x' = x' + the biases of v, in the list's order
+ *   x' = -inf                                     where v is not allowed.
+ * A logit that none of these concerns is copied as it is.  Any pointer may be
+ * NULL: what it would give is left out.  The struct is host memory, read during
+ * the call only.
+ *   history     : int32 [B, L], rows history_stride apart; the sequence's tokens
+ *                 but for the step's.  Entries outside [0, V) count for nothing.
+ *   history_len : int32 [B]: entries in use (NULL: L).
+ *   prompt_len  : int32 [B]: of these, the first ones that are the prompt's
+ *                 (NULL: none).
+ *   draft       : int32 [B, T], contiguous: the step's tokens; row t's path are
+ *                 those that its mask names, its own token among them.  T <= 32.
+ *   mask        : as in qlin_kv_step, tree_stride too (NULL: the rows up to its own).
+ *   repetition  : fp32 [B]; not above 0, or NaN: 1.   presence, frequency: fp32 [B].
+ *   bias_token, bias : int32, fp32 [B, n_bias], rows bias_stride apart (0: one
+ *                 list for all).  Tokens outside [0, V) are left out.
+ *   allowed     : int32, rows allowed_stride apart (0: one for all), token v the
+ *                 bit v % 32 of word v / 32: 1 where it is allowed.
+ *   L           : 0..QLIN_MAX_HISTORY.      n_bias : 0..QLIN_MAX_BIAS.
+ */
+#define QLIN_MAX_HISTORY 1000000
+#define QLIN_MAX_BIAS 1024
+typedef struct {
+  const int32_t *history, *history_len, *prompt_len, *draft, *mask;
+  const float *repetition, *presence, *frequency;
+  const int32_t* bias_token;
+  const float* bias;
+  const int32_t* allowed;
+  int64_t history_stride, tree_stride, bias_stride, allowed_stride;
+  int32_t L, n_bias;
+} qlin_adjustments;
+
+/*
+ *   V           : 1..524288.   dtype : QLIN_F32 or QLIN_BF16, of logits and out.
+ *   logits, out : [B * T, V], rows ld and out_ld elements apart, aligned to the
+ *                 element.  out may be the logits themselves (same rows; then
+ *                 only what changes is read and written); else they share no
+ *                 memory (QLIN_ERR_INVALID_ARG).  Nor does out with what the
+ *                 struct names.
+ */
+qlin_status qlin_adjust_logits(int B, int T, int64_t V, int dtype, const void* logits, int64_t ld, void* out,
+                               int64_t out_ld, const qlin_adjustments* adjustments, unsigned flags, void* stream);
 
 /*
  * Test export: the weights that qlin_sample gives to logits x under their row's

@@ -18,6 +18,9 @@ struct AppendParams {
   void* q_out;
   const float *q_gamma, *k_gamma;
   const uint64_t* turns;
+  const int32_t* position;  // a row's positions, `position_stride` apart between rows, or none: len + depth
+  int64_t position_stride;
+  uint64_t axis[4];         // which of a row's positions turns pair i: bits 2 (i % 32) of word i / 32, a word per warp
   uint32_t* status;
   float eps;
   int Hq, n_turns, pairs;
@@ -103,12 +106,17 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) qlin_append_kernel(const __
     gamma[1][i] = p.k_gamma ? p.k_gamma[i] : 1.f;
   }
   const int len = p.step.len[b], used = step_rows(p.step, b);
-  const int depth = p.step.depth ? p.step.depth[b * p.step.tree_stride + t] : t;
+  int64_t pos;
+  if (p.position)
+    pos = threadIdx.x < p.n_turns
+              ? p.position[row * p.position_stride + (p.axis[threadIdx.x / 32] >> 2 * (threadIdx.x % 32) & 3)] : 0;
+  else
+    pos = (int64_t)len + (p.step.depth ? p.step.depth[b * p.step.tree_stride + t] : t);
   if (len < 0 || t >= used) return;
   const int n = p.n_turns;
   static_assert(APPEND_THREADS >= D / 2, "a thread per angle");
   if (threadIdx.x < n) {
-    const int64_t angle = (int64_t)((uint64_t)((int64_t)len + depth) * turn);  // in [-1/2, 1/2) turns of 2^64
+    const int64_t angle = (int64_t)((uint64_t)pos * turn);  // in [-1/2, 1/2) turns of 2^64
     float s, c;
     sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &s, &c);
     cs[threadIdx.x] = make_float2(c, s);
@@ -318,11 +326,11 @@ qlin_status qlin_rope_turns(const double* radians, int n, uint64_t* turns) {
   return QLIN_OK;
 }
 
-qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, int src, const void* q,
-                           int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
-                           const float* q_gamma, const float* k_gamma, float eps, const uint64_t* turns, int n_turns,
-                           int pairs, void* q_out, int64_t q_out_stride, void* ws, size_t ws_bytes, unsigned flags,
-                           void* stream) {
+static qlin_status append(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, int src, const void* q,
+                          int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const float* q_gamma, const float* k_gamma, float eps, const uint64_t* turns, int n_turns,
+                          int pairs, const int32_t* position, int64_t position_stride, int axes, const uint8_t* axis,
+                          void* q_out, int64_t q_out_stride, void* ws, size_t ws_bytes, unsigned flags, void* stream) {
   qlin_status st = check_cache(cache);
   if (st != QLIN_OK) return st;
   st = check_step(step, 0x7FFFFFFF);
@@ -335,6 +343,13 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step,
   if (!(eps >= 0.f) || !std::isfinite(eps)) return QLIN_ERR_INVALID_ARG;
   if ((q_gamma && !is_aligned(q_gamma, 16)) || (k_gamma && !is_aligned(k_gamma, 16))) return QLIN_ERR_INVALID_ARG;
   if (n_turns && (!turns || !is_aligned(turns, 8))) return QLIN_ERR_INVALID_ARG;
+  if (position) {
+    if (axes < 1 || axes > QLIN_MAX_AXES || !is_aligned(position, 4) || position_stride < axes ||
+        (axes > 1 && n_turns && !axis))
+      return QLIN_ERR_INVALID_ARG;
+    for (int i = 0; axis && i < n_turns; i++)
+      if (axis[i] >= axes) return QLIN_ERR_INVALID_ARG;
+  }
   if ((k == nullptr) != (v == nullptr)) return QLIN_ERR_INVALID_ARG;
   st = check_status_ws(ws, ws_bytes);
   if (st != QLIN_OK) return st;
@@ -354,6 +369,8 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step,
         rows_overlap(q_out, q_out_stride * 2, Hq * D * 2, k, k_stride * size, kv * size, n) ||
         rows_overlap(q_out, q_out_stride * 2, Hq * D * 2, v, v_stride * size, kv * size, n))
       return QLIN_ERR_INVALID_ARG;
+    if (position && rows_overlap(q_out, q_out_stride * 2, Hq * D * 2, position, position_stride * 4, axes * 4, n))
+      return QLIN_ERR_INVALID_ARG;
   }
   AppendParams p = {};
   p.cache = *cache;
@@ -363,6 +380,9 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step,
   p.q_out = q_out;
   p.q_gamma = q_gamma, p.k_gamma = k_gamma;
   p.turns = turns;
+  p.position = position;
+  p.position_stride = position_stride;
+  for (int i = 0; position && axis && i < n_turns; i++) p.axis[i / 32] |= (uint64_t)axis[i] << 2 * (i % 32);
   p.status = static_cast<uint32_t*>(ws);
   p.eps = eps;
   p.Hq = q ? Hq : 0;
@@ -380,6 +400,28 @@ qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step,
   return launch_step(append_fn(src, cache->dtype, cache->width),
                      dim3((unsigned)rows, (unsigned)((p.heads + per - 1) / per), 1), dim3(APPEND_THREADS, 1, 1), 0,
                      static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0);
+}
+
+qlin_status qlin_kv_append(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, int src, const void* q,
+                           int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const float* q_gamma, const float* k_gamma, float eps, const uint64_t* turns, int n_turns,
+                           int pairs, void* q_out, int64_t q_out_stride, void* ws, size_t ws_bytes, unsigned flags,
+                           void* stream) {
+  return append(cache, step, Hq, src, q, q_stride, k, k_stride, v, v_stride, q_gamma, k_gamma, eps, turns, n_turns,
+                pairs, nullptr, 0, 0, nullptr, q_out, q_out_stride, ws, ws_bytes, flags, stream);
+}
+
+qlin_status qlin_kv_append_at(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, int src, const void* q,
+                              int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              const float* q_gamma, const float* k_gamma, float eps, const uint64_t* turns,
+                              int n_turns, int pairs, const int32_t* position, int64_t position_stride, int axes,
+                              const uint8_t* axis, void* q_out, int64_t q_out_stride, void* ws, size_t ws_bytes,
+                              unsigned flags, void* stream) {
+  if (!position) {  // but an empty step has none to give
+    if (!step || (step->B != 0 && step->T != 0)) return QLIN_ERR_INVALID_ARG;
+  }
+  return append(cache, step, Hq, src, q, q_stride, k, k_stride, v, v_stride, q_gamma, k_gamma, eps, turns, n_turns,
+                pairs, position, position_stride, axes, axis, q_out, q_out_stride, ws, ws_bytes, flags, stream);
 }
 
 qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, const int32_t* keep,

@@ -80,6 +80,8 @@ def lib() -> ctypes.CDLL:
                 "qlin_rope_turns": (st, [vp, i32, vp]),
                 "qlin_kv_append": (st, [vp, vp, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, vp, i32,
                                         i32, vp, i64, vp, sz, ctypes.c_uint, vp]),
+                "qlin_kv_append_at": (st, [vp, vp, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, vp, i32,
+                                           i32, vp, i64, i32, ctypes.c_char_p, vp, i64, vp, sz, ctypes.c_uint, vp]),
                 "qlin_tree_attention_workspace_bytes": (st, [vp, i32, i32, i32, ctypes.POINTER(sz)]),
                 "qlin_tree_attention": (st, [vp, vp, i32, vp, i64, ctypes.c_float, vp, i64, vp, sz, ctypes.c_uint,
                                              vp]),
@@ -87,6 +89,7 @@ def lib() -> ctypes.CDLL:
                 "qlin_kv_keep": (st, [vp, vp, vp, i64, vp, vp, vp, sz, ctypes.c_uint, vp]),
                 "qlin_debug_sample_plan": (st, [i64, i64, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
                 "qlin_debug_sample_weight": (st, [i32, vp, vp, vp, vp]),
+                "qlin_adjust_logits": (st, [i32, i32, i64, i32, vp, i64, vp, i64, vp, ctypes.c_uint, vp]),
                 "qlin_sample": (st, [i32, i64, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint, vp]),
             }
             for name, (res, args) in sig.items():
@@ -538,15 +541,36 @@ def rope_turns(theta: float = 1e4, rot: int = 0, radians=None, device="cuda") ->
     return out.to(device)
 
 
+def rope_axes(sections, dealt: bool = False) -> bytes:
+    """Which axis of a row's positions turns each pair, for ``kv_append``: ``sections[a]``
+    pairs on axis a (up to four axes), one section behind the other, or ``dealt``
+    in turn to the axes that still have some."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0:
+        raise ValueError("sections must be one to four counts, none negative")
+    if not dealt:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    axis = bytearray()
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                left[a] -= 1
+                axis.append(a)
+    return bytes(axis)
+
+
 def kv_append(cache: KVCache, step: KVStep, q=None, k=None, v=None, q_gamma=None, k_gamma=None, eps: float = 1e-6,
-              turns=None, pairs: bool = False, q_out=None, ws=None, flags: int = 0, stream=None):
+              turns=None, pairs: bool = False, q_out=None, ws=None, flags: int = 0, stream=None, position=None,
+              axis: bytes | None = None):
     """Head norms and rotation of a step's projected q and k ([B * T, heads * width],
     fp32 or bf16); k and v are stored behind the sequences' committed tokens.
     Returns the normed and rotated q in the cache's type (or None without q).
     ``ws`` (256 bytes): its status word gets ``ERR_BAD_INDEX`` for a page out of
-    range; without one nothing is reported."""
+    range; without one nothing is reported.  A row's position is the committed
+    length plus its depth, unless ``position`` gives it: int32 [B * T], or
+    [B * T, axes] with ``axis`` (``rope_axes``) naming the axis of each pair."""
     n, D, dev = step.B * step.T, cache.width, cache._index
-    _same_device(dev, step.len, q, k, v, q_gamma, k_gamma, turns, q_out, ws)
+    _same_device(dev, step.len, q, k, v, q_gamma, k_gamma, turns, q_out, ws, position)
     if (k is None) != (v is None):
         raise ValueError("k and v are given together")
     src = q if q is not None else k
@@ -567,12 +591,25 @@ def kv_append(cache: KVCache, step: KVStep, q=None, k=None, v=None, q_gamma=None
         nt = turns.numel()
         if turns.dtype is not torch.int64 or not turns.is_contiguous():
             raise ValueError("turns must come from rope_turns")
-    status = _fn("qlin_kv_append")(
-        cache._ref, step._ref, Hq, DTYPES.get(dtype, -1), None if q is None else q.data_ptr(), qs,
-        None if k is None else k.data_ptr(), ks, None if v is None else v.data_ptr(), vs,
-        _floats(q_gamma, D, "q_gamma"), _floats(k_gamma, D, "k_gamma"), eps, turns.data_ptr() if nt else None, nt,
-        1 if pairs else 0, None if q is None else q_out.data_ptr(), os_, None if ws is None else ws.data_ptr(),
-        0 if ws is None else ws.numel(), flags, _current_stream(dev) if stream is None else _raw_stream(stream, dev))
+    head = (cache._ref, step._ref, Hq, DTYPES.get(dtype, -1), None if q is None else q.data_ptr(), qs,
+            None if k is None else k.data_ptr(), ks, None if v is None else v.data_ptr(), vs,
+            _floats(q_gamma, D, "q_gamma"), _floats(k_gamma, D, "k_gamma"), eps, turns.data_ptr() if nt else None, nt,
+            1 if pairs else 0)
+    tail = (None if q is None else q_out.data_ptr(), os_, None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel(), flags, _current_stream(dev) if stream is None else _raw_stream(stream, dev))
+    if position is None:
+        if axis is not None:
+            raise ValueError("axis names axes of position, which is not given")
+        status = _fn("qlin_kv_append")(*head, *tail)
+    else:
+        axes = position.shape[1] if position.dim() == 2 else 1
+        if position.dtype is not _I32 or position.shape[:1] != (n,) or position.dim() > 2 or (
+                axes > 1 and position.stride(1) != 1):
+            raise ValueError(f"position must be an int32 tensor of [{n}] or [{n}, axes] with contiguous rows")
+        if axis is not None and (type(axis) is not bytes or len(axis) != nt):
+            raise ValueError("axis must come from rope_axes, one entry for each of turns")
+        status = _fn("qlin_kv_append_at")(*head, position.data_ptr(), position.stride(0) if n > 1 else axes, axes, axis,
+                                          *tail)
     if status:
         _check(status, "kv_append")
     return q_out
@@ -655,6 +692,98 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
                               _floats(top_p, M, "top_p"), _floats(min_p, M, "min_p"), _ints(token, M, "token"),
                               _floats(prob, M, "prob"), flags, _raw_stream(stream, dev)), "sample")
     return token
+
+
+class _AdjustStruct(ctypes.Structure):  # qlin_adjustments
+    _fields_ = [(n, ctypes.c_void_p) for n in ("history", "history_len", "prompt_len", "draft", "mask", "repetition", "presence",
+                                               "frequency", "bias_token", "bias", "allowed")] + [
+        (n, ctypes.c_int64) for n in ("history_stride", "tree_stride", "bias_stride", "allowed_stride")] + [
+        (n, ctypes.c_int32) for n in ("L", "n_bias")]
+
+
+def _table(t, rows: int, dtype, what: str) -> tuple[int, int]:
+    """Width and row stride of a [rows, width] tensor of ``dtype``, or of [width] for all rows (stride 0)."""
+    if t.dtype is not dtype or not 1 <= t.dim() <= 2 or (t.dim() == 2 and t.shape[0] != rows) or (
+            t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what} must be a {dtype} tensor of {rows} contiguous rows, or of one row for all")
+    n = t.shape[-1]
+    return n, 0 if t.dim() == 1 else t.stride(0) if rows > 1 else max(n, 1)
+
+
+def adjust_logits(logits: torch.Tensor, out=None, history=None, history_len=None, prompt_len=None, draft=None, mask=None,
+                  repetition=None, presence=None, frequency=None, bias_token=None, bias=None, allowed=None,
+                  flags: int = 0, stream=None) -> torch.Tensor:
+    """Penalties for repeated tokens, biases and a grammar's mask on ``logits``
+    ([B * T, V], fp32 or bf16, T rows per sequence), before ``sample``.  Returns
+    ``out`` (new unless given; ``logits`` itself: in place).
+
+    ``history`` int32 [B, L]: the sequences' tokens, ``history_len`` int32 [B] of
+    them in use, the first ``prompt_len`` int32 [B] the prompt's; ``draft`` int32
+    [B, T] and ``mask`` (as in ``KVStep``): the step's tokens, of which a row
+    sees its own path's.  Tokens seen: divided (multiplied, where not above 0)
+    by ``repetition``; tokens generated n times: less frequency * n + presence
+    (fp32 [B] each).  ``bias_token`` int32 and ``bias`` fp32 [B, n] or [n]: added.
+    ``allowed`` int32 [B * T, ceil(V / 32)] or [ceil(V / 32)]: a bit per token,
+    the others become -inf.  B is the rows of history, draft, or a penalty; else
+    of bias_token; without any of these, each row is its own sequence."""
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [B * T, V] with contiguous rows")
+    M, V = logits.shape
+    dev = logits.get_device()
+    _same_device(dev, out, history, history_len, prompt_len, draft, mask, repetition, presence, frequency, bias_token, bias,
+                 allowed)
+    B = M
+    for t in (history, draft, history_len, prompt_len, repetition, presence, frequency):
+        if t is not None:
+            B = t.shape[0] if t.dim() else 0
+            break
+    else:
+        if bias_token is not None and bias_token.dim() == 2:
+            B = bias_token.shape[0]
+    if (B < 1 or M % B) if M else B != 0:
+        raise ValueError(f"{M} rows of logits do not belong to {B} sequences")
+    T = M // B if B else 0
+    a = _AdjustStruct()
+    if history is not None:
+        if history.dim() != 2:
+            raise ValueError("history must be [B, L]")
+        a.L, a.history_stride = _table(history, B, _I32, "history")
+        a.history = history.data_ptr()
+    a.history_len, a.prompt_len = _ints(history_len, B, "history_len"), _ints(prompt_len, B, "prompt_len")
+    if draft is not None:
+        if draft.shape != (B, T):
+            raise ValueError("draft must be [B, T]")
+        a.draft = _ints(draft, M, "draft")
+        if mask is not None:
+            if mask.dtype is not _I32 or mask.shape not in ((T,), (B, T)) or not mask.is_contiguous():
+                raise ValueError("mask must be a contiguous int32 [T] or [B, T] tensor")
+            a.mask, a.tree_stride = mask.data_ptr(), T if mask.dim() == 2 else 0
+    elif mask is not None:
+        raise ValueError("mask names rows of draft, which is not given")
+    a.repetition, a.presence = _floats(repetition, B, "repetition"), _floats(presence, B, "presence")
+    a.frequency = _floats(frequency, B, "frequency")
+    if (bias_token is None) != (bias is None):
+        raise ValueError("bias_token and bias are given together")
+    if bias is not None:
+        a.n_bias, a.bias_stride = _table(bias_token, B, _I32, "bias_token")
+        if bias.shape != bias_token.shape or _table(bias, B, _F32, "bias") != (a.n_bias, a.bias_stride):
+            raise ValueError("bias must have the shape and strides of bias_token")
+        a.bias_token, a.bias = bias_token.data_ptr(), bias.data_ptr()
+    if allowed is not None:
+        words, a.allowed_stride = _table(allowed, M, _I32, "allowed")
+        if words < (V + 31) // 32:
+            raise ValueError("allowed must have a bit for each token")
+        a.allowed = allowed.data_ptr()
+    if out is None:
+        out = _empty((M, V), logits.dtype, logits.device, stream)
+    elif out.shape != logits.shape or out.dtype != logits.dtype or (out.stride(1) != 1 and V > 1):
+        raise ValueError("out must have the shape and type of logits, with contiguous rows")
+    status = _fn("qlin_adjust_logits")(B, T, V, DTYPES.get(logits.dtype, -1), logits.data_ptr(),
+                                       logits.stride(0) if M > 1 else V, out.data_ptr(), out.stride(0) if M > 1 else V,
+                                       ctypes.addressof(a), flags, _raw_stream(stream, dev))
+    if status:
+        _check(status, "adjust_logits")
+    return out
 
 
 def debug_sample_weight(x: torch.Tensor, max: torch.Tensor, temperature: torch.Tensor) -> torch.Tensor:
