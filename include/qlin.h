@@ -586,6 +586,49 @@ qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, c
                          unsigned flags, void* stream);
 
 /*
+ * Eviction by accumulated weight (qlin_kv_weigh): of each sequence's committed
+ * tokens, head by head, the n_keep[b] of the highest score stay (all, where there
+ * are no more); equal scores by index, the lowest first, NaN behind all others.
+ * A token whose position is below `first`, or at least since[b], counts as the
+ * highest.  Kept tokens before place n_keep[b] stay where they are; those
+ * behind it move, in order, into the places that empty before it: keys, values,
+ * scores and positions.  len_out[b] = the tokens left, the same for all heads.
+ * The order of a head's tokens is then no longer that of their positions
+ * (attention does not depend on it; rows appended later need qlin_kv_append_at,
+ * and what is kept by position needs `position`).
+ *   score        : fp32 [B, heads, room], sequences seq_stride and heads
+ *                  head_stride elements apart, the tokens' contiguous.
+ *   position     : int32 in the same layout, the tokens' positions; NULL: a
+ *                  token's place is its position.
+ *   score_out    : of the same shape, strides of its own: the tokens left.  May
+ *                  be score itself (of the same strides); else the ranges that
+ *                  these four lie in do not overlap (QLIN_ERR_INVALID_ARG).
+ *   position_out : the same for position, or NULL.  (position NULL and
+ *                  position_out given: where the tokens left have been.)
+ *   room         : 0..QLIN_MAX_ROOM.  A sequence of more tokens than that, or
+ *                  than its page table names, is left alone, and the status word gets
+ *                  QLIN_ERR_BAD_INDEX; so are rows on a page out of range.
+ *   n_keep       : int32 [B] (below 0: as 0).
+ *   first        : 0 or more.     since : int32 [B], or NULL: none.
+ *   len_out      : int32 [B], or NULL; may be step->len itself.  Not written where
+ *                  len[b] < 0.
+ *   ws           : 256-byte aligned, at least qlin_kv_evict_workspace_bytes; its
+ *                  first word is the status word.  Calls that overlap on the GPU
+ *                  need workspaces of their own.
+ *   flags        : 0 or QLIN_FLAG_PDL.
+ * count, depth and mask are not read.  The places of two sequences' committed
+ * tokens must not lie on one page: the rows of one would move under the other.
+ * Scores and positions behind the tokens left are not written.
+ */
+#define QLIN_MAX_ROOM 1048576
+qlin_status qlin_kv_evict_workspace_bytes(const qlin_kv_cache* cache, int B, int64_t room, size_t* bytes);
+qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const qlin_kv_step* step, const float* score,
+                          const int32_t* position, int64_t seq_stride, int64_t head_stride, float* score_out,
+                          int32_t* position_out, int64_t out_seq_stride, int64_t out_head_stride, int64_t room,
+                          const int32_t* n_keep, int first, const int32_t* since, int32_t* len_out, void* ws,
+                          size_t ws_bytes, unsigned flags, void* stream);
+
+/*
  * One token per row of logits, from a given uniform number.  The row's tokens
  * stand in order of their logits, equal ones by index.  Kept are the first
  * top_k; of those the shortest beginning whose mass is at least top_p of

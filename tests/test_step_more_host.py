@@ -91,3 +91,40 @@ def test_the_binding_refuses_adjustments_it_can_see():
         qlin.adjust_logits(x)
     with pytest.raises(ValueError, match="contiguous"):
         qlin.adjust_logits(torch.zeros(10, 4).t())
+
+
+def evict(so, /, c=None, s=None, **kw):
+    a = dict(score=1 << 20, position=None, ss=4 * 64, hs=64, score_out=1 << 20, position_out=None, oss=4 * 64, ohs=64, room=64,
+             n_keep=4096, first=0, since=None, len_out=None, ws=1 << 30, wsb=1 << 20, flags=0)
+    a.update(kw)
+    c, s = c or cache(), s or step()
+    return so.qlin_kv_evict(ctypes.addressof(c), ctypes.addressof(s), *[a[n] for n in (
+        "score", "position", "ss", "hs", "score_out", "position_out", "oss", "ohs", "room", "n_keep", "first", "since", "len_out",
+        "ws", "wsb", "flags")], None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(score=None), dict(score_out=None), dict(n_keep=None), dict(ws=None), dict(ws=4096 + 16), dict(room=-1), dict(first=-1),
+    dict(score=4098), dict(position=4097), dict(since=4098), dict(len_out=4097), dict(n_keep=4098), dict(flags=2), dict(hs=63),
+    dict(ss=64), dict(ohs=63), dict(oss=64), dict(ss=-256), dict(score_out=(1 << 20) + 4), dict(score_out=(1 << 20) - 2048 + 4),
+    dict(oss=5 * 64), dict(position=1 << 20), dict(position_out=1 << 20), dict(position=1 << 24, position_out=(1 << 24) + 64),
+    dict(position=1 << 24, score_out=1 << 24), dict(score_out=1 << 24, position_out=(1 << 24) + 1024)])
+def test_evict_refusals(L, bad):
+    assert evict(L, **bad) == qlin.ERR_INVALID_ARG
+
+
+def test_evict_refuses_what_others_do_and_limits(L):
+    for kw, status in BAD_CACHE:
+        assert evict(L, c=cache(**kw)) == status
+    for kw, status in BAD_STEP:
+        assert evict(L, s=step(**kw)) == status
+    assert evict(L, wsb=256) == qlin.ERR_WORKSPACE
+    assert evict(L, room=1 << 21, hs=1 << 21, ss=1 << 23, ohs=1 << 21, oss=1 << 23) == qlin.ERR_UNSUPPORTED
+    assert evict(L, s=step(B=1 << 19), ss=64, hs=1 << 26) == qlin.ERR_UNSUPPORTED
+    assert evict(L, s=step(B=0), score=None, ws=None) == qlin.OK
+    n = ctypes.c_size_t()
+    c = cache()
+    assert L.qlin_kv_evict_workspace_bytes(ctypes.addressof(c), 2, 64, ctypes.byref(n)) == qlin.OK
+    assert n.value >= 256 + 8 * 8 + 8 * 2 * 32 * 4
+    assert L.qlin_kv_evict_workspace_bytes(ctypes.addressof(c), -1, 64, ctypes.byref(n)) == qlin.ERR_INVALID_ARG
+    assert L.qlin_kv_evict_workspace_bytes(ctypes.addressof(c), 2, 64, None) == qlin.ERR_INVALID_ARG

@@ -70,6 +70,19 @@ inline bool rows_overlap(const void* a, int64_t sa, int64_t wa, const void* b, i
   return k < n && ahead + k * sa < wa;
 }
 
+// Accumulated scores: [B, heads, room] 32-bit values, the strides in elements; no
+// two items share a place.
+inline bool scores_ok(int64_t B, int64_t heads, int64_t room, int64_t seq_stride, int64_t head_stride) {
+  if (seq_stride < 0 || head_stride < 0 || seq_stride > (int64_t(1) << 40) || head_stride > (int64_t(1) << 40)) return false;
+  const bool heads_inside = head_stride >= room && (B == 1 || seq_stride >= (heads - 1) * head_stride + room);
+  const bool seqs_inside = seq_stride >= room && (heads == 1 || head_stride >= (B - 1) * seq_stride + room);
+  return (heads == 1 || head_stride >= room) && (B == 1 || seq_stride >= room) &&
+         (heads == 1 || B == 1 || heads_inside || seqs_inside);
+}
+inline int64_t scores_span(int64_t B, int64_t heads, int64_t room, int64_t seq_stride, int64_t head_stride) {
+  return (B - 1) * seq_stride + (heads - 1) * head_stride + room;
+}
+
 inline qlin_status check_status_ws(const void* ws, size_t ws_bytes) {  // an optional workspace
   if (!ws) return QLIN_OK;
   if (!is_aligned(ws, 256)) return QLIN_ERR_INVALID_ARG;

@@ -87,6 +87,9 @@ def lib() -> ctypes.CDLL:
                                              vp]),
                 "qlin_debug_tree_attention_fault": (st, [vp, vp, i32, vp, i64, ctypes.c_float, vp, i64, vp, sz, i64, vp]),
                 "qlin_kv_keep": (st, [vp, vp, vp, i64, vp, vp, vp, sz, ctypes.c_uint, vp]),
+                "qlin_kv_evict_workspace_bytes": (st, [vp, i32, i64, ctypes.POINTER(sz)]),
+                "qlin_kv_evict": (st, [vp, vp, vp, vp, i64, i64, vp, vp, i64, i64, i64, vp, i32, vp, vp, vp, sz,
+                                       ctypes.c_uint, vp]),
                 "qlin_debug_sample_plan": (st, [i64, i64, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
                 "qlin_debug_sample_weight": (st, [i32, vp, vp, vp, vp]),
                 "qlin_adjust_logits": (st, [i32, i32, i64, i32, vp, i64, vp, i64, vp, ctypes.c_uint, vp]),
@@ -672,6 +675,60 @@ def kv_keep(cache: KVCache, step: KVStep, keep: torch.Tensor, n_keep: torch.Tens
     _check(_fn("qlin_kv_keep")(cache._ref, step._ref, keep.data_ptr(), keep.stride(0) if B > 1 else T,
                                _ints(n_keep, B, "n_keep"), _ints(len_out, B, "len_out"), _ptr(ws),
                                0 if ws is None else ws.numel(), flags, _raw_stream(stream, cache._index)), "kv_keep")
+
+
+def _scores(t, shape, dtype, what: str) -> tuple[int, int]:
+    """Strides of a [B, heads, room] tensor of ``dtype``, its tokens contiguous."""
+    if t.shape != shape or t.dtype is not dtype or (shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what} must be a {dtype} tensor of {list(shape)} with contiguous tokens")
+    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2], t.stride(1) if shape[1] > 1 else shape[2]
+
+
+def _score_pair(score, position, shape, what: str) -> tuple[int, int]:
+    strides = _scores(score, shape, _F32, what)
+    if position is not None and _scores(position, shape, _I32, "position" + what[5:]) != strides:
+        raise ValueError(f"position{what[5:]} must have the strides of {what}")
+    return strides
+
+
+def kv_evict_workspace_bytes(cache: KVCache, step: KVStep, room: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_fn("qlin_kv_evict_workspace_bytes")(cache._ref, step.B, room, ctypes.byref(n)), "kv_evict_workspace_bytes")
+    return n.value
+
+
+def kv_evict(cache: KVCache, step: KVStep, score: torch.Tensor, n_keep: torch.Tensor, first: int = 0, since=None,
+             position=None, score_out=None, position_out=None, len_out=None, ws=None, flags: int = 0, stream=None) -> None:
+    """Keep, head by head, the ``n_keep[b]`` committed tokens of the highest ``score``
+    (fp32 [B, heads, room]; equal ones by index) of each sequence; those of
+    positions below ``first`` or from ``since[b]`` on before all others.  Kept tokens
+    behind place n_keep move into the places that empty before it: keys, values,
+    scores and ``position`` (int32, like score; a token's place unless given).
+    ``score_out`` and ``position_out``: where the scores and positions left go, in
+    place unless given.  ``len_out`` (int32 [B], may be the step's ``len``) gets
+    the new lengths.  Without ``ws`` the call takes memory of its own, and what its
+    status word gets (``ERR_BAD_INDEX``) is lost with it."""
+    _same_device(cache._index, step.len, score, n_keep, since, position, score_out, position_out, len_out, ws)
+    B = step.B
+    if score.dim() != 3:
+        raise ValueError("score must be [B, heads, room]")
+    shape = (B, cache.heads, score.shape[2])
+    seq, head = _score_pair(score, position, shape, "score")
+    if score_out is None:
+        score_out = score
+    if position_out is None:
+        position_out = position
+    out_seq, out_head = _score_pair(score_out, position_out, shape, "score_out")
+    raw = _raw_stream(stream, cache._index)
+    if ws is None:
+        ws = _empty(kv_evict_workspace_bytes(cache, step, shape[2]), torch.uint8, cache.device, stream)
+        workspace_init(ws, raw)
+    status = _fn("qlin_kv_evict")(
+        cache._ref, step._ref, score.data_ptr(), _ptr(position), seq, head, score_out.data_ptr(), _ptr(position_out),
+        out_seq, out_head, shape[2], _ints(n_keep, B, "n_keep"), first, _ints(since, B, "since"),
+        _ints(len_out, B, "len_out"), ws.data_ptr(), ws.numel(), flags, raw)
+    if status:
+        _check(status, "kv_evict")
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None, token=None,
