@@ -551,6 +551,17 @@ qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* 
                                 size_t ws_bytes, unsigned flags, void* stream);
 
 /*
+ * qlin_tree_attention, and the rows' softmax statistics beside it: stats, fp32
+ * [B * T, Hq, 2], contiguous, 8-byte aligned, gets each row's reference r and sum
+ * l: the weight of token j is 2^(scale log2(e) q . k_j - r) / l.  (-inf, 0): the
+ * row saw nothing.  r is near the row's largest score, not always equal to it.
+ * Rows not in use are left as they were.  Shares no memory with q and out.
+ */
+qlin_status qlin_tree_attention_stats(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, const void* q,
+                                      int64_t q_stride, float scale, void* out, int64_t out_stride, float* stats,
+                                      void* ws, size_t ws_bytes, unsigned flags, void* stream);
+
+/*
  * Test export for failure detection: qlin_tree_attention without flags, except
  * that the launch's first CTA never issues its `copy`-th copy of a tile (0: the
  * keys of its first tile, 1: their values, 2: the next tile's keys ...).  The
@@ -584,6 +595,55 @@ qlin_status qlin_debug_tree_attention_fault(const qlin_kv_cache* cache, const ql
 qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, const int32_t* keep,
                          int64_t keep_stride, const int32_t* n_keep, int32_t* len_out, void* ws, size_t ws_bytes,
                          unsigned flags, void* stream);
+
+#define QLIN_MAX_ROOM 1048576
+/*
+ * The attention weight that the cache's tokens got from a step's rows, added to
+ * what they got before: for cache head h and each committed token j
+ *   score_out[b][h][j] = decay * score[b][h][j] + sum of the weights of j
+ * over the kept rows and the query heads that read h.  The step's own tokens of
+ * kept rows get their weights alone, at the places len[b] + i that qlin_kv_keep
+ * gives them (call this before it), and position_out their positions there.
+ *   Hq, q, scale : as qlin_tree_attention was given them.
+ *   stats        : from qlin_tree_attention_stats.
+ *   keep, n_keep : as for qlin_kv_keep: the accepted path, of which each row sees
+ *                  those before it and itself.  Both NULL: the rows in use are
+ *                  all kept, and see one another as the step's mask says.  A bad
+ *                  list keeps nothing, and the status word gets QLIN_ERR_BAD_INDEX.
+ *   decay        : finite; 1: nothing fades.
+ *   score, score_out, position_out, the strides, room : as for qlin_kv_evict
+ *                  (score_out may be score); position_out may be NULL.  What would
+ *                  lie at room or behind is left out and reported.
+ *   at           : int32 [B * T]: the rows' positions, as given to
+ *                  qlin_kv_append_at; NULL: len + depth.
+ *   T            : 1..32 rows per sequence, T * Hq / heads <= 128.
+ *   ws           : a workspace (256 bytes) for the status word, or NULL.
+ *   flags        : 0 or QLIN_FLAG_PDL.
+ * Scores and sums are fp32.  A key that is not finite makes its own token's score
+ * not finite and no other's.  Places of tokens that are not there, and whole
+ * sequences with len[b] < 0, are left as they were.  Where scores pass 2^23 (log2
+ * units), and fp32 holds them a unit or more apart, a weight is no more than 1.
+ */
+qlin_status qlin_kv_weigh(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, const void* q, int64_t q_stride,
+                          const float* stats, float scale, const int32_t* keep, int64_t keep_stride,
+                          const int32_t* n_keep, float decay, const float* score, int64_t seq_stride,
+                          int64_t head_stride, float* score_out, int32_t* position_out, int64_t out_seq_stride,
+                          int64_t out_head_stride, int64_t room, const int32_t* at, void* ws, size_t ws_bytes,
+                          unsigned flags, void* stream);
+
+/*
+ * Test export for failure detection: qlin_kv_weigh of all rows in place or with
+ * the strides of score, except that the launch's first CTA never issues its
+ * `copy`-th copy of a panel of keys.  The bounded waits on it expire after about
+ * a second; the kernel writes QLIN_ERR_DEVICE_TIMEOUT into the status word, waits
+ * (bounded) for the copies and products that it did issue, frees its tensor memory
+ * and returns.  score_out is unspecified afterwards.  Nothing faults.  bf16 caches
+ * of width 128 only (else QLIN_ERR_UNSUPPORTED).
+ */
+qlin_status qlin_debug_kv_weigh_fault(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, const void* q,
+                                      int64_t q_stride, const float* stats, float scale, const float* score,
+                                      int64_t seq_stride, int64_t head_stride, float* score_out, int64_t room, void* ws,
+                                      size_t ws_bytes, int64_t copy, void* stream);
 
 /*
  * Eviction by accumulated weight (qlin_kv_weigh): of each sequence's committed
@@ -620,7 +680,6 @@ qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, c
  * tokens must not lie on one page: the rows of one would move under the other.
  * Scores and positions behind the tokens left are not written.
  */
-#define QLIN_MAX_ROOM 1048576
 qlin_status qlin_kv_evict_workspace_bytes(const qlin_kv_cache* cache, int B, int64_t room, size_t* bytes);
 qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const qlin_kv_step* step, const float* score,
                           const int32_t* position, int64_t seq_stride, int64_t head_stride, float* score_out,

@@ -128,3 +128,47 @@ def test_evict_refuses_what_others_do_and_limits(L):
     assert n.value >= 256 + 8 * 8 + 8 * 2 * 32 * 4
     assert L.qlin_kv_evict_workspace_bytes(ctypes.addressof(c), -1, 64, ctypes.byref(n)) == qlin.ERR_INVALID_ARG
     assert L.qlin_kv_evict_workspace_bytes(ctypes.addressof(c), 2, 64, None) == qlin.ERR_INVALID_ARG
+
+
+def weigh(so, /, c=None, s=None, **kw):
+    a = dict(Hq=8, q=4096, qs=1024, stats=4096, scale=0.1, keep=None, ks=0, n_keep=None, decay=1.0, score=1 << 20, ss=256, hs=64,
+             score_out=1 << 20, position_out=None, oss=256, ohs=64, room=64, at=None, ws=None, wsb=0, flags=0)
+    a.update(kw)
+    c, s = c or cache(), s or step()
+    return so.qlin_kv_weigh(ctypes.addressof(c), ctypes.addressof(s), *[a[n] for n in (
+        "Hq", "q", "qs", "stats", "scale", "keep", "ks", "n_keep", "decay", "score", "ss", "hs", "score_out", "position_out", "oss",
+        "ohs", "room", "at", "ws", "wsb", "flags")], None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(Hq=0), dict(Hq=6), dict(q=None), dict(q=4104), dict(qs=1023), dict(stats=None), dict(stats=4100), dict(scale=float("inf")),
+    dict(decay=float("nan")), dict(keep=4096, ks=3), dict(n_keep=4096), dict(keep=4096, n_keep=4096, ks=2), dict(keep=4097, n_keep=4096, ks=3),
+    dict(score=None), dict(score_out=None), dict(score=4098), dict(room=-1), dict(hs=63), dict(oss=64), dict(score_out=(1 << 20) + 8),
+    dict(oss=512), dict(position_out=1 << 20), dict(at=4098), dict(ws=4096 + 8, wsb=256), dict(flags=4)])
+def test_weigh_refusals(L, bad):
+    assert weigh(L, **bad) == qlin.ERR_INVALID_ARG
+
+
+def test_weigh_refuses_what_others_do_and_limits(L):
+    for kw, status in BAD_CACHE:
+        assert weigh(L, c=cache(**kw)) == status
+    for kw, status in BAD_STEP:
+        assert weigh(L, s=step(**kw)) == status
+    assert weigh(L, s=step(T=33)) == qlin.ERR_UNSUPPORTED
+    assert weigh(L, Hq=4 * 43, qs=4 * 43 * 128) == qlin.ERR_UNSUPPORTED
+    assert weigh(L, room=1 << 21) == qlin.ERR_UNSUPPORTED
+    assert weigh(L, ws=4096, wsb=255) == qlin.ERR_WORKSPACE
+    assert weigh(L, s=step(B=0), q=None, stats=None, score=None) == qlin.OK
+    c, s = cache(), step()
+    fault = lambda c, copy: L.qlin_debug_kv_weigh_fault(  # noqa: E731
+        ctypes.addressof(c), ctypes.addressof(s), 8, 4096, 1024, 4096, 0.1, 1 << 20, 256, 64, 1 << 20, 64, None, 0, copy, None)
+    assert fault(c, -1) == qlin.ERR_INVALID_ARG and fault(cache(dtype=1), 0) == qlin.ERR_UNSUPPORTED
+
+
+def test_attention_statistics_refusals(L):
+    c, s = cache(), step()
+    call = lambda stats, q=1 << 24, s=s: L.qlin_tree_attention_stats(  # noqa: E731
+        ctypes.addressof(c), ctypes.addressof(s), 8, q, 1024, 0.1, 1 << 28, 1024, stats, 1 << 32, 1 << 30, 0, None)
+    for bad in (None, 4100, 1 << 24, (1 << 28) + 64):
+        assert call(bad) == qlin.ERR_INVALID_ARG
+    assert call(None, s=step(T=0)) == qlin.OK

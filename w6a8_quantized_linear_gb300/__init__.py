@@ -15,6 +15,6 @@ from .qlin import (  # noqa: F401
     packed_bytes, read_device_status, repack, repack_workspace_bytes, workspace_init,
 )
 from .qlin import (  # noqa: F401
-    KVCache, KVStep, adjust_logits, kv_append, kv_evict, kv_evict_workspace_bytes, kv_keep, rope_axes, rope_turns, sample,
-    tree_attention, tree_attention_workspace_bytes,
+    KVCache, KVStep, adjust_logits, kv_append, kv_evict, kv_evict_workspace_bytes, kv_keep, kv_weigh, rope_axes,
+    rope_turns, sample, tree_attention, tree_attention_workspace_bytes,
 )

@@ -8,15 +8,12 @@
 // rows (at most 32 keys, under the tree's mask, on the CUDA cores, each row
 // reading only the keys that it sees) and normalises; it computes the scores
 // of those while the first still runs.
-#include <cuda.h>
-
 #include <cmath>
 #include <mutex>
 #include <type_traits>
 #include <utility>
 
-#include "qlin_ptx.cuh"
-#include "qlin_step.h"
+#include "qlin_tiles.cuh"
 
 namespace qlin {
 namespace {
@@ -61,200 +58,21 @@ struct AttentionParams {
   int box;           // tokens per TMA copy: a page or a tile, whichever is smaller
   int page_shift;    // log2 of the page size
   int64_t fault_copy;  // test only (FAULT): the copy that the first CTA never issues
+  float* stats;      // the rows' references and sums of weights, or none
+
+  __device__ __forceinline__ int64_t tokens(int b) const {  // the committed ones that are there
+    const int64_t len = step.len[b];
+    if (len <= 0 || step_rows(step, b) == 0) return 0;
+    const int64_t most = (int64_t)step.max_pages * cache.page_size;
+    return len < most ? len : most;
+  }
 };
 
-__device__ __forceinline__ int64_t committed(const AttentionParams& p, int b) {  // tokens that are there
-  const int64_t len = p.step.len[b];
-  if (len <= 0 || step_rows(p.step, b) == 0) return 0;
-  const int64_t most = (int64_t)p.step.max_pages * p.cache.page_size;
-  return len < most ? len : most;
-}
-template <int D>
-__device__ __forceinline__ int64_t tokens_to_tiles(int64_t n) { return (n + tile_tokens(D) - 1) / tile_tokens(D); }
-template <int D>
-__device__ __forceinline__ int64_t tiles_of(const AttentionParams& p, int b) {
-  return tokens_to_tiles<D>(committed(p, b));
-}
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-// Work is measured in tiles, and GAP more between two items: what a CTA loses
-// when its run goes on with another item (the sums' way out of tensor memory,
-// other query rows, the pipeline filled again: 5 to 7 us against 1.5 us for a
-// tile; with 1, 2, 3, 4 and 6, five items of 275 tiles took 31.1, 29.9, 28.9,
-// 29.5 and 29.2 us, 152 of 4 to 14 tiles 33.5, 32.0, 30.8, 31.5 and 32.2).  An
-// item's n tiles are [start, start + n), and the gap follows.
+// Work of a change to another item: 5 to 7 us (the sums' way out of tensor memory,
+// other query rows, the pipeline filled again) against 1.5 us for a tile; with 1,
+// 2, 3, 4 and 6, five items of 275 tiles took 31.1, 29.9, 28.9, 29.5 and 29.2 us,
+// 152 of 4 to 14 tiles 33.5, 32.0, 30.8, 31.5 and 32.2.
 constexpr int GAP = 3;
-template <int D>
-__device__ __forceinline__ int64_t work_of(const AttentionParams& p, int64_t tiles) {  // a sequence's
-  return tiles ? (tiles + GAP) * p.cache.heads : 0;
-}
-// Work of the sequences before b, and of all; a whole warp.
-template <int D>
-__device__ __forceinline__ void work_before(const AttentionParams& p, int b, int64_t* before, int64_t* all) {
-  const int lane = threadIdx.x & 31;
-  int64_t x = 0, y = 0;
-  for (int i = lane; i < p.step.B; i += 32) {
-    const int64_t n = work_of<D>(p, tiles_of<D>(p, i));
-    y += n;
-    if (i < b) x += n;
-  }
-  *before = warp_sum64(x);
-  *all = warp_sum64(y);
-}
-
-// A CTA's run, item by item.
-struct Walk {
-  int64_t left;    // work of the run still ahead, this item's included
-  int64_t tile;    // first tile of this item's part
-  int64_t n;       // tiles of this part
-  int64_t tokens;  // committed tokens of the sequence
-  int b, h;
-};
-template <int D>
-__device__ __forceinline__ void enter(const AttentionParams& p, Walk& w) {  // the part of the item that w names
-  const int64_t n = tokens_to_tiles<D>(w.tokens) - w.tile;
-  w.n = n < w.left ? n : w.left;
-}
-template <int D>
-__device__ __forceinline__ bool next_item(const AttentionParams& p, Walk& w) {
-  w.left -= w.n + GAP;
-  if (w.left <= 0) return false;
-  w.tile = 0;
-  if (++w.h == p.cache.heads) {
-    w.h = 0;
-    do {
-      if (++w.b >= p.step.B) return false;  // the run ends in the gap behind the last item
-      w.tokens = committed(p, w.b);
-    } while (w.tokens == 0);
-  }
-  enter<D>(p, w);
-  return true;
-}
-// Runs that work N is cut into: each at least one long, so that the CTAs
-// between an item's first and last have all left a partial result of it.
-__device__ __forceinline__ int runs_of(const AttentionParams& p, int64_t N) { return N < p.ctas ? (int)N : p.ctas; }
-// Where run c begins, floor(N c / runs), in 32 bits where they suffice.
-__device__ __forceinline__ int64_t run_start(int64_t N, int c, int runs) {
-  const int64_t x = N * c;
-  return x >> 32 ? x / runs : (int64_t)((uint32_t)x / (uint32_t)runs);
-}
-// Where CTA c's run begins; a whole warp.  Up to 32 sequences' lengths are
-// read once, in one trip.
-template <int D>
-__device__ __forceinline__ Walk first_item(const AttentionParams& p, int c) {
-  const int lane = threadIdx.x & 31;
-  int64_t tokens = lane < p.step.B ? committed(p, lane) : 0, all = work_of<D>(p, tokens_to_tiles<D>(tokens));
-  for (int i = lane + 32; i < p.step.B; i += 32) all += work_of<D>(p, tiles_of<D>(p, i));
-  const int64_t N = warp_sum64(all);
-  const int runs = runs_of(p, N);
-  Walk w = {0, 0, 0, 0, 0, 0};
-  if (c >= runs) return w;
-  const int64_t x0 = run_start(N, c, runs);
-  w.left = run_start(N, c + 1, runs) - x0;
-  int64_t run = 0;
-  for (int i0 = 0; i0 < p.step.B; i0 += 32) {
-    if (i0) tokens = i0 + lane < p.step.B ? committed(p, i0 + lane) : 0;
-    const int64_t n = work_of<D>(p, tokens_to_tiles<D>(tokens));
-    int64_t inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t a = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= o) inc += a;
-    }
-    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, x0 < run + inc);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      const int64_t start = __shfl_sync(0xFFFFFFFFu, run + inc - n, l);
-      w.tokens = __shfl_sync(0xFFFFFFFFu, tokens, l);
-      const int64_t tiles = tokens_to_tiles<D>(w.tokens), per = tiles + GAP;
-      w.b = i0 + l;
-      w.h = (int)run_start(x0 - start, 1, (int)per);  // tiles of one head: below 2^31
-      w.tile = x0 - start - w.h * per;
-      if (w.tile < tiles) {
-        enter<D>(p, w);
-      } else {  // in a gap: on with the item behind it
-        w.left += w.tile - tiles;
-        w.n = 0;
-        if (!next_item<D>(p, w)) w.left = 0;
-      }
-      return w;
-    }
-    run += __shfl_sync(0xFFFFFFFFu, inc, 31);
-  }
-  w.left = 0;
-  return w;
-}
-// The CTA whose run holds place x of N: floor(c N / runs) <= x < floor((c + 1) N / runs)
-__device__ __forceinline__ int cta_of(int64_t x, int64_t N, int runs) {
-  const int64_t y = (x + 1) * runs - 1;
-  return (y | N) >> 32 ? (int)(y / N) : (int)((uint32_t)y / (uint32_t)N);
-}
-
-// ---- PTX -------------------------------------------------------------------------
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int token, int head, int page,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-          "r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-// One lane of the warp, the same at every call.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
-}
-// Matrix descriptor of a 128-byte-swizzled operand: rows of 64 16-bit values
-// (128 bytes, on a 1024-byte boundary every eighth), `lbo` bytes between its
-// 64-wide panels where the panels run along M or N, 1024 between groups of
-// eight rows.
-__device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr, uint32_t lbo) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // below 2^-126: 0
-  return y;
-}
 
 // A barrier of the four softmax warps that tells all of them whether all are
 // still at work (every wait before it is bounded, so all four reach it).
@@ -356,7 +174,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
   pdl_wait();
   pdl_launch_dependents();
   if (warp == PRODUCER) {
-    const Walk w = first_item<D>(p, blockIdx.x);
+    const Walk w = first_item<TK, GAP>(p, blockIdx.x);
     if (lane == 0) s->walk = w;
   }
   tc_fence_before();
@@ -399,7 +217,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
                           (int)(token & (p.cache.page_size - 1)), w.h, page, &s->full[slot]);
           }
         }
-      } while (ok && next_item<D>(p, w));
+      } while (ok && next_item<TK, GAP>(p, w));
       // nothing leaves while its copies are in flight, whichever role gave up
       // (this one may have issued its last copy long before); where none did,
       // they are all waited for elsewhere too
@@ -468,7 +286,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
         }
         n += tiles;
         seg++;
-      } while (ok && next_item<D>(p, w));
+      } while (ok && next_item<TK, GAP>(p, w));
       if (!ok && elect_one()) {  // the products in flight end before tensor memory is freed
         mma_commit(&s->drained);
         (void)mbar_wait(&s->drained, 0);
@@ -496,7 +314,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
           __syncwarp();
           if (lane == 0) mbar_arrive(&s->v_clean);
         }
-      } while (next_item<D>(p, w));
+      } while (next_item<TK, GAP>(p, w));
     } else {
       // ---- softmax: a thread per query row
       const int at = threadIdx.x, row = at % LANES, copy = at / LANES;  // `at`: the lane of tensor memory
@@ -733,7 +551,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
         }
         n += (uint32_t)w.n;
         seg++;
-      } while (next_item<D>(p, w));
+      } while (next_item<TK, GAP>(p, w));
     }
   }
   __syncwarp();
@@ -757,7 +575,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(co
   __shared__ int64_t place[QLIN_MAX_TREE];
   __shared__ __align__(16) float sums[JOIN_GROUPS][JOIN_COLS][8];
   __shared__ int64_t range[2];
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, TILE = tile_tokens(D);
   const int item = blockIdx.x, b = item / p.cache.heads, h = item % p.cache.heads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r0 = blockIdx.y * 8, row = r0 + warp, t = row / p.group;
@@ -765,7 +583,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(co
   const bool live = len >= 0 && warp < 8 && row < p.R && t < rows;  // a warp per row for its weights
   if (warp == 8) {
     int64_t before, all;
-    work_before<D>(p, b, &before, &all);
+    work_before<TILE, GAP>(p, b, &before, &all);
     if (lane == 0) range[0] = before, range[1] = all;
   }
   if (len >= 0 && warp == 0) {
@@ -800,7 +618,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(co
     }
   }
   // this item's tiles among all, and the CTAs whose runs hold them
-  const int64_t per = tiles_of<D>(p, b), N = range[1];
+  const int64_t per = tokens_to_tiles<TILE>(p.tokens(b)), N = range[1];
   const int64_t start = range[0] + h * (per + GAP);
   const int runs = runs_of(p, N);
   const int first = per ? cta_of(start, N, runs) : 0;
@@ -860,6 +678,9 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) qlin_attention_join_kernel(co
     }
 #pragma unroll
     for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, i);
+    if (p.stats && blockIdx.z == 0 && lane == 0)
+      reinterpret_cast<float2*>(p.stats)[((int64_t)b * p.step.T + t) * ((int64_t)p.group * p.cache.heads) +
+                                         (int64_t)h * p.group + row % p.group] = make_float2(m, l);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     own[lane][warp] = w * inv;
 #pragma unroll
@@ -942,18 +763,12 @@ constexpr size_t attention_smem(int width) {  // query rows, ring, and the way t
   return (size_t)q_bytes(width) + (size_t)ring_buffers(width) * tile_bytes(width) + 1024;
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 struct AttentionDevice {
   std::once_flag once;
   qlin_status ready = QLIN_ERR_CUDA;
   int ctas = 0;
 };
 AttentionDevice g_attention[64];
-EncodeTiled g_encode = nullptr;
-std::once_flag g_encode_once;
 
 // SM count, kernel attributes and the driver's encoder, once per device.
 qlin_status attention_setup(int* ctas) {
@@ -962,14 +777,6 @@ qlin_status attention_setup(int* ctas) {
   if (e != cudaSuccess) return status_of(e);
   if (dev < 0 || dev >= 64) return QLIN_ERR_CUDA;
   AttentionDevice& d = g_attention[dev];
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) ==
-            cudaSuccess &&
-        found == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<EncodeTiled>(fn);
-  });
   std::call_once(d.once, [&d, dev] {
     int sms = 0;
     cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -984,24 +791,11 @@ qlin_status attention_setup(int* ctas) {
         for (const void* fn : attention_kernels(dtype, width).main) prepare(fn, width);
     prepare(attention_fault_kernel(), 128);
     d.ctas = sms < ATT_MAX_CTAS ? sms : ATT_MAX_CTAS;
-    d.ready = e == cudaSuccess && g_encode && sms > 0 ? QLIN_OK : QLIN_ERR_CUDA;
+    d.ready = e == cudaSuccess && encode_tiled() && sms > 0 ? QLIN_OK : QLIN_ERR_CUDA;
     if (e != cudaSuccess) (void)cudaGetLastError();
   });
   *ctas = d.ctas;
   return d.ready;
-}
-
-// [pages, heads, page_size, width] as boxes of 64 elements x `box` tokens,
-// 128-byte swizzled
-bool encode(CUtensorMap* map, const qlin_kv_cache* c, void* base, int box) {
-  const cuuint64_t dims[4] = {(cuuint64_t)c->width, (cuuint64_t)c->page_size, (cuuint64_t)c->heads,
-                              (cuuint64_t)c->pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)c->token_stride * 2, (cuuint64_t)c->head_stride * 2,
-                                 (cuuint64_t)c->page_stride * 2};
-  const cuuint32_t shape[4] = {64, (cuuint32_t)box, 1, 1}, one[4] = {1, 1, 1, 1};
-  return g_encode(map, c->dtype == QLIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                  base, dims, strides, shape, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The query rows [B * T, Hq, width] as boxes of 64 elements x group x T: an
@@ -1010,7 +804,7 @@ bool encode_q(CUtensorMap* map, const qlin_kv_cache* c, const qlin_kv_step* s, c
   const cuuint64_t dims[3] = {(cuuint64_t)c->width, (cuuint64_t)Hq, (cuuint64_t)((int64_t)s->B * s->T)};
   const cuuint64_t strides[2] = {(cuuint64_t)c->width * 2, (cuuint64_t)stride * 2};
   const cuuint32_t shape[3] = {64, (cuuint32_t)(Hq / c->heads), (cuuint32_t)s->T}, one[3] = {1, 1, 1};
-  return g_encode(map, c->dtype == QLIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+  return encode_tiled()(map, c->dtype == QLIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                   const_cast<void*>(q), dims, strides, shape, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1045,7 +839,7 @@ qlin_status qlin_tree_attention_workspace_bytes(const qlin_kv_cache* cache, int 
 
 static qlin_status attend(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, const void* q, int64_t q_stride,
                           float scale, void* out, int64_t out_stride, void* ws, size_t ws_bytes, unsigned flags,
-                          void* stream, int64_t fault_copy = -1) {
+                          void* stream, float* stats, int64_t fault_copy = -1) {
   qlin_status st = check_cache(cache);
   if (st != QLIN_OK) return st;
   st = check_step(step, QLIN_MAX_TREE);
@@ -1063,13 +857,19 @@ static qlin_status attend(const qlin_kv_cache* cache, const qlin_kv_step* step, 
   // the second launch writes some columns of a row while others read its q
   if (rows_overlap(out, out_stride * 2, Hq * D * 2, q, q_stride * 2, Hq * D * 2, (int64_t)step->B * step->T))
     return QLIN_ERR_INVALID_ARG;
+  if (stats) {  // written where other blocks still read q
+    const int64_t n = (int64_t)step->B * step->T;
+    if (!is_aligned(stats, 8) || rows_overlap(stats, Hq * 8, Hq * 8, q, q_stride * 2, Hq * D * 2, n) ||
+        rows_overlap(stats, Hq * 8, Hq * 8, out, out_stride * 2, Hq * D * 2, n))
+      return QLIN_ERR_INVALID_ARG;
+  }
   int ctas = 0;
   st = attention_setup(&ctas);
   if (st != QLIN_OK) return st;
   AttentionParams p;
   const int tile = tile_tokens(cache->width);
   p.box = cache->page_size < tile ? cache->page_size : tile;
-  if (!encode(&p.map_k, cache, cache->k, p.box) || !encode(&p.map_v, cache, cache->v, p.box) ||
+  if (!encode(encode_tiled(), &p.map_k, cache, cache->k, p.box) || !encode(encode_tiled(), &p.map_v, cache, cache->v, p.box) ||
       !encode_q(&p.map_q, cache, step, q, q_stride, Hq))
     return QLIN_ERR_CUDA;
   p.page_shift = 0;
@@ -1087,6 +887,7 @@ static qlin_status attend(const qlin_kv_cache* cache, const qlin_kv_step* step, 
   p.Rp = padded_rows(step->T, p.group);
   p.ctas = ctas;
   p.fault_copy = fault_copy;
+  p.stats = stats;
   void* args[] = {&p};
   const Kernels fn = attention_kernels(cache->dtype, cache->width);
   const int copies = p.R > ATT_ROWS / 2 ? 0 : p.R > ATT_ROWS / 4 ? 1 : 2;
@@ -1106,7 +907,14 @@ static qlin_status attend(const qlin_kv_cache* cache, const qlin_kv_step* step, 
 qlin_status qlin_tree_attention(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, const void* q,
                                 int64_t q_stride, float scale, void* out, int64_t out_stride, void* ws,
                                 size_t ws_bytes, unsigned flags, void* stream) {
-  return attend(cache, step, Hq, q, q_stride, scale, out, out_stride, ws, ws_bytes, flags, stream);
+  return attend(cache, step, Hq, q, q_stride, scale, out, out_stride, ws, ws_bytes, flags, stream, nullptr);
+}
+
+qlin_status qlin_tree_attention_stats(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, const void* q,
+                                      int64_t q_stride, float scale, void* out, int64_t out_stride, float* stats,
+                                      void* ws, size_t ws_bytes, unsigned flags, void* stream) {
+  if (!stats && (!step || (step->B != 0 && step->T != 0))) return QLIN_ERR_INVALID_ARG;
+  return attend(cache, step, Hq, q, q_stride, scale, out, out_stride, ws, ws_bytes, flags, stream, stats);
 }
 
 qlin_status qlin_debug_tree_attention_fault(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq,
@@ -1118,7 +926,7 @@ qlin_status qlin_debug_tree_attention_fault(const qlin_kv_cache* cache, const ql
   if (copy < 0 || !step || step->T < 0 || Hq < 1) return QLIN_ERR_INVALID_ARG;
   if (cache->dtype != QLIN_BF16 || cache->width != 128 || (int64_t)step->T * (Hq / cache->heads) > ATT_ROWS / 4)
     return QLIN_ERR_UNSUPPORTED;
-  return attend(cache, step, Hq, q, q_stride, scale, out, out_stride, ws, ws_bytes, 0, stream, copy);
+  return attend(cache, step, Hq, q, q_stride, scale, out, out_stride, ws, ws_bytes, 0, stream, nullptr, copy);
 }
 
 }  // extern "C"

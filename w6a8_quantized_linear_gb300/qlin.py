@@ -85,6 +85,12 @@ def lib() -> ctypes.CDLL:
                 "qlin_tree_attention_workspace_bytes": (st, [vp, i32, i32, i32, ctypes.POINTER(sz)]),
                 "qlin_tree_attention": (st, [vp, vp, i32, vp, i64, ctypes.c_float, vp, i64, vp, sz, ctypes.c_uint,
                                              vp]),
+                "qlin_tree_attention_stats": (st, [vp, vp, i32, vp, i64, ctypes.c_float, vp, i64, vp, vp, sz, ctypes.c_uint,
+                                                   vp]),
+                "qlin_kv_weigh": (st, [vp, vp, i32, vp, i64, vp, ctypes.c_float, vp, i64, vp, ctypes.c_float, vp, i64, i64,
+                                       vp, vp, i64, i64, i64, vp, vp, sz, ctypes.c_uint, vp]),
+                "qlin_debug_kv_weigh_fault": (st, [vp, vp, i32, vp, i64, vp, ctypes.c_float, vp, i64, i64, vp, i64, vp, sz,
+                                                   i64, vp]),
                 "qlin_debug_tree_attention_fault": (st, [vp, vp, i32, vp, i64, ctypes.c_float, vp, i64, vp, sz, i64, vp]),
                 "qlin_kv_keep": (st, [vp, vp, vp, i64, vp, vp, vp, sz, ctypes.c_uint, vp]),
                 "qlin_kv_evict_workspace_bytes": (st, [vp, i32, i64, ctypes.POINTER(sz)]),
@@ -626,15 +632,17 @@ def tree_attention_workspace_bytes(cache: KVCache, B: int, T: int, Hq: int) -> i
 
 
 def tree_attention(cache: KVCache, step: KVStep, q: torch.Tensor, scale: float | None = None, out=None, ws=None,
-                   flags: int = 0, stream=None) -> torch.Tensor:
+                   flags: int = 0, stream=None, stats=None) -> torch.Tensor:
     """Attention of a step's rows (q of ``kv_append``, [B * T, Hq * width]) over the
     cache: every row sees the committed tokens of its sequence and the step's
     rows that its mask names.  Returns bf16 [B * T, Hq * width].  ``scale``:
     width ** -0.5 unless given.  Without ``ws`` the call takes memory of its own,
     and what its status word gets (``ERR_BAD_INDEX``, ``ERR_DEVICE_TIMEOUT``) is
-    lost with it: a caller that reads ``read_device_status`` gives one."""
+    lost with it: a caller that reads ``read_device_status`` gives one.  ``stats``
+    (fp32 [B * T, Hq, 2], optional) gets the rows' softmax references (log2 units)
+    and sums, for ``kv_weigh``."""
     n, D, dev = step.B * step.T, cache.width, cache._index
-    _same_device(dev, step.len, q, out, ws)
+    _same_device(dev, step.len, q, out, ws, stats)
     Hq = _heads(q, D, "q")
     qs = _rows(q, n, Hq * D, cache.dtype, "q")
     if out is None:
@@ -644,9 +652,21 @@ def tree_attention(cache: KVCache, step: KVStep, q: torch.Tensor, scale: float |
     if ws is None:
         ws = _empty(tree_attention_workspace_bytes(cache, step.B, step.T, Hq), torch.uint8, cache.device, stream)
         workspace_init(ws, raw)
-    _check(_fn("qlin_tree_attention")(cache._ref, step._ref, Hq, q.data_ptr(), qs, D ** -0.5 if scale is None else scale,
-                                      out.data_ptr(), os_, ws.data_ptr(), ws.numel(), flags, raw), "tree_attention")
+    head = (cache._ref, step._ref, Hq, q.data_ptr(), qs, D ** -0.5 if scale is None else scale, out.data_ptr(), os_)
+    tail = (ws.data_ptr(), ws.numel(), flags, raw)
+    if stats is None:
+        status = _fn("qlin_tree_attention")(*head, *tail)
+    else:
+        status = _fn("qlin_tree_attention_stats")(*head, _stats(stats, n, Hq), *tail)
+    if status:
+        _check(status, "tree_attention")
     return out
+
+
+def _stats(t, n: int, Hq: int) -> int:
+    if t.dtype is not _F32 or t.shape != (n, Hq, 2) or not t.is_contiguous():
+        raise ValueError(f"stats must be a contiguous float32 tensor of [{n}, {Hq}, 2]")
+    return t.data_ptr()
 
 
 def debug_tree_attention_fault(cache: KVCache, step: KVStep, q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
@@ -689,6 +709,57 @@ def _score_pair(score, position, shape, what: str) -> tuple[int, int]:
     if position is not None and _scores(position, shape, _I32, "position" + what[5:]) != strides:
         raise ValueError(f"position{what[5:]} must have the strides of {what}")
     return strides
+
+
+def kv_weigh(cache: KVCache, step: KVStep, q: torch.Tensor, stats: torch.Tensor, score: torch.Tensor, keep=None,
+             n_keep=None, decay: float = 1.0, scale: float | None = None, score_out=None, position_out=None, at=None, ws=None,
+             flags: int = 0, stream=None) -> torch.Tensor:
+    """Add to ``score`` (fp32 [B, heads, room]) the attention weight that each token
+    of the cache got from a step's rows (``q`` and ``stats`` as ``tree_attention``
+    took and gave them): decay * score + the weights of the kept rows.  ``keep``,
+    ``n_keep`` as in ``kv_keep`` (call this before it): the accepted path; without
+    them all rows are kept.  The kept rows' own tokens get theirs at the places
+    that ``kv_keep`` gives them, and ``position_out`` (int32, like score, optional)
+    their positions: ``at`` (int32 [B * T]), or len + depth.  Returns ``score_out``
+    (in place unless given)."""
+    n, D, dev = step.B * step.T, cache.width, cache._index
+    _same_device(dev, step.len, q, stats, score, keep, n_keep, score_out, position_out, at, ws)
+    Hq = _heads(q, D, "q")
+    qs = _rows(q, n, Hq * D, cache.dtype, "q")
+    B, T = step.B, step.T
+    ks = 0
+    if keep is not None:
+        if keep.shape != (B, T) or keep.dtype is not _I32 or (T > 1 and keep.stride(1) != 1):
+            raise ValueError("keep must be an int32 [B, T] tensor with contiguous rows")
+        ks = keep.stride(0) if B > 1 else T
+    if score.dim() != 3:
+        raise ValueError("score must be [B, heads, room]")
+    shape = (B, cache.heads, score.shape[2])
+    seq, head = _scores(score, shape, _F32, "score")
+    if score_out is None:
+        score_out = score
+    out_seq, out_head = _score_pair(score_out, position_out, shape, "score_out")
+    status = _fn("qlin_kv_weigh")(
+        cache._ref, step._ref, Hq, q.data_ptr(), qs, _stats(stats, n, Hq), D ** -0.5 if scale is None else scale, _ptr(keep),
+        ks, _ints(n_keep, B, "n_keep"), decay, score.data_ptr(), seq, head, score_out.data_ptr(), _ptr(position_out), out_seq,
+        out_head, shape[2], _ints(at, n, "at"), _ptr(ws), 0 if ws is None else ws.numel(), flags,
+        _current_stream(dev) if stream is None else _raw_stream(stream, dev))
+    if status:
+        _check(status, "kv_weigh")
+    return score_out
+
+
+def debug_kv_weigh_fault(cache: KVCache, step: KVStep, q: torch.Tensor, stats: torch.Tensor, score: torch.Tensor,
+                         ws: torch.Tensor, copy: int, stream=None) -> int:
+    """Test export: ``kv_weigh`` of all rows in place whose first CTA never issues its ``copy``-th copy of a panel of
+    keys; returns the launch status (the device status word is read separately)."""
+    n, D, dev = step.B * step.T, cache.width, cache._index
+    _same_device(dev, step.len, q, stats, score, ws)
+    Hq = _heads(q, D, "q")
+    seq, head = _scores(score, (step.B, cache.heads, score.shape[2]), _F32, "score")
+    return _fn("qlin_debug_kv_weigh_fault")(
+        cache._ref, step._ref, Hq, q.data_ptr(), _rows(q, n, Hq * D, cache.dtype, "q"), _stats(stats, n, Hq), D ** -0.5,
+        score.data_ptr(), seq, head, score.data_ptr(), score.shape[2], ws.data_ptr(), ws.numel(), copy, _raw_stream(stream, dev))
 
 
 def kv_evict_workspace_bytes(cache: KVCache, step: KVStep, room: int) -> int:
