@@ -122,6 +122,8 @@ CASES = [
     (5, 3, 50257, 9000, BF, 20, 0.001, True, 7, False),
     (1, 1, 524288, 60000, BF, 0, 0.5, False, 0, False),
     (7, 1, 70001, 1, F32, 0, 0.0, False, 1, False),
+    (2, 70, 999, 50, F32, 4, 0.5, False, 1, False),
+    (70, 1, 20000, 9999, BF, 3, None, True, 0, False),
 ]
 
 

@@ -18,8 +18,9 @@ namespace {
 constexpr int SELECT_THREADS = 512, SELECT_WARPS = SELECT_THREADS / 32;
 constexpr int BINS = 2048;            // of one pass over 11 bits of the keys
 constexpr int MAX_CLUSTER = 16;
-constexpr int MAX_STAGED = 40960;     // keys of a block in shared memory at most; those behind are formed again
-constexpr int MOVE_THREADS = 256;
+constexpr int MOVE_THREADS = 256, MOVE_WARPS = MOVE_THREADS / 32;
+constexpr int MOVE_ITEMS = 1024;      // items whose moves are shared out evenly among their blocks
+constexpr uint32_t ALL = 0xFFFFFFFFu;
 
 struct EvictParams {
   qlin_kv_cache cache;
@@ -36,8 +37,7 @@ struct EvictParams {
   int32_t* lists;  // per item: the emptied places, then the tokens that move there, `half` each
   int64_t half;
   int room, first;
-  int cluster, staged;
-  int blocks;  // of the second launch, per item
+  int cluster, items;
 };
 
 // Larger is kept: the scores' order, equal ones by index, NaN below all, what
@@ -64,50 +64,40 @@ __device__ __forceinline__ uint4 cluster_load4(uint32_t addr) {
 struct SelectShared {
   uint32_t hist[BINS];
   __align__(16) uint32_t total[3][BINS];  // the cluster's counts of this block's share of the bins
-  __align__(16) uint4 sums;               // kept for sure and equals, before and behind the border
-  uint4 all[MAX_CLUSTER];
-  uint64_t warp[SELECT_WARPS];
-  uint32_t bin, above, in_bin;
+  __align__(16) uint4 sums;               // above the border and equal to it, before place `stays`; the same behind it
+  uint4 cta[MAX_CLUSTER], warp[SELECT_WARPS];
+  uint32_t above[SELECT_WARPS];
+  uint32_t bin, over, in_bin;
 };
 
-// Exclusive sums over the block of two counts in one word; *all: the whole sum.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, SelectShared* s, uint64_t* all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t inc = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t a = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-    if (lane >= o) inc += a;
-  }
-  if (lane == 31) s->warp[warp] = inc;
-  __syncthreads();
-  uint64_t before = 0, sum = 0;
-#pragma unroll
-  for (int w = 0; w < SELECT_WARPS; w++) {
-    if (w < warp) before += s->warp[w];
-    sum += s->warp[w];
-  }
-  __syncthreads();
-  *all = sum;
-  return before + inc - v;
-}
-__device__ __forceinline__ uint64_t two(uint32_t a, uint32_t b) { return (uint64_t)b << 32 | a; }
+__device__ __forceinline__ uint32_t warp_sum(uint32_t v) { return __reduce_add_sync(ALL, v); }
 
-// One cluster per item, a run of places per block, its keys staged in shared
-// memory.  The border is found from the keys' upper bits down, 11 at a time: a
-// histogram per block, added into the bins' owners, and read by all.
+// Of a run of places in order, with `before` equals in front of it and the counts c
+// (above and equal before `stays`, the same behind): those that stay.
+__device__ __forceinline__ uint2 staying(uint4 c, uint32_t before, uint32_t ties) {
+  const uint32_t left = ties > before ? ties - before : 0, low = min(left, c.y);
+  return make_uint2(c.x + low, c.z + min(left - low, c.w));
+}
+
+// One cluster per item, a run of places per block, a run of those per warp: lane l
+// holds places 32 j + l of it, K of them in registers (K = 0: formed again each
+// time), so that ranks come from ballots.  The border is found from the keys' upper
+// bits down, 11 at a time: a histogram per block, added into the bins' owners,
+// and read by all; where a whole bin stays, what lies below need not be looked at.
+template <int K>
 __global__ void __launch_bounds__(SELECT_THREADS) qlin_evict_select_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ SelectShared sh;
   SelectShared* s = &sh;
-  const int C = p.cluster, tid = threadIdx.x;
+  const int C = p.cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = C > 1 ? (int)cluster_ctarank() : 0;
   const int item = blockIdx.x / C, b = item / p.cache.heads, h = item % p.cache.heads;
-  for (int i = tid; i < 3 * BINS; i += SELECT_THREADS) (&s->total[0][0])[i] = 0;
+  for (int i = tid; i < 3 * BINS / 4; i += SELECT_THREADS) reinterpret_cast<uint4*>(s->total)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < BINS / 4; i += SELECT_THREADS) reinterpret_cast<uint4*>(s->hist)[i] = make_uint4(0, 0, 0, 0);
   pdl_wait();
   pdl_launch_dependents();
   const int len = p.step.len[b];
   const int want = p.n_keep[b];
+  const int since = p.since ? p.since[b] : 0x7FFFFFFF;
   const bool lost = len > p.room || (int64_t)len > (int64_t)p.step.max_pages * p.cache.page_size;
   const int n = lost || len < 0 ? 0 : len;
   const int stays = want < 0 ? 0 : want < n ? want : n;
@@ -115,192 +105,301 @@ __global__ void __launch_bounds__(SELECT_THREADS) qlin_evict_select_kernel(const
     if (lost) report(p.status, QLIN_ERR_BAD_INDEX);
     p.chosen[item] = make_int2(0, lost ? len : len < 0 ? -1 : stays);
   }
-  const int per = (n + C - 1) / C, i0 = min(rank * per, n), count = min(per, n - i0);
-  const float* score = p.score + b * p.seq_stride + h * p.head_stride + i0;
-  const int32_t* position = p.position ? p.position + b * p.seq_stride + h * p.head_stride + i0 : nullptr;
+  const int per = ((n + C * SELECT_WARPS - 1) / (C * SELECT_WARPS) + 31) / 32 * 32;  // places of a warp
+  const int i0 = min((rank * SELECT_WARPS + warp) * per, n), end = min(i0 + per, n), rounds = (end - i0 + 31) / 32;
+  const float* score = p.score + b * p.seq_stride + h * p.head_stride;
+  const int32_t* position = p.position ? p.position + b * p.seq_stride + h * p.head_stride : nullptr;
   // what stays in place goes to the other arrays as it is; the emptied places are overwritten by the second launch
-  float* score_out = p.score_out + b * p.out_seq_stride + h * p.out_head_stride + i0;
-  int32_t* position_out = p.position_out ? p.position_out + b * p.out_seq_stride + h * p.out_head_stride + i0 : nullptr;
+  float* score_out = p.score_out + b * p.out_seq_stride + h * p.out_head_stride;
+  int32_t* position_out = p.position_out ? p.position_out + b * p.out_seq_stride + h * p.out_head_stride : nullptr;
   const bool copy_score = score_out != score, copy_position = position_out && position_out != position;
-  const int since = p.since ? p.since[b] : 0x7FFFFFFF;
   auto form = [&](float x, int at) { return key_of(x, at < p.first || (p.since && at >= since)); };
-#pragma unroll 4
-  for (int i = tid; i < count; i += SELECT_THREADS) {
-    const float x = score[i];
-    const int at = position ? position[i] : i0 + i;
-    if (i < p.staged) keys[i] = form(x, at);
-    if (i0 + i < stays) {
+
+  uint32_t keys[K ? K : 1];
+  auto take = [&](int i, float x, int at) {
+    if (i < min(end, stays)) {
       if (copy_score) score_out[i] = x;
       if (copy_position) position_out[i] = at;
     }
+    return form(x, at);
+  };
+  if constexpr (K > 0) {
+    float x[K];
+#pragma unroll
+    for (int j = 0; j < K; j++) {  // all on their way at once
+      const int i = i0 + 32 * j + lane;
+      x[j] = i < end ? score[i] : 0.f;
+      keys[j] = (uint32_t)(position && i < end ? position[i] : i);
+    }
+#pragma unroll
+    for (int j = 0; j < K; j++) keys[j] = take(i0 + 32 * j + lane, x[j], (int)keys[j]);
+  } else if (copy_score || copy_position) {
+#pragma unroll 4
+    for (int i = i0 + lane; i < end; i += 32) (void)take(i, score[i], position ? position[i] : i);
   }
   if (stays == n || stays == 0) return;  // nothing moves; the whole cluster leaves
-  auto key = [&](int i) { return i < p.staged ? keys[i] : form(score[i], position ? position[i] : i0 + i); };
-  if (C > 1) {
-    cluster_arrive();
-    cluster_wait();
-  }
+  // f(key, j) for the warp's keys, all lanes at once; a lane behind the end is not there
+  auto each = [&](auto&& f) {
+    if constexpr (K > 0) {
+#pragma unroll
+      for (int j = 0; j < K; j++)
+        if (j < rounds) f(keys[j], i0 + 32 * j + lane);
+    } else {
+#pragma unroll 4
+      for (int j = 0; j < rounds; j++) {
+        const int i = i0 + 32 * j + lane;
+        f(i < end ? form(score[i], position ? position[i] : i) : 0u, i);
+      }
+    }
+  };
+  if (C > 1) cluster_arrive();  // the totals are zero
+  __syncthreads();
 
-  // ---- the border: keys above `border` stay, and the first `ties` of its equals
+  // ---- the border: keys above it stay, and the first `ties` of its equals
   uint32_t prefix = 0, border = 0, ties = (uint32_t)stays;
   const int share = BINS / C;  // bins that a block owns
 #pragma unroll 1
   for (int pass = 0; pass < 3; pass++) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    for (int i = tid; i < BINS; i += SELECT_THREADS) s->hist[i] = 0;
-    __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < count; i += SELECT_THREADS) {
-      const uint32_t k = key(i);
-      if (pass == 0 || k >> (shift + bits) == prefix) atomicAdd(&s->hist[k >> shift & (BINS - 1) & ((1u << bits) - 1)], 1u);
-    }
-    __syncthreads();
-    const uint32_t total = smem_u32(s->total[pass]);
-    for (int i = tid; i < BINS; i += SELECT_THREADS)
-      if (s->hist[i]) {
-        const uint32_t at = total + (uint32_t)(i % share) * 4;
-        cluster_add(C > 1 ? dsmem_addr_u32(at, (uint32_t)(i / share)) : at, s->hist[i]);
-      }
-    if (C > 1) {
-      cluster_arrive();
-      cluster_wait();
-    } else {
+    if (pass) {
+      reinterpret_cast<uint4*>(s->hist)[tid] = make_uint4(0, 0, 0, 0);
       __syncthreads();
     }
+    each([&](uint32_t k, int i) {
+      if (i < end && (pass == 0 || k >> (shift + bits) == prefix)) atomicAdd(&s->hist[k >> shift & ((1u << bits) - 1)], 1u);
+    });
+    if (C > 1 && pass == 0) cluster_wait();
+    __syncthreads();
     // a thread's four bins, the highest bins first
     const int bin = BINS - 4 - 4 * tid;
-    const uint32_t at = total + (uint32_t)(bin % share) * 4;
-    const uint4 c = cluster_load4(C > 1 ? dsmem_addr_u32(at, (uint32_t)(bin / share)) : at);
-    uint64_t all;
-    uint32_t above = (uint32_t)block_scan(c.x + c.y + c.z + c.w, s, &all);
+    uint4 c = *reinterpret_cast<const uint4*>(&s->hist[bin]);
+    if (C > 1) {
+      const uint32_t at = dsmem_addr_u32(smem_u32(s->total[pass]) + (uint32_t)(bin % share) * 4, (uint32_t)(bin / share));
+      if (c.x) cluster_add(at, c.x);
+      if (c.y) cluster_add(at + 4, c.y);
+      if (c.z) cluster_add(at + 8, c.z);
+      if (c.w) cluster_add(at + 12, c.w);
+      cluster_arrive();
+      cluster_wait();
+      c = cluster_load4(at);
+    }
+    const uint32_t mine = c.x + c.y + c.z + c.w;
+    uint32_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t a = __shfl_up_sync(ALL, upto, o);
+      if (lane >= o) upto += a;
+    }
+    if (lane == 31) s->above[warp] = upto;
+    __syncthreads();
+    uint32_t above = upto - mine + warp_sum(lane < warp ? s->above[lane & 15] : 0);
     const uint32_t counts[4] = {c.w, c.z, c.y, c.x};
 #pragma unroll
     for (int e = 0; e < 4; e++) {
       if (above < ties && ties <= above + counts[e]) {
         s->bin = (uint32_t)(bin + 3 - e);
-        s->above = above;
+        s->over = above;
         s->in_bin = counts[e];
       }
       above += counts[e];
     }
     __syncthreads();
     prefix = prefix << bits | s->bin;
-    ties -= s->above;
+    ties -= s->over;
     border = prefix << shift;
     if (s->in_bin == ties) {  // the whole bin stays: the border lies below it, and no equals are left to choose from
       border--;               // (never 0: with the bin of key 0 everything would stay)
       ties = 0;
       break;
     }
-    __syncthreads();
   }
 
-  // ---- who stays: each thread a run of places in order
-  const int run = ((per + SELECT_THREADS - 1) / SELECT_THREADS) | 1;  // odd: no bank twice
-  const int from = min(tid * run, count), to = min(from + run, count);
-  uint32_t sure_low = 0, sure_high = 0, equal_low = 0, equal_high = 0;
-  for (int i = from; i < to; i++) {
-    const uint32_t k = key(i);
-    const bool low = i0 + i < stays;
-    if (k > border) (low ? sure_low : sure_high)++;
-    if (k == border) (low ? equal_low : equal_high)++;
+  // ---- who stays
+  uint4 c = make_uint4(0, 0, 0, 0);
+  each([&](uint32_t k, int i) {
+    const bool there = i < end, low = i < stays;
+    c.x += __popc(__ballot_sync(ALL, there && low && k > border));
+    c.z += __popc(__ballot_sync(ALL, there && !low && k > border));
+    if (ties) {
+      c.y += __popc(__ballot_sync(ALL, there && low && k == border));
+      c.w += __popc(__ballot_sync(ALL, there && !low && k == border));
+    }
+  });
+  if (lane == 0) s->warp[warp] = c;
+  __syncthreads();
+  if (warp == 0) {
+    const uint4 w = lane < SELECT_WARPS ? s->warp[lane] : make_uint4(0, 0, 0, 0);
+    const uint4 sum = make_uint4(warp_sum(w.x), warp_sum(w.y), warp_sum(w.z), warp_sum(w.w));
+    if (lane == 0) s->sums = sum;
   }
-  uint64_t sums_low, sums_high;
-  const uint64_t before_low = block_scan(two(sure_low, equal_low), s, &sums_low);
-  const uint64_t before_high = block_scan(two(sure_high, equal_high), s, &sums_high);
-  uint32_t equals_before = (uint32_t)(before_low >> 32) + (uint32_t)(before_high >> 32);  // in this block, in order
-  if (tid == 0) s->sums = make_uint4((uint32_t)sums_low, (uint32_t)(sums_low >> 32), (uint32_t)sums_high, (uint32_t)(sums_high >> 32));
   if (C > 1) {
     cluster_arrive();
     cluster_wait();
-  } else {
+    if (tid < C) s->cta[tid] = cluster_load4(dsmem_addr(&s->sums, tid));
+    cluster_arrive();  // waited for at the end: no block leaves before its sums have been read
     __syncthreads();
   }
-  if (tid < C) s->all[tid] = cluster_load4(C > 1 ? dsmem_addr(&s->sums, tid) : smem_u32(&s->sums));
-  if (C > 1) cluster_arrive();  // no block leaves before its sums have been read
-  __syncthreads();
-  uint32_t left = ties, mine = 0, holes = 0, movers = 0;  // equals still to be taken; before this block
-  for (int r = 0; r < C; r++) {
-    const uint4 a = s->all[r];
-    const uint32_t low = min(left, a.y), high = min(left - low, a.w);
-    const int first = min(r * per, n), end = min(first + per, n);
-    const uint32_t size_low = (uint32_t)max(0, min(end, stays) - first);
-    if (r == rank) mine = left;
-    if (r < rank) holes += size_low - a.x - low, movers += a.z + high;
-    left -= low + high;
-  }
-  auto kept = [&](int i, uint32_t& equals) {
-    const uint32_t k = key(i);
-    return k > border || (k == border && equals++ < mine);
-  };
-  uint32_t my_holes = 0, my_movers = 0, equals = equals_before;
-  for (int i = from; i < to; i++) {
-    const bool stay = kept(i, equals);
-    if (i0 + i < stays)
-      my_holes += !stay;
-    else
-      my_movers += stay;
-  }
-  uint64_t listed;
-  const uint64_t before = block_scan(two(my_holes, my_movers), s, &listed);
-  int32_t* hole = p.lists + (int64_t)item * 2 * p.half + holes + (uint32_t)before;
-  int32_t* mover = p.lists + ((int64_t)item * 2 + 1) * p.half + movers + (uint32_t)(before >> 32);
-  equals = equals_before;
-  for (int i = from; i < to; i++) {
-    const bool stay = kept(i, equals);
-    if (i0 + i < stays) {
-      if (!stay) *hole++ = i0 + i;
-    } else if (stay) {
-      *mover++ = i0 + i;
+  // this warp's places among all: lane r has block r's counts, lane w then warp w's
+  uint32_t equals = 0, holes = 0, movers = 0;
+  auto before = [&](uint4 x, int first, int size, bool counted) {  // adds the runs in front, each `size` places from `first` on
+    uint32_t inc = x.y + x.w;
+    const uint32_t own = inc;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      const uint32_t a = __shfl_up_sync(ALL, inc, o);
+      if (lane >= o) inc += a;
     }
-  }
-  if (rank == C - 1 && tid == 0) p.chosen[item] = make_int2((int)(movers + (uint32_t)(listed >> 32)), stays);
+    const uint2 stay = staying(x, equals + inc - own, ties);
+    const int low = max(0, min(min(first + size, n), stays) - min(first, n));
+    holes += warp_sum(counted ? (uint32_t)low - stay.x : 0);
+    movers += warp_sum(counted ? stay.y : 0);
+    equals += warp_sum(counted ? own : 0);
+  };
+  if (C > 1) before(lane < C ? s->cta[lane] : make_uint4(0, 0, 0, 0), lane * SELECT_WARPS * per, SELECT_WARPS * per, lane < rank);
+  before(lane < SELECT_WARPS ? s->warp[lane] : make_uint4(0, 0, 0, 0), (rank * SELECT_WARPS + lane) * per, per, lane < warp);
+  int32_t* hole = p.lists + (int64_t)item * 2 * p.half + holes;
+  int32_t* mover = p.lists + ((int64_t)item * 2 + 1) * p.half + movers;
+  const uint32_t below = (1u << lane) - 1;
+  uint32_t moved = 0;
+  each([&](uint32_t k, int i) {
+    bool stay = k > border;
+    if (ties) {
+      const uint32_t equal = __ballot_sync(ALL, i < end && k == border);
+      stay |= k == border && equals + __popc(equal & below) < ties;
+      equals += __popc(equal);
+    }
+    const bool empty = i < min(end, stays) && !stay, moves = i < end && i >= stays && stay;
+    const uint32_t e = __ballot_sync(ALL, empty), m = __ballot_sync(ALL, moves);
+    if (empty) hole[__popc(e & below)] = i;
+    if (moves) mover[__popc(m & below)] = i;
+    hole += __popc(e);
+    mover += __popc(m);
+    moved += __popc(m);
+  });
+  if (rank == C - 1 && warp == SELECT_WARPS - 1 && lane == 0) p.chosen[item] = make_int2((int)(movers + moved), stays);
   if (C > 1) cluster_wait();
 }
 
-// A row of keys or values per group of width / 8 threads, 16 bytes each, four
-// rows on their way per group.
+// All items' moves are laid end to end and shared out evenly among the warps (of
+// MOVE_ITEMS items at a time).  A lane finds the rows of one move, then all of
+// them copy it: 16 bytes a lane, keys and values of a row of 128 at once, eight
+// loads on their way per lane.
+template <int D>
 __global__ void __launch_bounds__(MOVE_THREADS) qlin_evict_move_kernel(const __grid_constant__ EvictParams p) {
-  const int item = blockIdx.x / p.blocks, part = blockIdx.x % p.blocks;
-  const int b = item / p.cache.heads, h = item % p.cache.heads;
+  __shared__ int starts[MOVE_ITEMS + 1];
+  __shared__ int warp_total[MOVE_WARPS];
+  __shared__ __align__(16) longlong2 rows[MOVE_WARPS][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int item0 = blockIdx.y * MOVE_ITEMS, items = min(p.items - item0, MOVE_ITEMS);
   pdl_wait();
   pdl_launch_dependents();
-  const int2 chosen = p.chosen[item];
-  const int32_t* holes = p.lists + (int64_t)item * 2 * p.half;
-  const int32_t* movers = holes + p.half;
-  if (h == 0 && part == 0 && threadIdx.x == 0 && p.len_out && chosen.y >= 0) p.len_out[b] = chosen.y;
-  const int lanes = p.cache.width / 8, groups = MOVE_THREADS / lanes * p.blocks;
-  const int column = threadIdx.x % lanes * 8;
-  constexpr int AHEAD = 4;
-  const int64_t head = h * p.cache.head_stride + column;
-  for (int u0 = part * (MOVE_THREADS / lanes) + threadIdx.x / lanes; u0 < 2 * chosen.x; u0 += AHEAD * groups) {
-    uint4 x[AHEAD];
-    int64_t to[AHEAD];
+  // ---- where each item's moves begin
+  constexpr int PER = MOVE_ITEMS / MOVE_THREADS;
+  int count[PER], sum = 0;
 #pragma unroll
-    for (int k = 0; k < AHEAD; k++) {
-      const int u = u0 + k * groups;
-      to[k] = -1;
-      if (u >= 2 * chosen.x) continue;
-      const int64_t from = token_offset(p.cache, p.step, b, movers[u >> 1]);
-      to[k] = token_offset(p.cache, p.step, b, holes[u >> 1]);
-      if (from < 0 || to[k] < 0) {
-        to[k] = -1;
-        report(p.status, QLIN_ERR_BAD_INDEX);
-        continue;
+  for (int e = 0; e < PER; e++) {
+    const int i = tid * PER + e;
+    count[e] = 0;
+    if (i >= items) continue;
+    const int2 chosen = p.chosen[item0 + i];
+    count[e] = chosen.x;
+    if (p.len_out && blockIdx.x == 0 && (item0 + i) % p.cache.heads == 0 && chosen.y >= 0)
+      p.len_out[(item0 + i) / p.cache.heads] = chosen.y;
+    sum += chosen.x;
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(ALL, inc, o);
+    if (lane >= o) inc += a;
+  }
+  if (lane == 31) warp_total[warp] = inc;
+  __syncthreads();
+  int at = inc - sum + (int)__reduce_add_sync(ALL, lane < warp ? warp_total[lane & (MOVE_WARPS - 1)] : 0);
+#pragma unroll
+  for (int e = 0; e < PER; e++) {
+    const int i = tid * PER + e;
+    if (i < items) starts[i] = at;
+    at += count[e];
+  }
+  if (tid == MOVE_THREADS - 1) starts[items] = at;
+  __syncthreads();
+  const int64_t all = starts[items];
+  const int warps = gridDim.x * MOVE_WARPS, w = blockIdx.x * MOVE_WARPS + warp;
+  const int first = (int)(all * w / warps), end = (int)(all * (w + 1) / warps);
+
+  constexpr int ROWS = D == 64 ? 2 : 1;        // moves that a warp's lanes cover at once
+  constexpr int LOADS = D == 256 ? 2 : 1;      // 16-byte loads of a lane per move
+  constexpr int AHEAD = 8 / LOADS;
+  constexpr int LANES = 32 / ROWS;             // of a move
+  const int sub = lane % LANES;
+  uint16_t* const base = static_cast<uint16_t*>(LOADS == 1 && sub >= LANES / 2 ? p.cache.v : p.cache.k) +
+                         sub % (D / 8) * 8;
+  const int64_t other = static_cast<uint16_t*>(p.cache.v) - static_cast<uint16_t*>(p.cache.k);
+  for (int m0 = first; m0 < end; m0 += 32) {
+    const int m = m0 + lane;
+    longlong2 place = make_longlong2(-1, -1);
+    if (m < end) {
+      int lo = 0, hi = items;  // the item whose moves hold m: starts[lo] <= m < starts[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        (starts[mid] <= m ? lo : hi) = mid;
       }
-      x[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(u & 1 ? p.cache.v : p.cache.k) + from + head);
+      const int item = item0 + lo, b = item / p.cache.heads, h = item % p.cache.heads, i = m - starts[lo];
+      const int32_t* list = p.lists + (int64_t)item * 2 * p.half;
+      const int to = list[i], from = list[p.half + i];
+      place.x = token_offset(p.cache, p.step, b, from);
+      place.y = token_offset(p.cache, p.step, b, to);
+      const int64_t in = b * p.seq_stride + h * p.head_stride, out = b * p.out_seq_stride + h * p.out_head_stride;
+      p.score_out[out + to] = p.score[in + from];
+      if (p.position_out) p.position_out[out + to] = p.position ? p.position[in + from] : from;
+      if (place.x < 0 || place.y < 0) {
+        place.x = -1;
+        report(p.status, QLIN_ERR_BAD_INDEX);
+      } else {
+        place.x += h * p.cache.head_stride, place.y += h * p.cache.head_stride;
+      }
     }
+    rows[warp][lane] = place;
+    __syncwarp();
+    const int moves = min(32, end - m0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < moves; i0 += AHEAD * ROWS) {
+      uint4 x[AHEAD][LOADS];
+      int64_t to[AHEAD];
 #pragma unroll
-    for (int k = 0; k < AHEAD; k++)
-      if (to[k] >= 0)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>((u0 + k * groups) & 1 ? p.cache.v : p.cache.k) + to[k] + head) = x[k];
+      for (int u = 0; u < AHEAD; u++) {
+        const int i = i0 + u * ROWS + lane / LANES;
+        to[u] = -1;
+        if (i >= moves) continue;
+        const longlong2 r = rows[warp][i];
+        if (r.x < 0) continue;
+        to[u] = r.y;
+        x[u][0] = *reinterpret_cast<const uint4*>(base + r.x);
+        if constexpr (LOADS == 2) x[u][1] = *reinterpret_cast<const uint4*>(base + other + r.x);
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; u++) {
+        if (to[u] < 0) continue;
+        *reinterpret_cast<uint4*>(base + to[u]) = x[u][0];
+        if constexpr (LOADS == 2) *reinterpret_cast<uint4*>(base + other + to[u]) = x[u][1];
+      }
+    }
+    __syncwarp();
   }
-  const int64_t in = b * p.seq_stride + h * p.head_stride, out = b * p.out_seq_stride + h * p.out_head_stride;
-  for (int i = part * MOVE_THREADS + threadIdx.x; i < chosen.x; i += MOVE_THREADS * p.blocks) {
-    const int from = movers[i], to = holes[i];
-    p.score_out[out + to] = p.score[in + from];
-    if (p.position_out) p.position_out[out + to] = p.position ? p.position[in + from] : from;
-  }
+}
+
+// Keys of a lane in registers: as many as the longest sequence may need.
+const void* select_fn(int64_t per_lane) {
+  return per_lane <= 4    ? reinterpret_cast<const void*>(qlin_evict_select_kernel<4>)
+         : per_lane <= 16 ? reinterpret_cast<const void*>(qlin_evict_select_kernel<16>)
+         : per_lane <= 32 ? reinterpret_cast<const void*>(qlin_evict_select_kernel<32>)
+                          : reinterpret_cast<const void*>(qlin_evict_select_kernel<0>);
+}
+const void* move_fn(int width) {
+  return width == 64    ? reinterpret_cast<const void*>(qlin_evict_move_kernel<64>)
+         : width == 128 ? reinterpret_cast<const void*>(qlin_evict_move_kernel<128>)
+                        : reinterpret_cast<const void*>(qlin_evict_move_kernel<256>);
 }
 
 struct EvictDevice {
@@ -318,26 +417,28 @@ qlin_status evict_setup(EvictDevice** device) {
   if (dev < 0 || dev >= 64) return QLIN_ERR_CUDA;
   EvictDevice& d = g_evict[dev];
   std::call_once(d.once, [&d, dev] {
-    const void* fn = reinterpret_cast<const void*>(qlin_evict_select_kernel);
     cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_STAGED * 4);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(MAX_CLUSTER, 1, 1);
-    cfg.blockDim = dim3(SELECT_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = MAX_STAGED * 4;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = MAX_CLUSTER;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (e == cudaSuccess && cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
-      (void)cudaGetLastError();
-      n = 0;
+    int clusters = 1;
+    for (int per_lane : {4, 16, 32, 64}) {
+      const void* fn = select_fn(per_lane);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(MAX_CLUSTER, 1, 1);
+      cfg.blockDim = dim3(SELECT_THREADS, 1, 1);
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = MAX_CLUSTER;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (e == cudaSuccess && cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+      }
+      if (n < clusters) clusters = n;
     }
-    if (n > 0) d.most = MAX_CLUSTER;
+    if (clusters > 0) d.most = MAX_CLUSTER;
     d.ready = d.sms > 0 ? status_of(e) : QLIN_ERR_CUDA;
   });
   *device = &d;
@@ -421,19 +522,21 @@ qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const qlin_kv_step* step, 
   p.room = (int)room, p.first = first;
   int64_t most = (int64_t)step->max_pages * cache->page_size;  // tokens of a sequence
   most = most < room ? most : room;
+  p.items = (int)items;
   p.cluster = 1;
   while (p.cluster < d->most && p.cluster * 2048 < most && 2 * p.cluster * items <= 2 * d->sms) p.cluster *= 2;
-  int64_t staged = (most + p.cluster - 1) / p.cluster;
-  p.staged = (int)(staged < MAX_STAGED ? staged : MAX_STAGED);
-  int64_t blocks = (4 * d->sms + items - 1) / items, useful = (most * cache->width / 8) / (MOVE_THREADS * 4) + 1;
-  p.blocks = (int)(blocks < useful ? blocks : useful);
+  const int64_t lanes = (int64_t)p.cluster * SELECT_THREADS;
   void* args[] = {&p};
-  st = launch_step(reinterpret_cast<const void*>(qlin_evict_select_kernel), dim3((unsigned)(items * p.cluster), 1, 1),
-                   dim3(SELECT_THREADS, 1, 1), (size_t)p.staged * 4, static_cast<cudaStream_t>(stream), args,
-                   (flags & QLIN_FLAG_PDL) != 0, p.cluster);
+  st = launch_step(select_fn((most + lanes - 1) / lanes), dim3((unsigned)(items * p.cluster), 1, 1),
+                   dim3(SELECT_THREADS, 1, 1), 0, static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0,
+                   p.cluster);
   if (st != QLIN_OK) return st;
-  return launch_step(reinterpret_cast<const void*>(qlin_evict_move_kernel), dim3((unsigned)(items * p.blocks), 1, 1),
-                     dim3(MOVE_THREADS, 1, 1), 0, static_cast<cudaStream_t>(stream), args, true);
+  const int64_t groups = (items + MOVE_ITEMS - 1) / MOVE_ITEMS;
+  int64_t blocks = (4 * d->sms + groups - 1) / groups;
+  const int64_t useful = items * (most / 2) / (8 * MOVE_WARPS) + 1;  // eight moves a warp
+  if (blocks > useful) blocks = useful;
+  return launch_step(move_fn(cache->width), dim3((unsigned)blocks, (unsigned)groups, 1), dim3(MOVE_THREADS, 1, 1), 0,
+                     static_cast<cudaStream_t>(stream), args, true);
 }
 
 }  // extern "C"
