@@ -9,10 +9,10 @@
 namespace qlin {
 namespace {
 
-constexpr int ADJUST_THREADS = 256;
+constexpr int ADJUST_THREADS = 512;
 constexpr int AHEAD = 4;              // vectors of 16 bytes in flight per thread
 constexpr int HISTORY_AHEAD = 8;      // tokens of the history in flight per thread
-constexpr int MAX_SLICE = 16384;      // tokens of a block at most
+constexpr int FIXES_AHEAD = 4;        // changed logits in flight per thread
 constexpr int CLUSTER = 8;            // blocks that share the reading of a long history
 constexpr int LONG_HISTORY = 4096;
 constexpr int CLUSTER_SLICE = 2048;   // tokens of a block of theirs at most: each counts for all eight
@@ -30,11 +30,14 @@ struct AdjustParams {
   const void* logits;
   void* out;
   int64_t ld, out_ld, V;
-  int T, slice, cluster;
-  int column;        // words between the eight columns that a slice's words lie in
-  uint32_t inverse;  // 2^32 / (vectors of a row), rounded up
-  bool in_place;
+  int T, slice;
+  int vectors;              // of a row's slice, on the row's alignment
+  uint32_t vectors_inverse; // 2^32 / vectors, rounded up
+  bool in_place, history_vectors;
 };
+
+// One row per sequence, several, or a tree's drafted ones.
+enum class Rows { ONE, SEVERAL, DRAFTED };
 
 // A sequence's penalties.
 struct Penalties {
@@ -55,58 +58,62 @@ __device__ __forceinline__ float from_float<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16(x); }
 
-// One block per sequence, slice of the vocabulary and (at most 32 of its) rows: the
-// slice's words first, from the whole history, then the rows' slices in 16-byte
-// vectors on their own alignment, whose first loads are on their way meanwhile.  A
-// long history is read once per cluster: each block counts a part of it for all
-// slices of the cluster, and adds up its own slice's counts from all blocks.
-// Word i of a slice lies in column i % 8 (so that vectors' words fall into
-// different banks), and a bit per token says which words are not zero.
-template <typename T>
-__global__ void __launch_bounds__(ADJUST_THREADS) qlin_adjust_kernel(const __grid_constant__ AdjustParams p) {
-  constexpr int VEC = 16 / sizeof(T);
-  extern __shared__ __align__(16) uint32_t shared[];  // words of the cluster's slices, bits of this one
+// One block per sequence, slice of the vocabulary and (at most 32 of its) rows.  The
+// slice's words are formed first, from the whole history, and with them a list of
+// the tokens that they concern, few of the slice's as a rule.  The rows' slices
+// are copied in 16-byte vectors on their own alignment, loaded before all that and
+// stored without what is forbidden, and then the listed tokens' logits are written,
+// a thread each: looked for within the vectors they cost a warp its time wherever
+// one lane has one.  A long history is read once per cluster: each block counts a
+// part of it for all slices of the cluster, and adds up its own slice's counts.
+template <typename T, bool CLUSTERS, Rows KIND>
+__global__ void __launch_bounds__(ADJUST_THREADS, 2) qlin_adjust_kernel(const __grid_constant__ AdjustParams p) {
+  constexpr int VEC = 16 / sizeof(T), C = CLUSTERS ? CLUSTER : 1;
+  constexpr bool DRAFTS = KIND == Rows::DRAFTED, ONE = KIND == Rows::ONE;
+  extern __shared__ __align__(16) uint32_t shared[];  // words of the cluster's slices, the list of this one
   __shared__ float bias[QLIN_MAX_BIAS];
   __shared__ int draft[ROWS];
   __shared__ uint32_t tree[ROWS];
+  __shared__ int listed;
+  __shared__ uint16_t queues[ADJUST_THREADS / 32][32 * HISTORY_AHEAD];
   const qlin_adjustments& a = p.a;
-  const int b = blockIdx.y, tid = threadIdx.x, S = p.slice, column = p.column;
-  const int rank = p.cluster > 1 ? (int)cluster_ctarank() : 0;
-  const int t0 = blockIdx.z * ROWS, rows = min(p.T - t0, ROWS);
-  const int64_t v0 = (int64_t)blockIdx.x * S;
-  const int n = (int)max((int64_t)0, min((int64_t)S, p.V - v0));  // tokens of this slice
-  uint32_t* words = shared + rank * 8 * column;
-  uint32_t* bits = shared + p.cluster * 8 * column;
-  auto place = [column](int i) { return (i & 7) * column + (i >> 3); };
+  const int b = blockIdx.y, tid = threadIdx.x, S = p.slice, V = (int)p.V;
+  const int rank = CLUSTERS ? (int)cluster_ctarank() : 0;
+  const int t0 = ONE ? 0 : blockIdx.z * ROWS, rows = ONE ? 1 : min(p.T - t0, ROWS);
+  const int v0 = blockIdx.x * S, n = max(0, min(S, V - v0));  // tokens of this slice
+  uint32_t* words = shared + rank * S;
+  uint16_t* list = reinterpret_cast<uint16_t*>(shared + C * S);
   pdl_wait();
   pdl_launch_dependents();
-  const bool counts = a.history != nullptr, drafts = a.draft != nullptr;
+  const bool counts = a.history != nullptr;
   const int64_t row0 = (int64_t)b * p.T + t0;
 
-  auto allowed_bits = [&](int64_t row, int64_t lo, int64_t hi) -> uint32_t {  // of at most 8 tokens, the first in bit 0
-    const int32_t* w = a.allowed + row * a.allowed_stride + (lo >> 5);
-    const int sh = (int)(lo & 31);
-    uint32_t m = (uint32_t)w[0] >> sh;
-    if (((hi - 1) ^ lo) >> 5) m |= (uint32_t)w[1] << (32 - sh);
+  auto allowed_bits = [&](int t, int lo, int hi) -> uint32_t {  // of at most 8 tokens of the slice, the first in bit 0
+    lo += v0, hi += v0;
+    const int32_t* w = a.allowed + (row0 + t) * a.allowed_stride + (lo >> 5);
+    uint32_t m = (uint32_t)w[0] >> (lo & 31);
+    if (((hi - 1) ^ lo) >> 5) m |= (uint32_t)w[1] << (32 - (lo & 31));
     return m;
   };
 
-  // ---- vectors of the rows: which, and what is loaded of them ahead
-  const int vectors = S / VEC + 1, total = n ? vectors * rows : 0;
+  // ---- vectors of the rows
+  const int total = n ? p.vectors * rows : 0;
   struct Vector {
     const T* src;
     T* dst;
-    int t, lo, hi;  // its tokens' places in the slice
+    int t, lo, hi;  // its row, its tokens' places in the slice
     bool whole;     // 16 bytes on both sides
   };
   auto vector = [&](int i) {
     Vector v;
-    v.t = rows > 1 ? (int)__umulhi((uint32_t)i, p.inverse) : 0;
+    v.t = ONE ? 0 : (int)__umulhi((uint32_t)i, p.vectors_inverse);
     v.src = static_cast<const T*>(p.logits) + (row0 + v.t) * p.ld + v0;
     v.dst = static_cast<T*>(p.out) + (row0 + v.t) * p.out_ld + v0;
-    const int e = (i - v.t * vectors) * VEC - (int)(reinterpret_cast<uintptr_t>(v.src) / sizeof(T) % VEC);
+    const int shift = (int)(reinterpret_cast<uintptr_t>(v.src) / sizeof(T) % VEC);
+    const int out_shift = (int)(reinterpret_cast<uintptr_t>(v.dst) / sizeof(T) % VEC);
+    const int e = (i - v.t * p.vectors) * VEC - shift;
     v.lo = max(e, 0), v.hi = i < total ? min(e + VEC, n) : 0;
-    v.whole = v.hi - v.lo == VEC && reinterpret_cast<uintptr_t>(v.dst + v.lo) % 16 == 0;
+    v.whole = v.hi - v.lo == VEC && shift == out_shift;
     return v;
   };
   uint4 x[AHEAD];
@@ -118,133 +125,159 @@ __global__ void __launch_bounds__(ADJUST_THREADS) qlin_adjust_kernel(const __gri
       open[u] = 0xFFFFFFFFu;
       if (v.lo >= v.hi) continue;
       const uint32_t behind = 0xFFFFFFFFu << (v.hi - v.lo);
-      if (a.allowed) open[u] = allowed_bits(row0 + v.t, v0 + v.lo, v0 + v.hi) | behind;
+      if (a.allowed) open[u] = allowed_bits(v.t, v.lo, v.hi) | behind;
       if (v.whole && !p.in_place && open[u] != behind) x[u] = *reinterpret_cast<const uint4*>(v.src + v.lo);
     }
   };
   load(tid);
 
-  // ---- the words
+  // ---- the words and their list
   bool any_draft = false;
-  if (counts || drafts || a.n_bias) {
-    const int32_t* h = counts ? a.history + b * a.history_stride : nullptr;
-    const int step = p.cluster * ADJUST_THREADS, h0 = rank * ADJUST_THREADS + tid;
-    int token[HISTORY_AHEAD];
-    auto read = [&](int i0) {
-#pragma unroll
-      for (int u = 0; u < HISTORY_AHEAD; u++) token[u] = i0 + u * step < a.L ? h[i0 + u * step] : -1;
-    };
-    if (counts) read(h0);
-    int L = a.L, prompt = 0;
-    if (counts) {
-      if (a.history_len) L = max(0, min(a.history_len[b], L));
-      if (a.prompt_len) prompt = a.prompt_len[b];
-    }
-    const int32_t* bias_token = a.bias_token + b * a.bias_stride;
-    int first_bias = tid < 32 && tid < a.n_bias ? bias_token[tid] : -1;
-    if (drafts && tid < p.T) {
+  int fixes = 0;
+  if (counts || DRAFTS || a.n_bias) {
+    int first_bias = -1;
+    float first_value = 0.f;
+    if (tid < 32 && tid < a.n_bias)
+      first_bias = a.bias_token[b * a.bias_stride + tid], first_value = a.bias[b * a.bias_stride + tid];
+    if (DRAFTS && tid < p.T) {
       draft[tid] = a.draft[(int64_t)b * p.T + tid];
       tree[tid] = a.mask ? (uint32_t)a.mask[b * a.tree_stride + tid] : 0xFFFFFFFFu >> (31 - tid);
     }
-    for (int i = tid; i < (p.cluster * 8 * column + S / 32 + 3) / 4; i += ADJUST_THREADS)
-      reinterpret_cast<uint4*>(shared)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+    if (tid == 0) listed = 0;
+    auto clear = [&] {
+      for (int i = tid; i < C * S / 4; i += ADJUST_THREADS) reinterpret_cast<uint4*>(shared)[i] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+    };
     if (counts) {
-      const int64_t base = v0 - (int64_t)rank * S;
-      const int range = p.cluster > 1 ? S * p.cluster : n;
+      // four consecutive tokens at a time where that can be, HISTORY_AHEAD on their way
+      const int32_t* h = a.history + b * a.history_stride;
+      int token[HISTORY_AHEAD], L = a.L, prompt = 0;
+      constexpr int QUADS = HISTORY_AHEAD / 4, STEP = C * ADJUST_THREADS;
+      const int h0 = rank * ADJUST_THREADS + tid;
+      auto at_of = [&](int r, int u) {  // place in the history of token u of round r
+        return p.history_vectors ? ((r * QUADS + u / 4) * STEP + h0) * 4 + u % 4 : (r * HISTORY_AHEAD + u) * STEP + h0;
+      };
+      auto read = [&](int r) {
+        if (p.history_vectors) {
+#pragma unroll
+          for (int u = 0; u < HISTORY_AHEAD; u += 4) {
+            const int i = at_of(r, u);
+            const int4 q = i < a.L ? *reinterpret_cast<const int4*>(h + i) : make_int4(-1, -1, -1, -1);
+            token[u] = q.x, token[u + 1] = q.y, token[u + 2] = q.z, token[u + 3] = q.w;
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < HISTORY_AHEAD; u++) token[u] = at_of(r, u) < a.L ? h[at_of(r, u)] : -1;
+        }
+      };
+      read(0);
+      if (a.history_len) L = max(0, min(a.history_len[b], L));
+      if (a.prompt_len) prompt = a.prompt_len[b];
+      clear();
+      const int base = v0 - rank * S;
+      uint16_t* queue = queues[tid >> 5];
+      const uint32_t below = (1u << (tid & 31)) - 1;
+      const uint32_t range = CLUSTERS ? (uint32_t)min(C * S, V - base) : (uint32_t)n;
 #pragma unroll 1
-      for (int i0 = h0; i0 < L; i0 += HISTORY_AHEAD * step) {
-        if (i0 != h0) read(i0);
+      for (int r = 0; r * HISTORY_AHEAD * STEP < L; r++) {
+        if (r) read(r);
+        // what concerns these slices goes through a queue of the warp, so that few
+        // lanes with something to count do not hold up the others time and again
+        int queued = 0;
 #pragma unroll
         for (int u = 0; u < HISTORY_AHEAD; u++) {
-          const int i = i0 + u * step;
-          const int64_t at = token[u] - base;
-          if (i >= L || at < 0 || at >= range || token[u] >= p.V) continue;
-          uint32_t* word;
-          if (p.cluster > 1) {
-            const uint32_t owner = (uint32_t)at / (uint32_t)S;
-            word = shared + owner * 8 * column + place((int)at - owner * S);
-          } else {
-            word = words + place((int)at);
-            atomicOr(&bits[at >> 5], 1u << (at & 31));
-          }
-          if (i < prompt)
-            atomicOr(word, IN_PROMPT);
-          else
-            atomicAdd(word, 1u);
+          const uint32_t at = (uint32_t)(token[u] - base);  // (a token below 0: far above)
+          const int i = at_of(r, u);
+          const bool hit = at < range && i < L;
+          const uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit);
+          if (hit) queue[queued + __popc(hits & below)] = (uint16_t)(at | (i < prompt ? 0x8000u : 0u));
+          queued += __popc(hits);
         }
+        __syncwarp();
+        for (int i = tid & 31; i < queued; i += 32) {
+          const uint32_t e = queue[i], at = e & 0x7FFF;
+          uint32_t* word = CLUSTERS ? &shared[at] : &words[at];
+          if (CLUSTERS) {
+            if (e >> 15)
+              atomicOr(word, IN_PROMPT);
+            else
+              atomicAdd(word, 1u);
+          } else if ((e >> 15 ? atomicOr(word, IN_PROMPT) : atomicAdd(word, 1u)) == 0) {
+            list[atomicAdd(&listed, 1)] = (uint16_t)at;
+          }
+        }
+        __syncwarp();
       }
-      if (p.cluster > 1) {
+      if constexpr (CLUSTERS) {
         cluster_arrive();
         cluster_wait();
-        // all lanes of a warp stay: a ballot per 32 tokens
+        const uint32_t mine = smem_u32(words);
         for (int i = tid; i < S; i += ADJUST_THREADS) {
-          const uint32_t mine = smem_u32(words + place(i));
-          uint32_t sum = 0;
+          uint32_t w[C], sum = 0;
 #pragma unroll
-          for (int r = 0; r < CLUSTER; r++) {
-            uint32_t w;
-            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(w) : "r"(dsmem_addr_u32(mine, r)) : "memory");
-            sum = ((sum & ~IN_PROMPT) + (w & ~IN_PROMPT)) | ((sum | w) & IN_PROMPT);
-          }
-          words[place(i)] = sum;  // read by this block alone
-          const uint32_t any = __ballot_sync(0xFFFFFFFFu, sum != 0);
-          if ((tid & 31) == 0) bits[i >> 5] = any;
+          for (int r = 0; r < C; r++)
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(w[r]) : "r"(dsmem_addr_u32(mine + i * 4, r)) : "memory");
+#pragma unroll
+          for (int r = 0; r < C; r++) sum = ((sum & ~IN_PROMPT) + (w[r] & ~IN_PROMPT)) | ((sum | w[r]) & IN_PROMPT);
+          words[i] = sum;  // read by this block alone
+          if (sum) list[atomicAdd(&listed, 1)] = (uint16_t)i;
         }
         cluster_arrive();  // waited for at the end: no block leaves while others read its words
       }
       __syncthreads();
+    } else {
+      clear();
     }
     if (a.n_bias && tid < 32) {  // one warp, in the list's order: biases of one token are added in that order
-      const float* values = a.bias + b * a.bias_stride;
       int used = 0;
       for (int i0 = 0; i0 < a.n_bias; i0 += 32) {
         const int i = i0 + tid;
-        const int64_t at = i < a.n_bias ? (i0 ? bias_token[i] : first_bias) - v0 : -1;
-        const bool here = at >= 0 && at < n;
-        const uint32_t all = __ballot_sync(0xFFFFFFFFu, here);
-        if (!all) continue;
-        const float value = here ? values[i] : 0.f;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, here ? (int)at : -1 - tid);
+        if (i0) {
+          first_bias = i < a.n_bias ? a.bias_token[b * a.bias_stride + i] : -1;
+          first_value = i < a.n_bias ? a.bias[b * a.bias_stride + i] : 0.f;
+        }
+        const bool here = first_bias >= 0 && (uint32_t)(first_bias - v0) < (uint32_t)n;
+        if (!__any_sync(0xFFFFFFFFu, here)) continue;
+        const int at = here ? first_bias - v0 : 0;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, here ? at : -1 - tid);
         const bool first = here && (same & ((1u << tid) - 1)) == 0;
-        uint32_t* word = words + place(here ? (int)at : 0);
-        uint32_t slot = first ? slot_of(*word) : 0;
+        uint32_t slot = first ? slot_of(words[at]) : 0;
         const bool fresh = first && !slot;
         const uint32_t made = __ballot_sync(0xFFFFFFFFu, fresh);
         if (fresh) {
           slot = used + __popc(made & ((1u << tid) - 1)) + 1;
-          *word |= slot << 20;
-          atomicOr(&bits[at >> 5], 1u << (at & 31));
-          bias[slot - 1] = value;
+          if (words[at] == 0) list[atomicAdd(&listed, 1)] = (uint16_t)at;
+          words[at] |= slot << 20;
+          bias[slot - 1] = first_value;
         }
         used += __popc(made);
         __syncwarp();
         uint32_t again = __ballot_sync(0xFFFFFFFFu, here && !fresh);
         while (again) {
-          if (tid == __ffs(again) - 1) bias[slot_of(*word) - 1] += value;
+          if (tid == __ffs(again) - 1) bias[slot_of(words[at]) - 1] += first_value;
           again &= again - 1;
           __syncwarp();
         }
       }
     }
-    if (a.n_bias || drafts) any_draft = __syncthreads_or(drafts && tid < p.T && draft[tid] >= v0 && draft[tid] < v0 + n);
+    if (a.n_bias || DRAFTS)
+      any_draft = __syncthreads_or(DRAFTS && tid < p.T && draft[tid] >= 0 && (uint32_t)(draft[tid] - v0) < (uint32_t)n);
+    fixes = counts || a.n_bias ? listed * rows : 0;
   }
   Penalties value = {1.f, 0.f, 0.f};
   if (a.repetition) value.r = a.repetition[b];
   if (!(value.r > 0.f)) value.r = 1.f;
   if (a.presence) value.p = a.presence[b];
   if (a.frequency) value.f = a.frequency[b];
-  const bool touched_at_all = counts || a.n_bias;
 
   // Tokens of the tree's rows: a row's path counts its own, on top of the history.
-  // Their values are formed before anything is written, as out may be the logits.
-  float path_value[MAX_PAIRS];
-  bool path_here[MAX_PAIRS];
-  if (any_draft) {
+  // Their values are formed before any changed one is written, as out may be the logits.
+  float path_value[DRAFTS ? MAX_PAIRS : 1];
+  uint32_t path_here = 0;
+  if (DRAFTS && any_draft) {
 #pragma unroll
     for (int k = 0; k < MAX_PAIRS; k++) {
       const int pair = tid + k * ADJUST_THREADS, t = pair / p.T, j = pair % p.T;
-      path_here[k] = false;
       if (t >= p.T || !(tree[t] >> j & 1) || draft[j] < v0 || draft[j] >= v0 + n) continue;
       uint32_t more = 0;
       bool first = true;
@@ -253,64 +286,94 @@ __global__ void __launch_bounds__(ADJUST_THREADS) qlin_adjust_kernel(const __gri
           more++;
           if (i < j) first = false;
         }
-      if (!first || (a.allowed && !(allowed_bits(row0 + t, draft[j], (int64_t)draft[j] + 1) & 1))) continue;
-      const T* in = static_cast<const T*>(p.logits) + (row0 + t) * p.ld;
-      path_value[k] = value(to_float(in[draft[j]]), words[place((int)(draft[j] - v0))], more, bias);
-      path_here[k] = true;
+      const int at = draft[j] - v0;
+      if (!first || (a.allowed && !(allowed_bits(t, at, at + 1) & 1))) continue;
+      path_value[k] = value(to_float(static_cast<const T*>(p.logits)[(row0 + t) * p.ld + draft[j]]), words[at], more, bias);
+      path_here |= 1u << k;
     }
-    if (p.in_place) __syncthreads();
   }
+
+  // Changed logits, FIXES_AHEAD of them at once: their logits and whether they are
+  // allowed, then their values.  (What is stored in between leaves allowed logits
+  // as they are, also in place.)
+  float y[FIXES_AHEAD];
+  uint32_t stands = 0;
+  const uint32_t per_row = fixes ? (uint32_t)listed : 1u, per_row_inverse = ONE ? 0u : 0xFFFFFFFFu / per_row + 1;
+  auto row_of = [&](int i) {  // i / per_row
+    if (ONE) return 0;
+    if (per_row == 1) return i;
+    const int t = (int)__umulhi((uint32_t)i, per_row_inverse);  // or one more, far out
+    return t * (int)per_row > i ? t - 1 : t;
+  };
+  auto fetch = [&](int i0) {
+    stands = 0;
+#pragma unroll
+    for (int k = 0; k < FIXES_AHEAD; k++) {
+      const int i = i0 + k * ADJUST_THREADS;
+      if (i >= fixes) continue;
+      const int t = row_of(i), at = list[i - t * (int)per_row];
+      y[k] = to_float(static_cast<const T*>(p.logits)[(row0 + t) * p.ld + v0 + at]);
+      stands |= (a.allowed ? allowed_bits(t, at, at + 1) & 1 : 1u) << k;
+    }
+  };
+  auto settle = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < FIXES_AHEAD; k++) {
+      const int i = i0 + k * ADJUST_THREADS;
+      if (!(stands >> k & 1)) continue;
+      const int t = row_of(i), at = list[i - t * (int)per_row];
+      static_cast<T*>(p.out)[(row0 + t) * p.out_ld + v0 + at] = from_float<T>(value(y[k], words[at], 0, bias));
+    }
+  };
+  fetch(tid);
 
   // ---- the rows
   const T forbidden = from_float<T>(-INFINITY);
-  if (!p.in_place || touched_at_all || a.allowed) {
+  if (!p.in_place || a.allowed) {
 #pragma unroll 1
     for (int i0 = tid; i0 < total; i0 += AHEAD * ADJUST_THREADS) {
       if (i0 != tid) load(i0);
 #pragma unroll
       for (int u = 0; u < AHEAD; u++) {
         const Vector v = vector(i0 + u * ADJUST_THREADS);
-        if (v.lo >= v.hi) continue;
-        uint32_t any = 0;
-        if (touched_at_all) {
-          any = bits[v.lo >> 5] >> (v.lo & 31);
-          if ((v.hi - 1) >> 5 != v.lo >> 5) any |= bits[(v.hi - 1) >> 5] << (32 - (v.lo & 31));
-          any &= ~(0xFFFFFFFFu << (v.hi - v.lo));
-        }
-        if (p.in_place && !any && open[u] == 0xFFFFFFFFu) continue;
+        if (v.lo >= v.hi || (p.in_place && open[u] == 0xFFFFFFFFu)) continue;
         if (v.whole) {
           if (p.in_place) x[u] = *reinterpret_cast<const uint4*>(v.src + v.lo);
-          if (any || open[u] != 0xFFFFFFFFu) {
-            T y[VEC];
-            *reinterpret_cast<uint4*>(y) = x[u];
+          if (open[u] != 0xFFFFFFFFu) {
+            T z[VEC];
+            *reinterpret_cast<uint4*>(z) = x[u];
 #pragma unroll
-            for (int e = 0; e < VEC; e++) {
-              if (any >> e & 1) y[e] = from_float<T>(value(to_float(y[e]), words[place(v.lo + e)], 0, bias));
-              if (!(open[u] >> e & 1)) y[e] = forbidden;
-            }
-            x[u] = *reinterpret_cast<const uint4*>(y);
+            for (int e = 0; e < VEC; e++)
+              if (!(open[u] >> e & 1)) z[e] = forbidden;
+            x[u] = *reinterpret_cast<const uint4*>(z);
           }
           *reinterpret_cast<uint4*>(v.dst + v.lo) = x[u];
         } else {
-          for (int e = 0; e < v.hi - v.lo; e++) {
-            T y = v.src[v.lo + e];
-            if (any >> e & 1) y = from_float<T>(value(to_float(y), words[place(v.lo + e)], 0, bias));
-            if (!(open[u] >> e & 1)) y = forbidden;
-            v.dst[v.lo + e] = y;
-          }
+          for (int e = 0; e < v.hi - v.lo; e++) v.dst[v.lo + e] = open[u] >> e & 1 ? v.src[v.lo + e] : forbidden;
         }
       }
     }
   }
-  if (any_draft) {
+
+  // ---- what changes
+  if (fixes) {
+    __syncthreads();
+    settle(tid);
+#pragma unroll 1
+    for (int i0 = tid + FIXES_AHEAD * ADJUST_THREADS; i0 < fixes; i0 += FIXES_AHEAD * ADJUST_THREADS) {
+      fetch(i0);
+      settle(i0);
+    }
+  }
+  if (DRAFTS && any_draft) {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < MAX_PAIRS; k++) {
       const int pair = tid + k * ADJUST_THREADS, t = pair / p.T, j = pair % p.T;
-      if (path_here[k]) static_cast<T*>(p.out)[(row0 + t) * p.out_ld + draft[j]] = from_float<T>(path_value[k]);
+      if (path_here >> k & 1) static_cast<T*>(p.out)[(row0 + t) * p.out_ld + draft[j]] = from_float<T>(path_value[k]);
     }
   }
-  if (p.cluster > 1) cluster_wait();
+  if constexpr (CLUSTERS) cluster_wait();
 }
 
 struct AdjustDevice {
@@ -320,12 +383,17 @@ struct AdjustDevice {
 };
 AdjustDevice g_adjust[64];
 
-constexpr int64_t column_of(int64_t slice) { return (slice / 8 + 27) / 32 * 32 + 4; }  // banks: 4 more per column
-constexpr int64_t adjust_smem(int64_t slice, int cluster) { return (cluster * 8 * column_of(slice) + slice / 32 + 4) * 4; }
+constexpr int64_t adjust_smem(int64_t slice, int cluster) { return slice * (4 * cluster + 2); }
 
-const void* adjust_fn(int dtype) {
-  return dtype == QLIN_F32 ? reinterpret_cast<const void*>(qlin_adjust_kernel<float>)
-                           : reinterpret_cast<const void*>(qlin_adjust_kernel<__nv_bfloat16>);
+template <typename T, bool CLUSTERS>
+const void* adjust_fn_t(Rows kind) {
+  return kind == Rows::ONE       ? reinterpret_cast<const void*>(qlin_adjust_kernel<T, CLUSTERS, Rows::ONE>)
+         : kind == Rows::SEVERAL ? reinterpret_cast<const void*>(qlin_adjust_kernel<T, CLUSTERS, Rows::SEVERAL>)
+                                 : reinterpret_cast<const void*>(qlin_adjust_kernel<T, CLUSTERS, Rows::DRAFTED>);
+}
+const void* adjust_fn(int dtype, bool clusters, Rows kind) {
+  if (dtype == QLIN_F32) return clusters ? adjust_fn_t<float, true>(kind) : adjust_fn_t<float, false>(kind);
+  return clusters ? adjust_fn_t<__nv_bfloat16, true>(kind) : adjust_fn_t<__nv_bfloat16, false>(kind);
 }
 
 qlin_status adjust_setup(int* sms) {
@@ -336,10 +404,12 @@ qlin_status adjust_setup(int* sms) {
   AdjustDevice& d = g_adjust[dev];
   std::call_once(d.once, [&d, dev] {
     cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t one = adjust_smem(MAX_SLICE, 1), many = adjust_smem(CLUSTER_SLICE, CLUSTER);
     for (int dtype : {QLIN_F32, QLIN_BF16})
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(adjust_fn(dtype), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(one > many ? one : many));
+      for (bool clusters : {false, true})
+        for (Rows kind : {Rows::ONE, Rows::SEVERAL, Rows::DRAFTED})
+          if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(adjust_fn(dtype, clusters, kind), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)(clusters ? adjust_smem(CLUSTER_SLICE, CLUSTER) : adjust_smem(AHEAD * ADJUST_THREADS * 8, 1)));
     d.ready = d.sms > 0 ? status_of(e) : QLIN_ERR_CUDA;
   });
   *sms = d.sms;
@@ -384,18 +454,26 @@ extern "C" qlin_status qlin_adjust_logits(int B, int T, int64_t V, int dtype, co
   int sms = 0;
   const qlin_status st = adjust_setup(&sms);
   if (st != QLIN_OK) return st;
-  p.cluster = a.history && a.L > LONG_HISTORY && V > 4096 ? CLUSTER : 1;
-  const int64_t most = p.cluster > 1 ? CLUSTER_SLICE : MAX_SLICE;
-  int64_t slice = (V * B + 3 * sms - 1) / (3 * sms);
-  slice = slice < 512 ? 512 : slice > most ? most : (slice + 127) / 128 * 128;
+  const bool clusters = a.history && a.L > LONG_HISTORY && V > 4096;
+  const Rows kind = a.draft ? Rows::DRAFTED : T > 1 ? Rows::SEVERAL : Rows::ONE;
+  p.history_vectors = a.history && is_aligned(a.history, 16) && a.L % 4 == 0 && (B == 1 || a.history_stride % 4 == 0);
+  // A thread's vectors of a block: AHEAD, or fewer where that leaves SMs idle.  Rows
+  // off the 16-byte grid take one vector more than their slice has.
+  const int64_t vec = 16 / size, rows = T < ROWS ? T : ROWS;
+  const int64_t spare = is_aligned(logits, 16) && (M == 1 || ld % vec == 0) ? 0 : 1;
+  int64_t vectors = AHEAD * ADJUST_THREADS / rows;                      // of a row
+  const int64_t even = (V * B + 2 * sms - 1) / (2 * sms) / vec + 1;     // two blocks per SM
+  if (vectors > even) vectors = even;
+  if (vectors < 128) vectors = 128;
+  if (clusters && (vectors - spare) * vec > CLUSTER_SLICE) vectors = CLUSTER_SLICE / vec + spare;
+  const int64_t slice = (vectors - spare) * vec;
   int64_t slices = (V + slice - 1) / slice;
-  slices = (slices + p.cluster - 1) / p.cluster * p.cluster;
+  if (clusters) slices = (slices + CLUSTER - 1) / CLUSTER * CLUSTER;
   p.slice = (int)slice;
-  p.column = (int)column_of(slice);
-  const int64_t vectors = slice * size / 16 + 1;
-  p.inverse = (uint32_t)(((1ull << 32) + vectors - 1) / vectors);
+  p.vectors = (int)vectors;
+  p.vectors_inverse = (uint32_t)(((1ull << 32) + vectors - 1) / vectors);
   void* args[] = {&p};
-  return launch_step(adjust_fn(dtype), dim3((unsigned)slices, (unsigned)B, (unsigned)((T + ROWS - 1) / ROWS)),
-                     dim3(ADJUST_THREADS, 1, 1), (size_t)adjust_smem(slice, p.cluster), static_cast<cudaStream_t>(stream),
-                     args, (flags & QLIN_FLAG_PDL) != 0, p.cluster);
+  return launch_step(adjust_fn(dtype, clusters, kind), dim3((unsigned)slices, (unsigned)B, (unsigned)((T + ROWS - 1) / ROWS)),
+                     dim3(ADJUST_THREADS, 1, 1), (size_t)adjust_smem(slice, clusters ? CLUSTER : 1),
+                     static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0, clusters ? CLUSTER : 1);
 }
