@@ -9,14 +9,17 @@
 namespace qlin {
 namespace {
 
-constexpr int WEIGH_THREADS = 320;  // eight weighing warps, then the producer and the issuer
-constexpr int WEIGHING = 256, PRODUCER = 8, ISSUER = 9;
+constexpr int SETS = 4;             // of four weighing warps each, which take the tiles in turn
+constexpr int PRODUCERS = 2;        // warps that load tiles in turn
+constexpr int PRODUCER = 4 * SETS, ISSUER = PRODUCER + PRODUCERS;
+constexpr int WEIGHING = 128 * SETS, WEIGH_THREADS = WEIGHING + 32 * PRODUCERS + 32;
 constexpr int TILE = 128;           // tokens of a tile: the lanes of tensor memory
 constexpr int MAX_ROWS = 128;       // query rows of an item at most: columns of an accumulator
 constexpr int SLOT_BYTES = TILE * 128;  // a ring slot: a 64-wide panel of a tile's keys
 constexpr int MAX_SLOTS = 12, ACCUMULATORS = 4;
 constexpr int WEIGH_SMEM = 208 * 1024;
 constexpr int GAP = 1;              // work of a change to another item, in tiles
+constexpr uint32_t ALL = 0xFFFFFFFFu;
 constexpr float FAR = 0x1p23f;      // from here on fp32 scores (log2 units) are a step or more apart
 
 struct WeighParams {
@@ -52,8 +55,8 @@ struct WeighShared {
   uint32_t tmem;
   int dead;  // a wait has expired: every role leaves its loop
   Walk walk;
-  // of the item: per column the negative reference and the inverse sum of weights, and its kept row
-  __align__(16) float2 stat[MAX_ROWS];
+  // of the item: two columns' negative references and inverse sums of weights at a time, and a column's kept row
+  float4 stat[MAX_ROWS / 2];
   uint8_t row_of[MAX_ROWS];
   int kept[QLIN_MAX_TREE];       // the kept rows
   int own[QLIN_MAX_TREE];        // the step's row: its place among the kept ones, or -1
@@ -72,12 +75,21 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, WeighS
 __device__ __forceinline__ bool weighing_bar(bool ok) {
   uint32_t all;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 256, p;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(all)
-      : "r"((uint32_t)ok)
+      : "r"((uint32_t)ok), "n"(WEIGHING)
       : "memory");
   return all != 0;
+}
+// a * b + c on two numbers
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
 
 // The item's rows and what they see, by one warp.
@@ -151,42 +163,53 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
   Walk w = s->walk;
 
   if (w.left > 0) {
-    if (warp == PRODUCER) {
-      // ---- a lane per TMA copy: a page's or a tile's rows of a panel
-      const int copies = TILE / p.box;
-      uint32_t slot = 0, phase = 1, issued = 0;  // the first round finds every slot empty
+    if (warp >= PRODUCER && warp < ISSUER) {
+      // ---- a lane per TMA copy (a page's or a tile's rows of a panel), the
+      // producers' warps a tile each in turn: a warp's lanes issue their copies one
+      // after the other, of small pages too slowly for the memory
+      const int copies = TILE / p.box, box = lane % copies, panel = lane / copies;  // at most 8 and 4
+      const uint32_t slots = (uint32_t)p.slots, mine = (uint32_t)(warp - PRODUCER);
+      uint32_t i = mine * PANELS + panel, slot = i, phase = 1;  // this lane's next panel of the run, its place in the ring
+      uint32_t n = 0;                                           // tiles of the items before
       bool ok = true;
       do {
         const int32_t* table = p.step.page_table + w.b * p.step.table_stride;
-        int64_t token = w.tile * TILE + lane * p.box;
-        int next = lane < copies && token < w.tokens ? table[token >> p.page_shift] : -1;
-        for (int64_t t = 0; t < w.n && ok; t++, token += TILE) {
+        const int skip = (int)((mine + PRODUCERS - n % PRODUCERS) % PRODUCERS);  // tiles of the item before this warp's first
+        int64_t token = (w.tile + skip) * TILE + box * p.box;
+        auto page_of = [&](int64_t t, int64_t at) { return t < w.n && panel < PANELS && at < w.tokens ? table[at >> p.page_shift] : -1; };
+        int next = page_of(skip, token);
+        for (int64_t t = skip; t < w.n && ok; t += PRODUCERS, token += PRODUCERS * TILE) {
           int page = next;
-          if (lane < copies && token < w.tokens && (page < 0 || page >= p.cache.pages)) {
+          if (panel < PANELS && token < w.tokens && (page < 0 || page >= p.cache.pages)) {
             page = -1;
             report(p.status, QLIN_ERR_BAD_INDEX);
           }
-          next = t + 1 < w.n && lane < copies && token + TILE < w.tokens ? table[(token + TILE) >> p.page_shift] : -1;
-          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0)) * p.box * 128;
-#pragma unroll 1
-          for (int e = 0; e < PANELS; e++) {
-            if (issued >= (uint32_t)p.slots) ok = role_wait(&s->empty[slot], phase, s, p.status);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&s->full[slot], bytes);
-            __syncwarp();
-            const bool lost = FAULT && blockIdx.x == 0 && issued == p.fault_copy;  // test only: never completes
-            if (page >= 0 && !lost)
-              tma_load_4d(ring + slot * SLOT_BYTES + lane * p.box * 128, &p.map_k, e * 64,
-                          (int)(token & (p.cache.page_size - 1)), w.h, page, &s->full[slot]);
-            issued++;
-            if (++slot == (uint32_t)p.slots) slot = 0, phase ^= 1;
-          }
+          next = page_of(t + PRODUCERS, token + PRODUCERS * TILE);
+          if (i >= slots && panel < PANELS) ok = role_wait(&s->empty[slot], phase, s, p.status);
+          ok = __all_sync(ALL, ok);
+          if (!ok) break;
+          const uint32_t bytes = __popc(__ballot_sync(ALL, page >= 0 && panel == 0)) * p.box * 128;
+          if (box == 0 && panel < PANELS) mbar_arrive_expect_tx(&s->full[slot], bytes);
+          __syncwarp();
+          const bool lost = FAULT && blockIdx.x == 0 && i == p.fault_copy;  // test only: never completes
+          if (page >= 0 && !lost)
+            tma_load_4d(ring + slot * SLOT_BYTES + box * p.box * 128, &p.map_k, panel * 64,
+                        (int)(token & (p.cache.page_size - 1)), w.h, page, &s->full[slot]);
+          i += PRODUCERS * PANELS;
+          slot += PRODUCERS * PANELS;
+          if (slot >= slots) slot -= slots, phase ^= 1;
         }
+        n += (uint32_t)w.n;
       } while (ok && next_item<TILE, GAP>(p, w));
-      // nothing leaves while its copies are in flight, whichever role gave up
-      for (uint32_t j = issued > (uint32_t)p.slots ? issued - p.slots : 0; j < issued; j++)
-        (void)mbar_wait(&s->full[j % p.slots], j / p.slots & 1);
+      // nothing leaves while its copies are in flight, whichever role gave up: of
+      // the ring's last round, as what lies before that has been waited for
+      const uint32_t end = ok ? n * PANELS : i;
+      if (box == 0 && panel < PANELS)
+        for (uint32_t j = i; j >= PRODUCERS * PANELS;) {
+          j -= PRODUCERS * PANELS;
+          if (j + slots < end) break;
+          (void)mbar_wait(&s->full[j % slots], j / slots & 1);
+        }
     } else if (warp == ISSUER) {
       constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u;
       const uint32_t id = mma_idesc_f16(TILE, p.Rp) | type;
@@ -221,8 +244,8 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
         mma_commit(&s->drained);
         (void)mbar_wait(&s->drained, 0);
       }
-    } else {
-      // ---- weighing: two sets of four warps take the tiles in turn
+    } else if (warp < PRODUCER) {
+      // ---- weighing: sets of four warps take the tiles in turn
       const int tid = threadIdx.x, set = warp / 4;
       const int at = tid % TILE;  // this thread's token of a tile
       const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
@@ -238,15 +261,22 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
         for (int c = tid; c < cols; c += WEIGHING) {
           const int i = c / p.group, head = w.h * p.group + c % p.group;
           const float2 rl = p.stats[(row0 + s->kept[i]) * ((int64_t)p.group * p.cache.heads) + head];
-          s->stat[c] = rl.y == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(-rl.x, 1.f / rl.y);
+          float* st = reinterpret_cast<float*>(&s->stat[c / 2]) + c % 2;
+          st[0] = rl.y == 0.f ? -INFINITY : -rl.x;
+          st[2] = rl.y == 0.f ? 0.f : 1.f / rl.y;
           s->row_of[c] = (uint8_t)i;
           if (fabsf(rl.x) >= FAR && rl.y != 0.f) s->far = 1;
         }
-        for (int x = tid; x < cols * (D / 8); x += WEIGHING) {  // swizzled as the keys are by TMA
+        for (int c = cols + tid; c < p.Rp; c += WEIGHING) {  // columns that weigh nothing
+          float* st = reinterpret_cast<float*>(&s->stat[c / 2]) + c % 2;
+          st[0] = -INFINITY, st[2] = 0.f;
+        }
+        for (int x = tid; x < p.Rp * (D / 8); x += WEIGHING) {  // swizzled as the keys are by TMA
           const int c = x / (D / 8), u = x % (D / 8);
-          const T* src = static_cast<const T*>(p.q) + (row0 + s->kept[c / p.group]) * p.q_stride +
-                         (int64_t)(w.h * p.group + c % p.group) * D + u * 8;
-          const uint4 v = *reinterpret_cast<const uint4*>(src);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (c < cols)
+            v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (row0 + s->kept[c / p.group]) * p.q_stride +
+                                                (int64_t)(w.h * p.group + c % p.group) * D + u * 8);
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_smem + (u / 8) * panel_bytes + c * 128 +
                                                                         (((u & 7) ^ (c & 7)) << 4)),
                        "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
@@ -262,7 +292,7 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
         int32_t* position_out = p.position_out ? p.position_out + w.b * p.out_seq_stride + w.h * p.out_head_stride : nullptr;
 
         for (int t = 0; t < (int)w.n; t++, m++) {
-          if ((int)(m & 1) != set) continue;
+          if ((int)(m % SETS) != set) continue;
           const int64_t first = (w.tile + t) * TILE, token = first + at;
           const bool old = token < len && token < w.tokens;
           const int r = old || token >= w.tokens ? -1 : (int)(token - len), place = r >= 0 ? s->own[r] : -1;
@@ -275,27 +305,28 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
           if (!ok) break;
           tc_fence_after();
           const uint32_t from = tmem + lanes + acc * MAX_ROWS;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          float2 sum[4] = {};
           if (first + TILE <= len && !far) {  // every row sees every token
+            uint32_t x[32];  // 32 columns at a time
+            const float2 scale = make_float2(p.scale_log2, p.scale_log2);
+            auto add = [&](int c0, int c) {  // two columns
+              const float4 st = s->stat[(c0 + c) / 2];
+              const float2 e = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale, make_float2(st.x, st.y));
+              sum[c / 2 & 3] = fma2(make_float2(exp2_approx(e.x), exp2_approx(e.y)), make_float2(st.z, st.w), sum[c / 2 & 3]);
+            };
 #pragma unroll 1
-            for (int c0 = 0; c0 < cols; c0 += 16) {
-              uint32_t x[16];
-              tmem_ld16(from + c0, x);
+            for (int c0 = 0; c0 < p.Rp; c0 += 32) {
+              const bool half = p.Rp - c0 < 32;
+              if (half)
+                tmem_ld16(from + c0, *reinterpret_cast<uint32_t(*)[16]>(x));
+              else
+                tmem_ld32(from + c0, x);
               tmem_wait_ld();
-              if (c0 + 16 <= cols) {
 #pragma unroll
-                for (int c = 0; c < 16; c++) {
-                  const float2 st = s->stat[c0 + c];
-                  sum[c & 3] = fmaf(exp2_approx(fmaf(__uint_as_float(x[c]), p.scale_log2, st.x)), st.y, sum[c & 3]);
-                }
-              } else {
+              for (int c = 0; c < 16; c += 2) add(c0, c);
+              if (half) break;
 #pragma unroll
-                for (int c = 0; c < 16; c++)
-                  if (c0 + c < cols) {
-                    const float2 st = s->stat[c0 + c];
-                    sum[c & 3] = fmaf(exp2_approx(fmaf(__uint_as_float(x[c]), p.scale_log2, st.x)), st.y, sum[c & 3]);
-                  }
-              }
+              for (int c = 16; c < 32; c += 2) add(c0, c);
             }
           } else {
             // A reference far out comes from a rounded product: the scores are rounded
@@ -309,13 +340,13 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
 #pragma unroll
               for (int c = 0; c < 16; c++)
                 if (c0 + c < cols && seen >> s->row_of[c0 + c] & 1) {
-                  const float2 st = s->stat[c0 + c];
-                  const float v = __uint_as_float(x[c]);
+                  const float4 st = s->stat[(c0 + c) / 2];
+                  const float v = __uint_as_float(x[c]), shift = c & 1 ? st.y : st.x, inv = c & 1 ? st.w : st.z;
                   if (far) {
-                    const float e = exp2_approx(__fmul_rn(v, p.scale_log2) + st.x) * st.y;
-                    sum[c & 3] += e > 1.f ? 1.f : e;
+                    const float e = exp2_approx(__fmul_rn(v, p.scale_log2) + shift) * inv;
+                    sum[c & 3].x += e > 1.f ? 1.f : e;
                   } else {
-                    sum[c & 3] = fmaf(exp2_approx(fmaf(v, p.scale_log2, st.x)), st.y, sum[c & 3]);
+                    sum[c & 3].x = fmaf(exp2_approx(fmaf(v, p.scale_log2, shift)), inv, sum[c & 3].x);
                   }
                 }
             }
@@ -323,7 +354,7 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s->acc_free[acc]);
-          const float weight = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          const float weight = ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
           if (here) {
             score_out[to] = old ? fmaf(p.decay, before, weight) : weight;
             if (!old && position_out) {
@@ -403,7 +434,7 @@ qlin_status weigh(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, 
   st = check_status_ws(ws, ws_bytes);
   if (st != QLIN_OK) return st;
   if (step->B == 0 || step->T == 0) return QLIN_OK;
-  const int64_t B = step->B, D = cache->width, n = B * step->T;
+  const int64_t B = step->B, D = cache->width;
   if (!rows_ok(q, q_stride, Hq * D, 2) || !stats || !is_aligned(stats, 8) || !score || !score_out) return QLIN_ERR_INVALID_ARG;
   for (const void* x : {(const void*)keep, (const void*)n_keep, (const void*)at, (const void*)score, (const void*)score_out,
                         (const void*)position_out})
