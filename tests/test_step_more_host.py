@@ -62,8 +62,10 @@ def adjust(so, /, B=2, T=3, V=1000, dtype=2, logits=1 << 20, ld=1000, out=1 << 2
     a = dict(history=4096, history_len=None, prompt_len=None, draft=4096, mask=None, repetition=4096, presence=None, frequency=None,
              bias_token=4096, bias=4096, allowed=4096, history_stride=50, tree_stride=0, bias_stride=0, allowed_stride=32, L=50, n_bias=9)
     a.update(kw)
-    s = qlin._AdjustStruct(**a)
-    return so.qlin_adjust_logits(B, T, V, dtype, logits, ld, out, old, ctypes.addressof(s) if struct else None, flags, None)
+    s = qlin._ADJUSTMENTS.pack(*[a[n] or 0 for n in (
+        "history", "history_len", "prompt_len", "draft", "mask", "repetition", "presence", "frequency", "bias_token", "bias",
+        "allowed", "history_stride", "tree_stride", "bias_stride", "allowed_stride", "L", "n_bias")])
+    return so.qlin_adjust_logits(B, T, V, dtype, logits, ld, out, old, s if struct else None, flags, None)
 
 
 @pytest.mark.parametrize("bad", [

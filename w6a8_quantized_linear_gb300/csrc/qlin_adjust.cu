@@ -10,6 +10,7 @@ namespace qlin {
 namespace {
 
 constexpr int ADJUST_THREADS = 512;
+constexpr int BLOCKS = 2;             // per SM
 constexpr int AHEAD = 4;              // vectors of 16 bytes in flight per thread
 constexpr int HISTORY_AHEAD = 8;      // tokens of the history in flight per thread
 constexpr int FIXES_AHEAD = 4;        // changed logits in flight per thread
@@ -61,13 +62,13 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { re
 // One block per sequence, slice of the vocabulary and (at most 32 of its) rows.  The
 // slice's words are formed first, from the whole history, and with them a list of
 // the tokens that they concern, few of the slice's as a rule.  The rows' slices
-// are copied in 16-byte vectors on their own alignment, loaded before all that and
-// stored without what is forbidden, and then the listed tokens' logits are written,
-// a thread each: looked for within the vectors they cost a warp its time wherever
-// one lane has one.  A long history is read once per cluster: each block counts a
+// are copied meanwhile, in 16-byte vectors on their own alignment and without what
+// is forbidden, and in the end the listed tokens' logits are written, a thread
+// each: looked for within the vectors they cost a warp its time wherever one lane
+// has one.  A long history is read once per cluster: each block counts a
 // part of it for all slices of the cluster, and adds up its own slice's counts.
 template <typename T, bool CLUSTERS, Rows KIND>
-__global__ void __launch_bounds__(ADJUST_THREADS, 2) qlin_adjust_kernel(const __grid_constant__ AdjustParams p) {
+__global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(const __grid_constant__ AdjustParams p) {
   constexpr int VEC = 16 / sizeof(T), C = CLUSTERS ? CLUSTER : 1;
   constexpr bool DRAFTS = KIND == Rows::DRAFTED, ONE = KIND == Rows::ONE;
   extern __shared__ __align__(16) uint32_t shared[];  // words of the cluster's slices, the list of this one
@@ -131,6 +132,36 @@ __global__ void __launch_bounds__(ADJUST_THREADS, 2) qlin_adjust_kernel(const __
   };
   load(tid);
 
+  // ---- the rows, without what is forbidden (as the words below do not concern them)
+  auto copy = [&] {
+    const T forbidden = from_float<T>(-INFINITY);
+    if (!p.in_place || a.allowed) {
+#pragma unroll 1
+      for (int i0 = tid; i0 < total; i0 += AHEAD * ADJUST_THREADS) {
+        if (i0 != tid) load(i0);
+#pragma unroll
+        for (int u = 0; u < AHEAD; u++) {
+          const Vector v = vector(i0 + u * ADJUST_THREADS);
+          if (v.lo >= v.hi || (p.in_place && open[u] == 0xFFFFFFFFu)) continue;
+          if (v.whole) {
+            if (p.in_place) x[u] = *reinterpret_cast<const uint4*>(v.src + v.lo);
+            if (open[u] != 0xFFFFFFFFu) {
+              T z[VEC];
+              *reinterpret_cast<uint4*>(z) = x[u];
+#pragma unroll
+              for (int e = 0; e < VEC; e++)
+                if (!(open[u] >> e & 1)) z[e] = forbidden;
+              x[u] = *reinterpret_cast<const uint4*>(z);
+            }
+            *reinterpret_cast<uint4*>(v.dst + v.lo) = x[u];
+          } else {
+            for (int e = 0; e < v.hi - v.lo; e++) v.dst[v.lo + e] = open[u] >> e & 1 ? v.src[v.lo + e] : forbidden;
+          }
+        }
+      }
+    }
+  };
+
   // ---- the words and their list
   bool any_draft = false;
   int fixes = 0;
@@ -146,6 +177,7 @@ __global__ void __launch_bounds__(ADJUST_THREADS, 2) qlin_adjust_kernel(const __
     if (tid == 0) listed = 0;
     auto clear = [&] {
       for (int i = tid; i < C * S / 4; i += ADJUST_THREADS) reinterpret_cast<uint4*>(shared)[i] = make_uint4(0, 0, 0, 0);
+      copy();
       __syncthreads();
     };
     if (counts) {
@@ -263,6 +295,8 @@ __global__ void __launch_bounds__(ADJUST_THREADS, 2) qlin_adjust_kernel(const __
     if (a.n_bias || DRAFTS)
       any_draft = __syncthreads_or(DRAFTS && tid < p.T && draft[tid] >= 0 && (uint32_t)(draft[tid] - v0) < (uint32_t)n);
     fixes = counts || a.n_bias ? listed * rows : 0;
+  } else {
+    copy();
   }
   Penalties value = {1.f, 0.f, 0.f};
   if (a.repetition) value.r = a.repetition[b];
@@ -294,8 +328,8 @@ __global__ void __launch_bounds__(ADJUST_THREADS, 2) qlin_adjust_kernel(const __
   }
 
   // Changed logits, FIXES_AHEAD of them at once: their logits and whether they are
-  // allowed, then their values.  (What is stored in between leaves allowed logits
-  // as they are, also in place.)
+  // allowed, then their values.  (The copy has left allowed logits as they were,
+  // also in place.)
   float y[FIXES_AHEAD];
   uint32_t stands = 0;
   const uint32_t per_row = fixes ? (uint32_t)listed : 1u, per_row_inverse = ONE ? 0u : 0xFFFFFFFFu / per_row + 1;
@@ -325,45 +359,12 @@ __global__ void __launch_bounds__(ADJUST_THREADS, 2) qlin_adjust_kernel(const __
       static_cast<T*>(p.out)[(row0 + t) * p.out_ld + v0 + at] = from_float<T>(value(y[k], words[at], 0, bias));
     }
   };
-  fetch(tid);
-
-  // ---- the rows
-  const T forbidden = from_float<T>(-INFINITY);
-  if (!p.in_place || a.allowed) {
-#pragma unroll 1
-    for (int i0 = tid; i0 < total; i0 += AHEAD * ADJUST_THREADS) {
-      if (i0 != tid) load(i0);
-#pragma unroll
-      for (int u = 0; u < AHEAD; u++) {
-        const Vector v = vector(i0 + u * ADJUST_THREADS);
-        if (v.lo >= v.hi || (p.in_place && open[u] == 0xFFFFFFFFu)) continue;
-        if (v.whole) {
-          if (p.in_place) x[u] = *reinterpret_cast<const uint4*>(v.src + v.lo);
-          if (open[u] != 0xFFFFFFFFu) {
-            T z[VEC];
-            *reinterpret_cast<uint4*>(z) = x[u];
-#pragma unroll
-            for (int e = 0; e < VEC; e++)
-              if (!(open[u] >> e & 1)) z[e] = forbidden;
-            x[u] = *reinterpret_cast<const uint4*>(z);
-          }
-          *reinterpret_cast<uint4*>(v.dst + v.lo) = x[u];
-        } else {
-          for (int e = 0; e < v.hi - v.lo; e++) v.dst[v.lo + e] = open[u] >> e & 1 ? v.src[v.lo + e] : forbidden;
-        }
-      }
-    }
-  }
-
   // ---- what changes
-  if (fixes) {
-    __syncthreads();
-    settle(tid);
+  if (DRAFTS && any_draft && p.in_place) __syncthreads();
 #pragma unroll 1
-    for (int i0 = tid + FIXES_AHEAD * ADJUST_THREADS; i0 < fixes; i0 += FIXES_AHEAD * ADJUST_THREADS) {
-      fetch(i0);
-      settle(i0);
-    }
+  for (int i0 = tid; i0 < fixes; i0 += FIXES_AHEAD * ADJUST_THREADS) {
+    fetch(i0);
+    settle(i0);
   }
   if (DRAFTS && any_draft) {
     __syncthreads();
@@ -457,17 +458,23 @@ extern "C" qlin_status qlin_adjust_logits(int B, int T, int64_t V, int dtype, co
   const bool clusters = a.history && a.L > LONG_HISTORY && V > 4096;
   const Rows kind = a.draft ? Rows::DRAFTED : T > 1 ? Rows::SEVERAL : Rows::ONE;
   p.history_vectors = a.history && is_aligned(a.history, 16) && a.L % 4 == 0 && (B == 1 || a.history_stride % 4 == 0);
-  // A thread's vectors of a block: AHEAD, or fewer where that leaves SMs idle.  Rows
-  // off the 16-byte grid take one vector more than their slice has.
-  const int64_t vec = 16 / size, rows = T < ROWS ? T : ROWS;
+  // A thread's vectors of a block: AHEAD, or fewer where that leaves SMs idle; then
+  // as many as make the blocks fill whole rounds of the SMs.  Rows off the 16-byte
+  // grid take one vector more than their slice has.
+  const int64_t vec = 16 / size, rows = T < ROWS ? T : ROWS, groups = B * ((T + ROWS - 1) / ROWS);
   const int64_t spare = is_aligned(logits, 16) && (M == 1 || ld % vec == 0) ? 0 : 1;
-  int64_t vectors = AHEAD * ADJUST_THREADS / rows;                      // of a row
-  const int64_t even = (V * B + 2 * sms - 1) / (2 * sms) / vec + 1;     // two blocks per SM
-  if (vectors > even) vectors = even;
-  if (vectors < 128) vectors = 128;
+  const int64_t round = BLOCKS * sms;
+  int64_t vectors = AHEAD * ADJUST_THREADS / rows;  // of a row, at most
   if (clusters && (vectors - spare) * vec > CLUSTER_SLICE) vectors = CLUSTER_SLICE / vec + spare;
+  int64_t slices = (V + (vectors - spare) * vec - 1) / ((vectors - spare) * vec);
+  const int64_t rounds = (slices * groups + round - 1) / round;
+  slices = rounds * round / groups;  // at least as many
+  if (clusters) slices = (slices + CLUSTER - 1) / CLUSTER * CLUSTER;
+  const int64_t least = (V + slices * vec - 1) / (slices * vec) + spare;
+  if (vectors > least) vectors = least;
+  if (vectors < 128) vectors = 128;
   const int64_t slice = (vectors - spare) * vec;
-  int64_t slices = (V + slice - 1) / slice;
+  slices = (V + slice - 1) / slice;
   if (clusters) slices = (slices + CLUSTER - 1) / CLUSTER * CLUSTER;
   p.slice = (int)slice;
   p.vectors = (int)vectors;

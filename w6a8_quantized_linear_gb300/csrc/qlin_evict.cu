@@ -85,7 +85,7 @@ __device__ __forceinline__ uint2 staying(uint4 c, uint32_t before, uint32_t ties
 // bits down, 11 at a time: a histogram per block, added into the bins' owners,
 // and read by all; where a whole bin stays, what lies below need not be looked at.
 template <int K>
-__global__ void __launch_bounds__(SELECT_THREADS) qlin_evict_select_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 2) qlin_evict_select_kernel(const __grid_constant__ EvictParams p) {
   __shared__ SelectShared sh;
   SelectShared* s = &sh;
   const int C = p.cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -98,7 +99,7 @@ def lib() -> ctypes.CDLL:
                                        ctypes.c_uint, vp]),
                 "qlin_debug_sample_plan": (st, [i64, i64, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
                 "qlin_debug_sample_weight": (st, [i32, vp, vp, vp, vp]),
-                "qlin_adjust_logits": (st, [i32, i32, i64, i32, vp, i64, vp, i64, vp, ctypes.c_uint, vp]),
+                "qlin_adjust_logits": (st, [i32, i32, i64, i32, vp, i64, vp, i64, ctypes.c_char_p, ctypes.c_uint, vp]),
                 "qlin_sample": (st, [i32, i64, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint, vp]),
             }
             for name, (res, args) in sig.items():
@@ -522,7 +523,7 @@ def _heads(t, width: int, what: str) -> int:
 def _floats(t, n: int, what: str):
     if t is None:
         return None
-    if t.dtype is not _F32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _F32 or t.numel() != n or (n > 1 and not t.is_contiguous()):
         raise ValueError(f"{what} must be a contiguous float32 tensor of {n} values")
     return t.data_ptr()
 
@@ -530,7 +531,7 @@ def _floats(t, n: int, what: str):
 def _ints(t, n: int, what: str):
     if t is None:
         return None
-    if t.dtype is not _I32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _I32 or t.numel() != n or (n > 1 and not t.is_contiguous()):
         raise ValueError(f"{what} must be a contiguous int32 tensor of {n} values")
     return t.data_ptr()
 
@@ -611,14 +612,16 @@ def kv_append(cache: KVCache, step: KVStep, q=None, k=None, v=None, q_gamma=None
             raise ValueError("axis names axes of position, which is not given")
         status = _fn("qlin_kv_append")(*head, *tail)
     else:
-        axes = position.shape[1] if position.dim() == 2 else 1
-        if position.dtype is not _I32 or position.shape[:1] != (n,) or position.dim() > 2 or (
-                axes > 1 and position.stride(1) != 1):
+        shape = position.shape
+        axes = shape[1] if len(shape) == 2 else 1
+        whole = position.is_contiguous()
+        if position.dtype is not _I32 or not 1 <= len(shape) <= 2 or shape[0] != n or (
+                not whole and axes > 1 and position.stride(1) != 1):
             raise ValueError(f"position must be an int32 tensor of [{n}] or [{n}, axes] with contiguous rows")
         if axis is not None and (type(axis) is not bytes or len(axis) != nt):
             raise ValueError("axis must come from rope_axes, one entry for each of turns")
-        status = _fn("qlin_kv_append_at")(*head, position.data_ptr(), position.stride(0) if n > 1 else axes, axes, axis,
-                                          *tail)
+        status = _fn("qlin_kv_append_at")(*head, position.data_ptr(), axes if whole or n < 2 else position.stride(0), axes,
+                                          axis, *tail)
     if status:
         _check(status, "kv_append")
     return q_out
@@ -699,8 +702,12 @@ def kv_keep(cache: KVCache, step: KVStep, keep: torch.Tensor, n_keep: torch.Tens
 
 def _scores(t, shape, dtype, what: str) -> tuple[int, int]:
     """Strides of a [B, heads, room] tensor of ``dtype``, its tokens contiguous."""
-    if t.shape != shape or t.dtype is not dtype or (shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{what} must be a {dtype} tensor of {list(shape)} with contiguous tokens")
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{what} must be a {dtype} tensor of {list(shape)}")
+    if t.is_contiguous():
+        return shape[1] * shape[2], shape[2]
+    if shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"the tokens of {what} must be contiguous")
     return t.stride(0) if shape[0] > 1 else shape[1] * shape[2], t.stride(1) if shape[1] > 1 else shape[2]
 
 
@@ -822,20 +829,20 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     return token
 
 
-class _AdjustStruct(ctypes.Structure):  # qlin_adjustments
-    _fields_ = [(n, ctypes.c_void_p) for n in ("history", "history_len", "prompt_len", "draft", "mask", "repetition", "presence",
-                                               "frequency", "bias_token", "bias", "allowed")] + [
-        (n, ctypes.c_int64) for n in ("history_stride", "tree_stride", "bias_stride", "allowed_stride")] + [
-        (n, ctypes.c_int32) for n in ("L", "n_bias")]
+# qlin_adjustments: eleven addresses, four strides, L and n_bias; packed, as that costs a call less than setting fields
+_ADJUSTMENTS = struct.Struct("@11P4q2i")
 
 
 def _table(t, rows: int, dtype, what: str) -> tuple[int, int]:
     """Width and row stride of a [rows, width] tensor of ``dtype``, or of [width] for all rows (stride 0)."""
-    if t.dtype is not dtype or not 1 <= t.dim() <= 2 or (t.dim() == 2 and t.shape[0] != rows) or (
-            t.shape[-1] > 1 and t.stride(-1) != 1):
+    shape = t.shape
+    if t.dtype is dtype and len(shape) == 2 and shape[0] == rows and t.is_contiguous():
+        return shape[1], shape[1]
+    if t.dtype is not dtype or not 1 <= len(shape) <= 2 or (len(shape) == 2 and shape[0] != rows) or (
+            shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{what} must be a {dtype} tensor of {rows} contiguous rows, or of one row for all")
-    n = t.shape[-1]
-    return n, 0 if t.dim() == 1 else t.stride(0) if rows > 1 else max(n, 1)
+    n = shape[-1]
+    return n, 0 if len(shape) == 1 else t.stride(0) if rows > 1 else n
 
 
 def adjust_logits(logits: torch.Tensor, out=None, history=None, history_len=None, prompt_len=None, draft=None, mask=None,
@@ -854,61 +861,76 @@ def adjust_logits(logits: torch.Tensor, out=None, history=None, history_len=None
     ``allowed`` int32 [B * T, ceil(V / 32)] or [ceil(V / 32)]: a bit per token,
     the others become -inf.  B is the rows of history, draft, or a penalty; else
     of bias_token; without any of these, each row is its own sequence."""
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
-        raise ValueError("logits must be [B * T, V] with contiguous rows")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [B * T, V]")
     M, V = logits.shape
+    ld = V
+    if not logits.is_contiguous():
+        if logits.stride(1) != 1 and V > 1:
+            raise ValueError("logits must have contiguous rows")
+        ld = logits.stride(0) if M > 1 else V
     dev = logits.get_device()
-    _same_device(dev, out, history, history_len, prompt_len, draft, mask, repetition, presence, frequency, bias_token, bias,
-                 allowed)
+    _same_device(dev, *[t for t in (out, history, history_len, prompt_len, draft, mask, repetition, presence, frequency, bias_token,
+                                    bias, allowed) if t is not None])
     B = M
     for t in (history, draft, history_len, prompt_len, repetition, presence, frequency):
         if t is not None:
-            B = t.shape[0] if t.dim() else 0
+            B = len(t) if t.dim() else 0
             break
     else:
         if bias_token is not None and bias_token.dim() == 2:
-            B = bias_token.shape[0]
+            B = len(bias_token)
     if (B < 1 or M % B) if M else B != 0:
         raise ValueError(f"{M} rows of logits do not belong to {B} sequences")
     T = M // B if B else 0
-    a = _AdjustStruct()
+    L = history_stride = tree_stride = n_bias = bias_stride = allowed_stride = 0
+    at_history = at_draft = at_mask = at_token = at_bias = at_allowed = 0
     if history is not None:
         if history.dim() != 2:
             raise ValueError("history must be [B, L]")
-        a.L, a.history_stride = _table(history, B, _I32, "history")
-        a.history = history.data_ptr()
-    a.history_len, a.prompt_len = _ints(history_len, B, "history_len"), _ints(prompt_len, B, "prompt_len")
+        L, history_stride = _table(history, B, _I32, "history")
+        at_history = history.data_ptr()
     if draft is not None:
         if draft.shape != (B, T):
             raise ValueError("draft must be [B, T]")
-        a.draft = _ints(draft, M, "draft")
+        at_draft = _ints(draft, M, "draft")
         if mask is not None:
             if mask.dtype is not _I32 or mask.shape not in ((T,), (B, T)) or not mask.is_contiguous():
                 raise ValueError("mask must be a contiguous int32 [T] or [B, T] tensor")
-            a.mask, a.tree_stride = mask.data_ptr(), T if mask.dim() == 2 else 0
+            at_mask, tree_stride = mask.data_ptr(), T if mask.dim() == 2 else 0
     elif mask is not None:
         raise ValueError("mask names rows of draft, which is not given")
-    a.repetition, a.presence = _floats(repetition, B, "repetition"), _floats(presence, B, "presence")
-    a.frequency = _floats(frequency, B, "frequency")
     if (bias_token is None) != (bias is None):
         raise ValueError("bias_token and bias are given together")
     if bias is not None:
-        a.n_bias, a.bias_stride = _table(bias_token, B, _I32, "bias_token")
-        if bias.shape != bias_token.shape or _table(bias, B, _F32, "bias") != (a.n_bias, a.bias_stride):
+        n_bias, bias_stride = _table(bias_token, B, _I32, "bias_token")
+        if bias.shape != bias_token.shape or _table(bias, B, _F32, "bias") != (n_bias, bias_stride):
             raise ValueError("bias must have the shape and strides of bias_token")
-        a.bias_token, a.bias = bias_token.data_ptr(), bias.data_ptr()
+        at_token, at_bias = bias_token.data_ptr(), bias.data_ptr()
     if allowed is not None:
-        words, a.allowed_stride = _table(allowed, M, _I32, "allowed")
+        words, allowed_stride = _table(allowed, M, _I32, "allowed")
         if words < (V + 31) // 32:
             raise ValueError("allowed must have a bit for each token")
-        a.allowed = allowed.data_ptr()
+        at_allowed = allowed.data_ptr()
+    packed = _ADJUSTMENTS.pack(
+        at_history, _ints(history_len, B, "history_len") or 0, _ints(prompt_len, B, "prompt_len") or 0, at_draft, at_mask,
+        _floats(repetition, B, "repetition") or 0, _floats(presence, B, "presence") or 0,
+        _floats(frequency, B, "frequency") or 0, at_token, at_bias, at_allowed, history_stride, tree_stride, bias_stride,
+        allowed_stride, L, n_bias)
+    out_ld = V
     if out is None:
         out = _empty((M, V), logits.dtype, logits.device, stream)
-    elif out.shape != logits.shape or out.dtype != logits.dtype or (out.stride(1) != 1 and V > 1):
-        raise ValueError("out must have the shape and type of logits, with contiguous rows")
-    status = _fn("qlin_adjust_logits")(B, T, V, DTYPES.get(logits.dtype, -1), logits.data_ptr(),
-                                       logits.stride(0) if M > 1 else V, out.data_ptr(), out.stride(0) if M > 1 else V,
-                                       ctypes.addressof(a), flags, _raw_stream(stream, dev))
+    elif out is logits:
+        out_ld = ld
+    else:
+        if out.dtype is not logits.dtype or out.shape != (M, V):
+            raise ValueError("out must have the shape and type of logits")
+        if not out.is_contiguous():
+            if out.stride(1) != 1 and V > 1:
+                raise ValueError("out must have contiguous rows")
+            out_ld = out.stride(0) if M > 1 else V
+    status = _fn("qlin_adjust_logits")(B, T, V, DTYPES.get(logits.dtype, -1), logits.data_ptr(), ld,
+                                       out.data_ptr(), out_ld, packed, flags, _current_stream(dev) if stream is None else _raw_stream(stream, dev))
     if status:
         _check(status, "adjust_logits")
     return out
