@@ -14,9 +14,9 @@ constexpr int BLOCKS = 2;             // per SM
 constexpr int AHEAD = 4;              // vectors of 16 bytes in flight per thread
 constexpr int HISTORY_AHEAD = 8;      // tokens of the history in flight per thread
 constexpr int FIXES_AHEAD = 4;        // changed logits in flight per thread
-constexpr int CLUSTER = 8;            // blocks that share the reading of a long history
+constexpr int CLUSTER = 4;            // blocks that share the reading of a long history
 constexpr int LONG_HISTORY = 4096;
-constexpr int CLUSTER_SLICE = 2048;   // tokens of a block of theirs at most: each counts for all eight
+constexpr int CLUSTER_SLICE = 2048;   // tokens of a block of theirs at most: each counts for all of them
 constexpr int ROWS = QLIN_MAX_TREE;   // rows of a block at most
 constexpr int MAX_PAIRS = ROWS * ROWS / ADJUST_THREADS;
 
@@ -35,6 +35,7 @@ struct AdjustParams {
   int vectors;              // of a row's slice, on the row's alignment
   uint32_t vectors_inverse; // 2^32 / vectors, rounded up
   bool in_place, history_vectors;
+  bool aligned;             // every row of both on the 16-byte grid
 };
 
 // One row per sequence, several, or a tree's drafted ones.
@@ -119,6 +120,10 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
   };
   uint4 x[AHEAD];
   uint32_t open[AHEAD];  // allowed tokens
+  const T* const src = static_cast<const T*>(p.logits) + row0 * p.ld + v0;
+  T* const dst = static_cast<T*>(p.out) + row0 * p.out_ld + v0;
+  const T forbidden = from_float<T>(-INFINITY);
+  const bool plain = ONE && p.aligned && !a.allowed, idle = p.in_place && !a.allowed;
   auto load = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < AHEAD; u++) {
@@ -130,33 +135,44 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
       if (v.whole && !p.in_place && open[u] != behind) x[u] = *reinterpret_cast<const uint4*>(v.src + v.lo);
     }
   };
-  load(tid);
+  if (plain && !idle) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; u++)
+      if (tid + u * ADJUST_THREADS < n / VEC) x[u] = reinterpret_cast<const uint4*>(src)[tid + u * ADJUST_THREADS];
+  } else if (!idle) {
+    load(tid);
+  }
 
   // ---- the rows, without what is forbidden (as the words below do not concern them)
   auto copy = [&] {
-    const T forbidden = from_float<T>(-INFINITY);
-    if (!p.in_place || a.allowed) {
+    if (idle) return;
+    if (plain) {  // at most AHEAD vectors a thread
+#pragma unroll
+      for (int u = 0; u < AHEAD; u++)
+        if (tid + u * ADJUST_THREADS < n / VEC) reinterpret_cast<uint4*>(dst)[tid + u * ADJUST_THREADS] = x[u];
+      if (tid < n % VEC) dst[n / VEC * VEC + tid] = src[n / VEC * VEC + tid];
+      return;
+    }
 #pragma unroll 1
-      for (int i0 = tid; i0 < total; i0 += AHEAD * ADJUST_THREADS) {
-        if (i0 != tid) load(i0);
+    for (int i0 = tid; i0 < total; i0 += AHEAD * ADJUST_THREADS) {
+      if (i0 != tid) load(i0);
 #pragma unroll
-        for (int u = 0; u < AHEAD; u++) {
-          const Vector v = vector(i0 + u * ADJUST_THREADS);
-          if (v.lo >= v.hi || (p.in_place && open[u] == 0xFFFFFFFFu)) continue;
-          if (v.whole) {
-            if (p.in_place) x[u] = *reinterpret_cast<const uint4*>(v.src + v.lo);
-            if (open[u] != 0xFFFFFFFFu) {
-              T z[VEC];
-              *reinterpret_cast<uint4*>(z) = x[u];
+      for (int u = 0; u < AHEAD; u++) {
+        const Vector v = vector(i0 + u * ADJUST_THREADS);
+        if (v.lo >= v.hi || (p.in_place && open[u] == 0xFFFFFFFFu)) continue;
+        if (v.whole) {
+          if (p.in_place) x[u] = *reinterpret_cast<const uint4*>(v.src + v.lo);
+          if (open[u] != 0xFFFFFFFFu) {
+            T z[VEC];
+            *reinterpret_cast<uint4*>(z) = x[u];
 #pragma unroll
-              for (int e = 0; e < VEC; e++)
-                if (!(open[u] >> e & 1)) z[e] = forbidden;
-              x[u] = *reinterpret_cast<const uint4*>(z);
-            }
-            *reinterpret_cast<uint4*>(v.dst + v.lo) = x[u];
-          } else {
-            for (int e = 0; e < v.hi - v.lo; e++) v.dst[v.lo + e] = open[u] >> e & 1 ? v.src[v.lo + e] : forbidden;
+            for (int e = 0; e < VEC; e++)
+              if (!(open[u] >> e & 1)) z[e] = forbidden;
+            x[u] = *reinterpret_cast<const uint4*>(z);
           }
+          *reinterpret_cast<uint4*>(v.dst + v.lo) = x[u];
+        } else {
+          for (int e = 0; e < v.hi - v.lo; e++) v.dst[v.lo + e] = open[u] >> e & 1 ? v.src[v.lo + e] : forbidden;
         }
       }
     }
@@ -181,64 +197,55 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
       __syncthreads();
     };
     if (counts) {
-      // four consecutive tokens at a time where that can be, HISTORY_AHEAD on their way
+      // a thread takes four tokens in a row, HISTORY_AHEAD on their way
       const int32_t* h = a.history + b * a.history_stride;
       int token[HISTORY_AHEAD], L = a.L, prompt = 0;
-      constexpr int QUADS = HISTORY_AHEAD / 4, STEP = C * ADJUST_THREADS;
-      const int h0 = rank * ADJUST_THREADS + tid;
-      auto at_of = [&](int r, int u) {  // place in the history of token u of round r
-        return p.history_vectors ? ((r * QUADS + u / 4) * STEP + h0) * 4 + u % 4 : (r * HISTORY_AHEAD + u) * STEP + h0;
-      };
-      auto read = [&](int r) {
+      constexpr int ROUND = C * ADJUST_THREADS * HISTORY_AHEAD;
+      auto ahead = [](int u) { return u / 4 * (C * ADJUST_THREADS * 4) + u % 4; };
+      int h0 = (rank * ADJUST_THREADS + tid) * 4;  // this thread's first token of the round
+      auto read = [&] {
         if (p.history_vectors) {
 #pragma unroll
           for (int u = 0; u < HISTORY_AHEAD; u += 4) {
-            const int i = at_of(r, u);
-            const int4 q = i < a.L ? *reinterpret_cast<const int4*>(h + i) : make_int4(-1, -1, -1, -1);
+            const int4 q = h0 + ahead(u) < a.L ? *reinterpret_cast<const int4*>(h + h0 + ahead(u)) : make_int4(-1, -1, -1, -1);
             token[u] = q.x, token[u + 1] = q.y, token[u + 2] = q.z, token[u + 3] = q.w;
           }
         } else {
 #pragma unroll
-          for (int u = 0; u < HISTORY_AHEAD; u++) token[u] = at_of(r, u) < a.L ? h[at_of(r, u)] : -1;
+          for (int u = 0; u < HISTORY_AHEAD; u++) token[u] = h0 + ahead(u) < a.L ? h[h0 + ahead(u)] : -1;
         }
       };
-      read(0);
+      read();
       if (a.history_len) L = max(0, min(a.history_len[b], L));
       if (a.prompt_len) prompt = a.prompt_len[b];
       clear();
       const int base = v0 - rank * S;
-      uint16_t* queue = queues[tid >> 5];
-      const uint32_t below = (1u << (tid & 31)) - 1;
       const uint32_t range = CLUSTERS ? (uint32_t)min(C * S, V - base) : (uint32_t)n;
+      uint16_t* queue = queues[tid >> 5] + (tid & 31);
 #pragma unroll 1
-      for (int r = 0; r * HISTORY_AHEAD * STEP < L; r++) {
-        if (r) read(r);
-        // what concerns these slices goes through a queue of the warp, so that few
-        // lanes with something to count do not hold up the others time and again
+      for (int r0 = 0; r0 < L; r0 += ROUND, h0 += ROUND) {
+        if (r0) read();
+        // What concerns these slices goes through a queue per lane: few of a warp's
+        // lanes with something to count do not hold up the others token by token.
         int queued = 0;
 #pragma unroll
         for (int u = 0; u < HISTORY_AHEAD; u++) {
           const uint32_t at = (uint32_t)(token[u] - base);  // (a token below 0: far above)
-          const int i = at_of(r, u);
-          const bool hit = at < range && i < L;
-          const uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit);
-          if (hit) queue[queued + __popc(hits & below)] = (uint16_t)(at | (i < prompt ? 0x8000u : 0u));
-          queued += __popc(hits);
+          if (at < range && ahead(u) < L - h0) queue[32 * queued++] = (uint16_t)(at | (ahead(u) < prompt - h0 ? 0x8000u : 0u));
         }
-        __syncwarp();
-        for (int i = tid & 31; i < queued; i += 32) {
-          const uint32_t e = queue[i], at = e & 0x7FFF;
-          uint32_t* word = CLUSTERS ? &shared[at] : &words[at];
+        const int most = __reduce_max_sync(0xFFFFFFFFu, queued);
+        for (int i = 0; i < most; i++) {
+          if (i >= queued) continue;
+          const uint32_t e = queue[32 * i], at = e & 0x7FFF;
           if (CLUSTERS) {
             if (e >> 15)
-              atomicOr(word, IN_PROMPT);
+              atomicOr(&shared[at], IN_PROMPT);
             else
-              atomicAdd(word, 1u);
-          } else if ((e >> 15 ? atomicOr(word, IN_PROMPT) : atomicAdd(word, 1u)) == 0) {
+              atomicAdd(&shared[at], 1u);
+          } else if ((e >> 15 ? atomicOr(&words[at], IN_PROMPT) : atomicAdd(&words[at], 1u)) == 0) {
             list[atomicAdd(&listed, 1)] = (uint16_t)at;
           }
         }
-        __syncwarp();
       }
       if constexpr (CLUSTERS) {
         cluster_arrive();
@@ -476,6 +483,7 @@ extern "C" qlin_status qlin_adjust_logits(int B, int T, int64_t V, int dtype, co
   const int64_t slice = (vectors - spare) * vec;
   slices = (V + slice - 1) / slice;
   if (clusters) slices = (slices + CLUSTER - 1) / CLUSTER * CLUSTER;
+  p.aligned = !spare && is_aligned(out, 16) && (M == 1 || out_ld % vec == 0);
   p.slice = (int)slice;
   p.vectors = (int)vectors;
   p.vectors_inverse = (uint32_t)(((1ull << 32) + vectors - 1) / vectors);
