@@ -311,3 +311,20 @@ def test_append_attend_weigh_keep_evict_as_one_step():
                 for j, p in enumerate(places):
                     assert ((kk[h, j] - host[p][0][h]).abs() <= R.append_bound(host[p][0], BF)[h]).all()
                     assert ((vv[h, j] - host[p][1][h]).abs() <= 2.0 ** -8 * host[p][1][h].abs()).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_statistics_do_not_depend_on_what_shared_memory_held(dtype):
+    """The same call behind one that leaves large numbers where rows of a fuller step lie: the same bits."""
+    c = Case([300], 4, 4, 128, 64, dtype, seed=3)
+    g = torch.Generator().manual_seed(9)
+    q = torch.randn(4, 8 * 128, generator=g).to(dtype).to(DEV)
+    full = Case([300], 16, 4, 128, 64, dtype, seed=4)
+    large = (torch.randn(16, 8 * 128, generator=g) * 2.0 ** 14).to(dtype).to(DEV)
+    small = torch.zeros_like(large)
+    results = []
+    for before in (small, large, small):
+        qlin.tree_attention(full.cache, full.step, before, scale=1e4)
+        results.append(attend(c, q, 8))
+    for out, stats in results[1:]:
+        assert torch.equal(stats, results[0][1]) and torch.equal(out.view(torch.int16), results[0][0].view(torch.int16))

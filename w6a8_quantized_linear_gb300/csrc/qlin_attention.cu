@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) qlin_attention_kernel(const __
             // keeps what was rounded off there, up to half a step.  Of scores FAR out
             // that passes the type's range (fp16's from 2^24 on, bf16's from 2^31
             // on), so there the product is rounded as the maximum's was.
-            const bool far = __any_sync(0xFFFFFFFFu, fabsf(m_ref) >= FAR);
+            const bool far = __any_sync(0xFFFFFFFFu, live && fabsf(m_ref) >= FAR);  // (lanes without a row: anything)
             const float factor = far ? 1.f : p.scale_log2;
             if (m >= 2) {
               ok = __all_sync(0xFFFFFFFFu, role_wait(&s->p_free[m & 1], ((m >> 1) - 1) & 1, s, p.status));
