@@ -612,8 +612,9 @@ qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, c
  *                  list keeps nothing, and the status word gets QLIN_ERR_BAD_INDEX.
  *   decay        : finite; 1: nothing fades.
  *   score, score_out, position_out, the strides, room : as for qlin_kv_evict
- *                  (score_out may be score); position_out may be NULL.  What would
- *                  lie at room or behind is left out and reported.
+ *                  (score_out may be score); position_out may be NULL.  Neither
+ *                  shares memory with q, stats and at (QLIN_ERR_INVALID_ARG).
+ *                  What would lie at room or behind is left out and reported.
  *   at           : int32 [B * T]: the rows' positions, as given to
  *                  qlin_kv_append_at; NULL: len + depth.
  *   T            : 1..32 rows per sequence, T * Hq / heads <= 128.

@@ -230,3 +230,21 @@ def test_replay_streams_and_then_sampling():
         qlin.adjust_logits(x, out=other, **a)
     side.synchronize()
     assert torch.equal(other, out)
+
+
+def test_lengths_and_tokens_far_outside():
+    """Lengths below 0 and above the history's width, tokens at the ends of their type, prompts of any length."""
+    V = 5000
+    h = i32([[-2 ** 31, 2 ** 31 - 1, 7, V, -1, 4999, 7, 0]] * 4)
+    x = torch.zeros(4, V, device=DEV)
+    one = torch.ones(4, device=DEV)
+    got = qlin.adjust_logits(x, history=h, history_len=i32([8, 2 ** 31 - 1, -2 ** 31, 3]), prompt_len=i32([-2 ** 31, 6, 0, 2 ** 31 - 1]),
+                             frequency=one).cpu()
+    want = torch.zeros(4, V)
+    want[0, 7], want[0, 4999], want[0, 0] = -2, -1, -1
+    want[1, 7], want[1, 0] = -1, -1
+    assert torch.equal(got, want)
+    long = h.repeat(1, 700)  # the same, by clusters
+    got = qlin.adjust_logits(x, history=long, history_len=i32([8, 2 ** 31 - 1, -2 ** 31, 3]),
+                             prompt_len=i32([-2 ** 31, 5598, 0, 2 ** 31 - 1]), frequency=one).cpu()
+    assert torch.equal(got, want)

@@ -210,3 +210,54 @@ def test_evict_on_another_stream_and_behind_another_kernel():
     with torch.cuda.stream(side):
         e.run([1000, 1500], flags=qlin.FLAG_PDL)
     torch.cuda.current_stream().wait_stream(side)
+
+
+def test_weights_and_eviction_past_32_bits_and_a_table_inside_a_wider_one():
+    """The same tokens on the last pages of a cache of 2.3e9 elements and on a small one: the same bits."""
+    heads, page, D, T, n = 4, 64, 128, 4, 300
+    many = 70001  # pages of 32768 elements
+    g = torch.Generator().manual_seed(3)
+    k0, v0 = (torch.randn(6, heads, page, D, generator=g).to(BF).to(DEV) for _ in range(2))
+    q = torch.randn(T, 8 * D, generator=g).to(BF).to(DEV)
+    results = []
+    for pages, order in ((6, [2, 0, 5, 1, 4, 3]), (many, [many - 1, many - 5, 66000, many - 2, 65537, 69000])):
+        ck, cv = (torch.empty(pages, heads, page, D, dtype=BF, device=DEV) for _ in range(2))
+        at = torch.tensor(order, device=DEV)
+        ck[at], cv[at] = k0, v0
+        wide = torch.full((1, 9), -3, dtype=torch.int32, device=DEV)
+        wide[0, 2:8] = i32(order)
+        step = qlin.KVStep(wide[:, 2:8], i32([n]), T)
+        cache = qlin.KVCache(ck, cv)
+        stats = torch.empty(T, 8, 2, device=DEV)
+        out = qlin.tree_attention(cache, step, q, stats=stats)
+        score, position = torch.zeros(1, heads, 350, device=DEV), torch.arange(350, dtype=torch.int32, device=DEV).repeat(1, heads, 1)
+        qlin.kv_weigh(cache, step, q, stats, score, position_out=position)
+        step.len.fill_(n + T)
+        qlin.kv_evict(cache, step, score, i32([150]), since=i32([n]), position=position, len_out=step.len)
+        results.append((out, stats, score, position, ck[at], cv[at], step.len.clone()))
+        del ck, cv, cache, step
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_workspaces_shared_by_two_graphs_one_after_the_other():
+    """Two captured evictions of other shapes on one workspace, replayed in turn."""
+    parts = [Evict([900, 700], 2, 64, 16, seed=5), Evict([3000], 4, 128, 32, seed=6)]
+    keep = [i32([400, 300]), i32([1000])]
+    ws = qlin.new_workspace(max(qlin.kv_evict_workspace_bytes(e.c.cache, e.c.step, e.room) for e in parts), DEV)
+    scores, graphs, length = [e.score.to(DEV) for e in parts], [], [torch.zeros(len(e.lens), dtype=torch.int32, device=DEV) for e in parts]
+    out = [torch.zeros_like(s) for s in scores]
+    for e, s, k, o, n in zip(parts, scores, keep, out, length):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            qlin.kv_evict(e.c.cache, e.c.step, s, k, score_out=o, len_out=n, ws=ws)
+        graphs.append(graph)
+    for i in (0, 1, 1, 0):
+        out[i].zero_()
+        graphs[i].replay()
+    for e, s, k, o, n in zip(parts, scores, keep, out, length):
+        assert torch.equal(n, k)
+        for b in range(len(e.lens)):
+            m = int(k[b])
+            want = e.score[b, :, : e.lens[b]].sort(-1, descending=True).values[:, :m]
+            assert torch.equal(o[b, :, :m].cpu().sort(-1, descending=True).values, want) and (o[b, :, m:] == 0).all()

@@ -146,7 +146,8 @@ def weigh(so, /, c=None, s=None, **kw):
     dict(Hq=0), dict(Hq=6), dict(q=None), dict(q=4104), dict(qs=1023), dict(stats=None), dict(stats=4100), dict(scale=float("inf")),
     dict(decay=float("nan")), dict(keep=4096, ks=3), dict(n_keep=4096), dict(keep=4096, n_keep=4096, ks=2), dict(keep=4097, n_keep=4096, ks=3),
     dict(score=None), dict(score_out=None), dict(score=4098), dict(room=-1), dict(hs=63), dict(oss=64), dict(score_out=(1 << 20) + 8),
-    dict(oss=512), dict(position_out=1 << 20), dict(at=4098), dict(ws=4096 + 8, wsb=256), dict(flags=4)])
+    dict(oss=512), dict(position_out=1 << 20), dict(at=4098), dict(ws=4096 + 8, wsb=256), dict(flags=4),
+    dict(score_out=1 << 24, q=(1 << 24) + 1024), dict(position_out=1 << 24, stats=(1 << 24) + 8), dict(score_out=1 << 24, at=(1 << 24) + 2040)])
 def test_weigh_refusals(L, bad):
     assert weigh(L, **bad) == qlin.ERR_INVALID_ARG
 

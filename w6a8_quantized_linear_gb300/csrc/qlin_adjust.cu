@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
       };
       read();
       if (a.history_len) L = max(0, min(a.history_len[b], L));
-      if (a.prompt_len) prompt = a.prompt_len[b];
+      if (a.prompt_len) prompt = max(0, a.prompt_len[b]);
       clear();
       const int base = v0 - rank * S;
       const uint32_t range = CLUSTERS ? (uint32_t)min(C * S, V - base) : (uint32_t)n;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
         int queued = 0;
 #pragma unroll
         for (int u = 0; u < HISTORY_AHEAD; u++) {
-          const uint32_t at = (uint32_t)(token[u] - base);  // (a token below 0: far above)
+          const uint32_t at = (uint32_t)token[u] - (uint32_t)base;  // (a token below 0: far above)
           if (at < range && ahead(u) < L - h0) queue[32 * queued++] = (uint16_t)(at | (ahead(u) < prompt - h0 ? 0x8000u : 0u));
         }
         const int most = __reduce_max_sync(0xFFFFFFFFu, queued);

@@ -450,6 +450,13 @@ qlin_status weigh(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, 
       rows_overlap(score, span, span, position_out, out_span, out_span, 1) ||
       rows_overlap(score_out, out_span, out_span, position_out, out_span, out_span, 1))
     return QLIN_ERR_INVALID_ARG;
+  for (const void* out : {(const void*)score_out, (const void*)position_out}) {  // some CTAs write while others still read
+    const int64_t rows = B * step->T, heads = Hq;
+    if (rows_overlap(out, out_span, out_span, q, (rows - 1) * q_stride * 2 + heads * D * 2, (rows - 1) * q_stride * 2 + heads * D * 2, 1) ||
+        rows_overlap(out, out_span, out_span, stats, rows * heads * 8, rows * heads * 8, 1) ||
+        rows_overlap(out, out_span, out_span, at, rows * 4, rows * 4, 1))
+      return QLIN_ERR_INVALID_ARG;
+  }
   int ctas = 0;
   st = weigh_setup(&ctas);
   if (st != QLIN_OK) return st;
