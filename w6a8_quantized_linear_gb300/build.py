@@ -1,4 +1,6 @@
-"""Build libqlin.so (sm_103a) in-tree with nvcc.
+"""Build libqlin.so (sm_103a) in-tree with nvcc, and the binding's short way
+beside it (``_qlin_binding.so``, g++, against the headers of the torch that is
+installed).
 
 Translation units compiled in parallel (the host API with the repack
 kernels, the sets of forward-kernel variants, and the append, attention and
@@ -11,6 +13,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libqlin.so")
+BINDING = os.path.join(BUILD, "_qlin_binding.so")
 UNITS = ["qlin_api.cu", "qlin_kernels_w4.cu", "qlin_kernels_w6.cu", "qlin_kernels_codebook.cu",
          "qlin_kernels_moe_w4.cu", "qlin_kernels_moe_w6.cu", "qlin_kernels_export_w4.cu", "qlin_kernels_export_w6.cu",
          "qlin_kernels_tc.cu", "qlin_kernels_tc_export.cu", "qlin_kernels_w4_one_row.cu", "qlin_kernels_w6_one_row.cu",
@@ -40,11 +44,38 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found")
 
 
+BINDING_SOURCE = os.path.join(CSRC, "qlin_binding.cpp")
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
     t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(s) <= t for s in SOURCES)
+    return all(os.path.getmtime(s) <= t for s in SOURCES) and os.path.getmtime(BINDING_SOURCE) <= os.path.getmtime(BINDING)
+
+
+def _torch_folder() -> str:
+    import torch
+    return os.path.dirname(os.path.abspath(torch.__file__))
+
+
+def _binding_command(obj: str) -> list:
+    import torch
+    inc = os.path.join(_torch_folder(), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", inc, "-isystem",
+            os.path.join(inc, "torch", "csrc", "api", "include"), "-c", BINDING_SOURCE, "-o", obj]
+
+
+def _link_binding(obj: str, tag: str) -> str:
+    lib = os.path.join(_torch_folder(), "lib")
+    tmp = BINDING + tag
+    r = subprocess.run(["g++", "-shared", obj, "-o", tmp, "-L", BUILD, "-l:libqlin.so", "-L", lib, "-ltorch_python", "-ltorch_cpu",
+                        "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("linking the binding failed:\n" + r.stdout + r.stderr)
+    os.replace(tmp, BINDING)
+    return r.stdout + r.stderr
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
@@ -76,12 +107,15 @@ def _compile_and_link(nvcc, cuda_lib, common, tag, verbose):
         cmd = common + ["-c", os.path.join(CSRC, u), "-o", obj]
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
         objs.append(obj)
+    binding = os.path.join(BUILD, "qlin_binding" + tag + ".o")
+    cmd = _binding_command(binding)
+    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     logs = []
     for cmd, pr in procs:
         out, _ = pr.communicate()
         logs.append(out)
         if pr.returncode != 0:
-            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + out)
+            raise RuntimeError("compiling failed:\n" + " ".join(cmd) + "\n" + out)
     tmp = LIB + tag
     cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-cudart", "shared", "-Xlinker",
            f"-rpath,{cuda_lib}"] + objs + ["-o", tmp]
@@ -89,6 +123,7 @@ def _compile_and_link(nvcc, cuda_lib, common, tag, verbose):
     if r.returncode != 0:
         raise RuntimeError("nvcc link failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB)
+    logs.append(_link_binding(binding, tag))
     if verbose:
         print("".join(logs) + r.stdout + r.stderr)
     return LIB

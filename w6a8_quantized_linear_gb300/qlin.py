@@ -4,11 +4,17 @@ Argument marshalling only: every step of the path runs in the library's CUDA
 kernels.  PyTorch supplies device memory and streams.  There is no fallback:
 if the library is missing, every call raises.
 
+Calls whose arguments are all contiguous tensors of the right types on the
+current device, with nothing to be allocated, take a short way through a small
+extension (``csrc/qlin_binding.cpp``) that reads the tensors itself (4 to 7 us a
+call less); all others are looked at here, argument by argument.
+
 Names follow the C ABI in ``include/qlin.h`` without the ``qlin_`` prefix.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import struct
 import threading
@@ -108,6 +114,25 @@ def lib() -> ctypes.CDLL:
                 fn.argtypes = args
             _lib = L
     return _lib
+
+
+_binding = None
+
+
+def _load_binding():
+    """The short way's extension, loaded with the library that it calls."""
+    global _binding
+    lib()
+    with _lock:
+        if _binding is None:
+            if not os.path.exists(_build.BINDING):
+                raise RuntimeError(f"_qlin_binding.so is not built ({_build.BINDING}); run __graft_entry__.build() "
+                                   "or python -m w6a8_quantized_linear_gb300.build")
+            spec = importlib.util.spec_from_file_location("_qlin_binding", _build.BINDING)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            _binding = module
+    return _binding
 
 
 def status_string(status: int) -> str:
@@ -423,6 +448,7 @@ class KVCache:
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), self.pages, step[0], step[1], k.stride(2),
                                     DTYPES[k.dtype], self.heads, self.width, self.page_size)
         self._ref = ctypes.addressof(self._struct)
+        self._code = DTYPES[k.dtype]
 
 
 class KVStep:
@@ -452,6 +478,7 @@ class KVStep:
         self._struct = _StepStruct(_ptr(page_table), _ptr(len), _ptr(count), _ptr(depth), _ptr(mask),
                                    page_table.stride(0) if B > 1 else n, T if tree and tree[0].dim() == 2 else 0, B, T, n)
         self._ref = ctypes.addressof(self._struct)
+        self._index = len.get_device()
 
 
 _fns: dict = {}
@@ -580,6 +607,14 @@ def kv_append(cache: KVCache, step: KVStep, q=None, k=None, v=None, q_gamma=None
     length plus its depth, unless ``position`` gives it: int32 [B * T], or
     [B * T, axes] with ``axis`` (``rope_axes``) naming the axis of each pair."""
     n, D, dev = step.B * step.T, cache.width, cache._index
+    if stream is None and 0 <= dev == step._index and dev == _current_device():
+        status = (_binding or _load_binding()).kv_append(
+            dev, cache._ref, step._ref, n, D, cache.heads, cache._code, q, k, v, q_gamma, k_gamma, eps, turns, pairs, q_out, ws,
+            flags, _current_stream(dev), position, axis)
+        if status is not None:
+            if status:
+                _check(status, "kv_append")
+            return q_out
     _same_device(dev, step.len, q, k, v, q_gamma, k_gamma, turns, q_out, ws, position)
     if (k is None) != (v is None):
         raise ValueError("k and v are given together")
@@ -730,6 +765,14 @@ def kv_weigh(cache: KVCache, step: KVStep, q: torch.Tensor, stats: torch.Tensor,
     their positions: ``at`` (int32 [B * T]), or len + depth.  Returns ``score_out``
     (in place unless given)."""
     n, D, dev = step.B * step.T, cache.width, cache._index
+    if stream is None and 0 <= dev == step._index and dev == _current_device():
+        status = (_binding or _load_binding()).kv_weigh(
+            dev, cache._ref, step._ref, step.B, step.T, D, cache.heads, cache._code, q, stats, score, keep, n_keep, decay,
+            D ** -0.5 if scale is None else scale, score_out, position_out, at, ws, flags, _current_stream(dev))
+        if status is not None:
+            if status:
+                _check(status, "kv_weigh")
+            return score if score_out is None else score_out
     _same_device(dev, step.len, q, stats, score, keep, n_keep, score_out, position_out, at, ws)
     Hq = _heads(q, D, "q")
     qs = _rows(q, n, Hq * D, cache.dtype, "q")
@@ -786,7 +829,16 @@ def kv_evict(cache: KVCache, step: KVStep, score: torch.Tensor, n_keep: torch.Te
     place unless given.  ``len_out`` (int32 [B], may be the step's ``len``) gets
     the new lengths.  Without ``ws`` the call takes memory of its own, and what its
     status word gets (``ERR_BAD_INDEX``) is lost with it."""
-    _same_device(cache._index, step.len, score, n_keep, since, position, score_out, position_out, len_out, ws)
+    dev = cache._index
+    if stream is None and 0 <= dev == step._index and dev == _current_device():
+        status = (_binding or _load_binding()).kv_evict(
+            dev, cache._ref, step._ref, step.B, cache.heads, score, n_keep, first, since, position, score_out, position_out, len_out,
+            ws, flags, _current_stream(dev))
+        if status is not None:
+            if status:
+                _check(status, "kv_evict")
+            return
+    _same_device(dev, step.len, score, n_keep, since, position, score_out, position_out, len_out, ws)
     B = step.B
     if score.dim() != 3:
         raise ValueError("score must be [B, heads, room]")
@@ -861,6 +913,15 @@ def adjust_logits(logits: torch.Tensor, out=None, history=None, history_len=None
     ``allowed`` int32 [B * T, ceil(V / 32)] or [ceil(V / 32)]: a bit per token,
     the others become -inf.  B is the rows of history, draft, or a penalty; else
     of bias_token; without any of these, each row is its own sequence."""
+    dev = logits.get_device()
+    if stream is None and 0 <= dev == _current_device():
+        status = (_binding or _load_binding()).adjust_logits(
+            dev, logits, out, history, history_len, prompt_len, draft, mask, repetition, presence, frequency, bias_token, bias,
+            allowed, flags, _current_stream(dev))
+        if status is not None:
+            if status:
+                _check(status, "adjust_logits")
+            return out
     if logits.dim() != 2:
         raise ValueError("logits must be [B * T, V]")
     M, V = logits.shape
@@ -869,7 +930,6 @@ def adjust_logits(logits: torch.Tensor, out=None, history=None, history_len=None
         if logits.stride(1) != 1 and V > 1:
             raise ValueError("logits must have contiguous rows")
         ld = logits.stride(0) if M > 1 else V
-    dev = logits.get_device()
     _same_device(dev, *[t for t in (out, history, history_len, prompt_len, draft, mask, repetition, presence, frequency, bias_token,
                                     bias, allowed) if t is not None])
     B = M
