@@ -21,7 +21,7 @@ constexpr int ROWS = QLIN_MAX_TREE;   // rows of a block at most
 constexpr int MAX_PAIRS = ROWS * ROWS / ADJUST_THREADS;
 
 // What a block knows of a token of its slice, in a word: how often it stands in
-// the history behind the prompt, its place + 1 among the slice's biases, and
+// the history behind the prompt, the place + 1 of its first one among the slice's biases, and
 // whether it stands in the prompt.
 constexpr uint32_t COUNT = (1u << 20) - 1, IN_PROMPT = 1u << 31;
 __device__ __forceinline__ uint32_t slot_of(uint32_t word) { return word >> 20 & 0x7FF; }
@@ -74,6 +74,8 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
   constexpr bool DRAFTS = KIND == Rows::DRAFTED, ONE = KIND == Rows::ONE;
   extern __shared__ __align__(16) uint32_t shared[];  // words of the cluster's slices, the list of this one
   __shared__ float bias[QLIN_MAX_BIAS];
+  __shared__ uint16_t bias_at[QLIN_MAX_BIAS];
+  __shared__ int bias_hits[ADJUST_THREADS / 32];
   __shared__ int draft[ROWS];
   __shared__ uint32_t tree[ROWS];
   __shared__ int listed;
@@ -184,17 +186,48 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
   if (counts || DRAFTS || a.n_bias) {
     int first_bias = -1;
     float first_value = 0.f;
-    if (tid < 32 && tid < a.n_bias)
+    if (tid < a.n_bias)
       first_bias = a.bias_token[b * a.bias_stride + tid], first_value = a.bias[b * a.bias_stride + tid];
     if (DRAFTS && tid < p.T) {
       draft[tid] = a.draft[(int64_t)b * p.T + tid];
       tree[tid] = a.mask ? (uint32_t)a.mask[b * a.tree_stride + tid] : 0xFFFFFFFFu >> (31 - tid);
     }
     if (tid == 0) listed = 0;
+    // Biases of the slice, in the list's order: their places and values.  (Found
+    // before a barrier and held behind it; counted among the warps in between.)
+    int held = 0;
+    bool bias_here = false;
+    uint32_t bias_lanes = 0;
+    auto find_biases = [&] {
+      bias_here = first_bias >= 0 && (uint32_t)(first_bias - v0) < (uint32_t)n;
+      bias_lanes = __ballot_sync(0xFFFFFFFFu, bias_here);
+      if ((tid & 31) == 0) bias_hits[tid >> 5] = __popc(bias_lanes);
+    };
+    auto hold_biases = [&] {
+      if (a.n_bias <= 32) {  // the first warp's alone
+        if (bias_here) {
+          const int k = __popc(bias_lanes & ((1u << tid) - 1));
+          bias_at[k] = (uint16_t)(first_bias - v0);
+          bias[k] = first_value;
+        }
+        held = __popc(bias_lanes);
+        return;
+      }
+      const int of_warp = bias_hits[tid & (ADJUST_THREADS / 32 - 1)], lane = tid & 31;
+      const int before = __reduce_add_sync(0xFFFFFFFFu, lane < (tid >> 5) ? of_warp : 0);
+      if (bias_here) {
+        const int k = held + before + __popc(bias_lanes & ((1u << lane) - 1));
+        bias_at[k] = (uint16_t)(first_bias - v0);
+        bias[k] = first_value;
+      }
+      held += __reduce_add_sync(0xFFFFFFFFu, lane < ADJUST_THREADS / 32 ? of_warp : 0);
+    };
     auto clear = [&] {
       for (int i = tid; i < C * S / 4; i += ADJUST_THREADS) reinterpret_cast<uint4*>(shared)[i] = make_uint4(0, 0, 0, 0);
       copy();
+      if (a.n_bias) find_biases();
       __syncthreads();
+      if (a.n_bias) hold_biases();
     };
     if (counts) {
       // a thread takes four tokens in a row, HISTORY_AHEAD on their way
@@ -267,37 +300,38 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
     } else {
       clear();
     }
-    if (a.n_bias && tid < 32) {  // one warp, in the list's order: biases of one token are added in that order
-      int used = 0;
-      for (int i0 = 0; i0 < a.n_bias; i0 += 32) {
+    if (a.n_bias) {
+      for (int i0 = ADJUST_THREADS; i0 < a.n_bias; i0 += ADJUST_THREADS) {  // a longer list's
         const int i = i0 + tid;
-        if (i0) {
-          first_bias = i < a.n_bias ? a.bias_token[b * a.bias_stride + i] : -1;
-          first_value = i < a.n_bias ? a.bias[b * a.bias_stride + i] : 0.f;
-        }
-        const bool here = first_bias >= 0 && (uint32_t)(first_bias - v0) < (uint32_t)n;
-        if (!__any_sync(0xFFFFFFFFu, here)) continue;
-        const int at = here ? first_bias - v0 : 0;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, here ? at : -1 - tid);
-        const bool first = here && (same & ((1u << tid) - 1)) == 0;
-        uint32_t slot = first ? slot_of(words[at]) : 0;
-        const bool fresh = first && !slot;
-        const uint32_t made = __ballot_sync(0xFFFFFFFFu, fresh);
-        if (fresh) {
-          slot = used + __popc(made & ((1u << tid) - 1)) + 1;
-          if (words[at] == 0) list[atomicAdd(&listed, 1)] = (uint16_t)at;
-          words[at] |= slot << 20;
-          bias[slot - 1] = first_value;
-        }
-        used += __popc(made);
-        __syncwarp();
-        uint32_t again = __ballot_sync(0xFFFFFFFFu, here && !fresh);
-        while (again) {
-          if (tid == __ffs(again) - 1) bias[slot_of(words[at]) - 1] += first_value;
-          again &= again - 1;
-          __syncwarp();
-        }
+        first_bias = i < a.n_bias ? a.bias_token[b * a.bias_stride + i] : -1;
+        first_value = i < a.n_bias ? a.bias[b * a.bias_stride + i] : 0.f;
+        __syncthreads();
+        find_biases();
+        __syncthreads();
+        hold_biases();
       }
+      if (!counts || a.n_bias > ADJUST_THREADS) __syncthreads();
+      // biases of one token are added up in the first one's place, in order, by one warp
+      if (tid < 32)
+        for (int k0 = 0; k0 < held; k0 += 32) {
+          const int k = k0 + tid;
+          const bool here = k < held;
+          const int at = here ? bias_at[k] : 0;
+          const uint32_t same = __match_any_sync(0xFFFFFFFFu, here ? at : -1 - tid);
+          const bool first = here && (same & ((1u << tid) - 1)) == 0, fresh = first && !slot_of(words[at]);
+          __syncwarp();
+          if (fresh) {
+            if (words[at] == 0) list[atomicAdd(&listed, 1)] = (uint16_t)at;
+            words[at] |= (uint32_t)(k + 1) << 20;
+          }
+          __syncwarp();
+          uint32_t again = __ballot_sync(0xFFFFFFFFu, here && !fresh);
+          while (again) {
+            if (tid == __ffs(again) - 1) bias[slot_of(words[at]) - 1] += bias[k];
+            again &= again - 1;
+            __syncwarp();
+          }
+        }
     }
     if (a.n_bias || DRAFTS)
       any_draft = __syncthreads_or(DRAFTS && tid < p.T && draft[tid] >= 0 && (uint32_t)(draft[tid] - v0) < (uint32_t)n);

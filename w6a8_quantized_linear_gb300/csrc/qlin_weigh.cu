@@ -36,6 +36,7 @@ struct WeighParams {
   uint32_t* status;
   float scale_log2, decay;
   int room;
+  uint32_t group_inverse;  // 2^16 / group, rounded up: the kept row of a column (below 128)
   int group, Rp;   // query heads of a cache head; columns of an accumulator: T * group, padded to 16
   int slots;       // of the ring
   int ctas, box, page_shift;
@@ -55,9 +56,8 @@ struct WeighShared {
   uint32_t tmem;
   int dead;  // a wait has expired: every role leaves its loop
   Walk walk;
-  // of the item: two columns' negative references and inverse sums of weights at a time, and a column's kept row
+  // of the item: two columns' negative references and inverse sums of weights at a time
   float4 stat[MAX_ROWS / 2];
-  uint8_t row_of[MAX_ROWS];
   int kept[QLIN_MAX_TREE];       // the kept rows
   int own[QLIN_MAX_TREE];        // the step's row: its place among the kept ones, or -1
   uint32_t seen[QLIN_MAX_TREE];  // kept rows (bits) that see the step's row
@@ -264,23 +264,33 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
           float* st = reinterpret_cast<float*>(&s->stat[c / 2]) + c % 2;
           st[0] = rl.y == 0.f ? -INFINITY : -rl.x;
           st[2] = rl.y == 0.f ? 0.f : 1.f / rl.y;
-          s->row_of[c] = (uint8_t)i;
           if (fabsf(rl.x) >= FAR && rl.y != 0.f) s->far = 1;
         }
         for (int c = cols + tid; c < p.Rp; c += WEIGHING) {  // columns that weigh nothing
           float* st = reinterpret_cast<float*>(&s->stat[c / 2]) + c % 2;
           st[0] = -INFINITY, st[2] = 0.f;
         }
-        for (int x = tid; x < p.Rp * (D / 8); x += WEIGHING) {  // swizzled as the keys are by TMA
-          const int c = x / (D / 8), u = x % (D / 8);
-          uint4 v = make_uint4(0, 0, 0, 0);
+        // the query rows, swizzled as the keys are by TMA: a thread's units of 16 bytes
+        // (the same place of every STEP-th row) all on their way at once
+        constexpr int UNITS = D / 8, STEP = WEIGHING / UNITS, MOST = MAX_ROWS / STEP;
+        const int u = tid % UNITS;
+        uint4 v[MOST];
+#pragma unroll
+        for (int k = 0; k < MOST; k++) {
+          const int c = tid / UNITS + k * STEP;
+          v[k] = make_uint4(0, 0, 0, 0);
           if (c < cols)
-            v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (row0 + s->kept[c / p.group]) * p.q_stride +
-                                                (int64_t)(w.h * p.group + c % p.group) * D + u * 8);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_smem + (u / 8) * panel_bytes + c * 128 +
-                                                                        (((u & 7) ^ (c & 7)) << 4)),
-                       "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                       : "memory");
+            v[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (row0 + s->kept[c / p.group]) * p.q_stride +
+                                                   (int64_t)(w.h * p.group + c % p.group) * D + u * 8);
+        }
+#pragma unroll
+        for (int k = 0; k < MOST; k++) {
+          const int c = tid / UNITS + k * STEP;
+          if (c < p.Rp)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_smem + (u / 8) * panel_bytes + c * 128 +
+                                                                          (((u & 7) ^ (c & 7)) << 4)),
+                         "r"(v[k].x), "r"(v[k].y), "r"(v[k].z), "r"(v[k].w)
+                         : "memory");
         }
         fence_proxy_async_smem();
         weighing_bar(true);
@@ -306,32 +316,46 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
           tc_fence_after();
           const uint32_t from = tmem + lanes + acc * MAX_ROWS;
           float2 sum[4] = {};
-          if (first + TILE <= len && !far) {  // every row sees every token
+          const uint32_t seen = old ? ALL : place >= 0 ? s->seen[r] : 0;  // of the kept rows
+          if (!far) {
             uint32_t x[32];  // 32 columns at a time
             const float2 scale = make_float2(p.scale_log2, p.scale_log2);
-            auto add = [&](int c0, int c) {  // two columns
-              const float4 st = s->stat[(c0 + c) / 2];
+            auto weights = [&](int c, const float4& st) {  // of two columns, but for the sums of weights
               const float2 e = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale, make_float2(st.x, st.y));
-              sum[c / 2 & 3] = fma2(make_float2(exp2_approx(e.x), exp2_approx(e.y)), make_float2(st.z, st.w), sum[c / 2 & 3]);
+              return make_float2(exp2_approx(e.x), exp2_approx(e.y));
             };
+            auto add = [&](int c0, int c, auto every) {
+              const float4 st = s->stat[(c0 + c) / 2];
+              float2 e = weights(c, st);
+              if constexpr (!decltype(every)::value) {  // what a row does not see may be NaN
+                if (!(seen >> ((c0 + c) * p.group_inverse >> 16) & 1)) e.x = 0.f;
+                if (!(seen >> ((c0 + c + 1) * p.group_inverse >> 16) & 1)) e.y = 0.f;
+              }
+              sum[c / 2 & 3] = fma2(e, make_float2(st.z, st.w), sum[c / 2 & 3]);
+            };
+            auto all = [&](auto every) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < p.Rp; c0 += 32) {
-              const bool half = p.Rp - c0 < 32;
-              if (half)
-                tmem_ld16(from + c0, *reinterpret_cast<uint32_t(*)[16]>(x));
-              else
-                tmem_ld32(from + c0, x);
-              tmem_wait_ld();
+              for (int c0 = 0; c0 < p.Rp; c0 += 32) {
+                const bool half = p.Rp - c0 < 32;
+                if (half)
+                  tmem_ld16(from + c0, *reinterpret_cast<uint32_t(*)[16]>(x));
+                else
+                  tmem_ld32(from + c0, x);
+                tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < 16; c += 2) add(c0, c);
-              if (half) break;
+                for (int c = 0; c < 16; c += 2) add(c0, c, every);
+                if (half) break;
 #pragma unroll
-              for (int c = 16; c < 32; c += 2) add(c0, c);
-            }
+                for (int c = 16; c < 32; c += 2) add(c0, c, every);
+              }
+            };
+            if (first + TILE <= len)  // every row sees every token
+              all(std::true_type());
+            else
+              all(std::false_type());
           } else {
             // A reference far out comes from a rounded product: the scores are rounded
             // as it was, and what still rises above it is no more than a whole weight.
-            const uint32_t seen = old ? 0xFFFFFFFFu : place >= 0 ? s->seen[r] : 0;
 #pragma unroll 1
             for (int c0 = 0; c0 < cols; c0 += 16) {
               uint32_t x[16];
@@ -339,15 +363,11 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
               tmem_wait_ld();
 #pragma unroll
               for (int c = 0; c < 16; c++)
-                if (c0 + c < cols && seen >> s->row_of[c0 + c] & 1) {
+                if (c0 + c < cols && seen >> ((c0 + c) * p.group_inverse >> 16) & 1) {
                   const float4 st = s->stat[(c0 + c) / 2];
-                  const float v = __uint_as_float(x[c]), shift = c & 1 ? st.y : st.x, inv = c & 1 ? st.w : st.z;
-                  if (far) {
-                    const float e = exp2_approx(__fmul_rn(v, p.scale_log2) + shift) * inv;
-                    sum[c & 3].x += e > 1.f ? 1.f : e;
-                  } else {
-                    sum[c & 3].x = fmaf(exp2_approx(fmaf(v, p.scale_log2, shift)), inv, sum[c & 3].x);
-                  }
+                  const float shift = c & 1 ? st.y : st.x, inv = c & 1 ? st.w : st.z;
+                  const float e = exp2_approx(__fmul_rn(__uint_as_float(x[c]), p.scale_log2) + shift) * inv;
+                  sum[c & 3].x += e > 1.f ? 1.f : e;
                 }
             }
           }
@@ -476,6 +496,7 @@ qlin_status weigh(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, 
   p.decay = decay;
   p.room = (int)room;
   p.group = Hq / cache->heads;
+  p.group_inverse = (65536u + (uint32_t)p.group - 1) / (uint32_t)p.group;
   p.Rp = (step->T * p.group + 15) / 16 * 16;
   const int q_bytes = p.Rp * cache->width * 2, fit = (WEIGH_SMEM - q_bytes) / SLOT_BYTES;
   p.slots = fit < MAX_SLOTS ? fit : MAX_SLOTS;
