@@ -116,12 +116,13 @@ __global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 2) qlin_evict_sel
   auto form = [&](float x, int at) { return key_of(x, at < p.first || (p.since && at >= since)); };
 
   uint32_t keys[K ? K : 1];
+  // of this run: the places before `stays` and those behind it
+  const bool copies = (copy_score || copy_position) && i0 < stays;
   auto take = [&](int i, float x, int at) {
-    if (i < min(end, stays)) {
+    if (copies && i < min(end, stays)) {
       if (copy_score) score_out[i] = x;
       if (copy_position) position_out[i] = at;
     }
-    return form(x, at);
   };
   if constexpr (K > 0) {
     float x[K];
@@ -132,13 +133,17 @@ __global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 2) qlin_evict_sel
       keys[j] = (uint32_t)(position && i < end ? position[i] : i);
     }
 #pragma unroll
-    for (int j = 0; j < K; j++) keys[j] = take(i0 + 32 * j + lane, x[j], (int)keys[j]);
-  } else if (copy_score || copy_position) {
+    for (int j = 0; j < K; j++) {
+      const int i = i0 + 32 * j + lane, at = (int)keys[j];
+      take(i, x[j], at);
+      keys[j] = i < end ? form(x[j], at) : 0;
+    }
+  } else if (copies) {
 #pragma unroll 4
-    for (int i = i0 + lane; i < end; i += 32) (void)take(i, score[i], position ? position[i] : i);
+    for (int i = i0 + lane; i < end; i += 32) take(i, score[i], position ? position[i] : i);
   }
   if (stays == n || stays == 0) return;  // nothing moves; the whole cluster leaves
-  // f(key, j) for the warp's keys, all lanes at once; a lane behind the end is not there
+  // f(key, place) for the warp's keys, all lanes at once; behind the end: key 0
   auto each = [&](auto&& f) {
     if constexpr (K > 0) {
 #pragma unroll
@@ -215,16 +220,27 @@ __global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 2) qlin_evict_sel
   }
 
   // ---- who stays
+  // (A run lies on one side of place `stays` as a rule: one ballot per 32 keys.)
+  const int side = end <= stays ? 0 : i0 >= stays ? 1 : 2;
   uint4 c = make_uint4(0, 0, 0, 0);
-  each([&](uint32_t k, int i) {
-    const bool there = i < end, low = i < stays;
-    c.x += __popc(__ballot_sync(ALL, there && low && k > border));
-    c.z += __popc(__ballot_sync(ALL, there && !low && k > border));
-    if (ties) {
-      c.y += __popc(__ballot_sync(ALL, there && low && k == border));
-      c.w += __popc(__ballot_sync(ALL, there && !low && k == border));
-    }
-  });
+  if (side < 2) {
+    uint32_t sure = 0, equal = 0;
+    each([&](uint32_t k, int i) {
+      sure += __popc(__ballot_sync(ALL, k > border));
+      if (ties) equal += __popc(__ballot_sync(ALL, i < end && k == border));
+    });
+    c = side ? make_uint4(0, 0, sure, equal) : make_uint4(sure, equal, 0, 0);
+  } else {
+    each([&](uint32_t k, int i) {
+      const bool low = i < stays;
+      c.x += __popc(__ballot_sync(ALL, low && k > border));
+      c.z += __popc(__ballot_sync(ALL, !low && k > border));
+      if (ties) {
+        c.y += __popc(__ballot_sync(ALL, low && k == border));
+        c.w += __popc(__ballot_sync(ALL, !low && i < end && k == border));
+      }
+    });
+  }
   if (lane == 0) s->warp[warp] = c;
   __syncthreads();
   if (warp == 0) {
@@ -261,21 +277,36 @@ __global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 2) qlin_evict_sel
   int32_t* mover = p.lists + ((int64_t)item * 2 + 1) * p.half + movers;
   const uint32_t below = (1u << lane) - 1;
   uint32_t moved = 0;
-  each([&](uint32_t k, int i) {
+  auto stays_put = [&](uint32_t k, int i) {
     bool stay = k > border;
     if (ties) {
       const uint32_t equal = __ballot_sync(ALL, i < end && k == border);
       stay |= k == border && equals + __popc(equal & below) < ties;
       equals += __popc(equal);
     }
-    const bool empty = i < min(end, stays) && !stay, moves = i < end && i >= stays && stay;
-    const uint32_t e = __ballot_sync(ALL, empty), m = __ballot_sync(ALL, moves);
-    if (empty) hole[__popc(e & below)] = i;
-    if (moves) mover[__popc(m & below)] = i;
-    hole += __popc(e);
-    mover += __popc(m);
-    moved += __popc(m);
-  });
+    return stay;
+  };
+  if (side < 2) {
+    int32_t* list = side ? mover : hole;
+    each([&](uint32_t k, int i) {
+      const bool stay = stays_put(k, i), listed = i < end && stay == (side == 1);
+      const uint32_t m = __ballot_sync(ALL, listed);
+      if (listed) list[__popc(m & below)] = i;
+      list += __popc(m);
+    });
+    if (side) moved = (uint32_t)(list - mover);
+  } else {
+    each([&](uint32_t k, int i) {
+      const bool stay = stays_put(k, i);
+      const bool empty = i < min(end, stays) && !stay, moves = i < end && i >= stays && stay;
+      const uint32_t e = __ballot_sync(ALL, empty), m = __ballot_sync(ALL, moves);
+      if (empty) hole[__popc(e & below)] = i;
+      if (moves) mover[__popc(m & below)] = i;
+      hole += __popc(e);
+      mover += __popc(m);
+      moved += __popc(m);
+    });
+  }
   if (rank == C - 1 && warp == SELECT_WARPS - 1 && lane == 0) p.chosen[item] = make_int2((int)(movers + moved), stays);
   if (C > 1) cluster_wait();
 }
