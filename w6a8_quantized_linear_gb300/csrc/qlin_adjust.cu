@@ -188,8 +188,10 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
     float first_value = 0.f;
     if (tid < a.n_bias)
       first_bias = a.bias_token[b * a.bias_stride + tid], first_value = a.bias[b * a.bias_stride + tid];
+    bool concerned = CLUSTERS || a.n_bias > ADJUST_THREADS;  // something here concerns this slice, as far as this thread knows
     if (DRAFTS && tid < p.T) {
       draft[tid] = a.draft[(int64_t)b * p.T + tid];
+      concerned |= draft[tid] >= 0 && (uint32_t)(draft[tid] - v0) < (uint32_t)n;
       tree[tid] = a.mask ? (uint32_t)a.mask[b * a.tree_stride + tid] : 0xFFFFFFFFu >> (31 - tid);
     }
     if (tid == 0) listed = 0;
@@ -226,8 +228,9 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
       for (int i = tid; i < C * S / 4; i += ADJUST_THREADS) reinterpret_cast<uint4*>(shared)[i] = make_uint4(0, 0, 0, 0);
       copy();
       if (a.n_bias) find_biases();
-      __syncthreads();
+      if (!__syncthreads_or(concerned || bias_here)) return false;
       if (a.n_bias) hold_biases();
+      return true;
     };
     if (counts) {
       // a thread takes four tokens in a row, HISTORY_AHEAD on their way
@@ -251,9 +254,13 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
       read();
       if (a.history_len) L = max(0, min(a.history_len[b], L));
       if (a.prompt_len) prompt = max(0, a.prompt_len[b]);
-      clear();
       const int base = v0 - rank * S;
       const uint32_t range = CLUSTERS ? (uint32_t)min(C * S, V - base) : (uint32_t)n;
+      concerned |= L > ROUND;
+#pragma unroll
+      for (int u = 0; u < HISTORY_AHEAD; u++)
+        concerned |= (uint32_t)token[u] - (uint32_t)base < range && ahead(u) < L - h0;
+      if (!clear()) return;  // (in no cluster)
       uint16_t* queue = queues[tid >> 5] + (tid & 31);
 #pragma unroll 1
       for (int r0 = 0; r0 < L; r0 += ROUND, h0 += ROUND) {
@@ -297,8 +304,8 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
         cluster_arrive();  // waited for at the end: no block leaves while others read its words
       }
       __syncthreads();
-    } else {
-      clear();
+    } else if (!clear()) {
+      return;
     }
     if (a.n_bias) {
       for (int i0 = ADJUST_THREADS; i0 < a.n_bias; i0 += ADJUST_THREADS) {  // a longer list's

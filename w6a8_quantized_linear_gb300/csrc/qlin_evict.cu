@@ -15,7 +15,6 @@
 namespace qlin {
 namespace {
 
-constexpr int SELECT_THREADS = 512, SELECT_WARPS = SELECT_THREADS / 32;
 constexpr int BINS = 2048;            // of one pass over 11 bits of the keys
 constexpr int MAX_CLUSTER = 16;
 constexpr int MOVE_THREADS = 256, MOVE_WARPS = MOVE_THREADS / 32;
@@ -52,6 +51,15 @@ __device__ __forceinline__ uint32_t key_of(float score, bool safe) {
 __device__ __forceinline__ void cluster_add(uint32_t addr, uint32_t v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_load(uint32_t addr, uint32_t (&v)[2]) {
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void cluster_load(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ uint4 cluster_load4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -65,8 +73,8 @@ struct SelectShared {
   uint32_t hist[BINS];
   __align__(16) uint32_t total[3][BINS];  // the cluster's counts of this block's share of the bins
   __align__(16) uint4 sums;               // above the border and equal to it, before place `stays`; the same behind it
-  uint4 cta[MAX_CLUSTER], warp[SELECT_WARPS];
-  uint32_t above[SELECT_WARPS];
+  uint4 cta[MAX_CLUSTER], warp[32];
+  uint32_t above[32];
   uint32_t bin, over, in_bin;
 };
 
@@ -84,8 +92,11 @@ __device__ __forceinline__ uint2 staying(uint4 c, uint32_t before, uint32_t ties
 // time), so that ranks come from ballots.  The border is found from the keys' upper
 // bits down, 11 at a time: a histogram per block, added into the bins' owners,
 // and read by all; where a whole bin stays, what lies below need not be looked at.
-template <int K>
-__global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 2) qlin_evict_select_kernel(const __grid_constant__ EvictParams p) {
+template <int K, int SELECT_THREADS>
+__global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 1024 / SELECT_THREADS)
+    qlin_evict_select_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int SELECT_WARPS = SELECT_THREADS / 32, PER = BINS / SELECT_THREADS;  // PER: a thread's bins
+  static_assert(PER == 4 || PER == 2, "bins are read 16 or 8 bytes at a time");
   __shared__ SelectShared sh;
   SelectShared* s = &sh;
   const int C = p.cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -167,7 +178,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 2) qlin_evict_sel
   for (int pass = 0; pass < 3; pass++) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     if (pass) {
-      reinterpret_cast<uint4*>(s->hist)[tid] = make_uint4(0, 0, 0, 0);
+      for (int i = tid; i < BINS / 4; i += SELECT_THREADS) reinterpret_cast<uint4*>(s->hist)[i] = make_uint4(0, 0, 0, 0);
       __syncthreads();
     }
     each([&](uint32_t k, int i) {
@@ -175,20 +186,23 @@ __global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 2) qlin_evict_sel
     });
     if (C > 1 && pass == 0) cluster_wait();
     __syncthreads();
-    // a thread's four bins, the highest bins first
-    const int bin = BINS - 4 - 4 * tid;
-    uint4 c = *reinterpret_cast<const uint4*>(&s->hist[bin]);
+    // a thread's bins, the highest first
+    const int bin = BINS - PER * (tid + 1);
+    uint32_t counts[PER], mine = 0;
     if (C > 1) {
       const uint32_t at = dsmem_addr_u32(smem_u32(s->total[pass]) + (uint32_t)(bin % share) * 4, (uint32_t)(bin / share));
-      if (c.x) cluster_add(at, c.x);
-      if (c.y) cluster_add(at + 4, c.y);
-      if (c.z) cluster_add(at + 8, c.z);
-      if (c.w) cluster_add(at + 12, c.w);
+#pragma unroll
+      for (int e = 0; e < PER; e++)
+        if (s->hist[bin + e]) cluster_add(at + e * 4, s->hist[bin + e]);
       cluster_arrive();
       cluster_wait();
-      c = cluster_load4(at);
+      cluster_load(at, counts);
+    } else {
+#pragma unroll
+      for (int e = 0; e < PER; e++) counts[e] = s->hist[bin + e];
     }
-    const uint32_t mine = c.x + c.y + c.z + c.w;
+#pragma unroll
+    for (int e = 0; e < PER; e++) mine += counts[e];
     uint32_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -197,12 +211,11 @@ __global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 2) qlin_evict_sel
     }
     if (lane == 31) s->above[warp] = upto;
     __syncthreads();
-    uint32_t above = upto - mine + warp_sum(lane < warp ? s->above[lane & 15] : 0);
-    const uint32_t counts[4] = {c.w, c.z, c.y, c.x};
+    uint32_t above = upto - mine + warp_sum(lane < warp ? s->above[lane] : 0);
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
+    for (int e = PER - 1; e >= 0; e--) {
       if (above < ties && ties <= above + counts[e]) {
-        s->bin = (uint32_t)(bin + 3 - e);
+        s->bin = (uint32_t)(bin + e);
         s->over = above;
         s->in_bin = counts[e];
       }
@@ -261,7 +274,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 2) qlin_evict_sel
     uint32_t inc = x.y + x.w;
     const uint32_t own = inc;
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
+    for (int o = 1; o < 32; o <<= 1) {
       const uint32_t a = __shfl_up_sync(ALL, inc, o);
       if (lane >= o) inc += a;
     }
@@ -421,11 +434,17 @@ __global__ void __launch_bounds__(MOVE_THREADS) qlin_evict_move_kernel(const __g
 }
 
 // Keys of a lane in registers: as many as the longest sequence may need.
-const void* select_fn(int64_t per_lane) {
-  return per_lane <= 4    ? reinterpret_cast<const void*>(qlin_evict_select_kernel<4>)
-         : per_lane <= 16 ? reinterpret_cast<const void*>(qlin_evict_select_kernel<16>)
-         : per_lane <= 32 ? reinterpret_cast<const void*>(qlin_evict_select_kernel<32>)
-                          : reinterpret_cast<const void*>(qlin_evict_select_kernel<0>);
+struct Select {
+  const void* fn;
+  int threads;
+};
+template <int K, int THREADS>
+Select select_of() {
+  return {reinterpret_cast<const void*>(qlin_evict_select_kernel<K, THREADS>), THREADS};
+}
+Select select_fn(int64_t places, int cluster) {  // places of a block
+  if (cluster == 1 && places > 2048 && places <= 8192) return places <= 4096 ? select_of<4, 1024>() : select_of<8, 1024>();
+  return places <= 2048 ? select_of<4, 512>() : places <= 8192 ? select_of<16, 512>() : places <= 16384 ? select_of<32, 512>() : select_of<0, 512>();
 }
 const void* move_fn(int width) {
   return width == 64    ? reinterpret_cast<const void*>(qlin_evict_move_kernel<64>)
@@ -450,12 +469,13 @@ qlin_status evict_setup(EvictDevice** device) {
   std::call_once(d.once, [&d, dev] {
     cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
     int clusters = 1;
-    for (int per_lane : {4, 16, 32, 64}) {
-      const void* fn = select_fn(per_lane);
+    for (int64_t places : {2048, 8192, 16384, 16385}) {  // the ones that clusters run
+      const Select select = select_fn(places, MAX_CLUSTER);
+      const void* fn = select.fn;
       if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(MAX_CLUSTER, 1, 1);
-      cfg.blockDim = dim3(SELECT_THREADS, 1, 1);
+      cfg.blockDim = dim3((unsigned)select.threads, 1, 1);
       cudaLaunchAttribute attr;
       attr.id = cudaLaunchAttributeClusterDimension;
       attr.val.clusterDim.x = MAX_CLUSTER;
@@ -555,12 +575,16 @@ qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const qlin_kv_step* step, 
   most = most < room ? most : room;
   p.items = (int)items;
   p.cluster = 1;
-  while (p.cluster < d->most && p.cluster * 2048 < most && 2 * p.cluster * items <= 2 * d->sms) p.cluster *= 2;
-  const int64_t lanes = (int64_t)p.cluster * SELECT_THREADS;
+  // One block of 1024 threads per item spares the clusters' barriers (four items of
+  // 2094 tokens 8.9 us, against 10.2 in clusters of two; 128 of 4000 24.6 and 27.5,
+  // of 8000 42.0 and 47.3), but leaves SMs idle where items are few and long (eight of
+  // 8000 13.9 us against 13.3).
+  if (most > (2 * items >= d->sms ? 8192 : 4096))
+    while (p.cluster < d->most && p.cluster * 2048 < most && 2 * p.cluster * items <= 2 * d->sms) p.cluster *= 2;
+  const Select select = select_fn((most + p.cluster - 1) / p.cluster, p.cluster);
   void* args[] = {&p};
-  st = launch_step(select_fn((most + lanes - 1) / lanes), dim3((unsigned)(items * p.cluster), 1, 1),
-                   dim3(SELECT_THREADS, 1, 1), 0, static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0,
-                   p.cluster);
+  st = launch_step(select.fn, dim3((unsigned)(items * p.cluster), 1, 1), dim3((unsigned)select.threads, 1, 1), 0,
+                   static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0, p.cluster);
   if (st != QLIN_OK) return st;
   const int64_t groups = (items + MOVE_ITEMS - 1) / MOVE_ITEMS;
   int64_t blocks = (4 * d->sms + groups - 1) / groups;
