@@ -329,45 +329,63 @@ __global__ void __launch_bounds__(SELECT_THREADS, K > 16 ? 1 : 1024 / SELECT_THR
 // them copy it: 16 bytes a lane, keys and values of a row of 128 at once, eight
 // loads on their way per lane.
 template <int D>
-__global__ void __launch_bounds__(MOVE_THREADS) qlin_evict_move_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int starts[MOVE_ITEMS + 1];
+__global__ void __launch_bounds__(MOVE_THREADS, 4) qlin_evict_move_kernel(const __grid_constant__ EvictParams p) {
+  __shared__ int all_starts[MOVE_ITEMS + 1];
+  static_assert(MOVE_WARPS * 33 <= MOVE_ITEMS, "a copy per warp");
   __shared__ int warp_total[MOVE_WARPS];
   __shared__ __align__(16) longlong2 rows[MOVE_WARPS][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int item0 = blockIdx.y * MOVE_ITEMS, items = min(p.items - item0, MOVE_ITEMS);
+  int* starts = all_starts;
   pdl_wait();
   pdl_launch_dependents();
   // ---- where each item's moves begin
-  constexpr int PER = MOVE_ITEMS / MOVE_THREADS;
-  int count[PER], sum = 0;
+  if (items <= 32) {  // each warp for itself
+    const int2 chosen = lane < items ? p.chosen[item0 + lane] : make_int2(0, -1);
+    if (p.len_out && blockIdx.x == 0 && warp == 0 && lane < items && (item0 + lane) % p.cache.heads == 0 && chosen.y >= 0)
+      p.len_out[(item0 + lane) / p.cache.heads] = chosen.y;
+    int upto = chosen.x;
 #pragma unroll
-  for (int e = 0; e < PER; e++) {
-    const int i = tid * PER + e;
-    count[e] = 0;
-    if (i >= items) continue;
-    const int2 chosen = p.chosen[item0 + i];
-    count[e] = chosen.x;
-    if (p.len_out && blockIdx.x == 0 && (item0 + i) % p.cache.heads == 0 && chosen.y >= 0)
-      p.len_out[(item0 + i) / p.cache.heads] = chosen.y;
-    sum += chosen.x;
-  }
-  int inc = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(ALL, upto, o);
+      if (lane >= o) upto += a;
+    }
+    starts += warp * 33;
+    starts[lane + 1] = upto;
+    if (lane == 0) starts[0] = 0;
+    __syncwarp();
+  } else {
+    constexpr int PER = MOVE_ITEMS / MOVE_THREADS;
+    int count[PER], sum = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(ALL, inc, o);
-    if (lane >= o) inc += a;
-  }
-  if (lane == 31) warp_total[warp] = inc;
-  __syncthreads();
-  int at = inc - sum + (int)__reduce_add_sync(ALL, lane < warp ? warp_total[lane & (MOVE_WARPS - 1)] : 0);
+    for (int e = 0; e < PER; e++) {
+      const int i = tid * PER + e;
+      count[e] = 0;
+      if (i >= items) continue;
+      const int2 chosen = p.chosen[item0 + i];
+      count[e] = chosen.x;
+      if (p.len_out && blockIdx.x == 0 && (item0 + i) % p.cache.heads == 0 && chosen.y >= 0)
+        p.len_out[(item0 + i) / p.cache.heads] = chosen.y;
+      sum += chosen.x;
+    }
+    int inc = sum;
 #pragma unroll
-  for (int e = 0; e < PER; e++) {
-    const int i = tid * PER + e;
-    if (i < items) starts[i] = at;
-    at += count[e];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(ALL, inc, o);
+      if (lane >= o) inc += a;
+    }
+    if (lane == 31) warp_total[warp] = inc;
+    __syncthreads();
+    int at = inc - sum + (int)__reduce_add_sync(ALL, lane < warp ? warp_total[lane & (MOVE_WARPS - 1)] : 0);
+#pragma unroll
+    for (int e = 0; e < PER; e++) {
+      const int i = tid * PER + e;
+      if (i < items) starts[i] = at;
+      at += count[e];
+    }
+    if (tid == MOVE_THREADS - 1) starts[items] = at;
+    __syncthreads();
   }
-  if (tid == MOVE_THREADS - 1) starts[items] = at;
-  __syncthreads();
   const int64_t all = starts[items];
   const int warps = gridDim.x * MOVE_WARPS, w = blockIdx.x * MOVE_WARPS + warp;
   const int first = (int)(all * w / warps), end = (int)(all * (w + 1) / warps);
