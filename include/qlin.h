@@ -394,7 +394,10 @@ qlin_status qlin_forward_noalloc(int fmt, int prologue, int M, int64_t N, int64_
  * linears ("Doubling the LLM token rate in ComfyUI", section "Adaptive-tree
  * MTP": one committed token and a tree of drafted ones are verified in one
  * pass).  q/k/v (qlin_forward_multi) -> qlin_kv_append -> qlin_tree_attention
- * -> o (qlin_forward) ... -> qlin_sample -> qlin_kv_keep.
+ * -> o (qlin_forward) ... -> qlin_sample -> qlin_kv_keep.  With images or videos,
+ * a cache kept within its room, or rules on the logits: qlin_kv_append_at ->
+ * qlin_tree_attention_stats ... -> qlin_adjust_logits -> qlin_sample ->
+ * qlin_kv_weigh -> qlin_kv_keep -> qlin_kv_evict.
  *
  * The conventions above hold: device pointers, nothing allocated or
  * synchronised, errors of arguments returned before anything is enqueued.  The

@@ -4,8 +4,10 @@ The compute path is the C-ABI library ``libqlin.so`` (include/qlin.h): an
 in-place weight repack, a fused RMSNorm/SwiGLU + int8 quantisation prologue,
 and a TMA-streamed tensor-core GEMV with in-launch split-K reduction; and the
 rest of a decode or verification step around those linears: head norms, position
-rotation and the append to a paged cache, attention of a drafted tree over it,
-keeping an accepted path, and sampling.  This package holds its sources (``csrc/``), the nvcc build (``build.py``), the thin
+rotation (on several axes too) and the append to a paged cache, attention of a
+drafted tree over it, keeping an accepted path, accumulated attention weights of
+the cached tokens and eviction by them, penalties, biases and masks on logits,
+and sampling.  This package holds its sources (``csrc/``), the nvcc build (``build.py``), the thin
 ctypes binding (``qlin.py``) and the seeded synthetic input generators
 (``inputs.py``).
 """

@@ -3,8 +3,8 @@ beside it (``_qlin_binding.so``, g++, against the headers of the torch that is
 installed).
 
 Translation units compiled in parallel (the host API with the repack
-kernels, the sets of forward-kernel variants, and the append, attention and
-sampling kernels), one -gencode, shared CUDA runtime (so the library and PyTorch share one runtime
+kernels, the sets of forward-kernel variants, and the kernels around the
+cache and the logits), one -gencode, shared CUDA runtime (so the library and PyTorch share one runtime
 and one notion of the current device).  The output goes to
 ``w6a8_quantized_linear_gb300/_build/libqlin.so`` (git-ignored).
 """

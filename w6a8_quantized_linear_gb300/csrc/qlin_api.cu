@@ -525,7 +525,7 @@ qlin_status noalloc_scratch(void** out) {
 extern "C" {
 
 const char* qlin_version(void) {
-  return "qlin 0.4 (sm_103a: fused prologue + TMA-streamed fp16 mma.sync GEMV, cluster split-K; paged tree attention, sampling)";
+  return "qlin 0.5 (sm_103a: fused prologue + TMA-streamed fp16 mma.sync GEMV, cluster split-K; paged tree attention, eviction, sampling)";
 }
 
 const char* qlin_status_string(qlin_status s) {

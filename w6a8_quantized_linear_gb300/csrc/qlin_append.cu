@@ -69,13 +69,17 @@ __device__ __forceinline__ void store4(const float* x, DST* p) {
 // where a whole head turns, both of a pair are the lane's own.
 //   x' = x gamma / sqrt(mean(x^2) + eps);  (a, b) -> (a cos - b sin, b cos + a sin)
 // The angle is pos * turns[i] mod 1, exact in 64-bit integers whatever the
-// position, so only its last conversion to fp32 rounds.  Bound by the bytes of
+// position, so only its last conversion to fp32 rounds; pos is the row's place, or
+// its given position on the axis of pair i (two bits per pair, a word per warp, so
+// that a thread reads its own with the rows).  Bound by the bytes of
 // the rows for a prompt in fp32 (6 per element), by instruction issue in bf16
 // (74 % of cycles, DRAM at 36 %), by the launch for a step.
 // Measured, 4001 rows of 64 heads of 128: fp32 34.2 us (197 MB, 5.7 TB/s, 0.85
 // of the measured copy), bf16 29.6 us (131 MB; 40 us with half the loads in
 // flight).  A warp per head with four elements a lane issued three times the
-// instructions and was bound by them (48 us).
+// instructions and was bound by them (48 us).  At positions of three axes: 4098
+// rows of 64 heads of 128 in fp32 35.1 us (0.85 of the copy), 2411 of 32 heads of
+// 256 in bf16 21.8 us (79 MB; instruction issue: 190 a warp for 256 elements).
 template <typename SRC, typename DST, int D>
 __global__ void __launch_bounds__(APPEND_THREADS, 7) qlin_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LANES = D / 8, PASS = APPEND_THREADS / LANES;  // lanes of a head, heads of a pass
