@@ -28,11 +28,11 @@ struct AppendParams {
   int heads_per_block;
 };
 
-// A thread's two runs of four elements of a head, as they were loaded.
-template <typename SRC>
+// A thread's two runs of R elements of a head, as they were loaded.
+template <typename SRC, int R>
 struct Raw;
 template <>
-struct Raw<float> {
+struct Raw<float, 4> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* p, int half) {
     a = *reinterpret_cast<const float4*>(p);
@@ -42,30 +42,38 @@ struct Raw<float> {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
 };
-template <>
-struct Raw<__nv_bfloat16> {
-  uint2 a, b;
+template <int R>
+struct Raw<__nv_bfloat16, R> {
+  uint32_t w[R];  // two elements each
   __device__ __forceinline__ void load(const __nv_bfloat16* p, int half) {
-    a = *reinterpret_cast<const uint2*>(p);
-    b = *reinterpret_cast<const uint2*>(p + half);
+    if constexpr (R == 4) {
+      *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+      *reinterpret_cast<uint2*>(w + 2) = *reinterpret_cast<const uint2*>(p + half);
+    } else {
+      *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+      *reinterpret_cast<uint4*>(w + 4) = *reinterpret_cast<const uint4*>(p + half);
+    }
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+  __device__ __forceinline__ void get(float (&x)[2 * R]) const {
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
+    for (int e = 0; e < R; e++) {
       const float2 f = unpack2(w[e], __nv_bfloat16());
       x[2 * e] = f.x, x[2 * e + 1] = f.y;
     }
   }
 };
-template <typename DST>
-__device__ __forceinline__ void store4(const float* x, DST* p) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0], x[1], DST()), pack2(x[2], x[3], DST()));
+template <int R, typename DST>
+__device__ __forceinline__ void store_run(const float* x, DST* p) {
+  const uint2 lo = make_uint2(pack2(x[0], x[1], DST()), pack2(x[2], x[3], DST()));
+  if constexpr (R == 4)
+    *reinterpret_cast<uint2*>(p) = lo;
+  else
+    *reinterpret_cast<uint4*>(p) = make_uint4(lo.x, lo.y, pack2(x[4], x[5], DST()), pack2(x[6], x[7], DST()));
 }
 
-// One block per token row and run of heads; D / 8 lanes per head, so that a
-// warp's instructions work on up to four heads, and two or four passes' loads
-// in flight.  Lane l of a head holds elements 4 l .. 4 l + 3 of each half, so that
+// One block per token row and run of heads; D / (2 R) lanes per head, so that a
+// warp's instructions work on up to eight heads, and one to four passes' loads
+// in flight.  Lane l of a head holds elements R l .. R l + R - 1 of each half, so that
 // where a whole head turns, both of a pair are the lane's own.
 //   x' = x gamma / sqrt(mean(x^2) + eps);  (a, b) -> (a cos - b sin, b cos + a sin)
 // The angle is pos * turns[i] mod 1, exact in 64-bit integers whatever the
@@ -73,22 +81,25 @@ __device__ __forceinline__ void store4(const float* x, DST* p) {
 // its given position on the axis of pair i (two bits per pair, a word per warp, so
 // that a thread reads its own with the rows).  Bound by the bytes of
 // the rows for a prompt in fp32 (6 per element), by instruction issue in bf16
-// (74 % of cycles, DRAM at 36 %), by the launch for a step.
+// (0.67 of the cycles, DRAM at 29 %), by the launch for a step.
 // Measured, 4001 rows of 64 heads of 128: fp32 34.2 us (197 MB, 5.7 TB/s, 0.85
-// of the measured copy), bf16 29.6 us (131 MB; 40 us with half the loads in
-// flight).  A warp per head with four elements a lane issued three times the
-// instructions and was bound by them (48 us).  At positions of three axes: 4098
-// rows of 64 heads of 128 in fp32 35.1 us (0.85 of the copy), 2411 of 32 heads of
-// 256 in bf16 21.8 us (79 MB; instruction issue: 190 a warp for 256 elements).
-template <typename SRC, typename DST, int D>
-__global__ void __launch_bounds__(APPEND_THREADS, 7) qlin_append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int LANES = D / 8, PASS = APPEND_THREADS / LANES;  // lanes of a head, heads of a pass
-  constexpr int AHEAD = sizeof(SRC) == 4 ? 2 : 4, H = D / 2;  // passes in flight: 64 bytes a thread
+// of the measured copy), bf16 26.1 us (131 MB).  A warp per head with four elements
+// a lane issued three times the instructions and was bound by them (48 us).  At
+// positions of three axes: 4098 rows of 64 heads of 128 in fp32 35.1 us (0.85 of the
+// copy), 2411 of 32 heads of 256 in bf16 17.5 us (79 MB).
+// R = 8 where a bf16 prompt's rows fill a pass of blocks: twice the elements share a
+// lane's addresses, shuffles and root (30.4 and 21.9 us with R = 4).  One pass in
+// flight and eight blocks per SM then do better than two and seven (26.3 and 19.7).
+template <typename SRC, typename DST, int D, int R>
+__global__ void __launch_bounds__(APPEND_THREADS, R == 8 ? 8 : 7) qlin_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int LANES = D / (2 * R), PASS = APPEND_THREADS / LANES;  // lanes of a head, heads of a pass
+  constexpr int AHEAD = R == 8 ? 1 : sizeof(SRC) == 4 ? 2 : 4;  // passes in flight: 64 bytes a thread, or 32
+  constexpr int H = D / 2;
   __shared__ float2 cs[D / 2];                  // cos, sin of this row's angles
   __shared__ __align__(16) float gamma[2][D];   // of q, of k
   __shared__ float rows[PASS][D];
   const int row = blockIdx.x, b = row / p.step.T, t = row - b * p.step.T;
-  const int at4 = threadIdx.x % LANES * 4, slot = threadIdx.x / LANES;  // this thread's elements, its head of a pass
+  const int at0 = threadIdx.x % LANES * R, slot = threadIdx.x / LANES;  // this thread's elements, its head of a pass
   pdl_wait();
   pdl_launch_dependents();
   // everything that is read goes out before anything is waited for
@@ -96,11 +107,11 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) qlin_append_kernel(const __
   const int h = blockIdx.y * p.heads_per_block + slot;
   // the heads of a token: of q, then of k, then of v
   const int v0 = p.Hq + p.cache.heads;
-  const SRC* qs = static_cast<const SRC*>(p.q) + row * p.q_stride + at4;
-  const SRC* ks = static_cast<const SRC*>(p.k) + (row * p.k_stride - (int64_t)p.Hq * D) + at4;
-  const SRC* vs = static_cast<const SRC*>(p.v) + (row * p.v_stride - (int64_t)v0 * D) + at4;
-  auto load = [&](Raw<SRC>& x, int head) { x.load((head < p.Hq ? qs : head < v0 ? ks : vs) + head * D, H); };
-  Raw<SRC> x[AHEAD];
+  const SRC* qs = static_cast<const SRC*>(p.q) + row * p.q_stride + at0;
+  const SRC* ks = static_cast<const SRC*>(p.k) + (row * p.k_stride - (int64_t)p.Hq * D) + at0;
+  const SRC* vs = static_cast<const SRC*>(p.v) + (row * p.v_stride - (int64_t)v0 * D) + at0;
+  auto load = [&](Raw<SRC, R>& x, int head) { x.load((head < p.Hq ? qs : head < v0 ? ks : vs) + head * D, H); };
+  Raw<SRC, R> x[AHEAD];
 #pragma unroll
   for (int u = 0; u < AHEAD; u++)
     if (h + u * PASS < h1) load(x[u], h + u * PASS);
@@ -129,48 +140,66 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) qlin_append_kernel(const __
   if (at < 0 && threadIdx.x == 0) report(p.status, QLIN_ERR_BAD_INDEX);
   __syncthreads();
   // How a head turns: not at all; pairs, or whole halves, within the lane;
-  // a power of two of whole lanes, with lane ^ flip; any other, through shared
-  // memory.  The lane's cosines and sines are the same for all heads.
-  const int flip = !p.pairs && n && n < H && n % 4 == 0 && (n & (n - 1)) == 0 && 2 * n <= H ? n / 4 : 0;
+  // a power of two of whole lanes, with lane ^ flip (or, of half a lane, within
+  // it); any other, through shared memory.  The lane's cosines and sines are the
+  // same for all heads.
+  const bool across = !p.pairs && n && n < H && n % 4 == 0 && (n & (n - 1)) == 0 && 2 * n <= H;
+  const bool near = R == 8 && across && n == 4;
+  const int flip = across && !near ? n / R : 0;
   const bool own = !p.pairs && n == H;
-  float tc[4], ts[4];  // pairs: of elements 0 and 2 of each half; else of the first half's (flip: signed by its side)
+  float tc[R], ts[R];  // pairs: of the even elements of each half; else of the first half's (across: signed by its side)
 #pragma unroll
-  for (int e = 0; e < 4; e++) {
-    int i = at4 + e;
-    if (p.pairs) i = (e < 2 ? at4 + 2 * e : H + at4 + 2 * (e - 2)) / 2;
-    const bool second = flip && i >= n;
+  for (int e = 0; e < R; e++) {
+    int i = at0 + e;
+    if (p.pairs) i = (e < R / 2 ? at0 + 2 * e : H + at0 + 2 * (e - R / 2)) / 2;
+    const bool second = across && i >= n;
     if (second) i -= n;
     const float2 w = i < n ? cs[i] : make_float2(1.f, 0.f);
     tc[e] = w.x;
-    ts[e] = flip && !second ? -w.y : w.y;
+    ts[e] = across && !second ? -w.y : w.y;
   }
-  DST* const qd = static_cast<DST*>(p.q_out) + row * p.q_out_stride + at4;
-  auto finish = [&](float (&x)[8], int head) {
+  DST* const qd = static_cast<DST*>(p.q_out) + row * p.q_out_stride + at0;
+  auto finish = [&](float (&x)[2 * R], int head) {
     const bool is_q = head < p.Hq, is_v = head >= v0, here = head < h1;
     if (__any_sync(0xFFFFFFFFu, here && !is_v)) {  // all lanes: the warp's heads may differ in kind
       if (p.q_gamma || p.k_gamma) {
-        float ss = 0.f;
+        // (four elements of each half at a time, and those added last: one order of
+        // sums whatever a lane holds)
+        float part[R / 4];
 #pragma unroll
-        for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
+        for (int k = 0; k < R / 4; k++) {
+          part[k] = 0.f;
 #pragma unroll
-        for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+          for (int e = 0; e < 8; e++) {
+            const float y = x[e % 4 + 4 * k + e / 4 * R];
+            part[k] = fmaf(y, y, part[k]);
+          }
+        }
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1)
+#pragma unroll
+          for (int k = 0; k < R / 4; k++) part[k] += __shfl_xor_sync(0xFFFFFFFFu, part[k], o);
+        const float ss = R == 4 ? part[0] : part[0] + part[R / 4 - 1];
         const float a = ss * (1.0f / D) + p.eps;
         float r = rsqrtf(a);  // and a Newton step, to one ulp (a = 0 or infinite: as it is)
         const float d = fmaf(-a * r, r, 1.f);
         if (fabsf(d) < 1.f) r = fmaf(0.5f * r, d, r);
         if ((is_q ? p.q_gamma : p.k_gamma) && !is_v) {
-          const float* g = gamma[is_q ? 0 : 1] + at4;
-          const float4 g0 = *reinterpret_cast<const float4*>(g), g1 = *reinterpret_cast<const float4*>(g + H);
-          x[0] *= r * g0.x, x[1] *= r * g0.y, x[2] *= r * g0.z, x[3] *= r * g0.w;
-          x[4] *= r * g1.x, x[5] *= r * g1.y, x[6] *= r * g1.z, x[7] *= r * g1.w;
+          const float* g = gamma[is_q ? 0 : 1] + at0;
+#pragma unroll
+          for (int k = 0; k < R; k += 4) {
+            const float4 g0 = *reinterpret_cast<const float4*>(g + k), g1 = *reinterpret_cast<const float4*>(g + H + k);
+            x[k] *= r * g0.x, x[k + 1] *= r * g0.y, x[k + 2] *= r * g0.z, x[k + 3] *= r * g0.w;
+            x[R + k] *= r * g1.x, x[R + k + 1] *= r * g1.y, x[R + k + 2] *= r * g1.z, x[R + k + 3] *= r * g1.w;
+          }
         }
       }
       if (p.pairs) {
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const int i = e < 2 ? 2 * e : 4 + 2 * (e - 2);
+        for (int e = 0; e < R; e++) {
+          const int i = e < R / 2 ? 2 * e : R + 2 * (e - R / 2);
           const float u = x[i], w = x[i + 1];
-          if ((e < 2 ? at4 + 2 * e : H + at4 + 2 * (e - 2)) < 2 * n && !is_v) {
+          if ((e < R / 2 ? at0 + 2 * e : H + at0 + 2 * (e - R / 2)) < 2 * n && !is_v) {
             x[i] = u * tc[e] - w * ts[e];
             x[i + 1] = w * tc[e] + u * ts[e];
           }
@@ -178,25 +207,35 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) qlin_append_kernel(const __
       } else if (own) {
         if (!is_v)
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const float u = x[e], w = x[4 + e];
+          for (int e = 0; e < R; e++) {
+            const float u = x[e], w = x[R + e];
             x[e] = u * tc[e] - w * ts[e];
-            x[4 + e] = w * tc[e] + u * ts[e];
+            x[R + e] = w * tc[e] + u * ts[e];
           }
       } else if (flip) {
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
+        for (int e = 0; e < R; e++) {
           const float other = __shfl_xor_sync(0xFFFFFFFFu, x[e], flip);
-          if (at4 < 2 * n && !is_v) x[e] = x[e] * tc[e] + other * ts[e];
+          if (at0 < 2 * n && !is_v) x[e] = x[e] * tc[e] + other * ts[e];
+        }
+      } else if (near) {
+        if constexpr (R == 8) {
+          if (at0 == 0 && !is_v)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              const float u = x[e], w = x[e + 4];
+              x[e] = u * tc[e] + w * ts[e];
+              x[e + 4] = w * tc[e + 4] + u * ts[e + 4];
+            }
         }
       } else if (n) {
         float* mine = rows[slot];
 #pragma unroll
-        for (int e = 0; e < 8; e++) mine[at4 + e % 4 + e / 4 * H] = x[e];
+        for (int e = 0; e < 2 * R; e++) mine[at0 + e % R + e / R * H] = x[e];
         __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-          const int i = at4 + e % 4 + e / 4 * H;
+        for (int e = 0; e < 2 * R; e++) {
+          const int i = at0 + e % R + e / R * H;
           if (i < 2 * n && !is_v) {
             const float2 w = cs[i >= n ? i - n : i];
             x[e] = i >= n ? x[e] * w.x + mine[i - n] * w.y : x[e] * w.x - mine[i + n] * w.y;
@@ -207,12 +246,12 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) qlin_append_kernel(const __
     }
     if (!here) return;
     if (is_q) {
-      store4(x, qd + head * D);
-      store4(x + 4, qd + head * D + H);
+      store_run<R>(x, qd + head * D);
+      store_run<R>(x + R, qd + head * D + H);
     } else if (at >= 0) {
-      DST* dst = static_cast<DST*>(is_v ? p.cache.v : p.cache.k) + at + (head - (is_v ? v0 : p.Hq)) * p.cache.head_stride + at4;
-      store4(x, dst);
-      store4(x + 4, dst + H);
+      DST* dst = static_cast<DST*>(is_v ? p.cache.v : p.cache.k) + at + (head - (is_v ? v0 : p.Hq)) * p.cache.head_stride + at0;
+      store_run<R>(x, dst);
+      store_run<R>(x + R, dst + H);
     }
   };
   const int warp_first = h - slot + (int)(threadIdx.x & ~31u) / LANES;  // the same in all lanes of a warp
@@ -221,7 +260,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) qlin_append_kernel(const __
     for (int u = 0; u < AHEAD; u++) {
       const int head = h + off + u * PASS;
       if (warp_first + off + u * PASS >= h1) break;
-      float now[8];
+      float now[2 * R];
       x[u].get(now);
       if (head + AHEAD * PASS < h1) load(x[u], head + AHEAD * PASS);
       finish(now, head);
@@ -229,17 +268,19 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) qlin_append_kernel(const __
   }
 }
 
-template <typename SRC, typename DST>
+template <typename SRC, typename DST, int R>
 const void* append_fn_d(int width) {
-  return width == 64    ? reinterpret_cast<const void*>(qlin_append_kernel<SRC, DST, 64>)
-         : width == 128 ? reinterpret_cast<const void*>(qlin_append_kernel<SRC, DST, 128>)
-                        : reinterpret_cast<const void*>(qlin_append_kernel<SRC, DST, 256>);
+  return width == 64    ? reinterpret_cast<const void*>(qlin_append_kernel<SRC, DST, 64, R>)
+         : width == 128 ? reinterpret_cast<const void*>(qlin_append_kernel<SRC, DST, 128, R>)
+                        : reinterpret_cast<const void*>(qlin_append_kernel<SRC, DST, 256, R>);
 }
-const void* append_fn(int src, int dst, int width) {
+const void* append_fn(int src, int dst, int width, int run) {
   if (src == QLIN_F32)
-    return dst == QLIN_BF16 ? append_fn_d<float, __nv_bfloat16>(width) : append_fn_d<float, __half>(width);
-  return dst == QLIN_BF16 ? append_fn_d<__nv_bfloat16, __nv_bfloat16>(width)
-                          : append_fn_d<__nv_bfloat16, __half>(width);
+    return dst == QLIN_BF16 ? append_fn_d<float, __nv_bfloat16, 4>(width) : append_fn_d<float, __half, 4>(width);
+  if (run == 4)
+    return dst == QLIN_BF16 ? append_fn_d<__nv_bfloat16, __nv_bfloat16, 4>(width)
+                            : append_fn_d<__nv_bfloat16, __half, 4>(width);
+  return dst == QLIN_BF16 ? append_fn_d<__nv_bfloat16, __nv_bfloat16, 8>(width) : append_fn_d<__nv_bfloat16, __half, 8>(width);
 }
 
 // ---- keep ----------------------------------------------------------------------
@@ -397,11 +438,13 @@ static qlin_status append(const qlin_kv_cache* cache, const qlin_kv_step* step, 
   // a few blocks per SM where the step has that many heads, a whole row per block beyond
   const int64_t want = (1216 + rows - 1) / rows;
   int64_t per = (p.heads + want - 1) / want;
-  const int64_t pass = APPEND_THREADS / (D / 8);
+  // eight elements to a run where that leaves no lanes idle, and there is more than a step's rows
+  const int run = src == QLIN_BF16 && rows >= 64 && p.heads >= APPEND_THREADS / (D / 16) ? 8 : 4;
+  const int64_t pass = APPEND_THREADS / (D / (2 * run));
   per = (per + pass - 1) / pass * pass;
   p.heads_per_block = (int)per;
   void* args[] = {&p};
-  return launch_step(append_fn(src, cache->dtype, cache->width),
+  return launch_step(append_fn(src, cache->dtype, cache->width, run),
                      dim3((unsigned)rows, (unsigned)((p.heads + per - 1) / per), 1), dim3(APPEND_THREADS, 1, 1), 0,
                      static_cast<cudaStream_t>(stream), args, (flags & QLIN_FLAG_PDL) != 0);
 }
