@@ -752,6 +752,7 @@ qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logits, int64_t
  */
 #define QLIN_MAX_HISTORY 1000000
 #define QLIN_MAX_BIAS 1024
+#define QLIN_MAX_SEQUENCES 65535
 typedef struct {
   const int32_t *history, *history_len, *prompt_len, *draft, *mask;
   const float *repetition, *presence, *frequency;
@@ -763,6 +764,7 @@ typedef struct {
 } qlin_adjustments;
 
 /*
+ *   B           : 0..QLIN_MAX_SEQUENCES, B * T at most 2^24.
  *   V           : 1..524288.   dtype : QLIN_F32 or QLIN_BF16, of logits and out.
  *   logits, out : [B * T, V], rows ld and out_ld elements apart, aligned to the
  *                 element.  out may be the logits themselves (same rows; then

@@ -248,3 +248,43 @@ def test_lengths_and_tokens_far_outside():
     got = qlin.adjust_logits(x, history=long, history_len=i32([8, 2 ** 31 - 1, -2 ** 31, 3]),
                              prompt_len=i32([-2 ** 31, 5598, 0, 2 ** 31 - 1]), frequency=one).cpu()
     assert torch.equal(got, want)
+
+
+def test_more_rows_than_sequences():
+    """Rows that nothing tells apart, more of them than a call has sequences, from the logits' own memory and from a slice."""
+    M, V = 66000, 100
+    wide = torch.randn(M, V + 4, generator=torch.Generator().manual_seed(3)).bfloat16()
+    allowed = torch.randint(-2 ** 31, 2 ** 31, (M, 4), generator=torch.Generator().manual_seed(4), dtype=torch.int64).int()
+    bits = (allowed.long()[:, torch.arange(V) // 32] >> torch.arange(V) % 32) & 1
+    for x in (wide.to(DEV)[:, :V], wide[:, :V].contiguous().to(DEV)):
+        want = torch.where(bits == 1, wide[:, :V].float(), -math.inf)
+        want[:, 7] += torch.where(bits[:, 7] == 1, 2.0, 0.0)
+        for out in (None, torch.empty(M, V, dtype=BF, device=DEV)):
+            got = qlin.adjust_logits(x, out=out, allowed=allowed.to(DEV), bias_token=i32([7]), bias=torch.tensor([2.0], device=DEV))
+            assert torch.equal(got.cpu(), want.bfloat16())
+
+
+def test_arguments_of_the_two_ways_agree():
+    """The same operands as plain tensors (read by the extension) and as slices of wider ones (read one by one)."""
+    c = Case(3, 4, 5003, 600, F32, 11, 40, 0.5, True)
+    a = c.args()
+    x = c.logits.to(DEV)
+    plain = qlin.adjust_logits(x, out=torch.empty_like(x), **a)
+    slices = {}
+    for k, t in a.items():
+        if t is None or t.dim() < 2 or k in ("draft", "mask"):
+            slices[k] = t
+            continue
+        wide = torch.zeros(t.shape[0], t.shape[1] + 3, dtype=t.dtype, device=DEV)
+        wide[:, 2:-1] = t
+        slices[k] = wide[:, 2:-1]
+    assert torch.equal(qlin.adjust_logits(x, **slices), plain)
+    with pytest.raises(ValueError):
+        qlin.adjust_logits(x, out=torch.empty_like(x), **{**a, "history": a["history"].long()})
+    with pytest.raises(ValueError):
+        qlin.adjust_logits(x, out=torch.empty_like(x), **{**a, "presence": a["presence"][:2]})
+    with pytest.raises(ValueError, match="cpu"):
+        qlin.adjust_logits(x, out=torch.empty_like(x), **{**a, "allowed": a["allowed"].cpu()})
+    with pytest.raises(qlin.QlinError):
+        qlin.adjust_logits(x.half(), out=torch.empty_like(x.half()), **a)
+    c.check(plain)

@@ -328,3 +328,35 @@ def test_statistics_do_not_depend_on_what_shared_memory_held(dtype):
         results.append(attend(c, q, 8))
     for out, stats in results[1:]:
         assert torch.equal(stats, results[0][1]) and torch.equal(out.view(torch.int16), results[0][0].view(torch.int16))
+
+
+def test_arguments_of_the_two_ways_agree():
+    """The same operands as plain tensors (read by the extension) and as slices of wider ones (read one by one)."""
+    c = Case([500, 77], 3, 2, 64, 16, BF, seed=5, parents=[-1, 0, 0])
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(6, 4 * 64, generator=g).bfloat16().to(DEV)
+    _, stats = attend(c, q, 4)
+    keep, n_keep, score = i32([[0, 2, 0], [0, 1, 0]]), i32([2, 1]), torch.rand(2, 2, 520, generator=g).to(DEV)
+    position = torch.zeros(2, 2, 520, dtype=torch.int32, device=DEV)
+    plain = qlin.kv_weigh(c.cache, c.step, q, stats, score, keep=keep, n_keep=n_keep, score_out=torch.zeros_like(score), position_out=position)
+    wide_q = torch.zeros(6, 4 * 64 + 16, dtype=BF, device=DEV)
+    wide_q[:, 8:-8] = q
+    wide = torch.zeros(2, 2, 2, 530, device=DEV)
+    wide[:, 0, :, 5:525] = score
+    wide_keep = torch.zeros(2, 9, dtype=torch.int32, device=DEV)
+    wide_keep[:, 4:7] = keep
+    out = torch.zeros(2, 2, 600, device=DEV)[:, :, 3:523]
+    where = torch.zeros(2, 2, 600, dtype=torch.int32, device=DEV)[:, :, 3:523]
+    got = qlin.kv_weigh(c.cache, c.step, wide_q[:, 8:-8], stats, wide[:, 0, :, 5:525], keep=wide_keep[:, 4:7], n_keep=n_keep, score_out=out,
+                        position_out=where)
+    assert torch.equal(got, plain) and torch.equal(where, position)
+    with pytest.raises(ValueError, match="strides"):
+        qlin.kv_weigh(c.cache, c.step, q, stats, score, score_out=out, position_out=position)
+    with pytest.raises(ValueError, match="stats"):
+        qlin.kv_weigh(c.cache, c.step, q, stats[:, :2], score)
+    with pytest.raises(ValueError, match="n_keep"):
+        qlin.kv_weigh(c.cache, c.step, q, stats, score, keep=keep, n_keep=n_keep[:1])
+    with pytest.raises(qlin.QlinError):
+        qlin.kv_weigh(c.cache, c.step, q, stats, score, n_keep=n_keep)
+    with pytest.raises(qlin.QlinError):
+        qlin.kv_weigh(c.cache, c.step, q, stats, score, decay=math.nan)

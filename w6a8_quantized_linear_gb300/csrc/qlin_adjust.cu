@@ -487,7 +487,7 @@ extern "C" qlin_status qlin_adjust_logits(int B, int T, int64_t V, int dtype, co
   qlin_adjustments a = *adjustments;
   if (flags & ~QLIN_FLAG_PDL) return QLIN_ERR_INVALID_ARG;
   if (a.L < 0 || a.n_bias < 0) return QLIN_ERR_INVALID_ARG;
-  if (V > QLIN_SAMPLE_MAX_V || B > 65535 || T > 65535 * ROWS || (int64_t)B * T > (1 << 24) || a.L > QLIN_MAX_HISTORY ||
+  if (V > QLIN_SAMPLE_MAX_V || B > QLIN_MAX_SEQUENCES || T > 65535 * ROWS || (int64_t)B * T > (1 << 24) || a.L > QLIN_MAX_HISTORY ||
       a.n_bias > QLIN_MAX_BIAS || (a.draft && T > QLIN_MAX_TREE))
     return QLIN_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return QLIN_OK;

@@ -235,7 +235,7 @@ PyObject* adjust_logits(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       if (t && !of_sequences) of_sequences = t;
     if (!of_sequences && token && token->dim() == 2) of_sequences = token;
     if (of_sequences) want(of_sequences->dim() > 0);
-    const int64_t B = of_sequences ? of_sequences->size(0) : M;
+    const int64_t B = of_sequences ? of_sequences->size(0) : M > QLIN_MAX_SEQUENCES ? 1 : M;  // (rows that nothing tells apart)
     want(M > 0 && B > 0 && M % B == 0);
     const int64_t T = M / B;
     qlin_adjustments s = {};

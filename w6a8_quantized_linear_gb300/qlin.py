@@ -881,6 +881,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     return token
 
 
+_MAX_SEQUENCES = 65535  # of a call of adjust_logits
 # qlin_adjustments: eleven addresses, four strides, L and n_bias; packed, as that costs a call less than setting fields
 _ADJUSTMENTS = struct.Struct("@11P4q2i")
 
@@ -940,6 +941,8 @@ def adjust_logits(logits: torch.Tensor, out=None, history=None, history_len=None
     else:
         if bias_token is not None and bias_token.dim() == 2:
             B = len(bias_token)
+        elif M > _MAX_SEQUENCES:  # rows that nothing tells apart
+            B = 1
     if (B < 1 or M % B) if M else B != 0:
         raise ValueError(f"{M} rows of logits do not belong to {B} sequences")
     T = M // B if B else 0
