@@ -94,7 +94,7 @@ __device__ __forceinline__ uint2 staying(uint4 c, uint32_t before, uint32_t ties
 // and read by all; where a whole bin stays, what lies below need not be looked at.
 // Bound by latency: reads of the length and then of the scores, and per pass (two
 // as a rule) the atomics of hot bins, a cluster barrier and reads from the other
-// blocks.  17 us of 36 for 131000 tokens of 4 heads (64 blocks), and of 50 for 128
+// blocks.  17 us of 36 for 131000 tokens of 4 heads (64 blocks), 15 of 49 for 128
 // items of up to 9001; keys staged in shared memory and ranks by block-wide sums
 // took 33 and 25.
 template <int K, int SELECT_THREADS>
@@ -468,7 +468,8 @@ Select select_of() {
   return {reinterpret_cast<const void*>(qlin_evict_select_kernel<K, THREADS>), THREADS};
 }
 Select select_fn(int64_t places, int cluster) {  // places of a block
-  if (cluster == 1 && places > 2048 && places <= 8192) return places <= 4096 ? select_of<4, 1024>() : select_of<8, 1024>();
+  if (cluster == 1 && places > 2048 && places <= 16384)
+    return places <= 4096 ? select_of<4, 1024>() : places <= 8192 ? select_of<8, 1024>() : select_of<16, 1024>();
   return places <= 2048 ? select_of<4, 512>() : places <= 8192 ? select_of<16, 512>() : places <= 16384 ? select_of<32, 512>() : select_of<0, 512>();
 }
 const void* move_fn(int width) {
@@ -601,10 +602,10 @@ qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const qlin_kv_step* step, 
   p.items = (int)items;
   p.cluster = 1;
   // One block of 1024 threads per item spares the clusters' barriers (four items of
-  // 2094 tokens 8.9 us, against 10.2 in clusters of two; 128 of 4000 24.6 and 27.5,
-  // of 8000 42.0 and 47.3), but leaves SMs idle where items are few and long (eight of
-  // 8000 13.9 us against 13.3).
-  if (most > (2 * items >= d->sms ? 8192 : 4096))
+  // 2094 tokens 8.7 us, against 10.2 in clusters of two; 128 of 4000 24.6 and 27.5,
+  // of up to 12000 61.1 and 63.5), but leaves SMs idle where items are few and long
+  // (eight of 8000 13.9 us against 13.1).
+  if (most > (2 * items >= d->sms ? 16384 : 4096))
     while (p.cluster < d->most && p.cluster * 2048 < most && 2 * p.cluster * items <= 2 * d->sms) p.cluster *= 2;
   const Select select = select_fn((most + p.cluster - 1) / p.cluster, p.cluster);
   void* args[] = {&p};
