@@ -1,5 +1,6 @@
 // qlin_adjust_logits: penalties for repeated tokens, biases and a grammar's mask
 // on the rows of logits that sampling then reads.
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -15,8 +16,8 @@ constexpr int AHEAD = 4;              // vectors of 16 bytes in flight per threa
 constexpr int HISTORY_AHEAD = 8;      // tokens of the history in flight per thread
 constexpr int FIXES_AHEAD = 4;        // changed logits in flight per thread
 constexpr int CLUSTER = 4;            // blocks that share the reading of a long history
-constexpr int LONG_HISTORY = 4096;    // from here on (8 rows of 131071, 20011 tokens: 12.7 us with clusters, 15.6 without)
-constexpr int CLUSTER_SLICE = 2048;   // tokens of a block of theirs at most: each counts for all of them
+constexpr int LONG_HISTORY = 4096, VERY_LONG_HISTORY = 32768;
+constexpr int64_t CLUSTER_SLICE = 4096;  // tokens of a block of theirs at most: each counts for all of them
 constexpr int ROWS = QLIN_MAX_TREE;   // rows of a block at most
 constexpr int MAX_PAIRS = ROWS * ROWS / ADJUST_THREADS;
 
@@ -513,7 +514,6 @@ extern "C" qlin_status qlin_adjust_logits(int B, int T, int64_t V, int dtype, co
   int sms = 0;
   const qlin_status st = adjust_setup(&sms);
   if (st != QLIN_OK) return st;
-  const bool clusters = a.history && a.L > LONG_HISTORY && V > 4096;
   const Rows kind = a.draft ? Rows::DRAFTED : T > 1 ? Rows::SEVERAL : Rows::ONE;
   p.history_vectors = a.history && is_aligned(a.history, 16) && a.L % 4 == 0 && (B == 1 || a.history_stride % 4 == 0);
   // A thread's vectors of a block: AHEAD, or fewer where that leaves SMs idle; then
@@ -523,11 +523,20 @@ extern "C" qlin_status qlin_adjust_logits(int B, int T, int64_t V, int dtype, co
   const int64_t spare = is_aligned(logits, 16) && (M == 1 || ld % vec == 0) ? 0 : 1;
   const int64_t round = BLOCKS * sms;
   int64_t vectors = AHEAD * ADJUST_THREADS / rows;  // of a row, at most
-  if (clusters && (vectors - spare) * vec > CLUSTER_SLICE) vectors = CLUSTER_SLICE / vec + spare;
-  int64_t slices = (V + (vectors - spare) * vec - 1) / ((vectors - spare) * vec);
+  auto slices_of = [&](int64_t vectors) { return (V + (vectors - spare) * vec - 1) / ((vectors - spare) * vec); };
+  // Clusters where their smaller slices still make one round of blocks (8 rows of
+  // 131071 and 20011 tokens 12.8 us, 15.6 without), not where they make several (64
+  // rows of 131071 and 8000 tokens 73 us, 30 without), and again where the history
+  // is so long that reading it in each block costs more than the rounds (64 rows of
+  // 32000 and 60000 tokens 28 us, 42 without; but 64 of 131071 and 50000 83 and 74).
+  const int64_t fewer = std::min(vectors, CLUSTER_SLICE / vec + spare);
+  const int64_t in_clusters = (slices_of(fewer) + CLUSTER - 1) / CLUSTER * CLUSTER;
+  const bool clusters = a.history && V > 4096 && a.L > (in_clusters * groups <= round ? LONG_HISTORY : VERY_LONG_HISTORY);
+  if (clusters) vectors = fewer;
+  int64_t slices = clusters ? in_clusters : slices_of(vectors);
   const int64_t rounds = (slices * groups + round - 1) / round;
   slices = rounds * round / groups;  // at least as many
-  if (clusters) slices = (slices + CLUSTER - 1) / CLUSTER * CLUSTER;
+  if (clusters) slices = slices / CLUSTER * CLUSTER;
   const int64_t least = (V + slices * vec - 1) / (slices * vec) + spare;
   if (vectors > least) vectors = least;
   if (vectors < 128) vectors = 128;
