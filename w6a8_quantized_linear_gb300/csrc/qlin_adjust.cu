@@ -329,27 +329,47 @@ __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(con
         hold_biases();
       }
       if (!counts || a.n_bias > ADJUST_THREADS) __syncthreads();
-      // biases of one token are added up in the first one's place, in order, by one warp
-      if (tid < 32)
+      // A word names the first bias of its token; the others (few lists have any) are
+      // added to that one, in order.
+      constexpr uint32_t SLOT = 0x7FFu << 20;
+      auto first_of = [&](int k) {  // whether bias k is its token's first
+        const uint32_t word = words[bias_at[k]];
+        if (slot_of(word) != (uint32_t)k + 1) return false;
+        if (!(word & ~SLOT)) list[atomicAdd(&listed, 1)] = bias_at[k];
+        return true;
+      };
+      auto name = [&](int k) {
+        uint32_t* word = &words[bias_at[k]];
+        for (uint32_t old = *word; !slot_of(old) || slot_of(old) > (uint32_t)k + 1;) {
+          const uint32_t seen = atomicCAS(word, old, (old & ~SLOT) | (uint32_t)(k + 1) << 20);
+          if (seen == old) break;
+          old = seen;
+        }
+      };
+      auto add_others = [&] {  // one warp
         for (int k0 = 0; k0 < held; k0 += 32) {
-          const int k = k0 + tid;
-          const bool here = k < held;
-          const int at = here ? bias_at[k] : 0;
-          const uint32_t same = __match_any_sync(0xFFFFFFFFu, here ? at : -1 - tid);
-          const bool first = here && (same & ((1u << tid) - 1)) == 0, fresh = first && !slot_of(words[at]);
-          __syncwarp();
-          if (fresh) {
-            if (words[at] == 0) list[atomicAdd(&listed, 1)] = (uint16_t)at;
-            words[at] |= (uint32_t)(k + 1) << 20;
-          }
-          __syncwarp();
-          uint32_t again = __ballot_sync(0xFFFFFFFFu, here && !fresh);
+          const int k = k0 + tid, slot = k < held ? (int)slot_of(words[bias_at[k]]) : 0;
+          uint32_t again = __ballot_sync(0xFFFFFFFFu, k < held && slot != k + 1);
           while (again) {
-            if (tid == __ffs(again) - 1) bias[slot_of(words[at]) - 1] += bias[k];
+            if (tid == __ffs(again) - 1) bias[slot - 1] += bias[k];
             again &= again - 1;
             __syncwarp();
           }
         }
+      };
+      if (a.n_bias <= 32) {  // the first warp's
+        if (tid < 32) {
+          if (tid < held) name(tid);
+          __syncwarp();
+          if (__any_sync(0xFFFFFFFFu, tid < held && !first_of(tid))) add_others();
+        }
+      } else {
+        for (int k = tid; k < held; k += ADJUST_THREADS) name(k);
+        __syncthreads();
+        bool others = false;
+        for (int k = tid; k < held; k += ADJUST_THREADS) others |= !first_of(k);
+        if (__syncthreads_or(others) && tid < 32) add_others();
+      }
     }
     if (a.n_bias || DRAFTS)
       any_draft = __syncthreads_or(DRAFTS && tid < p.T && draft[tid] >= 0 && (uint32_t)(draft[tid] - v0) < (uint32_t)n);
