@@ -467,10 +467,17 @@ template <int K, int THREADS>
 Select select_of() {
   return {reinterpret_cast<const void*>(qlin_evict_select_kernel<K, THREADS>), THREADS};
 }
+constexpr int64_t SIZES[4] = {2048, 8192, 16384, 16385};  // of the blocks that make clusters (the last: any more)
+int size_of(int64_t places) { return places <= SIZES[0] ? 0 : places <= SIZES[1] ? 1 : places <= SIZES[2] ? 2 : 3; }
 Select select_fn(int64_t places, int cluster) {  // places of a block
   if (cluster == 1 && places > 2048 && places <= 16384)
     return places <= 4096 ? select_of<4, 1024>() : places <= 8192 ? select_of<8, 1024>() : select_of<16, 1024>();
-  return places <= 2048 ? select_of<4, 512>() : places <= 8192 ? select_of<16, 512>() : places <= 16384 ? select_of<32, 512>() : select_of<0, 512>();
+  switch (size_of(places)) {
+    case 0: return select_of<4, 512>();
+    case 1: return select_of<16, 512>();
+    case 2: return select_of<32, 512>();
+    default: return select_of<0, 512>();
+  }
 }
 const void* move_fn(int width) {
   return width == 64    ? reinterpret_cast<const void*>(qlin_evict_move_kernel<64>)
@@ -481,7 +488,8 @@ const void* move_fn(int width) {
 struct EvictDevice {
   std::once_flag once;
   qlin_status ready = QLIN_ERR_CUDA;
-  int most = 8;  // CTAs of a cluster
+  int most = 8;     // CTAs of a cluster
+  int at_once[4] = {};  // clusters of 16 that find room at the same time, by their blocks' size
   int sms = 0;
 };
 EvictDevice g_evict[64];
@@ -494,9 +502,9 @@ qlin_status evict_setup(EvictDevice** device) {
   EvictDevice& d = g_evict[dev];
   std::call_once(d.once, [&d, dev] {
     cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    int clusters = 1;
-    for (int64_t places : {2048, 8192, 16384, 16385}) {  // the ones that clusters run
-      const Select select = select_fn(places, MAX_CLUSTER);
+    int clusters = 64;
+    for (int size = 0; size < 4; size++) {
+      const Select select = select_fn(SIZES[size], MAX_CLUSTER);
       const void* fn = select.fn;
       if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       cudaLaunchConfig_t cfg = {};
@@ -513,6 +521,7 @@ qlin_status evict_setup(EvictDevice** device) {
         (void)cudaGetLastError();
         n = 0;
       }
+      d.at_once[size] = n;
       if (n < clusters) clusters = n;
     }
     if (clusters > 0) d.most = MAX_CLUSTER;
@@ -604,9 +613,13 @@ qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const qlin_kv_step* step, 
   // One block of 1024 threads per item spares the clusters' barriers (four items of
   // 2094 tokens 8.7 us, against 10.2 in clusters of two; 128 of 4000 24.6 and 27.5,
   // of up to 12000 61.1 and 63.5), but leaves SMs idle where items are few and long
-  // (eight of 8000 13.9 us against 13.1).
+  // (eight of 8000 13.9 us against 13.1).  Clusters of 16 (one item of 93375 tokens
+  // 14.4 us, 18.5 with eight) where all find room at once: they are placed within a
+  // part of the device (16 items of 60000 41.6 us, 35.2 with eight).
   if (most > (2 * items >= d->sms ? 16384 : 4096))
-    while (p.cluster < d->most && p.cluster * 2048 < most && 2 * p.cluster * items <= 2 * d->sms) p.cluster *= 2;
+    while (p.cluster < d->most && p.cluster * 2048 < most && 2 * p.cluster * items <= 2 * d->sms &&
+           (p.cluster < 8 || items <= d->at_once[size_of((most + MAX_CLUSTER - 1) / MAX_CLUSTER)]))
+      p.cluster *= 2;
   const Select select = select_fn((most + p.cluster - 1) / p.cluster, p.cluster);
   void* args[] = {&p};
   st = launch_step(select.fn, dim3((unsigned)(items * p.cluster), 1, 1), dim3((unsigned)select.threads, 1, 1), 0,
