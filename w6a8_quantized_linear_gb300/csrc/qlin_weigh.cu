@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
         }
         seg++;
       } while (ok && next_item<TILE, GAP>(p, w));
-      if (!ok && elect_one()) {  // the products in flight end before tensor memory is freed
+      // whichever role gave up, the products in flight end before tensor memory is freed
+      if (__any_sync(ALL, !ok || *(volatile int*)&s->dead) && elect_one()) {
         mma_commit(&s->drained);
         (void)mbar_wait(&s->drained, 0);
       }
