@@ -623,8 +623,10 @@ qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, c
  *   T            : 1..32 rows per sequence, T * Hq / heads <= 128.
  *   ws           : a workspace (256 bytes) for the status word, or NULL.
  *   flags        : 0 or QLIN_FLAG_PDL.
- * Scores and sums are fp32.  A key that is not finite makes its own token's score
- * not finite and no other's.  Places of tokens that are not there, and whole
+ * Scores and sums are fp32.  A row whose statistics are not finite (a key that it
+ * sees, or its own query, is not) weighs nothing in that cache head, as one that
+ * saw nothing does; a key that is not finite may make its own token's score not
+ * finite, and no other's.  Places of tokens that are not there, and whole
  * sequences with len[b] < 0, are left as they were.  Where scores pass 2^23 (log2
  * units), and fp32 holds them a unit or more apart, a weight is no more than 1.
  */

@@ -360,3 +360,46 @@ def test_arguments_of_the_two_ways_agree():
         qlin.kv_weigh(c.cache, c.step, q, stats, score, n_keep=n_keep)
     with pytest.raises(qlin.QlinError):
         qlin.kv_weigh(c.cache, c.step, q, stats, score, decay=math.nan)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("poison", [math.nan, math.inf])
+@pytest.mark.parametrize("place", [17, 202])  # a committed token; row 2's own, which rows 0 and 1 do not see
+def test_a_key_that_is_not_finite_before_attention(dtype, poison, place):
+    """Rows whose softmax has become NaN by it weigh nothing in that cache head; what other rows and heads give is what it was,
+    and what stays by the scores stays."""
+    c = Case([200], 3, 2, 64, 16, dtype, seed=2, parents=[-1, 0, 0])
+    q = torch.randn(3, 4 * 64, generator=torch.Generator().manual_seed(3)).to(dtype).to(DEV)
+    start = torch.rand(1, 2, 203, generator=torch.Generator().manual_seed(4)).to(DEV)
+    _, stats = attend(c, q, 4)
+    want = qlin.kv_weigh(c.cache, c.step, q, stats, start, score_out=torch.zeros_like(start), decay=0.5)
+    without = qlin.kv_weigh(c.cache, c.step, q, stats, start, score_out=torch.zeros_like(start), decay=0.5, keep=i32([[0, 1, 0]]),
+                            n_keep=i32([2]))
+    p, r = c.places(0, place, 1)
+    c.k[p, 0, r] = poison  # infinities of both signs in the products: NaN
+    _, stats = attend(c, q, 4)
+    assert not stats.view(3, 2, 2, 2)[2, 0, :, 1].isfinite().any()
+    got = qlin.kv_weigh(c.cache, c.step, q, stats, start, score_out=torch.zeros_like(start), decay=0.5)
+    assert torch.equal(got[0, 1], want[0, 1])
+    others = [i for i in range(203) if i != place]
+    if place == 17:  # no row of the head weighs anything
+        assert torch.equal(got[0, 0, :200][others[:199]], 0.5 * start[0, 0, :200][others[:199]]) and (got[0, 0, 200:] == 0).all()
+    else:
+        assert torch.equal(got[0, 0, others], without[0, 0, others])
+    c.step.len.fill_(203)
+    best = got[0].nan_to_num(nan=-1.0).topk(60, -1).values.sort(-1).values
+    qlin.kv_evict(c.cache, c.step, got, i32([60]))
+    assert torch.equal(got[0, :, :60].sort(-1).values, best)
+
+
+def test_a_query_row_that_is_not_finite():
+    """It weighs nothing; the other rows weigh what they did."""
+    c = Case([300], 3, 2, 128, 32, BF, seed=2, parents=[-1, 0, 0])
+    q = torch.randn(3, 4 * 128, generator=torch.Generator().manual_seed(3)).bfloat16().to(DEV)
+    _, stats = attend(c, q, 4)
+    without = qlin.kv_weigh(c.cache, c.step, q, stats, torch.zeros(1, 2, 303, device=DEV), keep=i32([[0, 2, 0]]), n_keep=i32([2]))
+    q[1] = math.nan
+    _, stats = attend(c, q, 4)
+    got = qlin.kv_weigh(c.cache, c.step, q, stats, torch.zeros(1, 2, 303, device=DEV))
+    assert torch.equal(got[:, :, :301], without[:, :, :301]) and (got[:, :, 301] == 0).all()
+    assert torch.equal(got[:, :, 302], without[:, :, 301])

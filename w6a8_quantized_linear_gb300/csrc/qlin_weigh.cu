@@ -269,22 +269,20 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
         weighing_bar(true);
         const int n = s->rows, cols = n * p.group;
         const int64_t row0 = (int64_t)w.b * p.step.T;
-        for (int c = tid; c < cols; c += WEIGHING) {
-          const int i = c / p.group, head = w.h * p.group + c % p.group;
-          const float2 rl = p.stats[(row0 + s->kept[i]) * ((int64_t)p.group * p.cache.heads) + head];
-          float* st = reinterpret_cast<float*>(&s->stat[c / 2]) + c % 2;
-          st[0] = rl.y == 0.f ? -INFINITY : -rl.x;
-          st[2] = rl.y == 0.f ? 0.f : 1.f / rl.y;
-          if (fabsf(rl.x) >= FAR && rl.y != 0.f) s->far = 1;
-        }
-        for (int c = cols + tid; c < p.Rp; c += WEIGHING) {  // columns that weigh nothing
-          float* st = reinterpret_cast<float*>(&s->stat[c / 2]) + c % 2;
-          st[0] = -INFINITY, st[2] = 0.f;
-        }
+        static_assert(WEIGHING >= MAX_ROWS, "a thread per column");
+        float2 rl = make_float2(0.f, 0.f);  // a column that weighs nothing
+        if (tid < cols)
+          rl = p.stats[(row0 + s->kept[tid / p.group]) * ((int64_t)p.group * p.cache.heads) + w.h * p.group + tid % p.group];
         // the query rows, swizzled as the keys are by TMA: a thread's units of 16 bytes
         // (the same place of every STEP-th row) all on their way at once
         constexpr int UNITS = D / 8, STEP = WEIGHING / UNITS, MOST = MAX_ROWS / STEP;
         const int u = tid % UNITS;
+        auto put = [&](int c, uint4 x) {
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_smem + (u / 8) * panel_bytes + c * 128 +
+                                                                        (((u & 7) ^ (c & 7)) << 4)),
+                       "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                       : "memory");
+        };
         uint4 v[MOST];
 #pragma unroll
         for (int k = 0; k < MOST; k++) {
@@ -294,17 +292,28 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
             v[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (row0 + s->kept[c / p.group]) * p.q_stride +
                                                    (int64_t)(w.h * p.group + c % p.group) * D + u * 8);
         }
+        // a row that saw nothing, or whose softmax is NaN by a key or a query that is not finite, weighs nothing
+        const bool weighs = rl.y > 0.f && rl.y < INFINITY && fabsf(rl.x) < INFINITY;
+        if (tid < p.Rp) {
+          float* st = reinterpret_cast<float*>(&s->stat[tid / 2]) + tid % 2;
+          st[0] = weighs ? -rl.x : -INFINITY;
+          st[2] = weighs ? 1.f / rl.y : 0.f;
+          if (weighs && fabsf(rl.x) >= FAR) s->far = 1;
+        }
 #pragma unroll
         for (int k = 0; k < MOST; k++) {
           const int c = tid / UNITS + k * STEP;
-          if (c < p.Rp)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_smem + (u / 8) * panel_bytes + c * 128 +
-                                                                          (((u & 7) ^ (c & 7)) << 4)),
-                         "r"(v[k].x), "r"(v[k].y), "r"(v[k].z), "r"(v[k].w)
-                         : "memory");
+          if (c < p.Rp) put(c, v[k]);
         }
         fence_proxy_async_smem();
-        weighing_bar(true);
+        if (!weighing_bar(weighs || tid >= cols)) {  // such a row's query becomes zeros: one that is not finite would reach every token
+          for (int c = tid / UNITS; c < cols; c += STEP) {
+            const float4 st = s->stat[c / 2];
+            if ((c & 1 ? st.w : st.z) == 0.f) put(c, make_uint4(0, 0, 0, 0));
+          }
+          fence_proxy_async_smem();
+          weighing_bar(true);
+        }
         if (tid == 0) mbar_arrive(&s->q_full);
         const bool far = s->far != 0;
         const int64_t len = p.step.len[w.b];

@@ -762,8 +762,8 @@ def kv_weigh(cache: KVCache, step: KVStep, q: torch.Tensor, stats: torch.Tensor,
     ``n_keep`` as in ``kv_keep`` (call this before it): the accepted path; without
     them all rows are kept.  The kept rows' own tokens get theirs at the places
     that ``kv_keep`` gives them, and ``position_out`` (int32, like score, optional)
-    their positions: ``at`` (int32 [B * T]), or len + depth.  Returns ``score_out``
-    (in place unless given)."""
+    their positions: ``at`` (int32 [B * T]), or len + depth.  A row whose statistics
+    are not finite weighs nothing.  Returns ``score_out`` (in place unless given)."""
     n, D, dev = step.B * step.T, cache.width, cache._index
     if stream is None and 0 <= dev == step._index and dev == _current_device():
         status = (_binding or _load_binding()).kv_weigh(
