@@ -626,9 +626,10 @@ qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, c
  * Scores and sums are fp32.  A row whose statistics are not finite (a key that it
  * sees, or its own query, is not) weighs nothing in that cache head, as one that
  * saw nothing does; a key that is not finite may make its own token's score not
- * finite, and no other's.  Places of tokens that are not there, and whole
- * sequences with len[b] < 0, are left as they were.  Where scores pass 2^23 (log2
- * units), and fp32 holds them a unit or more apart, a weight is no more than 1.
+ * finite, and no other's.  Places of tokens that are not there, or lie
+ * on a page out of range, and whole sequences with len[b] < 0, are left as they
+ * were.  Where scores pass 2^23 (log2 units), and fp32 holds them a unit or more
+ * apart, a weight is no more than 1.
  */
 qlin_status qlin_kv_weigh(const qlin_kv_cache* cache, const qlin_kv_step* step, int Hq, const void* q, int64_t q_stride,
                           const float* stats, float scale, const int32_t* keep, int64_t keep_stride,

@@ -403,3 +403,25 @@ def test_a_query_row_that_is_not_finite():
     got = qlin.kv_weigh(c.cache, c.step, q, stats, torch.zeros(1, 2, 303, device=DEV))
     assert torch.equal(got[:, :, :301], without[:, :, :301]) and (got[:, :, 301] == 0).all()
     assert torch.equal(got[:, :, 302], without[:, :, 301])
+
+
+@pytest.mark.parametrize("apart", [False, True], ids=["in place", "apart"])
+def test_tokens_on_a_page_out_of_range_are_left_as_they_were(apart):
+    """Committed ones, and a step's own; the others of the sequence get what they got."""
+    c = Case([50, 60], 4, 2, 64, 16, BF, seed=2)
+    q = torch.randn(8, 2 * 64, generator=torch.Generator().manual_seed(3)).bfloat16().to(DEV)
+    _, stats = attend(c, q, 2)
+    start = torch.rand(2, 2, 70, generator=torch.Generator().manual_seed(4)).to(DEV)
+    want = qlin.kv_weigh(c.cache, c.step, q, stats, start, score_out=torch.zeros_like(start), decay=0.5)
+    table = c.table.clone()
+    table[0, 3], table[1, 1] = -1, 1 << 28
+    step = qlin.KVStep(table.to(DEV), c.step.len, 4, depth=c.step.depth, mask=c.step.mask)
+    out, ws = torch.full_like(start, 7.0) if apart else start.clone(), qlin.new_workspace(256, DEV)
+    before = out.clone()
+    position = torch.full((2, 2, 70), -5, dtype=torch.int32, device=DEV)
+    qlin.kv_weigh(c.cache, step, q, stats, start if apart else out, score_out=out, position_out=position, decay=0.5, ws=ws)
+    assert qlin.read_device_status(ws) == qlin.ERR_BAD_INDEX
+    lost = torch.zeros(2, 2, 70, dtype=torch.bool, device=DEV)
+    lost[0, :, 48:] = lost[1, :, 16:32] = lost[1, :, 64:] = True
+    assert torch.equal(out[lost], before[lost]) and torch.equal(out[~lost], want[~lost])
+    assert (position[0] == -5).all() and (position[1, :, :60] == -5).all() and position[1, 0, 60:64].tolist() == [60, 61, 62, 63]

@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
         const float* score = p.score + w.b * p.seq_stride + w.h * p.head_stride;
         float* score_out = p.score_out + w.b * p.out_seq_stride + w.h * p.out_head_stride;
         int32_t* position_out = p.position_out ? p.position_out + w.b * p.out_seq_stride + w.h * p.out_head_stride : nullptr;
+        const int32_t* table = p.step.page_table + w.b * p.step.table_stride;
 
         for (int t = 0; t < (int)w.n; t++, m++) {
           if ((int)(m % SETS) != set) continue;
@@ -327,9 +328,10 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
           const bool old = token < len && token < w.tokens;
           const int r = old || token >= w.tokens ? -1 : (int)(token - len), place = r >= 0 ? s->own[r] : -1;
           const int64_t to = place >= 0 ? len + place : token;
-          const bool here = (old || place >= 0) && to < p.room;
+          const bool known = (old || place >= 0) && to < p.room;
           if ((old || place >= 0) && to >= p.room) report(p.status, QLIN_ERR_BAD_INDEX);
-          const float before = old && here ? score[token] : 0.f;
+          const int page = known ? table[token >> p.page_shift] : -1;
+          const float before = old && known ? score[token] : 0.f;
           const uint32_t acc = m % ACCUMULATORS;
           ok = __all_sync(0xFFFFFFFFu, role_wait(&s->acc_full[acc], m / ACCUMULATORS & 1, s, p.status));
           if (!ok) break;
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
           __syncwarp();
           if (lane == 0) mbar_arrive(&s->acc_free[acc]);
           const float weight = ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
-          if (here) {
+          if (page >= 0 && page < p.cache.pages) {  // (of one out of range the ring holds another tile's keys)
             score_out[to] = old ? fmaf(p.decay, before, weight) : weight;
             if (!old && position_out) {
               const int64_t row = row0 + r;
