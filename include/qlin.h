@@ -617,7 +617,8 @@ qlin_status qlin_kv_keep(const qlin_kv_cache* cache, const qlin_kv_step* step, c
  *   score, score_out, position_out, the strides, room : as for qlin_kv_evict
  *                  (score_out may be score); position_out may be NULL.  Neither
  *                  shares memory with q, stats and at (QLIN_ERR_INVALID_ARG).
- *                  What would lie at room or behind is left out and reported.
+ *                  What would lie at room or behind is left out and reported,
+ *                  as are committed tokens and kept rows behind the page table.
  *   at           : int32 [B * T]: the rows' positions, as given to
  *                  qlin_kv_append_at; NULL: len + depth.
  *   T            : 1..32 rows per sequence, T * Hq / heads <= 128.

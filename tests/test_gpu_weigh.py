@@ -425,3 +425,24 @@ def test_tokens_on_a_page_out_of_range_are_left_as_they_were(apart):
     lost[0, :, 48:] = lost[1, :, 16:32] = lost[1, :, 64:] = True
     assert torch.equal(out[lost], before[lost]) and torch.equal(out[~lost], want[~lost])
     assert (position[0] == -5).all() and (position[1, :, :60] == -5).all() and position[1, 0, 60:64].tolist() == [60, 61, 62, 63]
+
+
+def test_tokens_behind_the_table_are_reported():
+    """Committed ones, and kept rows' own; rows that are not kept may lie behind it."""
+    for lens, keep, status in (([50, 60], None, 0), ([50, 61], None, qlin.ERR_BAD_INDEX), ([64, 64], [], 0), ([63, 60], [0], 0),
+                               ([63, 62], [0, 2], qlin.ERR_BAD_INDEX), ([62, 3], [1], 0), ([50, 70], [], qlin.ERR_BAD_INDEX),
+                               ([200, -1], [0], qlin.ERR_BAD_INDEX), ([-1, 0], [0, 1, 2, 3], 0)):
+        c = Case(lens, 4, 2, 64, 16, BF, seed=2)
+        q = torch.randn(8, 2 * 64, generator=torch.Generator().manual_seed(3)).bfloat16().to(DEV)
+        _, stats = attend(c, q, 2)
+        lists = {} if keep is None else dict(keep=i32([keep + [0] * (4 - len(keep))] * 2), n_keep=i32([len(keep)] * 2))
+        start = torch.rand(2, 2, 210, generator=torch.Generator().manual_seed(4)).to(DEV)
+        want = qlin.kv_weigh(c.cache, c.step, q, stats, start, score_out=start.clone(), decay=0.5, **lists)
+        step = qlin.KVStep(c.table[:, :4].to(DEV), c.step.len, 4)
+        ws = qlin.new_workspace(256, DEV)
+        got = qlin.kv_weigh(c.cache, step, q, stats, start, score_out=start.clone(), decay=0.5, ws=ws, **lists)
+        assert qlin.read_device_status(ws) == status, (lens, keep)
+        for b, n in enumerate(lens):
+            kept = [r for r in (range(4) if keep is None else keep) if n >= 0 and n + r < 64]
+            end = min(max(n, 0) + len(kept), 64)
+            assert torch.equal(got[b, :, :end], want[b, :, :end]) and torch.equal(got[b, :, max(end, 64):], start[b, :, max(end, 64):])

@@ -94,7 +94,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 
 // The item's rows and what they see, by one warp.
 __device__ __forceinline__ void item_rows(const WeighParams& p, int b, WeighShared* s) {
-  const int lane = threadIdx.x & 31, rows = step_rows(p.step, b);
+  const int lane = threadIdx.x & 31, len = p.step.len[b], rows = step_rows(p.step, b);
   s->own[lane] = -1;
   s->seen[lane] = 0;
   __syncwarp();
@@ -123,7 +123,13 @@ __device__ __forceinline__ void item_rows(const WeighParams& p, int b, WeighShar
     }
     if (lane < n) s->kept[lane] = lane, s->own[lane] = lane;
   }
-  if (lane == 0) s->rows = n, s->far = 0;
+  __syncwarp();
+  if (lane == 0) {
+    s->rows = n, s->far = 0;
+    // committed tokens and kept rows' own behind the table are left out
+    if (len + (int64_t)(n ? s->kept[n - 1] + 1 : 0) > (int64_t)p.step.max_pages * p.cache.page_size)
+      report(p.status, QLIN_ERR_BAD_INDEX);
+  }
 }
 
 // X = K Q^T on tcgen05, a tile of 128 tokens as the rows (lanes of tensor memory)
