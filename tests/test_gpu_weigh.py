@@ -446,3 +446,21 @@ def test_tokens_behind_the_table_are_reported():
             kept = [r for r in (range(4) if keep is None else keep) if n >= 0 and n + r < 64]
             end = min(max(n, 0) + len(kept), 64)
             assert torch.equal(got[b, :, :end], want[b, :, :end]) and torch.equal(got[b, :, max(end, 64):], start[b, :, max(end, 64):])
+
+
+@pytest.mark.parametrize("copy", [9, 13, 26])
+def test_a_wait_that_expires_far_into_a_run(copy):
+    """Behind the ring's first round and the accumulators' first use."""
+    n = 152 * 128 * 16
+    c = Case([n], 2, 1, 128, 256, BF, seed=2)
+    q = torch.randn(2, 4 * 128, generator=torch.Generator().manual_seed(3)).bfloat16().to(DEV)
+    _, stats = attend(c, q, 4)
+    ws = qlin.new_workspace(256, DEV)
+    start = torch.rand(1, 1, n + 2, device=DEV)
+    want = qlin.kv_weigh(c.cache, c.step, q, stats, start.clone(), ws=ws)
+    assert qlin.debug_kv_weigh_fault(c.cache, c.step, q, stats, start.clone(), ws, copy) == 0
+    torch.cuda.synchronize()
+    assert qlin.read_device_status(ws) == qlin.ERR_DEVICE_TIMEOUT
+    ws = qlin.new_workspace(256, DEV)
+    assert torch.equal(qlin.kv_weigh(c.cache, c.step, q, stats, start.clone(), ws=ws), want)
+    assert qlin.read_device_status(ws) == 0

@@ -236,9 +236,10 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
         const int tiles = __shfl_sync(0xFFFFFFFFu, (int)w.n, 0);
         for (int t = 0; t < tiles && ok; t++, m++) {
           const uint32_t acc = m % ACCUMULATORS, d = tmem + acc * MAX_ROWS;
-          if (m >= ACCUMULATORS) ok = role_wait(&s->acc_free[acc], (m / ACCUMULATORS - 1) & 1, s, p.status);
+          if (m >= ACCUMULATORS)
+            ok = __all_sync(ALL, role_wait(&s->acc_free[acc], (m / ACCUMULATORS - 1) & 1, s, p.status));
           for (int e = 0; e < PANELS && ok; e++) {
-            ok = __all_sync(0xFFFFFFFFu, ok && role_wait(&s->full[slot], phase, s, p.status));
+            ok = __all_sync(0xFFFFFFFFu, role_wait(&s->full[slot], phase, s, p.status));
             if (!ok) break;
             tc_fence_after();
             const uint32_t at = __shfl_sync(0xFFFFFFFFu, slot, 0), kb = ring + at * SLOT_BYTES, qb = q_smem + e * panel_bytes;
@@ -252,7 +253,6 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
             __syncwarp();
             if (++slot == (uint32_t)p.slots) slot = 0, phase ^= 1;
           }
-          ok = __all_sync(0xFFFFFFFFu, ok);
         }
         seg++;
       } while (ok && next_item<TILE, GAP>(p, w));
