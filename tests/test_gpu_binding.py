@@ -1,0 +1,45 @@
+"""The two ways through the Python binding of the step calls: that the short one gives and takes what the other does, and that
+nothing but its speed depends on it."""
+import threading
+import time
+
+import pytest
+import torch
+
+from gpu_util import DEV, built
+from w6a8_quantized_linear_gb300 import qlin
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    built()
+    torch.cuda.set_device(DEV)
+
+
+def test_other_threads_run_while_a_launch_waits():
+    """A stream's queue of launches is full behind a kernel of most of a second: who launches into it waits, no other thread."""
+    x = torch.randn(1, 64, device=DEV)
+    out = torch.empty_like(x)
+    qlin.adjust_logits(x, out=out)
+    torch.cuda.synchronize()
+    took = []
+
+    def launch():
+        t = time.perf_counter()
+        for _ in range(4000):  # more than a queue holds
+            qlin.adjust_logits(x, out=out)
+        took.append(time.perf_counter() - t)
+
+    thread = threading.Thread(target=launch)
+    torch.cuda._sleep(1_500_000_000)
+    last, gap = time.perf_counter(), 0.0
+    thread.start()
+    while thread.is_alive():
+        time.sleep(1e-3)
+        now = time.perf_counter()
+        gap, last = max(gap, now - last), now
+    thread.join()
+    torch.cuda.synchronize()
+    assert took[0] > 0.4 and gap < 0.2, (took, gap)

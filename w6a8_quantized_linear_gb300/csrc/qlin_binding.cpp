@@ -86,6 +86,19 @@ size_t bytes_of(const at::Tensor* t) {
   return (size_t)t->numel();
 }
 
+// A call of the library, its arguments formed before, while other threads run: a
+// launch waits where the stream's queue is full.  (What the arguments name is held
+// by the caller's frame.)
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename... P, typename... A>
+qlin_status unlocked(qlin_status (*call)(P...), A... a) {
+  const Unlocked other_threads_run;
+  return call(a...);
+}
+
 template <typename F>
 PyObject* guarded(PyObject* const* args, Py_ssize_t n, F&& f) {
   try {
@@ -129,8 +142,8 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const auto* turn = nt ? data<const uint64_t>(turns) : nullptr;
     if (!position) {
       want(axis == Py_None);
-      return qlin_kv_append(cache, step, (int)Hq, src, data(q), Hq * D, data(k), heads * D, data(v), heads * D, q_gamma,
-                            k_gamma, eps, turn, (int)nt, pairs, data(q_out), Hq * D, data(ws), bytes_of(ws), flags, stream);
+      return unlocked(qlin_kv_append, cache, step, (int)Hq, src, data(q), Hq * D, data(k), heads * D, data(v), heads * D,
+                      q_gamma, k_gamma, eps, turn, (int)nt, pairs, data(q_out), Hq * D, data(ws), bytes_of(ws), flags, stream);
     }
     want((position->dim() == 1 || position->dim() == 2) && position->size(0) == n);
     const int64_t axes = position->dim() == 2 ? position->size(1) : 1;
@@ -140,9 +153,9 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       axis_of = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(axis));
     }
     want(axes <= QLIN_MAX_AXES);
-    return qlin_kv_append_at(cache, step, (int)Hq, src, data(q), Hq * D, data(k), heads * D, data(v), heads * D, q_gamma,
-                             k_gamma, eps, turn, (int)nt, pairs, data<const int32_t>(position), axes, (int)axes, axis_of,
-                             data(q_out), Hq * D, data(ws), bytes_of(ws), flags, stream);
+    return unlocked(qlin_kv_append_at, cache, step, (int)Hq, src, data(q), Hq * D, data(k), heads * D, data(v), heads * D,
+                    q_gamma, k_gamma, eps, turn, (int)nt, pairs, data<const int32_t>(position), axes, (int)axes, axis_of,
+                    data(q_out), Hq * D, data(ws), bytes_of(ws), flags, stream);
   });
 }
 
@@ -183,10 +196,10 @@ PyObject* kv_weigh(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const at::Tensor* ws = a.tensor();
     const unsigned flags = (unsigned)a.integer();
     void* stream = a.address();
-    return qlin_kv_weigh(cache, step, (int)Hq, data(q), Hq * D, data<const float>(stats), scale, data<const int32_t>(keep), T,
-                         n_keep, decay, scores_of(score, B, heads, room), heads * room, room,
-                         scores_of(score_out ? score_out : score, B, heads, room), positions_of(position_out, B, heads, room),
-                         heads * room, room, room, at_, data(ws), bytes_of(ws), flags, stream);
+    return unlocked(qlin_kv_weigh, cache, step, (int)Hq, data(q), Hq * D, data<const float>(stats), scale,
+                    data<const int32_t>(keep), T, n_keep, decay, scores_of(score, B, heads, room), heads * room, room,
+                    scores_of(score_out ? score_out : score, B, heads, room), positions_of(position_out, B, heads, room),
+                    heads * room, room, room, at_, data(ws), bytes_of(ws), flags, stream);
   });
 }
 
@@ -208,10 +221,10 @@ PyObject* kv_evict(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const unsigned flags = (unsigned)a.integer();
     void* stream = a.address();
     want(ws && n_keep && first >= 0 && first <= INT32_MAX);
-    return qlin_kv_evict(cache, step, scores_of(score, B, heads, room), positions_of(position, B, heads, room), heads * room, room,
-                         scores_of(score_out ? score_out : score, B, heads, room),
-                         positions_of(position_out ? position_out : position, B, heads, room), heads * room, room, room, n_keep,
-                         (int)first, since, len_out, data(ws), bytes_of(ws), flags, stream);
+    return unlocked(qlin_kv_evict, cache, step, scores_of(score, B, heads, room), positions_of(position, B, heads, room),
+                    heads * room, room, scores_of(score_out ? score_out : score, B, heads, room),
+                    positions_of(position_out ? position_out : position, B, heads, room), heads * room, room, room, n_keep,
+                    (int)first, since, len_out, data(ws), bytes_of(ws), flags, stream);
   });
 }
 
@@ -264,7 +277,7 @@ PyObject* adjust_logits(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     s.repetition = data<const float>(repetition), s.presence = data<const float>(presence);
     s.frequency = data<const float>(frequency), s.bias_token = data<const int32_t>(token), s.bias = data<const float>(bias);
     s.allowed = data<const int32_t>(allowed);
-    return qlin_adjust_logits((int)B, (int)T, V, code_of(logits), data(logits), V, data(out), V, &s, flags, stream);
+    return unlocked(qlin_adjust_logits, (int)B, (int)T, V, code_of(logits), data(logits), V, data(out), V, &s, flags, stream);
   });
 }
 
