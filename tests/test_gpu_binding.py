@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from gpu_util import DEV, built
+from test_gpu_step import BF, Case
 from w6a8_quantized_linear_gb300 import qlin
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +44,12 @@ def test_other_threads_run_while_a_launch_waits():
     thread.join()
     torch.cuda.synchronize()
     assert took[0] > 0.4 and gap < 0.2, (took, gap)
+
+
+def test_pairs_is_any_truth_value():
+    c = Case([7], 3, 2, 64, 16, BF, seed=2, fill=False)
+    q = torch.randn(3, 4 * 64, generator=torch.Generator().manual_seed(3)).to(DEV)
+    turns, out = qlin.rope_turns(1e4, 64, device=DEV), [torch.empty(3, 4 * 64, dtype=BF, device=DEV) for _ in range(3)]
+    for o, pairs in zip(out, (True, 2, "yes")):
+        qlin.kv_append(c.cache, c.step, q, turns=turns, pairs=pairs, q_out=o)
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])

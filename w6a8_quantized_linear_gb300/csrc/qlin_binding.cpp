@@ -124,7 +124,7 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const float *q_gamma = a.floats(D), *k_gamma = a.floats(D);
     const float eps = (float)a.number();
     const at::Tensor* turns = a.tensor(at::kLong);
-    const int pairs = (int)a.integer();
+    const int pairs = a.integer() != 0;
     const at::Tensor *q_out = a.tensor(), *ws = a.tensor();
     const unsigned flags = (unsigned)a.integer();
     void* stream = a.address();
