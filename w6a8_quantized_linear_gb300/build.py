@@ -22,6 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libqlin.so")
 BINDING = os.path.join(BUILD, "_qlin_binding.so")
+STAMP = BINDING + ".torch"  # what the binding was built for; not there while a build is under way
+HEADER = os.path.join(INCLUDE, "qlin.h")
 UNITS = ["qlin_api.cu", "qlin_kernels_w4.cu", "qlin_kernels_w6.cu", "qlin_kernels_codebook.cu",
          "qlin_kernels_moe_w4.cu", "qlin_kernels_moe_w6.cu", "qlin_kernels_export_w4.cu", "qlin_kernels_export_w6.cu",
          "qlin_kernels_tc.cu", "qlin_kernels_tc_export.cu", "qlin_kernels_w4_one_row.cu", "qlin_kernels_w6_one_row.cu",
@@ -31,7 +33,7 @@ UNITS = ["qlin_api.cu", "qlin_kernels_w4.cu", "qlin_kernels_w6.cu", "qlin_kernel
 SOURCES = [os.path.join(CSRC, f) for f in UNITS + ["qlin_forward.cuh", "qlin_forward_tc.cuh", "qlin_repack.cuh", "qlin_layout.h",
                                                    "qlin_ptx.cuh", "qlin_instances.h", "qlin_step.h", "qlin_tiles.cuh",
                                                    "qlin_sample_weight.h"]] + [
-    os.path.join(INCLUDE, "qlin.h")]
+    HEADER]
 
 
 def nvcc_path() -> str:
@@ -47,11 +49,30 @@ def nvcc_path() -> str:
 BINDING_SOURCE = os.path.join(CSRC, "qlin_binding.cpp")
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def stamp() -> str:
+    """What an extension depends on beside its sources: the torch and the Python that are installed."""
+    import torch
+    return f"torch {torch.__version__} abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')}\n"
+
+
+def binding_fits() -> bool:
+    """Whether the extension was built whole, with the library that lies beside it, for this torch and Python."""
+    try:
+        with open(STAMP) as f:
+            return f.read() == stamp()
+    except OSError:
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(s) <= t for s in SOURCES) and os.path.getmtime(BINDING_SOURCE) <= os.path.getmtime(BINDING)
+
+
+def up_to_date() -> bool:
+    if not os.path.exists(LIB) or not os.path.exists(BINDING) or not binding_fits():
+        return False
+
+    def newer(target, sources):
+        t = os.path.getmtime(target)
+        return all(os.path.getmtime(s) <= t for s in sources)
+
+    return newer(LIB, SOURCES) and newer(BINDING, [BINDING_SOURCE, HEADER])
 
 
 def _torch_folder() -> str:
@@ -122,8 +143,13 @@ def _compile_and_link(nvcc, cuda_lib, common, tag, verbose):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc link failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if os.path.exists(STAMP):
+        os.remove(STAMP)
     os.replace(tmp, LIB)
     logs.append(_link_binding(binding, tag))
+    with open(STAMP + tag, "w") as f:
+        f.write(stamp())
+    os.replace(STAMP + tag, STAMP)
     if verbose:
         print("".join(logs) + r.stdout + r.stderr)
     return LIB
