@@ -1,10 +1,11 @@
-"""When the library and the binding's extension are built again."""
+"""When the library and the binding's extension are built again, and when the extension is not loaded."""
 import os
 
 import pytest
 import torch
 
-from w6a8_quantized_linear_gb300 import build
+import __graft_entry__
+from w6a8_quantized_linear_gb300 import build, qlin
 
 
 @pytest.fixture
@@ -70,3 +71,14 @@ def test_a_build_that_ends_between_the_library_and_the_extension_is_not_taken_fo
         build.build_library(force=True)
     assert os.path.getmtime(build.LIB) > 10000  # replaced
     assert not build.up_to_date() and not build.binding_fits()
+
+
+def test_what_takes_an_extensions_place_refers_every_call_to_the_other_way(tmp_path, monkeypatch):
+    __graft_entry__.build()
+    monkeypatch.setattr(qlin, "_binding", None)
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_qlin_binding.so"))
+    with pytest.warns(RuntimeWarning, match="_qlin_binding"):
+        binding = qlin._load_binding()
+    assert qlin._load_binding() is binding
+    for call in ("kv_append", "kv_weigh", "kv_evict", "adjust_logits"):
+        assert getattr(binding, call)(0, 1, None) is None

@@ -7,7 +7,8 @@ if the library is missing, every call raises.
 Calls whose arguments are all contiguous tensors of the right types on the
 current device, with nothing to be allocated, take a short way through a small
 extension (``csrc/qlin_binding.cpp``) that reads the tensors itself (4 to 7 us a
-call less); all others are looked at here, argument by argument.
+call less); all others are looked at here, argument by argument, and so are those
+of a program whose torch the extension was not built for (a warning says so).
 
 Names follow the C ABI in ``include/qlin.h`` without the ``qlin_`` prefix.
 """
@@ -18,6 +19,7 @@ import importlib.util
 import os
 import struct
 import threading
+import warnings
 
 import torch
 
@@ -119,18 +121,28 @@ def lib() -> ctypes.CDLL:
 _binding = None
 
 
+class _NoBinding:
+    """In the extension's place where it cannot be loaded: no call is for the short way."""
+    kv_append = kv_weigh = kv_evict = adjust_logits = staticmethod(lambda *args: None)
+
+
 def _load_binding():
     """The short way's extension, loaded with the library that it calls."""
     global _binding
     lib()
     with _lock:
         if _binding is None:
-            if not os.path.exists(_build.BINDING):
-                raise RuntimeError(f"_qlin_binding.so is not built ({_build.BINDING}); run __graft_entry__.build() "
-                                   "or python -m w6a8_quantized_linear_gb300.build")
-            spec = importlib.util.spec_from_file_location("_qlin_binding", _build.BINDING)
-            module = importlib.util.module_from_spec(spec)
-            spec.loader.exec_module(module)
+            try:
+                if not _build.binding_fits():
+                    raise ImportError("it was not built for this torch and Python")
+                spec = importlib.util.spec_from_file_location("_qlin_binding", _build.BINDING)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+            except ImportError as e:
+                warnings.warn(f"_qlin_binding.so is not loaded, and calls take some microseconds longer: {e}; run "
+                              "__graft_entry__.build() or python -m w6a8_quantized_linear_gb300.build", RuntimeWarning,
+                              stacklevel=3)
+                module = _NoBinding
             _binding = module
     return _binding
 
