@@ -734,7 +734,8 @@ qlin_status qlin_sample(int M, int64_t V, int dtype, const void* logits, int64_t
  * path of drafted tokens.  Then, in fp32, rounded once at the end,
  *   x' = x / r if x > 0, else x * r   where v stands in the history or the path
  *   x' = x' - frequency * n - presence            where n > 0
- *   x' = x' + the biases of v, in the list's order
+ *   x' = x' + bias                 of v; several of them are first added to one
+ *                                  another, in the list's order, in fp32
  *   x' = -inf                                     where v is not allowed.
  * A logit that none of these concerns is copied as it is.  Any pointer may be
  * NULL: what it would give is left out.  The struct is host memory, read during

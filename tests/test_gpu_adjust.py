@@ -288,3 +288,18 @@ def test_arguments_of_the_two_ways_agree():
     with pytest.raises(qlin.QlinError):
         qlin.adjust_logits(x.half(), out=torch.empty_like(x.half()), **a)
     c.check(plain)
+
+
+@pytest.mark.parametrize("n", [3, 40, 700])
+def test_biases_of_one_token_are_added_to_one_another_first(n):
+    """In the list's order, in fp32: of 1e8, 1 and -1e8 nothing is left to be added to the logit."""
+    V = 5000
+    x = torch.ones(2, V, device=DEV)
+    token, bias = torch.arange(100, 100 + n, dtype=torch.int32).repeat(2, 1), torch.zeros(2, n)
+    token[:, [0, n // 2, n - 1]] = i32([7, 7, 7]).cpu()
+    bias[0, [0, n // 2, n - 1]] = torch.tensor([1e8, 1.0, -1e8])
+    bias[1, [0, n // 2, n - 1]] = torch.tensor([1e8, -1e8, 1.0])
+    got = qlin.adjust_logits(x, bias_token=token.to(DEV), bias=bias.to(DEV)).cpu()
+    want = torch.ones(2, V)
+    want[1, 7] = 2.0
+    assert torch.equal(got, want)

@@ -922,10 +922,11 @@ def adjust_logits(logits: torch.Tensor, out=None, history=None, history_len=None
     [B, T] and ``mask`` (as in ``KVStep``): the step's tokens, of which a row
     sees its own path's.  Tokens seen: divided (multiplied, where not above 0)
     by ``repetition``; tokens generated n times: less frequency * n + presence
-    (fp32 [B] each).  ``bias_token`` int32 and ``bias`` fp32 [B, n] or [n]: added.
-    ``allowed`` int32 [B * T, ceil(V / 32)] or [ceil(V / 32)]: a bit per token,
-    the others become -inf.  B is the rows of history, draft, or a penalty; else
-    of bias_token; without any of these, each row is its own sequence."""
+    (fp32 [B] each).  ``bias_token`` int32 and ``bias`` fp32 [B, n] or [n]: added
+    (those of one token to one another first, in order).  ``allowed`` int32
+    [B * T, ceil(V / 32)] or [ceil(V / 32)]: a bit per token, the others become
+    -inf.  B is the rows of history, draft, or a penalty; else of bias_token;
+    without any of these, each row is its own sequence."""
     dev = logits.get_device()
     if stream is None and 0 <= dev == _current_device():
         status = (_binding or _load_binding()).adjust_logits(
