@@ -303,3 +303,27 @@ def test_biases_of_one_token_are_added_to_one_another_first(n):
     want = torch.ones(2, V)
     want[1, 7] = 2.0
     assert torch.equal(got, want)
+
+
+def test_operands_of_no_width():
+    """A history or lists of biases of width 0: as if not given; through both ways of the binding."""
+    x = torch.randn(6, 500, generator=torch.Generator().manual_seed(1)).to(DEV)
+    none, nothing = torch.zeros(2, 0, dtype=torch.int32, device=DEV), torch.zeros(2, 0, device=DEV)
+    one = torch.ones(2, device=DEV)
+    for kw in (dict(history=none, presence=one, repetition=2 * one), dict(history=none, history_len=i32([0, 5]), prompt_len=i32([3, 0]), frequency=one),
+               dict(bias_token=none, bias=nothing), dict(bias_token=none[0], bias=nothing[0]), dict(history=none, bias_token=none, bias=nothing)):
+        assert torch.equal(qlin.adjust_logits(x, **kw), x)
+        assert torch.equal(qlin.adjust_logits(x, out=torch.empty_like(x), **kw), x)
+        y = x.clone()
+        assert qlin.adjust_logits(y, out=y, **kw) is y and torch.equal(y, x)
+        draft = i32([[3, 4, 3], [9, 9, 9]])  # beside them, what does count
+        got = qlin.adjust_logits(x, **kw, draft=draft, **({} if "presence" in kw else dict(presence=one)))
+        want = x.clone()
+        for m in range(6):
+            for v in set(draft[m // 3, : m % 3 + 1].tolist()):
+                y = want[m, v]
+                if "repetition" in kw:
+                    y = y / 2 if y > 0 else y * 2
+                n = draft[m // 3, : m % 3 + 1].tolist().count(v)
+                want[m, v] = y - (n if "frequency" in kw else 0) - 1
+        assert torch.equal(got, want)
