@@ -327,3 +327,31 @@ def test_operands_of_no_width():
                 n = draft[m // 3, : m % 3 + 1].tolist().count(v)
                 want[m, v] = y - (n if "frequency" in kw else 0) - 1
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("case", [(2, 3, 20000, 6000, F32, 9, 0.7), (3, 40, 9001, 5000, BF, 0, None), (40, 2, 33001, 33000, BF, 3, None),
+                                  (40, 2, 131071, 8000, F32, 3, None)], ids=["0", "1", "2", "3"])
+def test_several_rows_without_drafts_under_a_long_history(case):
+    """By clusters, where these make one round of blocks or the history is very long; by single blocks else."""
+    B, T, V, L, dtype, n_bias, allowed = case
+    c = Case(B, T, V, L, dtype, V, n_bias, allowed)
+    x = c.logits.to(DEV)
+    got = qlin.adjust_logits(x, **c.args())
+    c.check(got, rows=sorted({0, 1, B * T - 1, B * T // 2}))
+    qlin.adjust_logits(x, out=x, **c.args())
+    assert torch.equal(x, got)
+
+
+@pytest.mark.parametrize("case", [(2, 1, 50000, F32, False), (64, 1, 131071, BF, False), (3, 5, 20000, BF, True), (1, 8, 131071, F32, True)],
+                         ids=["0", "1", "2", "3"])
+def test_a_history_much_wider_than_its_lengths(case):
+    """The same values as from a history cut to them; what lies behind the lengths is anything."""
+    B, T, V, dtype, drafts = case
+    c = Case(B, T, V, 1000, dtype, 5, 4, None, drafts)
+    a = c.args()
+    x = c.logits.to(DEV)
+    want = qlin.adjust_logits(x, **a)
+    c.check(want, rows=sorted({0, B * T - 1}))
+    wide = torch.randint(0, V, (B, 40000), generator=torch.Generator().manual_seed(6), dtype=torch.int32)
+    wide[:, :1000] = c.history
+    assert torch.equal(qlin.adjust_logits(x, **{**a, "history": wide.to(DEV)}), want)

@@ -261,3 +261,16 @@ def test_workspaces_shared_by_two_graphs_one_after_the_other():
             m = int(k[b])
             want = e.score[b, :, : e.lens[b]].sort(-1, descending=True).values[:, :m]
             assert torch.equal(o[b, :, :m].cpu().sort(-1, descending=True).values, want) and (o[b, :, m:] == 0).all()
+
+
+@pytest.mark.parametrize("lens, heads, room, width", [([300, 50], 2, 100000, 64), ([5000], 8, 60000, 128), ([100 + 9 * i for i in range(45)], 2, 20000, 64)],
+                         ids=["0", "1", "2"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_room_and_table_much_wider_than_the_lengths(lens, heads, room, width, in_place):
+    """As a program has them that captures its step once: clusters with hardly anything to do, keys not held in registers."""
+    e = Evict(lens, heads, width, 16, seed=12, room=room, kind="ties")
+    c = e.c
+    table = torch.full((len(lens), -(-room // 16)), -7, dtype=torch.int32)
+    table[:, : c.table.shape[1]] = c.table
+    c.step = qlin.KVStep(table.to(DEV), c.step.len, 1)
+    e.run([max(1, n // 3) for n in lens], 2, [n - 8 for n in lens], in_place=in_place, len_in_place=in_place)
