@@ -72,13 +72,15 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { re
 // up its own slice's counts.  A block that nothing concerns leaves behind the copy.
 //
 // Without a history the copy runs at the memory's rate: 64 rows of 262144 in bf16,
-// 67 MB, 11.5 us.  With 4096 tokens of history 23.5 us: per block the tokens, the
+// 67 MB, 11.8 us.  With 4096 tokens of history 23.9 us: per block the tokens, the
 // counts, the listed logits and their way back are waited for one after the other,
 // by two blocks per SM (registers), four rounds of them.  Blocks that stay and go
 // through slices with the next one's vectors on their way took 33 us (spills, and
 // fewer phases side by side); three blocks per SM, 28.
 // 8 rows of 131071 with a history of 20011 tokens 13 us (the cluster's barrier and
-// sums 5 of them; 15.6 with every block reading it all), one row of 32000 3.5 us.
+// sums 5 of them; 15.6 with every block reading it all), one row of 32000 3.7 us.
+// Biases found by the whole block and blocks that leave early cost the 64 rows 0.9
+// of their us, for 4.9 of 12.9 with 300 biases and 1.5 of 21.7 with 30 rows of 200321.
 template <typename T, bool CLUSTERS, Rows KIND>
 __global__ void __launch_bounds__(ADJUST_THREADS, BLOCKS) qlin_adjust_kernel(const __grid_constant__ AdjustParams p) {
   constexpr int VEC = 16 / sizeof(T), C = CLUSTERS ? CLUSTER : 1;
@@ -548,7 +550,11 @@ extern "C" qlin_status qlin_adjust_logits(int B, int T, int64_t V, int dtype, co
   // 131071 and 20011 tokens 12.8 us, 15.6 without), not where they make several (64
   // rows of 131071 and 8000 tokens 73 us, 30 without), and again where the history
   // is so long that reading it in each block costs more than the rounds (64 rows of
-  // 32000 and 60000 tokens 28 us, 42 without; but 64 of 131071 and 50000 83 and 74).
+  // 32000 and 60000 tokens 28 us, 42 without).  That border lies at one length for
+  // all vocabularies, and too low for large ones: 64 rows of 131071 and 50000 tokens
+  // take 83 us, 74 without.  The length is the history's width, as those in use are
+  // known on the device alone: 8000 tokens in one of 40000 take those rows 71 us, 29
+  // in one of 8000.
   const int64_t fewer = std::min(vectors, CLUSTER_SLICE / vec + spare);
   const int64_t in_clusters = (slices_of(fewer) + CLUSTER - 1) / CLUSTER * CLUSTER;
   const bool clusters = a.history && V > 4096 && a.L > (in_clusters * groups <= round ? LONG_HISTORY : VERY_LONG_HISTORY);

@@ -80,8 +80,9 @@ __device__ __forceinline__ void store_run(const float* x, DST* p) {
 // position, so only its last conversion to fp32 rounds; pos is the row's place, or
 // its given position on the axis of pair i (two bits per pair, a word per warp, so
 // that a thread reads its own with the rows).  Bound by the bytes of
-// the rows for a prompt in fp32 (6 per element), by instruction issue in bf16
-// (0.67 of the cycles, DRAM at 29 %), by the launch for a step.
+// the rows for a prompt in fp32 (6 per element), by the launch for a step; in bf16
+// by no unit alone (issue 0.67 of the cycles, DRAM 29 %, warps 43 %): a block's start
+// (length, page, angles, a barrier) stands before each row's work.
 // Measured, 4001 rows of 64 heads of 128: fp32 34.2 us (197 MB, 5.7 TB/s, 0.85
 // of the measured copy), bf16 26.1 us (131 MB).  A warp per head with four elements
 // a lane issued three times the instructions and was bound by them (48 us).  At

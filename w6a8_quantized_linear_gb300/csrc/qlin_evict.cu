@@ -615,7 +615,10 @@ qlin_status qlin_kv_evict(const qlin_kv_cache* cache, const qlin_kv_step* step, 
   // of up to 12000 61.1 and 63.5), but leaves SMs idle where items are few and long
   // (eight of 8000 13.9 us against 13.1).  Clusters of 16 (one item of 93375 tokens
   // 14.4 us, 18.5 with eight) where all find room at once: they are placed within a
-  // part of the device (16 items of 60000 41.6 us, 35.2 with eight).
+  // part of the device (16 items of 60000 41.6 us, 35.2 with eight).  All this goes by
+  // what the table and the scores have room for, as lengths are known on the device
+  // alone: with eight times the room four heads of 131000 tokens take 57 us, 36 without
+  // (their keys are formed again in each pass), 128 items of up to 9001 70 and 48.
   if (most > (2 * items >= d->sms ? 16384 : 4096))
     while (p.cluster < d->most && p.cluster * 2048 < most && 2 * p.cluster * items <= 2 * d->sms &&
            (p.cluster < 8 || items <= d->at_once[size_of((most + MAX_CLUSTER - 1) / MAX_CLUSTER)]))

@@ -143,9 +143,9 @@ __device__ __forceinline__ void item_rows(const WeighParams& p, int b, WeighShar
 //
 // Bound by the stream of keys: 32 KB of a tile take an SM 0.74 us at the measured
 // copy bandwidth.  Measured: one row of 6 heads over 131k tokens of 8 heads of 128,
-// 47.8 us for 277 MB (0.86 of the copy; the rest is the start: length, page table,
-// first keys); 96 rows 50 us (0.82); up to 30 rows over 8 sequences of up to 30011
-// tokens, 342 MB, 61.2 us (0.83); one token's rows over 1777 tokens 7.2 us, the
+// 48.0 us for 277 MB (0.85 of the copy; the rest is the start: length, page table,
+// first keys); 96 rows 48.9 us (0.84); up to 30 rows over 8 sequences of up to 30011
+// tokens, 342 MB, 60.0 us (0.84); one token's rows over 1777 tokens 7.0 us, the
 // chain of dependent reads before the first keys.  With two sets and one producer
 // the 96 rows took 65.7 us with pages of 16.
 template <typename T, int D, bool FAULT = false>
@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(WEIGH_THREADS, 1) qlin_weigh_kernel(const __gr
           if (c < p.Rp) put(c, v[k]);
         }
         fence_proxy_async_smem();
-        if (!weighing_bar(weighs || tid >= cols)) {  // such a row's query becomes zeros: one that is not finite would reach every token
+        // (its query becomes zeros: one that is not finite would reach every token)
+        if (!weighing_bar(weighs || tid >= cols)) {
           for (int c = tid / UNITS; c < cols; c += STEP) {
             const float4 st = s->stat[c / 2];
             if ((c & 1 ? st.w : st.z) == 0.f) put(c, make_uint4(0, 0, 0, 0));
