@@ -82,3 +82,27 @@ def test_what_takes_an_extensions_place_refers_every_call_to_the_other_way(tmp_p
     assert qlin._load_binding() is binding
     for call in ("kv_append", "kv_weigh", "kv_evict", "adjust_logits"):
         assert getattr(binding, call)(0, 1, None) is None
+
+
+def test_two_builds_at_once_do_not_trip_over_the_stamp(tree):
+    class Done:
+        returncode, stdout, stderr = 0, "", ""
+
+        def __init__(self, cmd, **kw):
+            pass
+
+        def communicate(self):
+            return "", ""
+
+    def link(cmd, **kw):
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return Done(cmd)
+
+    exists = os.path.exists  # the other build takes the stamp away between a look and a step
+    tree.setattr(os.path, "exists", lambda p: True if p == build.STAMP else exists(p))
+    os.remove(build.STAMP)
+    tree.setattr(build.subprocess, "Popen", Done)
+    tree.setattr(build.subprocess, "run", link)
+    tree.setattr(build, "_link_binding", lambda obj, tag: "")
+    build.build_library(force=True)
+    assert build.binding_fits()

@@ -10,6 +10,7 @@ and one notion of the current device).  The output goes to
 """
 from __future__ import annotations
 
+import contextlib
 import os
 import shutil
 import subprocess
@@ -143,7 +144,7 @@ def _compile_and_link(nvcc, cuda_lib, common, tag, verbose):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc link failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
-    if os.path.exists(STAMP):
+    with contextlib.suppress(FileNotFoundError):  # (also where another process's build has just removed it)
         os.remove(STAMP)
     os.replace(tmp, LIB)
     logs.append(_link_binding(binding, tag))
